@@ -398,6 +398,135 @@ TIM_API int tim_tis_ppo(const float *logp_theta, const float *logp_old, const fl
                         float eps_low, float eps_high, float C, const tim_ppo_out *out,
                         tim_stream_t stream);
 
+/* ------------------------------------------------------------------ a head's logits
+ *
+ * The calls below take the logits [N, V] of a vocabulary head where a program
+ * holds them: an inference engine between the head and the sampler, a trainer
+ * that keeps its logits.  Element types, by these codes: */
+enum tim_dtype { TIM_F32 = 0, TIM_BF16 = 1, TIM_F16 = 2 };
+
+/* The sampler's rules, row by row (icarus page, section "logits processor": the
+ * rollout engine samples from processed logits, and the trainer's logprob is
+ * comparable only under the same rules).  For row i and id v, with c the number
+ * of times v is among the row's generated tokens:
+ *   x = z_iv + bias_iv                            (where the row lists v)
+ *   x = x > 0 ? x / repetition : x * repetition   if v is anywhere in the row's history
+ *   x = x - frequency * c - presence              if c > 0
+ *   y = x / temperature;  y = -inf where the row's grammar does not allow v.
+ * The pages give no formulas or order; this is the order inference engines use.
+ * Host struct; every pointer is a device pointer, and NULL leaves its rule out.
+ *   temperature, repetition  fp32 [N], > 0, finite (and so 1 / x)
+ *   presence, frequency      fp32 [N], finite
+ *   history                  int32 [num_history]: token ids; ids outside [0, V) are skipped
+ *   history_spans            int32 [N][3]: begin, first generated token, end of the
+ *                            row's part of history, 0 <= begin <= generated <= end
+ *                            <= num_history.  Rows may share tokens: the positions of a
+ *                            packed sequence are spans of one array.
+ *   bias_offsets             int32 [N + 1]: row i lists entries bias_offsets[i] ..
+ *                            bias_offsets[i + 1] - 1 of bias_ids (ascending, each once,
+ *                            in [0, V)) and bias_values (fp32; -inf bans the id)
+ *   allowed                  uint32 [num_allowed][allowed_stride]: bit v % 32 of word
+ *                            v / 32 set = v is allowed; allowed_stride >= ceil(V / 32)
+ *   allowed_rows             int32 [N]: the row of `allowed` that row i is under, negative
+ *                            = none; NULL: row i is under row i (num_allowed >= N)
+ * A row whose parameters, span, bias entries or mask row break these limits (found
+ * on the device) gets NaN in every output and sets TIM_ERR_BAD_INPUT (tim_check). */
+typedef struct {
+    const float *temperature;
+    const float *repetition;
+    const float *presence;
+    const float *frequency;
+    const int32_t *history;
+    const int32_t *history_spans;
+    const int32_t *bias_offsets;
+    const int32_t *bias_ids;
+    const float *bias_values;
+    const uint32_t *allowed;
+    const int32_t *allowed_rows;
+    int64_t allowed_stride;      /* words */
+    int32_t num_history;
+    int32_t num_bias;            /* entries of bias_ids and bias_values */
+    int32_t num_allowed;
+} tim_logits_rules;
+
+/* The processed logits, y above, rounded once to the output's type.
+ *   logits   [N, V] of type dtype, rows `stride` elements apart (>= V), aligned to
+ *            its elements (16-byte-aligned rows are the fast case)
+ *   N, V     0 <= N < 2^31, 0 < V <= 2^20, N * ceil(V / 1024) < 2^31
+ *   rules    host struct above; NULL: no rule
+ *   out      [N, V] of type out_dtype (dtype, or TIM_F32), rows out_stride apart;
+ *            may be the logits themselves (same type and stride), else no overlap */
+TIM_API int tim_process_logits(const void *logits, int dtype, int64_t N, int64_t V, int64_t stride,
+                               const tim_logits_rules *rules, void *out, int out_dtype, int64_t out_stride,
+                               tim_stream_t stream);
+
+/* The chosen token's log-probability under the processed logits, which are not
+ * written: l_i = y_{i, a_i} - lse_i, lse_i = log sum_v e^{y_iv}, all in fp32.
+ *   targets   int32 [N]; an id outside [0, V) gives out_logp = NaN
+ *   out_logp  fp32 [N]; -inf where y_{i, a_i} = -inf
+ *   out_lse   fp32 [N]; -inf for a row with nothing left (its out_logp is -inf too)
+ * A NaN or +inf among the allowed logits makes a row's outputs NaN.  A row's bits do
+ * not depend on the batch. */
+TIM_API int tim_processed_logprob(const void *logits, int dtype, int64_t N, int64_t V, int64_t stride,
+                                  const tim_logits_rules *rules, const int32_t *targets, float *out_logp,
+                                  float *out_lse, tim_stream_t stream);
+
+/* Its gradient: dlogits_iv = g_i (1[v = a_i] - e^{y_iv - lse_i}) dy_iv / dz_iv, which is
+ * 0 where y_iv = -inf, rounded once to the logits' type.
+ *   grad_logp  fp32 [N]: g; a row with g = 0 is written as zeros without being read
+ *   lse        fp32 [N]: the forward's out_lse
+ *   dlogits    [N, V] of type dtype; may be the logits themselves, else no overlap
+ * A target outside [0, V) takes no one-hot term. */
+TIM_API int tim_processed_logprob_backward(const void *logits, int dtype, int64_t N, int64_t V, int64_t stride,
+                                           const tim_logits_rules *rules, const int32_t *targets,
+                                           const float *grad_logp, const float *lse, void *dlogits,
+                                           int64_t dlogits_stride, tim_stream_t stream);
+
+/* Distillation from a teacher's top logits (a second policy that scores the same
+ * tokens; no counterpart on the pages).  Row i lists K ids with the teacher's
+ * logits t; with p = softmax(z / temperature),
+ *   teacher_lse NULL:  q = softmax over the listed ids of t / temperature,
+ *                      loss = sum_k q_k (log q_k - log p_k);
+ *   else               q_k = e^(t_k / temperature - teacher_lse), and the rest of both
+ *                      distributions is one more outcome, q_o = max(0, 1 - sum_k q_k)
+ *                      and p_o = the probability of the ids not listed:
+ *                      loss = sum_k q_k (log q_k - log p_k) + q_o (log q_o - log p_o).
+ * Terms with q = 0 are 0.  With teacher_lse NULL a row that lists nothing has loss 0
+ * and gradient 0.
+ *   logits, dtype, N, V, stride   as above
+ *   teacher_ids     int32 [N, K], 1 <= K <= 1024; an id outside [0, V) is an empty
+ *                   entry, an id listed twice adds up
+ *   teacher_logits  fp32 [N, K]
+ *   teacher_lse     fp32 [N] or NULL: log-sum-exp of the teacher's whole row at
+ *                   `temperature`
+ *   temperature     > 0, finite (and so 1 / temperature)
+ *   loss, lse       out: fp32 [N]; lse = log sum_v e^(z_v / temperature)
+ *   lse_tail        out: fp32 [N], the same over the ids not listed; with teacher_lse
+ *                   only (else NULL) */
+#define TIM_DISTILL_MAX_K 1024
+TIM_API int tim_distill_topk(const void *logits, int dtype, int64_t N, int64_t V, int64_t stride,
+                             const int32_t *teacher_ids, const float *teacher_logits, const float *teacher_lse,
+                             int64_t K, float temperature, float *loss, float *lse, float *lse_tail,
+                             tim_stream_t stream);
+
+/* Its gradient for an upstream g_i = dL / dloss_i, from the forward's lse and (with
+ * teacher_lse) lse_tail: dlogits_iv = g_i (p_v - q_v) / temperature for listed ids, and
+ * with teacher_lse g_i p_v (1 - q_o / p_o) / temperature for the others.  dlogits as in
+ * tim_processed_logprob_backward; a row with g = 0 is zeros. */
+TIM_API int tim_distill_topk_backward(const void *logits, int dtype, int64_t N, int64_t V, int64_t stride,
+                                      const int32_t *teacher_ids, const float *teacher_logits,
+                                      const float *teacher_lse, int64_t K, float temperature,
+                                      const float *grad_loss, const float *lse, const float *lse_tail,
+                                      void *dlogits, int64_t dlogits_stride, tim_stream_t stream);
+
+/* Both in one call, for an upstream known beforehand (a token's weight in the
+ * batch's mean): the logits come from memory once. */
+TIM_API int tim_distill_topk_step(const void *logits, int dtype, int64_t N, int64_t V, int64_t stride,
+                                  const int32_t *teacher_ids, const float *teacher_logits,
+                                  const float *teacher_lse, int64_t K, float temperature, const float *grad_loss,
+                                  float *loss, float *lse, float *lse_tail, void *dlogits,
+                                  int64_t dlogits_stride, tim_stream_t stream);
+
 /* ------------------------------------------------------------------ failure-detection self-test
  *
  * No counterpart on the pages.  Runs the library's bounded-wait path on purpose,

@@ -17,11 +17,18 @@ rejection flag (VeXact summary, eq. (1) and "Algorithmic TIM Compensation";
 LoongSage "Train-Inference Consistency", sections 4-5).  ``tis_ppo`` gives the
 clipped PPO surrogate weighted by the truncated importance weight, its
 gradient and masked means (VeXact summary eq. (2)-(3)).
+
+Where a program holds the logits themselves, ``process_logits`` applies the
+sampler's rules (biases, penalties for repeated tokens, temperature, grammar
+masks), ``processed_logprob`` gives the chosen token's log-probability under them
+(with its gradient), and ``distill_topk`` distils from a teacher's top logits
+(icarus page, section "logits processor"; no formulas there).
 """
 from __future__ import annotations
 
 import contextlib
 import ctypes
+import dataclasses
 import math
 import os
 import threading
@@ -34,6 +41,9 @@ __all__ = [
     "tim_token_logprob_fp32_head", "tim_token_logprob_backward", "tim_selftest_wait_timeout", "tim_check", "tim_last_error", "tim_version",
     "tim_debug_violation", "tim_debug_build", "load_debug", "checked", "CHECKS",
     "token_logprob", "token_logprob_backward", "split_weight_fp32", "token_logprob_fp32_head", "mismatch_stats", "mismatch_monitor", "tis_ppo", "check",
+    "LogitsRules", "tim_logits_rules", "tim_process_logits", "tim_processed_logprob", "tim_processed_logprob_backward",
+    "tim_distill_topk", "tim_distill_topk_backward", "tim_distill_topk_step", "process_logits", "processed_logprob",
+    "processed_logprob_backward", "distill_topk", "distill_topk_backward", "distill_topk_step", "packed_spans",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -53,6 +63,8 @@ CHECKS = {0: "none", 1: "target", 2: "mask", 3: "logit", 4: "backward_input", 5:
           6: "tma_coord", 7: "store", 8: "unit", 9: "bulk"}
 
 SEQ_RECORD_WORDS = 16   # TIM_SEQ_RECORD_WORDS
+TIM_F32, TIM_BF16, TIM_F16 = 0, 1, 2   # enum tim_dtype
+DISTILL_MAX_K = 1024    # TIM_DISTILL_MAX_K
 SEQ_FIELDS = ("n_mask", "n_used", "n_nan", "n_clip", "mean_delta", "mean_abs_delta",
               "max_abs_delta", "mean_k1", "mean_k2", "mean_k3", "mean_w", "mean_rel")
 BATCH_FIELDS = ("n_mask", "n_used", "n_nan", "n_clip", "mean_delta", "mean_abs_delta",
@@ -100,6 +112,18 @@ class tim_ppo_out(ctypes.Structure):
     ]
 
 
+class tim_logits_rules(ctypes.Structure):
+    """Mirror of the C struct tim_logits_rules (host struct of device pointers)."""
+    _fields_ = [(n, ctypes.c_void_p) for n in
+                ("temperature", "repetition", "presence", "frequency", "history", "history_spans", "bias_offsets",
+                 "bias_ids", "bias_values", "allowed", "allowed_rows")] + [
+        ("allowed_stride", ctypes.c_int64),
+        ("num_history", ctypes.c_int32),
+        ("num_bias", ctypes.c_int32),
+        ("num_allowed", ctypes.c_int32),
+    ]
+
+
 _lock = threading.Lock()
 _lib = None          # the library calls go to (libtim.so, or libtim_debug.so inside `checked()`)
 _release = None
@@ -140,6 +164,17 @@ def _open(path: str, what: str):
     lib.tim_token_logprob_backward.restype = ctypes.c_int
     lib.tim_mismatch_monitor.argtypes = [P, P, P, I64, F, P, P, P]
     lib.tim_mismatch_monitor.restype = ctypes.c_int
+    head = [P, ctypes.c_int, I64, I64, I64]   # logits, dtype, N, V, stride
+    RP = ctypes.POINTER(tim_logits_rules)
+    teacher = [P, P, P, I64, F]               # ids, logits, lse, K, temperature
+    for name, args in (("tim_process_logits", head + [RP, P, ctypes.c_int, I64, P]),
+                       ("tim_processed_logprob", head + [RP, P, P, P, P]),
+                       ("tim_processed_logprob_backward", head + [RP, P, P, P, P, I64, P]),
+                       ("tim_distill_topk", head + teacher + [P, P, P, P]),
+                       ("tim_distill_topk_backward", head + teacher + [P, P, P, P, I64, P]),
+                       ("tim_distill_topk_step", head + teacher + [P, P, P, P, P, I64, P])):
+        getattr(lib, name).argtypes = args
+        getattr(lib, name).restype = ctypes.c_int
     lib.tim_selftest_wait_timeout.argtypes = [ctypes.c_uint32, P]
     lib.tim_selftest_wait_timeout.restype = ctypes.c_int
     lib.tim_check.argtypes = [P]
@@ -248,6 +283,39 @@ def tim_token_logprob_fp32_head(h, W_split, targets, N, D, V, temperature, out_l
 def tim_mismatch_monitor(logp_train, logp_rollout, mask, N, tau_tok, token_reject, out, stream) -> int:
     return load().tim_mismatch_monitor(logp_train, logp_rollout, mask, N, float(tau_tok), token_reject, out,
                                        stream)
+
+
+def tim_process_logits(logits, dtype, N, V, stride, rules, out, out_dtype, out_stride, stream) -> int:
+    """C ABI; rules is a tim_logits_rules or None."""
+    return load().tim_process_logits(logits, dtype, N, V, stride, rules, out, out_dtype, out_stride, stream)
+
+
+def tim_processed_logprob(logits, dtype, N, V, stride, rules, targets, out_logp, out_lse, stream) -> int:
+    return load().tim_processed_logprob(logits, dtype, N, V, stride, rules, targets, out_logp, out_lse, stream)
+
+
+def tim_processed_logprob_backward(logits, dtype, N, V, stride, rules, targets, grad_logp, lse, dlogits,
+                                   dlogits_stride, stream) -> int:
+    return load().tim_processed_logprob_backward(logits, dtype, N, V, stride, rules, targets, grad_logp, lse, dlogits,
+                                                 dlogits_stride, stream)
+
+
+def tim_distill_topk(logits, dtype, N, V, stride, teacher_ids, teacher_logits, teacher_lse, K, temperature, loss, lse,
+                     lse_tail, stream) -> int:
+    return load().tim_distill_topk(logits, dtype, N, V, stride, teacher_ids, teacher_logits, teacher_lse, K,
+                                   temperature, loss, lse, lse_tail, stream)
+
+
+def tim_distill_topk_backward(logits, dtype, N, V, stride, teacher_ids, teacher_logits, teacher_lse, K, temperature,
+                              grad_loss, lse, lse_tail, dlogits, dlogits_stride, stream) -> int:
+    return load().tim_distill_topk_backward(logits, dtype, N, V, stride, teacher_ids, teacher_logits, teacher_lse, K,
+                                            temperature, grad_loss, lse, lse_tail, dlogits, dlogits_stride, stream)
+
+
+def tim_distill_topk_step(logits, dtype, N, V, stride, teacher_ids, teacher_logits, teacher_lse, K, temperature,
+                          grad_loss, loss, lse, lse_tail, dlogits, dlogits_stride, stream) -> int:
+    return load().tim_distill_topk_step(logits, dtype, N, V, stride, teacher_ids, teacher_logits, teacher_lse, K,
+                                        temperature, grad_loss, loss, lse, lse_tail, dlogits, dlogits_stride, stream)
 
 
 def tim_selftest_wait_timeout(budget_us, stream) -> int:
@@ -581,6 +649,286 @@ def tis_ppo(logp_theta, logp_old, logp_rollout, advantages, mask, seq_offsets, e
         rc = tim_tis_ppo(logp_theta.data_ptr(), logp_old.data_ptr(), logp_rollout.data_ptr(),
                          advantages.data_ptr(), mask.data_ptr(), seq_offsets.data_ptr(), eps_low, eps_high, C,
                          d, _stream_handle(stream, dev))
+    _raise_if(rc)
+    return out
+
+
+# ----------------------------------------------------------------------------- a head's logits
+@dataclasses.dataclass
+class LogitsRules:
+    """The sampler's rules, row by row (tim_logits_rules in include/tim.h); None
+    leaves a rule out.  All on the logits' device and contiguous: temperature,
+    repetition, presence, frequency fp32 [N]; history int32 [H] with history_spans
+    int32 [N, 3] (begin, first generated token, end); bias_offsets int32 [N + 1]
+    with bias_ids int32 and bias_values fp32 [B] (a row's ids ascending); allowed
+    int32 or uint32 [R, ceil(V / 32) or more] bits, with allowed_rows int32 [N]
+    (a row of `allowed`, negative = none) or R >= N."""
+    temperature: object = None
+    repetition: object = None
+    presence: object = None
+    frequency: object = None
+    history: object = None
+    history_spans: object = None
+    bias_offsets: object = None
+    bias_ids: object = None
+    bias_values: object = None
+    allowed: object = None
+    allowed_rows: object = None
+
+    def struct(self, N: int, V: int, device):
+        """The C struct, after checking every tensor against N rows of V logits."""
+        import torch
+        r = tim_logits_rules()
+        for name in ("temperature", "repetition", "presence", "frequency"):
+            t = getattr(self, name)
+            if t is not None:
+                _need_out(t, name, torch.float32, (N,), device)
+                setattr(r, name, t.data_ptr())
+        if (self.history is None) != (self.history_spans is None):
+            raise ValueError("history and history_spans go together")
+        if self.history is not None:
+            _need(self.history, "history", torch.int32, 1, device)
+            _need_out(self.history_spans, "history_spans", torch.int32, (N, 3), device)
+            r.history, r.num_history = self.history.data_ptr(), _int32_size(self.history, "history")
+            r.history_spans = self.history_spans.data_ptr()
+        bias = (self.bias_offsets, self.bias_ids, self.bias_values)
+        if any(t is None for t in bias) != all(t is None for t in bias):
+            raise ValueError("bias_offsets, bias_ids and bias_values go together")
+        if self.bias_ids is not None:
+            _need_out(self.bias_offsets, "bias_offsets", torch.int32, (N + 1,), device)
+            _need(self.bias_ids, "bias_ids", torch.int32, 1, device)
+            _need_out(self.bias_values, "bias_values", torch.float32, (self.bias_ids.shape[0],), device)
+            r.bias_offsets, r.bias_ids = self.bias_offsets.data_ptr(), self.bias_ids.data_ptr()
+            r.bias_values, r.num_bias = self.bias_values.data_ptr(), _int32_size(self.bias_ids, "bias_ids")
+        if self.allowed is not None:
+            _need(self.allowed, "allowed", (torch.int32, torch.uint32), 2, device)
+            if self.allowed.shape[1] < (V + 31) // 32:
+                raise ValueError("allowed must have at least %d words a row" % ((V + 31) // 32))
+            r.allowed, r.allowed_stride = self.allowed.data_ptr(), self.allowed.shape[1]
+            r.num_allowed = min(self.allowed.shape[0], 2 ** 31 - 1)
+            if self.allowed_rows is not None:
+                _need_out(self.allowed_rows, "allowed_rows", torch.int32, (N,), device)
+                r.allowed_rows = self.allowed_rows.data_ptr()
+            elif self.allowed.shape[0] < N:
+                raise ValueError("allowed has fewer rows than the logits: give allowed_rows")
+        elif self.allowed_rows is not None:
+            raise ValueError("allowed_rows without allowed")
+        return r
+
+
+def _int32_size(t, name):
+    if t.shape[0] >= 2 ** 31:
+        raise ValueError("%s must have fewer than 2^31 entries" % name)
+    return t.shape[0]
+
+
+def _dtype_code(dtype):
+    import torch
+    return {torch.float32: TIM_F32, torch.bfloat16: TIM_BF16, torch.float16: TIM_F16}[dtype]
+
+
+def _need_logits(t, name, dtype=None, device=None, shape=None):
+    """Rows of logits: 2-D, a row's elements adjacent, rows any stride >= V apart.
+    Returns the stride."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    allowed = (torch.float32, torch.bfloat16, torch.float16) if dtype is None else (dtype,)
+    if t.dtype not in allowed:
+        raise TypeError("%s must have dtype %s, got %s" % (name, " or ".join(map(str, allowed)), t.dtype))
+    if t.dim() != 2:
+        raise ValueError("%s must be 2-D" % name)
+    N, V = t.shape
+    if shape is not None and (N, V) != tuple(shape):
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), (N, V)))
+    if V < 1:
+        raise ValueError("%s must have at least one column" % name)
+    if V > 1 and t.stride(1) != 1:
+        raise ValueError("a row of %s must be contiguous" % name)
+    if device is not None and t.device != device:
+        raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
+    if N <= 1:
+        return V
+    if t.stride(0) < V:
+        raise ValueError("the rows of %s must not overlap" % name)
+    return t.stride(0)
+
+
+def _rules_struct(rules, N, V, dev):
+    return None if rules is None else ctypes.byref(rules.struct(N, V, dev))
+
+
+def packed_spans(seq_offsets, prompt_lens, num_tokens: int):
+    """history_spans (int32 [T, 3], T = num_tokens = seq_offsets[S]) of packed
+    sequences for LogitsRules, with the packed input tokens as the history:
+    position t of sequence s has read the tokens from seq_offsets[s] up to its
+    own, the first prompt_lens[s] of them the prompt.  seq_offsets int32 [S + 1],
+    prompt_lens int32 [S], on one device."""
+    import torch
+    off = seq_offsets.long()
+    t = torch.arange(num_tokens, device=off.device)
+    s = torch.bucketize(t, off[1:], right=True).clamp_(max=max(0, off.shape[0] - 2))
+    begin, end = off[s], t + 1
+    return torch.stack([begin, torch.minimum(begin + prompt_lens.long()[s], end), end], 1).to(torch.int32)
+
+
+def process_logits(logits, rules, out=None, out_dtype=None, stream=None):
+    """The processed logits [N, V] (y in include/tim.h) of fp32, bf16 or fp16
+    logits under `rules` (a LogitsRules or None), in the logits' type or fp32.
+    out may be the logits themselves."""
+    import torch
+    stride = _need_logits(logits, "logits")
+    dev = logits.device
+    N, V = logits.shape
+    if out is None:
+        out = torch.empty((N, V), dtype=out_dtype or logits.dtype, device=dev)
+    if out_dtype is not None and out.dtype != out_dtype:
+        raise TypeError("out must have dtype %s, got %s" % (out_dtype, out.dtype))
+    if out.dtype not in (logits.dtype, torch.float32):
+        raise TypeError("out must have the logits' dtype or float32, got %s" % out.dtype)
+    out_stride = _need_logits(out, "out", out.dtype, dev, (N, V))
+    r = _rules_struct(rules, N, V, dev)
+    with torch.cuda.device(dev):
+        rc = tim_process_logits(logits.data_ptr(), _dtype_code(logits.dtype), N, V, stride, r, out.data_ptr(),
+                                _dtype_code(out.dtype), out_stride, _stream_handle(stream, dev))
+    _raise_if(rc)
+    return out
+
+
+def processed_logprob(logits, rules, targets, out_logp=None, out_lse=None, stream=None):
+    """(logp [N] fp32, lse [N] fp32) of the int32 targets [N] under the processed
+    logits, which are not written."""
+    import torch
+    stride = _need_logits(logits, "logits")
+    dev = logits.device
+    N, V = logits.shape
+    _need_out(targets, "targets", torch.int32, (N,), dev)
+    if out_logp is None:
+        out_logp = torch.empty(N, dtype=torch.float32, device=dev)
+    if out_lse is None:
+        out_lse = torch.empty(N, dtype=torch.float32, device=dev)
+    _need_out(out_logp, "out_logp", torch.float32, (N,), dev)
+    _need_out(out_lse, "out_lse", torch.float32, (N,), dev)
+    r = _rules_struct(rules, N, V, dev)
+    with torch.cuda.device(dev):
+        rc = tim_processed_logprob(logits.data_ptr(), _dtype_code(logits.dtype), N, V, stride, r, targets.data_ptr(),
+                                   out_logp.data_ptr(), out_lse.data_ptr(), _stream_handle(stream, dev))
+    _raise_if(rc)
+    return out_logp, out_lse
+
+
+def processed_logprob_backward(logits, rules, targets, grad_logp, lse, dlogits=None, stream=None):
+    """The gradient [N, V], in the logits' type, of sum_i grad_logp_i logp_i with
+    respect to the raw logits, from the forward's lse.  dlogits may be the
+    logits themselves."""
+    import torch
+    stride = _need_logits(logits, "logits")
+    dev = logits.device
+    N, V = logits.shape
+    _need_out(targets, "targets", torch.int32, (N,), dev)
+    _need_out(grad_logp, "grad_logp", torch.float32, (N,), dev)
+    _need_out(lse, "lse", torch.float32, (N,), dev)
+    if dlogits is None:
+        dlogits = torch.empty((N, V), dtype=logits.dtype, device=dev)
+    dstride = _need_logits(dlogits, "dlogits", logits.dtype, dev, (N, V))
+    r = _rules_struct(rules, N, V, dev)
+    with torch.cuda.device(dev):
+        rc = tim_processed_logprob_backward(logits.data_ptr(), _dtype_code(logits.dtype), N, V, stride, r,
+                                            targets.data_ptr(), grad_logp.data_ptr(), lse.data_ptr(),
+                                            dlogits.data_ptr(), dstride, _stream_handle(stream, dev))
+    _raise_if(rc)
+    return dlogits
+
+
+def _distill_inputs(logits, teacher_ids, teacher_logits, teacher_lse):
+    import torch
+    stride = _need_logits(logits, "logits")
+    dev = logits.device
+    N, V = logits.shape
+    _need(teacher_ids, "teacher_ids", torch.int32, 2, dev)
+    K = teacher_ids.shape[1]
+    if teacher_ids.shape[0] != N or not 1 <= K <= DISTILL_MAX_K:
+        raise ValueError("teacher_ids must be [%d, 1 .. %d], got %s" % (N, DISTILL_MAX_K, tuple(teacher_ids.shape)))
+    _need_out(teacher_logits, "teacher_logits", torch.float32, (N, K), dev)
+    if teacher_lse is not None:
+        _need_out(teacher_lse, "teacher_lse", torch.float32, (N,), dev)
+    args = (logits.data_ptr(), _dtype_code(logits.dtype), N, V, stride, teacher_ids.data_ptr(),
+            teacher_logits.data_ptr(), None if teacher_lse is None else teacher_lse.data_ptr(), K)
+    return args, N, V, dev
+
+
+def _distill_rows(out, N, tail, dev):
+    import torch
+    out = {} if out is None else dict(out)
+    for name in ("loss", "lse") + (("lse_tail",) if tail else ()):
+        if out.get(name) is None:
+            out[name] = torch.empty(N, dtype=torch.float32, device=dev)
+        _need_out(out[name], name, torch.float32, (N,), dev)
+    if not tail:
+        out["lse_tail"] = None
+    return out, out["lse_tail"].data_ptr() if tail else None
+
+
+def distill_topk(logits, teacher_ids, teacher_logits, teacher_lse=None, temperature: float = 1.0, out=None,
+                 stream=None):
+    """Distillation loss of fp32, bf16 or fp16 logits [N, V] from a teacher's top
+    logits: teacher_ids int32 [N, K] (an id outside [0, V) is an empty entry),
+    teacher_logits fp32 [N, K], and teacher_lse fp32 [N] where the teacher's mass
+    outside its list is one more outcome.  Returns a dict: loss, lse fp32 [N] and
+    lse_tail (fp32 [N] with teacher_lse, else None)."""
+    import torch
+    args, N, _, dev = _distill_inputs(logits, teacher_ids, teacher_logits, teacher_lse)
+    out, tail = _distill_rows(out, N, teacher_lse is not None, dev)
+    with torch.cuda.device(dev):
+        rc = tim_distill_topk(*args, float(temperature), out["loss"].data_ptr(), out["lse"].data_ptr(), tail,
+                              _stream_handle(stream, dev))
+    _raise_if(rc)
+    return out
+
+
+def distill_topk_backward(logits, teacher_ids, teacher_logits, grad_loss, lse, lse_tail=None, teacher_lse=None,
+                          temperature: float = 1.0, dlogits=None, stream=None):
+    """The gradient [N, V], in the logits' type, of sum_i grad_loss_i loss_i, from
+    the forward's lse and (with teacher_lse) lse_tail.  dlogits may be the logits
+    themselves."""
+    import torch
+    args, N, V, dev = _distill_inputs(logits, teacher_ids, teacher_logits, teacher_lse)
+    _need_out(grad_loss, "grad_loss", torch.float32, (N,), dev)
+    _need_out(lse, "lse", torch.float32, (N,), dev)
+    if (lse_tail is None) != (teacher_lse is None):
+        raise ValueError("lse_tail and teacher_lse go together")
+    if lse_tail is not None:
+        _need_out(lse_tail, "lse_tail", torch.float32, (N,), dev)
+    if dlogits is None:
+        dlogits = torch.empty((N, V), dtype=logits.dtype, device=dev)
+    dstride = _need_logits(dlogits, "dlogits", logits.dtype, dev, (N, V))
+    with torch.cuda.device(dev):
+        rc = tim_distill_topk_backward(*args, float(temperature), grad_loss.data_ptr(), lse.data_ptr(),
+                                       None if lse_tail is None else lse_tail.data_ptr(), dlogits.data_ptr(), dstride,
+                                       _stream_handle(stream, dev))
+    _raise_if(rc)
+    return dlogits
+
+
+def distill_topk_step(logits, teacher_ids, teacher_logits, grad_loss, teacher_lse=None, temperature: float = 1.0,
+                      out=None, dlogits=None, stream=None):
+    """distill_topk and its gradient in one call, for weights grad_loss fp32 [N]
+    known beforehand: the dict of distill_topk with dlogits [N, V] added (which
+    may be the logits themselves)."""
+    import torch
+    args, N, V, dev = _distill_inputs(logits, teacher_ids, teacher_logits, teacher_lse)
+    _need_out(grad_loss, "grad_loss", torch.float32, (N,), dev)
+    out, tail = _distill_rows(out, N, teacher_lse is not None, dev)
+    if dlogits is None:
+        dlogits = torch.empty((N, V), dtype=logits.dtype, device=dev)
+    dstride = _need_logits(dlogits, "dlogits", logits.dtype, dev, (N, V))
+    out["dlogits"] = dlogits
+    with torch.cuda.device(dev):
+        rc = tim_distill_topk_step(*args, float(temperature), grad_loss.data_ptr(), out["loss"].data_ptr(),
+                                   out["lse"].data_ptr(), tail, dlogits.data_ptr(), dstride,
+                                   _stream_handle(stream, dev))
     _raise_if(rc)
     return out
 

@@ -1,0 +1,375 @@
+// distill_topk.cu -- distillation of a head's logits from a teacher's top
+// logits: the loss, its gradient, and both in one call.
+//
+// Row i lists ids k with the teacher's logits t_k.  With p = softmax(z / tau):
+//   without the teacher's lse  q = softmax over the listed ids of t / tau,
+//                              L = sum_k q_k (log q_k - log p_k),
+//                              dL/dz_v = (p_v - q_v) / tau;
+//   with it                    q_k = e^(t_k / tau - lse_T), the rest q_o = 1 - sum q_k is
+//                              one more outcome, whose student probability is that of
+//                              the ids not listed, p_o = 1 - sum p_k:
+//                              L = sum_k q_k (log q_k - log p_k) + q_o (log q_o - log p_o),
+//                              dL/dz_v = (p_v - q_v) / tau for the listed ids and
+//                              p_v (1 - q_o / p_o) / tau for the others.
+// (q_v is 0 for ids that are not listed; an id listed twice adds up.)  log p_o is the
+// log-sum-exp over the columns whose bit is not set in a bitmap of the listed
+// ids, never 1 - sum p_k, which loses all its digits when p_o is small.
+//
+// What bounds it: the row streams through once for the sums and, in a step, once
+// more (from L2, where the cluster's rows of the moment fit) for the gradient;
+// the listed ids cost K gathers and K stores.  The gradient pass writes every
+// column as if it were not listed; after a barrier the listed ones, all of
+// which the same CTA owns, are written over.
+#include <algorithm>
+
+#include "logits_rows.cuh"
+
+namespace tim {
+namespace {
+
+struct Teacher {
+    int id[LD_MAX_K];      // -1: not in use
+    float q[LD_MAX_K];
+    float logq[LD_MAX_K];
+    float t2[LD_MAX_K];    // the student's base-2 exponent at id
+};
+
+// log q of a listed id from t / tau = hi + lo and the teacher's log-sum-exp:
+// hi - lse is exact when they are close, so large probabilities keep their digits.
+__device__ __forceinline__ float teacher_logq(float t, float tau, float lse)
+{
+    const float hi = t / tau;
+    const float lo = isfinite(hi) ? fmaf(-hi, tau, t) / tau : 0.f;
+    return (hi - lse) + lo;
+}
+
+template <typename T, int OP, bool TAIL>
+__global__ void __launch_bounds__(LD_THREADS) distill_kernel(const DistillArgs a)
+{
+    constexpr bool SUMS = OP != LD_BACKWARD, GRAD = OP != LD_FORWARD, BITS = TAIL || GRAD;
+    extern __shared__ uint32_t bitmap[];   // columns of this rank
+    __shared__ float4 part[SUMS ? LG_MAX_SLICES : 1];
+    __shared__ Teacher th;
+    __shared__ int dup;
+    const int rank = static_cast<int>(cluster_ctarank());
+    const int row = static_cast<int>(blockIdx.x / static_cast<unsigned>(a.ranks));
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int slices = (a.V + LG_SLICE - 1) / LG_SLICE;
+    const int s0 = min(slices, rank * a.per), s1 = min(slices, s0 + a.per);
+    const int c0 = s0 * LG_SLICE, c1 = min(a.V, s1 * LG_SLICE);
+    const T *z = static_cast<const T *>(a.z) + row * a.ld;
+    T *dz = GRAD ? static_cast<T *>(a.dz) + row * a.ldo : nullptr;
+    const bool vec = row_vec(z), vec_out = GRAD && row_vec(dz);
+    const float tau = a.temperature, k2 = LG_LOG2E / tau;
+    float g = 0.f;
+    if constexpr (GRAD)
+        g = a.grad[row];
+    if (SUMS && a.ranks > 1)
+        cluster_arrive();   // waited for before the first store into another CTA's shared memory
+
+    auto zero_row = [&] {
+        const float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        for (int col = c0 + static_cast<int>(threadIdx.x) * 8; col < c1; col += LD_THREADS * 8)
+            store8<T>(dz, col, c1, vec_out, v);
+    };
+    if constexpr (!SUMS) {
+        if (g == 0.f) {
+            zero_row();
+            return;
+        }
+    }
+
+    // the teacher's row
+    if (BITS) {
+        for (int j = threadIdx.x; j < (c1 - c0 + 31) / 32; j += LD_THREADS)
+            bitmap[j] = 0;
+        if (threadIdx.x == 0)
+            dup = 0;
+    }
+    for (int k = threadIdx.x; k < a.K; k += LD_THREADS) {
+        const int64_t at = static_cast<int64_t>(row) * a.K + k;
+        int id = a.ids[at];
+        id = id >= 0 && id < a.V ? id : -1;
+        th.id[k] = id;
+        th.logq[k] = id >= 0 ? a.teacher[at] : neg_inf();
+        if (SUMS)
+            th.t2[k] = id >= 0 ? Elem<T>::load(z + id) * k2 : 0.f;
+    }
+    __syncthreads();
+    // (every warp finds the row's normaliser for itself)
+    float q_all = 0.f, q_max = neg_inf();
+    bool any = false;
+    for (int k = lane; k < a.K; k += 32) {
+        any |= th.id[k] >= 0;
+        q_max = fmaxf(q_max, th.logq[k]);
+    }
+    any = __any_sync(0xffffffffu, any);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1)
+        q_max = fmaxf(q_max, __shfl_xor_sync(0xffffffffu, q_max, d));
+    float q_lse = 0.f;
+    if constexpr (TAIL) {
+        q_lse = a.teacher_lse[row];
+    } else {
+        float s = 0.f;
+        for (int k = lane; k < a.K; k += 32)
+            s += th.id[k] >= 0 ? expf((th.logq[k] - finite_ref(q_max)) / tau) : 0.f;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1)
+            s += __shfl_xor_sync(0xffffffffu, s, d);
+        any = any && s != 0.f;
+        q_lse = logf(s);
+    }
+    __syncthreads();   // th.logq still held t
+    for (int k = threadIdx.x; k < a.K; k += LD_THREADS) {
+        const float t = th.logq[k];
+        float lq = TAIL ? teacher_logq(t, tau, q_lse) : teacher_logq(t - finite_ref(q_max), tau, q_lse);
+        const int id = th.id[k];
+        if (id < 0 || !any)
+            lq = neg_inf();
+        th.logq[k] = lq;
+        th.q[k] = lq == neg_inf() ? 0.f : expf(lq);
+        if (BITS && id >= c0 && id < c1) {
+            const uint32_t bit = 1u << ((id - c0) & 31);
+            if (atomicOr(bitmap + ((id - c0) >> 5), bit) & bit)
+                dup = 1;
+        }
+    }
+    __syncthreads();
+    float q_rest = 0.f;
+    if constexpr (TAIL) {
+        for (int k = lane; k < a.K; k += 32)
+            q_all += th.q[k];
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1)
+            q_all += __shfl_xor_sync(0xffffffffu, q_all, d);
+        q_rest = q_all <= 1.f ? 1.f - q_all : (q_all > 1.f ? 0.f : q_all);   // NaN stays
+    }
+
+    // The sums: (m, s) of the columns that are not listed (all of them without a
+    // tail), (mk, sk) of the listed ones.
+    float m = neg_inf(), s = 0.f, mr = neg_inf(), sr = 0.f;
+    if constexpr (SUMS) {
+        for (int sl = s0 + warp; sl < s1; sl += LD_WARPS) {
+            Raw8<T> raw[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                load8<T>(raw[u], z, sl * LG_SLICE + u * 256 + lane * 8, a.V, vec);
+            float lm = neg_inf(), ls = 0.f, km = neg_inf(), ks = 0.f;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int col = sl * LG_SLICE + u * 256 + lane * 8;
+                float t[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    t[i] = Elem<T>::get(raw[u].w, i) * k2;
+                if constexpr (TAIL) {
+                    const uint32_t bits =
+                        col < a.V ? reinterpret_cast<const uint8_t *>(bitmap)[(col - c0) >> 3] : 0u;
+                    if (bits) {
+                        float l[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            l[i] = bits >> i & 1 ? t[i] : neg_inf();
+                            t[i] = bits >> i & 1 ? neg_inf() : t[i];
+                        }
+                        lane_add8(km, ks, l);
+                    }
+                }
+                lane_add8(lm, ls, t);
+            }
+            warp_join(lm, ls);
+            if constexpr (TAIL)
+                warp_join(km, ks);
+            if (lane == 0)
+                part[sl] = make_float4(lm, ls, km, ks);
+        }
+        __syncthreads();
+        if (a.ranks > 1) {
+            cluster_wait();
+            for (int d = 0; d < (GRAD ? a.ranks : 1); ++d) {
+                if (d == rank)
+                    continue;
+                const uint32_t to = mapa_shared(smem_u32(part), static_cast<uint32_t>(d));
+                for (int j = s0 + static_cast<int>(threadIdx.x); j < s1; j += LD_THREADS) {
+                    st_cluster_f2(to + j * 16, part[j].x, part[j].y);
+                    st_cluster_f2(to + j * 16 + 8, part[j].z, part[j].w);
+                }
+            }
+            __syncwarp();
+            cluster_arrive();
+            cluster_wait();
+        }
+        if (!GRAD && (rank != 0 || warp != 0))
+            return;
+        // fold in slice order: lane l takes slices l, l + 32, ...
+        float km = neg_inf(), ks = 0.f;
+        for (int j = lane; j < slices; j += 32) {
+            const float4 p = part[j];
+            join(mr, sr, p.x, p.y);
+            if constexpr (TAIL)
+                join(km, ks, p.z, p.w);
+        }
+        warp_join(mr, sr);
+        m = mr;
+        s = sr;
+        if constexpr (TAIL) {
+            warp_join(km, ks);
+            join(m, s, km, ks);
+        }
+        if (rank == 0 && warp == 0) {
+            float loss = 0.f;
+            for (int k = lane; k < a.K; k += 32)
+                if (th.q[k] != 0.f)   // NaN goes on
+                    loss += th.q[k] * (th.logq[k] - row_logp(th.t2[k], m, s));
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1)
+                loss += __shfl_xor_sync(0xffffffffu, loss, d);
+            if constexpr (TAIL)
+                if (q_rest != 0.f)
+                    loss += q_rest * (logf(q_rest) - (sr == 0.f ? neg_inf() : ((mr - m) + (log2f(sr) - log2f(s))) * LG_LN2));
+            if (lane == 0) {
+                a.loss[row] = loss;
+                a.out_lse[row] = row_lse(m, s);
+                if (TAIL)
+                    a.out_lse_tail[row] = row_lse(mr, sr);
+            }
+        }
+    }
+
+    if constexpr (GRAD) {
+        if (SUMS && g == 0.f) {
+            zero_row();
+            return;
+        }
+        // p_v = 2^(t_v - m) / s in a step, e^(z_v / tau - lse) from the forward's lse
+        const float gi = g / tau;
+        float lse = 0.f, inv_s = 0.f, w = any ? 1.f : 0.f;
+        if constexpr (SUMS) {
+            inv_s = s == 0.f ? 0.f : 1.f / s;
+            m = finite_ref(m);
+            if constexpr (TAIL)
+                w = sr == 0.f ? 0.f : 1.f - q_rest / (sr * exp2_approx(mr - m) * inv_s);
+        } else {
+            lse = a.lse[row];
+            if constexpr (TAIL) {
+                const float lt = a.lse_tail[row];
+                w = lt == neg_inf() ? 0.f : 1.f - q_rest * expf(lse - lt);
+            }
+            if (lse == neg_inf())
+                lse = -neg_inf();
+        }
+        const float inv_tau = 1.f / tau;
+        auto prob = [&](float x) {
+            if constexpr (SUMS)
+                return exp2_approx(x * k2 - m) * inv_s;
+            else
+                return exp2_approx(fmaf(x, inv_tau, -lse) * LG_LOG2E);
+        };
+        // the listed ids' values first: z may be overwritten in place
+        constexpr int KPT = (LD_MAX_K + LD_THREADS - 1) / LD_THREADS;
+        float own[KPT];
+#pragma unroll
+        for (int n = 0; n < KPT; ++n) {
+            const int k = static_cast<int>(threadIdx.x) + n * LD_THREADS;
+            own[n] = 0.f;
+            if (k < a.K && th.id[k] >= c0 && th.id[k] < c1) {
+                float q = th.q[k];
+                if (dup) {   // ids listed more than once add up, in the list's order
+                    q = 0.f;
+                    for (int j = 0; j < a.K; ++j)
+                        q += th.id[j] == th.id[k] ? th.q[j] : 0.f;
+                }
+                own[n] = (prob(Elem<T>::load(z + th.id[k])) - q) * gi;
+            }
+        }
+        __syncthreads();
+        const float wgi = w * gi;
+        for (int col = c0 + static_cast<int>(threadIdx.x) * 8; col < c1; col += LD_THREADS * 8) {
+            Raw8<T> raw;
+            load8<T>(raw, z, col, c1, vec);
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                v[i] = prob(Elem<T>::get(raw.w, i)) * wgi;
+            store8<T>(dz, col, c1, vec_out, v);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int n = 0; n < KPT; ++n) {
+            const int k = static_cast<int>(threadIdx.x) + n * LD_THREADS;
+            if (k < a.K && th.id[k] >= c0 && th.id[k] < c1)
+                dz[th.id[k]] = Elem<T>::from(own[n]);
+        }
+    }
+}
+
+template <typename T, int OP, bool TAIL> cudaError_t launch(DistillArgs a, int num_sms, cudaStream_t s)
+{
+    const int slices = lg_slices(a.V);
+    int ranks = 1;   // CTAs of a row: more while the rows alone leave SMs idle
+    while (ranks < LG_CLUSTER && ranks * 2 <= slices && static_cast<int64_t>(a.N) * ranks < 2 * num_sms)
+        ranks *= 2;
+    if (OP == LD_STEP && slices >= LG_CLUSTER)
+        ranks = LG_CLUSTER;   // the rows in flight stay in L2 between the two passes
+    a.ranks = ranks;
+    a.per = (slices + ranks - 1) / ranks;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(a.N) * static_cast<unsigned>(ranks));
+    cfg.blockDim = dim3(LD_THREADS);
+    cfg.dynamicSmemBytes = OP != LD_FORWARD || TAIL ? static_cast<size_t>(a.per) * (LG_SLICE / 8) : 0;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = static_cast<unsigned>(ranks);
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, distill_kernel<T, OP, TAIL>, a);
+}
+
+template <typename T> cudaError_t launch_op(const DistillArgs &a, int op, int num_sms, cudaStream_t s)
+{
+    const bool tail = a.teacher_lse != nullptr;
+    if (op == LD_FORWARD)
+        return tail ? launch<T, LD_FORWARD, true>(a, num_sms, s) : launch<T, LD_FORWARD, false>(a, num_sms, s);
+    if (op == LD_BACKWARD)
+        return tail ? launch<T, LD_BACKWARD, true>(a, num_sms, s) : launch<T, LD_BACKWARD, false>(a, num_sms, s);
+    return tail ? launch<T, LD_STEP, true>(a, num_sms, s) : launch<T, LD_STEP, false>(a, num_sms, s);
+}
+
+template <typename T, int OP, bool TAIL> cudaError_t set_smem()
+{
+    return cudaFuncSetAttribute(distill_kernel<T, OP, TAIL>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                LG_MAX_SLICES * (LG_SLICE / 8));
+}
+
+template <typename T> cudaError_t prepare()
+{
+    for (cudaError_t e : {set_smem<T, LD_FORWARD, true>(), set_smem<T, LD_BACKWARD, false>(),
+                          set_smem<T, LD_BACKWARD, true>(), set_smem<T, LD_STEP, false>(), set_smem<T, LD_STEP, true>()})
+        if (e != cudaSuccess)
+            return e;
+    return cudaSuccess;
+}
+
+} // namespace
+
+cudaError_t distill_topk_launch(DistillArgs a, int op, int dtype, int num_sms, cudaStream_t s)
+{
+    if (dtype == TIM_F32)
+        return launch_op<float>(a, op, num_sms, s);
+    if (dtype == TIM_BF16)
+        return launch_op<__nv_bfloat16>(a, op, num_sms, s);
+    return launch_op<__half>(a, op, num_sms, s);
+}
+
+cudaError_t distill_topk_prepare_device()
+{
+    for (cudaError_t e : {prepare<float>(), prepare<__nv_bfloat16>(), prepare<__half>()})
+        if (e != cudaSuccess)
+            return e;
+    return cudaSuccess;
+}
+
+} // namespace tim

@@ -1,0 +1,90 @@
+// logits_internal.h -- launch shapes and arguments of the operators on a head's
+// logits (processing, processed log-probability, distillation).  Not part of
+// the ABI.
+#pragma once
+
+#include <cstdint>
+
+#include <cuda_runtime.h>
+
+namespace tim {
+
+// A row of logits is cut into slices of 1024 columns.  One warp reduces a
+// slice, lane by lane in column order, and the slices' partials are folded in
+// slice order; nothing else enters a row's sums, so a row has the same bits
+// whatever the batch and however many CTAs share it.
+constexpr int LG_SLICE = 1024;
+constexpr int64_t LG_MAX_V = int64_t(1) << 20;
+constexpr int LG_MAX_SLICES = static_cast<int>(LG_MAX_V / LG_SLICE);
+constexpr int LG_CLUSTER = 8;                      // CTAs that share a row, at most
+
+inline int lg_slices(int64_t V) { return static_cast<int>((V + LG_SLICE - 1) / LG_SLICE); }
+
+// ---------------------------------------------------------------- processing
+constexpr int LP_THREADS = 512;
+constexpr int LP_WARPS = LP_THREADS / 32;
+constexpr int LP_SEG_SLICES = LP_WARPS;            // slices a CTA holds slots for at a time
+constexpr int LP_SEG = LP_SEG_SLICES * LG_SLICE;   // columns of a segment
+
+enum { LP_WRITE = 0, LP_LOGP = 1, LP_GRAD = 2 };
+
+struct ProcArgs {
+    const void *z;             // [N, V], rows ld apart
+    int64_t ld;
+    int32_t N, V;
+    const float *temperature, *repetition, *presence, *frequency;   // [N] or null
+    const int32_t *history;    // token ids, history_len of them
+    const int32_t *spans;      // [N][3]: begin, first generated token, end
+    int32_t history_len;
+    const int32_t *bias_offsets, *bias_ids;
+    const float *bias_values;
+    int32_t num_bias;
+    const uint32_t *allowed;   // [num_allowed][allowed_ld] bits
+    const int32_t *allowed_rows;
+    int64_t allowed_ld;
+    int32_t num_allowed;
+    const int32_t *targets;    // LOGP, GRAD
+    const float *grad, *lse;   // GRAD
+    void *out;                 // WRITE: processed logits; GRAD: gradient
+    int64_t ldo;
+    float *out_logp, *out_lse; // LOGP
+    int32_t seg_slices;        // WRITE, GRAD: slices of a CTA; LOGP: of a cluster rank
+    int32_t segs;              // CTAs of a row
+    int *status;
+};
+
+// dtype and out_dtype: TIM_F32 / TIM_BF16 / TIM_F16
+cudaError_t logits_process_launch(ProcArgs a, int op, int dtype, int out_dtype, int num_sms, cudaStream_t s);
+
+// ---------------------------------------------------------------- distillation
+constexpr int LD_THREADS = 512;
+constexpr int LD_WARPS = LD_THREADS / 32;
+constexpr int LD_MAX_K = 1024;
+
+enum { LD_FORWARD = 0, LD_BACKWARD = 1, LD_STEP = 2 };
+
+struct DistillArgs {
+    const void *z;
+    int64_t ld;
+    int32_t N, V, K;
+    const int32_t *ids;        // [N, K]
+    const float *teacher;      // [N, K]
+    const float *teacher_lse;  // [N] or null: renormalised over the K
+    float temperature;
+    const float *grad;         // [N]: BACKWARD, STEP
+    const float *lse, *lse_tail;              // BACKWARD
+    float *loss, *out_lse, *out_lse_tail;     // FORWARD, STEP
+    void *dz;                  // BACKWARD, STEP
+    int64_t ldo;
+    int32_t per;               // slices of a cluster rank
+    int32_t ranks;             // CTAs of a row
+    int *status;
+};
+
+cudaError_t distill_topk_launch(DistillArgs a, int op, int dtype, int num_sms, cudaStream_t s);
+
+// shared-memory sizes of the kernels above
+cudaError_t logits_process_prepare_device();
+cudaError_t distill_topk_prepare_device();
+
+} // namespace tim

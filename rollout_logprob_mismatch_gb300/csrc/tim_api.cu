@@ -15,6 +15,7 @@
 #include "ppo_internal.h"
 #include "k1_internal.h"
 #include "k2_internal.h"
+#include "logits_internal.h"
 #include "tim_internal.h"
 
 namespace {
@@ -106,7 +107,9 @@ int device_state(DeviceState **out)
     if ((e = cudaMemPoolSetAttribute(d.pool, cudaMemPoolAttrReleaseThreshold, &keep)) != cudaSuccess)
         return cuda_fail(e, "cudaMemPoolSetAttribute");
     if ((e = tim::k1_prepare_device()) != cudaSuccess || (e = tim::k2_prepare_device()) != cudaSuccess ||
-        (e = tim::monitor_prepare_device()) != cudaSuccess || (e = tim::gemm_prepare_device()) != cudaSuccess)
+        (e = tim::monitor_prepare_device()) != cudaSuccess || (e = tim::gemm_prepare_device()) != cudaSuccess ||
+        (e = tim::logits_process_prepare_device()) != cudaSuccess ||
+        (e = tim::distill_topk_prepare_device()) != cudaSuccess)
         return cuda_fail(e, "cudaFuncSetAttribute");
     if (!g_encode) {
         void *fn = nullptr;
@@ -208,6 +211,28 @@ namespace tim {
 cudaError_t status_word_address(int **out)
 {
     return cudaGetSymbolAddress(reinterpret_cast<void **>(out), g_status);
+}
+
+// Sets the current device up (device_state) and gives its status word and SM count.
+int use_device(int **status, int *sms)
+{
+    DeviceState *d = nullptr;
+    const int rc = device_state(&d);
+    if (rc == TIM_OK) {
+        *status = d->status;
+        *sms = d->sms;
+    }
+    return rc;
+}
+
+// Records a formatted message for tim_last_error() on the calling thread; returns code.
+int fail_message(int code, const char *fmt, ...)
+{
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(g_msg, sizeof g_msg, fmt, ap);
+    va_end(ap);
+    return code;
 }
 
 // Records a message for tim_last_error() on the calling thread; returns code.
