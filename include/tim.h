@@ -417,7 +417,8 @@ enum tim_dtype { TIM_F32 = 0, TIM_BF16 = 1, TIM_F16 = 2 };
  * Host struct; every pointer is a device pointer, and NULL leaves its rule out.
  *   temperature, repetition  fp32 [N], > 0, finite (and so 1 / x)
  *   presence, frequency      fp32 [N], finite
- *   history                  int32 [num_history]: token ids; ids outside [0, V) are skipped
+ *   history                  int32 [num_history], num_history < 2^30: token ids; ids
+ *                            outside [0, V) are skipped
  *   history_spans            int32 [N][3]: begin, first generated token, end of the
  *                            row's part of history, 0 <= begin <= generated <= end
  *                            <= num_history.  Rows may share tokens: the positions of a

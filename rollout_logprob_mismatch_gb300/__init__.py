@@ -717,8 +717,8 @@ class LogitsRules:
 
 
 def _int32_size(t, name):
-    if t.shape[0] >= 2 ** 31:
-        raise ValueError("%s must have fewer than 2^31 entries" % name)
+    if t.shape[0] >= 2 ** 30:
+        raise ValueError("%s must have fewer than 2^30 entries" % name)
     return t.shape[0]
 
 

@@ -31,7 +31,7 @@ struct Teacher {
     int id[LD_MAX_K];      // -1: not in use
     float q[LD_MAX_K];
     float logq[LD_MAX_K];
-    float t2[LD_MAX_K];    // the student's base-2 exponent at id
+    float y[LD_MAX_K];     // the student's z / tau at id
 };
 
 // log q of a listed id from t / tau = hi + lo and the teacher's log-sum-exp:
@@ -59,8 +59,8 @@ __global__ void __launch_bounds__(LD_THREADS) distill_kernel(const DistillArgs a
     const int c0 = s0 * LG_SLICE, c1 = min(a.V, s1 * LG_SLICE);
     const T *z = static_cast<const T *>(a.z) + row * a.ld;
     T *dz = GRAD ? static_cast<T *>(a.dz) + row * a.ldo : nullptr;
-    const bool vec = row_vec(z), vec_out = GRAD && row_vec(dz);
-    const float tau = a.temperature, k2 = LG_LOG2E / tau;
+    const uint32_t shift = row_shift(z), shift_out = GRAD ? row_shift(dz) : 0u;
+    const float tau = a.temperature, inv_tau = 1.f / tau, k2 = LG_LOG2E * inv_tau;
     float g = 0.f;
     if constexpr (GRAD)
         g = a.grad[row];
@@ -69,8 +69,8 @@ __global__ void __launch_bounds__(LD_THREADS) distill_kernel(const DistillArgs a
 
     auto zero_row = [&] {
         const float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        for (int col = c0 + static_cast<int>(threadIdx.x) * 8; col < c1; col += LD_THREADS * 8)
-            store8<T>(dz, col, c1, vec_out, v);
+        for (int b = c0 + warp * 256; b < c1; b += LD_WARPS * 256)
+            store8<T>(dz, b + lane * 8, c1, shift_out, v);
     };
     if constexpr (!SUMS) {
         if (g == 0.f) {
@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(LD_THREADS) distill_kernel(const DistillArgs a
         th.id[k] = id;
         th.logq[k] = id >= 0 ? a.teacher[at] : neg_inf();
         if (SUMS)
-            th.t2[k] = id >= 0 ? Elem<T>::load(z + id) * k2 : 0.f;
+            th.y[k] = id >= 0 ? __fmul_rn(Elem<T>::load(z + id), inv_tau) : 0.f;
     }
     __syncthreads();
     // (every warp finds the row's normaliser for itself)
@@ -104,9 +104,7 @@ __global__ void __launch_bounds__(LD_THREADS) distill_kernel(const DistillArgs a
         q_max = fmaxf(q_max, th.logq[k]);
     }
     any = __any_sync(0xffffffffu, any);
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1)
-        q_max = fmaxf(q_max, __shfl_xor_sync(0xffffffffu, q_max, d));
+    q_max = warp_max(q_max);
     float q_lse = 0.f;
     if constexpr (TAIL) {
         q_lse = a.teacher_lse[row];
@@ -114,9 +112,7 @@ __global__ void __launch_bounds__(LD_THREADS) distill_kernel(const DistillArgs a
         float s = 0.f;
         for (int k = lane; k < a.K; k += 32)
             s += th.id[k] >= 0 ? expf((th.logq[k] - finite_ref(q_max)) / tau) : 0.f;
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1)
-            s += __shfl_xor_sync(0xffffffffu, s, d);
+        s = warp_sum(s);
         any = any && s != 0.f;
         q_lse = logf(s);
     }
@@ -140,9 +136,7 @@ __global__ void __launch_bounds__(LD_THREADS) distill_kernel(const DistillArgs a
     if constexpr (TAIL) {
         for (int k = lane; k < a.K; k += 32)
             q_all += th.q[k];
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1)
-            q_all += __shfl_xor_sync(0xffffffffu, q_all, d);
+        q_all = warp_sum(q_all);
         q_rest = q_all <= 1.f ? 1.f - q_all : (q_all > 1.f ? 0.f : q_all);   // NaN stays
     }
 
@@ -154,33 +148,26 @@ __global__ void __launch_bounds__(LD_THREADS) distill_kernel(const DistillArgs a
             Raw8<T> raw[4];
 #pragma unroll
             for (int u = 0; u < 4; ++u)
-                load8<T>(raw[u], z, sl * LG_SLICE + u * 256 + lane * 8, a.V, vec);
-            float lm = neg_inf(), ls = 0.f, km = neg_inf(), ks = 0.f;
+                load8<T>(raw[u], z, sl * LG_SLICE + u * 256 + lane * 8, a.V, shift);
+            float lm, ls, km = neg_inf(), ks = 0.f;
+            if constexpr (TAIL) {   // the listed ones out of the stream, one by one
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const int col = sl * LG_SLICE + u * 256 + lane * 8;
-                float t[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    t[i] = Elem<T>::get(raw[u].w, i) * k2;
-                if constexpr (TAIL) {
+                for (int u = 0; u < 4; ++u) {
+                    const int col = sl * LG_SLICE + u * 256 + lane * 8;
                     const uint32_t bits =
                         col < a.V ? reinterpret_cast<const uint8_t *>(bitmap)[(col - c0) >> 3] : 0u;
                     if (bits) {
-                        float l[8];
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            l[i] = bits >> i & 1 ? t[i] : neg_inf();
-                            t[i] = bits >> i & 1 ? neg_inf() : t[i];
-                        }
-                        lane_add8(km, ks, l);
+                        for (int i = 0; i < 8; ++i)
+                            if (bits >> i & 1)
+                                join_value(km, ks, __fmul_rn(Elem<T>::get(raw[u].w, i), inv_tau));
+                        drop8(raw[u], bits);
                     }
                 }
-                lane_add8(lm, ls, t);
+                if (__any_sync(0xffffffffu, ks != 0.f))
+                    warp_join(km, ks);
             }
-            warp_join(lm, ls);
-            if constexpr (TAIL)
-                warp_join(km, ks);
+            warp_sums<T, 4>(raw, inv_tau, k2, lm, ls);
             if (lane == 0)
                 part[sl] = make_float4(lm, ls, km, ks);
         }
@@ -221,13 +208,11 @@ __global__ void __launch_bounds__(LD_THREADS) distill_kernel(const DistillArgs a
             float loss = 0.f;
             for (int k = lane; k < a.K; k += 32)
                 if (th.q[k] != 0.f)   // NaN goes on
-                    loss += th.q[k] * (th.logq[k] - row_logp(th.t2[k], m, s));
-#pragma unroll
-            for (int d = 16; d > 0; d >>= 1)
-                loss += __shfl_xor_sync(0xffffffffu, loss, d);
+                    loss = __fmaf_rn(th.q[k], th.logq[k] - row_logp(th.y[k], m, s), loss);
+            loss = warp_sum(loss);
             if constexpr (TAIL)
                 if (q_rest != 0.f)
-                    loss += q_rest * (logf(q_rest) - (sr == 0.f ? neg_inf() : ((mr - m) + (log2f(sr) - log2f(s))) * LG_LN2));
+                    loss += q_rest * (logf(q_rest) - (sr == 0.f ? neg_inf() : (mr - m) + (logf(sr) - logf(s))));
             if (lane == 0) {
                 a.loss[row] = loss;
                 a.out_lse[row] = row_lse(m, s);
@@ -242,14 +227,14 @@ __global__ void __launch_bounds__(LD_THREADS) distill_kernel(const DistillArgs a
             zero_row();
             return;
         }
-        // p_v = 2^(t_v - m) / s in a step, e^(z_v / tau - lse) from the forward's lse
+        // p_v = e^(y_v - m) / s in a step, e^(y_v - lse) from the forward's lse
         const float gi = g / tau;
         float lse = 0.f, inv_s = 0.f, w = any ? 1.f : 0.f;
         if constexpr (SUMS) {
             inv_s = s == 0.f ? 0.f : 1.f / s;
             m = finite_ref(m);
             if constexpr (TAIL)
-                w = sr == 0.f ? 0.f : 1.f - q_rest / (sr * exp2_approx(mr - m) * inv_s);
+                w = sr == 0.f ? 0.f : 1.f - q_rest / (sr * exp2_approx((mr - m) * LG_LOG2E) * inv_s);
         } else {
             lse = a.lse[row];
             if constexpr (TAIL) {
@@ -259,13 +244,8 @@ __global__ void __launch_bounds__(LD_THREADS) distill_kernel(const DistillArgs a
             if (lse == neg_inf())
                 lse = -neg_inf();
         }
-        const float inv_tau = 1.f / tau;
-        auto prob = [&](float x) {
-            if constexpr (SUMS)
-                return exp2_approx(x * k2 - m) * inv_s;
-            else
-                return exp2_approx(fmaf(x, inv_tau, -lse) * LG_LOG2E);
-        };
+        const float ref = SUMS ? m : lse, scale = SUMS ? inv_s : 1.f;
+        auto prob = [&](float x) { return exp2_approx(fmaf(x, inv_tau, -ref) * LG_LOG2E) * scale; };
         // the listed ids' values first: z may be overwritten in place
         constexpr int KPT = (LD_MAX_K + LD_THREADS - 1) / LD_THREADS;
         float own[KPT];
@@ -284,15 +264,25 @@ __global__ void __launch_bounds__(LD_THREADS) distill_kernel(const DistillArgs a
             }
         }
         __syncthreads();
-        const float wgi = w * gi;
-        for (int col = c0 + static_cast<int>(threadIdx.x) * 8; col < c1; col += LD_THREADS * 8) {
-            Raw8<T> raw;
-            load8<T>(raw, z, col, c1, vec);
-            float v[8];
+        const float wgi = w * gi * scale;
+        const Pair inv2 = pair(inv_tau, inv_tau), ref2 = pair(-ref, -ref), e2 = pair(LG_LOG2E, LG_LOG2E),
+                   w2 = pair(wgi, wgi);
+        for (int b = c0 + warp * 512; b < c1; b += LD_WARPS * 512) {
+            Raw8<T> raw[2];
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                v[i] = prob(Elem<T>::get(raw.w, i)) * wgi;
-            store8<T>(dz, col, c1, vec_out, v);
+            for (int u = 0; u < 2; ++u)
+                load8<T>(raw[u], z, b + u * 256 + lane * 8, c1, shift);
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                float v[8];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    float lo, hi;
+                    unpair(mul2(fma2(get2<T>(raw[u], k), inv2, ref2), e2), lo, hi);
+                    unpair(mul2(pair(exp2_approx(lo), exp2_approx(hi)), w2), v[2 * k], v[2 * k + 1]);
+                }
+                store8<T>(dz, b + u * 256 + lane * 8, c1, shift_out, v);
+            }
         }
         __syncthreads();
 #pragma unroll

@@ -21,10 +21,10 @@ constexpr int LG_CLUSTER = 8;                      // CTAs that share a row, at 
 inline int lg_slices(int64_t V) { return static_cast<int>((V + LG_SLICE - 1) / LG_SLICE); }
 
 // ---------------------------------------------------------------- processing
-constexpr int LP_THREADS = 512;
+constexpr int LP_THREADS = 384;
 constexpr int LP_WARPS = LP_THREADS / 32;
-constexpr int LP_SEG_SLICES = LP_WARPS;            // slices a CTA holds slots for at a time
-constexpr int LP_SEG = LP_SEG_SLICES * LG_SLICE;   // columns of a segment
+constexpr int LP_CAP = 8192;                       // touched columns a table holds (a multiple of LG_SLICE)
+constexpr int LP_TABLE = 1 << 18;                  // columns a table covers
 
 enum { LP_WRITE = 0, LP_LOGP = 1, LP_GRAD = 2 };
 
@@ -50,6 +50,7 @@ struct ProcArgs {
     float *out_logp, *out_lse; // LOGP
     int32_t seg_slices;        // WRITE, GRAD: slices of a CTA; LOGP: of a cluster rank
     int32_t segs;              // CTAs of a row
+    int32_t table_columns;     // columns the shared-memory table has room for
     int *status;
 };
 

@@ -14,21 +14,25 @@
 //
 // What bounds it: every operation streams the row (and its mask, V / 8 bytes)
 // once; only the few touched columns (history and biased ids) need more.  So the
-// columns are treated as untouched, with one multiplication each, and the
-// touched ones are replaced from a table in shared memory: a CTA owns a segment
-// of at most 16384 columns with one 4-byte slot each (64 KB, so that two CTAs fit an
-// SM and one's table phase runs under the other's loads).  It scans the row's
-// history three times: the slots of its ids are set to zero, then counted with
-// shared-memory atomics (integers: no order), then one thread per distinct id
-// (the one that sets its bit in a bitmap) turns the count into the column's
-// final value.  Nothing has to be cleared between segments, no sort, no hash, any
-// history length.  The first slice of each warp is loaded before the scans.
+// columns are streamed as if none were touched, and a table in shared memory
+// holds the touched ones: a bitmap of the CTA's columns, the number of bits
+// before each of its words, and one 4-byte entry per touched column, in column
+// order.  Building it takes two scans of the row's history (set the bits; count
+// with shared-memory integer atomics, which have no order) and one gather per
+// distinct id; no sort, no hash, any history length (a history that could fill
+// more than LP_CAP entries is handled LP_CAP columns at a time).  The log-probability
+// takes the touched columns out of the stream and adds the table's entries of the
+// same slice; the others write their columns first and the touched ones over them.
 #include <algorithm>
 
 #include "logits_rows.cuh"
 
 namespace tim {
 namespace {
+
+// A table entry while it is counted: seen in the prompt, listed with a bias, and
+// the number of times among the generated tokens (the host keeps it below 2^30).
+constexpr uint32_t kPrompt = 0x80000000u, kBiased = 0x40000000u, kCount = 0x3fffffffu;
 
 struct RowRules {
     float tau, inv_tau, rho, pres, freq;
@@ -66,7 +70,7 @@ __device__ __forceinline__ RowRules row_rules(const ProcArgs &a, int row)
         r.bad = true;
         r.h0 = r.hg = r.h1 = 0;
     }
-    if (r.b0 < 0 || r.b1 < r.b0 || r.b1 > a.num_bias) {
+    if (r.b0 < 0 || r.b1 < r.b0 || r.b1 > a.num_bias || r.b1 - r.b0 > a.V) {
         r.bad = true;
         r.b0 = r.b1 = 0;
     }
@@ -87,116 +91,167 @@ __device__ __forceinline__ float touched_value(const RowRules &r, float z, float
         slope = x > 0.f ? 1.f / r.rho : r.rho;
         x = x > 0.f ? x / r.rho : x * r.rho;
     }
-    const uint32_t c = word & 0x7fffffffu;
+    const uint32_t c = word & kCount;
     if (c != 0)
         x = x - r.freq * static_cast<float>(c) - r.pres;
     slope /= r.tau;
     return x / r.tau;
 }
 
-__device__ __forceinline__ float bias_of(const ProcArgs &a, const RowRules &r, int id)
+// ---------------------------------------------------------------- touched columns
+struct Table {
+    uint32_t *value;     // [LP_CAP]: counts, then the column's replacement (fp32 bits)
+    uint32_t *bitmap;    // [LP_TABLE / 32]
+    uint16_t *before;    // [LP_TABLE / 32]: bits set in the words before
+    int words, used;     // of the columns in hand
+};
+
+__device__ __forceinline__ int rank_of(const Table &t, unsigned k)
 {
-    int lo = r.b0, hi = r.b1;
+    const uint32_t w = t.bitmap[k >> 5];
+    return t.before[k >> 5] + __popc(w & ((1u << (k & 31)) - 1));
+}
+
+// Column (relative to the table's first) of entry n.
+__device__ __forceinline__ int column_of(const Table &t, int n)
+{
+    int lo = 0, hi = t.words - 1;   // the last word with before <= n
     while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (a.bias_ids[mid] < id)
-            lo = mid + 1;
+        const int mid = (lo + hi + 1) >> 1;
+        if (t.before[mid] <= n)
+            lo = mid;
         else
-            hi = mid;
+            hi = mid - 1;
     }
-    return lo < r.b1 && a.bias_ids[lo] == id ? a.bias_values[lo] : 0.f;
+    uint32_t w = t.bitmap[lo];
+    for (int skip = n - t.before[lo]; skip > 0; --skip)
+        w &= w - 1;
+    return lo * 32 + __ffs(static_cast<int>(w)) - 1;
 }
 
-// Fills the table of columns c0 .. c0 + width - 1: bit set and slot = the
-// replacement, as op needs it.  All threads of the CTA.
-template <typename T, int OP>
-__device__ void fill_table(const ProcArgs &a, const RowRules &r, const T *z, int c0, int width, uint32_t *slot,
-                           uint32_t *bitmap, int target, float g, float lse)
+// f(position, id relative to c0) for the entries ids[j0 .. j1) within [c0, c0 + width).
+template <typename F>
+__device__ __forceinline__ void scan_ids(const int32_t *ids, int j0, int j1, int c0, int width, F f)
 {
-    const unsigned w = static_cast<unsigned>(width);
-    for (int j = threadIdx.x; j < (width + 31) / 32; j += LP_THREADS)
-        bitmap[j] = 0;
-    for (int j = r.h0 + static_cast<int>(threadIdx.x); j < r.h1; j += LP_THREADS) {
-        const unsigned k = static_cast<unsigned>(a.history[j]) - static_cast<unsigned>(c0);
-        if (k < w)
-            slot[k] = 0;
+    for (int j = j0 + static_cast<int>(threadIdx.x); j < j1; j += LP_THREADS) {
+        const unsigned k = static_cast<unsigned>(ids[j]) - static_cast<unsigned>(c0);
+        if (k < static_cast<unsigned>(width))
+            f(j, k);
     }
-    for (int j = r.b0 + static_cast<int>(threadIdx.x); j < r.b1; j += LP_THREADS) {
-        const unsigned k = static_cast<unsigned>(a.bias_ids[j]) - static_cast<unsigned>(c0);
-        if (k < w)
-            slot[k] = 0;
-    }
-    __syncthreads();
-    for (int j = r.h0 + static_cast<int>(threadIdx.x); j < r.h1; j += LP_THREADS) {
-        const unsigned k = static_cast<unsigned>(a.history[j]) - static_cast<unsigned>(c0);
-        if (k < w) {
-            if (j >= r.hg)
-                atomicAdd(slot + k, 1u);
-            else
-                atomicOr(slot + k, 0x80000000u);
-        }
-    }
-    __syncthreads();
-    auto claim = [&](unsigned k, int id, float bias) {
-        float slope;
-        float y = touched_value(r, Elem<T>::load(z + id), bias, slot[k], slope);
-        if constexpr (OP == LP_LOGP)
-            y *= LG_LOG2E;
-        if constexpr (OP == LP_GRAD) {
-            const float p = exp2_approx((y - lse) * LG_LOG2E);
-            y = y == neg_inf() ? 0.f : ((id == target ? 1.f : 0.f) - p) * (g * slope);
-        }
-        slot[k] = __float_as_uint(y);
-    };
-    for (int j = r.h0 + static_cast<int>(threadIdx.x); j < r.h1; j += LP_THREADS) {
-        const int id = a.history[j];
-        const unsigned k = static_cast<unsigned>(id) - static_cast<unsigned>(c0);
-        if (k < w) {
-            const uint32_t bit = 1u << (k & 31);
-            if (!(atomicOr(bitmap + (k >> 5), bit) & bit))
-                claim(k, id, r.b1 > r.b0 ? bias_of(a, r, id) : 0.f);
-        }
-    }
-    for (int j = r.b0 + static_cast<int>(threadIdx.x); j < r.b1; j += LP_THREADS) {
-        const int id = a.bias_ids[j];
-        const unsigned k = static_cast<unsigned>(id) - static_cast<unsigned>(c0);
-        if (k < w) {
-            const uint32_t bit = 1u << (k & 31);
-            if (!(atomicOr(bitmap + (k >> 5), bit) & bit))
-                claim(k, id, a.bias_values[j]);
-        }
-    }
-    __syncthreads();
 }
 
-// Whether any of the row's bias ids is out of range or out of order (all
-// threads; a barrier).
-__device__ __forceinline__ bool bias_bad(const ProcArgs &a, const RowRules &r)
+// Builds the table of columns c0 .. c0 + width - 1 with replacement(id, y, slope)
+// for each.  All threads of the CTA; false (in all) where the row's bias ids are
+// out of range or order.  Ends with a barrier.
+template <typename T, typename F>
+__device__ bool build_table(const ProcArgs &a, const RowRules &r, const T *z, int c0, int width, Table &t, F replacement)
 {
+    __shared__ int warp_bits[LP_WARPS];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    t.words = (width + 31) / 32;
+    for (int j = threadIdx.x; j < t.words; j += LP_THREADS)
+        t.bitmap[j] = 0;
+    for (int j = threadIdx.x; j < min(LP_CAP, r.h1 - r.h0 + r.b1 - r.b0); j += LP_THREADS)
+        t.value[j] = 0;
     bool bad = false;
     for (int j = r.b0 + static_cast<int>(threadIdx.x); j < r.b1; j += LP_THREADS) {
         const int id = a.bias_ids[j];
         bad |= id < 0 || id >= a.V || (j > r.b0 && a.bias_ids[j - 1] >= id);
     }
-    return __syncthreads_or(bad) != 0;
+    if (__syncthreads_or(bad))
+        return false;
+    auto mark = [&](int, unsigned k) { atomicOr(t.bitmap + (k >> 5), 1u << (k & 31)); };
+    scan_ids(a.history, r.h0, r.h1, c0, width, mark);
+    scan_ids(a.bias_ids, r.b0, r.b1, c0, width, mark);
+    __syncthreads();
+    // bits before each word: a run of words per thread
+    const int run = (t.words + LP_THREADS - 1) / LP_THREADS;
+    const int w0 = min(t.words, static_cast<int>(threadIdx.x) * run), w1 = min(t.words, w0 + run);
+    int bits = 0;
+    for (int w = w0; w < w1; ++w)
+        bits += __popc(t.bitmap[w]);
+    int upto = bits;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, upto, d);
+        upto += lane >= d ? v : 0;
+    }
+    if (lane == 31)
+        warp_bits[warp] = upto;
+    __syncthreads();
+    int base = upto - bits;
+    t.used = 0;
+#pragma unroll
+    for (int w = 0; w < LP_WARPS; ++w) {
+        base += w < warp ? warp_bits[w] : 0;
+        t.used += warp_bits[w];
+    }
+    for (int w = w0; w < w1; ++w) {
+        t.before[w] = static_cast<uint16_t>(base);
+        base += __popc(t.bitmap[w]);
+    }
+    __syncthreads();
+    scan_ids(a.history, r.h0, r.h1, c0, width, [&](int j, unsigned k) {
+        uint32_t *v = t.value + rank_of(t, k);
+        if (j >= r.hg)
+            atomicAdd(v, 1u);
+        else
+            atomicOr(v, kPrompt);
+    });
+    scan_ids(a.bias_ids, r.b0, r.b1, c0, width, [&](int, unsigned k) { atomicOr(t.value + rank_of(t, k), kBiased); });
+    __syncthreads();
+    auto finish = [&](int n, int id, float bias) {
+        float slope;
+        float y = touched_value(r, Elem<T>::load(z + id), bias, t.value[n] & ~kBiased, slope);
+        if (r.mask && !(r.mask[id >> 3] >> (id & 7) & 1))
+            y = neg_inf();
+        t.value[n] = __float_as_uint(replacement(id, y, slope));
+    };
+    for (int n = threadIdx.x; n < t.used; n += LP_THREADS)
+        if (!(t.value[n] & kBiased))
+            finish(n, c0 + column_of(t, n), 0.f);
+    __syncthreads();
+    if (r.b1 > r.b0) {   // the biased ones, by their bias entry
+        scan_ids(a.bias_ids, r.b0, r.b1, c0, width,
+                 [&](int j, unsigned k) { finish(rank_of(t, k), c0 + static_cast<int>(k), a.bias_values[j]); });
+        __syncthreads();
+    }
+    return true;
 }
 
+// Columns a table covers at a time.
+__device__ __forceinline__ int table_step(const RowRules &r)
+{
+    return r.h1 - r.h0 + r.b1 - r.b0 <= LP_CAP ? LP_TABLE : LP_CAP;
+}
+
+__device__ __forceinline__ Table carve(uint32_t *smem, int table_columns)
+{
+    Table t;
+    t.value = smem;
+    t.bitmap = smem + LP_CAP;
+    t.before = reinterpret_cast<uint16_t *>(t.bitmap + table_columns / 32);
+    t.words = t.used = 0;
+    return t;
+}
+
+// ---------------------------------------------------------------- kernels
 // WRITE and GRAD: one CTA per (row, segment); no column depends on another.
 template <typename T, typename TO, int OP, bool TOUCH>
 __global__ void __launch_bounds__(LP_THREADS) process_map_kernel(const ProcArgs a)
 {
     extern __shared__ uint32_t smem[];
-    uint32_t *slot = smem, *bitmap = smem + LP_SEG;
     const int row = static_cast<int>(blockIdx.x / static_cast<unsigned>(a.segs));
     const int seg = static_cast<int>(blockIdx.x % static_cast<unsigned>(a.segs));
-    const int c0 = seg * a.seg_slices * LG_SLICE;
-    const int c1 = min(a.V, c0 + a.seg_slices * LG_SLICE);
+    const int seg0 = seg * a.seg_slices * LG_SLICE, seg1 = min(a.V, seg0 + a.seg_slices * LG_SLICE);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const T *z = static_cast<const T *>(a.z) + row * a.ld;
     TO *out = static_cast<TO *>(a.out) + row * a.ldo;
-    const bool vec = row_vec(z), vec_out = row_vec(out);
+    const uint32_t shift = row_shift(z), shift_out = row_shift(out);
 
-    RowRules r = row_rules(a, row);
-    float g = 1.f, lse = 0.f;
+    const RowRules r = row_rules(a, row);
+    bool bad = r.bad;
+    float g = 1.f, lse = 0.f, target_v = 0.f;
     int target = -1;
     if constexpr (OP == LP_GRAD) {
         g = a.grad[row];
@@ -205,184 +260,226 @@ __global__ void __launch_bounds__(LP_THREADS) process_map_kernel(const ProcArgs 
             lse = -neg_inf();   // nothing is left of the row: every probability is 0
         target = a.targets[row];
     }
-    if constexpr (TOUCH)
-        r.bad |= bias_bad(a, r);
-    if (r.bad || (OP == LP_GRAD && g == 0.f)) {
-        float v[8];
-        const float fill = r.bad ? quiet_nan() : 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            v[i] = fill;
-        for (int col = c0 + static_cast<int>(threadIdx.x) * 8; col < c1; col += LP_THREADS * 8)
-            store8<TO>(out, col, c1, vec_out, v);
-        if (r.bad && threadIdx.x == 0)
-            report_bad_input(a.status);
-        return;
-    }
-    if constexpr (TOUCH)
-        fill_table<T, OP>(a, r, z, c0, c1 - c0, slot, bitmap, target, g, lse);
-
+    auto probability = [&](float y) { return exp2_approx((y - lse) * LG_LOG2E); };
     const float gi = g * r.inv_tau;
-    for (int col = c0 + static_cast<int>(threadIdx.x) * 8; col < c1; col += LP_THREADS * 8) {
-        Raw8<T> raw;
-        load8<T>(raw, z, col, c1, vec);
-        float v[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float x = Elem<T>::get(raw.w, i);
-            if constexpr (OP == LP_WRITE) {
-                v[i] = x * r.inv_tau;
-            } else {
-                const float p = exp2_approx(fmaf(x, r.inv_tau, -lse) * LG_LOG2E);
-                v[i] = -p * gi;
-                if (col + i == target)
-                    v[i] = x == neg_inf() ? 0.f : (1.f - p) * gi;
+    const int step = TOUCH ? table_step(r) : LP_TABLE;
+    Table t = carve(smem, a.table_columns);
+    for (int c0 = seg0; c0 < seg1; c0 += step) {
+        const int c1 = min(seg1, c0 + step);
+        const bool zero = OP == LP_GRAD && g == 0.f;
+        const bool has_target = OP == LP_GRAD && target >= c0 && target < c1;
+        if constexpr (OP == LP_GRAD) {
+            if (has_target && threadIdx.x == 0) {   // an untouched target's one-hot term
+                const float x = Elem<T>::load(z + target);
+                const bool in = !r.mask || (r.mask[target >> 3] >> (target & 7) & 1);
+                target_v = in && x != neg_inf() ? (1.f - exp2_approx(fmaf(x, r.inv_tau, -lse) * LG_LOG2E)) * gi : 0.f;
             }
+            if constexpr (!TOUCH)
+                __syncthreads();   // read before it is written over in place
         }
         if constexpr (TOUCH) {
-            const int k = col - c0;
-            const uint32_t bits = reinterpret_cast<const uint8_t *>(bitmap)[k >> 3];
-            if (bits) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (bits >> i & 1)
-                        v[i] = __uint_as_float(slot[k + i]);
+            if (!bad && !zero) {
+                if (c0 != seg0)
+                    __syncthreads();   // the table before has been written out
+                bad = !build_table(a, r, z, c0, c1 - c0, t, [&](int id, float y, float slope) {
+                    if constexpr (OP == LP_GRAD)
+                        return y == neg_inf() ? 0.f : ((id == target ? 1.f : 0.f) - probability(y)) * (g * slope);
+                    else
+                        return y;
+                });
             }
         }
-        if (r.mask) {
-            const uint32_t bits = r.mask[col >> 3];
+        if (bad || zero) {
+            float v[8];
+            const float fill = bad ? quiet_nan() : 0.f;
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                if (!(bits >> i & 1))
-                    v[i] = OP == LP_WRITE ? neg_inf() : 0.f;
+                v[i] = fill;
+            for (int b = c0 + warp * 256; b < c1; b += LP_WARPS * 256)
+                store8<TO>(out, b + lane * 8, c1, shift_out, v);
+            continue;
         }
-        store8<TO>(out, col, c1, vec_out, v);
+        const Pair inv2 = pair(r.inv_tau, r.inv_tau), lse2 = pair(-lse, -lse), e2 = pair(LG_LOG2E, LG_LOG2E),
+                   g2 = pair(-gi, -gi);
+        for (int b = c0 + warp * 512; b < c1; b += LP_WARPS * 512) {
+            Raw8<T> raw[2];
+            uint32_t ok[2] = {0xffu, 0xffu};
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int col = b + u * 256 + lane * 8;
+                load8<T>(raw[u], z, col, c1, shift);
+                if (r.mask && col < c1)
+                    ok[u] = r.mask[col >> 3];
+            }
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                float v[8];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const Pair x = get2<T>(raw[u], k);
+                    if constexpr (OP == LP_WRITE) {
+                        unpair(mul2(x, inv2), v[2 * k], v[2 * k + 1]);
+                    } else {
+                        float lo, hi;
+                        unpair(mul2(fma2(x, inv2, lse2), e2), lo, hi);
+                        unpair(mul2(pair(exp2_approx(lo), exp2_approx(hi)), g2), v[2 * k], v[2 * k + 1]);
+                    }
+                }
+                if (ok[u] != 0xffu) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (!(ok[u] >> i & 1))
+                            v[i] = OP == LP_WRITE ? neg_inf() : 0.f;
+                }
+                store8<TO>(out, b + u * 256 + lane * 8, c1, shift_out, v);
+            }
+        }
+        if (TOUCH || OP == LP_GRAD) {
+            __syncthreads();   // the touched columns go over what has just been written
+            if (OP == LP_GRAD && has_target && threadIdx.x == 0 &&
+                !(TOUCH && (t.bitmap[(target - c0) >> 5] >> ((target - c0) & 31) & 1)))
+                out[target] = Elem<TO>::from(target_v);
+        }
+        if constexpr (TOUCH) {
+            for (int n = threadIdx.x; n < t.used; n += LP_THREADS)
+                out[c0 + column_of(t, n)] = Elem<TO>::from(__uint_as_float(t.value[n]));
+        }
     }
+    if (bad && threadIdx.x == 0)
+        report_bad_input(a.status);
 }
 
 // LOGP: a cluster per row; each rank reduces seg_slices slices, one warp per
-// slice, in segments of at most LP_SEG_SLICES where there is a table.  The
-// slices' partials go to rank 0's shared memory, which folds them.
+// slice.  The slices' partials go to rank 0's shared memory, which folds them.
 template <typename T, bool TOUCH>
 __global__ void __launch_bounds__(LP_THREADS) process_logp_kernel(const ProcArgs a)
 {
     extern __shared__ uint32_t smem[];
-    uint32_t *slot = smem, *bitmap = smem + LP_SEG;
     __shared__ float2 part[LG_MAX_SLICES];
-    __shared__ float target_t;
+    __shared__ float target_y;
     const int rank = static_cast<int>(cluster_ctarank());
     const int row = static_cast<int>(blockIdx.x / static_cast<unsigned>(a.segs));
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int slices = (a.V + LG_SLICE - 1) / LG_SLICE;
     const int s0 = min(slices, rank * a.seg_slices), s1 = min(slices, s0 + a.seg_slices);
     const T *z = static_cast<const T *>(a.z) + row * a.ld;
-    const bool vec = row_vec(z);
-    cluster_arrive();   // waited for before the first store into rank 0's shared memory
+    const uint32_t shift = row_shift(z);
+    if (a.segs > 1)
+        cluster_arrive();   // waited for before the first store into rank 0's shared memory
 
-    RowRules r = row_rules(a, row);
+    const RowRules r = row_rules(a, row);
+    bool bad = r.bad;
     const int target = a.targets[row];
-    if constexpr (TOUCH)
-        r.bad |= bias_bad(a, r);
-    const float k2 = LG_LOG2E / r.tau;
-    const int step = TOUCH ? LP_SEG_SLICES : LG_MAX_SLICES;
-    for (int f0 = s0; f0 < s1 && !r.bad; f0 += step) {
+    const bool has_target = target >= s0 * LG_SLICE && target < min(a.V, s1 * LG_SLICE);
+    const float k2 = LG_LOG2E * r.inv_tau;
+    const int step = (TOUCH ? table_step(r) : LP_TABLE) / LG_SLICE;
+    Table t = carve(smem, a.table_columns);
+    for (int f0 = s0; f0 < s1 && !bad; f0 += step) {
         const int f1 = min(s1, f0 + step);
         const int c0 = f0 * LG_SLICE;
         if constexpr (TOUCH) {
             if (f0 != s0)
-                __syncthreads();   // the segment before has been read
-            fill_table<T, LP_LOGP>(a, r, z, c0, min(a.V, f1 * LG_SLICE) - c0, slot, bitmap, target, 0.f, 0.f);
+                __syncthreads();   // the table before has been read
+            bad = !build_table(a, r, z, c0, min(a.V, f1 * LG_SLICE) - c0, t, [](int, float y, float) { return y; });
+            if (bad)
+                break;
+        }
+        if (threadIdx.x == 0 && target >= c0 && target < min(a.V, f1 * LG_SLICE)) {
+            if (TOUCH && (t.bitmap[(target - c0) >> 5] >> ((target - c0) & 31) & 1)) {
+                target_y = __uint_as_float(t.value[rank_of(t, target - c0)]);
+            } else {
+                const bool in = !r.mask || (r.mask[target >> 3] >> (target & 7) & 1);
+                target_y = in ? __fmul_rn(Elem<T>::load(z + target), r.inv_tau) : neg_inf();
+            }
         }
         for (int s = f0 + warp; s < f1; s += LP_WARPS) {
             Raw8<T> raw[4];
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-                load8<T>(raw[u], z, s * LG_SLICE + u * 256 + lane * 8, a.V, vec);
-            float m = neg_inf(), sum = 0.f;
+            uint32_t drop[4];
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
                 const int col = s * LG_SLICE + u * 256 + lane * 8;
-                float t[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    t[i] = Elem<T>::get(raw[u].w, i) * k2;
-                if (TOUCH && col < a.V) {
-                    const int k = col - c0;
-                    const uint32_t bits = reinterpret_cast<const uint8_t *>(bitmap)[k >> 3];
-                    if (bits) {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            if (bits >> i & 1)
-                                t[i] = __uint_as_float(slot[k + i]);
-                    }
-                }
-                if (r.mask && col < a.V) {
-                    const uint32_t bits = r.mask[col >> 3];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        if (!(bits >> i & 1))
-                            t[i] = neg_inf();
-                }
-                if (static_cast<unsigned>(target) - static_cast<unsigned>(col) < 8u) {
-                    float v = t[0];
-#pragma unroll
-                    for (int i = 1; i < 8; ++i)
-                        v = target - col == i ? t[i] : v;
-                    target_t = v;
-                }
-                lane_add8(m, sum, t);
+                load8<T>(raw[u], z, col, a.V, shift);
+                drop[u] = r.mask && col < a.V ? ~static_cast<uint32_t>(r.mask[col >> 3]) & 0xffu : 0u;
             }
-            warp_join(m, sum);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int col = s * LG_SLICE + u * 256 + lane * 8;
+                if (TOUCH && col < a.V)
+                    drop[u] |= reinterpret_cast<const uint8_t *>(t.bitmap)[(col - c0) >> 3];
+                if (drop[u])
+                    drop8(raw[u], drop[u]);
+            }
+            float m, sum;
+            warp_sums<T, 4>(raw, r.inv_tau, k2, m, sum);
+            if constexpr (TOUCH) {
+                const int word = (s - f0) * (LG_SLICE / 32);
+                const int n0 = t.before[word], n1 = word + LG_SLICE / 32 < t.words ? t.before[word + LG_SLICE / 32] : t.used;
+                if (n1 > n0) {
+                    float tm = neg_inf(), ts = 0.f;
+                    for (int n = n0 + lane; n < n1; n += 32)
+                        join_value(tm, ts, __uint_as_float(t.value[n]));
+                    warp_join(tm, ts);
+                    join(m, sum, tm, ts);
+                }
+            }
             if (lane == 0)
                 part[s] = make_float2(m, sum);
         }
     }
     __syncthreads();
-    cluster_wait();
-    if (rank != 0) {
-        const uint32_t part0 = mapa_shared(smem_u32(part), 0);
-        for (int s = s0 + static_cast<int>(threadIdx.x); s < s1; s += LP_THREADS)
-            st_cluster_f2(part0 + s * 8, part[s].x, part[s].y);
-        if (threadIdx.x == 0 && target >= s0 * LG_SLICE && target < s1 * LG_SLICE)
-            st_shared_cluster(mapa_shared(smem_u32(&target_t), 0), __float_as_int(target_t));
+    if (a.segs > 1) {
+        cluster_wait();
+        if (rank != 0) {
+            const uint32_t part0 = mapa_shared(smem_u32(part), 0);
+            for (int s = s0 + static_cast<int>(threadIdx.x); s < s1; s += LP_THREADS)
+                st_cluster_f2(part0 + s * 8, part[s].x, part[s].y);
+            if (threadIdx.x == 0 && has_target)
+                st_shared_cluster(mapa_shared(smem_u32(&target_y), 0), __float_as_int(target_y));
+        }
+        __syncwarp();
+        cluster_arrive();
+        cluster_wait();
     }
-    __syncwarp();
-    cluster_arrive();
-    cluster_wait();
     if (rank == 0 && warp == 0) {
         float m = neg_inf(), sum = 0.f;
-        if (!r.bad)
-            fold_slices(part, slices, lane, m, sum);
+        if (!bad) {   // in slice order: lane l takes slices l, l + 32, ...
+            for (int s = lane; s < slices; s += 32)
+                join(m, sum, part[s].x, part[s].y);
+            warp_join(m, sum);
+        }
         if (lane == 0) {
             const bool in = target >= 0 && target < a.V;
-            a.out_lse[row] = r.bad ? quiet_nan() : row_lse(m, sum);
-            a.out_logp[row] = r.bad || !in ? quiet_nan() : row_logp(target_t, m, sum);
-            if (r.bad)
+            a.out_lse[row] = bad ? quiet_nan() : row_lse(m, sum);
+            a.out_logp[row] = bad || !in ? quiet_nan() : row_logp(target_y, m, sum);
+            if (bad)
                 report_bad_input(a.status);
         }
     }
 }
 
-constexpr int kTableBytes = (LP_SEG + LP_SEG / 32) * 4;
+// Dynamic shared memory of a table over `columns` columns (a multiple of 1024).
+size_t table_bytes(int columns) { return LP_CAP * 4 + columns / 32 * 6; }
 
 template <typename F> cudaError_t set_smem(F *kernel)
 {
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kTableBytes);
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                static_cast<int>(table_bytes(LP_TABLE)));
 }
 
 template <typename T, typename TO, int OP> cudaError_t launch_map(ProcArgs a, int num_sms, cudaStream_t s)
 {
     const bool touch = a.spans || a.bias_offsets;
     const int slices = lg_slices(a.V);
-    // segments of 16 slices; fewer while the rows alone do not give the GPU two CTAs per SM
-    int per = std::min(LP_SEG_SLICES, slices);
-    while (per > 4 && static_cast<int64_t>(a.N) * ((slices + per - 1) / per) < 2 * num_sms)
+    // segments of at most 64 slices, fewer while there are not four CTAs for every SM
+    int per = std::min(64, slices);
+    while (per > 4 && static_cast<int64_t>(a.N) * ((slices + per - 1) / per) < 4 * num_sms)
         per = (per + 1) / 2;
     a.seg_slices = per;
     a.segs = (slices + per - 1) / per;
+    a.table_columns = std::min(LP_TABLE, per * LG_SLICE);
     const unsigned grid = static_cast<unsigned>(a.N) * static_cast<unsigned>(a.segs);
     if (touch)
-        process_map_kernel<T, TO, OP, true><<<grid, LP_THREADS, kTableBytes, s>>>(a);
+        process_map_kernel<T, TO, OP, true><<<grid, LP_THREADS, table_bytes(a.table_columns), s>>>(a);
     else
         process_map_kernel<T, TO, OP, false><<<grid, LP_THREADS, 0, s>>>(a);
     return cudaGetLastError();
@@ -393,14 +490,15 @@ template <typename T> cudaError_t launch_logp(ProcArgs a, int num_sms, cudaStrea
     const bool touch = a.spans || a.bias_offsets;
     const int slices = lg_slices(a.V);
     int ranks = 1;   // CTAs of a row: more while the rows alone leave SMs idle
-    while (ranks < LG_CLUSTER && ranks * 2 <= slices && static_cast<int64_t>(a.N) * ranks < 2 * num_sms)
+    while (ranks < LG_CLUSTER && ranks * 2 <= slices && static_cast<int64_t>(a.N) * ranks < 4 * num_sms)
         ranks *= 2;
     a.segs = ranks;
     a.seg_slices = (slices + ranks - 1) / ranks;
+    a.table_columns = std::min(LP_TABLE, a.seg_slices * LG_SLICE);
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(a.N) * static_cast<unsigned>(ranks));
     cfg.blockDim = dim3(LP_THREADS);
-    cfg.dynamicSmemBytes = touch ? kTableBytes : 0;
+    cfg.dynamicSmemBytes = touch ? table_bytes(a.table_columns) : 0;
     cfg.stream = s;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;

@@ -2,10 +2,10 @@
 // eight columns of a row at a time (any element type, any alignment), and the
 // reduction of a slice of a row to (maximum, sum of exponentials).
 //
-// Log-sum-exp of a row, in base 2: with t_v = x_v log2(e), a set of columns is
-// the pair (M, S), M = max t, S = sum 2^(t - M); two sets join as
-// M = max(M1, M2), S = S1 2^(M1 - M) + S2 2^(M2 - M); lse = (M + log2 S) ln 2.
-// A set of -inf columns only is (-inf, 0).  NaN and +inf make S NaN.
+// Log-sum-exp: a set of columns with values y is the pair (M, S), M = max y,
+// S = sum e^(y - M); two sets join as M = max(M1, M2), S = S1 e^(M1 - M) +
+// S2 e^(M2 - M); lse = M + log S.  A set of -inf columns only is (-inf, 0).  NaN
+// and +inf make S NaN.
 #pragma once
 
 #include <cstdint>
@@ -21,7 +21,6 @@
 namespace tim {
 
 constexpr float LG_LOG2E = 1.4426950408889634f;
-constexpr float LG_LN2 = 0.6931471805599453f;
 
 __device__ __forceinline__ float neg_inf() { return __int_as_float(static_cast<int>(0xff800000u)); }
 __device__ __forceinline__ float quiet_nan() { return __int_as_float(0x7fc00000); }
@@ -86,48 +85,127 @@ template <> __device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi
 }
 
 // ---------------------------------------------------------------- eight columns
-// Columns col .. col + 7 of a row; columns past V read as -inf.  vec: the row
-// starts on a 16-byte boundary (col is a multiple of 8).
+// Columns col .. col + 7 of a row (col a multiple of 8, lanes side by side: a
+// warp covers 256 columns); columns past V read as -inf.
+//
+// A row that does not start on a 16-byte boundary (an odd V) is read in aligned
+// 16-byte pieces all the same: the pieces around the eight columns, shifted
+// together; the overlap with the next lane comes from L1.  Element loads in their
+// place took 2.2 times as long (500 rows of 50261 fp16 logits).  Stores hand the
+// tail of one lane's columns to the next lane and write aligned pieces.  A row's
+// first and last columns go element by element, so no access leaves the row.
 template <typename T> struct Raw8 {
     uint32_t w[Elem<T>::WORDS];
 };
 
-template <typename T> __device__ __forceinline__ bool row_vec(const T *row)
+// Bytes from the 16-byte boundary before the row's start (every chunk's too).
+template <typename T> __device__ __forceinline__ uint32_t row_shift(const T *row)
 {
-    return (reinterpret_cast<uintptr_t>(row) & 15) == 0;
+    return static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row) & 15);
 }
 
-template <typename T> __device__ __forceinline__ void load8(Raw8<T> &r, const T *row, int col, int V, bool vec)
+// w[i] of the byte sequence q read from byte `shift` on (shift below 16, a
+// multiple of the element size; W + 4 words in q).
+template <int W, bool HALVES> __device__ __forceinline__ void shift_words(uint32_t *w, uint32_t *q, uint32_t shift)
 {
-    if (vec && col + 8 <= V) {
-        const uint4 *p = reinterpret_cast<const uint4 *>(row + col);
 #pragma unroll
-        for (int k = 0; k < Elem<T>::WORDS / 4; ++k) {
-            const uint4 v = p[k];
-            r.w[4 * k] = v.x;
-            r.w[4 * k + 1] = v.y;
-            r.w[4 * k + 2] = v.z;
-            r.w[4 * k + 3] = v.w;
+    for (int i = 0; i < W + 2; ++i)
+        q[i] = shift & 8 ? q[i + 2] : q[i];
+#pragma unroll
+    for (int i = 0; i < W + 1; ++i)
+        q[i] = shift & 4 ? q[i + 1] : q[i];
+#pragma unroll
+    for (int i = 0; i < W; ++i)
+        w[i] = HALVES && (shift & 2) ? __funnelshift_r(q[i], q[i + 1], 16) : q[i];
+}
+
+template <typename T>
+__device__ __forceinline__ void load8(Raw8<T> &r, const T *row, int col, int V, uint32_t shift)
+{
+    constexpr int W = Elem<T>::WORDS;
+    if (shift == 0 ? col + 8 <= V : col >= 8 && col + 16 <= V) {
+        const uint4 *p = reinterpret_cast<const uint4 *>(reinterpret_cast<const char *>(row + col) - shift);
+        if (shift == 0) {
+#pragma unroll
+            for (int k = 0; k < W / 4; ++k) {
+                const uint4 v = p[k];
+                r.w[4 * k] = v.x;
+                r.w[4 * k + 1] = v.y;
+                r.w[4 * k + 2] = v.z;
+                r.w[4 * k + 3] = v.w;
+            }
+        } else {
+            uint32_t q[W + 4];
+#pragma unroll
+            for (int k = 0; k < W / 4 + 1; ++k) {
+                const uint4 v = p[k];
+                q[4 * k] = v.x;
+                q[4 * k + 1] = v.y;
+                q[4 * k + 2] = v.z;
+                q[4 * k + 3] = v.w;
+            }
+            shift_words<W, sizeof(T) == 2>(r.w, q, shift);
         }
         return;
     }
 #pragma unroll
-    for (int k = 0; k < Elem<T>::WORDS; ++k)
+    for (int k = 0; k < W; ++k)
         r.w[k] = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
         Elem<T>::put(r.w, i, col + i < V ? Elem<T>::bits(row + col + i) : Elem<T>::NEG_INF);
 }
 
-template <typename T> __device__ __forceinline__ void store8(T *row, int col, int V, bool vec, const float *v)
+// Stores the lane's eight values; the whole warp, col = its lane's column.
+template <typename T>
+__device__ __forceinline__ void store8(T *row, int col, int V, uint32_t shift, const float *v)
 {
-    if (vec && col + 8 <= V) {
-        uint4 *p = reinterpret_cast<uint4 *>(row + col);
-        if constexpr (sizeof(T) == 4) {
-            p[0] = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
-            p[1] = make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7]));
-        } else {
-            p[0] = make_uint4(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]), pack2<T>(v[4], v[5]), pack2<T>(v[6], v[7]));
+    constexpr int W = Elem<T>::WORDS;
+    const int lane = threadIdx.x & 31;
+    const bool whole = col - lane * 8 + 256 <= V;   // the same in every lane
+    if (shift == 0 ? col + 8 <= V : whole) {
+        uint32_t w[W];
+#pragma unroll
+        for (int k = 0; k < W; ++k) {
+            if constexpr (sizeof(T) == 4)
+                w[k] = __float_as_uint(v[k]);
+            else
+                w[k] = pack2<T>(v[2 * k], v[2 * k + 1]);
+        }
+        if (shift == 0) {
+            uint4 *p = reinterpret_cast<uint4 *>(row + col);
+#pragma unroll
+            for (int k = 0; k < W / 4; ++k)
+                p[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+            return;
+        }
+        // the 16 bytes before this lane's columns are the lane before's last
+        uint32_t q[W + 4], o[W];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            q[k] = __shfl_up_sync(0xffffffffu, w[W - 4 + k], 1);
+#pragma unroll
+        for (int k = 0; k < W; ++k)
+            q[4 + k] = w[k];
+        shift_words<W, sizeof(T) == 2>(o, q, 16 - shift);
+        uint4 *p = reinterpret_cast<uint4 *>(reinterpret_cast<char *>(row + col) - shift);
+        const int head = static_cast<int>((16 - shift) / sizeof(T));   // own elements in the first piece
+        if (lane != 0)
+            p[0] = make_uint4(o[0], o[1], o[2], o[3]);
+        if constexpr (W == 8)
+            p[1] = make_uint4(o[4], o[5], o[6], o[7]);
+        if (lane == 0) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i < head)
+                    row[col + i] = Elem<T>::from(v[i]);
+        }
+        if (lane == 31) {
+            const int tail = static_cast<int>(shift / sizeof(T));
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i >= 8 - tail)
+                    row[col + i] = Elem<T>::from(v[i]);
         }
         return;
     }
@@ -137,70 +215,163 @@ template <typename T> __device__ __forceinline__ void store8(T *row, int col, in
             row[col + i] = Elem<T>::from(v[i]);
 }
 
-// ---------------------------------------------------------------- reductions
-__device__ __forceinline__ float finite_ref(float m) { return m == neg_inf() ? 0.f : m; }
-
-// Adds t[0..7] (base-2 exponents) to the lane's running (m, s).
-__device__ __forceinline__ void lane_add8(float &m, float &s, const float *t)
+// Columns whose bit in `drop` is set become -inf.
+template <typename T> __device__ __forceinline__ void drop8(Raw8<T> &r, uint32_t drop)
 {
-    const float c = fmaxf(fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])), fmaxf(fmaxf(t[4], t[5]), fmaxf(t[6], t[7])));
-    const float n = fmaxf(m, c), ref = finite_ref(n);
-    float e[8];
+    if constexpr (sizeof(T) == 4) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        e[i] = exp2_approx(t[i] - ref);
-    s = s * exp2_approx(m - ref) + (((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7])));
-    m = n;
+        for (int i = 0; i < 8; ++i)
+            r.w[i] = drop >> i & 1 ? Elem<T>::NEG_INF : r.w[i];
+    } else {
+        constexpr uint32_t N = Elem<T>::NEG_INF;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const uint32_t two = drop >> (2 * k) & 3;
+            const uint32_t m = (two & 1 ? 0xffffu : 0u) | (two & 2 ? 0xffff0000u : 0u);
+            r.w[k] = (r.w[k] & ~m) | ((N | N << 16) & m);
+        }
+    }
 }
 
-// The warp's (m, s) from its lanes', in every lane; xor order, so the same in each.
-__device__ __forceinline__ void warp_join(float &m, float &s)
+// ---------------------------------------------------------------- packed pairs of fp32
+using Pair = unsigned long long;
+
+__device__ __forceinline__ Pair pair(float lo, float hi)
 {
-    float n = m;
+    Pair p;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(lo), "f"(hi));
+    return p;
+}
+__device__ __forceinline__ void unpair(Pair p, float &lo, float &hi)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(p));
+}
+__device__ __forceinline__ Pair add2(Pair a, Pair b)
+{
+    Pair p;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(p) : "l"(a), "l"(b));
+    return p;
+}
+__device__ __forceinline__ Pair mul2(Pair a, Pair b)
+{
+    Pair p;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(p) : "l"(a), "l"(b));
+    return p;
+}
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c)
+{
+    Pair p;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(p) : "l"(a), "l"(b), "l"(c));
+    return p;
+}
+template <typename T> __device__ __forceinline__ Pair get2(const Raw8<T> &r, int k)   // columns 2k, 2k + 1
+{
+    return pair(Elem<T>::get(r.w, 2 * k), Elem<T>::get(r.w, 2 * k + 1));
+}
+
+// ---------------------------------------------------------------- reductions
+// Products are rounded on their own (__fmul_rn) and sums in a fixed form, so that
+// no kernel contracts them in its own way: every entry point gives a row the
+// same sums.
+__device__ __forceinline__ float finite_ref(float m) { return m == neg_inf() ? 0.f : m; }
+
+__device__ __forceinline__ float warp_max(float x)   // NaN lanes do not count
+{
+    float y;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ float warp_sum(float x)   // xor order: the same bits in every lane
+{
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1)
-        n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, d));
-    s *= exp2_approx(m - finite_ref(n));
+        x += __shfl_xor_sync(0xffffffffu, x, d);
+    return x;
+}
+
+// The largest of n * 8 raw columns (NaN ones do not count).
+template <typename T, int N> __device__ __forceinline__ float raw_max(const Raw8<T> (&raw)[N])
+{
+    if constexpr (sizeof(T) == 4) {
+        float m = neg_inf();
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1)
-        s += __shfl_xor_sync(0xffffffffu, s, d);
-    m = n;
+        for (int u = 0; u < N; ++u)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                asm("max.f32 %0, %0, %1, %2;"
+                    : "+f"(m)
+                    : "f"(__uint_as_float(raw[u].w[2 * k])), "f"(__uint_as_float(raw[u].w[2 * k + 1])));
+        return m;
+    } else {
+        uint32_t m = raw[0].w[0];
+#pragma unroll
+        for (int u = 0; u < N; ++u)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if constexpr (Elem<T>::NEG_INF == 0xff80u)
+                    asm("max.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(raw[u].w[k]));
+                else
+                    asm("max.f16x2 %0, %0, %1;" : "+r"(m) : "r"(raw[u].w[k]));
+        return fmaxf(Elem<T>::get(&m, 0), Elem<T>::get(&m, 1));
+    }
+}
+
+// (M, S) of a warp's columns y = x / tau, in every lane: the warp's largest x
+// first (with packed maxima on the raw 16-bit pairs), then one pass of
+// e^((x - max) / tau) = 2^((x - max) k2), k2 = log2(e) / tau.  The difference comes
+// before the product, so a row of the type's lowest values does not overflow.
+template <typename T, int N>
+__device__ __forceinline__ void warp_sums(const Raw8<T> (&raw)[N], float inv_tau, float k2, float &M, float &S)
+{
+    const float m = warp_max(raw_max<T, N>(raw));
+    const float ref = finite_ref(m);
+    const Pair neg = pair(-ref, -ref), kk = pair(k2, k2);
+    Pair acc[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
+#pragma unroll
+    for (int u = 0; u < N; ++u)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            float lo, hi;
+            unpair(mul2(add2(get2<T>(raw[u], k), neg), kk), lo, hi);
+            acc[k & 1] = add2(acc[k & 1], pair(exp2_approx(lo), exp2_approx(hi)));
+        }
+    float lo, hi;
+    unpair(add2(acc[0], acc[1]), lo, hi);
+    M = __fmul_rn(m, inv_tau);
+    S = warp_sum(lo + hi);
 }
 
 // Joins (n, t) into (m, s).
 __device__ __forceinline__ void join(float &m, float &s, float n, float t)
 {
     const float k = fmaxf(m, n), ref = finite_ref(k);
-    s = s * exp2_approx(m - ref) + t * exp2_approx(n - ref);
+    s = __fmaf_rn(s, exp2_approx(__fmul_rn(m - ref, LG_LOG2E)), __fmul_rn(t, exp2_approx(__fmul_rn(n - ref, LG_LOG2E))));
     m = k;
 }
 
-// Folds n slice partials (one warp; the same value in every lane): lane l takes
-// slices l, l + 32, ... in order, then the lanes join.
-__device__ __forceinline__ void fold_slices(const float2 *part, int n, int lane, float &m, float &s)
+// Adds one value to a lane's (m, s).
+__device__ __forceinline__ void join_value(float &m, float &s, float y) { join(m, s, y, y == neg_inf() ? 0.f : 1.f); }
+
+// The warp's (m, s) from its lanes', in every lane.
+__device__ __forceinline__ void warp_join(float &m, float &s)
 {
-    m = neg_inf();
-    s = 0.f;
-    for (int i = lane; i < n; i += 32) {
-        join(m, s, part[i].x, part[i].y);
-    }
-    warp_join(m, s);
+    const float n = warp_max(m);
+    s = warp_sum(__fmul_rn(s, exp2_approx(__fmul_rn(m - finite_ref(n), LG_LOG2E))));
+    m = n;
 }
 
 // Natural log of a folded row's sum of exponentials: -inf for an empty row, NaN
 // where the row held a NaN or +inf.
-__device__ __forceinline__ float row_lse(float m, float s)
-{
-    return s == 0.f ? neg_inf() : (m + log2f(s)) * LG_LN2;
-}
+__device__ __forceinline__ float row_lse(float m, float s) { return s == 0.f ? neg_inf() : m + logf(s); }
 
-// log-probability of a column with base-2 exponent t (from the pair, not from
-// the rounded lse: exact to the rounding of a small number near 0).
-__device__ __forceinline__ float row_logp(float t, float m, float s)
+// log-probability of a column with value y (from the pair, not from the rounded
+// lse: a probability near 1 keeps its digits).
+__device__ __forceinline__ float row_logp(float y, float m, float s)
 {
-    if (s == 0.f || (t == neg_inf() && s == s))
+    if (s == 0.f || (y == neg_inf() && s == s))
         return neg_inf();
-    return ((t - m) - log2f(s)) * LG_LN2;
+    return (y - m) - logf(s);
 }
 
 __device__ __forceinline__ void report_bad_input(int *status)
