@@ -27,12 +27,32 @@
 namespace tim {
 namespace {
 
-struct Teacher {
-    int id[LD_MAX_K];      // -1: not in use
-    float q[LD_MAX_K];
-    float logq[LD_MAX_K];
-    float y[LD_MAX_K];     // the student's z / tau at id
+// Shared memory of a CTA: what does not depend on the sizes, then the slices'
+// partials, the teacher's row, the bitmap of the rank's columns, the rank's part
+// of the row.
+struct Layout {
+    uint32_t part, id, q, logq, y, bits, row, bytes;
 };
+
+struct Head {
+    uint64_t bar;
+    int dup, abort;
+};
+
+template <typename T> __host__ __device__ inline Layout layout(int slices, int per, int K, bool sums, bool bits, bool hold)
+{
+    const uint32_t k = static_cast<uint32_t>(K + 3) / 4 * 16;
+    Layout l;
+    l.part = sizeof(Head);
+    l.id = l.part + (sums ? static_cast<uint32_t>(slices) * 16 : 0);
+    l.q = l.id + k;
+    l.logq = l.q + k;
+    l.y = l.logq + k;
+    l.bits = l.y + (sums ? k : 0);
+    l.row = l.bits + (bits ? static_cast<uint32_t>(per) * (LG_SLICE / 8) : 0);
+    l.bytes = l.row + (hold ? static_cast<uint32_t>(per) * LG_SLICE * static_cast<uint32_t>(sizeof(T)) + 16 : 0);
+    return l;
+}
 
 // log q of a listed id from t / tau = hi + lo and the teacher's log-sum-exp:
 // hi - lse is exact when they are close, so large probabilities keep their digits.
@@ -43,20 +63,55 @@ __device__ __forceinline__ float teacher_logq(float t, float tau, float lse)
     return (hi - lse) + lo;
 }
 
-template <typename T, int OP, bool TAIL>
+// The rank's columns z[c0 .. c1) into shared memory at dst + shift bytes: one bulk
+// copy of the whole 16-byte pieces, the up to seven elements before and after
+// them by plain loads (so nothing outside the row is read).  All threads; the
+// plain stores are visible after the next barrier of the CTA.
+template <typename T>
+__device__ __forceinline__ void fetch_row(const T *z, int c0, int c1, uint32_t shift, uint8_t *dst, uint32_t bar)
+{
+    const uintptr_t a0 = reinterpret_cast<uintptr_t>(z + c0), a1 = reinterpret_cast<uintptr_t>(z + c1);
+    const uintptr_t base = a0 - shift;                       // the 16-byte boundary that dst stands for
+    uintptr_t lo = (a0 + 15) & ~uintptr_t(15), hi = a1 & ~uintptr_t(15);
+    if (hi <= lo)
+        lo = hi = a1;                                        // shorter than a piece
+    if (threadIdx.x == 0) {
+        const uint32_t bytes = static_cast<uint32_t>(hi - lo);
+        mbar_arrive_expect_tx(bar, bytes);
+        if (bytes > 0)
+            bulk_load(smem_u32(dst) + static_cast<uint32_t>(lo - base), reinterpret_cast<const void *>(lo), bytes, bar,
+                      l2_policy_evict_first());
+    }
+    const int head = static_cast<int>((lo - a0) / sizeof(T)), tail = static_cast<int>((a1 - hi) / sizeof(T));
+    T *s = reinterpret_cast<T *>(dst + shift);
+    for (int i = threadIdx.x; i < head + tail; i += LD_THREADS) {
+        const int col = i < head ? i : (c1 - c0) - (head + tail) + i;
+        s[col] = z[c0 + col];
+    }
+}
+
+// HOLD: the rank's part of the row stays in shared memory between the two passes
+// of a step.
+template <typename T, int OP, bool TAIL, bool HOLD>
 __global__ void __launch_bounds__(LD_THREADS) distill_kernel(const DistillArgs a)
 {
     constexpr bool SUMS = OP != LD_BACKWARD, GRAD = OP != LD_FORWARD, BITS = TAIL || GRAD;
-    extern __shared__ uint32_t bitmap[];   // columns of this rank
-    __shared__ float4 part[SUMS ? LG_MAX_SLICES : 1];
-    __shared__ Teacher th;
-    __shared__ int dup;
+    extern __shared__ __align__(16) uint8_t smem[];
+    const Layout lay = layout<T>((a.V + LG_SLICE - 1) / LG_SLICE, a.per, a.K, SUMS, BITS, HOLD);
+    Head &hd = *reinterpret_cast<Head *>(smem);
+    float4 *part = reinterpret_cast<float4 *>(smem + lay.part);
+    struct {
+        int *id;        // -1: not in use
+        float *q, *logq, *y;   // y: the student's z / tau at id
+    } const th = {reinterpret_cast<int *>(smem + lay.id), reinterpret_cast<float *>(smem + lay.q),
+                  reinterpret_cast<float *>(smem + lay.logq), reinterpret_cast<float *>(smem + lay.y)};
+    uint32_t *bitmap = reinterpret_cast<uint32_t *>(smem + lay.bits);   // columns of this rank
     const int rank = static_cast<int>(cluster_ctarank());
     const int row = static_cast<int>(blockIdx.x / static_cast<unsigned>(a.ranks));
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int slices = (a.V + LG_SLICE - 1) / LG_SLICE;
     const int s0 = min(slices, rank * a.per), s1 = min(slices, s0 + a.per);
-    const int c0 = s0 * LG_SLICE, c1 = min(a.V, s1 * LG_SLICE);
+    const int c0 = min(a.V, s0 * LG_SLICE), c1 = min(a.V, s1 * LG_SLICE);
     const T *z = static_cast<const T *>(a.z) + row * a.ld;
     T *dz = GRAD ? static_cast<T *>(a.dz) + row * a.ldo : nullptr;
     const uint32_t shift = row_shift(z), shift_out = GRAD ? row_shift(dz) : 0u;
@@ -64,6 +119,18 @@ __global__ void __launch_bounds__(LD_THREADS) distill_kernel(const DistillArgs a
     float g = 0.f;
     if constexpr (GRAD)
         g = a.grad[row];
+    // the columns as the passes read them: from memory, or from this CTA's copy
+    const T *src = HOLD ? reinterpret_cast<const T *>(smem + lay.row + shift) : z;
+    const int off = HOLD ? c0 : 0;
+    if constexpr (HOLD) {
+        if (threadIdx.x == 0) {
+            mbar_init(smem_u32(&hd.bar), 1);
+            hd.abort = 0;
+            fence_mbar_init();
+            fence_proxy_async_smem();
+        }
+        fetch_row<T>(z, c0, c1, shift, smem + lay.row, smem_u32(&hd.bar));
+    }
     if (SUMS && a.ranks > 1)
         cluster_arrive();   // waited for before the first store into another CTA's shared memory
 
@@ -84,7 +151,7 @@ __global__ void __launch_bounds__(LD_THREADS) distill_kernel(const DistillArgs a
         for (int j = threadIdx.x; j < (c1 - c0 + 31) / 32; j += LD_THREADS)
             bitmap[j] = 0;
         if (threadIdx.x == 0)
-            dup = 0;
+            hd.dup = 0;
     }
     for (int k = threadIdx.x; k < a.K; k += LD_THREADS) {
         const int64_t at = static_cast<int64_t>(row) * a.K + k;
@@ -128,7 +195,7 @@ __global__ void __launch_bounds__(LD_THREADS) distill_kernel(const DistillArgs a
         if (BITS && id >= c0 && id < c1) {
             const uint32_t bit = 1u << ((id - c0) & 31);
             if (atomicOr(bitmap + ((id - c0) >> 5), bit) & bit)
-                dup = 1;
+                hd.dup = 1;
         }
     }
     __syncthreads();
@@ -144,18 +211,26 @@ __global__ void __launch_bounds__(LD_THREADS) distill_kernel(const DistillArgs a
     // tail), (mk, sk) of the listed ones.
     float m = neg_inf(), s = 0.f, mr = neg_inf(), sr = 0.f;
     if constexpr (SUMS) {
+        bool late = false;
+        if constexpr (HOLD) {
+            late = !mbar_wait_sleep(smem_u32(&hd.bar), 0, &hd.abort, a.wait_budget_ns);
+            if (late) {
+                atomicCAS(a.status, 0, static_cast<int>(TIM_ERR_TIMEOUT));
+                drain_wait(smem_u32(&hd.bar), 0);
+            }
+        }
         for (int sl = s0 + warp; sl < s1; sl += LD_WARPS) {
             Raw8<T> raw[4];
 #pragma unroll
             for (int u = 0; u < 4; ++u)
-                load8<T>(raw[u], z, sl * LG_SLICE + u * 256 + lane * 8, a.V, shift);
+                load8<T>(raw[u], src, sl * LG_SLICE + u * 256 + lane * 8 - off, c1 - off, shift);
             float lm, ls, km = neg_inf(), ks = 0.f;
             if constexpr (TAIL) {   // the listed ones out of the stream, one by one
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
                     const int col = sl * LG_SLICE + u * 256 + lane * 8;
                     const uint32_t bits =
-                        col < a.V ? reinterpret_cast<const uint8_t *>(bitmap)[(col - c0) >> 3] : 0u;
+                        col < c1 ? reinterpret_cast<const uint8_t *>(bitmap)[(col - c0) >> 3] : 0u;
                     if (bits) {
 #pragma unroll
                         for (int i = 0; i < 8; ++i)
@@ -169,7 +244,7 @@ __global__ void __launch_bounds__(LD_THREADS) distill_kernel(const DistillArgs a
             }
             warp_sums<T, 4>(raw, inv_tau, k2, lm, ls);
             if (lane == 0)
-                part[sl] = make_float4(lm, ls, km, ks);
+                part[sl] = make_float4(lm, late ? quiet_nan() : ls, km, ks);
         }
         __syncthreads();
         if (a.ranks > 1) {
@@ -255,12 +330,12 @@ __global__ void __launch_bounds__(LD_THREADS) distill_kernel(const DistillArgs a
             own[n] = 0.f;
             if (k < a.K && th.id[k] >= c0 && th.id[k] < c1) {
                 float q = th.q[k];
-                if (dup) {   // ids listed more than once add up, in the list's order
+                if (hd.dup) {   // ids listed more than once add up, in the list's order
                     q = 0.f;
                     for (int j = 0; j < a.K; ++j)
                         q += th.id[j] == th.id[k] ? th.q[j] : 0.f;
                 }
-                own[n] = (prob(Elem<T>::load(z + th.id[k])) - q) * gi;
+                own[n] = (prob(Elem<T>::load(src + th.id[k] - off)) - q) * gi;
             }
         }
         __syncthreads();
@@ -271,7 +346,7 @@ __global__ void __launch_bounds__(LD_THREADS) distill_kernel(const DistillArgs a
             Raw8<T> raw[2];
 #pragma unroll
             for (int u = 0; u < 2; ++u)
-                load8<T>(raw[u], z, b + u * 256 + lane * 8, c1, shift);
+                load8<T>(raw[u], src, b + u * 256 + lane * 8 - off, c1 - off, shift);
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 float v[8];
@@ -294,28 +369,41 @@ __global__ void __launch_bounds__(LD_THREADS) distill_kernel(const DistillArgs a
     }
 }
 
+template <typename T, int OP, bool TAIL, bool HOLD>
+cudaError_t launch_kernel(const DistillArgs &a, const Layout &l, cudaStream_t s)
+{
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(a.N) * static_cast<unsigned>(a.ranks));
+    cfg.blockDim = dim3(LD_THREADS);
+    cfg.dynamicSmemBytes = l.bytes;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = static_cast<unsigned>(a.ranks);
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, distill_kernel<T, OP, TAIL, HOLD>, a);
+}
+
 template <typename T, int OP, bool TAIL> cudaError_t launch(DistillArgs a, int num_sms, cudaStream_t s)
 {
     const int slices = lg_slices(a.V);
     int ranks = 1;   // CTAs of a row: more while the rows alone leave SMs idle
-    while (ranks < LG_CLUSTER && ranks * 2 <= slices && static_cast<int64_t>(a.N) * ranks < 2 * num_sms)
+    while (ranks < LG_CLUSTER && ranks * 2 <= slices && static_cast<int64_t>(a.N) * ranks < 4 * num_sms)
         ranks *= 2;
-    if (OP == LD_STEP && slices >= LG_CLUSTER)
-        ranks = LG_CLUSTER;   // the rows in flight stay in L2 between the two passes
-    a.ranks = ranks;
+    if (OP == LD_STEP)   // a rank's part of the row: 40 KB, so that five CTAs fit an SM
+        while (ranks < LG_CLUSTER && static_cast<size_t>((slices + ranks - 1) / ranks) * LG_SLICE * sizeof(T) > 40 * 1024)
+            ranks *= 2;
     a.per = (slices + ranks - 1) / ranks;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(a.N) * static_cast<unsigned>(ranks));
-    cfg.blockDim = dim3(LD_THREADS);
-    cfg.dynamicSmemBytes = OP != LD_FORWARD || TAIL ? static_cast<size_t>(a.per) * (LG_SLICE / 8) : 0;
-    cfg.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = static_cast<unsigned>(ranks);
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, distill_kernel<T, OP, TAIL>, a);
+    a.ranks = (slices + a.per - 1) / a.per;
+    constexpr bool SUMS = OP != LD_BACKWARD, BITS = TAIL || OP != LD_FORWARD;
+    if constexpr (OP == LD_STEP) {
+        const Layout l = layout<T>(slices, a.per, a.K, SUMS, BITS, true);
+        if (l.bytes <= LD_SMEM)
+            return launch_kernel<T, OP, TAIL, true>(a, l, s);
+    }
+    return launch_kernel<T, OP, TAIL, false>(a, layout<T>(slices, a.per, a.K, SUMS, BITS, false), s);
 }
 
 template <typename T> cudaError_t launch_op(const DistillArgs &a, int op, int num_sms, cudaStream_t s)
@@ -328,19 +416,24 @@ template <typename T> cudaError_t launch_op(const DistillArgs &a, int op, int nu
     return tail ? launch<T, LD_STEP, true>(a, num_sms, s) : launch<T, LD_STEP, false>(a, num_sms, s);
 }
 
-template <typename T, int OP, bool TAIL> cudaError_t set_smem()
+template <typename T, int OP, bool TAIL, bool HOLD> cudaError_t set_smem()
 {
-    return cudaFuncSetAttribute(distill_kernel<T, OP, TAIL>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                LG_MAX_SLICES * (LG_SLICE / 8));
+    return cudaFuncSetAttribute(distill_kernel<T, OP, TAIL, HOLD>, cudaFuncAttributeMaxDynamicSharedMemorySize, LD_SMEM);
+}
+
+template <typename T, bool TAIL> cudaError_t prepare_tail()
+{
+    for (cudaError_t e : {set_smem<T, LD_FORWARD, TAIL, false>(), set_smem<T, LD_BACKWARD, TAIL, false>(),
+                          set_smem<T, LD_STEP, TAIL, false>(), set_smem<T, LD_STEP, TAIL, true>()})
+        if (e != cudaSuccess)
+            return e;
+    return cudaSuccess;
 }
 
 template <typename T> cudaError_t prepare()
 {
-    for (cudaError_t e : {set_smem<T, LD_FORWARD, true>(), set_smem<T, LD_BACKWARD, false>(),
-                          set_smem<T, LD_BACKWARD, true>(), set_smem<T, LD_STEP, false>(), set_smem<T, LD_STEP, true>()})
-        if (e != cudaSuccess)
-            return e;
-    return cudaSuccess;
+    const cudaError_t e = prepare_tail<T, false>();
+    return e != cudaSuccess ? e : prepare_tail<T, true>();
 }
 
 } // namespace

@@ -148,6 +148,7 @@ int distill(tim::DistillArgs a, int op, const void *logits, int dtype, int64_t N
     a.teacher = teacher;
     a.teacher_lse = teacher_lse;
     a.temperature = temperature;
+    a.wait_budget_ns = tim::pipeline_wait_budget_ns();
     return finish(tim::distill_topk_launch(a, op, dtype, sms, reinterpret_cast<cudaStream_t>(stream)), "launch");
 }
 

@@ -58,9 +58,10 @@ struct ProcArgs {
 cudaError_t logits_process_launch(ProcArgs a, int op, int dtype, int out_dtype, int num_sms, cudaStream_t s);
 
 // ---------------------------------------------------------------- distillation
-constexpr int LD_THREADS = 512;
+constexpr int LD_THREADS = 320;
 constexpr int LD_WARPS = LD_THREADS / 32;
 constexpr int LD_MAX_K = 1024;
+constexpr int LD_SMEM = 224 * 1024;                // shared memory a CTA may take
 
 enum { LD_FORWARD = 0, LD_BACKWARD = 1, LD_STEP = 2 };
 
@@ -79,6 +80,7 @@ struct DistillArgs {
     int64_t ldo;
     int32_t per;               // slices of a cluster rank
     int32_t ranks;             // CTAs of a row
+    uint64_t wait_budget_ns;   // STEP: wait for the row's copy
     int *status;
 };
 

@@ -492,17 +492,17 @@ template <typename T> cudaError_t launch_logp(ProcArgs a, int num_sms, cudaStrea
     int ranks = 1;   // CTAs of a row: more while the rows alone leave SMs idle
     while (ranks < LG_CLUSTER && ranks * 2 <= slices && static_cast<int64_t>(a.N) * ranks < 4 * num_sms)
         ranks *= 2;
-    a.segs = ranks;
     a.seg_slices = (slices + ranks - 1) / ranks;
+    a.segs = (slices + a.seg_slices - 1) / a.seg_slices;
     a.table_columns = std::min(LP_TABLE, a.seg_slices * LG_SLICE);
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(a.N) * static_cast<unsigned>(ranks));
+    cfg.gridDim = dim3(static_cast<unsigned>(a.N) * static_cast<unsigned>(a.segs));
     cfg.blockDim = dim3(LP_THREADS);
     cfg.dynamicSmemBytes = touch ? table_bytes(a.table_columns) : 0;
     cfg.stream = s;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = static_cast<unsigned>(ranks);
+    at[0].val.clusterDim.x = static_cast<unsigned>(a.segs);
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;

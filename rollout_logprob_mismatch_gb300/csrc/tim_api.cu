@@ -225,6 +225,8 @@ int use_device(int **status, int *sms)
     return rc;
 }
 
+uint64_t pipeline_wait_budget_ns() { return wait_budget_ns(); }
+
 // Records a formatted message for tim_last_error() on the calling thread; returns code.
 int fail_message(int code, const char *fmt, ...)
 {

@@ -49,6 +49,7 @@ __device__ __forceinline__ void debug_report(int *status, int check, int64_t ind
 cudaError_t status_word_address(int **out);   // the library's device status block
 int record_error(int code, const char *msg);  // message for tim_last_error()
 int use_device(int **status, int *sms);       // sets the current device up; a tim_status code
+uint64_t pipeline_wait_budget_ns();            // time budget of a wait inside a kernel
 int fail_message(int code, const char *fmt, ...) __attribute__((format(printf, 2, 3)));
 
 } // namespace tim
