@@ -21,34 +21,40 @@
 // column as if it were not listed; after a barrier the listed ones, all of
 // which the same CTA owns, are written over.
 #include <algorithm>
+#include <cstddef>
 
 #include "logits_rows.cuh"
 
 namespace tim {
 namespace {
 
-// Shared memory of a CTA: what does not depend on the sizes, then the slices'
-// partials, the teacher's row, the bitmap of the rank's columns, the rank's part
-// of the row.
-struct Layout {
-    uint32_t part, id, q, logq, y, bits, row, bytes;
+// What a row's teacher contributes besides its own q_k.
+struct TeacherRow {
+    float max;    // largest t_k (0 for a tail: not used)
+    float lse;    // log sum e^((t_k - max) / tau), or the given one
+    float rest;   // q_o (0 without a tail)
+    int any;      // the row lists something
 };
 
+// Shared memory of a CTA: the header, the slices' partials, the student's z at the
+// listed ids, the bitmap of the rank's columns, the rank's part of the row.
 struct Head {
     uint64_t bar;
     int dup, abort;
+    TeacherRow teacher;
+    float m, s, mr, sr;   // all columns; those that are not listed
+};
+
+struct Layout {
+    uint32_t part, x, bits, row, bytes;
 };
 
 template <typename T> __host__ __device__ inline Layout layout(int slices, int per, int K, bool sums, bool bits, bool hold)
 {
-    const uint32_t k = static_cast<uint32_t>(K + 3) / 4 * 16;
     Layout l;
     l.part = sizeof(Head);
-    l.id = l.part + (sums ? static_cast<uint32_t>(slices) * 16 : 0);
-    l.q = l.id + k;
-    l.logq = l.q + k;
-    l.y = l.logq + k;
-    l.bits = l.y + (sums ? k : 0);
+    l.x = l.part + (sums ? static_cast<uint32_t>(slices) * 16 : 0);
+    l.bits = l.x + (sums ? static_cast<uint32_t>(K + 3) / 4 * 16 : 0);
     l.row = l.bits + (bits ? static_cast<uint32_t>(per) * (LG_SLICE / 8) : 0);
     l.bytes = l.row + (hold ? static_cast<uint32_t>(per) * LG_SLICE * static_cast<uint32_t>(sizeof(T)) + 16 : 0);
     return l;
@@ -61,6 +67,50 @@ __device__ __forceinline__ float teacher_logq(float t, float tau, float lse)
     const float hi = t / tau;
     const float lo = isfinite(hi) ? fmaf(-hi, tau, t) / tau : 0.f;
     return (hi - lse) + lo;
+}
+
+// log q_k of a listed id.
+template <bool TAIL> __device__ __forceinline__ float listed_logq(float t, float tau, const TeacherRow &w)
+{
+    return w.any ? teacher_logq(TAIL ? t : t - w.max, tau, w.lse) : neg_inf();
+}
+
+__device__ __forceinline__ float q_of(float logq) { return logq == neg_inf() ? 0.f : expf(logq); }
+
+__device__ __forceinline__ bool in_use(int id, int V) { return id >= 0 && id < V; }
+
+// One warp; the same in every lane.
+template <bool TAIL> __device__ __forceinline__ TeacherRow teacher_row(const DistillArgs &a, int row, int lane)
+{
+    const int32_t *ids = a.ids + static_cast<int64_t>(row) * a.K;
+    const float *t = a.teacher + static_cast<int64_t>(row) * a.K;
+    TeacherRow w{0.f, 0.f, 0.f, 0};
+    bool any = false;
+    float top = neg_inf();
+    for (int k = lane; k < a.K; k += 32)
+        if (in_use(ids[k], a.V)) {
+            any = true;
+            top = fmaxf(top, t[k]);
+        }
+    w.any = __any_sync(0xffffffffu, any);
+    float s = 0.f;
+    if constexpr (TAIL) {
+        w.lse = a.teacher_lse[row];
+        for (int k = lane; k < a.K; k += 32)
+            if (in_use(ids[k], a.V))
+                s += q_of(listed_logq<true>(t[k], a.temperature, w));
+        s = warp_sum(s);
+        w.rest = s <= 1.f ? 1.f - s : (s > 1.f ? 0.f : s);   // NaN stays
+    } else {
+        w.max = finite_ref(warp_max(top));
+        for (int k = lane; k < a.K; k += 32)
+            if (in_use(ids[k], a.V))
+                s += expf((t[k] - w.max) / a.temperature);
+        s = warp_sum(s);
+        w.lse = logf(s);
+        w.any = w.any && s != 0.f;
+    }
+    return w;
 }
 
 // The rank's columns z[c0 .. c1) into shared memory at dst + shift bytes: one bulk
@@ -97,24 +147,22 @@ __global__ void __launch_bounds__(LD_THREADS) distill_kernel(const DistillArgs a
 {
     constexpr bool SUMS = OP != LD_BACKWARD, GRAD = OP != LD_FORWARD, BITS = TAIL || GRAD;
     extern __shared__ __align__(16) uint8_t smem[];
-    const Layout lay = layout<T>((a.V + LG_SLICE - 1) / LG_SLICE, a.per, a.K, SUMS, BITS, HOLD);
+    const int slices = (a.V + LG_SLICE - 1) / LG_SLICE;
+    const Layout lay = layout<T>(slices, a.per, a.K, SUMS, BITS, HOLD);
     Head &hd = *reinterpret_cast<Head *>(smem);
     float4 *part = reinterpret_cast<float4 *>(smem + lay.part);
-    struct {
-        int *id;        // -1: not in use
-        float *q, *logq, *y;   // y: the student's z / tau at id
-    } const th = {reinterpret_cast<int *>(smem + lay.id), reinterpret_cast<float *>(smem + lay.q),
-                  reinterpret_cast<float *>(smem + lay.logq), reinterpret_cast<float *>(smem + lay.y)};
+    float *listed_x = reinterpret_cast<float *>(smem + lay.x);
     uint32_t *bitmap = reinterpret_cast<uint32_t *>(smem + lay.bits);   // columns of this rank
     const int rank = static_cast<int>(cluster_ctarank());
     const int row = static_cast<int>(blockIdx.x / static_cast<unsigned>(a.ranks));
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int slices = (a.V + LG_SLICE - 1) / LG_SLICE;
     const int s0 = min(slices, rank * a.per), s1 = min(slices, s0 + a.per);
     const int c0 = min(a.V, s0 * LG_SLICE), c1 = min(a.V, s1 * LG_SLICE);
     const T *z = static_cast<const T *>(a.z) + row * a.ld;
     T *dz = GRAD ? static_cast<T *>(a.dz) + row * a.ldo : nullptr;
     const uint32_t shift = row_shift(z), shift_out = GRAD ? row_shift(dz) : 0u;
+    const int32_t *ids = a.ids + static_cast<int64_t>(row) * a.K;
+    const float *teacher = a.teacher + static_cast<int64_t>(row) * a.K;
     const float tau = a.temperature, inv_tau = 1.f / tau, k2 = LG_LOG2E * inv_tau;
     float g = 0.f;
     if constexpr (GRAD)
@@ -122,15 +170,17 @@ __global__ void __launch_bounds__(LD_THREADS) distill_kernel(const DistillArgs a
     // the columns as the passes read them: from memory, or from this CTA's copy
     const T *src = HOLD ? reinterpret_cast<const T *>(smem + lay.row + shift) : z;
     const int off = HOLD ? c0 : 0;
-    if constexpr (HOLD) {
-        if (threadIdx.x == 0) {
+    if (threadIdx.x == 0) {
+        hd.dup = 0;
+        if constexpr (HOLD) {
             mbar_init(smem_u32(&hd.bar), 1);
             hd.abort = 0;
             fence_mbar_init();
             fence_proxy_async_smem();
         }
-        fetch_row<T>(z, c0, c1, shift, smem + lay.row, smem_u32(&hd.bar));
     }
+    if constexpr (HOLD)
+        fetch_row<T>(z, c0, c1, shift, smem + lay.row, smem_u32(&hd.bar));
     if (SUMS && a.ranks > 1)
         cluster_arrive();   // waited for before the first store into another CTA's shared memory
 
@@ -146,71 +196,35 @@ __global__ void __launch_bounds__(LD_THREADS) distill_kernel(const DistillArgs a
         }
     }
 
-    // the teacher's row
-    if (BITS) {
+    // the listed ids: this rank's in the bitmap, for the loss the logits of all
+    if constexpr (BITS) {
         for (int j = threadIdx.x; j < (c1 - c0 + 31) / 32; j += LD_THREADS)
             bitmap[j] = 0;
-        if (threadIdx.x == 0)
-            hd.dup = 0;
+        __syncthreads();
     }
     for (int k = threadIdx.x; k < a.K; k += LD_THREADS) {
-        const int64_t at = static_cast<int64_t>(row) * a.K + k;
-        int id = a.ids[at];
-        id = id >= 0 && id < a.V ? id : -1;
-        th.id[k] = id;
-        th.logq[k] = id >= 0 ? a.teacher[at] : neg_inf();
-        if (SUMS)
-            th.y[k] = id >= 0 ? __fmul_rn(Elem<T>::load(z + id), inv_tau) : 0.f;
-    }
-    __syncthreads();
-    // (every warp finds the row's normaliser for itself)
-    float q_all = 0.f, q_max = neg_inf();
-    bool any = false;
-    for (int k = lane; k < a.K; k += 32) {
-        any |= th.id[k] >= 0;
-        q_max = fmaxf(q_max, th.logq[k]);
-    }
-    any = __any_sync(0xffffffffu, any);
-    q_max = warp_max(q_max);
-    float q_lse = 0.f;
-    if constexpr (TAIL) {
-        q_lse = a.teacher_lse[row];
-    } else {
-        float s = 0.f;
-        for (int k = lane; k < a.K; k += 32)
-            s += th.id[k] >= 0 ? expf((th.logq[k] - finite_ref(q_max)) / tau) : 0.f;
-        s = warp_sum(s);
-        any = any && s != 0.f;
-        q_lse = logf(s);
-    }
-    __syncthreads();   // th.logq still held t
-    for (int k = threadIdx.x; k < a.K; k += LD_THREADS) {
-        const float t = th.logq[k];
-        float lq = TAIL ? teacher_logq(t, tau, q_lse) : teacher_logq(t - finite_ref(q_max), tau, q_lse);
-        const int id = th.id[k];
-        if (id < 0 || !any)
-            lq = neg_inf();
-        th.logq[k] = lq;
-        th.q[k] = lq == neg_inf() ? 0.f : expf(lq);
+        const int id = ids[k];
+        if (SUMS && rank == 0)
+            listed_x[k] = in_use(id, a.V) ? Elem<T>::load(z + id) : 0.f;
         if (BITS && id >= c0 && id < c1) {
             const uint32_t bit = 1u << ((id - c0) & 31);
             if (atomicOr(bitmap + ((id - c0) >> 5), bit) & bit)
                 hd.dup = 1;
         }
     }
-    __syncthreads();
-    float q_rest = 0.f;
-    if constexpr (TAIL) {
-        for (int k = lane; k < a.K; k += 32)
-            q_all += th.q[k];
-        q_all = warp_sum(q_all);
-        q_rest = q_all <= 1.f ? 1.f - q_all : (q_all > 1.f ? 0.f : q_all);   // NaN stays
+    // the teacher's statistics: by the last warp (it has the fewest slices), while the
+    // others wait for the row; in a call with sums by rank 0, which hands them out
+    if (warp == LD_WARPS - 1 && (rank == 0 || !SUMS)) {
+        const TeacherRow tr = teacher_row<TAIL>(a, row, lane);
+        if (lane == 0)
+            hd.teacher = tr;
     }
+    if (TAIL || !SUMS)
+        __syncthreads();
 
-    // The sums: (m, s) of the columns that are not listed (all of them without a
-    // tail), (mk, sk) of the listed ones.
-    float m = neg_inf(), s = 0.f, mr = neg_inf(), sr = 0.f;
     if constexpr (SUMS) {
+        // The sums: of the columns that are not listed (all of them without a tail)
+        // and of the listed ones, slice by slice.
         bool late = false;
         if constexpr (HOLD) {
             late = !mbar_wait_sleep(smem_u32(&hd.bar), 0, &hd.abort, a.wait_budget_ns);
@@ -221,9 +235,7 @@ __global__ void __launch_bounds__(LD_THREADS) distill_kernel(const DistillArgs a
         }
         for (int sl = s0 + warp; sl < s1; sl += LD_WARPS) {
             Raw8<T> raw[4];
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-                load8<T>(raw[u], src, sl * LG_SLICE + u * 256 + lane * 8 - off, c1 - off, shift);
+            load_chunks<T, 4>(raw, src, sl * LG_SLICE - off, c1 - off, shift);
             float lm, ls, km = neg_inf(), ks = 0.f;
             if constexpr (TAIL) {   // the listed ones out of the stream, one by one
 #pragma unroll
@@ -235,14 +247,14 @@ __global__ void __launch_bounds__(LD_THREADS) distill_kernel(const DistillArgs a
 #pragma unroll
                         for (int i = 0; i < 8; ++i)
                             if (bits >> i & 1)
-                                join_value(km, ks, __fmul_rn(Elem<T>::get(raw[u].w, i), inv_tau));
+                                join_value(km, ks, Elem<T>::get(raw[u].w, i), k2);
                         drop8(raw[u], bits);
                     }
                 }
                 if (__any_sync(0xffffffffu, ks != 0.f))
-                    warp_join(km, ks);
+                    warp_join(km, ks, k2);
             }
-            warp_sums<T, 4>(raw, inv_tau, k2, lm, ls);
+            warp_sums<T, 4>(raw, k2, nullptr, 0, lm, ls);
             if (lane == 0)
                 part[sl] = make_float4(lm, late ? quiet_nan() : ls, km, ks);
         }
@@ -252,10 +264,16 @@ __global__ void __launch_bounds__(LD_THREADS) distill_kernel(const DistillArgs a
             for (int d = 0; d < (GRAD ? a.ranks : 1); ++d) {
                 if (d == rank)
                     continue;
-                const uint32_t to = mapa_shared(smem_u32(part), static_cast<uint32_t>(d));
+                const uint32_t to = mapa_shared(smem_u32(smem), static_cast<uint32_t>(d));
                 for (int j = s0 + static_cast<int>(threadIdx.x); j < s1; j += LD_THREADS) {
-                    st_cluster_f2(to + j * 16, part[j].x, part[j].y);
-                    st_cluster_f2(to + j * 16 + 8, part[j].z, part[j].w);
+                    const uint32_t at = to + lay.part + static_cast<uint32_t>(j) * 16;
+                    st_cluster_f2(at, part[j].x, part[j].y);
+                    st_cluster_f2(at + 8, part[j].z, part[j].w);
+                }
+                if (rank == 0 && threadIdx.x == 0) {
+                    const uint32_t at = to + static_cast<uint32_t>(offsetof(Head, teacher));
+                    st_cluster_f2(at, hd.teacher.max, hd.teacher.lse);
+                    st_cluster_f2(at + 8, hd.teacher.rest, __int_as_float(hd.teacher.any));
                 }
             }
             __syncwarp();
@@ -264,96 +282,120 @@ __global__ void __launch_bounds__(LD_THREADS) distill_kernel(const DistillArgs a
         }
         if (!GRAD && (rank != 0 || warp != 0))
             return;
-        // fold in slice order: lane l takes slices l, l + 32, ...
-        float km = neg_inf(), ks = 0.f;
-        for (int j = lane; j < slices; j += 32) {
-            const float4 p = part[j];
-            join(mr, sr, p.x, p.y);
-            if constexpr (TAIL)
-                join(km, ks, p.z, p.w);
-        }
-        warp_join(mr, sr);
-        m = mr;
-        s = sr;
-        if constexpr (TAIL) {
-            warp_join(km, ks);
-            join(m, s, km, ks);
-        }
-        if (rank == 0 && warp == 0) {
-            float loss = 0.f;
-            for (int k = lane; k < a.K; k += 32)
-                if (th.q[k] != 0.f)   // NaN goes on
-                    loss = __fmaf_rn(th.q[k], th.logq[k] - row_logp(th.y[k], m, s), loss);
-            loss = warp_sum(loss);
-            if constexpr (TAIL)
-                if (q_rest != 0.f)
-                    loss += q_rest * (logf(q_rest) - (sr == 0.f ? neg_inf() : (mr - m) + (logf(sr) - logf(s))));
-            if (lane == 0) {
-                a.loss[row] = loss;
-                a.out_lse[row] = row_lse(m, s);
-                if (TAIL)
-                    a.out_lse_tail[row] = row_lse(mr, sr);
+        if (warp == 0) {   // fold in slice order: lane l takes slices l, l + 32, ...
+            float mr = neg_inf(), sr = 0.f, km = neg_inf(), ks = 0.f;
+            for (int j = lane; j < slices; j += 32) {
+                const float4 p = part[j];
+                join(mr, sr, p.x, p.y, k2);
+                if constexpr (TAIL)
+                    join(km, ks, p.z, p.w, k2);
             }
+            warp_join(mr, sr, k2);
+            float m = mr, s = sr;
+            if constexpr (TAIL) {
+                warp_join(km, ks, k2);
+                join(m, s, km, ks, k2);
+            }
+            if (lane == 0) {
+                hd.m = m;
+                hd.s = s;
+                hd.mr = mr;
+                hd.sr = sr;
+            }
+            __syncwarp();
         }
+        if constexpr (GRAD)
+            __syncthreads();
+    }
+
+    auto write_loss = [&] {   // one warp of rank 0
+        const TeacherRow tr = hd.teacher;
+        const float m = hd.m, s = hd.s, mr = hd.mr, sr = hd.sr;
+        float loss = 0.f;
+        for (int k = lane; k < a.K; k += 32)
+            if (in_use(ids[k], a.V)) {
+                const float lq = listed_logq<TAIL>(teacher[k], tau, tr), q = q_of(lq);
+                if (q != 0.f)   // NaN goes on
+                    loss = __fmaf_rn(q, lq - row_logp(listed_x[k], m, s, inv_tau), loss);
+            }
+        loss = warp_sum(loss);
+        if constexpr (TAIL)
+            if (tr.rest != 0.f)
+                loss = __fmaf_rn(tr.rest,
+                                 logf(tr.rest) - (sr == 0.f ? neg_inf() : __fmaf_rn(mr - m, inv_tau, logf(sr) - logf(s))), loss);
+        if (lane == 0) {
+            a.loss[row] = loss;
+            a.out_lse[row] = row_lse(m, s, inv_tau);
+            if (TAIL)
+                a.out_lse_tail[row] = row_lse(mr, sr, inv_tau);
+        }
+    };
+    if constexpr (!GRAD) {
+        write_loss();
+        return;
     }
 
     if constexpr (GRAD) {
         if (SUMS && g == 0.f) {
             zero_row();
+            if (SUMS && rank == 0 && warp == LD_WARPS - 1)
+                write_loss();
             return;
         }
-        // p_v = e^(y_v - m) / s in a step, e^(y_v - lse) from the forward's lse
+        // p_v = 2^((z_v first - ref) second) scale: the row's maximum and 1 / sum in a
+        // step, the forward's lse in a backward call
+        const TeacherRow w = hd.teacher;
         const float gi = g / tau;
-        float lse = 0.f, inv_s = 0.f, w = any ? 1.f : 0.f;
+        const float first = SUMS ? 1.f : inv_tau, second = SUMS ? k2 : LG_LOG2E;
+        float ref, scale = 1.f, others = w.any ? 1.f : 0.f;   // factor of p_v for ids that are not listed
         if constexpr (SUMS) {
-            inv_s = s == 0.f ? 0.f : 1.f / s;
-            m = finite_ref(m);
+            ref = finite_ref(hd.m);
+            scale = hd.s == 0.f ? 0.f : 1.f / hd.s;
             if constexpr (TAIL)
-                w = sr == 0.f ? 0.f : 1.f - q_rest / (sr * exp2_approx((mr - m) * LG_LOG2E) * inv_s);
+                others = hd.sr == 0.f ? 0.f : 1.f - w.rest / (hd.sr * exp2_approx((hd.mr - ref) * k2) * scale);
         } else {
-            lse = a.lse[row];
+            ref = a.lse[row];
             if constexpr (TAIL) {
                 const float lt = a.lse_tail[row];
-                w = lt == neg_inf() ? 0.f : 1.f - q_rest * expf(lse - lt);
+                others = lt == neg_inf() ? 0.f : 1.f - w.rest * expf(ref - lt);
             }
-            if (lse == neg_inf())
-                lse = -neg_inf();
+            if (ref == neg_inf())
+                ref = -neg_inf();
         }
-        const float ref = SUMS ? m : lse, scale = SUMS ? inv_s : 1.f;
-        auto prob = [&](float x) { return exp2_approx(fmaf(x, inv_tau, -ref) * LG_LOG2E) * scale; };
-        // the listed ids' values first: z may be overwritten in place
+        // the listed ids' values first: z may be written over in place
         constexpr int KPT = (LD_MAX_K + LD_THREADS - 1) / LD_THREADS;
         float own[KPT];
 #pragma unroll
         for (int n = 0; n < KPT; ++n) {
             const int k = static_cast<int>(threadIdx.x) + n * LD_THREADS;
             own[n] = 0.f;
-            if (k < a.K && th.id[k] >= c0 && th.id[k] < c1) {
-                float q = th.q[k];
+            if (k < a.K && ids[k] >= c0 && ids[k] < c1) {
+                float q = 0.f;
                 if (hd.dup) {   // ids listed more than once add up, in the list's order
-                    q = 0.f;
                     for (int j = 0; j < a.K; ++j)
-                        q += th.id[j] == th.id[k] ? th.q[j] : 0.f;
+                        q += ids[j] == ids[k] ? q_of(listed_logq<TAIL>(teacher[j], tau, w)) : 0.f;
+                } else {
+                    q = q_of(listed_logq<TAIL>(teacher[k], tau, w));
                 }
-                own[n] = (prob(Elem<T>::load(src + th.id[k] - off)) - q) * gi;
+                const float p = exp2_approx(fmaf(Elem<T>::load(src + ids[k] - off), first, -ref) * second) * scale;
+                own[n] = (p - q) * gi;
             }
         }
-        __syncthreads();
-        const float wgi = w * gi * scale;
-        const Pair inv2 = pair(inv_tau, inv_tau), ref2 = pair(-ref, -ref), e2 = pair(LG_LOG2E, LG_LOG2E),
+        if constexpr (!HOLD)
+            __syncthreads();
+        const float wgi = others * gi * scale;
+        const Pair first2 = pair(first, first), ref2 = pair(-ref, -ref), second2 = pair(second, second),
                    w2 = pair(wgi, wgi);
         for (int b = c0 + warp * 512; b < c1; b += LD_WARPS * 512) {
             Raw8<T> raw[2];
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-                load8<T>(raw[u], src, b + u * 256 + lane * 8 - off, c1 - off, shift);
+            load_chunks<T, 2>(raw, src, b - off, c1 - off, shift);
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 float v[8];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     float lo, hi;
-                    unpair(mul2(fma2(get2<T>(raw[u], k), inv2, ref2), e2), lo, hi);
+                    unpair(mul2(fma2(get2<T>(raw[u], k), first2, ref2), second2), lo, hi);
                     unpair(mul2(pair(exp2_approx(lo), exp2_approx(hi)), w2), v[2 * k], v[2 * k + 1]);
                 }
                 store8<T>(dz, b + u * 256 + lane * 8, c1, shift_out, v);
@@ -363,9 +405,11 @@ __global__ void __launch_bounds__(LD_THREADS) distill_kernel(const DistillArgs a
 #pragma unroll
         for (int n = 0; n < KPT; ++n) {
             const int k = static_cast<int>(threadIdx.x) + n * LD_THREADS;
-            if (k < a.K && th.id[k] >= c0 && th.id[k] < c1)
-                dz[th.id[k]] = Elem<T>::from(own[n]);
+            if (k < a.K && ids[k] >= c0 && ids[k] < c1)
+                dz[ids[k]] = Elem<T>::from(own[n]);
         }
+        if (SUMS && rank == 0 && warp == LD_WARPS - 1)
+            write_loss();
     }
 }
 

@@ -82,7 +82,7 @@ __device__ __forceinline__ RowRules row_rules(const ProcArgs &a, int row)
     return r;
 }
 
-// A touched column: processed value y (mask apart) and its slope dy/dz.
+// A touched column before the temperature: x, and its slope dx/dz.
 __device__ __forceinline__ float touched_value(const RowRules &r, float z, float bias, uint32_t word, float &slope)
 {
     float x = z + bias;
@@ -94,8 +94,7 @@ __device__ __forceinline__ float touched_value(const RowRules &r, float z, float
     const uint32_t c = word & kCount;
     if (c != 0)
         x = x - r.freq * static_cast<float>(c) - r.pres;
-    slope /= r.tau;
-    return x / r.tau;
+    return x;
 }
 
 // ---------------------------------------------------------------- touched columns
@@ -140,7 +139,7 @@ __device__ __forceinline__ void scan_ids(const int32_t *ids, int j0, int j1, int
     }
 }
 
-// Builds the table of columns c0 .. c0 + width - 1 with replacement(id, y, slope)
+// Builds the table of columns c0 .. c0 + width - 1 with replacement(id, x, slope)
 // for each.  All threads of the CTA; false (in all) where the row's bias ids are
 // out of range or order.  Ends with a barrier.
 template <typename T, typename F>
@@ -202,10 +201,10 @@ __device__ bool build_table(const ProcArgs &a, const RowRules &r, const T *z, in
     __syncthreads();
     auto finish = [&](int n, int id, float bias) {
         float slope;
-        float y = touched_value(r, Elem<T>::load(z + id), bias, t.value[n] & ~kBiased, slope);
+        float x = touched_value(r, Elem<T>::load(z + id), bias, t.value[n] & ~kBiased, slope);
         if (r.mask && !(r.mask[id >> 3] >> (id & 7) & 1))
-            y = neg_inf();
-        t.value[n] = __float_as_uint(replacement(id, y, slope));
+            x = neg_inf();
+        t.value[n] = __float_as_uint(replacement(id, x, slope));
     };
     for (int n = threadIdx.x; n < t.used; n += LP_THREADS)
         if (!(t.value[n] & kBiased))
@@ -281,9 +280,10 @@ __global__ void __launch_bounds__(LP_THREADS) process_map_kernel(const ProcArgs 
             if (!bad && !zero) {
                 if (c0 != seg0)
                     __syncthreads();   // the table before has been written out
-                bad = !build_table(a, r, z, c0, c1 - c0, t, [&](int id, float y, float slope) {
+                bad = !build_table(a, r, z, c0, c1 - c0, t, [&](int id, float x, float slope) {
+                    const float y = x / r.tau;
                     if constexpr (OP == LP_GRAD)
-                        return y == neg_inf() ? 0.f : ((id == target ? 1.f : 0.f) - probability(y)) * (g * slope);
+                        return y == neg_inf() ? 0.f : ((id == target ? 1.f : 0.f) - probability(y)) * (g * (slope / r.tau));
                     else
                         return y;
                 });
@@ -304,12 +304,12 @@ __global__ void __launch_bounds__(LP_THREADS) process_map_kernel(const ProcArgs 
         for (int b = c0 + warp * 512; b < c1; b += LP_WARPS * 512) {
             Raw8<T> raw[2];
             uint32_t ok[2] = {0xffu, 0xffu};
+            load_chunks<T, 2>(raw, z, b, c1, shift);
+            if (r.mask) {
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const int col = b + u * 256 + lane * 8;
-                load8<T>(raw[u], z, col, c1, shift);
-                if (r.mask && col < c1)
-                    ok[u] = r.mask[col >> 3];
+                for (int u = 0; u < 2; ++u)
+                    if (b + u * 256 + lane * 8 < c1)
+                        ok[u] = r.mask[(b + u * 256 + lane * 8) >> 3];
             }
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
@@ -356,7 +356,7 @@ __global__ void __launch_bounds__(LP_THREADS) process_logp_kernel(const ProcArgs
 {
     extern __shared__ uint32_t smem[];
     __shared__ float2 part[LG_MAX_SLICES];
-    __shared__ float target_y;
+    __shared__ float target_x;
     const int rank = static_cast<int>(cluster_ctarank());
     const int row = static_cast<int>(blockIdx.x / static_cast<unsigned>(a.segs));
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -380,48 +380,45 @@ __global__ void __launch_bounds__(LP_THREADS) process_logp_kernel(const ProcArgs
         if constexpr (TOUCH) {
             if (f0 != s0)
                 __syncthreads();   // the table before has been read
-            bad = !build_table(a, r, z, c0, min(a.V, f1 * LG_SLICE) - c0, t, [](int, float y, float) { return y; });
+            bad = !build_table(a, r, z, c0, min(a.V, f1 * LG_SLICE) - c0, t, [](int, float x, float) { return x; });
             if (bad)
                 break;
         }
         if (threadIdx.x == 0 && target >= c0 && target < min(a.V, f1 * LG_SLICE)) {
-            if (TOUCH && (t.bitmap[(target - c0) >> 5] >> ((target - c0) & 31) & 1)) {
-                target_y = __uint_as_float(t.value[rank_of(t, target - c0)]);
-            } else {
-                const bool in = !r.mask || (r.mask[target >> 3] >> (target & 7) & 1);
-                target_y = in ? __fmul_rn(Elem<T>::load(z + target), r.inv_tau) : neg_inf();
-            }
+            const bool in = !r.mask || (r.mask[target >> 3] >> (target & 7) & 1);
+            if (!in)
+                target_x = neg_inf();
+            else if (TOUCH && (t.bitmap[(target - c0) >> 5] >> ((target - c0) & 31) & 1))
+                target_x = __uint_as_float(t.value[rank_of(t, target - c0)]);
+            else
+                target_x = Elem<T>::load(z + target);
         }
         for (int s = f0 + warp; s < f1; s += LP_WARPS) {
             Raw8<T> raw[4];
-            uint32_t drop[4];
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const int col = s * LG_SLICE + u * 256 + lane * 8;
-                load8<T>(raw[u], z, col, a.V, shift);
-                drop[u] = r.mask && col < a.V ? ~static_cast<uint32_t>(r.mask[col >> 3]) & 0xffu : 0u;
-            }
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const int col = s * LG_SLICE + u * 256 + lane * 8;
-                if (TOUCH && col < a.V)
-                    drop[u] |= reinterpret_cast<const uint8_t *>(t.bitmap)[(col - c0) >> 3];
-                if (drop[u])
-                    drop8(raw[u], drop[u]);
-            }
-            float m, sum;
-            warp_sums<T, 4>(raw, r.inv_tau, k2, m, sum);
+            load_chunks<T, 4>(raw, z, s * LG_SLICE, a.V, shift);
+            int n0 = 0, n1 = 0;   // the slice's touched columns
             if constexpr (TOUCH) {
                 const int word = (s - f0) * (LG_SLICE / 32);
-                const int n0 = t.before[word], n1 = word + LG_SLICE / 32 < t.words ? t.before[word + LG_SLICE / 32] : t.used;
-                if (n1 > n0) {
-                    float tm = neg_inf(), ts = 0.f;
-                    for (int n = n0 + lane; n < n1; n += 32)
-                        join_value(tm, ts, __uint_as_float(t.value[n]));
-                    warp_join(tm, ts);
-                    join(m, sum, tm, ts);
+                n0 = t.before[word];
+                n1 = word + LG_SLICE / 32 < t.words ? t.before[word + LG_SLICE / 32] : t.used;
+            }
+            if (r.mask || n1 > n0) {
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const int col = s * LG_SLICE + u * 256 + lane * 8;
+                    uint32_t drop = 0u;
+                    if (col < a.V) {
+                        if (r.mask)
+                            drop = ~static_cast<uint32_t>(r.mask[col >> 3]) & 0xffu;
+                        if (TOUCH)
+                            drop |= reinterpret_cast<const uint8_t *>(t.bitmap)[(col - c0) >> 3];
+                    }
+                    if (drop)
+                        drop8(raw[u], drop);
                 }
             }
+            float m, sum;
+            warp_sums<T, 4>(raw, k2, t.value + n0, n1 - n0, m, sum);
             if (lane == 0)
                 part[s] = make_float2(m, sum);
         }
@@ -434,7 +431,7 @@ __global__ void __launch_bounds__(LP_THREADS) process_logp_kernel(const ProcArgs
             for (int s = s0 + static_cast<int>(threadIdx.x); s < s1; s += LP_THREADS)
                 st_cluster_f2(part0 + s * 8, part[s].x, part[s].y);
             if (threadIdx.x == 0 && has_target)
-                st_shared_cluster(mapa_shared(smem_u32(&target_y), 0), __float_as_int(target_y));
+                st_shared_cluster(mapa_shared(smem_u32(&target_x), 0), __float_as_int(target_x));
         }
         __syncwarp();
         cluster_arrive();
@@ -444,13 +441,13 @@ __global__ void __launch_bounds__(LP_THREADS) process_logp_kernel(const ProcArgs
         float m = neg_inf(), sum = 0.f;
         if (!bad) {   // in slice order: lane l takes slices l, l + 32, ...
             for (int s = lane; s < slices; s += 32)
-                join(m, sum, part[s].x, part[s].y);
-            warp_join(m, sum);
+                join(m, sum, part[s].x, part[s].y, k2);
+            warp_join(m, sum, k2);
         }
         if (lane == 0) {
             const bool in = target >= 0 && target < a.V;
-            a.out_lse[row] = bad ? quiet_nan() : row_lse(m, sum);
-            a.out_logp[row] = bad || !in ? quiet_nan() : row_logp(target_y, m, sum);
+            a.out_lse[row] = bad ? quiet_nan() : row_lse(m, sum, r.inv_tau);
+            a.out_logp[row] = bad || !in ? quiet_nan() : row_logp(target_x, m, sum, r.inv_tau);
             if (bad)
                 report_bad_input(a.status);
         }

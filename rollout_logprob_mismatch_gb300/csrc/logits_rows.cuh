@@ -2,10 +2,12 @@
 // eight columns of a row at a time (any element type, any alignment), and the
 // reduction of a slice of a row to (maximum, sum of exponentials).
 //
-// Log-sum-exp: a set of columns with values y is the pair (M, S), M = max y,
-// S = sum e^(y - M); two sets join as M = max(M1, M2), S = S1 e^(M1 - M) +
-// S2 e^(M2 - M); lse = M + log S.  A set of -inf columns only is (-inf, 0).  NaN
-// and +inf make S NaN.
+// Log-sum-exp of y = x / tau: a set of columns is the pair (M, S), M = max x,
+// S = sum e^((x - M) / tau) = sum 2^((x - M) k2), k2 = log2(e) / tau; two sets join
+// as M = max(M1, M2), S = S1 2^((M1 - M) k2) + S2 2^((M2 - M) k2); lse = M / tau +
+// log S.  The difference comes before the scale: the largest column's term is
+// exactly 1, and a row of the type's lowest values does not overflow.  A set of
+// -inf columns only is (-inf, 0).  NaN and +inf make S NaN.
 #pragma once
 
 #include <cstdint>
@@ -215,6 +217,32 @@ __device__ __forceinline__ void store8(T *row, int col, int V, uint32_t shift, c
             row[col + i] = Elem<T>::from(v[i]);
 }
 
+// N chunks of 256 columns from column b on, into N registers of eight a lane.  Away
+// from a row's end, in an aligned row, nothing has to be looked at per load.
+template <typename T, int N>
+__device__ __forceinline__ void load_chunks(Raw8<T> (&r)[N], const T *row, int b, int V, uint32_t shift)
+{
+    constexpr int W = Elem<T>::WORDS;
+    const int lane = threadIdx.x & 31;
+    if (shift == 0 && b + N * 256 <= V) {
+        const uint4 *p = reinterpret_cast<const uint4 *>(row + b) + lane * (W / 4);
+#pragma unroll
+        for (int u = 0; u < N; ++u)
+#pragma unroll
+            for (int k = 0; k < W / 4; ++k) {
+                const uint4 v = p[u * 8 * W + k];
+                r[u].w[4 * k] = v.x;
+                r[u].w[4 * k + 1] = v.y;
+                r[u].w[4 * k + 2] = v.z;
+                r[u].w[4 * k + 3] = v.w;
+            }
+        return;
+    }
+#pragma unroll
+    for (int u = 0; u < N; ++u)
+        load8<T>(r[u], row, b + u * 256 + lane * 8, V, shift);
+}
+
 // Columns whose bit in `drop` is set become -inf.
 template <typename T> __device__ __forceinline__ void drop8(Raw8<T> &r, uint32_t drop)
 {
@@ -317,15 +345,18 @@ template <typename T, int N> __device__ __forceinline__ float raw_max(const Raw8
     }
 }
 
-// (M, S) of a warp's columns y = x / tau, in every lane: the warp's largest x
-// first (with packed maxima on the raw 16-bit pairs), then one pass of
-// e^((x - max) / tau) = 2^((x - max) k2), k2 = log2(e) / tau.  The difference comes
-// before the product, so a row of the type's lowest values does not overflow.
+// (M, S), in every lane, of a warp's columns and of the n values at `more`: the
+// largest first (with packed maxima on the raw 16-bit pairs), then the sum.
 template <typename T, int N>
-__device__ __forceinline__ void warp_sums(const Raw8<T> (&raw)[N], float inv_tau, float k2, float &M, float &S)
+__device__ __forceinline__ void warp_sums(const Raw8<T> (&raw)[N], float k2, const uint32_t *more, int n, float &M,
+                                          float &S)
 {
-    const float m = warp_max(raw_max<T, N>(raw));
-    const float ref = finite_ref(m);
+    const int lane = threadIdx.x & 31;
+    float top = raw_max<T, N>(raw);
+    for (int i = lane; i < n; i += 32)
+        top = fmaxf(top, __uint_as_float(more[i]));
+    M = warp_max(top);
+    const float ref = finite_ref(M);
     const Pair neg = pair(-ref, -ref), kk = pair(k2, k2);
     Pair acc[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
 #pragma unroll
@@ -338,40 +369,48 @@ __device__ __forceinline__ void warp_sums(const Raw8<T> (&raw)[N], float inv_tau
         }
     float lo, hi;
     unpair(add2(acc[0], acc[1]), lo, hi);
-    M = __fmul_rn(m, inv_tau);
-    S = warp_sum(lo + hi);
+    lo += hi;
+    for (int i = lane; i < n; i += 32)
+        lo += exp2_approx(__fmul_rn(__uint_as_float(more[i]) - ref, k2));
+    S = warp_sum(lo);
 }
 
 // Joins (n, t) into (m, s).
-__device__ __forceinline__ void join(float &m, float &s, float n, float t)
+__device__ __forceinline__ void join(float &m, float &s, float n, float t, float k2)
 {
     const float k = fmaxf(m, n), ref = finite_ref(k);
-    s = __fmaf_rn(s, exp2_approx(__fmul_rn(m - ref, LG_LOG2E)), __fmul_rn(t, exp2_approx(__fmul_rn(n - ref, LG_LOG2E))));
+    s = __fmaf_rn(s, exp2_approx(__fmul_rn(m - ref, k2)), __fmul_rn(t, exp2_approx(__fmul_rn(n - ref, k2))));
     m = k;
 }
 
-// Adds one value to a lane's (m, s).
-__device__ __forceinline__ void join_value(float &m, float &s, float y) { join(m, s, y, y == neg_inf() ? 0.f : 1.f); }
+// Adds one column to a lane's (m, s).
+__device__ __forceinline__ void join_value(float &m, float &s, float x, float k2)
+{
+    join(m, s, x, x == neg_inf() ? 0.f : 1.f, k2);
+}
 
 // The warp's (m, s) from its lanes', in every lane.
-__device__ __forceinline__ void warp_join(float &m, float &s)
+__device__ __forceinline__ void warp_join(float &m, float &s, float k2)
 {
     const float n = warp_max(m);
-    s = warp_sum(__fmul_rn(s, exp2_approx(__fmul_rn(m - finite_ref(n), LG_LOG2E))));
+    s = warp_sum(__fmul_rn(s, exp2_approx(__fmul_rn(m - finite_ref(n), k2))));
     m = n;
 }
 
 // Natural log of a folded row's sum of exponentials: -inf for an empty row, NaN
 // where the row held a NaN or +inf.
-__device__ __forceinline__ float row_lse(float m, float s) { return s == 0.f ? neg_inf() : m + logf(s); }
-
-// log-probability of a column with value y (from the pair, not from the rounded
-// lse: a probability near 1 keeps its digits).
-__device__ __forceinline__ float row_logp(float y, float m, float s)
+__device__ __forceinline__ float row_lse(float m, float s, float inv_tau)
 {
-    if (s == 0.f || (y == neg_inf() && s == s))
+    return s == 0.f ? neg_inf() : __fmaf_rn(m, inv_tau, logf(s));
+}
+
+// log-probability of a column x (from the pair, not from the rounded lse: a
+// probability near 1 keeps its digits).
+__device__ __forceinline__ float row_logp(float x, float m, float s, float inv_tau)
+{
+    if (s == 0.f || (x == neg_inf() && s == s))
         return neg_inf();
-    return (y - m) - logf(s);
+    return __fmaf_rn(x - m, inv_tau, -logf(s));
 }
 
 __device__ __forceinline__ void report_bad_input(int *status)
