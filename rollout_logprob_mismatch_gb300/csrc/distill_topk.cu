@@ -37,7 +37,8 @@ struct TeacherRow {
 };
 
 // Shared memory of a CTA: the header, the slices' partials, the student's z at the
-// listed ids, the bitmap of the rank's columns, the rank's part of the row.
+// listed ids, the bitmap of the rank's columns, the table drop8 takes (16-bit types
+// with a tail), the rank's part of the row.
 struct Head {
     uint64_t bar;
     int dup, abort;
@@ -46,16 +47,17 @@ struct Head {
 };
 
 struct Layout {
-    uint32_t part, x, bits, row, bytes;
+    uint32_t part, x, bits, masks, row, bytes;
 };
 
-template <typename T> __host__ __device__ inline Layout layout(int slices, int per, int K, bool sums, bool bits, bool hold)
+template <typename T> __host__ __device__ inline Layout layout(int slices, int per, int K, bool sums, bool bits, bool tail, bool hold)
 {
     Layout l;
     l.part = sizeof(Head);
     l.x = l.part + (sums ? static_cast<uint32_t>(slices) * 16 : 0);
     l.bits = l.x + (sums ? static_cast<uint32_t>(K + 3) / 4 * 16 : 0);
-    l.row = l.bits + (bits ? static_cast<uint32_t>(per) * (LG_SLICE / 8) : 0);
+    l.masks = l.bits + (bits ? static_cast<uint32_t>(per) * (LG_SLICE / 8) : 0);
+    l.row = l.masks + (sums && tail && sizeof(T) == 2 ? static_cast<uint32_t>(sizeof(HalfMasks)) : 0);
     l.bytes = l.row + (hold ? static_cast<uint32_t>(per) * LG_SLICE * static_cast<uint32_t>(sizeof(T)) + 16 : 0);
     return l;
 }
@@ -148,11 +150,12 @@ __global__ void __launch_bounds__(LD_THREADS) distill_kernel(const DistillArgs a
     constexpr bool SUMS = OP != LD_BACKWARD, GRAD = OP != LD_FORWARD, BITS = TAIL || GRAD;
     extern __shared__ __align__(16) uint8_t smem[];
     const int slices = (a.V + LG_SLICE - 1) / LG_SLICE;
-    const Layout lay = layout<T>(slices, a.per, a.K, SUMS, BITS, HOLD);
+    const Layout lay = layout<T>(slices, a.per, a.K, SUMS, BITS, TAIL, HOLD);
     Head &hd = *reinterpret_cast<Head *>(smem);
     float4 *part = reinterpret_cast<float4 *>(smem + lay.part);
     float *listed_x = reinterpret_cast<float *>(smem + lay.x);
     uint32_t *bitmap = reinterpret_cast<uint32_t *>(smem + lay.bits);   // columns of this rank
+    HalfMasks &masks = *reinterpret_cast<HalfMasks *>(smem + lay.masks);
     const int rank = static_cast<int>(cluster_ctarank());
     const int row = static_cast<int>(blockIdx.x / static_cast<unsigned>(a.ranks));
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -187,7 +190,7 @@ __global__ void __launch_bounds__(LD_THREADS) distill_kernel(const DistillArgs a
     auto zero_row = [&] {
         const float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
         for (int b = c0 + warp * 256; b < c1; b += LD_WARPS * 256)
-            store8<T>(dz, b + lane * 8, c1, shift_out, v);
+            store8<T>(dz, b + lane * 8, c1, shift_out, pack8<T>(v));
     };
     if constexpr (!SUMS) {
         if (g == 0.f) {
@@ -200,6 +203,8 @@ __global__ void __launch_bounds__(LD_THREADS) distill_kernel(const DistillArgs a
     if constexpr (BITS) {
         for (int j = threadIdx.x; j < (c1 - c0 + 31) / 32; j += LD_THREADS)
             bitmap[j] = 0;
+        if constexpr (SUMS && TAIL && sizeof(T) == 2)
+            masks.fill();
         __syncthreads();
     }
     for (int k = threadIdx.x; k < a.K; k += LD_THREADS) {
@@ -248,7 +253,7 @@ __global__ void __launch_bounds__(LD_THREADS) distill_kernel(const DistillArgs a
                         for (int i = 0; i < 8; ++i)
                             if (bits >> i & 1)
                                 join_value(km, ks, Elem<T>::get(raw[u].w, i), k2);
-                        drop8(raw[u], bits);
+                        drop8(raw[u], bits, masks);
                     }
                 }
                 if (__any_sync(0xffffffffu, ks != 0.f))
@@ -398,7 +403,7 @@ __global__ void __launch_bounds__(LD_THREADS) distill_kernel(const DistillArgs a
                     unpair(mul2(fma2(get2<T>(raw[u], k), first2, ref2), second2), lo, hi);
                     unpair(mul2(pair(exp2_approx(lo), exp2_approx(hi)), w2), v[2 * k], v[2 * k + 1]);
                 }
-                store8<T>(dz, b + u * 256 + lane * 8, c1, shift_out, v);
+                store8<T>(dz, b + u * 256 + lane * 8, c1, shift_out, pack8<T>(v));
             }
         }
         __syncthreads();
@@ -443,11 +448,11 @@ template <typename T, int OP, bool TAIL> cudaError_t launch(DistillArgs a, int n
     a.ranks = (slices + a.per - 1) / a.per;
     constexpr bool SUMS = OP != LD_BACKWARD, BITS = TAIL || OP != LD_FORWARD;
     if constexpr (OP == LD_STEP) {
-        const Layout l = layout<T>(slices, a.per, a.K, SUMS, BITS, true);
+        const Layout l = layout<T>(slices, a.per, a.K, SUMS, BITS, TAIL, true);
         if (l.bytes <= LD_SMEM)
             return launch_kernel<T, OP, TAIL, true>(a, l, s);
     }
-    return launch_kernel<T, OP, TAIL, false>(a, layout<T>(slices, a.per, a.K, SUMS, BITS, false), s);
+    return launch_kernel<T, OP, TAIL, false>(a, layout<T>(slices, a.per, a.K, SUMS, BITS, TAIL, false), s);
 }
 
 template <typename T> cudaError_t launch_op(const DistillArgs &a, int op, int num_sms, cudaStream_t s)

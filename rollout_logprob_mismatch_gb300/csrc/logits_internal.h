@@ -21,10 +21,12 @@ constexpr int LG_CLUSTER = 8;                      // CTAs that share a row, at 
 inline int lg_slices(int64_t V) { return static_cast<int>((V + LG_SLICE - 1) / LG_SLICE); }
 
 // ---------------------------------------------------------------- processing
-constexpr int LP_THREADS = 384;
-constexpr int LP_WARPS = LP_THREADS / 32;
-constexpr int LP_CAP = 8192;                       // touched columns a table holds (a multiple of LG_SLICE)
+constexpr int LP_MAP_THREADS = 256, LP_MAP_CTAS = 6;     // WRITE, GRAD; CTAs of an SM the registers are held to
+constexpr int LP_LOGP_THREADS = 384, LP_LOGP_CTAS = 4;   // LOGP
+constexpr int LP_MAP_SLICES = 64;                  // slices of a segment at most
+constexpr int LP_MAP_CAP = 3072, LP_LOGP_CAP = 2048;     // touched columns a table holds (at least LG_SLICE)
 constexpr int LP_TABLE = 1 << 18;                  // columns a table covers
+static_assert(LP_MAP_SLICES * LG_SLICE <= 65536, "a segment's columns are counted in 16 bits");
 
 enum { LP_WRITE = 0, LP_LOGP = 1, LP_GRAD = 2 };
 
@@ -51,6 +53,7 @@ struct ProcArgs {
     int32_t seg_slices;        // WRITE, GRAD: slices of a CTA; LOGP: of a cluster rank
     int32_t segs;              // CTAs of a row
     int32_t table_columns;     // columns the shared-memory table has room for
+    int32_t table_cap;         // touched ones among them
     int *status;
 };
 

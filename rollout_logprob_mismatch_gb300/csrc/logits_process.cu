@@ -36,33 +36,54 @@ constexpr uint32_t kPrompt = 0x80000000u, kBiased = 0x40000000u, kCount = 0x3fff
 
 struct RowRules {
     float tau, inv_tau, rho, pres, freq;
+    float grad, lse;           // GRAD
+    int target;                // LOGP, GRAD
     int h0, hg, h1;            // history span
     int b0, b1;                // bias entries
     const uint8_t *mask;       // the row's bits, or null
     bool bad;
 };
 
-__device__ __forceinline__ RowRules row_rules(const ProcArgs &a, int row)
+// One warp reads a row's scalars for its CTA, each lane one of them: the loads
+// overlap (one thread's chain of conditional loads cost 6 us a row).
+__device__ __forceinline__ void read_rules(const ProcArgs &a, int row, RowRules &out)
 {
+    const int lane = threadIdx.x & 31;
+    const void *p = nullptr;
+    int64_t at = row;
+    uint32_t v = 0;
+    switch (lane) {
+    case 0: p = a.temperature; v = 0x3f800000u; break;
+    case 1: p = a.repetition; v = 0x3f800000u; break;
+    case 2: p = a.presence; break;
+    case 3: p = a.frequency; break;
+    case 4: p = a.grad; break;
+    case 5: p = a.lse; break;
+    case 6: p = a.targets; v = 0xffffffffu; break;
+    case 7: p = a.allowed_rows; v = a.allowed ? static_cast<uint32_t>(row) : 0xffffffffu; break;
+    case 8: p = a.bias_offsets; break;
+    case 9: p = a.bias_offsets; at = static_cast<int64_t>(row) + 1; break;
+    case 10: case 11: case 12: p = a.spans; at = static_cast<int64_t>(row) * 3 + (lane - 10); break;
+    default: break;
+    }
+    if (p)
+        v = static_cast<const uint32_t *>(p)[at];
+    auto f = [&](int k) { return __uint_as_float(__shfl_sync(0xffffffffu, v, k)); };
+    auto i = [&](int k) { return static_cast<int>(__shfl_sync(0xffffffffu, v, k)); };
     RowRules r;
-    r.tau = a.temperature ? a.temperature[row] : 1.f;
-    r.rho = a.repetition ? a.repetition[row] : 1.f;
-    r.pres = a.presence ? a.presence[row] : 0.f;
-    r.freq = a.frequency ? a.frequency[row] : 0.f;
-    r.h0 = r.hg = r.h1 = r.b0 = r.b1 = 0;
-    if (a.spans) {
-        const int32_t *s = a.spans + static_cast<int64_t>(row) * 3;
-        r.h0 = s[0];
-        r.hg = s[1];
-        r.h1 = s[2];
-    }
-    if (a.bias_offsets) {
-        r.b0 = a.bias_offsets[row];
-        r.b1 = a.bias_offsets[row + 1];
-    }
-    int m = -1;
-    if (a.allowed)
-        m = a.allowed_rows ? a.allowed_rows[row] : row;
+    r.tau = f(0);
+    r.rho = f(1);
+    r.pres = f(2);
+    r.freq = f(3);
+    r.grad = f(4);
+    r.lse = f(5);
+    r.target = i(6);
+    int m = i(7);
+    r.b0 = i(8);
+    r.b1 = i(9);
+    r.h0 = i(10);
+    r.hg = i(11);
+    r.h1 = i(12);
     r.inv_tau = 1.f / r.tau;
     r.bad = !(r.tau > 0.f) || !isfinite(r.tau) || !isfinite(r.inv_tau) || !(r.rho > 0.f) || !isfinite(r.rho) ||
             !isfinite(1.f / r.rho) || !isfinite(r.pres) || !isfinite(r.freq);
@@ -74,12 +95,18 @@ __device__ __forceinline__ RowRules row_rules(const ProcArgs &a, int row)
         r.bad = true;
         r.b0 = r.b1 = 0;
     }
-    if (m >= a.num_allowed && a.allowed) {
+    if (a.allowed && m >= a.num_allowed) {
         r.bad = true;
         m = -1;
     }
-    r.mask = m >= 0 ? reinterpret_cast<const uint8_t *>(a.allowed + m * a.allowed_ld) : nullptr;
-    return r;
+    r.mask = a.allowed && m >= 0 ? reinterpret_cast<const uint8_t *>(a.allowed + m * a.allowed_ld) : nullptr;
+    if (lane == 0)
+        out = r;
+}
+
+__device__ __forceinline__ bool is_allowed(const uint8_t *mask, int id)
+{
+    return !mask || (mask[id >> 3] >> (id & 7) & 1);
 }
 
 // A touched column before the temperature: x, and its slope dx/dz.
@@ -98,77 +125,112 @@ __device__ __forceinline__ float touched_value(const RowRules &r, float z, float
 }
 
 // ---------------------------------------------------------------- touched columns
-struct Table {
-    uint32_t *value;     // [LP_CAP]: counts, then the column's replacement (fp32 bits)
-    uint32_t *bitmap;    // [LP_TABLE / 32]
-    uint16_t *before;    // [LP_TABLE / 32]: bits set in the words before
-    int words, used;     // of the columns in hand
+template <typename C> struct Table {
+    uint32_t *value;     // [cap]: counts, then the column's replacement (fp32 bits)
+    uint32_t *bitmap;    // [columns / 32]
+    uint16_t *before;    // [columns / 128]: bits set in the four-word groups before
+    C *column;           // [cap]: relative to the table's first
+    int cap;
+    int groups, used;    // of the columns in hand
 };
 
-__device__ __forceinline__ int rank_of(const Table &t, unsigned k)
+// Bytes of a table over `columns` columns (a multiple of 1024).
+template <typename C> __host__ __device__ inline size_t table_bytes(int columns, int cap)
 {
-    const uint32_t w = t.bitmap[k >> 5];
-    return t.before[k >> 5] + __popc(w & ((1u << (k & 31)) - 1));
+    return static_cast<size_t>(cap) * (4 + sizeof(C)) + columns / 8 + columns / 64;
 }
 
-// Column (relative to the table's first) of entry n.
-__device__ __forceinline__ int column_of(const Table &t, int n)
+template <typename C> __device__ __forceinline__ Table<C> carve(uint32_t *smem, int columns, int cap)
 {
-    int lo = 0, hi = t.words - 1;   // the last word with before <= n
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (t.before[mid] <= n)
-            lo = mid;
-        else
-            hi = mid - 1;
-    }
-    uint32_t w = t.bitmap[lo];
-    for (int skip = n - t.before[lo]; skip > 0; --skip)
-        w &= w - 1;
-    return lo * 32 + __ffs(static_cast<int>(w)) - 1;
+    Table<C> t;
+    t.cap = cap;
+    t.value = smem;
+    t.bitmap = smem + cap;
+    t.before = reinterpret_cast<uint16_t *>(t.bitmap + columns / 32);
+    t.column = reinterpret_cast<C *>(t.before + columns / 128);
+    t.groups = t.used = 0;
+    return t;
 }
 
-// f(position, id relative to c0) for the entries ids[j0 .. j1) within [c0, c0 + width).
-template <typename F>
+// Entry of column k (relative), whose bit is set.
+template <typename C> __device__ __forceinline__ int rank_of(const Table<C> &t, unsigned k)
+{
+    const uint4 w = reinterpret_cast<const uint4 *>(t.bitmap)[k >> 7];
+    const unsigned in = k >> 5 & 3;
+    const uint32_t mine = in == 0 ? w.x : in == 1 ? w.y : in == 2 ? w.z : w.w;
+    return t.before[k >> 7] + (in > 0 ? __popc(w.x) : 0) + (in > 1 ? __popc(w.y) : 0) + (in > 2 ? __popc(w.z) : 0) +
+           __popc(mine & ((1u << (k & 31)) - 1));
+}
+
+template <typename C> __device__ __forceinline__ bool is_touched(const Table<C> &t, int k)
+{
+    return t.bitmap[k >> 5] >> (k & 31) & 1;
+}
+
+// f(position, id relative to c0) for the entries ids[j0 .. j1) within [c0, c0 + width);
+// four loads at a time, so that a long history does not wait for each.
+template <int NT, typename F>
 __device__ __forceinline__ void scan_ids(const int32_t *ids, int j0, int j1, int c0, int width, F f)
 {
-    for (int j = j0 + static_cast<int>(threadIdx.x); j < j1; j += LP_THREADS) {
-        const unsigned k = static_cast<unsigned>(ids[j]) - static_cast<unsigned>(c0);
-        if (k < static_cast<unsigned>(width))
-            f(j, k);
+    for (int j = j0 + static_cast<int>(threadIdx.x); j < j1; j += 4 * NT) {
+        unsigned k[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            k[u] = j + u * NT < j1 ? static_cast<unsigned>(ids[j + u * NT]) - static_cast<unsigned>(c0) : 0xffffffffu;
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (k[u] < static_cast<unsigned>(width))
+                f(j + u * NT, k[u]);
     }
 }
 
-// Builds the table of columns c0 .. c0 + width - 1 with replacement(id, x, slope)
-// for each.  All threads of the CTA; false (in all) where the row's bias ids are
-// out of range or order.  Ends with a barrier.
-template <typename T, typename F>
-__device__ bool build_table(const ProcArgs &a, const RowRules &r, const T *z, int c0, int width, Table &t, F replacement)
+// Empties the table for `width` columns.  All threads; a barrier before use.
+template <int NT, typename C> __device__ __forceinline__ void clear_table(Table<C> &t, int width)
 {
-    __shared__ int warp_bits[LP_WARPS];
+    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+    t.groups = (width + 127) / 128;
+    for (int j = threadIdx.x; j < t.groups; j += NT)
+        reinterpret_cast<uint4 *>(t.bitmap)[j] = zero;
+    for (int j = threadIdx.x; j < t.cap / 4; j += NT)
+        reinterpret_cast<uint4 *>(t.value)[j] = zero;
+}
+
+// Builds the cleared table of columns c0 .. c0 + width - 1 with replacement(id, x,
+// slope) for each.  All threads of the CTA, and the same answer in all: kBad where
+// the row's bias ids are out of range or order, kFull where more columns than the
+// table holds
+// are touched (never for width <= its capacity).  Ends with a barrier.
+enum TableState { kBuilt, kBad, kFull };
+
+template <int NT, typename T, typename C, typename F>
+__device__ TableState build_table(const ProcArgs &a, const RowRules &r, const T *z, int c0, int width, Table<C> &t,
+                                  F replacement)
+{
+    __shared__ int warp_bits[NT / 32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    t.words = (width + 31) / 32;
-    for (int j = threadIdx.x; j < t.words; j += LP_THREADS)
-        t.bitmap[j] = 0;
-    for (int j = threadIdx.x; j < min(LP_CAP, r.h1 - r.h0 + r.b1 - r.b0); j += LP_THREADS)
-        t.value[j] = 0;
+    auto mark = [&](int, unsigned k) { atomicOr(t.bitmap + (k >> 5), 1u << (k & 31)); };
+    scan_ids<NT>(a.history, r.h0, r.h1, c0, width, mark);
     bool bad = false;
-    for (int j = r.b0 + static_cast<int>(threadIdx.x); j < r.b1; j += LP_THREADS) {
+    for (int j = r.b0 + static_cast<int>(threadIdx.x); j < r.b1; j += NT) {
         const int id = a.bias_ids[j];
         bad |= id < 0 || id >= a.V || (j > r.b0 && a.bias_ids[j - 1] >= id);
+        const unsigned k = static_cast<unsigned>(id) - static_cast<unsigned>(c0);
+        if (k < static_cast<unsigned>(width))
+            mark(j, k);
     }
     if (__syncthreads_or(bad))
-        return false;
-    auto mark = [&](int, unsigned k) { atomicOr(t.bitmap + (k >> 5), 1u << (k & 31)); };
-    scan_ids(a.history, r.h0, r.h1, c0, width, mark);
-    scan_ids(a.bias_ids, r.b0, r.b1, c0, width, mark);
-    __syncthreads();
-    // bits before each word: a run of words per thread
-    const int run = (t.words + LP_THREADS - 1) / LP_THREADS;
-    const int w0 = min(t.words, static_cast<int>(threadIdx.x) * run), w1 = min(t.words, w0 + run);
+        return kBad;
+    // bits before each group of four words: a run of groups per thread
+    const uint4 *groups = reinterpret_cast<const uint4 *>(t.bitmap);
+    const int run = (t.groups + NT - 1) / NT;
+    const int q0 = min(t.groups, static_cast<int>(threadIdx.x) * run), q1 = min(t.groups, q0 + run);
+    auto bits_of = [&](int q) {
+        const uint4 w = groups[q];
+        return __popc(w.x) + __popc(w.y) + __popc(w.z) + __popc(w.w);
+    };
     int bits = 0;
-    for (int w = w0; w < w1; ++w)
-        bits += __popc(t.bitmap[w]);
+    for (int q = q0; q < q1; ++q)
+        bits += bits_of(q);
     int upto = bits;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -181,65 +243,74 @@ __device__ bool build_table(const ProcArgs &a, const RowRules &r, const T *z, in
     int base = upto - bits;
     t.used = 0;
 #pragma unroll
-    for (int w = 0; w < LP_WARPS; ++w) {
+    for (int w = 0; w < NT / 32; ++w) {
         base += w < warp ? warp_bits[w] : 0;
         t.used += warp_bits[w];
     }
-    for (int w = w0; w < w1; ++w) {
-        t.before[w] = static_cast<uint16_t>(base);
-        base += __popc(t.bitmap[w]);
+    if (t.used > t.cap) {
+        __syncthreads();   // warp_bits is written again
+        return kFull;
+    }
+    for (int q = q0; q < q1; ++q) {
+        t.before[q] = static_cast<uint16_t>(base);
+        base += bits_of(q);
     }
     __syncthreads();
-    scan_ids(a.history, r.h0, r.h1, c0, width, [&](int j, unsigned k) {
-        uint32_t *v = t.value + rank_of(t, k);
+    scan_ids<NT>(a.history, r.h0, r.h1, c0, width, [&](int j, unsigned k) {
+        const int n = rank_of(t, k);
+        t.column[n] = static_cast<C>(k);   // the same from every token with this id
         if (j >= r.hg)
-            atomicAdd(v, 1u);
+            atomicAdd(t.value + n, 1u);
         else
-            atomicOr(v, kPrompt);
+            atomicOr(t.value + n, kPrompt);
     });
-    scan_ids(a.bias_ids, r.b0, r.b1, c0, width, [&](int, unsigned k) { atomicOr(t.value + rank_of(t, k), kBiased); });
+    scan_ids<NT>(a.bias_ids, r.b0, r.b1, c0, width, [&](int, unsigned k) {
+        const int n = rank_of(t, k);
+        t.column[n] = static_cast<C>(k);
+        atomicOr(t.value + n, kBiased);
+    });
     __syncthreads();
-    auto finish = [&](int n, int id, float bias) {
+    auto finish = [&](int n, int id, float logit, float bias) {
         float slope;
-        float x = touched_value(r, Elem<T>::load(z + id), bias, t.value[n] & ~kBiased, slope);
-        if (r.mask && !(r.mask[id >> 3] >> (id & 7) & 1))
+        float x = touched_value(r, logit, bias, t.value[n] & ~kBiased, slope);
+        if (!is_allowed(r.mask, id))
             x = neg_inf();
         t.value[n] = __float_as_uint(replacement(id, x, slope));
     };
-    for (int n = threadIdx.x; n < t.used; n += LP_THREADS)
-        if (!(t.value[n] & kBiased))
-            finish(n, c0 + column_of(t, n), 0.f);
+    for (int n = threadIdx.x; n < t.used; n += 2 * NT) {
+        const int n1 = n + NT;
+        const bool in0 = !(t.value[n] & kBiased), in1 = n1 < t.used && !(t.value[n1] & kBiased);
+        const int id0 = c0 + t.column[n], id1 = in1 ? c0 + t.column[n1] : 0;
+        const float z0 = in0 ? Elem<T>::load(z + id0) : 0.f, z1 = in1 ? Elem<T>::load(z + id1) : 0.f;
+        if (in0)
+            finish(n, id0, z0, 0.f);
+        if (in1)
+            finish(n1, id1, z1, 0.f);
+    }
     __syncthreads();
     if (r.b1 > r.b0) {   // the biased ones, by their bias entry
-        scan_ids(a.bias_ids, r.b0, r.b1, c0, width,
-                 [&](int j, unsigned k) { finish(rank_of(t, k), c0 + static_cast<int>(k), a.bias_values[j]); });
+        scan_ids<NT>(a.bias_ids, r.b0, r.b1, c0, width,
+                 [&](int j, unsigned k) {
+                         const int id = c0 + static_cast<int>(k);
+                         finish(rank_of(t, k), id, Elem<T>::load(z + id), a.bias_values[j]);
+                     });
         __syncthreads();
     }
-    return true;
+    return kBuilt;
 }
 
-// Columns a table covers at a time.
-__device__ __forceinline__ int table_step(const RowRules &r)
-{
-    return r.h1 - r.h0 + r.b1 - r.b0 <= LP_CAP ? LP_TABLE : LP_CAP;
-}
-
-__device__ __forceinline__ Table carve(uint32_t *smem, int table_columns)
-{
-    Table t;
-    t.value = smem;
-    t.bitmap = smem + LP_CAP;
-    t.before = reinterpret_cast<uint16_t *>(t.bitmap + table_columns / 32);
-    t.words = t.used = 0;
-    return t;
-}
+// Half as many columns, in whole slices.
+__device__ __forceinline__ int half(int columns) { return (columns / 2 + LG_SLICE - 1) / LG_SLICE * LG_SLICE; }
 
 // ---------------------------------------------------------------- kernels
 // WRITE and GRAD: one CTA per (row, segment); no column depends on another.
 template <typename T, typename TO, int OP, bool TOUCH>
-__global__ void __launch_bounds__(LP_THREADS) process_map_kernel(const ProcArgs a)
+__global__ void __launch_bounds__(LP_MAP_THREADS, LP_MAP_CTAS) process_map_kernel(const ProcArgs a)
 {
-    extern __shared__ uint32_t smem[];
+    constexpr int NT = LP_MAP_THREADS, WARPS = NT / 32;
+    extern __shared__ __align__(16) uint32_t smem[];
+    __shared__ RowRules r;
+    __shared__ HalfMasks masks;
     const int row = static_cast<int>(blockIdx.x / static_cast<unsigned>(a.segs));
     const int seg = static_cast<int>(blockIdx.x % static_cast<unsigned>(a.segs));
     const int seg0 = seg * a.seg_slices * LG_SLICE, seg1 = min(a.V, seg0 + a.seg_slices * LG_SLICE);
@@ -247,46 +318,57 @@ __global__ void __launch_bounds__(LP_THREADS) process_map_kernel(const ProcArgs 
     const T *z = static_cast<const T *>(a.z) + row * a.ld;
     TO *out = static_cast<TO *>(a.out) + row * a.ldo;
     const uint32_t shift = row_shift(z), shift_out = row_shift(out);
-
-    const RowRules r = row_rules(a, row);
+    using C = uint16_t;   // a segment has at most 65536 columns
+    Table<C> t = carve<C>(smem, a.table_columns, a.table_cap);
+    if (warp == 0)
+        read_rules(a, row, r);
+    if (sizeof(TO) == 2 && a.allowed)
+        masks.fill();
+    if constexpr (TOUCH)
+        clear_table<NT>(t, seg1 - seg0);
+    __syncthreads();
     bool bad = r.bad;
-    float g = 1.f, lse = 0.f, target_v = 0.f;
-    int target = -1;
-    if constexpr (OP == LP_GRAD) {
-        g = a.grad[row];
-        lse = a.lse[row];
-        if (lse == neg_inf())
-            lse = -neg_inf();   // nothing is left of the row: every probability is 0
-        target = a.targets[row];
-    }
-    auto probability = [&](float y) { return exp2_approx((y - lse) * LG_LOG2E); };
-    const float gi = g * r.inv_tau;
-    const int step = TOUCH ? table_step(r) : LP_TABLE;
-    Table t = carve(smem, a.table_columns);
-    for (int c0 = seg0; c0 < seg1; c0 += step) {
-        const int c1 = min(seg1, c0 + step);
-        const bool zero = OP == LP_GRAD && g == 0.f;
-        const bool has_target = OP == LP_GRAD && target >= c0 && target < c1;
+    const bool zero = OP == LP_GRAD && r.grad == 0.f;
+    const float inv_tau = r.inv_tau, gi = r.grad * inv_tau;
+    const float lse = r.lse == neg_inf() ? -neg_inf() : r.lse;   // an empty row: every probability is 0
+    const uint8_t *const mask = r.mask;
+    const int target = OP == LP_GRAD ? r.target : -1;
+    for (int c0 = seg0, c1, step = LP_TABLE; c0 < seg1; c0 = c1) {
+        c1 = min(seg1, c0 + step);
+        const bool has_target = target >= c0 && target < c1;
+        float target_v = 0.f;
         if constexpr (OP == LP_GRAD) {
-            if (has_target && threadIdx.x == 0) {   // an untouched target's one-hot term
+            if (has_target && threadIdx.x == NT - 1) {   // an untouched target's one-hot term
                 const float x = Elem<T>::load(z + target);
-                const bool in = !r.mask || (r.mask[target >> 3] >> (target & 7) & 1);
-                target_v = in && x != neg_inf() ? (1.f - exp2_approx(fmaf(x, r.inv_tau, -lse) * LG_LOG2E)) * gi : 0.f;
+                target_v = is_allowed(mask, target) && x != neg_inf()
+                               ? (1.f - exp2_approx(fmaf(x, inv_tau, -lse) * LG_LOG2E)) * gi
+                               : 0.f;
             }
             if constexpr (!TOUCH)
                 __syncthreads();   // read before it is written over in place
         }
         if constexpr (TOUCH) {
             if (!bad && !zero) {
-                if (c0 != seg0)
+                if (c0 != seg0 || step != LP_TABLE) {
                     __syncthreads();   // the table before has been written out
-                bad = !build_table(a, r, z, c0, c1 - c0, t, [&](int id, float x, float slope) {
+                    clear_table<NT>(t, c1 - c0);
+                    __syncthreads();
+                }
+                const TableState state = build_table<NT>(a, r, z, c0, c1 - c0, t, [&](int id, float x, float slope) {
                     const float y = x / r.tau;
                     if constexpr (OP == LP_GRAD)
-                        return y == neg_inf() ? 0.f : ((id == target ? 1.f : 0.f) - probability(y)) * (g * (slope / r.tau));
+                        return y == neg_inf() ? 0.f
+                                              : ((id == target ? 1.f : 0.f) - exp2_approx((y - lse) * LG_LOG2E)) *
+                                                    (r.grad * (slope / r.tau));
                     else
                         return y;
                 });
+                bad = state == kBad;
+                if (state == kFull) {
+                    step = half(c1 - c0);
+                    c1 = c0;
+                    continue;
+                }
             }
         }
         if (bad || zero) {
@@ -295,21 +377,22 @@ __global__ void __launch_bounds__(LP_THREADS) process_map_kernel(const ProcArgs 
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 v[i] = fill;
-            for (int b = c0 + warp * 256; b < c1; b += LP_WARPS * 256)
-                store8<TO>(out, b + lane * 8, c1, shift_out, v);
+            const Raw8<TO> f = pack8<TO>(v);
+            for (int b = c0 + warp * 256; b < c1; b += WARPS * 256)
+                store8<TO>(out, b + lane * 8, c1, shift_out, f);
             continue;
         }
-        const Pair inv2 = pair(r.inv_tau, r.inv_tau), lse2 = pair(-lse, -lse), e2 = pair(LG_LOG2E, LG_LOG2E),
+        const Pair inv2 = pair(inv_tau, inv_tau), lse2 = pair(-lse, -lse), e2 = pair(LG_LOG2E, LG_LOG2E),
                    g2 = pair(-gi, -gi);
-        for (int b = c0 + warp * 512; b < c1; b += LP_WARPS * 512) {
+        for (int b = c0 + warp * 512; b < c1; b += WARPS * 512) {
             Raw8<T> raw[2];
-            uint32_t ok[2] = {0xffu, 0xffu};
+            uint32_t drop[2] = {0u, 0u};
             load_chunks<T, 2>(raw, z, b, c1, shift);
-            if (r.mask) {
+            if (mask) {
 #pragma unroll
                 for (int u = 0; u < 2; ++u)
                     if (b + u * 256 + lane * 8 < c1)
-                        ok[u] = r.mask[(b + u * 256 + lane * 8) >> 3];
+                        drop[u] = ~static_cast<uint32_t>(mask[(b + u * 256 + lane * 8) >> 3]) & 0xffu;
             }
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
@@ -325,24 +408,20 @@ __global__ void __launch_bounds__(LP_THREADS) process_map_kernel(const ProcArgs 
                         unpair(mul2(pair(exp2_approx(lo), exp2_approx(hi)), g2), v[2 * k], v[2 * k + 1]);
                     }
                 }
-                if (ok[u] != 0xffu) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        if (!(ok[u] >> i & 1))
-                            v[i] = OP == LP_WRITE ? neg_inf() : 0.f;
-                }
-                store8<TO>(out, b + u * 256 + lane * 8, c1, shift_out, v);
+                Raw8<TO> o = pack8<TO>(v);
+                if (drop[u])
+                    drop8<TO>(o, drop[u], masks, OP == LP_WRITE ? Elem<TO>::NEG_INF : 0u);
+                store8<TO>(out, b + u * 256 + lane * 8, c1, shift_out, o);
             }
         }
         if (TOUCH || OP == LP_GRAD) {
             __syncthreads();   // the touched columns go over what has just been written
-            if (OP == LP_GRAD && has_target && threadIdx.x == 0 &&
-                !(TOUCH && (t.bitmap[(target - c0) >> 5] >> ((target - c0) & 31) & 1)))
+            if (has_target && threadIdx.x == NT - 1 && !(TOUCH && is_touched(t, target - c0)))
                 out[target] = Elem<TO>::from(target_v);
         }
         if constexpr (TOUCH) {
-            for (int n = threadIdx.x; n < t.used; n += LP_THREADS)
-                out[c0 + column_of(t, n)] = Elem<TO>::from(__uint_as_float(t.value[n]));
+            for (int n = threadIdx.x; n < t.used; n += NT)
+                out[c0 + t.column[n]] = Elem<TO>::from(__uint_as_float(t.value[n]));
         }
     }
     if (bad && threadIdx.x == 0)
@@ -352,69 +431,82 @@ __global__ void __launch_bounds__(LP_THREADS) process_map_kernel(const ProcArgs 
 // LOGP: a cluster per row; each rank reduces seg_slices slices, one warp per
 // slice.  The slices' partials go to rank 0's shared memory, which folds them.
 template <typename T, bool TOUCH>
-__global__ void __launch_bounds__(LP_THREADS) process_logp_kernel(const ProcArgs a)
+__global__ void __launch_bounds__(LP_LOGP_THREADS, LP_LOGP_CTAS) process_logp_kernel(const ProcArgs a)
 {
-    extern __shared__ uint32_t smem[];
-    __shared__ float2 part[LG_MAX_SLICES];
+    constexpr int NT = LP_LOGP_THREADS, WARPS = NT / 32;
+    extern __shared__ __align__(16) uint32_t smem[];
+    __shared__ RowRules r;
+    __shared__ HalfMasks masks;
     __shared__ float target_x;
     const int rank = static_cast<int>(cluster_ctarank());
     const int row = static_cast<int>(blockIdx.x / static_cast<unsigned>(a.segs));
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int slices = (a.V + LG_SLICE - 1) / LG_SLICE;
     const int s0 = min(slices, rank * a.seg_slices), s1 = min(slices, s0 + a.seg_slices);
+    using C = int32_t;
+    Table<C> t = carve<C>(smem, a.table_columns, a.table_cap);
+    float2 *part = reinterpret_cast<float2 *>(smem + (TOUCH ? table_bytes<C>(a.table_columns, a.table_cap) / 4 : 0));   // [slices]
     const T *z = static_cast<const T *>(a.z) + row * a.ld;
     const uint32_t shift = row_shift(z);
     if (a.segs > 1)
         cluster_arrive();   // waited for before the first store into rank 0's shared memory
-
-    const RowRules r = row_rules(a, row);
+    if (warp == 0)
+        read_rules(a, row, r);
+    if (sizeof(T) == 2 && (TOUCH || a.allowed))
+        masks.fill();
+    if constexpr (TOUCH)
+        clear_table<NT>(t, min(LP_TABLE, min(a.V, s1 * LG_SLICE) - s0 * LG_SLICE));
+    __syncthreads();
     bool bad = r.bad;
-    const int target = a.targets[row];
+    const float inv_tau = r.inv_tau, k2 = LG_LOG2E * inv_tau;
+    const uint8_t *const mask = r.mask;
+    const int target = r.target;
     const bool has_target = target >= s0 * LG_SLICE && target < min(a.V, s1 * LG_SLICE);
-    const float k2 = LG_LOG2E * r.inv_tau;
-    const int step = (TOUCH ? table_step(r) : LP_TABLE) / LG_SLICE;
-    Table t = carve(smem, a.table_columns);
-    for (int f0 = s0; f0 < s1 && !bad; f0 += step) {
-        const int f1 = min(s1, f0 + step);
-        const int c0 = f0 * LG_SLICE;
+    if (has_target && threadIdx.x == NT - 1)
+        target_x = is_allowed(mask, target) ? Elem<T>::load(z + target) : neg_inf();
+    for (int f0 = s0, f1, step = LP_TABLE / LG_SLICE; f0 < s1 && !bad; f0 = f1) {
+        f1 = min(s1, f0 + step);
+        const int c0 = f0 * LG_SLICE, c1 = min(a.V, f1 * LG_SLICE);
         if constexpr (TOUCH) {
-            if (f0 != s0)
+            if (f0 != s0 || step != LP_TABLE / LG_SLICE) {
                 __syncthreads();   // the table before has been read
-            bad = !build_table(a, r, z, c0, min(a.V, f1 * LG_SLICE) - c0, t, [](int, float x, float) { return x; });
+                clear_table<NT>(t, c1 - c0);
+                __syncthreads();
+            }
+            const TableState state = build_table<NT>(a, r, z, c0, c1 - c0, t, [](int, float x, float) { return x; });
+            bad = state == kBad;
             if (bad)
                 break;
-        }
-        if (threadIdx.x == 0 && target >= c0 && target < min(a.V, f1 * LG_SLICE)) {
-            const bool in = !r.mask || (r.mask[target >> 3] >> (target & 7) & 1);
-            if (!in)
-                target_x = neg_inf();
-            else if (TOUCH && (t.bitmap[(target - c0) >> 5] >> ((target - c0) & 31) & 1))
+            if (state == kFull) {
+                step = half(c1 - c0) / LG_SLICE;
+                f1 = f0;
+                continue;
+            }
+            if (threadIdx.x == NT - 1 && target >= c0 && target < c1 && is_touched(t, target - c0))
                 target_x = __uint_as_float(t.value[rank_of(t, target - c0)]);
-            else
-                target_x = Elem<T>::load(z + target);
         }
-        for (int s = f0 + warp; s < f1; s += LP_WARPS) {
+        for (int s = f0 + warp; s < f1; s += WARPS) {
             Raw8<T> raw[4];
             load_chunks<T, 4>(raw, z, s * LG_SLICE, a.V, shift);
             int n0 = 0, n1 = 0;   // the slice's touched columns
             if constexpr (TOUCH) {
-                const int word = (s - f0) * (LG_SLICE / 32);
-                n0 = t.before[word];
-                n1 = word + LG_SLICE / 32 < t.words ? t.before[word + LG_SLICE / 32] : t.used;
+                const int group = (s - f0) * (LG_SLICE / 128);
+                n0 = t.before[group];
+                n1 = group + LG_SLICE / 128 < t.groups ? t.before[group + LG_SLICE / 128] : t.used;
             }
-            if (r.mask || n1 > n0) {
+            if (mask || n1 > n0) {
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
                     const int col = s * LG_SLICE + u * 256 + lane * 8;
                     uint32_t drop = 0u;
                     if (col < a.V) {
-                        if (r.mask)
-                            drop = ~static_cast<uint32_t>(r.mask[col >> 3]) & 0xffu;
+                        if (mask)
+                            drop = ~static_cast<uint32_t>(mask[col >> 3]) & 0xffu;
                         if (TOUCH)
                             drop |= reinterpret_cast<const uint8_t *>(t.bitmap)[(col - c0) >> 3];
                     }
                     if (drop)
-                        drop8(raw[u], drop);
+                        drop8(raw[u], drop, masks);
                 }
             }
             float m, sum;
@@ -428,9 +520,9 @@ __global__ void __launch_bounds__(LP_THREADS) process_logp_kernel(const ProcArgs
         cluster_wait();
         if (rank != 0) {
             const uint32_t part0 = mapa_shared(smem_u32(part), 0);
-            for (int s = s0 + static_cast<int>(threadIdx.x); s < s1; s += LP_THREADS)
+            for (int s = s0 + static_cast<int>(threadIdx.x); s < s1; s += NT)
                 st_cluster_f2(part0 + s * 8, part[s].x, part[s].y);
-            if (threadIdx.x == 0 && has_target)
+            if (threadIdx.x == NT - 1 && has_target)
                 st_shared_cluster(mapa_shared(smem_u32(&target_x), 0), __float_as_int(target_x));
         }
         __syncwarp();
@@ -446,39 +538,38 @@ __global__ void __launch_bounds__(LP_THREADS) process_logp_kernel(const ProcArgs
         }
         if (lane == 0) {
             const bool in = target >= 0 && target < a.V;
-            a.out_lse[row] = bad ? quiet_nan() : row_lse(m, sum, r.inv_tau);
-            a.out_logp[row] = bad || !in ? quiet_nan() : row_logp(target_x, m, sum, r.inv_tau);
+            a.out_lse[row] = bad ? quiet_nan() : row_lse(m, sum, inv_tau);
+            a.out_logp[row] = bad || !in ? quiet_nan() : row_logp(target_x, m, sum, inv_tau);
             if (bad)
                 report_bad_input(a.status);
         }
     }
 }
 
-// Dynamic shared memory of a table over `columns` columns (a multiple of 1024).
-size_t table_bytes(int columns) { return LP_CAP * 4 + columns / 32 * 6; }
-
 template <typename F> cudaError_t set_smem(F *kernel)
 {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                static_cast<int>(table_bytes(LP_TABLE)));
+                                static_cast<int>(table_bytes<int32_t>(LP_TABLE, LP_LOGP_CAP)) + LG_MAX_SLICES * 8);
 }
 
 template <typename T, typename TO, int OP> cudaError_t launch_map(ProcArgs a, int num_sms, cudaStream_t s)
 {
     const bool touch = a.spans || a.bias_offsets;
     const int slices = lg_slices(a.V);
-    // segments of at most 64 slices, fewer while there are not four CTAs for every SM
-    int per = std::min(64, slices);
-    while (per > 4 && static_cast<int64_t>(a.N) * ((slices + per - 1) / per) < 4 * num_sms)
-        per = (per + 1) / 2;
-    a.seg_slices = per;
-    a.segs = (slices + per - 1) / per;
-    a.table_columns = std::min(LP_TABLE, per * LG_SLICE);
+    // segments of at most LP_MAP_SLICES, fewer while there are not four CTAs for every SM
+    int segs = (slices + LP_MAP_SLICES - 1) / LP_MAP_SLICES;
+    while (segs * 4 < slices && static_cast<int64_t>(a.N) * segs < 4 * num_sms)
+        segs *= 2;
+    a.seg_slices = (slices + segs - 1) / segs;
+    a.segs = (slices + a.seg_slices - 1) / a.seg_slices;
+    a.table_columns = a.seg_slices * LG_SLICE;
+    a.table_cap = LP_MAP_CAP;
     const unsigned grid = static_cast<unsigned>(a.N) * static_cast<unsigned>(a.segs);
     if (touch)
-        process_map_kernel<T, TO, OP, true><<<grid, LP_THREADS, table_bytes(a.table_columns), s>>>(a);
+        process_map_kernel<T, TO, OP, true>
+            <<<grid, LP_MAP_THREADS, table_bytes<uint16_t>(a.table_columns, a.table_cap), s>>>(a);
     else
-        process_map_kernel<T, TO, OP, false><<<grid, LP_THREADS, 0, s>>>(a);
+        process_map_kernel<T, TO, OP, false><<<grid, LP_MAP_THREADS, 0, s>>>(a);
     return cudaGetLastError();
 }
 
@@ -492,10 +583,11 @@ template <typename T> cudaError_t launch_logp(ProcArgs a, int num_sms, cudaStrea
     a.seg_slices = (slices + ranks - 1) / ranks;
     a.segs = (slices + a.seg_slices - 1) / a.seg_slices;
     a.table_columns = std::min(LP_TABLE, a.seg_slices * LG_SLICE);
+    a.table_cap = LP_LOGP_CAP;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(a.N) * static_cast<unsigned>(a.segs));
-    cfg.blockDim = dim3(LP_THREADS);
-    cfg.dynamicSmemBytes = touch ? table_bytes(a.table_columns) : 0;
+    cfg.blockDim = dim3(LP_LOGP_THREADS);
+    cfg.dynamicSmemBytes = static_cast<size_t>(slices) * 8 + (touch ? table_bytes<int32_t>(a.table_columns, a.table_cap) : 0);
     cfg.stream = s;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;

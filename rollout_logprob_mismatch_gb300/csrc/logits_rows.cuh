@@ -158,37 +158,52 @@ __device__ __forceinline__ void load8(Raw8<T> &r, const T *row, int col, int V, 
         Elem<T>::put(r.w, i, col + i < V ? Elem<T>::bits(row + col + i) : Elem<T>::NEG_INF);
 }
 
-// Stores the lane's eight values; the whole warp, col = its lane's column.
+// The lane's eight values, rounded to T and packed.
+template <typename T> __device__ __forceinline__ Raw8<T> pack8(const float *v)
+{
+    Raw8<T> r;
+#pragma unroll
+    for (int k = 0; k < Elem<T>::WORDS; ++k) {
+        if constexpr (sizeof(T) == 4)
+            r.w[k] = __float_as_uint(v[k]);
+        else
+            r.w[k] = pack2<T>(v[2 * k], v[2 * k + 1]);
+    }
+    return r;
+}
+
+// Element i of the lane's eight to its place.
+template <typename T> __device__ __forceinline__ void store1(T *row, int col, const Raw8<T> &r, int i)
+{
+    if constexpr (sizeof(T) == 4)
+        reinterpret_cast<uint32_t *>(row)[col + i] = r.w[i];
+    else
+        reinterpret_cast<uint16_t *>(row)[col + i] = static_cast<uint16_t>(r.w[i >> 1] >> ((i & 1) * 16));
+}
+
+// Stores the lane's eight; the whole warp, col = its lane's column.
 template <typename T>
-__device__ __forceinline__ void store8(T *row, int col, int V, uint32_t shift, const float *v)
+__device__ __forceinline__ void store8(T *row, int col, int V, uint32_t shift, const Raw8<T> &r)
 {
     constexpr int W = Elem<T>::WORDS;
     const int lane = threadIdx.x & 31;
     const bool whole = col - lane * 8 + 256 <= V;   // the same in every lane
     if (shift == 0 ? col + 8 <= V : whole) {
-        uint32_t w[W];
-#pragma unroll
-        for (int k = 0; k < W; ++k) {
-            if constexpr (sizeof(T) == 4)
-                w[k] = __float_as_uint(v[k]);
-            else
-                w[k] = pack2<T>(v[2 * k], v[2 * k + 1]);
-        }
         if (shift == 0) {
             uint4 *p = reinterpret_cast<uint4 *>(row + col);
 #pragma unroll
             for (int k = 0; k < W / 4; ++k)
-                p[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+                p[k] = make_uint4(r.w[4 * k], r.w[4 * k + 1], r.w[4 * k + 2], r.w[4 * k + 3]);
             return;
         }
         // the 16 bytes before this lane's columns are the lane before's last
         uint32_t q[W + 4], o[W];
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-            q[k] = __shfl_up_sync(0xffffffffu, w[W - 4 + k], 1);
+            q[k] = __shfl_up_sync(0xffffffffu, r.w[W - 4 + k], 1);
 #pragma unroll
         for (int k = 0; k < W; ++k)
-            q[4 + k] = w[k];
+            q[4 + k] = r.w[k];
         shift_words<W, sizeof(T) == 2>(o, q, 16 - shift);
         uint4 *p = reinterpret_cast<uint4 *>(reinterpret_cast<char *>(row + col) - shift);
         const int head = static_cast<int>((16 - shift) / sizeof(T));   // own elements in the first piece
@@ -200,21 +215,21 @@ __device__ __forceinline__ void store8(T *row, int col, int V, uint32_t shift, c
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 if (i < head)
-                    row[col + i] = Elem<T>::from(v[i]);
+                    store1(row, col, r, i);
         }
         if (lane == 31) {
             const int tail = static_cast<int>(shift / sizeof(T));
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 if (i >= 8 - tail)
-                    row[col + i] = Elem<T>::from(v[i]);
+                    store1(row, col, r, i);
         }
         return;
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i)
         if (col + i < V)
-            row[col + i] = Elem<T>::from(v[i]);
+            store1(row, col, r, i);
 }
 
 // N chunks of 256 columns from column b on, into N registers of eight a lane.  Away
@@ -243,21 +258,36 @@ __device__ __forceinline__ void load_chunks(Raw8<T> (&r)[N], const T *row, int b
         load8<T>(r[u], row, b + u * 256 + lane * 8, V, shift);
 }
 
-// Columns whose bit in `drop` is set become -inf.
-template <typename T> __device__ __forceinline__ void drop8(Raw8<T> &r, uint32_t drop)
+// For 16-bit types: the masks of two words whose halves' bits are set in a nibble
+// (128 bytes of shared memory; two 8-byte loads and a logic operation a word in
+// place of some 28 instructions per eight columns).
+struct HalfMasks {
+    uint2 of[16];
+    __device__ __forceinline__ void fill()   // a barrier before use
+    {
+        if (threadIdx.x < 16) {
+            const uint32_t b = threadIdx.x;
+            of[b] = make_uint2((b & 1 ? 0xffffu : 0u) | (b & 2 ? 0xffff0000u : 0u),
+                               (b & 4 ? 0xffffu : 0u) | (b & 8 ? 0xffff0000u : 0u));
+        }
+    }
+};
+
+// Columns whose bit in `drop` is set become `fill` (the bits of one element).
+template <typename T>
+__device__ __forceinline__ void drop8(Raw8<T> &r, uint32_t drop, const HalfMasks &masks, uint32_t fill = Elem<T>::NEG_INF)
 {
     if constexpr (sizeof(T) == 4) {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            r.w[i] = drop >> i & 1 ? Elem<T>::NEG_INF : r.w[i];
+            r.w[i] = drop >> i & 1 ? fill : r.w[i];
     } else {
-        constexpr uint32_t N = Elem<T>::NEG_INF;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const uint32_t two = drop >> (2 * k) & 3;
-            const uint32_t m = (two & 1 ? 0xffffu : 0u) | (two & 2 ? 0xffff0000u : 0u);
-            r.w[k] = (r.w[k] & ~m) | ((N | N << 16) & m);
-        }
+        const uint32_t two = fill | fill << 16;
+        const uint2 lo = masks.of[drop & 15], hi = masks.of[drop >> 4];
+        r.w[0] = (r.w[0] & ~lo.x) | (two & lo.x);
+        r.w[1] = (r.w[1] & ~lo.y) | (two & lo.y);
+        r.w[2] = (r.w[2] & ~hi.x) | (two & hi.x);
+        r.w[3] = (r.w[3] & ~hi.y) | (two & hi.y);
     }
 }
 
@@ -352,8 +382,9 @@ __device__ __forceinline__ void warp_sums(const Raw8<T> (&raw)[N], float k2, con
                                           float &S)
 {
     const int lane = threadIdx.x & 31;
-    float top = raw_max<T, N>(raw);
-    for (int i = lane; i < n; i += 32)
+    const float first = lane < n ? __uint_as_float(more[lane]) : neg_inf();
+    float top = fmaxf(raw_max<T, N>(raw), first);
+    for (int i = lane + 32; i < n; i += 32)
         top = fmaxf(top, __uint_as_float(more[i]));
     M = warp_max(top);
     const float ref = finite_ref(M);
@@ -370,7 +401,9 @@ __device__ __forceinline__ void warp_sums(const Raw8<T> (&raw)[N], float k2, con
     float lo, hi;
     unpair(add2(acc[0], acc[1]), lo, hi);
     lo += hi;
-    for (int i = lane; i < n; i += 32)
+    if (n > 0)
+        lo += exp2_approx(__fmul_rn(first - ref, k2));
+    for (int i = lane + 32; i < n; i += 32)
         lo += exp2_approx(__fmul_rn(__uint_as_float(more[i]) - ref, k2));
     S = warp_sum(lo);
 }
