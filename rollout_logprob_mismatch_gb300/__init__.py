@@ -388,6 +388,43 @@ def _need_out(t, name, dtype, shape, device):
         raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
 
 
+_modules = None
+
+
+def _torch():
+    """(torch, torch.Tensor, the raw handle of a device's current stream): looked up
+    once; a decoding step pays for every look-up of its calls."""
+    global _modules
+    if _modules is None:
+        import torch
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is None:
+            def raw(index):
+                return torch.cuda.current_stream(index).cuda_stream
+        _modules = (torch, torch.Tensor, raw)
+    return _modules
+
+
+def _need_array(t, name, dtype, shape, device):
+    """_need_out with its whole check in one condition where it holds."""
+    if not (t.__class__ is _torch()[1] and t.dtype is dtype and t.shape == shape and t.device == device
+            and t.is_contiguous()):
+        _need_out(t, name, dtype, shape, device)
+    return t.data_ptr()
+
+
+def _launch(function, device, stream, *args):
+    """Calls a C entry point on `device` and `stream` (None: the current one)."""
+    torch, _, raw = _torch()
+    if torch.cuda.current_device() == device.index:
+        rc = function(*args, raw(device.index) if stream is None else stream.cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            rc = function(*args, raw(device.index) if stream is None else stream.cuda_stream)
+    if rc != TIM_OK:
+        _raise_if(rc)
+
+
 def token_logprob(h, W, targets, out_logp=None, out_lse=None, stream=None, temperature: float = 1.0):
     """(logp [N] fp32, lse [N] fp32) for bf16 h [N, D], bf16 W [V, D], int32 targets [N]:
     log softmax(h W^T / temperature) at the targets (temperature 1: raw logits)."""
@@ -677,83 +714,93 @@ class LogitsRules:
 
     def struct(self, N: int, V: int, device):
         """The C struct, after checking every tensor against N rows of V logits."""
-        import torch
+        torch = _torch()[0]
+        f32, i32, rows = torch.float32, torch.int32, (N,)
         r = tim_logits_rules()
-        for name in ("temperature", "repetition", "presence", "frequency"):
-            t = getattr(self, name)
-            if t is not None:
-                _need_out(t, name, torch.float32, (N,), device)
-                setattr(r, name, t.data_ptr())
+        if self.temperature is not None:
+            r.temperature = _need_array(self.temperature, "temperature", f32, rows, device)
+        if self.repetition is not None:
+            r.repetition = _need_array(self.repetition, "repetition", f32, rows, device)
+        if self.presence is not None:
+            r.presence = _need_array(self.presence, "presence", f32, rows, device)
+        if self.frequency is not None:
+            r.frequency = _need_array(self.frequency, "frequency", f32, rows, device)
         if (self.history is None) != (self.history_spans is None):
             raise ValueError("history and history_spans go together")
         if self.history is not None:
-            _need(self.history, "history", torch.int32, 1, device)
-            _need_out(self.history_spans, "history_spans", torch.int32, (N, 3), device)
-            r.history, r.num_history = self.history.data_ptr(), _int32_size(self.history, "history")
-            r.history_spans = self.history_spans.data_ptr()
-        bias = (self.bias_offsets, self.bias_ids, self.bias_values)
-        if any(t is None for t in bias) != all(t is None for t in bias):
-            raise ValueError("bias_offsets, bias_ids and bias_values go together")
-        if self.bias_ids is not None:
-            _need_out(self.bias_offsets, "bias_offsets", torch.int32, (N + 1,), device)
-            _need(self.bias_ids, "bias_ids", torch.int32, 1, device)
-            _need_out(self.bias_values, "bias_values", torch.float32, (self.bias_ids.shape[0],), device)
-            r.bias_offsets, r.bias_ids = self.bias_offsets.data_ptr(), self.bias_ids.data_ptr()
-            r.bias_values, r.num_bias = self.bias_values.data_ptr(), _int32_size(self.bias_ids, "bias_ids")
+            r.num_history = _list_size(self.history, "history")
+            r.history = _need_array(self.history, "history", i32, (r.num_history,), device)
+            r.history_spans = _need_array(self.history_spans, "history_spans", i32, (N, 3), device)
+        if self.bias_offsets is not None or self.bias_ids is not None or self.bias_values is not None:
+            if self.bias_offsets is None or self.bias_ids is None or self.bias_values is None:
+                raise ValueError("bias_offsets, bias_ids and bias_values go together")
+            r.num_bias = _list_size(self.bias_ids, "bias_ids")
+            r.bias_offsets = _need_array(self.bias_offsets, "bias_offsets", i32, (N + 1,), device)
+            r.bias_ids = _need_array(self.bias_ids, "bias_ids", i32, (r.num_bias,), device)
+            r.bias_values = _need_array(self.bias_values, "bias_values", f32, (r.num_bias,), device)
         if self.allowed is not None:
-            _need(self.allowed, "allowed", (torch.int32, torch.uint32), 2, device)
-            if self.allowed.shape[1] < (V + 31) // 32:
+            _need(self.allowed, "allowed", (i32, torch.uint32), 2, device)
+            R, words = self.allowed.shape
+            if words < (V + 31) // 32:
                 raise ValueError("allowed must have at least %d words a row" % ((V + 31) // 32))
-            r.allowed, r.allowed_stride = self.allowed.data_ptr(), self.allowed.shape[1]
-            r.num_allowed = min(self.allowed.shape[0], 2 ** 31 - 1)
+            r.allowed, r.allowed_stride, r.num_allowed = self.allowed.data_ptr(), words, min(R, 2 ** 31 - 1)
             if self.allowed_rows is not None:
-                _need_out(self.allowed_rows, "allowed_rows", torch.int32, (N,), device)
-                r.allowed_rows = self.allowed_rows.data_ptr()
-            elif self.allowed.shape[0] < N:
+                r.allowed_rows = _need_array(self.allowed_rows, "allowed_rows", i32, rows, device)
+            elif R < N:
                 raise ValueError("allowed has fewer rows than the logits: give allowed_rows")
         elif self.allowed_rows is not None:
             raise ValueError("allowed_rows without allowed")
         return r
 
 
-def _int32_size(t, name):
+def _list_size(t, name):
+    if not isinstance(t, _torch()[1]):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if t.dim() != 1:
+        raise ValueError("%s must be 1-D" % name)
     if t.shape[0] >= 2 ** 30:
         raise ValueError("%s must have fewer than 2^30 entries" % name)
     return t.shape[0]
 
 
+_dtype_codes = {}
+
+
 def _dtype_code(dtype):
-    import torch
-    return {torch.float32: TIM_F32, torch.bfloat16: TIM_BF16, torch.float16: TIM_F16}[dtype]
+    if not _dtype_codes:
+        torch = _torch()[0]
+        _dtype_codes.update({torch.float32: TIM_F32, torch.bfloat16: TIM_BF16, torch.float16: TIM_F16})
+    return _dtype_codes.get(dtype)
 
 
 def _need_logits(t, name, dtype=None, device=None, shape=None):
     """Rows of logits: 2-D, a row's elements adjacent, rows any stride >= V apart.
-    Returns the stride."""
-    import torch
-    if not isinstance(t, torch.Tensor):
+    Returns (address, type code, N, V, stride)."""
+    if not isinstance(t, _torch()[1]):
         raise TypeError("%s must be a torch.Tensor" % name)
     if not t.is_cuda:
         raise ValueError("%s must be a CUDA tensor" % name)
-    allowed = (torch.float32, torch.bfloat16, torch.float16) if dtype is None else (dtype,)
-    if t.dtype not in allowed:
-        raise TypeError("%s must have dtype %s, got %s" % (name, " or ".join(map(str, allowed)), t.dtype))
+    code = _dtype_code(t.dtype)
+    if code is None or (dtype is not None and t.dtype is not dtype):
+        raise TypeError("%s must have dtype %s, got %s"
+                        % (name, "float32, bfloat16 or float16" if dtype is None else dtype, t.dtype))
     if t.dim() != 2:
         raise ValueError("%s must be 2-D" % name)
     N, V = t.shape
-    if shape is not None and (N, V) != tuple(shape):
-        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), (N, V)))
+    if shape is not None and (N, V) != shape:
+        raise ValueError("%s must have shape %s, got %s" % (name, shape, (N, V)))
     if V < 1:
         raise ValueError("%s must have at least one column" % name)
-    if V > 1 and t.stride(1) != 1:
+    stride, step = t.stride()
+    if V > 1 and step != 1:
         raise ValueError("a row of %s must be contiguous" % name)
     if device is not None and t.device != device:
         raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
     if N <= 1:
-        return V
-    if t.stride(0) < V:
+        stride = V
+    elif stride < V:
         raise ValueError("the rows of %s must not overlap" % name)
-    return t.stride(0)
+    return t.data_ptr(), code, N, V, stride
 
 
 def _rules_struct(rules, N, V, dev):
@@ -778,44 +825,34 @@ def process_logits(logits, rules, out=None, out_dtype=None, stream=None):
     """The processed logits [N, V] (y in include/tim.h) of fp32, bf16 or fp16
     logits under `rules` (a LogitsRules or None), in the logits' type or fp32.
     out may be the logits themselves."""
-    import torch
-    stride = _need_logits(logits, "logits")
-    dev = logits.device
-    N, V = logits.shape
+    head = _need_logits(logits, "logits")
+    dev, N, V = logits.device, head[2], head[3]
+    torch = _torch()[0]
     if out is None:
         out = torch.empty((N, V), dtype=out_dtype or logits.dtype, device=dev)
-    if out_dtype is not None and out.dtype != out_dtype:
+    elif out_dtype is not None and out.dtype != out_dtype:
         raise TypeError("out must have dtype %s, got %s" % (out_dtype, out.dtype))
-    if out.dtype not in (logits.dtype, torch.float32):
+    address, code, _, _, stride = _need_logits(out, "out", None, dev, (N, V))
+    if code != head[1] and code != TIM_F32:
         raise TypeError("out must have the logits' dtype or float32, got %s" % out.dtype)
-    out_stride = _need_logits(out, "out", out.dtype, dev, (N, V))
-    r = _rules_struct(rules, N, V, dev)
-    with torch.cuda.device(dev):
-        rc = tim_process_logits(logits.data_ptr(), _dtype_code(logits.dtype), N, V, stride, r, out.data_ptr(),
-                                _dtype_code(out.dtype), out_stride, _stream_handle(stream, dev))
-    _raise_if(rc)
+    _launch(tim_process_logits, dev, stream, *head, _rules_struct(rules, N, V, dev), address, code, stride)
     return out
 
 
 def processed_logprob(logits, rules, targets, out_logp=None, out_lse=None, stream=None):
     """(logp [N] fp32, lse [N] fp32) of the int32 targets [N] under the processed
     logits, which are not written."""
-    import torch
-    stride = _need_logits(logits, "logits")
-    dev = logits.device
-    N, V = logits.shape
-    _need_out(targets, "targets", torch.int32, (N,), dev)
+    head = _need_logits(logits, "logits")
+    dev, N, V = logits.device, head[2], head[3]
+    torch = _torch()[0]
+    f32 = torch.float32
+    t = _need_array(targets, "targets", torch.int32, (N,), dev)
     if out_logp is None:
-        out_logp = torch.empty(N, dtype=torch.float32, device=dev)
+        out_logp = torch.empty(N, dtype=f32, device=dev)
     if out_lse is None:
-        out_lse = torch.empty(N, dtype=torch.float32, device=dev)
-    _need_out(out_logp, "out_logp", torch.float32, (N,), dev)
-    _need_out(out_lse, "out_lse", torch.float32, (N,), dev)
-    r = _rules_struct(rules, N, V, dev)
-    with torch.cuda.device(dev):
-        rc = tim_processed_logprob(logits.data_ptr(), _dtype_code(logits.dtype), N, V, stride, r, targets.data_ptr(),
-                                   out_logp.data_ptr(), out_lse.data_ptr(), _stream_handle(stream, dev))
-    _raise_if(rc)
+        out_lse = torch.empty(N, dtype=f32, device=dev)
+    _launch(tim_processed_logprob, dev, stream, *head, _rules_struct(rules, N, V, dev), t,
+            _need_array(out_logp, "out_logp", f32, (N,), dev), _need_array(out_lse, "out_lse", f32, (N,), dev))
     return out_logp, out_lse
 
 
@@ -823,52 +860,49 @@ def processed_logprob_backward(logits, rules, targets, grad_logp, lse, dlogits=N
     """The gradient [N, V], in the logits' type, of sum_i grad_logp_i logp_i with
     respect to the raw logits, from the forward's lse.  dlogits may be the
     logits themselves."""
-    import torch
-    stride = _need_logits(logits, "logits")
-    dev = logits.device
-    N, V = logits.shape
-    _need_out(targets, "targets", torch.int32, (N,), dev)
-    _need_out(grad_logp, "grad_logp", torch.float32, (N,), dev)
-    _need_out(lse, "lse", torch.float32, (N,), dev)
+    head = _need_logits(logits, "logits")
+    dev, N, V = logits.device, head[2], head[3]
+    torch = _torch()[0]
+    f32 = torch.float32
+    t = _need_array(targets, "targets", torch.int32, (N,), dev)
+    g = _need_array(grad_logp, "grad_logp", f32, (N,), dev)
+    lse_ptr = _need_array(lse, "lse", f32, (N,), dev)
     if dlogits is None:
         dlogits = torch.empty((N, V), dtype=logits.dtype, device=dev)
-    dstride = _need_logits(dlogits, "dlogits", logits.dtype, dev, (N, V))
-    r = _rules_struct(rules, N, V, dev)
-    with torch.cuda.device(dev):
-        rc = tim_processed_logprob_backward(logits.data_ptr(), _dtype_code(logits.dtype), N, V, stride, r,
-                                            targets.data_ptr(), grad_logp.data_ptr(), lse.data_ptr(),
-                                            dlogits.data_ptr(), dstride, _stream_handle(stream, dev))
-    _raise_if(rc)
+    out = _need_logits(dlogits, "dlogits", logits.dtype, dev, (N, V))
+    _launch(tim_processed_logprob_backward, dev, stream, *head, _rules_struct(rules, N, V, dev), t, g, lse_ptr,
+            out[0], out[4])
     return dlogits
 
 
-def _distill_inputs(logits, teacher_ids, teacher_logits, teacher_lse):
-    import torch
-    stride = _need_logits(logits, "logits")
-    dev = logits.device
-    N, V = logits.shape
+def _distill_inputs(logits, teacher_ids, teacher_logits, teacher_lse, temperature):
+    """(C arguments up to the temperature, N, V, device)."""
+    torch = _torch()[0]
+    head = _need_logits(logits, "logits")
+    dev, N, V = logits.device, head[2], head[3]
     _need(teacher_ids, "teacher_ids", torch.int32, 2, dev)
     K = teacher_ids.shape[1]
     if teacher_ids.shape[0] != N or not 1 <= K <= DISTILL_MAX_K:
         raise ValueError("teacher_ids must be [%d, 1 .. %d], got %s" % (N, DISTILL_MAX_K, tuple(teacher_ids.shape)))
-    _need_out(teacher_logits, "teacher_logits", torch.float32, (N, K), dev)
-    if teacher_lse is not None:
-        _need_out(teacher_lse, "teacher_lse", torch.float32, (N,), dev)
-    args = (logits.data_ptr(), _dtype_code(logits.dtype), N, V, stride, teacher_ids.data_ptr(),
-            teacher_logits.data_ptr(), None if teacher_lse is None else teacher_lse.data_ptr(), K)
-    return args, N, V, dev
+    t = _need_array(teacher_logits, "teacher_logits", torch.float32, (N, K), dev)
+    lse = None if teacher_lse is None else _need_array(teacher_lse, "teacher_lse", torch.float32, (N,), dev)
+    return (*head, teacher_ids.data_ptr(), t, lse, K, float(temperature)), N, V, dev
 
 
 def _distill_rows(out, N, tail, dev):
-    import torch
+    """(dict of the row outputs, their addresses)."""
+    torch = _torch()[0]
     out = {} if out is None else dict(out)
-    for name in ("loss", "lse") + (("lse_tail",) if tail else ()):
+    ptrs = []
+    for name in ("loss", "lse", "lse_tail"):
+        if name == "lse_tail" and not tail:
+            out[name] = None
+            ptrs.append(None)
+            continue
         if out.get(name) is None:
             out[name] = torch.empty(N, dtype=torch.float32, device=dev)
-        _need_out(out[name], name, torch.float32, (N,), dev)
-    if not tail:
-        out["lse_tail"] = None
-    return out, out["lse_tail"].data_ptr() if tail else None
+        ptrs.append(_need_array(out[name], name, torch.float32, (N,), dev))
+    return out, ptrs
 
 
 def distill_topk(logits, teacher_ids, teacher_logits, teacher_lse=None, temperature: float = 1.0, out=None,
@@ -878,13 +912,9 @@ def distill_topk(logits, teacher_ids, teacher_logits, teacher_lse=None, temperat
     teacher_logits fp32 [N, K], and teacher_lse fp32 [N] where the teacher's mass
     outside its list is one more outcome.  Returns a dict: loss, lse fp32 [N] and
     lse_tail (fp32 [N] with teacher_lse, else None)."""
-    import torch
-    args, N, _, dev = _distill_inputs(logits, teacher_ids, teacher_logits, teacher_lse)
-    out, tail = _distill_rows(out, N, teacher_lse is not None, dev)
-    with torch.cuda.device(dev):
-        rc = tim_distill_topk(*args, float(temperature), out["loss"].data_ptr(), out["lse"].data_ptr(), tail,
-                              _stream_handle(stream, dev))
-    _raise_if(rc)
+    args, N, _, dev = _distill_inputs(logits, teacher_ids, teacher_logits, teacher_lse, temperature)
+    out, rows = _distill_rows(out, N, teacher_lse is not None, dev)
+    _launch(tim_distill_topk, dev, stream, *args, *rows)
     return out
 
 
@@ -893,22 +923,18 @@ def distill_topk_backward(logits, teacher_ids, teacher_logits, grad_loss, lse, l
     """The gradient [N, V], in the logits' type, of sum_i grad_loss_i loss_i, from
     the forward's lse and (with teacher_lse) lse_tail.  dlogits may be the logits
     themselves."""
-    import torch
-    args, N, V, dev = _distill_inputs(logits, teacher_ids, teacher_logits, teacher_lse)
-    _need_out(grad_loss, "grad_loss", torch.float32, (N,), dev)
-    _need_out(lse, "lse", torch.float32, (N,), dev)
+    torch = _torch()[0]
+    f32 = torch.float32
+    args, N, V, dev = _distill_inputs(logits, teacher_ids, teacher_logits, teacher_lse, temperature)
+    g = _need_array(grad_loss, "grad_loss", f32, (N,), dev)
+    lse_ptr = _need_array(lse, "lse", f32, (N,), dev)
     if (lse_tail is None) != (teacher_lse is None):
         raise ValueError("lse_tail and teacher_lse go together")
-    if lse_tail is not None:
-        _need_out(lse_tail, "lse_tail", torch.float32, (N,), dev)
+    tail = None if lse_tail is None else _need_array(lse_tail, "lse_tail", f32, (N,), dev)
     if dlogits is None:
         dlogits = torch.empty((N, V), dtype=logits.dtype, device=dev)
-    dstride = _need_logits(dlogits, "dlogits", logits.dtype, dev, (N, V))
-    with torch.cuda.device(dev):
-        rc = tim_distill_topk_backward(*args, float(temperature), grad_loss.data_ptr(), lse.data_ptr(),
-                                       None if lse_tail is None else lse_tail.data_ptr(), dlogits.data_ptr(), dstride,
-                                       _stream_handle(stream, dev))
-    _raise_if(rc)
+    out = _need_logits(dlogits, "dlogits", logits.dtype, dev, (N, V))
+    _launch(tim_distill_topk_backward, dev, stream, *args, g, lse_ptr, tail, out[0], out[4])
     return dlogits
 
 
@@ -917,19 +943,15 @@ def distill_topk_step(logits, teacher_ids, teacher_logits, grad_loss, teacher_ls
     """distill_topk and its gradient in one call, for weights grad_loss fp32 [N]
     known beforehand: the dict of distill_topk with dlogits [N, V] added (which
     may be the logits themselves)."""
-    import torch
-    args, N, V, dev = _distill_inputs(logits, teacher_ids, teacher_logits, teacher_lse)
-    _need_out(grad_loss, "grad_loss", torch.float32, (N,), dev)
-    out, tail = _distill_rows(out, N, teacher_lse is not None, dev)
+    torch = _torch()[0]
+    args, N, V, dev = _distill_inputs(logits, teacher_ids, teacher_logits, teacher_lse, temperature)
+    g = _need_array(grad_loss, "grad_loss", torch.float32, (N,), dev)
+    out, rows = _distill_rows(out, N, teacher_lse is not None, dev)
     if dlogits is None:
         dlogits = torch.empty((N, V), dtype=logits.dtype, device=dev)
-    dstride = _need_logits(dlogits, "dlogits", logits.dtype, dev, (N, V))
+    d = _need_logits(dlogits, "dlogits", logits.dtype, dev, (N, V))
     out["dlogits"] = dlogits
-    with torch.cuda.device(dev):
-        rc = tim_distill_topk_step(*args, float(temperature), grad_loss.data_ptr(), out["loss"].data_ptr(),
-                                   out["lse"].data_ptr(), tail, dlogits.data_ptr(), dstride,
-                                   _stream_handle(stream, dev))
-    _raise_if(rc)
+    _launch(tim_distill_topk_step, dev, stream, *args, g, *rows, d[0], d[4])
     return out
 
 

@@ -40,8 +40,8 @@ struct TeacherRow {
 // listed ids, the bitmap of the rank's columns, the table drop8 takes (16-bit types
 // with a tail), the rank's part of the row.
 struct Head {
-    uint64_t bar;
-    int dup, abort;
+    uint64_t bar, parts;   // the row's copy; the partials and the teacher's statistics
+    int dup, abort, pad[2];
     TeacherRow teacher;
     float m, s, mr, sr;   // all columns; those that are not listed
 };
@@ -81,8 +81,10 @@ __device__ __forceinline__ float q_of(float logq) { return logq == neg_inf() ? 0
 
 __device__ __forceinline__ bool in_use(int id, int V) { return id >= 0 && id < V; }
 
-// One warp; the same in every lane.
-template <bool TAIL> __device__ __forceinline__ TeacherRow teacher_row(const DistillArgs &a, int row, int lane)
+// One warp; the same in every lane.  Also the student's logits at the listed ids,
+// for the loss (listed_x, where it is given).
+template <typename T, bool TAIL>
+__device__ __forceinline__ TeacherRow teacher_row(const DistillArgs &a, int row, int lane, const T *z, float *listed_x)
 {
     const int32_t *ids = a.ids + static_cast<int64_t>(row) * a.K;
     const float *t = a.teacher + static_cast<int64_t>(row) * a.K;
@@ -93,6 +95,8 @@ template <bool TAIL> __device__ __forceinline__ TeacherRow teacher_row(const Dis
         if (in_use(ids[k], a.V)) {
             any = true;
             top = fmaxf(top, t[k]);
+            if (listed_x)
+                listed_x[k] = Elem<T>::load(z + ids[k]);
         }
     w.any = __any_sync(0xffffffffu, any);
     float s = 0.f;
@@ -156,7 +160,7 @@ __global__ void __launch_bounds__(LD_THREADS) distill_kernel(const DistillArgs a
     float *listed_x = reinterpret_cast<float *>(smem + lay.x);
     uint32_t *bitmap = reinterpret_cast<uint32_t *>(smem + lay.bits);   // columns of this rank
     HalfMasks &masks = *reinterpret_cast<HalfMasks *>(smem + lay.masks);
-    const int rank = static_cast<int>(cluster_ctarank());
+    const int rank = static_cast<int>(blockIdx.x % static_cast<unsigned>(a.ranks));
     const int row = static_cast<int>(blockIdx.x / static_cast<unsigned>(a.ranks));
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int s0 = min(slices, rank * a.per), s1 = min(slices, s0 + a.per);
@@ -170,22 +174,25 @@ __global__ void __launch_bounds__(LD_THREADS) distill_kernel(const DistillArgs a
     float g = 0.f;
     if constexpr (GRAD)
         g = a.grad[row];
+    const int takers = GRAD ? a.ranks : 1;   // ranks that fold the row's partials
     // the columns as the passes read them: from memory, or from this CTA's copy
     const T *src = HOLD ? reinterpret_cast<const T *>(smem + lay.row + shift) : z;
     const int off = HOLD ? c0 : 0;
     if (threadIdx.x == 0) {
         hd.dup = 0;
-        if constexpr (HOLD) {
+        hd.abort = 0;
+        if constexpr (SUMS) {
             mbar_init(smem_u32(&hd.bar), 1);
-            hd.abort = 0;
+            mbar_init(smem_u32(&hd.parts), 1);
             fence_mbar_init();
-            fence_proxy_async_smem();
+            if (a.ranks > 1 && rank < takers)
+                mbar_arrive_expect_tx(smem_u32(&hd.parts), static_cast<uint32_t>(slices) * 16 + 16);
         }
     }
     if constexpr (HOLD)
         fetch_row<T>(z, c0, c1, shift, smem + lay.row, smem_u32(&hd.bar));
     if (SUMS && a.ranks > 1)
-        cluster_arrive();   // waited for before the first store into another CTA's shared memory
+        cluster_arrive_relaxed();   // waited for before the first store into another CTA's shared memory
 
     auto zero_row = [&] {
         const float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
@@ -199,37 +206,58 @@ __global__ void __launch_bounds__(LD_THREADS) distill_kernel(const DistillArgs a
         }
     }
 
-    // the listed ids: this rank's in the bitmap, for the loss the logits of all
+    // the thread's first listed id and its teacher's logit, ahead of their use
+    const int id0 = static_cast<int>(threadIdx.x) < a.K ? ids[threadIdx.x] : -1;
+    const float t0 = static_cast<int>(threadIdx.x) < a.K ? teacher[threadIdx.x] : 0.f;
+    auto mark = [&] {   // this rank's listed ids in the bitmap
+        for (int k = threadIdx.x; k < a.K; k += LD_THREADS) {
+            const int id = k < LD_THREADS ? id0 : ids[k];
+            if (id >= c0 && id < c1) {
+                const uint32_t bit = 1u << ((id - c0) & 31);
+                if (atomicOr(bitmap + ((id - c0) >> 5), bit) & bit)
+                    hd.dup = 1;
+            }
+        }
+    };
     if constexpr (BITS) {
         for (int j = threadIdx.x; j < (c1 - c0 + 31) / 32; j += LD_THREADS)
             bitmap[j] = 0;
+    }
+    if constexpr (TAIL || !SUMS) {
         if constexpr (SUMS && TAIL && sizeof(T) == 2)
             masks.fill();
         __syncthreads();
+        mark();
+        __syncthreads();
     }
-    for (int k = threadIdx.x; k < a.K; k += LD_THREADS) {
-        const int id = ids[k];
-        if (SUMS && rank == 0)
-            listed_x[k] = in_use(id, a.V) ? Elem<T>::load(z + id) : 0.f;
-        if (BITS && id >= c0 && id < c1) {
-            const uint32_t bit = 1u << ((id - c0) & 31);
-            if (atomicOr(bitmap + ((id - c0) >> 5), bit) & bit)
-                hd.dup = 1;
-        }
-    }
-    // the teacher's statistics: by the last warp (it has the fewest slices), while the
-    // others wait for the row; in a call with sums by rank 0, which hands them out
+    // The teacher's statistics: by the last warp (it has the fewest slices), while the
+    // others wait for the row; in a call with sums by rank 0, which hands them out.
+    // No rank writes a gradient before it has them, so the gathers of z are over by then.
+    TeacherRow tr{0.f, 0.f, 0.f, 0};
     if (warp == LD_WARPS - 1 && (rank == 0 || !SUMS)) {
-        const TeacherRow tr = teacher_row<TAIL>(a, row, lane);
-        if (lane == 0)
+        tr = teacher_row<T, TAIL>(a, row, lane, z, SUMS ? listed_x : nullptr);
+        if (lane == 0 && (!SUMS || a.ranks == 1))
             hd.teacher = tr;
     }
-    if (TAIL || !SUMS)
+    if constexpr (!SUMS)
         __syncthreads();
 
     if constexpr (SUMS) {
         // The sums: of the columns that are not listed (all of them without a tail)
-        // and of the listed ones, slice by slice.
+        // and of the listed ones, slice by slice.  Each partial goes to every CTA that
+        // folds the row as it comes up: a store that counts its bytes on the other
+        // CTA's barrier, so no CTA waits for another's stores.
+        uint32_t peer = 0;   // shared memory of rank `lane`
+        if (a.ranks > 1) {
+            cluster_wait();   // every CTA's barriers exist
+            if (lane < takers)
+                peer = mapa_shared(smem_u32(smem), static_cast<uint32_t>(lane));
+            if (warp == LD_WARPS - 1 && rank == 0 && lane < takers)
+                st_async_f4(peer + static_cast<uint32_t>(offsetof(Head, teacher)), tr.max, tr.lse, tr.rest,
+                            __int_as_float(tr.any), peer + static_cast<uint32_t>(offsetof(Head, parts)));
+        } else {
+            __syncthreads();
+        }
         bool late = false;
         if constexpr (HOLD) {
             late = !mbar_wait_sleep(smem_u32(&hd.bar), 0, &hd.abort, a.wait_budget_ns);
@@ -260,33 +288,30 @@ __global__ void __launch_bounds__(LD_THREADS) distill_kernel(const DistillArgs a
                     warp_join(km, ks, k2);
             }
             warp_sums<T, 4>(raw, k2, nullptr, 0, lm, ls);
-            if (lane == 0)
-                part[sl] = make_float4(lm, late ? quiet_nan() : ls, km, ks);
-        }
-        __syncthreads();
-        if (a.ranks > 1) {
-            cluster_wait();
-            for (int d = 0; d < (GRAD ? a.ranks : 1); ++d) {
-                if (d == rank)
-                    continue;
-                const uint32_t to = mapa_shared(smem_u32(smem), static_cast<uint32_t>(d));
-                for (int j = s0 + static_cast<int>(threadIdx.x); j < s1; j += LD_THREADS) {
-                    const uint32_t at = to + lay.part + static_cast<uint32_t>(j) * 16;
-                    st_cluster_f2(at, part[j].x, part[j].y);
-                    st_cluster_f2(at + 8, part[j].z, part[j].w);
-                }
-                if (rank == 0 && threadIdx.x == 0) {
-                    const uint32_t at = to + static_cast<uint32_t>(offsetof(Head, teacher));
-                    st_cluster_f2(at, hd.teacher.max, hd.teacher.lse);
-                    st_cluster_f2(at + 8, hd.teacher.rest, __int_as_float(hd.teacher.any));
-                }
+            if (late)
+                ls = quiet_nan();
+            if (a.ranks == 1) {
+                if (lane == 0)
+                    part[sl] = make_float4(lm, ls, km, ks);
+            } else if (lane < takers) {
+                st_async_f4(peer + lay.part + static_cast<uint32_t>(sl) * 16, lm, ls, km, ks,
+                            peer + static_cast<uint32_t>(offsetof(Head, parts)));
             }
-            __syncwarp();
-            cluster_arrive();
-            cluster_wait();
         }
+        if (a.ranks == 1 || (GRAD && !TAIL))
+            __syncthreads();
         if (!GRAD && (rank != 0 || warp != 0))
             return;
+        if constexpr (GRAD && !TAIL)
+            mark();   // (while the other CTAs' partials come in)
+        bool lost = false;
+        if (a.ranks > 1 && warp == 0) {
+            lost = !mbar_wait_cluster(smem_u32(&hd.parts), 0, &hd.abort, a.wait_budget_ns);
+            if (lost) {
+                atomicCAS(a.status, 0, static_cast<int>(TIM_ERR_TIMEOUT));
+                drain_wait(smem_u32(&hd.parts), 0);
+            }
+        }
         if (warp == 0) {   // fold in slice order: lane l takes slices l, l + 32, ...
             float mr = neg_inf(), sr = 0.f, km = neg_inf(), ks = 0.f;
             for (int j = lane; j < slices; j += 32) {
@@ -303,7 +328,7 @@ __global__ void __launch_bounds__(LD_THREADS) distill_kernel(const DistillArgs a
             }
             if (lane == 0) {
                 hd.m = m;
-                hd.s = s;
+                hd.s = lost ? quiet_nan() : s;
                 hd.mr = mr;
                 hd.sr = sr;
             }
@@ -374,15 +399,18 @@ __global__ void __launch_bounds__(LD_THREADS) distill_kernel(const DistillArgs a
         for (int n = 0; n < KPT; ++n) {
             const int k = static_cast<int>(threadIdx.x) + n * LD_THREADS;
             own[n] = 0.f;
-            if (k < a.K && ids[k] >= c0 && ids[k] < c1) {
+            if (n * LD_THREADS >= a.K)
+                continue;
+            const int id = k >= a.K ? -1 : n == 0 ? id0 : ids[k];
+            if (id >= c0 && id < c1) {
                 float q = 0.f;
                 if (hd.dup) {   // ids listed more than once add up, in the list's order
                     for (int j = 0; j < a.K; ++j)
-                        q += ids[j] == ids[k] ? q_of(listed_logq<TAIL>(teacher[j], tau, w)) : 0.f;
+                        q += ids[j] == id ? q_of(listed_logq<TAIL>(teacher[j], tau, w)) : 0.f;
                 } else {
-                    q = q_of(listed_logq<TAIL>(teacher[k], tau, w));
+                    q = q_of(listed_logq<TAIL>(n == 0 ? t0 : teacher[k], tau, w));
                 }
-                const float p = exp2_approx(fmaf(Elem<T>::load(src + ids[k] - off), first, -ref) * second) * scale;
+                const float p = exp2_approx(fmaf(Elem<T>::load(src + id - off), first, -ref) * second) * scale;
                 own[n] = (p - q) * gi;
             }
         }
@@ -410,8 +438,11 @@ __global__ void __launch_bounds__(LD_THREADS) distill_kernel(const DistillArgs a
 #pragma unroll
         for (int n = 0; n < KPT; ++n) {
             const int k = static_cast<int>(threadIdx.x) + n * LD_THREADS;
-            if (k < a.K && ids[k] >= c0 && ids[k] < c1)
-                dz[ids[k]] = Elem<T>::from(own[n]);
+            if (n * LD_THREADS >= a.K)
+                break;
+            const int id = k >= a.K ? -1 : n == 0 ? id0 : ids[k];
+            if (id >= c0 && id < c1)
+                dz[id] = Elem<T>::from(own[n]);
         }
         if (SUMS && rank == 0 && warp == LD_WARPS - 1)
             write_loss();
@@ -431,7 +462,7 @@ cudaError_t launch_kernel(const DistillArgs &a, const Layout &l, cudaStream_t s)
     at[0].val.clusterDim.x = static_cast<unsigned>(a.ranks);
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = OP != LD_BACKWARD && a.ranks > 1 ? 1 : 0;   // (the backward's CTAs do not meet)
     return cudaLaunchKernelEx(&cfg, distill_kernel<T, OP, TAIL, HOLD>, a);
 }
 

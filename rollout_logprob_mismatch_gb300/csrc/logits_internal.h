@@ -61,7 +61,7 @@ struct ProcArgs {
 cudaError_t logits_process_launch(ProcArgs a, int op, int dtype, int out_dtype, int num_sms, cudaStream_t s);
 
 // ---------------------------------------------------------------- distillation
-constexpr int LD_THREADS = 320;
+constexpr int LD_THREADS = 256;
 constexpr int LD_WARPS = LD_THREADS / 32;
 constexpr int LD_MAX_K = 1024;
 constexpr int LD_SMEM = 224 * 1024;                // shared memory a CTA may take

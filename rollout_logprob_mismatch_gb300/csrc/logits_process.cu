@@ -438,7 +438,7 @@ __global__ void __launch_bounds__(LP_LOGP_THREADS, LP_LOGP_CTAS) process_logp_ke
     __shared__ RowRules r;
     __shared__ HalfMasks masks;
     __shared__ float target_x;
-    const int rank = static_cast<int>(cluster_ctarank());
+    const int rank = static_cast<int>(blockIdx.x % static_cast<unsigned>(a.segs));
     const int row = static_cast<int>(blockIdx.x / static_cast<unsigned>(a.segs));
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int slices = (a.V + LG_SLICE - 1) / LG_SLICE;
@@ -449,7 +449,7 @@ __global__ void __launch_bounds__(LP_LOGP_THREADS, LP_LOGP_CTAS) process_logp_ke
     const T *z = static_cast<const T *>(a.z) + row * a.ld;
     const uint32_t shift = row_shift(z);
     if (a.segs > 1)
-        cluster_arrive();   // waited for before the first store into rank 0's shared memory
+        cluster_arrive_relaxed();   // waited for before the first store into rank 0's shared memory
     if (warp == 0)
         read_rules(a, row, r);
     if (sizeof(T) == 2 && (TOUCH || a.allowed))
@@ -594,7 +594,7 @@ template <typename T> cudaError_t launch_logp(ProcArgs a, int num_sms, cudaStrea
     at[0].val.clusterDim.x = static_cast<unsigned>(a.segs);
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = a.segs > 1 ? 1 : 0;   // a plain launch where one CTA has the row
     return touch ? cudaLaunchKernelEx(&cfg, process_logp_kernel<T, true>, a)
                  : cudaLaunchKernelEx(&cfg, process_logp_kernel<T, false>, a);
 }

@@ -451,6 +451,9 @@ __device__ __forceinline__ void report_bad_input(int *status)
     atomicCAS(status, 0, static_cast<int>(TIM_ERR_BAD_INPUT));
 }
 
+// (relaxed: the CTA runs, and what a fence released before it; no store of this
+// thread is waited for)
+__device__ __forceinline__ void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 

@@ -213,6 +213,15 @@ __device__ __forceinline__ void st_shared_cluster(uint32_t addr, int32_t v)
     asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
+// Asynchronous 16-byte store to shared memory anywhere in the cluster; the bytes
+// are counted on the mbarrier at `bar` (shared::cluster address in the same CTA).
+__device__ __forceinline__ void st_async_f4(uint32_t addr, float x, float y, float z, float w, uint32_t bar)
+{
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(addr),
+                 "f"(x), "f"(y), "f"(z), "f"(w), "r"(bar)
+                 : "memory");
+}
+
 // mbar_wait with acquire at cluster scope, for a barrier that a thread of the
 // other CTA of a pair arrives on after writing data this thread then reads.
 __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, volatile int *abort,
