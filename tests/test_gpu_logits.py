@@ -551,3 +551,28 @@ def test_wrapper_refusals():
 
 def test_rules_are_a_dataclass_of_optional_tensors():
     assert all(getattr(tim.LogitsRules(), f.name) is None for f in dataclasses.fields(tim.LogitsRules))
+
+
+# ----------------------------------------------------------------------------- together
+def test_example_runs_the_operators_together():
+    """The example's engine and trainer agree under the rules (both sides in fp32 on
+    two matrix products: rounding only) and not without them; no drawn token breaks
+    its grammar; its gradients are finite."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "processed_rollout.py")
+    spec = importlib.util.spec_from_file_location("processed_rollout", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    r = mod.main()
+    # |y| stays below 40: a dozen roundings of it on each side
+    assert r["mean_abs_delta"] < 40 * 24 * ref.U
+    assert r["mean_abs_delta_without_the_rules"] > 0.05
+    tok = r["sampled"].cpu().numpy()
+    for b in range(tok.shape[0]):
+        if b % 2:
+            made = tok[b, 12:]
+            assert (made % 7 != 0).all() if b // 2 % 2 == 0 else (made % 2 == 0).all()
+    assert np.isfinite(r["grad_norm"]) and r["grad_norm"] > 0 and r["distill_loss"] > 0
+    # no gradient on the prompt's positions
+    assert bool((r["kd"]["dlogits"][r["weight"] == 0] == 0).all())
