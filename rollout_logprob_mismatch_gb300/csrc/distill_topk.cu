@@ -209,9 +209,15 @@ __global__ void __launch_bounds__(LD_THREADS) distill_kernel(const DistillArgs a
     // the thread's first listed id and its teacher's logit, ahead of their use
     const int id0 = static_cast<int>(threadIdx.x) < a.K ? ids[threadIdx.x] : -1;
     const float t0 = static_cast<int>(threadIdx.x) < a.K ? teacher[threadIdx.x] : 0.f;
+    // In a call with sums rank 0's last warp takes no columns: it finds the teacher's
+    // statistics while the row comes in and hands them to every rank.  (As one more
+    // task of a warp with columns they were what all the ranks waited for, some
+    // 2 us of a CTA's 11.)
+    const bool teacher_warp = SUMS && rank == 0 && warp == LD_WARPS - 1;
+    const int workers = SUMS && rank == 0 ? LD_WARPS - 1 : LD_WARPS;
     auto mark = [&] {   // this rank's listed ids in the bitmap
-        for (int k = threadIdx.x; k < a.K; k += LD_THREADS) {
-            const int id = k < LD_THREADS ? id0 : ids[k];
+        for (int k = threadIdx.x; k < a.K; k += workers * 32) {
+            const int id = ids[k];
             if (id >= c0 && id < c1) {
                 const uint32_t bit = 1u << ((id - c0) & 31);
                 if (atomicOr(bitmap + ((id - c0) >> 5), bit) & bit)
@@ -226,15 +232,19 @@ __global__ void __launch_bounds__(LD_THREADS) distill_kernel(const DistillArgs a
     if constexpr (TAIL || !SUMS) {
         if constexpr (SUMS && TAIL && sizeof(T) == 2)
             masks.fill();
-        __syncthreads();
-        mark();
-        __syncthreads();
+        if (teacher_warp) {   // does not wait for the bitmap
+            named_arrive(1, LD_THREADS);
+            named_arrive(2, LD_THREADS);
+        } else {
+            named_sync(1, LD_THREADS);
+            mark();
+            named_sync(2, LD_THREADS);
+        }
     }
-    // The teacher's statistics: by the last warp (it has the fewest slices), while the
-    // others wait for the row; in a call with sums by rank 0, which hands them out.
-    // No rank writes a gradient before it has them, so the gathers of z are over by then.
+    // No rank writes a gradient before it has the statistics, so the gathers of z are
+    // over by then.
     TeacherRow tr{0.f, 0.f, 0.f, 0};
-    if (warp == LD_WARPS - 1 && (rank == 0 || !SUMS)) {
+    if (teacher_warp || (!SUMS && warp == LD_WARPS - 1)) {
         tr = teacher_row<T, TAIL>(a, row, lane, z, SUMS ? listed_x : nullptr);
         if (lane == 0 && (!SUMS || a.ranks == 1))
             hd.teacher = tr;
@@ -252,7 +262,7 @@ __global__ void __launch_bounds__(LD_THREADS) distill_kernel(const DistillArgs a
             cluster_wait();   // every CTA's barriers exist
             if (lane < takers)
                 peer = mapa_shared(smem_u32(smem), static_cast<uint32_t>(lane));
-            if (warp == LD_WARPS - 1 && rank == 0 && lane < takers)
+            if (teacher_warp && lane < takers)
                 st_async_f4(peer + static_cast<uint32_t>(offsetof(Head, teacher)), tr.max, tr.lse, tr.rest,
                             __int_as_float(tr.any), peer + static_cast<uint32_t>(offsetof(Head, parts)));
         } else {
@@ -266,7 +276,7 @@ __global__ void __launch_bounds__(LD_THREADS) distill_kernel(const DistillArgs a
                 drain_wait(smem_u32(&hd.bar), 0);
             }
         }
-        for (int sl = s0 + warp; sl < s1; sl += LD_WARPS) {
+        for (int sl = teacher_warp ? s1 : s0 + warp; sl < s1; sl += workers) {
             Raw8<T> raw[4];
             load_chunks<T, 4>(raw, src, sl * LG_SLICE - off, c1 - off, shift);
             float lm, ls, km = neg_inf(), ks = 0.f;
@@ -303,7 +313,8 @@ __global__ void __launch_bounds__(LD_THREADS) distill_kernel(const DistillArgs a
         if (!GRAD && (rank != 0 || warp != 0))
             return;
         if constexpr (GRAD && !TAIL)
-            mark();   // (while the other CTAs' partials come in)
+            if (!teacher_warp)
+                mark();   // (while the other CTAs' partials come in)
         bool lost = false;
         if (a.ranks > 1 && warp == 0) {
             lost = !mbar_wait_cluster(smem_u32(&hd.parts), 0, &hd.abort, a.wait_budget_ns);
