@@ -121,6 +121,7 @@ int process(tim::ProcArgs a, int op, const void *logits, int dtype, int64_t N, i
     a.ld = stride;
     a.N = static_cast<int32_t>(N);
     a.V = static_cast<int32_t>(V);
+    a.in_place = a.out == logits;
     return finish(tim::logits_process_launch(a, op, dtype, out_dtype, sms, reinterpret_cast<cudaStream_t>(stream)),
                   "launch");
 }

@@ -22,6 +22,7 @@ inline int lg_slices(int64_t V) { return static_cast<int>((V + LG_SLICE - 1) / L
 
 // ---------------------------------------------------------------- processing
 constexpr int LP_MAP_THREADS = 256, LP_MAP_CTAS = 6;     // WRITE, GRAD; CTAs of an SM the registers are held to
+constexpr int LP_BUILDERS = 128, LP_SHORT = 12;    // threads that build the table of a segment above LP_SHORT slices
 constexpr int LP_LOGP_THREADS = 384, LP_LOGP_CTAS = 4;   // LOGP
 constexpr int LP_MAP_SLICES = 64;                  // slices of a segment at most
 constexpr int LP_MAP_CAP = 3072, LP_LOGP_CAP = 2048;     // touched columns a table holds (at least LG_SLICE)
@@ -49,6 +50,7 @@ struct ProcArgs {
     const float *grad, *lse;   // GRAD
     void *out;                 // WRITE: processed logits; GRAD: gradient
     int64_t ldo;
+    int32_t in_place;          // out is z
     float *out_logp, *out_lse; // LOGP
     int32_t seg_slices;        // WRITE, GRAD: slices of a CTA; LOGP: of a cluster rank
     int32_t segs;              // CTAs of a row

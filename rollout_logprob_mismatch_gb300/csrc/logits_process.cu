@@ -130,6 +130,7 @@ template <typename C> struct Table {
     uint32_t *bitmap;    // [columns / 32]
     uint16_t *before;    // [columns / 128]: bits set in the four-word groups before
     C *column;           // [cap]: relative to the table's first
+    int *bad;            // a bias list that breaks its limits
     int cap;
     int groups, used;    // of the columns in hand
 };
@@ -137,7 +138,7 @@ template <typename C> struct Table {
 // Bytes of a table over `columns` columns (a multiple of 1024).
 template <typename C> __host__ __device__ inline size_t table_bytes(int columns, int cap)
 {
-    return static_cast<size_t>(cap) * (4 + sizeof(C)) + columns / 8 + columns / 64;
+    return static_cast<size_t>(cap) * (4 + sizeof(C)) + columns / 8 + columns / 64 + 16;
 }
 
 template <typename C> __device__ __forceinline__ Table<C> carve(uint32_t *smem, int columns, int cap)
@@ -148,6 +149,7 @@ template <typename C> __device__ __forceinline__ Table<C> carve(uint32_t *smem, 
     t.bitmap = smem + cap;
     t.before = reinterpret_cast<uint16_t *>(t.bitmap + columns / 32);
     t.column = reinterpret_cast<C *>(t.before + columns / 128);
+    t.bad = reinterpret_cast<int *>(t.column + cap);
     t.groups = t.used = 0;
     return t;
 }
@@ -184,7 +186,7 @@ __device__ __forceinline__ void scan_ids(const int32_t *ids, int j0, int j1, int
     }
 }
 
-// Empties the table for `width` columns.  All threads; a barrier before use.
+// Empties the table for `width` columns: the first NT threads; a barrier before use.
 template <int NT, typename C> __device__ __forceinline__ void clear_table(Table<C> &t, int width)
 {
     const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
@@ -193,16 +195,19 @@ template <int NT, typename C> __device__ __forceinline__ void clear_table(Table<
         reinterpret_cast<uint4 *>(t.bitmap)[j] = zero;
     for (int j = threadIdx.x; j < t.cap / 4; j += NT)
         reinterpret_cast<uint4 *>(t.value)[j] = zero;
+    if (threadIdx.x == 0)
+        *t.bad = 0;
 }
 
 // Builds the cleared table of columns c0 .. c0 + width - 1 with replacement(id, x,
-// slope) for each.  All threads of the CTA, and the same answer in all: kBad where
+// slope) for each.  The CTA's first NT threads, which meet at barrier BAR, and the
+// same answer in all: kBad where
 // the row's bias ids are out of range or order, kFull where more columns than the
 // table holds
 // are touched (never for width <= its capacity).  Ends with a barrier.
 enum TableState { kBuilt, kBad, kFull };
 
-template <int NT, typename T, typename C, typename F>
+template <int NT, int BAR, typename T, typename C, typename F>
 __device__ TableState build_table(const ProcArgs &a, const RowRules &r, const T *z, int c0, int width, Table<C> &t,
                                   F replacement)
 {
@@ -218,7 +223,10 @@ __device__ TableState build_table(const ProcArgs &a, const RowRules &r, const T 
         if (k < static_cast<unsigned>(width))
             mark(j, k);
     }
-    if (__syncthreads_or(bad))
+    if (bad)
+        *t.bad = 1;
+    named_sync(BAR, NT);
+    if (*t.bad)
         return kBad;
     // bits before each group of four words: a run of groups per thread
     const uint4 *groups = reinterpret_cast<const uint4 *>(t.bitmap);
@@ -239,7 +247,7 @@ __device__ TableState build_table(const ProcArgs &a, const RowRules &r, const T 
     }
     if (lane == 31)
         warp_bits[warp] = upto;
-    __syncthreads();
+    named_sync(BAR, NT);
     int base = upto - bits;
     t.used = 0;
 #pragma unroll
@@ -248,14 +256,14 @@ __device__ TableState build_table(const ProcArgs &a, const RowRules &r, const T 
         t.used += warp_bits[w];
     }
     if (t.used > t.cap) {
-        __syncthreads();   // warp_bits is written again
+        named_sync(BAR, NT);   // warp_bits is written again
         return kFull;
     }
     for (int q = q0; q < q1; ++q) {
         t.before[q] = static_cast<uint16_t>(base);
         base += bits_of(q);
     }
-    __syncthreads();
+    named_sync(BAR, NT);
     scan_ids<NT>(a.history, r.h0, r.h1, c0, width, [&](int j, unsigned k) {
         const int n = rank_of(t, k);
         t.column[n] = static_cast<C>(k);   // the same from every token with this id
@@ -269,7 +277,7 @@ __device__ TableState build_table(const ProcArgs &a, const RowRules &r, const T 
         t.column[n] = static_cast<C>(k);
         atomicOr(t.value + n, kBiased);
     });
-    __syncthreads();
+    named_sync(BAR, NT);
     auto finish = [&](int n, int id, float logit, float bias) {
         float slope;
         float x = touched_value(r, logit, bias, t.value[n] & ~kBiased, slope);
@@ -287,14 +295,14 @@ __device__ TableState build_table(const ProcArgs &a, const RowRules &r, const T 
         if (in1)
             finish(n1, id1, z1, 0.f);
     }
-    __syncthreads();
+    named_sync(BAR, NT);
     if (r.b1 > r.b0) {   // the biased ones, by their bias entry
         scan_ids<NT>(a.bias_ids, r.b0, r.b1, c0, width,
                  [&](int j, unsigned k) {
                          const int id = c0 + static_cast<int>(k);
                          finish(rank_of(t, k), id, Elem<T>::load(z + id), a.bias_values[j]);
                      });
-        __syncthreads();
+        named_sync(BAR, NT);
     }
     return kBuilt;
 }
@@ -303,14 +311,22 @@ __device__ TableState build_table(const ProcArgs &a, const RowRules &r, const T 
 __device__ __forceinline__ int half(int columns) { return (columns / 2 + LG_SLICE - 1) / LG_SLICE * LG_SLICE; }
 
 // ---------------------------------------------------------------- kernels
-// WRITE and GRAD: one CTA per (row, segment); no column depends on another.
-template <typename T, typename TO, int OP, bool TOUCH>
+// WRITE and GRAD: one CTA per (row, segment); no column depends on another.  Its
+// first NB threads build the table while the others stream the columns (512 at a
+// time, claimed from a counter), then join them; the touched columns go over the
+// streamed ones at the end.  In place the table, which reads the touched logits,
+// comes first.  NB is 128 of the 256 where a segment is long (the stream hides the
+// table: 345 us against 351 us for the gradient of 4096 x 128256 bf16), all 256 where
+// it is short and the table is what takes the time (26 us against 32 us for 64 rows
+// of 128256, histories of some 1000 tokens).
+template <typename T, typename TO, int OP, bool TOUCH, int NB = LP_MAP_THREADS>
 __global__ void __launch_bounds__(LP_MAP_THREADS, LP_MAP_CTAS) process_map_kernel(const ProcArgs a)
 {
     constexpr int NT = LP_MAP_THREADS, WARPS = NT / 32;
     extern __shared__ __align__(16) uint32_t smem[];
     __shared__ RowRules r;
     __shared__ HalfMasks masks;
+    __shared__ int s_next, s_state, s_used;
     const int row = static_cast<int>(blockIdx.x / static_cast<unsigned>(a.segs));
     const int seg = static_cast<int>(blockIdx.x % static_cast<unsigned>(a.segs));
     const int seg0 = seg * a.seg_slices * LG_SLICE, seg1 = min(a.V, seg0 + a.seg_slices * LG_SLICE);
@@ -324,37 +340,100 @@ __global__ void __launch_bounds__(LP_MAP_THREADS, LP_MAP_CTAS) process_map_kerne
         read_rules(a, row, r);
     if (sizeof(TO) == 2 && a.allowed)
         masks.fill();
-    if constexpr (TOUCH)
-        clear_table<NT>(t, seg1 - seg0);
+    if (TOUCH && threadIdx.x < NB)
+        clear_table<NB>(t, seg1 - seg0);
+    if (threadIdx.x == 0)
+        s_next = seg0;
     __syncthreads();
-    bool bad = r.bad;
-    const bool zero = OP == LP_GRAD && r.grad == 0.f;
     const float inv_tau = r.inv_tau, gi = r.grad * inv_tau;
     const float lse = r.lse == neg_inf() ? -neg_inf() : r.lse;   // an empty row: every probability is 0
     const uint8_t *const mask = r.mask;
     const int target = OP == LP_GRAD ? r.target : -1;
-    for (int c0 = seg0, c1, step = LP_TABLE; c0 < seg1; c0 = c1) {
-        c1 = min(seg1, c0 + step);
-        const bool has_target = target >= c0 && target < c1;
-        float target_v = 0.f;
-        if constexpr (OP == LP_GRAD) {
-            if (has_target && threadIdx.x == NT - 1) {   // an untouched target's one-hot term
-                const float x = Elem<T>::load(z + target);
-                target_v = is_allowed(mask, target) && x != neg_inf()
-                               ? (1.f - exp2_approx(fmaf(x, inv_tau, -lse) * LG_LOG2E)) * gi
-                               : 0.f;
-            }
-            if constexpr (!TOUCH)
-                __syncthreads();   // read before it is written over in place
+
+    auto fill = [&](float value) {
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v[i] = value;
+        const Raw8<TO> f = pack8<TO>(v);
+        for (int b = seg0 + warp * 256; b < seg1; b += WARPS * 256)
+            store8<TO>(out, b + lane * 8, seg1, shift_out, f);
+    };
+    if (r.bad || (OP == LP_GRAD && r.grad == 0.f)) {
+        fill(r.bad ? quiet_nan() : 0.f);
+        if (r.bad && threadIdx.x == 0)
+            report_bad_input(a.status);
+        return;
+    }
+    const Pair inv2 = pair(inv_tau, inv_tau), lse2 = pair(-lse, -lse), e2 = pair(LG_LOG2E, LG_LOG2E), g2 = pair(-gi, -gi);
+    auto chunks = [&](int b, int end) {   // columns b .. b + 511
+        Raw8<T> raw[2];
+        uint32_t drop[2] = {0u, 0u};
+        load_chunks<T, 2>(raw, z, b, end, shift);
+        if (mask) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+                if (b + u * 256 + lane * 8 < end)
+                    drop[u] = ~static_cast<uint32_t>(mask[(b + u * 256 + lane * 8) >> 3]) & 0xffu;
         }
-        if constexpr (TOUCH) {
-            if (!bad && !zero) {
-                if (c0 != seg0 || step != LP_TABLE) {
-                    __syncthreads();   // the table before has been written out
-                    clear_table<NT>(t, c1 - c0);
-                    __syncthreads();
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            float v[8];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const Pair x = get2<T>(raw[u], k);
+                if constexpr (OP == LP_WRITE) {
+                    unpair(mul2(x, inv2), v[2 * k], v[2 * k + 1]);
+                } else {
+                    float lo, hi;
+                    unpair(mul2(fma2(x, inv2, lse2), e2), lo, hi);
+                    unpair(mul2(pair(exp2_approx(lo), exp2_approx(hi)), g2), v[2 * k], v[2 * k + 1]);
                 }
-                const TableState state = build_table<NT>(a, r, z, c0, c1 - c0, t, [&](int id, float x, float slope) {
+            }
+            Raw8<TO> o = pack8<TO>(v);
+            if (drop[u])
+                drop8<TO>(o, drop[u], masks, OP == LP_WRITE ? Elem<TO>::NEG_INF : 0u);
+            store8<TO>(out, b + u * 256 + lane * 8, end, shift_out, o);
+        }
+    };
+    auto stream = [&](int end) {   // until nothing is left to claim below `end`
+        int b = 0;
+        if (lane == 0)
+            b = atomicAdd(&s_next, 512);
+        b = __shfl_sync(0xffffffffu, b, 0);
+        while (b < end) {
+            int next = 0;
+            if (lane == 0)
+                next = atomicAdd(&s_next, 512);
+            chunks(b, end);
+            b = __shfl_sync(0xffffffffu, next, 0);
+        }
+    };
+    // an untouched target's one-hot term (read before anything is written)
+    float target_v = 0.f;
+    const bool target_mine = target >= seg0 && target < seg1 && threadIdx.x == NT - 1;
+    if (target_mine) {
+        const float x = Elem<T>::load(z + target);
+        target_v = is_allowed(mask, target) && x != neg_inf()
+                       ? (1.f - exp2_approx(fmaf(x, inv_tau, -lse) * LG_LOG2E)) * gi
+                       : 0.f;
+    }
+    if constexpr (!TOUCH) {
+        if (OP == LP_GRAD)
+            __syncthreads();   // (in place)
+        for (int b = seg0 + warp * 512; b < seg1; b += WARPS * 512)
+            chunks(b, seg1);
+        if constexpr (OP == LP_GRAD) {
+            __syncthreads();
+            if (target_mine)
+                out[target] = Elem<TO>::from(target_v);
+        }
+    } else {
+        bool streamed = a.in_place == 0;   // the whole segment, along with the first table
+        for (int c0 = seg0, c1, width = seg1 - seg0; c0 < seg1;) {
+            c1 = min(seg1, c0 + width);
+            if (threadIdx.x < NB) {
+                const TableState state = build_table<NB, 1>(a, r, z, c0, c1 - c0, t, [&](int id, float x, float slope) {
                     const float y = x / r.tau;
                     if constexpr (OP == LP_GRAD)
                         return y == neg_inf() ? 0.f
@@ -363,69 +442,44 @@ __global__ void __launch_bounds__(LP_MAP_THREADS, LP_MAP_CTAS) process_map_kerne
                     else
                         return y;
                 });
-                bad = state == kBad;
-                if (state == kFull) {
-                    step = half(c1 - c0);
-                    c1 = c0;
-                    continue;
+                if (threadIdx.x == 0) {
+                    s_state = state;
+                    s_used = t.used;
                 }
             }
-        }
-        if (bad || zero) {
-            float v[8];
-            const float fill = bad ? quiet_nan() : 0.f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                v[i] = fill;
-            const Raw8<TO> f = pack8<TO>(v);
-            for (int b = c0 + warp * 256; b < c1; b += WARPS * 256)
-                store8<TO>(out, b + lane * 8, c1, shift_out, f);
-            continue;
-        }
-        const Pair inv2 = pair(inv_tau, inv_tau), lse2 = pair(-lse, -lse), e2 = pair(LG_LOG2E, LG_LOG2E),
-                   g2 = pair(-gi, -gi);
-        for (int b = c0 + warp * 512; b < c1; b += WARPS * 512) {
-            Raw8<T> raw[2];
-            uint32_t drop[2] = {0u, 0u};
-            load_chunks<T, 2>(raw, z, b, c1, shift);
-            if (mask) {
-#pragma unroll
-                for (int u = 0; u < 2; ++u)
-                    if (b + u * 256 + lane * 8 < c1)
-                        drop[u] = ~static_cast<uint32_t>(mask[(b + u * 256 + lane * 8) >> 3]) & 0xffu;
+            if (streamed)
+                stream(seg1);
+            __syncthreads();
+            const int state = s_state, used = s_used;
+            if (state == kBad) {
+                fill(quiet_nan());
+                if (threadIdx.x == 0)
+                    report_bad_input(a.status);
+                return;
             }
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                float v[8];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const Pair x = get2<T>(raw[u], k);
-                    if constexpr (OP == LP_WRITE) {
-                        unpair(mul2(x, inv2), v[2 * k], v[2 * k + 1]);
-                    } else {
-                        float lo, hi;
-                        unpair(mul2(fma2(x, inv2, lse2), e2), lo, hi);
-                        unpair(mul2(pair(exp2_approx(lo), exp2_approx(hi)), g2), v[2 * k], v[2 * k + 1]);
-                    }
+            if (state == kBuilt) {
+                if (!streamed) {   // in place: these columns now, after their table
+                    stream(c1);
+                    __syncthreads();
                 }
-                Raw8<TO> o = pack8<TO>(v);
-                if (drop[u])
-                    drop8<TO>(o, drop[u], masks, OP == LP_WRITE ? Elem<TO>::NEG_INF : 0u);
-                store8<TO>(out, b + u * 256 + lane * 8, c1, shift_out, o);
+                if (OP == LP_GRAD && target_mine && target >= c0 && target < c1 && !is_touched(t, target - c0))
+                    out[target] = Elem<TO>::from(target_v);
+                for (int n = threadIdx.x; n < used; n += NT)
+                    out[c0 + t.column[n]] = Elem<TO>::from(__uint_as_float(t.value[n]));
+                c0 = c1;
+            } else {
+                width = half(c1 - c0);
             }
-        }
-        if (TOUCH || OP == LP_GRAD) {
-            __syncthreads();   // the touched columns go over what has just been written
-            if (has_target && threadIdx.x == NT - 1 && !(TOUCH && is_touched(t, target - c0)))
-                out[target] = Elem<TO>::from(target_v);
-        }
-        if constexpr (TOUCH) {
-            for (int n = threadIdx.x; n < t.used; n += NT)
-                out[c0 + t.column[n]] = Elem<TO>::from(__uint_as_float(t.value[n]));
+            if (c0 < seg1) {
+                __syncthreads();   // the table has been read
+                if (threadIdx.x < NB)
+                    clear_table<NB>(t, min(seg1, c0 + width) - c0);
+                if (threadIdx.x == 0 && !streamed)
+                    s_next = c0;
+                __syncthreads();
+            }
         }
     }
-    if (bad && threadIdx.x == 0)
-        report_bad_input(a.status);
 }
 
 // LOGP: a cluster per row; each rank reduces seg_slices slices, one warp per
@@ -473,7 +527,7 @@ __global__ void __launch_bounds__(LP_LOGP_THREADS, LP_LOGP_CTAS) process_logp_ke
                 clear_table<NT>(t, c1 - c0);
                 __syncthreads();
             }
-            const TableState state = build_table<NT>(a, r, z, c0, c1 - c0, t, [](int, float x, float) { return x; });
+            const TableState state = build_table<NT, 1>(a, r, z, c0, c1 - c0, t, [](int, float x, float) { return x; });
             bad = state == kBad;
             if (bad)
                 break;
@@ -556,18 +610,21 @@ template <typename T, typename TO, int OP> cudaError_t launch_map(ProcArgs a, in
 {
     const bool touch = a.spans || a.bias_offsets;
     const int slices = lg_slices(a.V);
-    // segments of at most LP_MAP_SLICES, fewer while there are not four CTAs for every SM
-    int segs = (slices + LP_MAP_SLICES - 1) / LP_MAP_SLICES;
-    while (segs * 4 < slices && static_cast<int64_t>(a.N) * segs < 4 * num_sms)
-        segs *= 2;
+    // segments of at most LP_MAP_SLICES, and of at least four; five CTAs for every SM if
+    // the rows do not give them (of 3, 4, 5 and 6 the best for 64 rows of 128256 and 333
+    // of 32003)
+    const int want = static_cast<int>((int64_t(5) * num_sms + a.N - 1) / a.N);
+    const int segs = std::max((slices + LP_MAP_SLICES - 1) / LP_MAP_SLICES, std::min((slices + 3) / 4, want));
     a.seg_slices = (slices + segs - 1) / segs;
     a.segs = (slices + a.seg_slices - 1) / a.seg_slices;
     a.table_columns = a.seg_slices * LG_SLICE;
     a.table_cap = LP_MAP_CAP;
     const unsigned grid = static_cast<unsigned>(a.N) * static_cast<unsigned>(a.segs);
-    if (touch)
-        process_map_kernel<T, TO, OP, true>
-            <<<grid, LP_MAP_THREADS, table_bytes<uint16_t>(a.table_columns, a.table_cap), s>>>(a);
+    const size_t bytes = table_bytes<uint16_t>(a.table_columns, a.table_cap);
+    if (touch && a.seg_slices > LP_SHORT)
+        process_map_kernel<T, TO, OP, true, LP_BUILDERS><<<grid, LP_MAP_THREADS, bytes, s>>>(a);
+    else if (touch)
+        process_map_kernel<T, TO, OP, true><<<grid, LP_MAP_THREADS, bytes, s>>>(a);
     else
         process_map_kernel<T, TO, OP, false><<<grid, LP_MAP_THREADS, 0, s>>>(a);
     return cudaGetLastError();
@@ -610,16 +667,19 @@ template <typename T> cudaError_t launch_op(const ProcArgs &a, int op, int out_d
     return launch_map<T, T, LP_WRITE>(a, num_sms, s);
 }
 
+template <typename T, typename TO, int OP> cudaError_t set_smem_map()
+{
+    const cudaError_t e = set_smem(process_map_kernel<T, TO, OP, true>);
+    return e != cudaSuccess ? e : set_smem(process_map_kernel<T, TO, OP, true, LP_BUILDERS>);
+}
+
 template <typename T> cudaError_t prepare()
 {
-    cudaError_t e = set_smem(process_map_kernel<T, T, LP_WRITE, true>);
-    if (e == cudaSuccess)
-        e = set_smem(process_map_kernel<T, float, LP_WRITE, true>);
-    if (e == cudaSuccess)
-        e = set_smem(process_map_kernel<T, T, LP_GRAD, true>);
-    if (e == cudaSuccess)
-        e = set_smem(process_logp_kernel<T, true>);
-    return e;
+    for (cudaError_t e : {set_smem_map<T, T, LP_WRITE>(), set_smem_map<T, float, LP_WRITE>(), set_smem_map<T, T, LP_GRAD>(),
+                          set_smem(process_logp_kernel<T, true>), set_smem(process_logp_kernel<T, false>)})
+        if (e != cudaSuccess)
+            return e;
+    return cudaSuccess;
 }
 
 } // namespace
