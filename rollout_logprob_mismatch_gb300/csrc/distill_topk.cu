@@ -123,7 +123,7 @@ __device__ __forceinline__ TeacherRow teacher_row(const DistillArgs &a, int row,
 // copy of the whole 16-byte pieces, the up to seven elements before and after
 // them by plain loads (so nothing outside the row is read).  All threads; the
 // plain stores are visible after the next barrier of the CTA.
-template <typename T>
+template <int NT, typename T>
 __device__ __forceinline__ void fetch_row(const T *z, int c0, int c1, uint32_t shift, uint8_t *dst, uint32_t bar)
 {
     const uintptr_t a0 = reinterpret_cast<uintptr_t>(z + c0), a1 = reinterpret_cast<uintptr_t>(z + c1);
@@ -140,7 +140,7 @@ __device__ __forceinline__ void fetch_row(const T *z, int c0, int c1, uint32_t s
     }
     const int head = static_cast<int>((lo - a0) / sizeof(T)), tail = static_cast<int>((a1 - hi) / sizeof(T));
     T *s = reinterpret_cast<T *>(dst + shift);
-    for (int i = threadIdx.x; i < head + tail; i += LD_THREADS) {
+    for (int i = threadIdx.x; i < head + tail; i += NT) {
         const int col = i < head ? i : (c1 - c0) - (head + tail) + i;
         s[col] = z[c0 + col];
     }
@@ -148,9 +148,10 @@ __device__ __forceinline__ void fetch_row(const T *z, int c0, int c1, uint32_t s
 
 // HOLD: the rank's part of the row stays in shared memory between the two passes
 // of a step.
-template <typename T, int OP, bool TAIL, bool HOLD>
-__global__ void __launch_bounds__(LD_THREADS) distill_kernel(const DistillArgs a)
+template <typename T, int OP, bool TAIL, bool HOLD, int NT>
+__global__ void __launch_bounds__(NT) distill_kernel(const DistillArgs a)
 {
+    constexpr int WARPS = NT / 32;
     constexpr bool SUMS = OP != LD_BACKWARD, GRAD = OP != LD_FORWARD, BITS = TAIL || GRAD;
     extern __shared__ __align__(16) uint8_t smem[];
     const int slices = (a.V + LG_SLICE - 1) / LG_SLICE;
@@ -190,13 +191,13 @@ __global__ void __launch_bounds__(LD_THREADS) distill_kernel(const DistillArgs a
         }
     }
     if constexpr (HOLD)
-        fetch_row<T>(z, c0, c1, shift, smem + lay.row, smem_u32(&hd.bar));
+        fetch_row<NT>(z, c0, c1, shift, smem + lay.row, smem_u32(&hd.bar));
     if (SUMS && a.ranks > 1)
         cluster_arrive_relaxed();   // waited for before the first store into another CTA's shared memory
 
     auto zero_row = [&] {
         const float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        for (int b = c0 + warp * 256; b < c1; b += LD_WARPS * 256)
+        for (int b = c0 + warp * 256; b < c1; b += WARPS * 256)
             store8<T>(dz, b + lane * 8, c1, shift_out, pack8<T>(v));
     };
     if constexpr (!SUMS) {
@@ -213,8 +214,8 @@ __global__ void __launch_bounds__(LD_THREADS) distill_kernel(const DistillArgs a
     // statistics while the row comes in and hands them to every rank.  (As one more
     // task of a warp with columns they were what all the ranks waited for, some
     // 2 us of a CTA's 11.)
-    const bool teacher_warp = SUMS && rank == 0 && warp == LD_WARPS - 1;
-    const int workers = SUMS && rank == 0 ? LD_WARPS - 1 : LD_WARPS;
+    const bool teacher_warp = SUMS && rank == 0 && warp == WARPS - 1;
+    const int workers = SUMS && rank == 0 ? WARPS - 1 : WARPS;
     auto mark = [&] {   // this rank's listed ids in the bitmap
         for (int k = threadIdx.x; k < a.K; k += workers * 32) {
             const int id = ids[k];
@@ -226,25 +227,25 @@ __global__ void __launch_bounds__(LD_THREADS) distill_kernel(const DistillArgs a
         }
     };
     if constexpr (BITS) {
-        for (int j = threadIdx.x; j < (c1 - c0 + 31) / 32; j += LD_THREADS)
+        for (int j = threadIdx.x; j < (c1 - c0 + 31) / 32; j += NT)
             bitmap[j] = 0;
     }
     if constexpr (TAIL || !SUMS) {
         if constexpr (SUMS && TAIL && sizeof(T) == 2)
             masks.fill();
         if (teacher_warp) {   // does not wait for the bitmap
-            named_arrive(1, LD_THREADS);
-            named_arrive(2, LD_THREADS);
+            named_arrive(1, NT);
+            named_arrive(2, NT);
         } else {
-            named_sync(1, LD_THREADS);
+            named_sync(1, NT);
             mark();
-            named_sync(2, LD_THREADS);
+            named_sync(2, NT);
         }
     }
     // No rank writes a gradient before it has the statistics, so the gathers of z are
     // over by then.
     TeacherRow tr{0.f, 0.f, 0.f, 0};
-    if (teacher_warp || (!SUMS && warp == LD_WARPS - 1)) {
+    if (teacher_warp || (!SUMS && warp == WARPS - 1)) {
         tr = teacher_row<T, TAIL>(a, row, lane, z, SUMS ? listed_x : nullptr);
         if (lane == 0 && (!SUMS || a.ranks == 1))
             hd.teacher = tr;
@@ -379,7 +380,7 @@ __global__ void __launch_bounds__(LD_THREADS) distill_kernel(const DistillArgs a
     if constexpr (GRAD) {
         if (SUMS && g == 0.f) {
             zero_row();
-            if (SUMS && rank == 0 && warp == LD_WARPS - 1)
+            if (SUMS && rank == 0 && warp == WARPS - 1)
                 write_loss();
             return;
         }
@@ -404,13 +405,13 @@ __global__ void __launch_bounds__(LD_THREADS) distill_kernel(const DistillArgs a
                 ref = -neg_inf();
         }
         // the listed ids' values first: z may be written over in place
-        constexpr int KPT = (LD_MAX_K + LD_THREADS - 1) / LD_THREADS;
+        constexpr int KPT = (LD_MAX_K + NT - 1) / NT;
         float own[KPT];
 #pragma unroll
         for (int n = 0; n < KPT; ++n) {
-            const int k = static_cast<int>(threadIdx.x) + n * LD_THREADS;
+            const int k = static_cast<int>(threadIdx.x) + n * NT;
             own[n] = 0.f;
-            if (n * LD_THREADS >= a.K)
+            if (n * NT >= a.K)
                 continue;
             const int id = k >= a.K ? -1 : n == 0 ? id0 : ids[k];
             if (id >= c0 && id < c1) {
@@ -430,7 +431,7 @@ __global__ void __launch_bounds__(LD_THREADS) distill_kernel(const DistillArgs a
         const float wgi = others * gi * scale;
         const Pair first2 = pair(first, first), ref2 = pair(-ref, -ref), second2 = pair(second, second),
                    w2 = pair(wgi, wgi);
-        for (int b = c0 + warp * 512; b < c1; b += LD_WARPS * 512) {
+        for (int b = c0 + warp * 512; b < c1; b += WARPS * 512) {
             Raw8<T> raw[2];
             load_chunks<T, 2>(raw, src, b - off, c1 - off, shift);
 #pragma unroll
@@ -448,24 +449,24 @@ __global__ void __launch_bounds__(LD_THREADS) distill_kernel(const DistillArgs a
         __syncthreads();
 #pragma unroll
         for (int n = 0; n < KPT; ++n) {
-            const int k = static_cast<int>(threadIdx.x) + n * LD_THREADS;
-            if (n * LD_THREADS >= a.K)
+            const int k = static_cast<int>(threadIdx.x) + n * NT;
+            if (n * NT >= a.K)
                 break;
             const int id = k >= a.K ? -1 : n == 0 ? id0 : ids[k];
             if (id >= c0 && id < c1)
                 dz[id] = Elem<T>::from(own[n]);
         }
-        if (SUMS && rank == 0 && warp == LD_WARPS - 1)
+        if (SUMS && rank == 0 && warp == WARPS - 1)
             write_loss();
     }
 }
 
-template <typename T, int OP, bool TAIL, bool HOLD>
+template <typename T, int OP, bool TAIL, bool HOLD, int NT>
 cudaError_t launch_kernel(const DistillArgs &a, const Layout &l, cudaStream_t s)
 {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(a.N) * static_cast<unsigned>(a.ranks));
-    cfg.blockDim = dim3(LD_THREADS);
+    cfg.blockDim = dim3(NT);
     cfg.dynamicSmemBytes = l.bytes;
     cfg.stream = s;
     cudaLaunchAttribute at[1];
@@ -474,27 +475,40 @@ cudaError_t launch_kernel(const DistillArgs &a, const Layout &l, cudaStream_t s)
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = OP != LD_BACKWARD && a.ranks > 1 ? 1 : 0;   // (the backward's CTAs do not meet)
-    return cudaLaunchKernelEx(&cfg, distill_kernel<T, OP, TAIL, HOLD>, a);
+    return cudaLaunchKernelEx(&cfg, distill_kernel<T, OP, TAIL, HOLD, NT>, a);
 }
 
 template <typename T, int OP, bool TAIL> cudaError_t launch(DistillArgs a, int num_sms, cudaStream_t s)
 {
     const int slices = lg_slices(a.V);
-    int ranks = 1;   // CTAs of a row: more while the rows alone leave SMs idle
-    while (ranks < LG_CLUSTER && ranks * 2 <= slices && static_cast<int64_t>(a.N) * ranks < 4 * num_sms)
+    // CTAs of a row: more while the rows alone leave SMs idle, and in the single passes
+    // while parts stay long, so that the last of the CTAs end together (forward of 1941
+    // rows of 116416 bf16 91 us against 105 us)
+    int ranks = 1;
+    const int64_t rows = a.N;
+    while (ranks < LG_CLUSTER && ((ranks * 2 <= slices && rows * ranks < 4 * num_sms) ||
+                                  (OP != LD_STEP && ranks * 32 <= slices && rows * ranks < 16 * num_sms)))
         ranks *= 2;
-    if (OP == LD_STEP)   // a rank's part of the row: 40 KB, so that five CTAs fit an SM
-        while (ranks < LG_CLUSTER && static_cast<size_t>((slices + ranks - 1) / ranks) * LG_SLICE * sizeof(T) > 40 * 1024)
+    if (OP == LD_STEP)   // a rank's part of the row: at most 52 KB, so that four or five CTAs fit an SM
+        while (ranks < LG_CLUSTER && static_cast<size_t>((slices + ranks - 1) / ranks) * LG_SLICE * sizeof(T) > 52 * 1024)
             ranks *= 2;
     a.per = (slices + ranks - 1) / ranks;
     a.ranks = (slices + a.per - 1) / a.per;
     constexpr bool SUMS = OP != LD_BACKWARD, BITS = TAIL || OP != LD_FORWARD;
+    // short parts: half the threads, twice the CTAs (step of 4096 rows of 8192 fp16 with a
+    // tail 52 us against 65 us)
+    const bool few = a.per <= LD_FEW;
     if constexpr (OP == LD_STEP) {
         const Layout l = layout<T>(slices, a.per, a.K, SUMS, BITS, TAIL, true);
         if (l.bytes <= LD_SMEM)
-            return launch_kernel<T, OP, TAIL, true>(a, l, s);
+            return few ? launch_kernel<T, OP, TAIL, true, LD_THREADS / 2>(a, l, s)
+                       : launch_kernel<T, OP, TAIL, true, LD_THREADS>(a, l, s);
+        return launch_kernel<T, OP, TAIL, false, LD_THREADS>(a, layout<T>(slices, a.per, a.K, SUMS, BITS, TAIL, false), s);
+    } else {
+        const Layout l = layout<T>(slices, a.per, a.K, SUMS, BITS, TAIL, false);
+        return few ? launch_kernel<T, OP, TAIL, false, LD_THREADS / 2>(a, l, s)
+                   : launch_kernel<T, OP, TAIL, false, LD_THREADS>(a, l, s);
     }
-    return launch_kernel<T, OP, TAIL, false>(a, layout<T>(slices, a.per, a.K, SUMS, BITS, TAIL, false), s);
 }
 
 template <typename T> cudaError_t launch_op(const DistillArgs &a, int op, int num_sms, cudaStream_t s)
@@ -509,7 +523,12 @@ template <typename T> cudaError_t launch_op(const DistillArgs &a, int op, int nu
 
 template <typename T, int OP, bool TAIL, bool HOLD> cudaError_t set_smem()
 {
-    return cudaFuncSetAttribute(distill_kernel<T, OP, TAIL, HOLD>, cudaFuncAttributeMaxDynamicSharedMemorySize, LD_SMEM);
+    cudaError_t e = cudaFuncSetAttribute(distill_kernel<T, OP, TAIL, HOLD, LD_THREADS>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, LD_SMEM);
+    if (HOLD && e == cudaSuccess)
+        e = cudaFuncSetAttribute(distill_kernel<T, OP, TAIL, HOLD, LD_THREADS / 2>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, LD_SMEM);
+    return e;
 }
 
 template <typename T, bool TAIL> cudaError_t prepare_tail()

@@ -23,9 +23,9 @@ inline int lg_slices(int64_t V) { return static_cast<int>((V + LG_SLICE - 1) / L
 // ---------------------------------------------------------------- processing
 constexpr int LP_MAP_THREADS = 256, LP_MAP_CTAS = 6;     // WRITE, GRAD; CTAs of an SM the registers are held to
 constexpr int LP_BUILDERS = 128, LP_SHORT = 12;    // threads that build the table of a segment above LP_SHORT slices
-constexpr int LP_LOGP_THREADS = 384, LP_LOGP_CTAS = 4;   // LOGP
 constexpr int LP_MAP_SLICES = 64;                  // slices of a segment at most
 constexpr int LP_MAP_CAP = 3072, LP_LOGP_CAP = 2048;     // touched columns a table holds (at least LG_SLICE)
+constexpr int LP_HEAVY = 1536, LP_HEAVY_CAP = 5120;      // tokens of history a row, on average; the table then
 constexpr int LP_TABLE = 1 << 18;                  // columns a table covers
 static_assert(LP_MAP_SLICES * LG_SLICE <= 65536, "a segment's columns are counted in 16 bits");
 
@@ -64,7 +64,7 @@ cudaError_t logits_process_launch(ProcArgs a, int op, int dtype, int out_dtype, 
 
 // ---------------------------------------------------------------- distillation
 constexpr int LD_THREADS = 256;
-constexpr int LD_WARPS = LD_THREADS / 32;
+constexpr int LD_FEW = 12;                         // slices of a CTA up to which half the threads run
 constexpr int LD_MAX_K = 1024;
 constexpr int LD_SMEM = 224 * 1024;                // shared memory a CTA may take
 

@@ -193,8 +193,6 @@ template <int NT, typename C> __device__ __forceinline__ void clear_table(Table<
     t.groups = (width + 127) / 128;
     for (int j = threadIdx.x; j < t.groups; j += NT)
         reinterpret_cast<uint4 *>(t.bitmap)[j] = zero;
-    for (int j = threadIdx.x; j < t.cap / 4; j += NT)
-        reinterpret_cast<uint4 *>(t.value)[j] = zero;
     if (threadIdx.x == 0)
         *t.bad = 0;
 }
@@ -263,6 +261,8 @@ __device__ TableState build_table(const ProcArgs &a, const RowRules &r, const T 
         t.before[q] = static_cast<uint16_t>(base);
         base += bits_of(q);
     }
+    for (int n = threadIdx.x; n < t.used; n += NT)
+        t.value[n] = 0;
     named_sync(BAR, NT);
     scan_ids<NT>(a.history, r.h0, r.h1, c0, width, [&](int j, unsigned k) {
         const int n = rank_of(t, k);
@@ -484,10 +484,10 @@ __global__ void __launch_bounds__(LP_MAP_THREADS, LP_MAP_CTAS) process_map_kerne
 
 // LOGP: a cluster per row; each rank reduces seg_slices slices, one warp per
 // slice.  The slices' partials go to rank 0's shared memory, which folds them.
-template <typename T, bool TOUCH>
-__global__ void __launch_bounds__(LP_LOGP_THREADS, LP_LOGP_CTAS) process_logp_kernel(const ProcArgs a)
+template <typename T, bool TOUCH, int NT, int CTAS>
+__global__ void __launch_bounds__(NT, CTAS) process_logp_kernel(const ProcArgs a)
 {
-    constexpr int NT = LP_LOGP_THREADS, WARPS = NT / 32;
+    constexpr int WARPS = NT / 32;
     extern __shared__ __align__(16) uint32_t smem[];
     __shared__ RowRules r;
     __shared__ HalfMasks masks;
@@ -602,8 +602,10 @@ __global__ void __launch_bounds__(LP_LOGP_THREADS, LP_LOGP_CTAS) process_logp_ke
 
 template <typename F> cudaError_t set_smem(F *kernel)
 {
+    const size_t logp = table_bytes<int32_t>(LP_TABLE, LP_LOGP_CAP) + LG_MAX_SLICES * 8;
+    const size_t map = table_bytes<uint16_t>(LP_MAP_SLICES * LG_SLICE, LP_HEAVY_CAP);
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                static_cast<int>(table_bytes<int32_t>(LP_TABLE, LP_LOGP_CAP)) + LG_MAX_SLICES * 8);
+                                static_cast<int>(std::max(logp, map)));
 }
 
 template <typename T, typename TO, int OP> cudaError_t launch_map(ProcArgs a, int num_sms, cudaStream_t s)
@@ -618,16 +620,37 @@ template <typename T, typename TO, int OP> cudaError_t launch_map(ProcArgs a, in
     a.seg_slices = (slices + segs - 1) / segs;
     a.segs = (slices + a.seg_slices - 1) / a.seg_slices;
     a.table_columns = a.seg_slices * LG_SLICE;
-    a.table_cap = LP_MAP_CAP;
+    // Rows with long histories of their own (on average: rows that share theirs count
+    // little) touch more columns than the usual table holds, and the table is what takes
+    // the time.
+    const bool heavy = a.history_len / LP_HEAVY >= a.N;
+    a.table_cap = heavy ? LP_HEAVY_CAP : LP_MAP_CAP;
     const unsigned grid = static_cast<unsigned>(a.N) * static_cast<unsigned>(a.segs);
     const size_t bytes = table_bytes<uint16_t>(a.table_columns, a.table_cap);
-    if (touch && a.seg_slices > LP_SHORT)
+    if (touch && a.seg_slices > LP_SHORT && !heavy)
         process_map_kernel<T, TO, OP, true, LP_BUILDERS><<<grid, LP_MAP_THREADS, bytes, s>>>(a);
     else if (touch)
         process_map_kernel<T, TO, OP, true><<<grid, LP_MAP_THREADS, bytes, s>>>(a);
     else
         process_map_kernel<T, TO, OP, false><<<grid, LP_MAP_THREADS, 0, s>>>(a);
     return cudaGetLastError();
+}
+
+template <typename T, bool TOUCH, int NT, int CTAS> cudaError_t launch_logp_kernel(const ProcArgs &a, cudaStream_t s)
+{
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(a.N) * static_cast<unsigned>(a.segs));
+    cfg.blockDim = dim3(NT);
+    cfg.dynamicSmemBytes = static_cast<size_t>(lg_slices(a.V)) * 8 +
+                           (TOUCH ? table_bytes<int32_t>(a.table_columns, a.table_cap) : 0);
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = static_cast<unsigned>(a.segs);
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = a.segs > 1 ? 1 : 0;   // a plain launch where one CTA has the row
+    return cudaLaunchKernelEx(&cfg, process_logp_kernel<T, TOUCH, NT, CTAS>, a);
 }
 
 template <typename T> cudaError_t launch_logp(ProcArgs a, int num_sms, cudaStream_t s)
@@ -640,20 +663,18 @@ template <typename T> cudaError_t launch_logp(ProcArgs a, int num_sms, cudaStrea
     a.seg_slices = (slices + ranks - 1) / ranks;
     a.segs = (slices + a.seg_slices - 1) / a.seg_slices;
     a.table_columns = std::min(LP_TABLE, a.seg_slices * LG_SLICE);
-    a.table_cap = LP_LOGP_CAP;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(a.N) * static_cast<unsigned>(a.segs));
-    cfg.blockDim = dim3(LP_LOGP_THREADS);
-    cfg.dynamicSmemBytes = static_cast<size_t>(slices) * 8 + (touch ? table_bytes<int32_t>(a.table_columns, a.table_cap) : 0);
-    cfg.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = static_cast<unsigned>(a.segs);
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = a.segs > 1 ? 1 : 0;   // a plain launch where one CTA has the row
-    return touch ? cudaLaunchKernelEx(&cfg, process_logp_kernel<T, true>, a)
-                 : cudaLaunchKernelEx(&cfg, process_logp_kernel<T, false>, a);
+    // The shorter a CTA's part of the row, the more of its time is the table's, and the
+    // more CTAs an SM needs to fill it: 128 threads against 384 took 55 us against 75 us
+    // for 2916 rows of 20544 fp16, 192 against 384 118 us against 138 us for 4096 of
+    // 50304 bf16; for 8192 of 151936 384 threads are 4 % faster than 256.
+    // (With more than 1024 entries their tables leave L1 too little for the loads in
+    // flight: 118 us became 128 us.)
+    a.table_cap = a.seg_slices <= 110 ? 1024 : LP_LOGP_CAP;
+    if (a.seg_slices <= 40)
+        return touch ? launch_logp_kernel<T, true, 128, 10>(a, s) : launch_logp_kernel<T, false, 128, 10>(a, s);
+    if (a.seg_slices <= 110)
+        return touch ? launch_logp_kernel<T, true, 192, 7>(a, s) : launch_logp_kernel<T, false, 192, 7>(a, s);
+    return touch ? launch_logp_kernel<T, true, 384, 4>(a, s) : launch_logp_kernel<T, false, 384, 4>(a, s);
 }
 
 template <typename T> cudaError_t launch_op(const ProcArgs &a, int op, int out_dtype, int num_sms, cudaStream_t s)
@@ -676,7 +697,7 @@ template <typename T, typename TO, int OP> cudaError_t set_smem_map()
 template <typename T> cudaError_t prepare()
 {
     for (cudaError_t e : {set_smem_map<T, T, LP_WRITE>(), set_smem_map<T, float, LP_WRITE>(), set_smem_map<T, T, LP_GRAD>(),
-                          set_smem(process_logp_kernel<T, true>), set_smem(process_logp_kernel<T, false>)})
+                          set_smem(process_logp_kernel<T, true, 192, 7>), set_smem(process_logp_kernel<T, true, 384, 4>)})
         if (e != cudaSuccess)
             return e;
     return cudaSuccess;
