@@ -15,11 +15,19 @@
 // log-sum-exp over the columns whose bit is not set in a bitmap of the listed
 // ids, never 1 - sum p_k, which loses all its digits when p_o is small.
 //
-// What bounds it: the row streams through once for the sums and, in a step, once
-// more (from L2, where the cluster's rows of the moment fit) for the gradient;
-// the listed ids cost K gathers and K stores.  The gradient pass writes every
-// column as if it were not listed; after a barrier the listed ones, all of
-// which the same CTA owns, are written over.
+// What bounds it: the row streams through once for the sums and once for the
+// gradient; the listed ids cost K gathers and K stores.  The gradient pass writes
+// every column as if it were not listed; after a barrier the listed ones, all of
+// which the same CTA owns, are written over.  In a step the row comes from memory
+// once: a cluster holds it in its CTAs' shared memory (one bulk copy each, at most
+// 52 KB) between the passes, and the CTAs exchange the slices' partials.
+//
+// Measured on a GB300 against the bytes each has to move at 6760 GB/s:
+//   loss      8192 x 151936 bf16, K = 64   390 us of 369 us: memory
+//   gradient  4096 x 128256 bf16, K = 64   312 us of 311 us: memory
+//   step      4096 x 151936 bf16, K = 64   511 us of 369 us, 1024 x 129280 fp32 with a
+//             tail, K = 128, 224 us of 157 us: a CTA's life of 10 us (row 2.5 us, sums 2 us,
+//             the other CTAs 2 us, gradient 2 us), of which five or two fit an SM
 #include <algorithm>
 #include <cstddef>
 
@@ -175,6 +183,8 @@ __global__ void __launch_bounds__(NT) distill_kernel(const DistillArgs a)
     float g = 0.f;
     if constexpr (GRAD)
         g = a.grad[row];
+    TIM_DCHECK(!GRAD || threadIdx.x != 0 || rank != 0 || (isfinite(g) && (SUMS || a.lse[row] < INFINITY)), a.status,
+               TIM_CHECK_BACKWARD_INPUT, row, __float_as_uint(g));
     const int takers = GRAD ? a.ranks : 1;   // ranks that fold the row's partials
     // the columns as the passes read them: from memory, or from this CTA's copy
     const T *src = HOLD ? reinterpret_cast<const T *>(smem + lay.row + shift) : z;

@@ -24,7 +24,7 @@ inline int lg_slices(int64_t V) { return static_cast<int>((V + LG_SLICE - 1) / L
 constexpr int LP_MAP_THREADS = 256, LP_MAP_CTAS = 6;     // WRITE, GRAD; CTAs of an SM the registers are held to
 constexpr int LP_BUILDERS = 128, LP_SHORT = 12;    // threads that build the table of a segment above LP_SHORT slices
 constexpr int LP_MAP_SLICES = 64;                  // slices of a segment at most
-constexpr int LP_MAP_CAP = 3072, LP_LOGP_CAP = 2048;     // touched columns a table holds (at least LG_SLICE)
+constexpr int LP_MAP_CAP = 3072, LP_LOGP_CAP = 1536;     // touched columns a table holds (at least LG_SLICE)
 constexpr int LP_HEAVY = 1536, LP_HEAVY_CAP = 5120;      // tokens of history a row, on average; the table then
 constexpr int LP_TABLE = 1 << 18;                  // columns a table covers
 static_assert(LP_MAP_SLICES * LG_SLICE <= 65536, "a segment's columns are counted in 16 bits");

@@ -16,13 +16,21 @@
 // once; only the few touched columns (history and biased ids) need more.  So the
 // columns are streamed as if none were touched, and a table in shared memory
 // holds the touched ones: a bitmap of the CTA's columns, the number of bits
-// before each of its words, and one 4-byte entry per touched column, in column
+// before each group of four of its words, and an entry per touched column, in column
 // order.  Building it takes two scans of the row's history (set the bits; count
 // with shared-memory integer atomics, which have no order) and one gather per
-// distinct id; no sort, no hash, any history length (a history that could fill
-// more than LP_CAP entries is handled LP_CAP columns at a time).  The log-probability
-// takes the touched columns out of the stream and adds the table's entries of the
-// same slice; the others write their columns first and the touched ones over them.
+// distinct id; no sort, no hash, any history length (where more columns are touched
+// than a table holds, the columns are handled in halves).  The log-probability takes
+// the touched columns out of the stream and adds the table's entries of the same
+// slice; the others write their columns first and the touched ones over them.
+//
+// Measured on a GB300 against the bytes each has to move at 6760 GB/s (inputs not in L2):
+//   process   512 x 151936 bf16, histories of 1000 tokens   79 us of 47 us: the tables
+//   process   64 x 128256 bf16 -> fp32, half under a grammar 26 us of 7 us: one table's
+//             chain of loads and barriers (rules, history, counts, gathers), then the stream
+//   logprob   8192 x 151936 bf16, packed sequences of 512   439 us of 368 us: issue slots
+//             (6 instructions a column for the sum, 3 more for table and touched columns)
+//   gradient  4096 x 128256 bf16, a quarter under a grammar 344 us of 313 us: memory
 #include <algorithm>
 
 #include "logits_rows.cuh"
@@ -349,6 +357,9 @@ __global__ void __launch_bounds__(LP_MAP_THREADS, LP_MAP_CTAS) process_map_kerne
     const float lse = r.lse == neg_inf() ? -neg_inf() : r.lse;   // an empty row: every probability is 0
     const uint8_t *const mask = r.mask;
     const int target = OP == LP_GRAD ? r.target : -1;
+    TIM_DCHECK(threadIdx.x != 0 || seg != 0 || target < a.V, a.status, TIM_CHECK_TARGET, row, target);
+    TIM_DCHECK(OP != LP_GRAD || threadIdx.x != 0 || seg != 0 || r.bad || (isfinite(r.grad) && r.lse < INFINITY), a.status,
+               TIM_CHECK_BACKWARD_INPUT, row, __float_as_uint(r.lse));
 
     auto fill = [&](float value) {
         float v[8];
@@ -515,6 +526,7 @@ __global__ void __launch_bounds__(NT, CTAS) process_logp_kernel(const ProcArgs a
     const float inv_tau = r.inv_tau, k2 = LG_LOG2E * inv_tau;
     const uint8_t *const mask = r.mask;
     const int target = r.target;
+    TIM_DCHECK(threadIdx.x != 0 || rank != 0 || target < a.V, a.status, TIM_CHECK_TARGET, row, target);
     const bool has_target = target >= s0 * LG_SLICE && target < min(a.V, s1 * LG_SLICE);
     if (has_target && threadIdx.x == NT - 1)
         target_x = is_allowed(mask, target) ? Elem<T>::load(z + target) : neg_inf();
@@ -664,17 +676,17 @@ template <typename T> cudaError_t launch_logp(ProcArgs a, int num_sms, cudaStrea
     a.segs = (slices + a.seg_slices - 1) / a.seg_slices;
     a.table_columns = std::min(LP_TABLE, a.seg_slices * LG_SLICE);
     // The shorter a CTA's part of the row, the more of its time is the table's, and the
-    // more CTAs an SM needs to fill it: 128 threads against 384 took 55 us against 75 us
-    // for 2916 rows of 20544 fp16, 192 against 384 118 us against 138 us for 4096 of
-    // 50304 bf16; for 8192 of 151936 384 threads are 4 % faster than 256.
-    // (With more than 1024 entries their tables leave L1 too little for the loads in
-    // flight: 118 us became 128 us.)
+    // more CTAs an SM needs to fill it.  128 threads against 384: 55 us against 75 us for
+    // 2916 rows of 20544 fp16; 192 against 384: 118 us against 138 us for 4096 of 50304
+    // bf16; 256 against 384: 439 us against 460 us for 8192 of 151936 bf16.  The tables
+    // are kept small because the loads in flight live in what shared memory leaves of
+    // L1 (2048 entries for 1024: 128 us for 118 us at 50304 columns).
     a.table_cap = a.seg_slices <= 110 ? 1024 : LP_LOGP_CAP;
     if (a.seg_slices <= 40)
         return touch ? launch_logp_kernel<T, true, 128, 10>(a, s) : launch_logp_kernel<T, false, 128, 10>(a, s);
     if (a.seg_slices <= 110)
         return touch ? launch_logp_kernel<T, true, 192, 7>(a, s) : launch_logp_kernel<T, false, 192, 7>(a, s);
-    return touch ? launch_logp_kernel<T, true, 384, 4>(a, s) : launch_logp_kernel<T, false, 384, 4>(a, s);
+    return touch ? launch_logp_kernel<T, true, 256, 5>(a, s) : launch_logp_kernel<T, false, 256, 5>(a, s);
 }
 
 template <typename T> cudaError_t launch_op(const ProcArgs &a, int op, int out_dtype, int num_sms, cudaStream_t s)
@@ -697,7 +709,7 @@ template <typename T, typename TO, int OP> cudaError_t set_smem_map()
 template <typename T> cudaError_t prepare()
 {
     for (cudaError_t e : {set_smem_map<T, T, LP_WRITE>(), set_smem_map<T, float, LP_WRITE>(), set_smem_map<T, T, LP_GRAD>(),
-                          set_smem(process_logp_kernel<T, true, 192, 7>), set_smem(process_logp_kernel<T, true, 384, 4>)})
+                          set_smem(process_logp_kernel<T, true, 192, 7>), set_smem(process_logp_kernel<T, true, 256, 5>)})
         if (e != cudaSuccess)
             return e;
     return cudaSuccess;

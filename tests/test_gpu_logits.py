@@ -508,6 +508,33 @@ def test_bad_rows_are_reported_and_nan():
     assert torch.isnan(y[2:]).all()
 
 
+def test_checked_build_records_targets_and_gradients():
+    """libtim_debug.so: a target past the vocabulary and a non-finite upstream
+    gradient are recorded, clean calls are not, and the bits are the release build's."""
+    N, V = 3, 1200
+    z, _ = draw_logits(N, V, "f32", 6)
+    t, g = np.array([1, 2, 3], np.int32), np.ones(N, np.float32)
+    R = rules(draw_rules(N, V, 3))
+    ids, tt, tlse = draw_teacher(N, V, 9, 2)
+    lp, lse = tim.processed_logprob(z, R, dev(t))
+    s = tim.distill_topk_step(z, dev(ids), dev(tt), dev(g), teacher_lse=dev(tlse))
+    with tim.checked():
+        lp2, lse2 = tim.processed_logprob(z, R, dev(t))
+        s2 = tim.distill_topk_step(z, dev(ids), dev(tt), dev(g), teacher_lse=dev(tlse))
+        tim.check()
+        assert torch.equal(lp, lp2) and torch.equal(lse, lse2)
+        assert all(torch.equal(s[k], s2[k]) for k in s)
+        tim.processed_logprob(z, R, dev(np.array([1, V, -100], np.int32)))
+        assert tim.tim_debug_violation() == ("target", 1, V)
+        tim.processed_logprob_backward(z, R, dev(t), dev(np.array([1, 1, np.nan], np.float32)), lse)
+        assert tim.tim_debug_violation()[:2] == ("backward_input", 2)
+        tim.distill_topk_step(z, dev(ids), dev(tt), dev(np.array([1, np.inf, 1], np.float32)))
+        assert tim.tim_debug_violation()[:2] == ("backward_input", 1)
+        with pytest.raises(tim.TimError):
+            tim.check()
+    tim.check()
+
+
 def test_wrapper_refusals():
     z = torch.zeros(4, 100, device="cuda")
     t = torch.zeros(4, dtype=torch.int32, device="cuda")
