@@ -603,3 +603,95 @@ def test_example_runs_the_operators_together():
     assert np.isfinite(r["grad_norm"]) and r["grad_norm"] > 0 and r["distill_loss"] > 0
     # no gradient on the prompt's positions
     assert bool((r["kd"]["dlogits"][r["weight"] == 0] == 0).all())
+
+
+# ----------------------------------------------------------------------------- sizes past the usual
+@pytest.mark.parametrize("V", [9001, 70001])
+def test_rows_that_share_a_long_history(V):
+    """More touched columns than a table holds, in rows that share their tokens (the
+    table is built for halves of the columns), in place and not."""
+    N, H = 30, 9000
+    z, z64 = draw_logits(N, V, "bf16", V)
+    rng = np.random.default_rng(V)
+    tok = rng.integers(0, V, H).astype(np.int32)
+    end = np.sort(rng.integers(H // 2, H + 1, N))
+    r = {"history": tok, "history_spans": np.stack([np.zeros(N), end // 3, end], 1).astype(np.int32),
+         "repetition": np.full(N, 1.3, np.float32), "frequency": np.full(N, 0.1, np.float32),
+         "presence": np.full(N, 0.2, np.float32), "temperature": rng.uniform(0.5, 1.5, N).astype(np.float32)}
+    R = rules(r)
+    want, tol = ref.process_ref(z64, r, "bf16")
+    y = tim.process_logits(z, R)
+    assert_close(y, want, tol)
+    t = rng.integers(0, V, N).astype(np.int32)
+    lp, lse = tim.processed_logprob(z, R, dev(t))
+    w, wl, ltol = ref.logprob_ref(z64, r, t)
+    assert_close(lse, wl, ltol)
+    assert_close(lp, w, ltol)
+    g = rng.normal(0, 1, N).astype(np.float32)
+    gw, gtol = ref.backward_ref(z64, r, t, g, lse.cpu().numpy(), "bf16")
+    d = tim.processed_logprob_backward(z, R, dev(t), dev(g), lse)
+    assert_close(d, gw, gtol)
+    z2 = z.clone()
+    assert torch.equal(tim.process_logits(z2, R, out=z2), y)
+    z2 = z.clone()
+    assert torch.equal(tim.processed_logprob_backward(z2, R, dev(t), dev(g), lse, dlogits=z2), d)
+    tim.check()
+
+
+@pytest.mark.parametrize("V", [300001, 1 << 20])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_widest_vocabularies(V, dtype):
+    """Rows wider than a table and than what a cluster's shared memory holds."""
+    N = 2
+    z, z64 = draw_logits(N, V, dtype, 3)
+    r = draw_rules(N, V, 4, hist=500, bias=50)
+    r["allowed_rows"][:] = -1
+    t = np.array([V - 1, 12345], np.int32)
+    R = rules(r)
+    w, wl, tol = ref.logprob_ref(z64, r, t)
+    lp, lse = tim.processed_logprob(z, R, dev(t))
+    assert_close(lp, w, tol)
+    assert_close(lse, wl, tol)
+    want, ptol = ref.process_ref(z64, r, "f32")
+    assert_close(tim.process_logits(z, R, out_dtype=torch.float32), want, ptol)
+    g = np.array([1.0, -0.5], np.float32)
+    gw, gtol = ref.backward_ref(z64, r, t, g, lse.cpu().numpy(), dtype)
+    assert_close(tim.processed_logprob_backward(z, R, dev(t), dev(g), lse), gw, gtol)
+    ids, tt, tlse = draw_teacher(N, V, 300, 7, holes=False)
+    o = tim.distill_topk_step(z, dev(ids), dev(tt), dev(g), teacher_lse=dev(tlse))
+    dw = ref.distill_ref(z64, ids, tt, tlse, 1.0, g, dtype)
+    assert_close(o["loss"], dw["loss"], dw["loss_tol"])
+    assert_close(o["lse_tail"], dw["lse_tail"], dw["lse_tol"])
+    assert_close(o["dlogits"], dw["dlogits"], dw["dlogits_tol"])
+    f = tim.distill_topk(z, dev(ids), dev(tt), dev(tlse))
+    assert torch.equal(f["loss"], o["loss"])
+    b = tim.distill_topk_backward(z, dev(ids), dev(tt), dev(g), f["lse"], f["lse_tail"], teacher_lse=dev(tlse))
+    bw = ref.distill_ref(z64, ids, tt, tlse, 1.0, g, dtype, (f["lse"].cpu().numpy(), f["lse_tail"].cpu().numpy()))
+    assert_close(b, bw["dlogits"], bw["dlogits_tol"])
+    tim.check()
+
+
+def test_offsets_past_32_bits():
+    """3.0e9 logits (6 GB): the last rows have the bits they have alone."""
+    N, V = 20000, 151936
+    z = torch.empty(N, V, dtype=torch.bfloat16, device="cuda")
+    for i in range(0, N, 2000):
+        z[i:i + 2000].normal_(generator=None)
+    last = slice(N - 3, N)
+    t = torch.arange(N, device="cuda", dtype=torch.int32)
+    one = torch.ones(N, device="cuda")
+    tau = one * 0.8
+    lp, lse = tim.processed_logprob(z, tim.LogitsRules(temperature=tau), t)
+    few = tim.LogitsRules(temperature=tau[last])
+    lp3, lse3 = tim.processed_logprob(z[last], few, t[last])
+    assert torch.equal(lp[last], lp3) and torch.equal(lse[last], lse3)
+    out = tim.process_logits(z, tim.LogitsRules(temperature=tau))
+    assert torch.equal(out[last], tim.process_logits(z[last], few))
+    d = tim.processed_logprob_backward(z, tim.LogitsRules(temperature=tau), t, one, lse, dlogits=out)
+    assert torch.equal(d[last], tim.processed_logprob_backward(z[last], few, t[last], one[:3], lse3))
+    ids = (torch.arange(8, device="cuda").repeat(N, 1) * 100 + t.view(-1, 1) % 50).int().contiguous()
+    tl = torch.zeros(N, 8, device="cuda")
+    s = tim.distill_topk_step(z, ids, tl, one, dlogits=out)
+    s3 = tim.distill_topk_step(z[last], ids[last], tl[last], one[:3])
+    assert torch.equal(s["loss"][last], s3["loss"]) and torch.equal(s["dlogits"][last], s3["dlogits"])
+    tim.check()
