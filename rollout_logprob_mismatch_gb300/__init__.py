@@ -413,6 +413,15 @@ def _need_array(t, name, dtype, shape, device):
     return t.data_ptr()
 
 
+def _row_output(t, name, N, device):
+    """An fp32 [N] output and its address: the caller's, checked, or a new one."""
+    if t is not None:
+        return t, _need_array(t, name, _torch()[0].float32, (N,), device)
+    torch = _torch()[0]
+    t = torch.empty(N, dtype=torch.float32, device=device)
+    return t, t.data_ptr()
+
+
 def _launch(function, device, stream, *args):
     """Calls a C entry point on `device` and `stream` (None: the current one)."""
     torch, _, raw = _torch()
@@ -827,9 +836,8 @@ def process_logits(logits, rules, out=None, out_dtype=None, stream=None):
     out may be the logits themselves."""
     head = _need_logits(logits, "logits")
     dev, N, V = logits.device, head[2], head[3]
-    torch = _torch()[0]
     if out is None:
-        out = torch.empty((N, V), dtype=out_dtype or logits.dtype, device=dev)
+        out = _torch()[0].empty((N, V), dtype=out_dtype or logits.dtype, device=dev)
     elif out_dtype is not None and out.dtype != out_dtype:
         raise TypeError("out must have dtype %s, got %s" % (out_dtype, out.dtype))
     address, code, _, _, stride = _need_logits(out, "out", None, dev, (N, V))
@@ -845,14 +853,10 @@ def processed_logprob(logits, rules, targets, out_logp=None, out_lse=None, strea
     head = _need_logits(logits, "logits")
     dev, N, V = logits.device, head[2], head[3]
     torch = _torch()[0]
-    f32 = torch.float32
     t = _need_array(targets, "targets", torch.int32, (N,), dev)
-    if out_logp is None:
-        out_logp = torch.empty(N, dtype=f32, device=dev)
-    if out_lse is None:
-        out_lse = torch.empty(N, dtype=f32, device=dev)
-    _launch(tim_processed_logprob, dev, stream, *head, _rules_struct(rules, N, V, dev), t,
-            _need_array(out_logp, "out_logp", f32, (N,), dev), _need_array(out_lse, "out_lse", f32, (N,), dev))
+    out_logp, logp_ptr = _row_output(out_logp, "out_logp", N, dev)
+    out_lse, lse_ptr = _row_output(out_lse, "out_lse", N, dev)
+    _launch(tim_processed_logprob, dev, stream, *head, _rules_struct(rules, N, V, dev), t, logp_ptr, lse_ptr)
     return out_logp, out_lse
 
 
@@ -891,18 +895,11 @@ def _distill_inputs(logits, teacher_ids, teacher_logits, teacher_lse, temperatur
 
 def _distill_rows(out, N, tail, dev):
     """(dict of the row outputs, their addresses)."""
-    torch = _torch()[0]
-    out = {} if out is None else dict(out)
-    ptrs = []
-    for name in ("loss", "lse", "lse_tail"):
-        if name == "lse_tail" and not tail:
-            out[name] = None
-            ptrs.append(None)
-            continue
-        if out.get(name) is None:
-            out[name] = torch.empty(N, dtype=torch.float32, device=dev)
-        ptrs.append(_need_array(out[name], name, torch.float32, (N,), dev))
-    return out, ptrs
+    given = {} if out is None else out
+    loss, loss_ptr = _row_output(given.get("loss"), "loss", N, dev)
+    lse, lse_ptr = _row_output(given.get("lse"), "lse", N, dev)
+    rest, rest_ptr = _row_output(given.get("lse_tail"), "lse_tail", N, dev) if tail else (None, None)
+    return {**given, "loss": loss, "lse": lse, "lse_tail": rest}, (loss_ptr, lse_ptr, rest_ptr)
 
 
 def distill_topk(logits, teacher_ids, teacher_logits, teacher_lse=None, temperature: float = 1.0, out=None,
