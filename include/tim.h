@@ -446,7 +446,7 @@ typedef struct {
     const int32_t *allowed_rows;
     int64_t allowed_stride;      /* words */
     int32_t num_history;
-    int32_t num_bias;            /* entries of bias_ids and bias_values */
+    int32_t num_bias;            /* entries of bias_ids and bias_values, below 2^30 */
     int32_t num_allowed;
 } tim_logits_rules;
 

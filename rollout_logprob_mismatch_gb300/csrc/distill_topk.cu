@@ -251,6 +251,11 @@ __global__ void __launch_bounds__(NT) distill_kernel(const DistillArgs a)
             mark();
             named_sync(2, NT);
         }
+    } else if constexpr (HOLD) {   // the row's first and last elements, stored plainly
+        if (teacher_warp)
+            named_arrive(1, NT);
+        else
+            named_sync(1, NT);
     }
     // No rank writes a gradient before it has the statistics, so the gathers of z are
     // over by then.
@@ -319,8 +324,8 @@ __global__ void __launch_bounds__(NT) distill_kernel(const DistillArgs a)
                             peer + static_cast<uint32_t>(offsetof(Head, parts)));
             }
         }
-        if (a.ranks == 1 || (GRAD && !TAIL))
-            __syncthreads();
+        if (a.ranks == 1 || (GRAD && !TAIL) || (!GRAD && rank == 0))
+            __syncthreads();   // partials and listed logits, the cleared bitmap
         if (!GRAD && (rank != 0 || warp != 0))
             return;
         if constexpr (GRAD && !TAIL)

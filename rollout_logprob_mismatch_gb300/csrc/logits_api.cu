@@ -66,8 +66,8 @@ int set_rules(tim::ProcArgs &a, const tim_logits_rules *r, int64_t N, int64_t V)
         return TIM_OK;
     if (r->num_history < 0 || r->num_bias < 0 || r->num_allowed < 0)
         return invalid("num_history, num_bias and num_allowed must be >= 0");
-    if (r->num_history >= 1 << 30)
-        return invalid("num_history must be below 2^30");
+    if (r->num_history >= 1 << 30 || r->num_bias >= 1 << 30)
+        return invalid("num_history and num_bias must be below 2^30");
     if (r->history_spans && r->num_history > 0 && !r->history)
         return invalid("history_spans without history");
     if (r->bias_offsets && r->num_bias > 0 && (!r->bias_ids || !r->bias_values))

@@ -207,10 +207,9 @@ template <int NT, typename C> __device__ __forceinline__ void clear_table(Table<
 
 // Builds the cleared table of columns c0 .. c0 + width - 1 with replacement(id, x,
 // slope) for each.  The CTA's first NT threads, which meet at barrier BAR, and the
-// same answer in all: kBad where
-// the row's bias ids are out of range or order, kFull where more columns than the
-// table holds
-// are touched (never for width <= its capacity).  Ends with a barrier.
+// same answer in all: kBad where the row's bias ids are out of range or order, kFull
+// where more columns are touched than the table holds (never for a width up to its
+// capacity).  Ends with a barrier.
 enum TableState { kBuilt, kBad, kFull };
 
 template <int NT, int BAR, typename T, typename C, typename F>
@@ -305,11 +304,10 @@ __device__ TableState build_table(const ProcArgs &a, const RowRules &r, const T 
     }
     named_sync(BAR, NT);
     if (r.b1 > r.b0) {   // the biased ones, by their bias entry
-        scan_ids<NT>(a.bias_ids, r.b0, r.b1, c0, width,
-                 [&](int j, unsigned k) {
-                         const int id = c0 + static_cast<int>(k);
-                         finish(rank_of(t, k), id, Elem<T>::load(z + id), a.bias_values[j]);
-                     });
+        scan_ids<NT>(a.bias_ids, r.b0, r.b1, c0, width, [&](int j, unsigned k) {
+            const int id = c0 + static_cast<int>(k);
+            finish(rank_of(t, k), id, Elem<T>::load(z + id), a.bias_values[j]);
+        });
         named_sync(BAR, NT);
     }
     return kBuilt;

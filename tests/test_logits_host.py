@@ -79,7 +79,7 @@ def test_bad_outputs_and_arrays():
 
 
 @pytest.mark.parametrize("fields", [
-    {"num_history": -1}, {"num_history": 1 << 30}, {"num_bias": -1}, {"num_allowed": -1}, {"history_spans": P, "num_history": 3},
+    {"num_history": -1}, {"num_history": 1 << 30}, {"num_bias": -1}, {"num_bias": 1 << 30}, {"num_allowed": -1}, {"history_spans": P, "num_history": 3},
     {"bias_offsets": P, "num_bias": 2, "bias_ids": P}, {"allowed": P, "allowed_stride": 3, "num_allowed": 4},
     {"allowed": P, "allowed_stride": 4, "num_allowed": 3}, {"allowed_rows": P}, {"temperature": P + 2}])
 def test_bad_rules(fields):
