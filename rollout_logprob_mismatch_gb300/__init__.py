@@ -413,12 +413,22 @@ def _need_array(t, name, dtype, shape, device):
     return t.data_ptr()
 
 
-def _row_output(t, name, N, device):
-    """An fp32 [N] output and its address: the caller's, checked, or a new one."""
-    if t is not None:
-        return t, _need_array(t, name, _torch()[0].float32, (N,), device)
+def _new(shape, dtype, device, stream):
+    """An output buffer in the memory of the stream that will write it (given back
+    while that stream still works on it, it is not handed to another)."""
     torch = _torch()[0]
-    t = torch.empty(N, dtype=torch.float32, device=device)
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _row_output(t, name, N, device, stream):
+    """An fp32 [N] output and its address: the caller's, checked, or a new one."""
+    f32 = _torch()[0].float32
+    if t is not None:
+        return t, _need_array(t, name, f32, (N,), device)
+    t = _new(N, f32, device, stream)
     return t, t.data_ptr()
 
 
@@ -837,7 +847,7 @@ def process_logits(logits, rules, out=None, out_dtype=None, stream=None):
     head = _need_logits(logits, "logits")
     dev, N, V = logits.device, head[2], head[3]
     if out is None:
-        out = _torch()[0].empty((N, V), dtype=out_dtype or logits.dtype, device=dev)
+        out = _new((N, V), out_dtype or logits.dtype, dev, stream)
     elif out_dtype is not None and out.dtype != out_dtype:
         raise TypeError("out must have dtype %s, got %s" % (out_dtype, out.dtype))
     address, code, _, _, stride = _need_logits(out, "out", None, dev, (N, V))
@@ -854,8 +864,8 @@ def processed_logprob(logits, rules, targets, out_logp=None, out_lse=None, strea
     dev, N, V = logits.device, head[2], head[3]
     torch = _torch()[0]
     t = _need_array(targets, "targets", torch.int32, (N,), dev)
-    out_logp, logp_ptr = _row_output(out_logp, "out_logp", N, dev)
-    out_lse, lse_ptr = _row_output(out_lse, "out_lse", N, dev)
+    out_logp, logp_ptr = _row_output(out_logp, "out_logp", N, dev, stream)
+    out_lse, lse_ptr = _row_output(out_lse, "out_lse", N, dev, stream)
     _launch(tim_processed_logprob, dev, stream, *head, _rules_struct(rules, N, V, dev), t, logp_ptr, lse_ptr)
     return out_logp, out_lse
 
@@ -872,7 +882,7 @@ def processed_logprob_backward(logits, rules, targets, grad_logp, lse, dlogits=N
     g = _need_array(grad_logp, "grad_logp", f32, (N,), dev)
     lse_ptr = _need_array(lse, "lse", f32, (N,), dev)
     if dlogits is None:
-        dlogits = torch.empty((N, V), dtype=logits.dtype, device=dev)
+        dlogits = _new((N, V), logits.dtype, dev, stream)
     out = _need_logits(dlogits, "dlogits", logits.dtype, dev, (N, V))
     _launch(tim_processed_logprob_backward, dev, stream, *head, _rules_struct(rules, N, V, dev), t, g, lse_ptr,
             out[0], out[4])
@@ -893,12 +903,12 @@ def _distill_inputs(logits, teacher_ids, teacher_logits, teacher_lse, temperatur
     return (*head, teacher_ids.data_ptr(), t, lse, K, float(temperature)), N, V, dev
 
 
-def _distill_rows(out, N, tail, dev):
+def _distill_rows(out, N, tail, dev, stream):
     """(dict of the row outputs, their addresses)."""
     given = {} if out is None else out
-    loss, loss_ptr = _row_output(given.get("loss"), "loss", N, dev)
-    lse, lse_ptr = _row_output(given.get("lse"), "lse", N, dev)
-    rest, rest_ptr = _row_output(given.get("lse_tail"), "lse_tail", N, dev) if tail else (None, None)
+    loss, loss_ptr = _row_output(given.get("loss"), "loss", N, dev, stream)
+    lse, lse_ptr = _row_output(given.get("lse"), "lse", N, dev, stream)
+    rest, rest_ptr = _row_output(given.get("lse_tail"), "lse_tail", N, dev, stream) if tail else (None, None)
     return {**given, "loss": loss, "lse": lse, "lse_tail": rest}, (loss_ptr, lse_ptr, rest_ptr)
 
 
@@ -910,7 +920,7 @@ def distill_topk(logits, teacher_ids, teacher_logits, teacher_lse=None, temperat
     outside its list is one more outcome.  Returns a dict: loss, lse fp32 [N] and
     lse_tail (fp32 [N] with teacher_lse, else None)."""
     args, N, _, dev = _distill_inputs(logits, teacher_ids, teacher_logits, teacher_lse, temperature)
-    out, rows = _distill_rows(out, N, teacher_lse is not None, dev)
+    out, rows = _distill_rows(out, N, teacher_lse is not None, dev, stream)
     _launch(tim_distill_topk, dev, stream, *args, *rows)
     return out
 
@@ -929,7 +939,7 @@ def distill_topk_backward(logits, teacher_ids, teacher_logits, grad_loss, lse, l
         raise ValueError("lse_tail and teacher_lse go together")
     tail = None if lse_tail is None else _need_array(lse_tail, "lse_tail", f32, (N,), dev)
     if dlogits is None:
-        dlogits = torch.empty((N, V), dtype=logits.dtype, device=dev)
+        dlogits = _new((N, V), logits.dtype, dev, stream)
     out = _need_logits(dlogits, "dlogits", logits.dtype, dev, (N, V))
     _launch(tim_distill_topk_backward, dev, stream, *args, g, lse_ptr, tail, out[0], out[4])
     return dlogits
@@ -943,9 +953,9 @@ def distill_topk_step(logits, teacher_ids, teacher_logits, grad_loss, teacher_ls
     torch = _torch()[0]
     args, N, V, dev = _distill_inputs(logits, teacher_ids, teacher_logits, teacher_lse, temperature)
     g = _need_array(grad_loss, "grad_loss", torch.float32, (N,), dev)
-    out, rows = _distill_rows(out, N, teacher_lse is not None, dev)
+    out, rows = _distill_rows(out, N, teacher_lse is not None, dev, stream)
     if dlogits is None:
-        dlogits = torch.empty((N, V), dtype=logits.dtype, device=dev)
+        dlogits = _new((N, V), logits.dtype, dev, stream)
     d = _need_logits(dlogits, "dlogits", logits.dtype, dev, (N, V))
     out["dlogits"] = dlogits
     _launch(tim_distill_topk_step, dev, stream, *args, g, *rows, d[0], d[4])

@@ -22,7 +22,8 @@ inline int lg_slices(int64_t V) { return static_cast<int>((V + LG_SLICE - 1) / L
 
 // ---------------------------------------------------------------- processing
 constexpr int LP_MAP_THREADS = 256, LP_MAP_CTAS = 6;     // WRITE, GRAD; CTAs of an SM the registers are held to
-constexpr int LP_BUILDERS = 128, LP_SHORT = 12;    // threads that build the table of a segment above LP_SHORT slices
+constexpr int LP_SHORT = 12, LP_LONG = 4096;       // slices up to which, tokens above which all of them build the table
+constexpr int LP_WARPS = 8;                        // warps of a CTA at most
 constexpr int LP_MAP_SLICES = 64;                  // slices of a segment at most
 constexpr int LP_MAP_CAP = 3072, LP_LOGP_CAP = 1536;     // touched columns a table holds (at least LG_SLICE)
 constexpr int LP_HEAVY = 1536, LP_HEAVY_CAP = 5120;      // tokens of history a row, on average; the table then

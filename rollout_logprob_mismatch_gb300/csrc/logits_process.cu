@@ -179,49 +179,49 @@ template <typename C> __device__ __forceinline__ bool is_touched(const Table<C> 
 
 // f(position, id relative to c0) for the entries ids[j0 .. j1) within [c0, c0 + width);
 // four loads at a time, so that a long history does not wait for each.
-template <int NT, typename F>
-__device__ __forceinline__ void scan_ids(const int32_t *ids, int j0, int j1, int c0, int width, F f)
+template <typename F>
+__device__ __forceinline__ void scan_ids(int nt, const int32_t *ids, int j0, int j1, int c0, int width, F f)
 {
-    for (int j = j0 + static_cast<int>(threadIdx.x); j < j1; j += 4 * NT) {
+    for (int j = j0 + static_cast<int>(threadIdx.x); j < j1; j += 4 * nt) {
         unsigned k[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u)
-            k[u] = j + u * NT < j1 ? static_cast<unsigned>(ids[j + u * NT]) - static_cast<unsigned>(c0) : 0xffffffffu;
+            k[u] = j + u * nt < j1 ? static_cast<unsigned>(ids[j + u * nt]) - static_cast<unsigned>(c0) : 0xffffffffu;
 #pragma unroll
         for (int u = 0; u < 4; ++u)
             if (k[u] < static_cast<unsigned>(width))
-                f(j + u * NT, k[u]);
+                f(j + u * nt, k[u]);
     }
 }
 
-// Empties the table for `width` columns: the first NT threads; a barrier before use.
-template <int NT, typename C> __device__ __forceinline__ void clear_table(Table<C> &t, int width)
+// Empties the table for `width` columns: the first nt threads; a barrier before use.
+template <typename C> __device__ __forceinline__ void clear_table(int nt, Table<C> &t, int width)
 {
     const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
     t.groups = (width + 127) / 128;
-    for (int j = threadIdx.x; j < t.groups; j += NT)
+    for (int j = threadIdx.x; j < t.groups; j += nt)
         reinterpret_cast<uint4 *>(t.bitmap)[j] = zero;
     if (threadIdx.x == 0)
         *t.bad = 0;
 }
 
 // Builds the cleared table of columns c0 .. c0 + width - 1 with replacement(id, x,
-// slope) for each.  The CTA's first NT threads, which meet at barrier BAR, and the
-// same answer in all: kBad where the row's bias ids are out of range or order, kFull
+// slope) for each.  The CTA's first nt threads (whole warps), which meet at
+// barrier 1, and the same answer in all: kBad where the row's bias ids are out of range or order, kFull
 // where more columns are touched than the table holds (never for a width up to its
 // capacity).  Ends with a barrier.
 enum TableState { kBuilt, kBad, kFull };
 
-template <int NT, int BAR, typename T, typename C, typename F>
-__device__ TableState build_table(const ProcArgs &a, const RowRules &r, const T *z, int c0, int width, Table<C> &t,
+template <typename T, typename C, typename F>
+__device__ __forceinline__ TableState build_table(int nt, const ProcArgs &a, const RowRules &r, const T *z, int c0, int width, Table<C> &t,
                                   F replacement)
 {
-    __shared__ int warp_bits[NT / 32];
+    __shared__ int warp_bits[LP_WARPS];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     auto mark = [&](int, unsigned k) { atomicOr(t.bitmap + (k >> 5), 1u << (k & 31)); };
-    scan_ids<NT>(a.history, r.h0, r.h1, c0, width, mark);
+    scan_ids(nt, a.history, r.h0, r.h1, c0, width, mark);
     bool bad = false;
-    for (int j = r.b0 + static_cast<int>(threadIdx.x); j < r.b1; j += NT) {
+    for (int j = r.b0 + static_cast<int>(threadIdx.x); j < r.b1; j += nt) {
         const int id = a.bias_ids[j];
         bad |= id < 0 || id >= a.V || (j > r.b0 && a.bias_ids[j - 1] >= id);
         const unsigned k = static_cast<unsigned>(id) - static_cast<unsigned>(c0);
@@ -230,12 +230,12 @@ __device__ TableState build_table(const ProcArgs &a, const RowRules &r, const T 
     }
     if (bad)
         *t.bad = 1;
-    named_sync(BAR, NT);
+    named_sync(1, nt);
     if (*t.bad)
         return kBad;
     // bits before each group of four words: a run of groups per thread
     const uint4 *groups = reinterpret_cast<const uint4 *>(t.bitmap);
-    const int run = (t.groups + NT - 1) / NT;
+    const int run = (t.groups + nt - 1) / nt;
     const int q0 = min(t.groups, static_cast<int>(threadIdx.x) * run), q1 = min(t.groups, q0 + run);
     auto bits_of = [&](int q) {
         const uint4 w = groups[q];
@@ -252,26 +252,27 @@ __device__ TableState build_table(const ProcArgs &a, const RowRules &r, const T 
     }
     if (lane == 31)
         warp_bits[warp] = upto;
-    named_sync(BAR, NT);
+    named_sync(1, nt);
     int base = upto - bits;
     t.used = 0;
 #pragma unroll
-    for (int w = 0; w < NT / 32; ++w) {
-        base += w < warp ? warp_bits[w] : 0;
-        t.used += warp_bits[w];
+    for (int w = 0; w < LP_WARPS; ++w) {
+        const int n = w < nt / 32 ? warp_bits[w] : 0;
+        base += w < warp ? n : 0;
+        t.used += n;
     }
     if (t.used > t.cap) {
-        named_sync(BAR, NT);   // warp_bits is written again
+        named_sync(1, nt);   // warp_bits is written again
         return kFull;
     }
     for (int q = q0; q < q1; ++q) {
         t.before[q] = static_cast<uint16_t>(base);
         base += bits_of(q);
     }
-    for (int n = threadIdx.x; n < t.used; n += NT)
+    for (int n = threadIdx.x; n < t.used; n += nt)
         t.value[n] = 0;
-    named_sync(BAR, NT);
-    scan_ids<NT>(a.history, r.h0, r.h1, c0, width, [&](int j, unsigned k) {
+    named_sync(1, nt);
+    scan_ids(nt, a.history, r.h0, r.h1, c0, width, [&](int j, unsigned k) {
         const int n = rank_of(t, k);
         t.column[n] = static_cast<C>(k);   // the same from every token with this id
         if (j >= r.hg)
@@ -279,12 +280,12 @@ __device__ TableState build_table(const ProcArgs &a, const RowRules &r, const T 
         else
             atomicOr(t.value + n, kPrompt);
     });
-    scan_ids<NT>(a.bias_ids, r.b0, r.b1, c0, width, [&](int, unsigned k) {
+    scan_ids(nt, a.bias_ids, r.b0, r.b1, c0, width, [&](int, unsigned k) {
         const int n = rank_of(t, k);
         t.column[n] = static_cast<C>(k);
         atomicOr(t.value + n, kBiased);
     });
-    named_sync(BAR, NT);
+    named_sync(1, nt);
     auto finish = [&](int n, int id, float logit, float bias) {
         float slope;
         float x = touched_value(r, logit, bias, t.value[n] & ~kBiased, slope);
@@ -292,8 +293,8 @@ __device__ TableState build_table(const ProcArgs &a, const RowRules &r, const T 
             x = neg_inf();
         t.value[n] = __float_as_uint(replacement(id, x, slope));
     };
-    for (int n = threadIdx.x; n < t.used; n += 2 * NT) {
-        const int n1 = n + NT;
+    for (int n = threadIdx.x; n < t.used; n += 2 * nt) {
+        const int n1 = n + nt;
         const bool in0 = !(t.value[n] & kBiased), in1 = n1 < t.used && !(t.value[n1] & kBiased);
         const int id0 = c0 + t.column[n], id1 = in1 ? c0 + t.column[n1] : 0;
         const float z0 = in0 ? Elem<T>::load(z + id0) : 0.f, z1 = in1 ? Elem<T>::load(z + id1) : 0.f;
@@ -302,13 +303,13 @@ __device__ TableState build_table(const ProcArgs &a, const RowRules &r, const T 
         if (in1)
             finish(n1, id1, z1, 0.f);
     }
-    named_sync(BAR, NT);
+    named_sync(1, nt);
     if (r.b1 > r.b0) {   // the biased ones, by their bias entry
-        scan_ids<NT>(a.bias_ids, r.b0, r.b1, c0, width, [&](int j, unsigned k) {
+        scan_ids(nt, a.bias_ids, r.b0, r.b1, c0, width, [&](int j, unsigned k) {
             const int id = c0 + static_cast<int>(k);
             finish(rank_of(t, k), id, Elem<T>::load(z + id), a.bias_values[j]);
         });
-        named_sync(BAR, NT);
+        named_sync(1, nt);
     }
     return kBuilt;
 }
@@ -318,17 +319,18 @@ __device__ __forceinline__ int half(int columns) { return (columns / 2 + LG_SLIC
 
 // ---------------------------------------------------------------- kernels
 // WRITE and GRAD: one CTA per (row, segment); no column depends on another.  Its
-// first NB threads build the table while the others stream the columns (512 at a
+// first nb threads build the table while the others stream the columns (512 at a
 // time, claimed from a counter), then join them; the touched columns go over the
 // streamed ones at the end.  In place the table, which reads the touched logits,
-// comes first.  NB is 128 of the 256 where a segment is long (the stream hides the
-// table: 345 us against 351 us for the gradient of 4096 x 128256 bf16), all 256 where
-// it is short and the table is what takes the time (26 us against 32 us for 64 rows
-// of 128256, histories of some 1000 tokens).
-template <typename T, typename TO, int OP, bool TOUCH, int NB = LP_MAP_THREADS>
+// comes first.  nb is half of the threads where the stream hides the table (345 us
+// against 351 us for the gradient of 4096 x 128256 bf16), all where a segment is short
+// (26 us against 32 us for 64 rows of 128256) or the history long (75 us against 84 us
+// for 400 rows of 100000 with some 1900 tokens each).
+template <typename T, typename TO, int OP, bool TOUCH>
 __global__ void __launch_bounds__(LP_MAP_THREADS, LP_MAP_CTAS) process_map_kernel(const ProcArgs a)
 {
     constexpr int NT = LP_MAP_THREADS, WARPS = NT / 32;
+    static_assert(WARPS <= LP_WARPS);
     extern __shared__ __align__(16) uint32_t smem[];
     __shared__ RowRules r;
     __shared__ HalfMasks masks;
@@ -346,11 +348,12 @@ __global__ void __launch_bounds__(LP_MAP_THREADS, LP_MAP_CTAS) process_map_kerne
         read_rules(a, row, r);
     if (sizeof(TO) == 2 && a.allowed)
         masks.fill();
-    if (TOUCH && threadIdx.x < NB)
-        clear_table<NB>(t, seg1 - seg0);
+    if constexpr (TOUCH)
+        clear_table(NT, t, seg1 - seg0);
     if (threadIdx.x == 0)
         s_next = seg0;
     __syncthreads();
+    const int nb = a.seg_slices <= LP_SHORT || r.h1 - r.h0 > LP_LONG ? NT : NT / 2;
     const float inv_tau = r.inv_tau, gi = r.grad * inv_tau;
     const float lse = r.lse == neg_inf() ? -neg_inf() : r.lse;   // an empty row: every probability is 0
     const uint8_t *const mask = r.mask;
@@ -441,8 +444,8 @@ __global__ void __launch_bounds__(LP_MAP_THREADS, LP_MAP_CTAS) process_map_kerne
         bool streamed = a.in_place == 0;   // the whole segment, along with the first table
         for (int c0 = seg0, c1, width = seg1 - seg0; c0 < seg1;) {
             c1 = min(seg1, c0 + width);
-            if (threadIdx.x < NB) {
-                const TableState state = build_table<NB, 1>(a, r, z, c0, c1 - c0, t, [&](int id, float x, float slope) {
+            if (threadIdx.x < nb) {
+                const TableState state = build_table(nb, a, r, z, c0, c1 - c0, t, [&](int id, float x, float slope) {
                     const float y = x / r.tau;
                     if constexpr (OP == LP_GRAD)
                         return y == neg_inf() ? 0.f
@@ -481,8 +484,8 @@ __global__ void __launch_bounds__(LP_MAP_THREADS, LP_MAP_CTAS) process_map_kerne
             }
             if (c0 < seg1) {
                 __syncthreads();   // the table has been read
-                if (threadIdx.x < NB)
-                    clear_table<NB>(t, min(seg1, c0 + width) - c0);
+                if (threadIdx.x < nb)
+                    clear_table(nb, t, min(seg1, c0 + width) - c0);
                 if (threadIdx.x == 0 && !streamed)
                     s_next = c0;
                 __syncthreads();
@@ -518,7 +521,7 @@ __global__ void __launch_bounds__(NT, CTAS) process_logp_kernel(const ProcArgs a
     if (sizeof(T) == 2 && (TOUCH || a.allowed))
         masks.fill();
     if constexpr (TOUCH)
-        clear_table<NT>(t, min(LP_TABLE, min(a.V, s1 * LG_SLICE) - s0 * LG_SLICE));
+        clear_table(NT, t, min(LP_TABLE, min(a.V, s1 * LG_SLICE) - s0 * LG_SLICE));
     __syncthreads();
     bool bad = r.bad;
     const float inv_tau = r.inv_tau, k2 = LG_LOG2E * inv_tau;
@@ -534,10 +537,10 @@ __global__ void __launch_bounds__(NT, CTAS) process_logp_kernel(const ProcArgs a
         if constexpr (TOUCH) {
             if (f0 != s0 || step != LP_TABLE / LG_SLICE) {
                 __syncthreads();   // the table before has been read
-                clear_table<NT>(t, c1 - c0);
+                clear_table(NT, t, c1 - c0);
                 __syncthreads();
             }
-            const TableState state = build_table<NT, 1>(a, r, z, c0, c1 - c0, t, [](int, float x, float) { return x; });
+            const TableState state = build_table(NT, a, r, z, c0, c1 - c0, t, [](int, float x, float) { return x; });
             bad = state == kBad;
             if (bad)
                 break;
@@ -631,16 +634,13 @@ template <typename T, typename TO, int OP> cudaError_t launch_map(ProcArgs a, in
     a.segs = (slices + a.seg_slices - 1) / a.seg_slices;
     a.table_columns = a.seg_slices * LG_SLICE;
     // Rows with long histories of their own (on average: rows that share theirs count
-    // little) touch more columns than the usual table holds, and the table is what takes
-    // the time.
+    // little) touch more columns than the usual table holds.
     const bool heavy = a.history_len / LP_HEAVY >= a.N;
     a.table_cap = heavy ? LP_HEAVY_CAP : LP_MAP_CAP;
     const unsigned grid = static_cast<unsigned>(a.N) * static_cast<unsigned>(a.segs);
-    const size_t bytes = table_bytes<uint16_t>(a.table_columns, a.table_cap);
-    if (touch && a.seg_slices > LP_SHORT && !heavy)
-        process_map_kernel<T, TO, OP, true, LP_BUILDERS><<<grid, LP_MAP_THREADS, bytes, s>>>(a);
-    else if (touch)
-        process_map_kernel<T, TO, OP, true><<<grid, LP_MAP_THREADS, bytes, s>>>(a);
+    if (touch)
+        process_map_kernel<T, TO, OP, true>
+            <<<grid, LP_MAP_THREADS, table_bytes<uint16_t>(a.table_columns, a.table_cap), s>>>(a);
     else
         process_map_kernel<T, TO, OP, false><<<grid, LP_MAP_THREADS, 0, s>>>(a);
     return cudaGetLastError();
@@ -698,15 +698,10 @@ template <typename T> cudaError_t launch_op(const ProcArgs &a, int op, int out_d
     return launch_map<T, T, LP_WRITE>(a, num_sms, s);
 }
 
-template <typename T, typename TO, int OP> cudaError_t set_smem_map()
-{
-    const cudaError_t e = set_smem(process_map_kernel<T, TO, OP, true>);
-    return e != cudaSuccess ? e : set_smem(process_map_kernel<T, TO, OP, true, LP_BUILDERS>);
-}
-
 template <typename T> cudaError_t prepare()
 {
-    for (cudaError_t e : {set_smem_map<T, T, LP_WRITE>(), set_smem_map<T, float, LP_WRITE>(), set_smem_map<T, T, LP_GRAD>(),
+    for (cudaError_t e : {set_smem(process_map_kernel<T, T, LP_WRITE, true>), set_smem(process_map_kernel<T, float, LP_WRITE, true>),
+                          set_smem(process_map_kernel<T, T, LP_GRAD, true>),
                           set_smem(process_logp_kernel<T, true, 192, 7>), set_smem(process_logp_kernel<T, true, 256, 5>)})
         if (e != cudaSuccess)
             return e;

@@ -695,3 +695,23 @@ def test_offsets_past_32_bits():
     s3 = tim.distill_topk_step(z[last], ids[last], tl[last], one[:3])
     assert torch.equal(s["loss"][last], s3["loss"]) and torch.equal(s["dlogits"][last], s3["dlogits"])
     tim.check()
+
+
+def test_outputs_given_to_a_stream_stay_its_own():
+    """Outputs that a call allocates for another stream come from that stream's memory:
+    dropping them at once does not let the current stream write over them early."""
+    V, N = 151936, 64
+    z = torch.randn(N, V, device="cuda")
+    want = tim.process_logits(z, None)
+    t = torch.zeros(N, dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for _ in range(20):
+        y = tim.process_logits(z, None, stream=side)
+        keep = [tim.processed_logprob(z, None, t, stream=side)[1] for _ in range(2)]
+        del keep
+        junk = torch.full((N, V), 7.0, device="cuda")     # would take a freed block of the current stream
+        side.synchronize()
+        assert torch.equal(y, want)
+        del junk, y
+    tim.check()
