@@ -200,8 +200,13 @@ __global__ void __launch_bounds__(NT) distill_kernel(const DistillArgs a)
                 mbar_arrive_expect_tx(smem_u32(&hd.parts), static_cast<uint32_t>(slices) * 16 + 16);
         }
     }
-    if constexpr (HOLD)
+    if constexpr (HOLD) {
+        // rank 0's last warp passes no other barrier before it waits for the row:
+        // barrier 3 brings it the abort word as it was set above
+        if (rank == 0 && warp == 0)
+            named_arrive(3, 64);
         fetch_row<NT>(z, c0, c1, shift, smem + lay.row, smem_u32(&hd.bar));
+    }
     if (SUMS && a.ranks > 1)
         cluster_arrive_relaxed();   // waited for before the first store into another CTA's shared memory
 
@@ -260,6 +265,9 @@ __global__ void __launch_bounds__(NT) distill_kernel(const DistillArgs a)
     // No rank writes a gradient before it has the statistics, so the gathers of z are
     // over by then.
     TeacherRow tr{0.f, 0.f, 0.f, 0};
+    if constexpr (HOLD)
+        if (teacher_warp)
+            named_sync(3, 64);
     if (teacher_warp || (!SUMS && warp == WARPS - 1)) {
         tr = teacher_row<T, TAIL>(a, row, lane, z, SUMS ? listed_x : nullptr);
         if (lane == 0 && (!SUMS || a.ranks == 1))
