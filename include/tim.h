@@ -512,8 +512,11 @@ TIM_API int tim_distill_topk(const void *logits, int dtype, int64_t N, int64_t V
 
 /* Its gradient for an upstream g_i = dL / dloss_i, from the forward's lse and (with
  * teacher_lse) lse_tail: dlogits_iv = g_i (p_v - q_v) / temperature for listed ids, and
- * with teacher_lse g_i p_v (1 - q_o / p_o) / temperature for the others.  dlogits as in
- * tim_processed_logprob_backward; a row with g = 0 is zeros. */
+ * with teacher_lse g_i (p_v - q_o r_v) / temperature for the others, r_v = p_v / p_o =
+ * e^(z_v / temperature - lse_tail), which is finite however small p_o is.  A fp32
+ * lse_tail of large size says r_v to |lse_tail| 2^-24 in its exponent only (the step
+ * below has no such limit).  dlogits as in tim_processed_logprob_backward; a row with
+ * g = 0 is zeros. */
 TIM_API int tim_distill_topk_backward(const void *logits, int dtype, int64_t N, int64_t V, int64_t stride,
                                       const int32_t *teacher_ids, const float *teacher_logits,
                                       const float *teacher_lse, int64_t K, float temperature,

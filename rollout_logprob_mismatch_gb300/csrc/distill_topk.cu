@@ -10,7 +10,8 @@
 //                              the ids not listed, p_o = 1 - sum p_k:
 //                              L = sum_k q_k (log q_k - log p_k) + q_o (log q_o - log p_o),
 //                              dL/dz_v = (p_v - q_v) / tau for the listed ids and
-//                              p_v (1 - q_o / p_o) / tau for the others.
+//                              p_v (1 - q_o / p_o) / tau = (p_o - q_o) r_v / tau for the
+//                              others, r_v = p_v / p_o (computed as a softmax of its own).
 // (q_v is 0 for ids that are not listed; an id listed twice adds up.)  log p_o is the
 // log-sum-exp over the columns whose bit is not set in a bitmap of the listed
 // ids, never 1 - sum p_k, which loses all its digits when p_o is small.
@@ -408,24 +409,35 @@ __global__ void __launch_bounds__(NT) distill_kernel(const DistillArgs a)
             return;
         }
         // p_v = 2^((z_v first - ref) second) scale: the row's maximum and 1 / sum in a
-        // step, the forward's lse in a backward call
+        // step, the forward's lse in a backward call.  The ids that are not listed have
+        // (p_o - q_o) r_v, r_v = 2^((z_v first - rest_ref) second) rest_scale <= 1 the
+        // student's distribution over them alone: p_v (1 - q_o / p_o) without a quotient
+        // that overflows when p_o is small.
         const TeacherRow w = hd.teacher;
         const float gi = g / tau;
         const float first = SUMS ? 1.f : inv_tau, second = SUMS ? k2 : LG_LOG2E;
-        float ref, scale = 1.f, others = w.any ? 1.f : 0.f;   // factor of p_v for ids that are not listed
+        float ref, scale = 1.f, rest_ref, others;   // others: what multiplies 2^(..) of the ids that are not listed
         if constexpr (SUMS) {
-            ref = finite_ref(hd.m);
+            ref = rest_ref = finite_ref(hd.m);
             scale = hd.s == 0.f ? 0.f : 1.f / hd.s;
-            if constexpr (TAIL)
-                others = hd.sr == 0.f ? 0.f : 1.f - w.rest / (hd.sr * exp2_approx((hd.mr - ref) * k2) * scale);
+            others = w.any ? scale : 0.f;
+            if constexpr (TAIL) {
+                rest_ref = finite_ref(hd.mr);
+                others = hd.sr == 0.f ? 0.f : (hd.sr * exp2_approx((hd.mr - ref) * k2) * scale - w.rest) / hd.sr;
+            }
         } else {
             ref = a.lse[row];
-            if constexpr (TAIL) {
-                const float lt = a.lse_tail[row];
-                others = lt == neg_inf() ? 0.f : 1.f - w.rest * expf(ref - lt);
-            }
+            const float lse = ref;
             if (ref == neg_inf())
                 ref = -neg_inf();
+            rest_ref = ref;
+            others = w.any ? 1.f : 0.f;
+            if constexpr (TAIL) {
+                rest_ref = a.lse_tail[row];
+                others = rest_ref == neg_inf() ? 0.f : expf(rest_ref - lse) - w.rest;
+                if (rest_ref == neg_inf())
+                    rest_ref = -neg_inf();
+            }
         }
         // the listed ids' values first: z may be written over in place
         constexpr int KPT = (LD_MAX_K + NT - 1) / NT;
@@ -451,8 +463,8 @@ __global__ void __launch_bounds__(NT) distill_kernel(const DistillArgs a)
         }
         if constexpr (!HOLD)
             __syncthreads();
-        const float wgi = others * gi * scale;
-        const Pair first2 = pair(first, first), ref2 = pair(-ref, -ref), second2 = pair(second, second),
+        const float wgi = others * gi;
+        const Pair first2 = pair(first, first), ref2 = pair(-rest_ref, -rest_ref), second2 = pair(second, second),
                    w2 = pair(wgi, wgi);
         for (int b = c0 + warp * 512; b < c1; b += WARPS * 512) {
             Raw8<T> raw[2];
@@ -464,6 +476,10 @@ __global__ void __launch_bounds__(NT) distill_kernel(const DistillArgs a)
                 for (int k = 0; k < 4; ++k) {
                     float lo, hi;
                     unpair(mul2(fma2(get2<T>(raw[u], k), first2, ref2), second2), lo, hi);
+                    if constexpr (!SUMS && TAIL) {   // r_v <= 1, whatever lse_tail's rounding makes of it
+                        lo = fmin_nan(lo, 0.f);
+                        hi = fmin_nan(hi, 0.f);
+                    }
                     unpair(mul2(pair(exp2_approx(lo), exp2_approx(hi)), w2), v[2 * k], v[2 * k + 1]);
                 }
                 store8<T>(dz, b + u * 256 + lane * 8, c1, shift_out, pack8<T>(v));

@@ -34,6 +34,13 @@ __device__ __forceinline__ float exp2_approx(float x)   // 2 ulp; 2^-inf = 0, 2^
     return y;
 }
 
+__device__ __forceinline__ float fmin_nan(float x, float y)   // NaN if either is
+{
+    float m;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(x), "f"(y));
+    return m;
+}
+
 // ---------------------------------------------------------------- element types
 template <typename T> struct Elem;
 

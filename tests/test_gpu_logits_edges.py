@@ -31,3 +31,148 @@ def test_step_on_clusters_records_no_timeout(dtype, tail):
         for k in ("loss", "lse", "dlogits"):
             assert torch.equal(again[k], first[k]), k
     tim.check()
+
+
+# ----------------------------------------------------------------------------- distillation in fp64
+U = 2.0 ** -24
+HALF = {"f32": 2.0 ** -24, "bf16": 2.0 ** -8, "f16": 2.0 ** -11}
+
+
+def lse_of(x):
+    """log sum e^x whose gradient keeps log(size) at values that swallow it, in fp64 too."""
+    m = x.max().detach()
+    return m + torch.logsumexp(x - m, 0) if bool(torch.isfinite(m)) else torch.logsumexp(x, 0)
+
+
+def distill64(z, ids, t, tlse, tau, g=None):
+    """(loss [N], its gradient [N, V] by automatic differentiation, lse, lse_tail) in
+    fp64, from the loss's definition; q_o counts as 0 where no unlisted id is left and
+    the rounding of tlse explains it; a row whose list carries nothing has loss 0."""
+    N, V = z.shape
+    x = torch.from_numpy(z / tau).double().requires_grad_(True)
+    loss, lse, lt = [], np.empty(N), np.empty(N)
+    for i in range(N):
+        on = (ids[i] >= 0) & (ids[i] < V)
+        cols = torch.from_numpy(ids[i][on].astype(np.int64))
+        tt = torch.from_numpy(t[i][on].astype(np.float64) / tau)
+        listed = torch.zeros(V, dtype=torch.bool)
+        listed[cols] = True
+        L = lse_of(x[i])
+        rest = x[i][~listed]
+        R = lse_of(rest) if rest.numel() else torch.tensor(-np.inf)
+        lse[i], lt[i] = float(L.detach()), float(R.detach())
+        if tlse is None:
+            logq = tt - torch.logsumexp(tt, 0) if (tt > -np.inf).any() else torch.full_like(tt, -np.inf)
+        else:
+            logq = tt - float(tlse[i])
+        q = torch.exp(logq)
+        some = q > 0
+        total = torch.sum(q[some] * (logq[some] - (x[i][cols[some]] - L))) if some.any() else x[i, 0] * 0
+        if tlse is not None:
+            qo = max(0.0, 1.0 - float(q.sum()))
+            if lt[i] == -np.inf and qo <= 2.0 ** -22 * (16 + abs(float(tlse[i]))):
+                qo = 0.0
+            if qo > 0:
+                total = total + qo * (np.log(qo) - (R - L))
+        loss.append(total)
+    loss = torch.stack(loss)
+    grad = None
+    if g is not None:
+        (grad,) = torch.autograd.grad((loss * torch.from_numpy(g).double()).sum(), x)
+        grad = grad.numpy() / tau
+    return loss.detach().numpy(), grad, lse, lt
+
+
+def far_tolerance(z, ids, t, tlse, tau, g, dtype, lse, lt, from_lse):
+    """What the gradient may be off by.  Listed ids: p and q as in logits_ref.  The
+    others are p_o r - q_o r, r = e^(y - lse_tail) <= 1 the student's distribution over
+    them: r's exponent carries 8 u of its terms (their spread in a step, the terms
+    themselves where lse_tail is given in fp32), p_o = e^(lse_tail - lse) and q_o their own."""
+    N, V = z.shape
+    tol = np.empty((N, V))
+    y = z / tau
+    for i in range(N):
+        on = (ids[i] >= 0) & (ids[i] < V)
+        logq = t[i][on].astype(np.float64) / tau - float(tlse[i])
+        q = np.exp(logq)
+        qo = max(0.0, 1.0 - q.sum())
+        T = np.abs(logq).max() + abs(float(tlse[i]))
+        listed = np.zeros(V, bool)
+        listed[ids[i][on]] = True
+        qv = np.zeros(V)
+        np.add.at(qv, ids[i][on], q)
+        p = np.exp(y[i] - lse[i])
+        near = U * (8 * (np.abs(y[i][listed]).max() + abs(lse[i])) + 96)
+        po = np.exp(lt[i] - lse[i])
+        top = y[i][~listed].max()
+        r = np.exp(y[i] - top, where=~listed, out=np.zeros(V))
+        r /= r.sum()
+        spread = np.abs(y[i]) + abs(lt[i]) if from_lse else np.abs(y[i] - top)
+        with np.errstate(over="ignore"):
+            dr = np.minimum(1.0, r * np.expm1(np.minimum(700.0, U * (8 * spread + 96))))
+            dpo = min(1.0, po * np.expm1(min(700.0, U * (8 * (abs(lt[i]) + abs(lse[i])) + 96))))
+        qerr = q.sum() * U * (8 * T + 32) + 8 * U
+        rest = (po + qo) * dr + (r + dr) * (dpo + qerr)
+        tol[i] = np.where(listed, p * near + qv * U * (8 * T + 32) + 2 * U * (p + qv), rest)
+    return tol * np.abs(g)[:, None] / tau
+
+
+# ----------------------------------------------------------------------------- a small p_o
+@pytest.mark.parametrize("tau", [1.0, 0.125])
+@pytest.mark.parametrize("dtype,gap", [("f32", 20.0), ("f32", 100.0), ("f32", 1e4), ("f32", None), ("bf16", 100.0),
+                                       ("bf16", None), ("f16", 1e4), ("f16", None)])
+@pytest.mark.parametrize("V", [300, 5001, 40001])
+def test_tail_gradient_of_students_that_all_but_rule_out_the_rest(V, dtype, gap, tau):
+    """Unlisted logits far below the listed ones (gap None: the type's lowest value, as
+    an additive mask writes it): p_o is small or 0 in fp32, and the others' gradient
+    g (p_v - q_o e^(z_v / tau - lse_tail)) / tau stays finite and right, with a teacher
+    that has a rest and one that has none."""
+    N, K = 4, 12
+    rng = np.random.default_rng(V)
+    z, _ = draw_logits(N, V, dtype, V + 1, std=1.0)
+    ids = np.stack([rng.choice(V, K, replace=False) for _ in range(N)]).astype(np.int32)
+    on = torch.zeros(N, V, dtype=torch.bool, device="cuda").scatter_(1, dev(ids).long(), True)
+    if gap is None:
+        z = torch.where(on, z, torch.full_like(z, torch.finfo(z.dtype).min))
+    else:
+        z = torch.where(on, z, z - gap)
+    z64 = z.double().cpu().numpy()
+    t = rng.normal(0, 1, (N, K)).astype(np.float32)
+    mass = np.log(np.exp(t.astype(np.float64) / tau).sum(1))
+    rest = np.array([0.25, 1e-3, 0.0, 0.0])
+    tlse = (mass - np.log1p(-rest) - np.array([0, 0, 1e-3, 1e-3])).astype(np.float32)   # rows 2, 3: sum q above 1
+    g = np.array([1.0, -0.5, 2.0, 1.0], np.float32)
+    with np.errstate(over="ignore", invalid="ignore"):
+        loss, grad, lse, lt = distill64(z64, ids, t, tlse, tau, g)
+        # a step knows sum q_k only as 1 where no rest is left: its listed term is p_v - q_v
+        sumq = np.exp(t.astype(np.float64) / tau - tlse.astype(np.float64)[:, None]).sum(1)
+        over = np.maximum(sumq - 1.0, 0.0)
+        p = np.exp(z64 / tau - lse[:, None])
+        grad = grad - (g * over / tau)[:, None] * p
+        tol = far_tolerance(z64, ids, t, tlse, tau, g, dtype, lse, lt, False)
+    least = 2.0 ** -25 if dtype == "f16" else 2.0 ** -126        # half of fp16's smallest step
+    tol = tol + HALF[dtype] * np.abs(grad) + least
+    args, tl = (dev(ids), dev(t)), dev(tlse)
+    s = tim.distill_topk_step(z, *args, dev(g), teacher_lse=tl, temperature=tau)
+    f = tim.distill_topk(z, *args, teacher_lse=tl, temperature=tau)
+    b = tim.distill_topk_backward(z, *args, dev(g), f["lse"], f["lse_tail"], teacher_lse=tl, temperature=tau)
+    tim.check()
+    d = s["dlogits"].double().cpu().numpy()
+    assert np.isfinite(d).all(), "step"
+    assert (np.abs(d - grad) <= tol).all(), ("step", (np.abs(d - grad) - tol).max())
+    with np.errstate(over="ignore", invalid="ignore"):
+        tol = far_tolerance(z64, ids, t, tlse, tau, g, dtype, lse, lt, True)
+    tol = tol + HALF[dtype] * np.abs(grad) + least
+    d = b.double().cpu().numpy()
+    assert np.isfinite(d).all(), "backward"
+    assert (np.abs(d - grad) <= tol).all(), ("backward", (np.abs(d - grad) - tol).max())
+    assert torch.equal(s["loss"], f["loss"])
+    if np.abs(lt).max() < 3e38:                       # (else z / tau itself passes fp32's range)
+        q = np.exp(t.astype(np.float64) / tau - tlse.astype(np.float64)[:, None])
+        T = np.abs(t / tau).max() + 2 * np.abs(tlse).max()
+        Y = np.abs(z64[on.cpu().numpy()]).max() / tau
+        qo = np.maximum(0.0, 1.0 - q.sum(1))
+        d = np.log(np.maximum(qo, 2.0 ** -24)) - (lt - lse)
+        qerr = (q.sum(1) * U * (8 * T + 32) + 8 * U) * (qo > 0)
+        ltol = U * (8 * (T + Y) + 200) * (30 + np.abs(loss)) + qerr * (np.abs(d) + 1)
+        assert (np.abs(s["loss"].double().cpu().numpy() - loss) <= ltol).all()
