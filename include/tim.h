@@ -492,8 +492,8 @@ TIM_API int tim_processed_logprob_backward(const void *logits, int dtype, int64_
  *                      distributions is one more outcome, q_o = max(0, 1 - sum_k q_k)
  *                      and p_o = the probability of the ids not listed:
  *                      loss = sum_k q_k (log q_k - log p_k) + q_o (log q_o - log p_o).
- * Terms with q = 0 are 0.  With teacher_lse NULL a row that lists nothing has loss 0
- * and gradient 0.
+ * Terms with q = 0 are 0.  With teacher_lse NULL a row that lists nothing, or only
+ * ids with a teacher logit of -inf, has loss 0 and gradient 0.
  *   logits, dtype, N, V, stride   as above
  *   teacher_ids     int32 [N, K], 1 <= K <= 1024; an id outside [0, V) is an empty
  *                   entry, an id listed twice adds up

@@ -42,7 +42,7 @@ struct TeacherRow {
     float max;    // largest t_k (0 for a tail: not used)
     float lse;    // log sum e^((t_k - max) / tau), or the given one
     float rest;   // q_o (0 without a tail)
-    int any;      // the row lists something
+    int any;      // the row lists something (without a tail: of a probability above 0)
 };
 
 // Shared memory of a CTA: the header, the slices' partials, the student's z at the
@@ -402,7 +402,8 @@ __global__ void __launch_bounds__(NT) distill_kernel(const DistillArgs a)
     }
 
     if constexpr (GRAD) {
-        if (SUMS && g == 0.f) {
+        // (a row whose list carries nothing has the constant loss 0)
+        if ((SUMS && g == 0.f) || (!TAIL && !hd.teacher.any)) {
             zero_row();
             if (SUMS && rank == 0 && warp == WARPS - 1)
                 write_loss();
@@ -420,7 +421,7 @@ __global__ void __launch_bounds__(NT) distill_kernel(const DistillArgs a)
         if constexpr (SUMS) {
             ref = rest_ref = finite_ref(hd.m);
             scale = hd.s == 0.f ? 0.f : 1.f / hd.s;
-            others = w.any ? scale : 0.f;
+            others = scale;
             if constexpr (TAIL) {
                 rest_ref = finite_ref(hd.mr);
                 others = hd.sr == 0.f ? 0.f : (hd.sr * exp2_approx((hd.mr - ref) * k2) * scale - w.rest) / hd.sr;
@@ -431,7 +432,7 @@ __global__ void __launch_bounds__(NT) distill_kernel(const DistillArgs a)
             if (ref == neg_inf())
                 ref = -neg_inf();
             rest_ref = ref;
-            others = w.any ? 1.f : 0.f;
+            others = 1.f;
             if constexpr (TAIL) {
                 rest_ref = a.lse_tail[row];
                 others = rest_ref == neg_inf() ? 0.f : expf(rest_ref - lse) - w.rest;

@@ -176,3 +176,42 @@ def test_tail_gradient_of_students_that_all_but_rule_out_the_rest(V, dtype, gap,
         qerr = (q.sum(1) * U * (8 * T + 32) + 8 * U) * (qo > 0)
         ltol = U * (8 * (T + Y) + 200) * (30 + np.abs(loss)) + qerr * (np.abs(d) + 1)
         assert (np.abs(s["loss"].double().cpu().numpy() - loss) <= ltol).all()
+
+
+# ----------------------------------------------------------------------------- lists that carry nothing
+@pytest.mark.parametrize("V,K", [(7, 3), (3000, 40), (40001, 64)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_rows_whose_listed_logits_are_all_minus_infinity(V, K, dtype):
+    """Valid ids with the teacher's logits all -inf (a list padded with an id and -inf)
+    and no teacher_lse: the loss is 0 whatever the student says, and so is its gradient,
+    also where the student has an infinity or a NaN."""
+    N = 5
+    z, _ = draw_logits(N, V, dtype, V)
+    rng = np.random.default_rng(V)
+    ids = np.stack([rng.choice(V, K, replace=False) for _ in range(N)]).astype(np.int32)
+    t = rng.normal(0, 1, (N, K)).astype(np.float32)
+    t[1] = -np.inf
+    ids[2], t[2] = 0, -np.inf            # padding alone: id 0 and -inf, K times
+    t[3, 1:] = -np.inf                   # one that carries all
+    t[4], ids[4, :] = -np.inf, -1        # an empty list
+    z[1, 0] = float("nan")
+    z[4, 1] = float("inf")
+    g = np.ones(N, np.float32)
+    use = [0, 3]
+    z64 = z.double().cpu().numpy()
+    loss, grad, lse, _ = distill64(z64[use], ids[use], t[use], None, 1.0, g[use])
+    args = (dev(ids), dev(t))
+    s = tim.distill_topk_step(z, *args, dev(g))
+    f = tim.distill_topk(z, *args)
+    b = tim.distill_topk_backward(z, *args, dev(g), f["lse"])
+    z2, z3 = z.clone(), z.clone()
+    tim.distill_topk_step(z2, *args, dev(g), dlogits=z2)
+    tim.distill_topk_backward(z3, *args, dev(g), f["lse"], dlogits=z3)
+    tim.check()
+    for name, d in (("step", s["dlogits"]), ("backward", b), ("step in place", z2), ("backward in place", z3)):
+        assert bool((d[[1, 2, 4]] == 0).all()), name
+        got = d[use].double().cpu().numpy()
+        tol = U * (16 * np.abs(z64[use]).max() + 200) + HALF[dtype] * np.abs(grad) + 2.0 ** -126
+        assert (np.abs(got - grad) <= tol).all(), name
+    assert bool((s["loss"][[1, 2, 4]] == 0).all()) and torch.equal(s["loss"], f["loss"])
+    assert (np.abs(s["loss"][use].double().cpu().numpy() - loss) <= U * (16 * np.abs(z64[use]).max() + 200) + U * 16 * (1 + np.abs(loss))).all()
