@@ -492,6 +492,9 @@ TIM_API int tim_processed_logprob_backward(const void *logits, int dtype, int64_
  *                      distributions is one more outcome, q_o = max(0, 1 - sum_k q_k)
  *                      and p_o = the probability of the ids not listed:
  *                      loss = sum_k q_k (log q_k - log p_k) + q_o (log q_o - log p_o).
+ *                      Where the student gives the ids not listed nothing (p_o = 0 in fp32,
+ *                      or none is left), a q_o of at most 2^-22 (16 + |teacher_lse|), which
+ *                      teacher_lse's rounding can leave, counts as 0, in the gradient too.
  * Terms with q = 0 are 0.  With teacher_lse NULL a row that lists nothing, or only
  * ids with a teacher logit of -inf, has loss 0 and gradient 0.
  *   logits, dtype, N, V, stride   as above

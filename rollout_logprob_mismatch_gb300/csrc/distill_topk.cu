@@ -50,7 +50,8 @@ struct TeacherRow {
 // with a tail), the rank's part of the row.
 struct Head {
     uint64_t bar, parts;   // the row's copy; the partials and the teacher's statistics
-    int dup, abort, pad[2];
+    int dup, abort;
+    float p_o, q_o;       // a tail in a call with sums: the student's rest, the teacher's that counts
     TeacherRow teacher;
     float m, s, mr, sr;   // all columns; those that are not listed
 };
@@ -87,6 +88,16 @@ template <bool TAIL> __device__ __forceinline__ float listed_logq(float t, float
 }
 
 __device__ __forceinline__ float q_of(float logq) { return logq == neg_inf() ? 0.f : expf(logq); }
+
+// The q_o that counts.  Where the student gives the rest nothing (p_o = 0 in fp32: a
+// list that holds every id, or a grammar both are under), what the rounding of the
+// teacher's lse and of sum q_k can leave of 1 - sum q_k is 0: four roundings of the
+// lse, 64 of the sum.  log p_o = -inf would make an infinite loss of it.
+__device__ __forceinline__ float counted_rest(const TeacherRow &w, float p_o)
+{
+    const float noise = fminf(0.5f, 0x1p-22f * (16.f + fabsf(w.lse)));
+    return p_o == 0.f && w.rest <= noise ? 0.f : w.rest;
+}
 
 __device__ __forceinline__ bool in_use(int id, int V) { return id >= 0 && id < V; }
 
@@ -367,6 +378,10 @@ __global__ void __launch_bounds__(NT) distill_kernel(const DistillArgs a)
                 hd.s = lost ? quiet_nan() : s;
                 hd.mr = mr;
                 hd.sr = sr;
+                if constexpr (TAIL) {
+                    hd.p_o = sr == 0.f ? 0.f : sr * exp2_approx((mr - finite_ref(m)) * k2) / hd.s;
+                    hd.q_o = counted_rest(hd.teacher, hd.p_o);
+                }
             }
             __syncwarp();
         }
@@ -385,10 +400,12 @@ __global__ void __launch_bounds__(NT) distill_kernel(const DistillArgs a)
                     loss = __fmaf_rn(q, lq - row_logp(listed_x[k], m, s, inv_tau), loss);
             }
         loss = warp_sum(loss);
-        if constexpr (TAIL)
-            if (tr.rest != 0.f)
-                loss = __fmaf_rn(tr.rest,
-                                 logf(tr.rest) - (sr == 0.f ? neg_inf() : __fmaf_rn(mr - m, inv_tau, logf(sr) - logf(s))), loss);
+        if constexpr (TAIL) {
+            const float rest = hd.q_o;
+            if (rest != 0.f)
+                loss = __fmaf_rn(rest,
+                                 logf(rest) - (sr == 0.f ? neg_inf() : __fmaf_rn(mr - m, inv_tau, logf(sr) - logf(s))), loss);
+        }
         if (lane == 0) {
             a.loss[row] = loss;
             a.out_lse[row] = row_lse(m, s, inv_tau);
@@ -424,7 +441,7 @@ __global__ void __launch_bounds__(NT) distill_kernel(const DistillArgs a)
             others = scale;
             if constexpr (TAIL) {
                 rest_ref = finite_ref(hd.mr);
-                others = hd.sr == 0.f ? 0.f : (hd.sr * exp2_approx((hd.mr - ref) * k2) * scale - w.rest) / hd.sr;
+                others = hd.sr == 0.f ? 0.f : (hd.p_o - hd.q_o) / hd.sr;
             }
         } else {
             ref = a.lse[row];
@@ -435,7 +452,8 @@ __global__ void __launch_bounds__(NT) distill_kernel(const DistillArgs a)
             others = 1.f;
             if constexpr (TAIL) {
                 rest_ref = a.lse_tail[row];
-                others = rest_ref == neg_inf() ? 0.f : expf(rest_ref - lse) - w.rest;
+                const float p_o = exp2_approx((rest_ref - lse) * LG_LOG2E);
+                others = rest_ref == neg_inf() ? 0.f : p_o - counted_rest(w, p_o);
                 if (rest_ref == neg_inf())
                     rest_ref = -neg_inf();
             }

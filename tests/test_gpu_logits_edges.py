@@ -46,7 +46,7 @@ def lse_of(x):
 
 def distill64(z, ids, t, tlse, tau, g=None):
     """(loss [N], its gradient [N, V] by automatic differentiation, lse, lse_tail) in
-    fp64, from the loss's definition; q_o counts as 0 where no unlisted id is left and
+    fp64, from the loss's definition; q_o counts as 0 where p_o is 0 in fp32 and
     the rounding of tlse explains it; a row whose list carries nothing has loss 0."""
     N, V = z.shape
     x = torch.from_numpy(z / tau).double().requires_grad_(True)
@@ -70,7 +70,7 @@ def distill64(z, ids, t, tlse, tau, g=None):
         total = torch.sum(q[some] * (logq[some] - (x[i][cols[some]] - L))) if some.any() else x[i, 0] * 0
         if tlse is not None:
             qo = max(0.0, 1.0 - float(q.sum()))
-            if lt[i] == -np.inf and qo <= 2.0 ** -22 * (16 + abs(float(tlse[i]))):
+            if lt[i] - lse[i] < -126 * np.log(2.0) and qo <= 2.0 ** -22 * (16 + abs(float(tlse[i]))):
                 qo = 0.0
             if qo > 0:
                 total = total + qo * (np.log(qo) - (R - L))
@@ -215,3 +215,49 @@ def test_rows_whose_listed_logits_are_all_minus_infinity(V, K, dtype):
         assert (np.abs(got - grad) <= tol).all(), name
     assert bool((s["loss"][[1, 2, 4]] == 0).all()) and torch.equal(s["loss"], f["loss"])
     assert (np.abs(s["loss"][use].double().cpu().numpy() - loss) <= U * (16 * np.abs(z64[use]).max() + 200) + U * 16 * (1 + np.abs(loss))).all()
+
+
+# ----------------------------------------------------------------------------- nothing unlisted is left
+@pytest.mark.parametrize("kind,low", [("covering", -np.inf), ("same grammar", -np.inf), ("same grammar, wide", -np.inf),
+                                      ("same grammar", -1e4), ("same grammar", -3.4028234663852886e38)])
+def test_no_infinite_loss_from_the_rounding_of_teacher_lse(kind, low):
+    """A list that holds every id the student gives anything: 1 - sum q_k is what the
+    rounding of teacher_lse leaves, some 1e-7, and no outcome.  A q_o that the rounding
+    does not explain, on ids the student rules out, makes the loss +inf as it should."""
+    N = 400
+    V, K = {"covering": (24, 24), "same grammar": (2000, 24), "same grammar, wide": (151936, 300)}[kind]
+    z, _ = draw_logits(N, V, "f32", 5)
+    rng = np.random.default_rng(K)
+    ids = np.stack([rng.choice(V, K, replace=False) for _ in range(N)]).astype(np.int32)
+    on = torch.zeros(N, V, dtype=torch.bool, device="cuda").scatter_(1, dev(ids).long(), True)
+    z = z.masked_fill(~on, low)
+    t = rng.normal(0, 3, (N, K)).astype(np.float32)
+    exact = np.log(np.exp(t.astype(np.float64)).sum(1))
+    tlse = exact.astype(np.float32)
+    tlse[:8] = (exact[:8] + 0.01).astype(np.float32)     # one percent on what the student rules out
+    g = np.ones(N, np.float32)
+    zl = z.gather(1, dev(ids).long()).double().cpu().numpy()
+    where = np.tile(np.arange(K, dtype=np.int32), (N, 1))
+    loss, grad, lse, _ = distill64(zl, where, t, tlse, 1.0, g)      # the listed columns are the whole row
+    assert (loss[:8] == np.inf).all() and np.isfinite(loss[8:]).all()
+    far = np.inf if low == -np.inf else 0.009 * -low      # what the first rows' one percent costs, at least
+    tl = dev(tlse)
+    s = tim.distill_topk_step(z, dev(ids), dev(t), dev(g), teacher_lse=tl)
+    f = tim.distill_topk(z, dev(ids), dev(t), teacher_lse=tl)
+    tim.check()
+    assert torch.equal(s["loss"], f["loss"]) and bool((s["lse_tail"] < low + 8).all() or low < -1e30)
+    b = tim.distill_topk_backward(z, dev(ids), dev(t), dev(g), f["lse"], f["lse_tail"], teacher_lse=tl)
+    tim.check()
+    got = s["loss"].double().cpu().numpy()
+    assert (got[:8] >= far).all()
+    assert np.isfinite(got[8:]).all(), int((~np.isfinite(got[8:])).sum())
+    logq = t.astype(np.float64) - tlse.astype(np.float64)[:, None]
+    weighed = (np.exp(logq) * np.abs(logq - (zl - lse[:, None]))).sum(1)
+    tol = U * (8 * (np.abs(zl).max() + np.abs(t).max() + 2 * np.abs(tlse).max()) + 200) * (2 + weighed[8:])
+    assert (np.abs(got[8:] - loss[8:]) <= tol).all()
+    # p_v - q_v: the fp64 gradient scales p by sum q_k, which the rounding of tlse keeps near 1
+    dtol = U * (16 * (np.abs(zl).max() + np.abs(tlse).max()) + 200)
+    for d in (s["dlogits"], b):
+        at = d.gather(1, dev(ids).long()).double().cpu().numpy()
+        assert (np.abs(at - grad)[8:] <= dtol).all()
+        assert bool((d.masked_fill(on, 0)[8:] == 0).all()) and bool(torch.isfinite(d).all())
