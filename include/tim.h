@@ -465,7 +465,9 @@ TIM_API int tim_process_logits(const void *logits, int dtype, int64_t N, int64_t
  * written: l_i = y_{i, a_i} - lse_i, lse_i = log sum_v e^{y_iv}, all in fp32.
  *   targets   int32 [N]; an id outside [0, V) gives out_logp = NaN
  *   out_logp  fp32 [N]; -inf where y_{i, a_i} = -inf
- *   out_lse   fp32 [N]; -inf for a row with nothing left (its out_logp is -inf too)
+ *   out_lse   fp32 [N]; -inf for a row with nothing left (its out_logp is -inf too), and
+ *             for one whose every y lies below fp32's range (out_logp, which is taken
+ *             from differences, is finite then; the gradient takes the row as empty)
  * A NaN or +inf among the allowed logits makes a row's outputs NaN.  A row's bits do
  * not depend on the batch. */
 TIM_API int tim_processed_logprob(const void *logits, int dtype, int64_t N, int64_t V, int64_t stride,
@@ -475,7 +477,10 @@ TIM_API int tim_processed_logprob(const void *logits, int dtype, int64_t N, int6
 /* Its gradient: dlogits_iv = g_i (1[v = a_i] - e^{y_iv - lse_i}) dy_iv / dz_iv, which is
  * 0 where y_iv = -inf, rounded once to the logits' type.
  *   grad_logp  fp32 [N]: g; a row with g = 0 is written as zeros without being read
- *   lse        fp32 [N]: the forward's out_lse
+ *   lse        fp32 [N]: the forward's out_lse.  Its rounding is in e^(y - lse): the
+ *              probability carries |lse| 2^-24 in its exponent and is at most 1, so a
+ *              row of additive masks' values (-1e9 and below) has a bounded gradient of
+ *              few true digits
  *   dlogits    [N, V] of type dtype; may be the logits themselves, else no overlap
  * A target outside [0, V) takes no one-hot term. */
 TIM_API int tim_processed_logprob_backward(const void *logits, int dtype, int64_t N, int64_t V, int64_t stride,

@@ -452,7 +452,7 @@ __global__ void __launch_bounds__(NT) distill_kernel(const DistillArgs a)
             others = 1.f;
             if constexpr (TAIL) {
                 rest_ref = a.lse_tail[row];
-                const float p_o = exp2_approx((rest_ref - lse) * LG_LOG2E);
+                const float p_o = prob2((rest_ref - lse) * LG_LOG2E);
                 others = rest_ref == neg_inf() ? 0.f : p_o - counted_rest(w, p_o);
                 if (rest_ref == neg_inf())
                     rest_ref = -neg_inf();
@@ -476,7 +476,8 @@ __global__ void __launch_bounds__(NT) distill_kernel(const DistillArgs a)
                 } else {
                     q = q_of(listed_logq<TAIL>(n == 0 ? t0 : teacher[k], tau, w));
                 }
-                const float p = exp2_approx(fmaf(Elem<T>::load(src + id - off), first, -ref) * second) * scale;
+                const float e = fmaf(Elem<T>::load(src + id - off), first, -ref) * second;
+                const float p = SUMS ? exp2_approx(e) * scale : prob2(e);
                 own[n] = (p - q) * gi;
             }
         }
@@ -495,11 +496,8 @@ __global__ void __launch_bounds__(NT) distill_kernel(const DistillArgs a)
                 for (int k = 0; k < 4; ++k) {
                     float lo, hi;
                     unpair(mul2(fma2(get2<T>(raw[u], k), first2, ref2), second2), lo, hi);
-                    if constexpr (!SUMS && TAIL) {   // r_v <= 1, whatever lse_tail's rounding makes of it
-                        lo = fmin_nan(lo, 0.f);
-                        hi = fmin_nan(hi, 0.f);
-                    }
-                    unpair(mul2(pair(exp2_approx(lo), exp2_approx(hi)), w2), v[2 * k], v[2 * k + 1]);
+                    const Pair p = SUMS ? pair(exp2_approx(lo), exp2_approx(hi)) : pair(prob2(lo), prob2(hi));
+                    unpair(mul2(p, w2), v[2 * k], v[2 * k + 1]);
                 }
                 store8<T>(dz, b + u * 256 + lane * 8, c1, shift_out, pack8<T>(v));
             }

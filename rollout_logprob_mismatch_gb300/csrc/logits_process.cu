@@ -399,7 +399,7 @@ __global__ void __launch_bounds__(LP_MAP_THREADS, LP_MAP_CTAS) process_map_kerne
                 } else {
                     float lo, hi;
                     unpair(mul2(fma2(x, inv2, lse2), e2), lo, hi);
-                    unpair(mul2(pair(exp2_approx(lo), exp2_approx(hi)), g2), v[2 * k], v[2 * k + 1]);
+                    unpair(mul2(pair(prob2(lo), prob2(hi)), g2), v[2 * k], v[2 * k + 1]);
                 }
             }
             Raw8<TO> o = pack8<TO>(v);
@@ -427,7 +427,7 @@ __global__ void __launch_bounds__(LP_MAP_THREADS, LP_MAP_CTAS) process_map_kerne
     if (target_mine) {
         const float x = Elem<T>::load(z + target);
         target_v = is_allowed(mask, target) && x != neg_inf()
-                       ? (1.f - exp2_approx(fmaf(x, inv_tau, -lse) * LG_LOG2E)) * gi
+                       ? (1.f - prob2(fmaf(x, inv_tau, -lse) * LG_LOG2E)) * gi
                        : 0.f;
     }
     if constexpr (!TOUCH) {
@@ -449,7 +449,7 @@ __global__ void __launch_bounds__(LP_MAP_THREADS, LP_MAP_CTAS) process_map_kerne
                     const float y = x / r.tau;
                     if constexpr (OP == LP_GRAD)
                         return y == neg_inf() ? 0.f
-                                              : ((id == target ? 1.f : 0.f) - exp2_approx((y - lse) * LG_LOG2E)) *
+                                              : ((id == target ? 1.f : 0.f) - prob2((y - lse) * LG_LOG2E)) *
                                                     (r.grad * (slope / r.tau));
                     else
                         return y;

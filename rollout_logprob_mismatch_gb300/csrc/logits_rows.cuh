@@ -41,6 +41,11 @@ __device__ __forceinline__ float fmin_nan(float x, float y)   // NaN if either i
     return m;
 }
 
+// 2^x of a probability from a rounded log-sum-exp: at most 1.  (Where |lse| passes
+// some 1e6, as in a row of an additive mask's values, its rounding alone is more than
+// the logarithm of any vocabulary, and 2^x without the limit may be 1e28.)
+__device__ __forceinline__ float prob2(float x) { return exp2_approx(fmin_nan(x, 0.f)); }
+
 // ---------------------------------------------------------------- element types
 template <typename T> struct Elem;
 

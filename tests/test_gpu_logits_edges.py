@@ -261,3 +261,42 @@ def test_no_infinite_loss_from_the_rounding_of_teacher_lse(kind, low):
         at = d.gather(1, dev(ids).long()).double().cpu().numpy()
         assert (np.abs(at - grad)[8:] <= dtol).all()
         assert bool((d.masked_fill(on, 0)[8:] == 0).all()) and bool(torch.isfinite(d).all())
+
+
+# ----------------------------------------------------------------------------- probabilities from a rounded lse
+@pytest.mark.parametrize("tau", [0.7, 1.0, 1.3, 3.0])
+@pytest.mark.parametrize("dtype,low", [("f32", -1e9), ("f32", None), ("bf16", -1e9), ("bf16", None), ("f16", None)])
+def test_gradients_of_rows_at_the_lowest_values_stay_bounded(dtype, low, tau):
+    """Rows whose every logit is an additive mask's value: lse's rounding in fp32 is
+    larger than log V, so e^(y - lse) says little there, but it is a probability: a
+    gradient is at most |g| times its slope."""
+    N, V = 5, 3001
+    low = torch.finfo({"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}[dtype]).min if low is None else low
+    z, _ = draw_logits(N, V, dtype, 2)
+    z[1:] = low
+    z[2, 7] = low / 2
+    z[4, 9] = float("nan")
+    hist = np.array([3, 4, 5, 5], np.int32)
+    r = tim.LogitsRules(temperature=dev(np.full(N, tau, np.float32)), repetition=dev(np.full(N, 1.0, np.float32)),
+                        history=dev(hist), history_spans=dev(np.tile([0, 1, 4], (N, 1)).astype(np.int32)))
+    for R in (r, tim.LogitsRules(temperature=r.temperature)):
+        for target in (5, 100):
+            a = dev(np.full(N, target, np.int32))
+            lp, lse = tim.processed_logprob(z, R, a)
+            g = np.linspace(1, 2, N).astype(np.float32)
+            d = tim.processed_logprob_backward(z, R, a, dev(g), lse).double().cpu().numpy()
+            limit = g / tau * (1 + 2 * HALF[dtype])
+            assert np.isfinite(d[:4]).all() and (np.abs(d[:4]).max(1) <= limit[:4]).all(), np.abs(d[:4]).max(1)
+            # (a column whose y is -inf has gradient 0, in a row that holds a NaN too)
+            some = torch.isfinite(tim.process_logits(z, R, out_dtype=torch.float32)[4]).cpu().numpy()
+            assert np.isnan(d[4][some]).all() and torch.isnan(lse[4])
+    ids = np.tile(np.array([1, 2, 3, 4, 5, 6, 7, 8], np.int32), (N, 1))
+    t = np.random.default_rng(1).normal(0, 1, ids.shape).astype(np.float32)
+    tlse = (np.log(np.exp(t.astype(np.float64) / tau).sum(1)) + 0.1).astype(np.float32)
+    for tl in (None, dev(tlse)):
+        f = tim.distill_topk(z, dev(ids), dev(t), teacher_lse=tl, temperature=tau)
+        b = tim.distill_topk_backward(z, dev(ids), dev(t), dev(g), f["lse"], f["lse_tail"], teacher_lse=tl, temperature=tau)
+        d = b.double().cpu().numpy()
+        assert np.isfinite(d[:4]).all() and (np.abs(d[:4]).max(1) <= limit[:4]).all(), np.abs(d[:4]).max(1)
+        assert np.isnan(d[4]).all()
+    tim.check()
