@@ -50,8 +50,7 @@ struct TeacherRow {
 // with a tail), the rank's part of the row.
 struct Head {
     uint64_t bar, parts;   // the row's copy; the partials and the teacher's statistics
-    int dup, abort;
-    float p_o, q_o;       // a tail in a call with sums: the student's rest, the teacher's that counts
+    int dup, abort, pad[2];
     TeacherRow teacher;
     float m, s, mr, sr;   // all columns; those that are not listed
 };
@@ -89,7 +88,8 @@ template <bool TAIL> __device__ __forceinline__ float listed_logq(float t, float
 
 __device__ __forceinline__ float q_of(float logq) { return logq == neg_inf() ? 0.f : expf(logq); }
 
-// The q_o that counts.  Where the student gives the rest nothing (p_o = 0 in fp32: a
+// The q_o that counts.  Where the student gives the rest nothing (p_o = 0 in fp32, or
+// the rest's largest probability relative to the row's: a
 // list that holds every id, or a grammar both are under), what the rounding of the
 // teacher's lse and of sum q_k can leave of 1 - sum q_k is 0: four roundings of the
 // lse, 64 of the sum.  log p_o = -inf would make an infinite loss of it.
@@ -378,10 +378,6 @@ __global__ void __launch_bounds__(NT) distill_kernel(const DistillArgs a)
                 hd.s = lost ? quiet_nan() : s;
                 hd.mr = mr;
                 hd.sr = sr;
-                if constexpr (TAIL) {
-                    hd.p_o = sr == 0.f ? 0.f : sr * exp2_approx((mr - finite_ref(m)) * k2) / hd.s;
-                    hd.q_o = counted_rest(hd.teacher, hd.p_o);
-                }
             }
             __syncwarp();
         }
@@ -401,7 +397,7 @@ __global__ void __launch_bounds__(NT) distill_kernel(const DistillArgs a)
             }
         loss = warp_sum(loss);
         if constexpr (TAIL) {
-            const float rest = hd.q_o;
+            const float rest = counted_rest(tr, sr == 0.f ? 0.f : exp2_approx((mr - m) * k2));
             if (rest != 0.f)
                 loss = __fmaf_rn(rest,
                                  logf(rest) - (sr == 0.f ? neg_inf() : __fmaf_rn(mr - m, inv_tau, logf(sr) - logf(s))), loss);
@@ -441,7 +437,8 @@ __global__ void __launch_bounds__(NT) distill_kernel(const DistillArgs a)
             others = scale;
             if constexpr (TAIL) {
                 rest_ref = finite_ref(hd.mr);
-                others = hd.sr == 0.f ? 0.f : (hd.p_o - hd.q_o) / hd.sr;
+                const float p_o = hd.sr * exp2_approx((hd.mr - ref) * k2) * scale;
+                others = hd.sr == 0.f ? 0.f : (p_o - counted_rest(w, p_o)) / hd.sr;
             }
         } else {
             ref = a.lse[row];
