@@ -450,7 +450,10 @@ typedef struct {
     int32_t num_allowed;
 } tim_logits_rules;
 
-/* The processed logits, y above, rounded once to the output's type.
+/* The processed logits, y above, in fp32 and rounded once to the output's type.  The
+ * division by the temperature is off by 1/2 + 2^-19 units of fp32's last place (1.5 for
+ * 16-bit outputs, before their rounding), by the same operation in every column: a
+ * column whose rules change nothing has the bits of one without rules.
  *   logits   [N, V] of type dtype, rows `stride` elements apart (>= V), aligned to
  *            its elements (16-byte-aligned rows are the fast case)
  *   N, V     0 <= N < 2^31, 0 < V <= 2^20, N * ceil(V / 1024) < 2^31

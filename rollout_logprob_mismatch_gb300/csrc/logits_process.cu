@@ -326,6 +326,11 @@ __device__ __forceinline__ int half(int columns) { return (columns / 2 + LG_SLIC
 // against 351 us for the gradient of 4096 x 128256 bf16), all where a segment is short
 // (26 us against 32 us for 64 rows of 128256) or the history long (75 us against 84 us
 // for 400 rows of 100000 with some 1900 tokens each).
+//
+// A column's x / tau is the same operation whether the column is touched or not, so that
+// equal logits stay equal: for fp32 outputs the corrected quotient, for 16-bit ones the
+// product with the rounded reciprocal, whose 1.5 units of fp32's last place are nothing
+// beside the output's rounding (with the quotient 2048 x 151936 bf16 took 202 us, not 197).
 template <typename T, typename TO, int OP, bool TOUCH>
 __global__ void __launch_bounds__(LP_MAP_THREADS, LP_MAP_CTAS) process_map_kernel(const ProcArgs a)
 {
@@ -377,7 +382,7 @@ __global__ void __launch_bounds__(LP_MAP_THREADS, LP_MAP_CTAS) process_map_kerne
             report_bad_input(a.status);
         return;
     }
-    const Pair inv2 = pair(inv_tau, inv_tau), lse2 = pair(-lse, -lse), e2 = pair(LG_LOG2E, LG_LOG2E), g2 = pair(-gi, -gi);
+    const Pair inv2 = pair(inv_tau, inv_tau), tau2 = pair(-r.tau, -r.tau), lse2 = pair(-lse, -lse), e2 = pair(LG_LOG2E, LG_LOG2E), g2 = pair(-gi, -gi);
     auto chunks = [&](int b, int end) {   // columns b .. b + 511
         Raw8<T> raw[2];
         uint32_t drop[2] = {0u, 0u};
@@ -395,7 +400,10 @@ __global__ void __launch_bounds__(LP_MAP_THREADS, LP_MAP_CTAS) process_map_kerne
             for (int k = 0; k < 4; ++k) {
                 const Pair x = get2<T>(raw[u], k);
                 if constexpr (OP == LP_WRITE) {
-                    unpair(mul2(x, inv2), v[2 * k], v[2 * k + 1]);
+                    if constexpr (sizeof(TO) == 4)
+                        quotient2(x, tau2, inv2, v[2 * k], v[2 * k + 1]);
+                    else
+                        unpair(mul2(x, inv2), v[2 * k], v[2 * k + 1]);
                 } else {
                     float lo, hi;
                     unpair(mul2(fma2(x, inv2, lse2), e2), lo, hi);
@@ -446,7 +454,7 @@ __global__ void __launch_bounds__(LP_MAP_THREADS, LP_MAP_CTAS) process_map_kerne
             c1 = min(seg1, c0 + width);
             if (threadIdx.x < nb) {
                 const TableState state = build_table(nb, a, r, z, c0, c1 - c0, t, [&](int id, float x, float slope) {
-                    const float y = x / r.tau;
+                    const float y = sizeof(TO) == 4 || OP == LP_GRAD ? quotient(x, r.tau, inv_tau) : __fmul_rn(x, inv_tau);
                     if constexpr (OP == LP_GRAD)
                         return y == neg_inf() ? 0.f
                                               : ((id == target ? 1.f : 0.f) - prob2((y - lse) * LG_LOG2E)) *

@@ -334,6 +334,25 @@ __device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c)
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(p) : "l"(a), "l"(b), "l"(c));
     return p;
 }
+
+// x / tau by the rounded reciprocal and one residual step: q = x inv, q + (x - q tau) inv.
+// q is off by up to 1.5 units in the last place, the step by that times 2^-24 before its
+// own rounding, so x / tau is off by (1/2 + 2^-20) of one.  An infinite or NaN q stays as it is.
+__device__ __forceinline__ float quotient(float x, float tau, float inv)
+{
+    const float q = __fmul_rn(x, inv);
+    const float better = __fmaf_rn(__fmaf_rn(-q, tau, x), inv, q);
+    return fabsf(q) < INFINITY ? better : q;
+}
+__device__ __forceinline__ void quotient2(Pair x, Pair minus_tau, Pair inv, float &lo, float &hi)   // two, the same bits
+{
+    const Pair q = mul2(x, inv);
+    float q0, q1;
+    unpair(q, q0, q1);
+    unpair(fma2(fma2(q, minus_tau, x), inv, q), lo, hi);
+    lo = fabsf(q0) < INFINITY ? lo : q0;
+    hi = fabsf(q1) < INFINITY ? hi : q1;
+}
 template <typename T> __device__ __forceinline__ Pair get2(const Raw8<T> &r, int k)   // columns 2k, 2k + 1
 {
     return pair(Elem<T>::get(r.w, 2 * k), Elem<T>::get(r.w, 2 * k + 1));

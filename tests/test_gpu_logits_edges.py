@@ -300,3 +300,39 @@ def test_gradients_of_rows_at_the_lowest_values_stay_bounded(dtype, low, tau):
         assert np.isfinite(d[:4]).all() and (np.abs(d[:4]).max(1) <= limit[:4]).all(), np.abs(d[:4]).max(1)
         assert np.isnan(d[4]).all()
     tim.check()
+
+
+# ----------------------------------------------------------------------------- one quotient for all columns
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_processed_logits_are_one_rounding_from_the_quotient(dtype):
+    """Without penalties y = z / temperature is off by half a unit in the last place of
+    fp32 (and 2^-20 of one: the quotient's correction), and a column that is in the
+    history with neutral parameters has the bits of one that is not."""
+    N, V = 64, 4099
+    z, z64 = draw_logits(N, V, dtype, 12, std=4.0)
+    rng = np.random.default_rng(8)
+    tau = rng.uniform(0.3, 2.5, N).astype(np.float32)
+    z[:, 0], z[:, 1], z[:, 2], z[:, 3] = float("inf"), -float("inf"), 0.0, torch.finfo(z.dtype).min
+    z64 = z.double().cpu().numpy()
+    one = dev(np.ones(N, np.float32))
+    R = tim.LogitsRules(temperature=dev(tau))
+    y = tim.process_logits(z, R, out_dtype=torch.float32)
+    hist = dev(np.arange(0, V, 2, dtype=np.int32))
+    spans = dev(np.tile([0, hist.shape[0] // 2, hist.shape[0]], (N, 1)).astype(np.int32))
+    neutral = tim.LogitsRules(temperature=dev(tau), repetition=one, presence=one * 0, frequency=one * 0, history=hist,
+                              history_spans=spans)
+    assert torch.equal(tim.process_logits(z, neutral, out_dtype=torch.float32), y)
+    if dtype != "f32":
+        assert torch.equal(tim.process_logits(z, neutral), tim.process_logits(z, R))
+    tim.check()
+    want = z64 / tau[:, None].astype(np.float64)
+    got = y.double().cpu().numpy()
+    inside = np.abs(want) < 3.4e38
+    with np.errstate(over="ignore"):
+        want32 = want.astype(np.float32)
+    ulp = np.spacing(np.abs(want32)).astype(np.float64)
+    off = np.abs(np.where(inside, got, 0.0) - np.where(inside, want, 0.0))
+    assert (off[inside] <= 0.5 * (1 + 2.0 ** -19) * ulp[inside]).all(), (off[inside] / ulp[inside]).max()
+    assert (got[:, 0] == np.inf).all() and (got[:, 1] == -np.inf).all()
+    past = np.abs(want) > 3.41e38
+    assert (got[past] == want32[past]).all()
