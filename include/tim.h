@@ -459,7 +459,8 @@ typedef struct {
  *   N, V     0 <= N < 2^31, 0 < V <= 2^20, N * ceil(V / 1024) < 2^31
  *   rules    host struct above; NULL: no rule
  *   out      [N, V] of type out_dtype (dtype, or TIM_F32), rows out_stride apart;
- *            may be the logits themselves (same type and stride), else no overlap */
+ *            may be the logits themselves (same type and stride), else no shared element
+ *            (rows of equal stride in bytes may lie between each other) */
 TIM_API int tim_process_logits(const void *logits, int dtype, int64_t N, int64_t V, int64_t stride,
                                const tim_logits_rules *rules, void *out, int out_dtype, int64_t out_stride,
                                tim_stream_t stream);

@@ -39,6 +39,20 @@ int check_logits(const void *logits, int dtype, int64_t N, int64_t V, int64_t st
     return TIM_OK;
 }
 
+// Do N rows of `size` bytes each, `step` bytes apart, share a byte with rows of `size2`
+// bytes, `step2` apart?  Exact for equal steps (two parts of one buffer's rows, side by
+// side); else the whole ranges are compared.
+bool share_bytes(uintptr_t a, uintptr_t step, uintptr_t size, uintptr_t b, uintptr_t step2, uintptr_t size2, int64_t N)
+{
+    const uintptr_t last = static_cast<uintptr_t>(N - 1);
+    if (a + last * step + size <= b || b + last * step2 + size2 <= a)
+        return false;
+    if (N == 1 || step != step2)
+        return true;
+    const uintptr_t at = b >= a ? (b - a) % step : (step - (a - b) % step) % step;   // a row of b within a row of a
+    return at < size || at + size2 > step;
+}
+
 // An output of the logits' shape: not null, aligned, and either apart from the
 // logits or exactly over them.
 int check_out(const void *logits, int dtype, int64_t N, int64_t V, int64_t stride, const void *out, int out_dtype,
@@ -52,10 +66,9 @@ int check_out(const void *logits, int dtype, int64_t N, int64_t V, int64_t strid
         return invalid("the output must be aligned to its elements");
     if (out == logits && out_dtype == dtype && (out_stride == stride || N == 1))
         return TIM_OK;
-    const uintptr_t a0 = reinterpret_cast<uintptr_t>(logits), b0 = reinterpret_cast<uintptr_t>(out);
-    const uintptr_t a1 = a0 + static_cast<uintptr_t>((N - 1) * stride + V) * elem_bytes(dtype);
-    const uintptr_t b1 = b0 + static_cast<uintptr_t>((N - 1) * out_stride + V) * elem_bytes(out_dtype);
-    if (a0 < b1 && b0 < a1)
+    const uintptr_t es = elem_bytes(dtype), eo = elem_bytes(out_dtype);
+    if (share_bytes(reinterpret_cast<uintptr_t>(logits), stride * es, V * es, reinterpret_cast<uintptr_t>(out),
+                    out_stride * eo, V * eo, N))
         return invalid("the output overlaps the logits without being the logits");
     return TIM_OK;
 }

@@ -336,3 +336,33 @@ def test_processed_logits_are_one_rounding_from_the_quotient(dtype):
     assert (got[:, 0] == np.inf).all() and (got[:, 1] == -np.inf).all()
     past = np.abs(want) > 3.41e38
     assert (got[past] == want32[past]).all()
+
+
+# ----------------------------------------------------------------------------- interleaved rows
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_outputs_between_the_rows_of_the_logits(dtype):
+    """Logits and output as the halves of one [N, 2, V] buffer: no element is shared, so
+    the call runs; halves that share a column are refused."""
+    N, V = 9, 1003
+    DT = {"f32": torch.float32, "bf16": torch.bfloat16}[dtype]
+    buf = torch.zeros(N, 2, V, dtype=DT, device="cuda")
+    z, _ = draw_logits(N, V, dtype, 3)
+    buf[:, 0] = z
+    R = tim.LogitsRules(temperature=dev(np.full(N, 0.8, np.float32)))
+    t = dev(np.arange(N, dtype=np.int32))
+    g = dev(np.ones(N, np.float32))
+    want = tim.process_logits(z, R)
+    tim.process_logits(buf[:, 0], R, out=buf[:, 1])
+    assert torch.equal(buf[:, 1], want) and torch.equal(buf[:, 0], z)
+    lse = tim.processed_logprob(z, R, t)[1]
+    tim.processed_logprob_backward(buf[:, 0], R, t, g, lse, dlogits=buf[:, 1])
+    assert torch.equal(buf[:, 1], tim.processed_logprob_backward(z, R, t, g, lse)) and torch.equal(buf[:, 0], z)
+    buf[:, 1] = z
+    tim.process_logits(buf[:, 1], R, out=buf[:, 0])      # the output before the logits
+    assert torch.equal(buf[:, 0], want) and torch.equal(buf[:, 1], z)
+    flat = torch.zeros(N, 2 * V, dtype=DT, device="cuda")
+    for a, b in ((flat[:, :V], flat[:, V - 1:2 * V - 1]), (flat[:, V:], flat[:, 1:V + 1]),
+                 (flat[1:, :V], flat.view(-1)[V:V + (N - 1) * 2 * V].view(N - 1, 2 * V)[:, 1:V + 1])):
+        with pytest.raises(tim.TimError):
+            tim.process_logits(a, R if a.shape[0] == N else None, out=b)
+    tim.check()
