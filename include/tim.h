@@ -456,7 +456,7 @@ typedef struct {
  * column whose rules change nothing has the bits of one without rules.
  *   logits   [N, V] of type dtype, rows `stride` elements apart (>= V), aligned to
  *            its elements (16-byte-aligned rows are the fast case)
- *   N, V     0 <= N < 2^31, 0 < V <= 2^20, N * ceil(V / 1024) < 2^31
+ *   N, V     0 <= N < 2^31, 0 < V <= 2^20, N * ceil(V / 1024) < 2^31, N * stride <= 2^56
  *   rules    host struct above; NULL: no rule
  *   out      [N, V] of type out_dtype (dtype, or TIM_F32), rows out_stride apart;
  *            may be the logits themselves (same type and stride), else no shared element

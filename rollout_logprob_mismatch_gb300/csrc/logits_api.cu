@@ -16,6 +16,10 @@ uintptr_t elem_bytes(int dtype) { return dtype == TIM_F32 ? 4 : 2; }
 
 int invalid(const char *msg) { return fail_message(TIM_ERR_INVALID_ARG, "%s", msg); }
 
+// Rows that reach past 2^56 elements are in no address space (and their extent in
+// bytes might not fit 64 bits).
+bool too_far(int64_t N, int64_t stride) { return N > 0 && stride > (int64_t(1) << 56) / N; }
+
 // Checks the logits' sizes; 1 = nothing to do (N = 0).
 int check_logits(const void *logits, int dtype, int64_t N, int64_t V, int64_t stride)
 {
@@ -30,6 +34,8 @@ int check_logits(const void *logits, int dtype, int64_t N, int64_t V, int64_t st
         return invalid("the rows' stride must be at least V");
     if (N * tim::lg_slices(V) >= (int64_t(1) << 31))
         return invalid("N x V too large for one call");
+    if (too_far(N, stride))
+        return invalid("the rows reach past the address space");
     if (N == 0)
         return 1;
     if (!logits)
@@ -62,6 +68,8 @@ int check_out(const void *logits, int dtype, int64_t N, int64_t V, int64_t strid
         return invalid("the output is null");
     if (out_stride < V || out_stride > (int64_t(1) << 40))
         return invalid("the output rows' stride must be at least V");
+    if (too_far(N, out_stride))
+        return invalid("the output's rows reach past the address space");
     if (!aligned(out, elem_bytes(out_dtype)))
         return invalid("the output must be aligned to its elements");
     if (out == logits && out_dtype == dtype && (out_stride == stride || N == 1))
