@@ -366,3 +366,49 @@ def test_outputs_between_the_rows_of_the_logits(dtype):
         with pytest.raises(tim.TimError):
             tim.process_logits(a, R if a.shape[0] == N else None, out=b)
     tim.check()
+
+
+# ----------------------------------------------------------------------------- outputs on other streams
+def test_outputs_of_another_stream_are_not_handed_to_the_current_one():
+    """Every output a call allocates for another stream comes from that stream's memory:
+    after it is dropped an allocation of its size on the current stream is another
+    block.  A block of the current stream is handed out again at once (the control that
+    makes this test able to fail)."""
+    side = torch.cuda.Stream()
+
+    def handed_out(holder):
+        """The output in `holder` dropped: is its block what the current stream gets next?"""
+        x = holder.pop()
+        shape, dtype, at = x.shape, x.dtype, x.data_ptr()
+        held = [torch.empty(shape, dtype=dtype, device="cuda") for _ in range(20)]   # whatever else is free
+        del x
+        new = torch.empty(shape, dtype=dtype, device="cuda")
+        del held
+        return new.data_ptr() == at
+
+    def check(N, V, calls):
+        # (every output is above 10 MB: a block of its own)
+        z = torch.randn(N, V, device="cuda")
+        t = torch.zeros(N, dtype=torch.int32, device="cuda")
+        f = torch.ones(N, device="cuda")
+        lse = torch.logsumexp(z, 1)
+        args = (z, t.view(N, 1), f.view(N, 1))
+        torch.cuda.synchronize()
+        for call in calls:
+            holder = [call(z, t, f, lse, args, None)]
+            torch.cuda.synchronize()
+            assert handed_out(holder), "the control: a block of the current stream"
+            holder = [call(z, t, f, lse, args, side)]
+            side.synchronize()
+            assert not handed_out(holder)
+
+    check(3 << 20, 2, [lambda z, t, f, lse, a, s: tim.processed_logprob(z, None, t, stream=s)[0],
+                       lambda z, t, f, lse, a, s: tim.processed_logprob(z, None, t, stream=s)[1],
+                       lambda z, t, f, lse, a, s: tim.distill_topk(*a, stream=s)["loss"],
+                       lambda z, t, f, lse, a, s: tim.distill_topk(*a, stream=s)["lse"],
+                       lambda z, t, f, lse, a, s: tim.distill_topk(*a, teacher_lse=lse, stream=s)["lse_tail"]])
+    check(64, 151936, [lambda z, t, f, lse, a, s: tim.process_logits(z, None, stream=s),
+                       lambda z, t, f, lse, a, s: tim.processed_logprob_backward(z, None, t, f, lse, stream=s),
+                       lambda z, t, f, lse, a, s: tim.distill_topk_backward(*a, f, lse, stream=s),
+                       lambda z, t, f, lse, a, s: tim.distill_topk_step(*a, f, stream=s)["dlogits"]])
+    tim.check()
