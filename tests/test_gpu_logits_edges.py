@@ -7,8 +7,9 @@ import pytest
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
+import logits_ref as ref  # noqa: E402
 import rollout_logprob_mismatch_gb300 as tim  # noqa: E402
-from test_gpu_logits import dev, draw_logits, draw_teacher  # noqa: E402
+from test_gpu_logits import assert_close, dev, draw_logits, draw_teacher, rules  # noqa: E402
 
 
 # ----------------------------------------------------------------------------- the step's waits
@@ -411,4 +412,54 @@ def test_outputs_of_another_stream_are_not_handed_to_the_current_one():
                        lambda z, t, f, lse, a, s: tim.processed_logprob_backward(z, None, t, f, lse, stream=s),
                        lambda z, t, f, lse, a, s: tim.distill_topk_backward(*a, f, lse, stream=s),
                        lambda z, t, f, lse, a, s: tim.distill_topk_step(*a, f, stream=s)["dlogits"]])
+    tim.check()
+
+
+# ----------------------------------------------------------------------------- long segments
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_long_segments_in_place_and_not(dtype):
+    """A batch large enough that a CTA has some fifty slices of a row: rows whose table
+    half of the CTA builds, whose table is full under half and under all of it, and
+    rows without history, out of place, in place, and each against fp64."""
+    N, V = 300, 151936
+    z, z64 = draw_logits(N, V, dtype, 41)
+    rng = np.random.default_rng(17)
+    # tokens of rows: none, few, 4000 distinct ones in the row's first third, 9000 anywhere,
+    # 9000 in the first third, 5000 of few ids
+    parts = [np.zeros(0), rng.integers(0, V, 60), rng.permutation(40000)[:4000], rng.integers(0, V, 9000),
+             rng.permutation(45000)[:9000], rng.integers(0, V, 200)[rng.integers(0, 200, 5000)]]
+    start = np.concatenate([[0], np.cumsum([p.size for p in parts])])
+    kind = np.arange(N) % len(parts)
+    spans = np.stack([start[kind], start[kind] + (start[kind + 1] - start[kind]) // 3, start[kind + 1]], 1)
+    r = {"history": np.concatenate(parts).astype(np.int32), "history_spans": spans.astype(np.int32),
+         "repetition": rng.choice([1.0, 1.2, 0.9], N).astype(np.float32), "presence": np.full(N, 0.3, np.float32),
+         "frequency": np.full(N, 0.1, np.float32), "temperature": rng.uniform(0.6, 1.4, N).astype(np.float32),
+         "bias_offsets": (np.arange(N + 1) * 5).astype(np.int32), "bias_values": rng.normal(0, 2, 5 * N).astype(np.float32),
+         "bias_ids": np.concatenate([np.sort(rng.choice(V, 5, replace=False)) for _ in range(N)]).astype(np.int32),
+         "allowed": rng.integers(-2 ** 31, 2 ** 31, (2, (V + 31) // 32)).astype(np.int32),
+         "allowed_rows": rng.integers(-1, 2, N).astype(np.int32)}
+    R = rules(r)
+    rows = np.r_[0:6, 150:156, N - 6:N]
+    sub = {k: (v[rows] if k in ("history_spans", "repetition", "presence", "frequency", "temperature", "allowed_rows") else v)
+           for k, v in r.items()}
+    sub["bias_offsets"] = (np.arange(rows.size + 1) * 5).astype(np.int32)
+    sub["bias_ids"] = r["bias_ids"].reshape(N, 5)[rows].reshape(-1)
+    sub["bias_values"] = r["bias_values"].reshape(N, 5)[rows].reshape(-1)
+    y = tim.process_logits(z, R)
+    want, tol = ref.process_ref(z64[rows], sub, dtype)
+    assert_close(y[rows], want, tol, "process")
+    z2 = z.clone()
+    assert torch.equal(tim.process_logits(z2, R, out=z2), y), "process in place"
+    t = rng.integers(0, V, N).astype(np.int32)
+    t[::2] = r["history"][spans[::2, 1] % r["history"].size]
+    lp, lse = tim.processed_logprob(z, R, dev(t))
+    wlp, wlse, ltol = ref.logprob_ref(z64[rows], sub, t[rows])
+    assert_close(lp[rows], wlp, ltol, "logp")
+    assert_close(lse[rows], wlse, ltol, "lse")
+    g = rng.normal(0, 1, N).astype(np.float32)
+    d = tim.processed_logprob_backward(z, R, dev(t), dev(g), lse)
+    want, tol = ref.backward_ref(z64[rows], sub, t[rows], g[rows], lse.cpu().numpy()[rows], dtype)
+    assert_close(d[rows], want, tol, "gradient")
+    z2 = z.clone()
+    assert torch.equal(tim.processed_logprob_backward(z2, R, dev(t), dev(g), lse, dlogits=z2), d), "gradient in place"
     tim.check()
