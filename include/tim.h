@@ -413,7 +413,9 @@ enum tim_dtype { TIM_F32 = 0, TIM_BF16 = 1, TIM_F16 = 2 };
  *   x = x > 0 ? x / repetition : x * repetition   if v is anywhere in the row's history
  *   x = x - frequency * c - presence              if c > 0
  *   y = x / temperature;  y = -inf where the row's grammar does not allow v.
- * The pages give no formulas or order; this is the order inference engines use.
+ * The pages give no formulas and no order; this order is fixed, and log-probabilities
+ * compare only with an engine that applies the same (one that adds its biases after
+ * the penalties, say, does not).
  * Host struct; every pointer is a device pointer, and NULL leaves its rule out.
  *   temperature, repetition  fp32 [N], > 0, finite (and so 1 / x)
  *   presence, frequency      fp32 [N], finite
@@ -508,7 +510,8 @@ TIM_API int tim_processed_logprob_backward(const void *logits, int dtype, int64_
  * ids with a teacher logit of -inf, has loss 0 and gradient 0.
  *   logits, dtype, N, V, stride   as above
  *   teacher_ids     int32 [N, K], 1 <= K <= 1024; an id outside [0, V) is an empty
- *                   entry, an id listed twice adds up
+ *                   entry, an id listed twice adds up (a row with such an id costs K steps
+ *                   for each listed id: pad with ids outside [0, V), not with repeats)
  *   teacher_logits  fp32 [N, K]
  *   teacher_lse     fp32 [N] or NULL: log-sum-exp of the teacher's whole row at
  *                   `temperature`

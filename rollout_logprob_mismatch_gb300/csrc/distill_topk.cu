@@ -20,15 +20,19 @@
 // gradient; the listed ids cost K gathers and K stores.  The gradient pass writes
 // every column as if it were not listed; after a barrier the listed ones, all of
 // which the same CTA owns, are written over.  In a step the row comes from memory
-// once: a cluster holds it in its CTAs' shared memory (one bulk copy each, at most
-// 52 KB) between the passes, and the CTAs exchange the slices' partials.
+// once: a cluster holds it in its CTAs' shared memory (one bulk copy each, of at most
+// 52 KB while fewer than eight CTAs share the row, up to LD_SMEM then) between the
+// passes, and the CTAs exchange the slices' partials.
 //
 // Measured on a GB300 against the bytes each has to move at 6760 GB/s:
-//   loss      8192 x 151936 bf16, K = 64   390 us of 369 us: memory
-//   gradient  4096 x 128256 bf16, K = 64   312 us of 311 us: memory
-//   step      4096 x 151936 bf16, K = 64   511 us of 369 us, 1024 x 129280 fp32 with a
-//             tail, K = 128, 224 us of 157 us: a CTA's life of 10 us (row 2.5 us, sums 2 us,
-//             the other CTAs 2 us, gradient 2 us), of which five or two fit an SM
+//   loss      8192 x 151936 bf16, K = 64   390 us of 369 us: memory; 495 us with a tail:
+//             issue slots; 1024 x 129280 fp32 81 us of 78 us
+//   gradient  4096 x 128256 bf16, K = 64   308 to 312 us of 311 us: memory; 1024 x 129280
+//             fp32 165 us of 157 us
+//   step      4096 x 151936 bf16, K = 64   511 us of 369 us (507 us with a tail), 1024 x
+//             129280 fp32 with a tail, K = 128, 222 us of 157 us: a CTA's life of 10 us (row
+//             2.5 us, sums 2 us, the other CTAs 2 us, gradient 2 us), of which five (39 KB of
+//             row each) or three (64 KB) fit an SM
 #include <algorithm>
 #include <cstddef>
 
@@ -467,7 +471,7 @@ __global__ void __launch_bounds__(NT) distill_kernel(const DistillArgs a)
             const int id = k >= a.K ? -1 : n == 0 ? id0 : ids[k];
             if (id >= c0 && id < c1) {
                 float q = 0.f;
-                if (hd.dup) {   // ids listed more than once add up, in the list's order
+                if (hd.dup) {   // ids listed more than once add up, in the list's order: K steps for each id of this CTA
                     for (int j = 0; j < a.K; ++j)
                         q += ids[j] == id ? q_of(listed_logq<TAIL>(teacher[j], tau, w)) : 0.f;
                 } else {
@@ -542,7 +546,7 @@ template <typename T, int OP, bool TAIL> cudaError_t launch(DistillArgs a, int n
     while (ranks < LG_CLUSTER && ((ranks * 2 <= slices && rows * ranks < 4 * num_sms) ||
                                   (OP != LD_STEP && ranks * 32 <= slices && rows * ranks < 16 * num_sms)))
         ranks *= 2;
-    if (OP == LD_STEP)   // a rank's part of the row: at most 52 KB, so that four or five CTAs fit an SM
+    if (OP == LD_STEP)   // a rank's part of the row: at most 52 KB where eight ranks allow it, so that four or five CTAs fit an SM
         while (ranks < LG_CLUSTER && static_cast<size_t>((slices + ranks - 1) / ranks) * LG_SLICE * sizeof(T) > 52 * 1024)
             ranks *= 2;
     a.per = (slices + ranks - 1) / ranks;

@@ -26,11 +26,14 @@
 //
 // Measured on a GB300 against the bytes each has to move at 6760 GB/s (inputs not in L2):
 //   process   512 x 151936 bf16, histories of 1000 tokens   79 us of 47 us: the tables
+//             (86 us in place, fp32 126 us of 93 us, bf16 to fp32 106 us of 70 us)
 //   process   64 x 128256 bf16 -> fp32, half under a grammar 26 us of 7 us: one table's
 //             chain of loads and barriers (rules, history, counts, gathers), then the stream
 //   logprob   8192 x 151936 bf16, packed sequences of 512   439 us of 368 us: issue slots
 //             (6 instructions a column for the sum, 3 more for table and touched columns)
-//   gradient  4096 x 128256 bf16, a quarter under a grammar 344 us of 313 us: memory
+//             (fp32 1024 x 129280 110 us of 78 us: registers, see launch_logp)
+//   gradient  4096 x 128256 bf16, a quarter under a grammar 341 us of 313 us: memory
+//             (371 us in place; fp32 1024 x 129280 165 us of 157 us)
 #include <algorithm>
 
 #include "logits_rows.cuh"
@@ -322,10 +325,12 @@ __device__ __forceinline__ int half(int columns) { return (columns / 2 + LG_SLIC
 // first nb threads build the table while the others stream the columns (512 at a
 // time, claimed from a counter), then join them; the touched columns go over the
 // streamed ones at the end.  In place the table, which reads the touched logits,
-// comes first.  nb is half of the threads where the stream hides the table (345 us
-// against 351 us for the gradient of 4096 x 128256 bf16), all where a segment is short
-// (26 us against 32 us for 64 rows of 128256) or the history long (75 us against 84 us
-// for 400 rows of 100000 with some 1900 tokens each).
+// comes first, and the others wait for it.  nb is half of the threads where the stream
+// hides the table, all where a segment is short or the row's history long.  All / half,
+// processing 512 rows of 151936 bf16 (50 slices a segment): histories of some 400 tokens
+// 69.2 / 64.1 us, 3500 92.8 / 87.4 us, 7000 111.5 / 121.6 us, 14000 241 / 333 us; gradient of
+// 4096 x 128256 bf16 350 / 344 us; processing 64 rows of 128256 (11 slices) 22.0 / 23.8 us; at
+// 17 to 25 slices the two are within 2 %.
 //
 // A column's x / tau is the same operation whether the column is touched or not, so that
 // equal logits stay equal: for fp32 outputs the corrected quotient, for 16-bit ones the
@@ -642,7 +647,8 @@ template <typename T, typename TO, int OP> cudaError_t launch_map(ProcArgs a, in
     a.segs = (slices + a.seg_slices - 1) / a.seg_slices;
     a.table_columns = a.seg_slices * LG_SLICE;
     // Rows with long histories of their own (on average: rows that share theirs count
-    // little) touch more columns than the usual table holds.
+    // little) touch more columns than the usual table holds.  The host sees the length of
+    // the array only: a padded token buffer counts whole.
     const bool heavy = a.history_len / LP_HEAVY >= a.N;
     a.table_cap = heavy ? LP_HEAVY_CAP : LP_MAP_CAP;
     const unsigned grid = static_cast<unsigned>(a.N) * static_cast<unsigned>(a.segs);
@@ -686,7 +692,9 @@ template <typename T> cudaError_t launch_logp(ProcArgs a, int num_sms, cudaStrea
     // 2916 rows of 20544 fp16; 192 against 384: 118 us against 138 us for 4096 of 50304
     // bf16; 256 against 384: 439 us against 460 us for 8192 of 151936 bf16.  The tables
     // are kept small because the loads in flight live in what shared memory leaves of
-    // L1 (2048 entries for 1024: 128 us for 118 us at 50304 columns).
+    // L1 (2048 entries for 1024: 128 us for 118 us at 50304 columns).  The limits on
+    // registers were set for 16-bit logits; a warp's slice of fp32 ones is 32 registers by
+    // itself, and those kernels spill: 44 to 52 bytes a thread, 204 at 192 threads.
     a.table_cap = a.seg_slices <= 110 ? 1024 : LP_LOGP_CAP;
     if (a.seg_slices <= 40)
         return touch ? launch_logp_kernel<T, true, 128, 10>(a, s) : launch_logp_kernel<T, false, 128, 10>(a, s);
