@@ -92,11 +92,11 @@ template <bool TAIL> __device__ __forceinline__ float listed_logq(float t, float
 
 __device__ __forceinline__ float q_of(float logq) { return logq == neg_inf() ? 0.f : expf(logq); }
 
-// The q_o that counts.  Where the student gives the rest nothing (p_o = 0 in fp32, or
-// the rest's largest probability relative to the row's: a
-// list that holds every id, or a grammar both are under), what the rounding of the
-// teacher's lse and of sum q_k can leave of 1 - sum q_k is 0: four roundings of the
-// lse, 64 of the sum.  log p_o = -inf would make an infinite loss of it.
+// The q_o that counts.  Where the student gives the rest nothing (p_o, or the largest of
+// the rest relative to the row's largest, is 0 in fp32: a list that holds every id, a
+// grammar both are under), what the rounding of the teacher's lse and of sum q_k can
+// leave of 1 - sum q_k is 0: four roundings of the lse, 64 of the sum.  log p_o = -inf
+// would make an infinite loss of it.
 __device__ __forceinline__ float counted_rest(const TeacherRow &w, float p_o)
 {
     const float noise = fminf(0.5f, 0x1p-22f * (16.f + fabsf(w.lse)));
