@@ -546,6 +546,87 @@ TIM_API int tim_distill_topk_step(const void *logits, int dtype, int64_t N, int6
                                   float *loss, float *lse, float *lse_tail, void *dlogits,
                                   int64_t dlogits_stride, tim_stream_t stream);
 
+/* ------------------------------------------------------------------ beside the head's table
+ *
+ * No counterpart on the pages: a policy that is trained and served as low-rank
+ * adapters on a shared head, and the other end of the table of a head that is tied
+ * to the embedding. */
+
+/* Low-rank adapters on a shared head W [V, D]: adapter a adds scale_a B_a A_a to it.
+ * Host struct; the pointers are device pointers.
+ *   A      bf16 [num_adapters, rank, D], 16-byte aligned
+ *   B      bf16 [num_adapters, V, rank], 16-byte aligned
+ *   scale  fp32 [num_adapters], or NULL: 1
+ *   rank   a multiple of 8, 8 .. 128 (an adapter of a smaller rank has zeros behind)
+ *   num_adapters  0 .. 65535 */
+#define TIM_ADAPTER_MAX_RANK 128
+#define TIM_ADAPTER_MAX_COUNT 65535
+typedef struct {
+    const void *A;
+    const void *B;
+    const float *scale;
+    int32_t rank;
+    int32_t num_adapters;
+} tim_adapters;
+
+/* The adapters' part of a head's logits, for rows that belong to different requests:
+ *   y_iv = z_iv + sum_r t_ir B_a[v, r],  t_i = scale_a A_a h_i,  a = rows[i],
+ * with fp32 sums (t is held to 2^-16 of its value for 16-bit logits, 2^-24 for fp32
+ * ones) and one rounding to the logits' type.  Before tim_process_logits in an engine,
+ * before tim_processed_logprob in a trainer.
+ *   logits, dtype, N, V, stride   as above, N < 2^30
+ *   h      bf16 [N, D], 16-byte aligned, D a multiple of 8 up to 65536
+ *   rows   int32 [N]: the row's adapter; outside [0, num_adapters): none, the row's
+ *          logits keep their bits
+ *   out    [N, V] of type dtype, rows out_stride apart; may be the logits themselves
+ *          (rows under no adapter are then not touched), else no shared element; its
+ *          extent, from the first row to the last, shares no byte with the other inputs
+ * An infinite or NaN factor of an adapter reaches no row of another.  A row's bits do
+ * not depend on the rows beside it.  Scratch (stream-ordered pool): 8 N + 4 num_adapters
+ * bytes and at most 768 N bytes. */
+TIM_API int tim_adapter_logits(const void *logits, int dtype, int64_t N, int64_t V, int64_t stride, const void *h,
+                               int64_t D, const tim_adapters *adapters, const int32_t *rows, void *out,
+                               int64_t out_stride, tim_stream_t stream);
+
+/* Its gradient from dlogits (dL / dy: that of the logits with the adapters' part, as
+ * tim_processed_logprob_backward gives it), with t as above and du_i = scale_a B_a^T dy_i:
+ *   dB_a = sum_i dy_i t_i^T,  dA_a = sum_i du_i h_i^T,  dh_i = A_a^T du_i,
+ * over the rows i of adapter a.  The shared head's part, dh += dlogits W, is the
+ * caller's (accumulate_dh adds to it); dL / dz is dlogits itself.  fp32 sums; t is held
+ * to 2^-16 of its value, fp32 dlogits to 2^-16, du to 2^-24.
+ *   dlogits, dtype, N, V, stride, h, D, adapters, rows   as above
+ *   dh   fp32 [N, D], 16-byte aligned; rows under no adapter: zeros (with accumulate_dh
+ *        not touched)
+ *   dA   fp32 [num_adapters, rank, D];  dB  fp32 [num_adapters, V, rank]; 16-byte
+ *        aligned; an adapter without rows: zeros (with accumulate_adapters not touched)
+ * No output shares a byte with an input or another.  The same call gives the same bits.
+ * Scratch (stream-ordered pool): up to about 2 KB a row, and partial sums of du of at
+ * most 1 GB (larger batches go in parts). */
+TIM_API int tim_adapter_logits_backward(const void *dlogits, int dtype, int64_t N, int64_t V, int64_t stride,
+                                        const void *h, int64_t D, const tim_adapters *adapters, const int32_t *rows,
+                                        float *dh, float *dA, float *dB, int accumulate_dh, int accumulate_adapters,
+                                        tim_stream_t stream);
+
+/* Rows of a table: out_n = scale W[tokens_n], in fp32 and rounded once to out_dtype.
+ *   tokens  int32 [N], N < 2^30; an id outside [0, V) (padding) gives a row of zeros
+ *   W       [V, D] of type dtype (enum tim_dtype), contiguous, aligned to its elements;
+ *           0 < V <= 2^20, 0 < D <= 65536, N ceil(D / 256) < 2^31
+ *   scale   finite (1: none)
+ *   out     [N, D] of type out_dtype, contiguous; shares no byte with the inputs */
+TIM_API int tim_embedding(const int32_t *tokens, int64_t N, const void *W, int dtype, int64_t V, int64_t D,
+                          float scale, void *out, int out_dtype, tim_stream_t stream);
+
+/* Its gradient: dW[v] (+)= scale sum over n with tokens_n = v of grad_n, in fp32, the
+ * tokens of an id added in their order (ids with more than 64 tokens in partial sums
+ * over tiles of 32): the same call gives the same bits.
+ *   grad           [N, D] of type dtype, contiguous, aligned to its elements
+ *   dW             fp32 [V, D], contiguous; written whole, or with accumulate_dW added to
+ *                  (rows without a token are not touched: the gradient of a tied head,
+ *                  after tim_token_logprob_backward)
+ * Scratch (stream-ordered pool): 4 V + 16 N + D ceil(N / 4) bytes. */
+TIM_API int tim_embedding_backward(const int32_t *tokens, int64_t N, const void *grad, int dtype, int64_t V,
+                                   int64_t D, float scale, float *dW, int accumulate_dW, tim_stream_t stream);
+
 /* ------------------------------------------------------------------ failure-detection self-test
  *
  * No counterpart on the pages.  Runs the library's bounded-wait path on purpose,

@@ -22,7 +22,10 @@ Where a program holds the logits themselves, ``process_logits`` applies the
 sampler's rules (biases, penalties for repeated tokens, temperature, grammar
 masks), ``processed_logprob`` gives the chosen token's log-probability under them
 (with its gradient), and ``distill_topk`` distils from a teacher's top logits
-(icarus page, section "logits processor"; no formulas there).
+(icarus page, section "logits processor"; no formulas there).  ``adapter_logits``
+adds the low-rank adapters of many requests to a shared head's logits, and
+``embedding`` takes rows of the table that a tied head shares, both with their
+gradients (no counterpart on the pages).
 """
 from __future__ import annotations
 
@@ -44,6 +47,8 @@ __all__ = [
     "LogitsRules", "tim_logits_rules", "tim_process_logits", "tim_processed_logprob", "tim_processed_logprob_backward",
     "tim_distill_topk", "tim_distill_topk_backward", "tim_distill_topk_step", "process_logits", "processed_logprob",
     "processed_logprob_backward", "distill_topk", "distill_topk_backward", "distill_topk_step", "packed_spans",
+    "Adapters", "tim_adapters", "tim_adapter_logits", "tim_adapter_logits_backward", "tim_embedding",
+    "tim_embedding_backward", "adapter_logits", "adapter_logits_backward", "embedding", "embedding_backward",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -65,6 +70,7 @@ CHECKS = {0: "none", 1: "target", 2: "mask", 3: "logit", 4: "backward_input", 5:
 SEQ_RECORD_WORDS = 16   # TIM_SEQ_RECORD_WORDS
 TIM_F32, TIM_BF16, TIM_F16 = 0, 1, 2   # enum tim_dtype
 DISTILL_MAX_K = 1024    # TIM_DISTILL_MAX_K
+ADAPTER_MAX_RANK, ADAPTER_MAX_COUNT = 128, 65535   # TIM_ADAPTER_MAX_*
 SEQ_FIELDS = ("n_mask", "n_used", "n_nan", "n_clip", "mean_delta", "mean_abs_delta",
               "max_abs_delta", "mean_k1", "mean_k2", "mean_k3", "mean_w", "mean_rel")
 BATCH_FIELDS = ("n_mask", "n_used", "n_nan", "n_clip", "mean_delta", "mean_abs_delta",
@@ -124,6 +130,17 @@ class tim_logits_rules(ctypes.Structure):
     ]
 
 
+class tim_adapters(ctypes.Structure):
+    """Mirror of the C struct tim_adapters (host struct of device pointers)."""
+    _fields_ = [
+        ("A", ctypes.c_void_p),
+        ("B", ctypes.c_void_p),
+        ("scale", ctypes.c_void_p),
+        ("rank", ctypes.c_int32),
+        ("num_adapters", ctypes.c_int32),
+    ]
+
+
 _lock = threading.Lock()
 _lib = None          # the library calls go to (libtim.so, or libtim_debug.so inside `checked()`)
 _release = None
@@ -166,13 +183,19 @@ def _open(path: str, what: str):
     lib.tim_mismatch_monitor.restype = ctypes.c_int
     head = [P, ctypes.c_int, I64, I64, I64]   # logits, dtype, N, V, stride
     RP = ctypes.POINTER(tim_logits_rules)
+    AP = ctypes.POINTER(tim_adapters)
     teacher = [P, P, P, I64, F]               # ids, logits, lse, K, temperature
     for name, args in (("tim_process_logits", head + [RP, P, ctypes.c_int, I64, P]),
                        ("tim_processed_logprob", head + [RP, P, P, P, P]),
                        ("tim_processed_logprob_backward", head + [RP, P, P, P, P, I64, P]),
                        ("tim_distill_topk", head + teacher + [P, P, P, P]),
                        ("tim_distill_topk_backward", head + teacher + [P, P, P, P, I64, P]),
-                       ("tim_distill_topk_step", head + teacher + [P, P, P, P, P, I64, P])):
+                       ("tim_distill_topk_step", head + teacher + [P, P, P, P, P, I64, P]),
+                       ("tim_adapter_logits", head + [P, I64, AP, P, P, I64, P]),
+                       ("tim_adapter_logits_backward",
+                        head + [P, I64, AP, P, P, P, P, ctypes.c_int, ctypes.c_int, P]),
+                       ("tim_embedding", [P, I64, P, ctypes.c_int, I64, I64, F, P, ctypes.c_int, P]),
+                       ("tim_embedding_backward", [P, I64, P, ctypes.c_int, I64, I64, F, P, ctypes.c_int, P])):
         getattr(lib, name).argtypes = args
         getattr(lib, name).restype = ctypes.c_int
     lib.tim_selftest_wait_timeout.argtypes = [ctypes.c_uint32, P]
@@ -316,6 +339,25 @@ def tim_distill_topk_step(logits, dtype, N, V, stride, teacher_ids, teacher_logi
                           grad_loss, loss, lse, lse_tail, dlogits, dlogits_stride, stream) -> int:
     return load().tim_distill_topk_step(logits, dtype, N, V, stride, teacher_ids, teacher_logits, teacher_lse, K,
                                         temperature, grad_loss, loss, lse, lse_tail, dlogits, dlogits_stride, stream)
+
+
+def tim_adapter_logits(logits, dtype, N, V, stride, h, D, adapters, rows, out, out_stride, stream) -> int:
+    """C ABI; adapters is a reference to a tim_adapters, or None (refused)."""
+    return load().tim_adapter_logits(logits, dtype, N, V, stride, h, D, adapters, rows, out, out_stride, stream)
+
+
+def tim_adapter_logits_backward(dlogits, dtype, N, V, stride, h, D, adapters, rows, dh, dA, dB, accumulate_dh,
+                                accumulate_adapters, stream) -> int:
+    return load().tim_adapter_logits_backward(dlogits, dtype, N, V, stride, h, D, adapters, rows, dh, dA, dB,
+                                              accumulate_dh, accumulate_adapters, stream)
+
+
+def tim_embedding(tokens, N, W, dtype, V, D, scale, out, out_dtype, stream) -> int:
+    return load().tim_embedding(tokens, N, W, dtype, V, D, scale, out, out_dtype, stream)
+
+
+def tim_embedding_backward(tokens, N, grad, dtype, V, D, scale, dW, accumulate_dW, stream) -> int:
+    return load().tim_embedding_backward(tokens, N, grad, dtype, V, D, scale, dW, accumulate_dW, stream)
 
 
 def tim_selftest_wait_timeout(budget_us, stream) -> int:
@@ -960,6 +1002,127 @@ def distill_topk_step(logits, teacher_ids, teacher_logits, grad_loss, teacher_ls
     out["dlogits"] = dlogits
     _launch(tim_distill_topk_step, dev, stream, *args, g, *rows, d[0], d[4])
     return out
+
+
+# ----------------------------------------------------------------------------- beside the head's table
+@dataclasses.dataclass
+class Adapters:
+    """Low-rank adapters on a shared head (tim_adapters in include/tim.h): A bf16
+    [n, R, D], B bf16 [n, V, R], R a multiple of 8 up to 128, scale fp32 [n] or None
+    (1), all contiguous on one device.  Adapter a adds scale_a B_a A_a to the head."""
+    A: object
+    B: object
+    scale: object = None
+
+    def struct(self, V: int, D: int, device):
+        """The C struct, after checking every tensor against a head [V, D]."""
+        torch = _torch()[0]
+        if not isinstance(self.A, torch.Tensor):
+            raise TypeError("A must be a torch.Tensor")
+        if self.A.dim() != 3:
+            raise ValueError("A must be [n, R, D]")
+        n, R, _ = self.A.shape
+        if R < 8 or R > ADAPTER_MAX_RANK or R % 8:
+            raise ValueError("the rank must be a multiple of 8 up to %d, got %d" % (ADAPTER_MAX_RANK, R))
+        if n > ADAPTER_MAX_COUNT:
+            raise ValueError("at most %d adapters, got %d" % (ADAPTER_MAX_COUNT, n))
+        r = tim_adapters()
+        r.A = _need_array(self.A, "A", torch.bfloat16, (n, R, D), device) or None
+        r.B = _need_array(self.B, "B", torch.bfloat16, (n, V, R), device) or None
+        if self.scale is not None:
+            r.scale = _need_array(self.scale, "scale", torch.float32, (n,), device) or None
+        r.rank, r.num_adapters = R, n
+        return r
+
+
+def _adapter_inputs(logits, name, h, adapters, rows):
+    """(C arguments up to the rows, device)."""
+    torch = _torch()[0]
+    head = _need_logits(logits, name)
+    dev, N, V = logits.device, head[2], head[3]
+    if not isinstance(adapters, Adapters):
+        raise TypeError("adapters must be Adapters")
+    _need(h, "h", torch.bfloat16, 2, dev)
+    D = h.shape[1]
+    if h.shape[0] != N:
+        raise ValueError("h must have %d rows, got %d" % (N, h.shape[0]))
+    ad = adapters.struct(V, D, dev)
+    r = _need_array(rows, "rows", torch.int32, (N,), dev)
+    return (*head, h.data_ptr(), D, ctypes.byref(ad), r), dev
+
+
+def adapter_logits(logits, h, adapters, rows, out=None, stream=None):
+    """fp32, bf16 or fp16 logits [N, V] of a shared head with the adapters' part added:
+    row i gets scale_a B_a A_a h_i, a = rows[i] (int32 [N]; outside [0, n): nothing),
+    for bf16 h [N, D].  out may be the logits themselves."""
+    args, dev = _adapter_inputs(logits, "logits", h, adapters, rows)
+    N, V = args[2], args[3]
+    if out is None:
+        out = _new((N, V), logits.dtype, dev, stream)
+    address, _, _, _, stride = _need_logits(out, "out", logits.dtype, dev, (N, V))
+    _launch(tim_adapter_logits, dev, stream, *args, address, stride)
+    return out
+
+
+def adapter_logits_backward(dlogits, h, adapters, rows, dh=None, dA=None, dB=None, accumulate_dh: bool = False,
+                            accumulate_adapters: bool = False, stream=None):
+    """(dh fp32 [N, D], dA fp32 [n, R, D], dB fp32 [n, V, R]) from the gradient dlogits
+    [N, V] (fp32, bf16 or fp16) of adapter_logits' output.  dh is the adapters' part:
+    with accumulate_dh it is added to dh, which holds the shared head's (dlogits W);
+    with accumulate_adapters dA and dB are added to."""
+    f32 = _torch()[0].float32
+    args, dev = _adapter_inputs(dlogits, "dlogits", h, adapters, rows)
+    N, V, D = args[2], args[3], args[6]
+    n, R, _ = adapters.A.shape
+    if (accumulate_dh and dh is None) or (accumulate_adapters and (dA is None or dB is None)):
+        raise ValueError("an accumulated output must be given")
+    dh = _new((N, D), f32, dev, stream) if dh is None else dh
+    dA = _new((n, R, D), f32, dev, stream) if dA is None else dA
+    dB = _new((n, V, R), f32, dev, stream) if dB is None else dB
+    _launch(tim_adapter_logits_backward, dev, stream, *args, _need_array(dh, "dh", f32, (N, D), dev),
+            _need_array(dA, "dA", f32, (n, R, D), dev), _need_array(dB, "dB", f32, (n, V, R), dev), int(accumulate_dh),
+            int(accumulate_adapters))
+    return dh, dA, dB
+
+
+def embedding(tokens, W, scale: float = 1.0, out=None, out_dtype=None, stream=None):
+    """scale * W[tokens] as [N, D]: int32 tokens [N] (an id outside [0, V): a row of
+    zeros), W fp32, bf16 or fp16 [V, D], out in W's type or out_dtype."""
+    torch = _torch()[0]
+    types = (torch.float32, torch.bfloat16, torch.float16)
+    _need(tokens, "tokens", torch.int32, 1)
+    dev = tokens.device
+    _need(W, "W", types, 2, dev)
+    N, (V, D) = tokens.shape[0], W.shape
+    if out is None:
+        out = _new((N, D), out_dtype or W.dtype, dev, stream)
+    elif out_dtype is not None and out.dtype != out_dtype:
+        raise TypeError("out must have dtype %s, got %s" % (out_dtype, out.dtype))
+    _need_out(out, "out", types, (N, D), dev)
+    _launch(tim_embedding, dev, stream, tokens.data_ptr(), N, W.data_ptr(), _dtype_code(W.dtype), V, D, float(scale),
+            out.data_ptr(), _dtype_code(out.dtype))
+    return out
+
+
+def embedding_backward(tokens, grad, V: int, scale: float = 1.0, dW=None, accumulate_dW: bool = False, stream=None):
+    """dW fp32 [V, D], row v the sum of scale * grad_n over the n with tokens_n = v, for
+    int32 tokens [N] and fp32, bf16 or fp16 grad [N, D]; with accumulate_dW added to dW
+    (the gradient of a head that shares the table)."""
+    torch = _torch()[0]
+    _need(tokens, "tokens", torch.int32, 1)
+    dev = tokens.device
+    _need(grad, "grad", (torch.float32, torch.bfloat16, torch.float16), 2, dev)
+    N, D = grad.shape
+    if tokens.shape[0] != N:
+        raise ValueError("tokens must have %d entries, got %d" % (N, tokens.shape[0]))
+    if dW is None:
+        if accumulate_dW:
+            raise ValueError("accumulate_dW needs dW")
+        dW = _new((V, D), torch.float32, dev, stream)
+    _need_out(dW, "dW", torch.float32, (V, D), dev)
+    _launch(tim_embedding_backward, dev, stream, tokens.data_ptr(), N, grad.data_ptr(), _dtype_code(grad.dtype), V, D,
+            float(scale), dW.data_ptr(), int(accumulate_dW))
+    return dW
 
 
 def check(stream=None, device=None):

@@ -1,0 +1,36 @@
+// adapters.cuh -- device code shared by the adapters' kernels: bf16 parts of fp32
+// values and the warp's 16 x 8 x 16 product.
+#pragma once
+
+#include "logits_rows.cuh"
+
+namespace tim {
+
+// D (16 x 8, fp32) += A (16 x 16) B (16 x 8), bf16.  Lane l = 4 g + q holds rows g and
+// g + 8 of A (k pairs 2q and 2q + 8), column g of B (the same k pairs), and columns 2q
+// and 2q + 1 of D in rows g and g + 8.  The order of k is the caller's as long as A and
+// B agree: the kernels here give a lane four (or eight) neighbouring k in place of two
+// pairs, so that its operands come in 8- and 16-byte loads.
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// x = p[0] + p[1] + ... up to half a unit of the last part: each part is what the ones
+// before leave, rounded to bf16 (2^-8 of it at most, so two parts leave 2^-16 |x| and
+// three 2^-24).  An infinite or NaN x is all in part 0.
+template <int PARTS> __device__ __forceinline__ void split_bf16(float x, uint16_t (&p)[PARTS])
+{
+    const bool finite = fabsf(x) <= 3.38953139e38f;   // bf16's largest
+#pragma unroll
+    for (int i = 0; i < PARTS; ++i) {
+        const __nv_bfloat16 b = __float2bfloat16_rn(x);
+        p[i] = i == 0 || finite ? __bfloat16_as_ushort(b) : uint16_t(0);
+        x -= __bfloat162float(b);
+    }
+}
+
+} // namespace tim

@@ -20,7 +20,10 @@ int invalid(const char *msg) { return fail_message(TIM_ERR_INVALID_ARG, "%s", ms
 // bytes might not fit 64 bits).
 bool too_far(int64_t N, int64_t stride) { return N > 0 && stride > (int64_t(1) << 56) / N; }
 
-// Checks the logits' sizes; 1 = nothing to do (N = 0).
+} // namespace
+
+namespace tim {
+
 int check_logits(const void *logits, int dtype, int64_t N, int64_t V, int64_t stride)
 {
     if (dtype != TIM_F32 && dtype != TIM_BF16 && dtype != TIM_F16)
@@ -45,6 +48,10 @@ int check_logits(const void *logits, int dtype, int64_t N, int64_t V, int64_t st
     return TIM_OK;
 }
 
+} // namespace tim
+
+namespace {
+
 // Do N rows of `size` bytes each, `step` bytes apart, share a byte with rows of `size2`
 // bytes, `step2` apart?  Exact for equal steps (two parts of one buffer's rows, side by
 // side); else the whole ranges are compared.
@@ -59,9 +66,11 @@ bool share_bytes(uintptr_t a, uintptr_t step, uintptr_t size, uintptr_t b, uintp
     return at < size || at + size2 > step;
 }
 
-// An output of the logits' shape: not null, aligned, and either apart from the
-// logits or exactly over them.
-int check_out(const void *logits, int dtype, int64_t N, int64_t V, int64_t stride, const void *out, int out_dtype,
+} // namespace
+
+namespace tim {
+
+int check_logits_out(const void *logits, int dtype, int64_t N, int64_t V, int64_t stride, const void *out, int out_dtype,
               int64_t out_stride)
 {
     if (!out)
@@ -80,6 +89,13 @@ int check_out(const void *logits, int dtype, int64_t N, int64_t V, int64_t strid
         return invalid("the output overlaps the logits without being the logits");
     return TIM_OK;
 }
+
+} // namespace tim
+
+namespace {
+
+using tim::check_logits;
+using tim::check_logits_out;
 
 int set_rules(tim::ProcArgs &a, const tim_logits_rules *r, int64_t N, int64_t V)
 {
@@ -202,7 +218,7 @@ int tim_process_logits(const void *logits, int dtype, int64_t N, int64_t V, int6
         return invalid("out_dtype must be dtype or TIM_F32");
     if (rc == 1)
         return tim::record_error(TIM_OK, "");
-    if ((rc = check_out(logits, dtype, N, V, stride, out, out_dtype, out_stride)) != TIM_OK)
+    if ((rc = check_logits_out(logits, dtype, N, V, stride, out, out_dtype, out_stride)) != TIM_OK)
         return rc;
     tim::ProcArgs a{};
     a.out = out;
@@ -243,7 +259,7 @@ int tim_processed_logprob_backward(const void *logits, int dtype, int64_t N, int
         return invalid("null pointer argument");
     if (!aligned(targets, 4) || !aligned(grad_logp, 4) || !aligned(lse, 4))
         return invalid("targets / grad_logp / lse must be 4-byte aligned");
-    if ((rc = check_out(logits, dtype, N, V, stride, dlogits, dtype, dlogits_stride)) != TIM_OK)
+    if ((rc = check_logits_out(logits, dtype, N, V, stride, dlogits, dtype, dlogits_stride)) != TIM_OK)
         return rc;
     tim::ProcArgs a{};
     a.targets = targets;
@@ -289,7 +305,7 @@ int tim_distill_topk_backward(const void *logits, int dtype, int64_t N, int64_t 
         return tim::record_error(TIM_OK, "");
     if (!grad_loss || !lse || (teacher_lse && !lse_tail))
         return invalid("grad_loss, lse and (with teacher_lse) lse_tail are required");
-    if ((rc = check_out(logits, dtype, N, V, stride, dlogits, dtype, dlogits_stride)) != TIM_OK)
+    if ((rc = check_logits_out(logits, dtype, N, V, stride, dlogits, dtype, dlogits_stride)) != TIM_OK)
         return rc;
     tim::DistillArgs a{};
     a.grad = grad_loss;
@@ -315,7 +331,7 @@ int tim_distill_topk_step(const void *logits, int dtype, int64_t N, int64_t V, i
         return tim::record_error(TIM_OK, "");
     if (!grad_loss || !loss || !lse || (teacher_lse && !lse_tail))
         return invalid("grad_loss, loss, lse and (with teacher_lse) lse_tail are required");
-    if ((rc = check_out(logits, dtype, N, V, stride, dlogits, dtype, dlogits_stride)) != TIM_OK)
+    if ((rc = check_logits_out(logits, dtype, N, V, stride, dlogits, dtype, dlogits_stride)) != TIM_OK)
         return rc;
     tim::DistillArgs a{};
     a.grad = grad_loss;

@@ -92,6 +92,14 @@ struct DistillArgs {
 
 cudaError_t distill_topk_launch(DistillArgs a, int op, int dtype, int num_sms, cudaStream_t s);
 
+// ---------------------------------------------------------------- argument checks
+// The logits' sizes: a tim_status code, or 1 = nothing to do (N = 0).
+int check_logits(const void *logits, int dtype, int64_t N, int64_t V, int64_t stride);
+// An output of the logits' shape: not null, aligned, and either apart from the
+// logits or exactly over them.
+int check_logits_out(const void *logits, int dtype, int64_t N, int64_t V, int64_t stride, const void *out, int out_dtype,
+                     int64_t out_stride);
+
 // shared-memory sizes of the kernels above
 cudaError_t logits_process_prepare_device();
 cudaError_t distill_topk_prepare_device();

@@ -1,0 +1,128 @@
+// table_internal.h -- launch shapes and arguments of the operators beside the
+// head's table: low-rank adapters on its logits, embedding lookup and gradient.
+// Not part of the ABI.
+#pragma once
+
+#include <cstdint>
+
+#include <cuda_runtime.h>
+
+namespace tim {
+
+// Device memory from the library's stream-ordered pool; a tim_status code.
+int workspace_alloc(void **p, size_t bytes, cudaStream_t s);
+cudaError_t workspace_free(void *p, cudaStream_t s);
+
+inline size_t ws_round(size_t x) { return (x + 255) / 256 * 256; }
+
+// ---------------------------------------------------------------- adapters
+constexpr int AD_MAX_RANK = 128;
+constexpr int AD_MAX_ADAPTERS = 65535;
+constexpr int AD_SHRINK_THREADS = 512;
+constexpr int AD_CHUNK = 64;         // rows of one adapter that a CTA projects at a time, at most
+constexpr int AD_MAP_THREADS = 256;  // eight warps
+constexpr int AD_MAP_ROWS = 256;     // positions of a CTA of the map, at most
+
+// Ranks are padded to 16, 32, 64 or 128 inside the kernels (zeros).
+inline int ad_rank_pad(int64_t R) { return R <= 16 ? 16 : R <= 32 ? 32 : R <= 64 ? 64 : 128; }
+
+// The batch's rows ordered by adapter (stable), and t = scale A h of each in bf16
+// parts: t = part 0 + part 1 (+ part 2), each the rest rounded to nearest.
+struct AdapterPlan {
+    int32_t *offsets;   // [n + 2]: positions of adapter a are offsets[a] .. offsets[a + 1]; n = no adapter
+    int32_t *perm;      // [N]: row of each position
+    int32_t *adapter;   // [N]: adapter of each position, n = none
+    uint16_t *t;        // bf16 [N][t_pitch]: [parts][RP] and padding
+    int32_t t_pitch;
+};
+
+struct AdapterArgs {
+    const uint16_t *h;        // [N, D] bf16
+    const uint16_t *A;        // [n, R, D]
+    const uint16_t *B;        // [n, V, R]
+    const float *scale;       // [n] or null
+    const int32_t *rows;      // [N]
+    int32_t N, V, D, R, n;
+    AdapterPlan plan;
+    const void *z;            // [N, V], rows ld apart
+    int64_t ld;
+    void *out;
+    int64_t ldo;
+    int32_t in_place;
+    int32_t chunk;            // shrink: rows at a time, 16 .. AD_CHUNK
+    int32_t row_chunk;        // map: positions of a CTA, a multiple of 16
+};
+
+// Orders the rows and projects them: one launch.  parts: 2 or 3.
+cudaError_t adapters_shrink_launch(AdapterArgs a, int parts, int num_sms, cudaStream_t s);
+// out = z + t B^T
+cudaError_t adapters_expand_launch(AdapterArgs a, int dtype, int num_sms, cudaStream_t s);
+
+// The gradient: slabs of the vocabulary, steps of 16 rows.
+constexpr int AG_STEP = 16;
+constexpr int AG_SMEM = 227 * 1024;
+constexpr int64_t AG_PARTIAL_BYTES = int64_t(1) << 30;   // du's partial sums at most, per part of the batch
+
+// Elements of a row of t in the gradient: two parts, and 16 bytes that spread the rows
+// over the banks.
+constexpr int ag_t_pitch(int RT) { return 2 * RT + 8; }
+
+// Columns of a slab: as many as dB's sums have registers for (128 a thread), or fewer
+// where the vocabulary would not give every SM a slab.
+constexpr int ag_cols(int RP, bool raw, bool wide)
+{
+    const int most = (RP <= 32 ? 1024 : 512) / (raw ? 2 : 1);
+    return wide ? most : most / 4 < 128 ? 128 : most / 4;
+}
+
+struct AdapterGradArgs {
+    const uint16_t *h, *A, *B;
+    const float *scale;
+    AdapterPlan plan;
+    const void *dy;           // [N, V], rows ld apart
+    int64_t ld;
+    int32_t N, V, D, R, n;
+    int32_t RT;               // the rank padded (16, 32, 64, 128)
+    int32_t raw;              // rows of dy that are not bf16 from a 16-byte boundary on
+    int32_t cols, slabs;      // columns of a slab, slabs
+    int32_t row_part;         // positions of a launch
+    int32_t p0, p1, r0;       // the launch's positions and first rank
+    int32_t row_chunk;        // dh: positions of a CTA
+    float *partial;           // [slabs][p1 - p0][min(RT, 64)]
+    uint16_t *du;             // [N][3][RT] bf16 parts of scale B^T dy
+    float *dh, *dA, *dB;
+    int32_t accumulate, accumulate_dh;
+    uint64_t wait_budget_ns;
+    int *status;
+};
+
+cudaError_t adapters_grad_launch(AdapterGradArgs a, int dtype, cudaStream_t s);
+cudaError_t adapters_grad_prepare_device();
+
+// ---------------------------------------------------------------- embedding
+constexpr int EM_RANGE = 512;        // ids that one CTA of the sort orders
+constexpr int EM_SORT_THREADS = 512;
+constexpr int EM_TILE = 32;          // sorted positions of a partial sum of a long row
+constexpr int EM_LONG = 64;          // tokens of an id above which its row is summed in tiles
+constexpr int EM_IDS = 8;            // rows of the table that a warp writes
+
+struct EmbeddingArgs {
+    const int32_t *tokens;    // [N]
+    int32_t N, V, D;
+    float scale;
+    const void *x;            // lookup: the table [V, D]; gradient: the rows' [N, D]
+    void *out;                // lookup: [N, D]
+    float *dW;                // gradient: [V, D]
+    int32_t accumulate;
+    int32_t *offsets;         // [V + 1] sorted positions of each id
+    int32_t *order;           // [N] tokens ordered by id (stable)
+    int32_t *ids;             // [N] id of each sorted position
+    int2 *staged;             // [N] scratch of the sort
+    float *partial;           // [ceil(N / EM_TILE)][2][D]
+};
+
+cudaError_t embedding_launch(const EmbeddingArgs &a, int dtype, int out_dtype, cudaStream_t s);
+cudaError_t embedding_sort_launch(const EmbeddingArgs &a, cudaStream_t s);
+cudaError_t embedding_sum_launch(const EmbeddingArgs &a, int dtype, cudaStream_t s);
+
+} // namespace tim

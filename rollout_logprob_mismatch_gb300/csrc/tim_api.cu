@@ -16,6 +16,7 @@
 #include "k1_internal.h"
 #include "k2_internal.h"
 #include "logits_internal.h"
+#include "table_internal.h"
 #include "tim_internal.h"
 
 namespace {
@@ -109,7 +110,8 @@ int device_state(DeviceState **out)
     if ((e = tim::k1_prepare_device()) != cudaSuccess || (e = tim::k2_prepare_device()) != cudaSuccess ||
         (e = tim::monitor_prepare_device()) != cudaSuccess || (e = tim::gemm_prepare_device()) != cudaSuccess ||
         (e = tim::logits_process_prepare_device()) != cudaSuccess ||
-        (e = tim::distill_topk_prepare_device()) != cudaSuccess)
+        (e = tim::distill_topk_prepare_device()) != cudaSuccess ||
+        (e = tim::adapters_grad_prepare_device()) != cudaSuccess)
         return cuda_fail(e, "cudaFuncSetAttribute");
     if (!g_encode) {
         void *fn = nullptr;
@@ -226,6 +228,18 @@ int use_device(int **status, int *sms)
 }
 
 uint64_t pipeline_wait_budget_ns() { return wait_budget_ns(); }
+
+int workspace_alloc(void **p, size_t bytes, cudaStream_t s)
+{
+    DeviceState *d = nullptr;
+    const int rc = device_state(&d);
+    if (rc != TIM_OK)
+        return rc;
+    const cudaError_t e = cudaMallocFromPoolAsync(p, bytes, d->pool, s);
+    return e == cudaSuccess ? TIM_OK : cuda_fail(e, "cudaMallocFromPoolAsync(workspace)");
+}
+
+cudaError_t workspace_free(void *p, cudaStream_t s) { return cudaFreeAsync(p, s); }
 
 // Records a formatted message for tim_last_error() on the calling thread; returns code.
 int fail_message(int code, const char *fmt, ...)
