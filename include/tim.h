@@ -583,7 +583,7 @@ typedef struct {
  *          extent, from the first row to the last, shares no byte with the other inputs
  * An infinite or NaN factor of an adapter reaches no row of another.  A row's bits do
  * not depend on the rows beside it.  Scratch (stream-ordered pool): 8 N + 4 num_adapters
- * bytes and at most 768 N bytes. */
+ * bytes and at most 784 N bytes. */
 TIM_API int tim_adapter_logits(const void *logits, int dtype, int64_t N, int64_t V, int64_t stride, const void *h,
                                int64_t D, const tim_adapters *adapters, const int32_t *rows, void *out,
                                int64_t out_stride, tim_stream_t stream);

@@ -227,188 +227,283 @@ template <int RP> struct Ranks {
     static constexpr int STEP = RP == 16 ? 4 : 8;        // neighbouring ranks of a lane
     static constexpr int GROUPS = RP == 16 ? 1 : RP / 32;
     static constexpr int WORDS = STEP / 2;
-    static constexpr int STEPS = RP / 16;                // products along the rank
 };
 
-template <int WORDS> __device__ __forceinline__ void load_words(uint32_t *w, const uint16_t *p, bool on)
+template <int WORDS> __device__ __forceinline__ void lds_words(uint32_t (&w)[4], uint32_t addr)
 {
     if constexpr (WORDS == 2) {
-        const uint2 v = on ? __ldg(reinterpret_cast<const uint2 *>(p)) : make_uint2(0u, 0u);
-        w[0] = v.x;
-        w[1] = v.y;
+        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr));
+        w[2] = w[3] = 0u;
     } else {
-        const uint4 v = on ? __ldg(reinterpret_cast<const uint4 *>(p)) : make_uint4(0u, 0u, 0u, 0u);
-        w[0] = v.x;
-        w[1] = v.y;
-        w[2] = v.z;
-        w[3] = v.w;
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                     : "r"(addr));
     }
 }
 
-// A warp's CB blocks of 32 columns: product j (of four) of a block has as its column n
-// the logits' column 8 (n / 2) + 2 j + n % 2, so that lane q's eight results are eight
-// neighbours.
-template <int RP, int CB> struct Factor {
-    uint32_t w[CB][4][Ranks<RP>::GROUPS][Ranks<RP>::WORDS];
-    __device__ __forceinline__ void load(const uint16_t *B, int v0, int V, int R)
-    {
-        using K = Ranks<RP>;
-        const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-#pragma unroll
-        for (int c = 0; c < CB; ++c)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int v = v0 + c * 32 + 8 * (g >> 1) + 2 * j + (g & 1);
-                const uint16_t *row = B + static_cast<size_t>(min(v, V - 1)) * R;
-#pragma unroll
-                for (int k = 0; k < K::GROUPS; ++k) {
-                    const int r = k * 32 + q * K::STEP;
-                    load_words<K::WORDS>(w[c][j][k], row + (r < R ? r : 0), v < V && r < R);
-                }
-            }
-    }
+// Shared memory of a CTA of the map: a ring of tiles (16 rows of the slab and their t),
+// and two buffers for the slab of an adapter's factor.
+template <typename T, int RP, int PARTS, int CB> struct MapShape {
+    static constexpr int COLS = 256 * CB;                              // columns of a slab
+    static constexpr int ROW = COLS * static_cast<int>(sizeof(T)) + 64;   // bytes of a staged row: a warp's 16-byte reads meet no bank twice
+    static constexpr int TROW = (PARTS * RP + 8) * 2;
+    static constexpr int STAGE = 16 * (ROW + TROW);
+    static constexpr int FACTOR = COLS * RP * 2;
+    static constexpr int MOST = AD_MAP_SMEM - 256 - 2 * FACTOR;
+    static constexpr int STAGES = 4 * STAGE <= MOST ? 4 : 3;
+    static constexpr int BYTES = STAGES * STAGE + 2 * FACTOR + 256;
+    static_assert(BYTES <= AD_MAP_SMEM, "shared memory of a CTA");
+    static_assert(ROW % 16 == 0 && TROW % 16 == 0, "alignment");
 };
 
 // A CTA: row_chunk positions, 256 CB columns, eight warps of 32 CB columns (the CTAs
-// side by side in the grid share their rows).  A tile is 16 positions; the next tile's logits are in flight while a tile is
-// multiplied, and an adapter's factor stays in registers while the adapter is the same.
+// side by side in the grid share their rows), and a ninth that keeps the copies of the
+// next tiles and factors in flight.  Product j (of four) of 32 columns has as its column n
+// the logits' column 8 (n / 2) + 2 j + n % 2, so that lane q's eight results are eight
+// neighbours.
 template <typename T, int RP, int PARTS, int CB, bool AL>
 __global__ void __launch_bounds__(AD_MAP_THREADS) adapters_map_kernel(const AdapterArgs a)
 {
     using K = Ranks<RP>;
+    using S = MapShape<T, RP, PARTS, CB>;
+    constexpr int WARPS = AD_MAP_THREADS / 32 - 1;
+    constexpr int W = Elem<T>::WORDS;
+    extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int32_t s_row[AD_MAP_ROWS], s_ad[AD_MAP_ROWS + 1];
-    const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-    const int slabs = (a.V + 256 * CB - 1) / (256 * CB);
-    const int v0 = (blockIdx.x % slabs * 8 + (threadIdx.x >> 5)) * 32 * CB;
-    const int p0 = blockIdx.x / slabs * a.row_chunk;
+    const uint32_t base = smem_u32(smem), factor0 = base + S::STAGES * S::STAGE;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + S::STAGES * S::STAGE + 2 * S::FACTOR);
+    const uint32_t bar0 = smem_u32(bars);
+    auto full = [&](int i) { return bar0 + 8u * i; };
+    auto empty = [&](int i) { return bar0 + 8u * (S::STAGES + i); };
+    auto ffull = [&](int i) { return bar0 + 8u * (2 * S::STAGES + i); };
+    auto fempty = [&](int i) { return bar0 + 8u * (2 * S::STAGES + 2 + i); };
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(bars + 2 * S::STAGES + 4);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q = lane & 3;
+    const int slabs = (a.V + S::COLS - 1) / S::COLS;
+    const int c0 = static_cast<int>(blockIdx.x % slabs) * S::COLS, c1 = min(a.V, c0 + S::COLS);
+    const int p0 = static_cast<int>(blockIdx.x / slabs) * a.row_chunk;
+    if (tid == 0) {
+        for (int i = 0; i < S::STAGES; ++i) {
+            mbar_init(full(i), 1);
+            mbar_init(empty(i), WARPS);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(ffull(i), 1);
+            mbar_init(fempty(i), WARPS);
+        }
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
     pdl_wait();
     pdl_launch_dependents();
     const int live = a.in_place ? a.plan.offsets[a.n] : a.N;   // rows under no adapter come last
     const int rows = min(live - p0, a.row_chunk);
     if (rows <= 0)
         return;
-    for (int i = threadIdx.x; i < rows; i += AD_MAP_THREADS) {
+    for (int i = tid; i < rows; i += AD_MAP_THREADS) {
         s_row[i] = a.plan.perm[p0 + i];
         s_ad[i] = a.plan.adapter[p0 + i];
     }
-    if (threadIdx.x == 0)
+    if (tid == 0)
         s_ad[rows] = -1;
     __syncthreads();
-    if (v0 >= a.V)
-        return;
     const T *z = static_cast<const T *>(a.z);
-    T *out = static_cast<T *>(a.out);
+    const uint64_t budget = a.wait_budget_ns;
 
-    auto load = [&](Raw8<T> (&x)[2][CB], int p) {
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            const int i = p + g + half * 8;
-            if (i < rows) {
-                const T *row = z + static_cast<size_t>(s_row[i]) * a.ld;
-#pragma unroll
-                for (int c = 0; c < CB; ++c) {
-                    const int col = v0 + c * 32 + q * 8;
-                    if (col < a.V)
-                        load8<T>(x[half][c], row, col, a.V, AL ? 0u : row_shift(row));
+    if (warp == WARPS) {
+        // ------------------------------------------------------------ copies
+        const uint64_t pol = l2_policy_evict_first(), pol_keep = l2_policy_evict_normal();
+        int stage = 0, held = -1;   // held: the adapter of the last factor copied
+        uint32_t phase = 0, loads = 0;
+        bool ok = true;
+        for (int p = 0; ok && p < rows; p += 16) {
+            ok = mbar_wait_sleep(empty(stage), phase ^ 1u, abort_flag, budget);
+            if (!ok)
+                break;
+            const int m = min(16, rows - p);
+            const uint32_t dst = base + stage * S::STAGE;
+            RowCopy c{};
+            if (lane < m)
+                c = stage_row<T>(z + static_cast<size_t>(s_row[p + lane]) * a.ld, c0, c1, a.V, smem + stage * S::STAGE + lane * S::ROW);
+            const uint32_t tbytes = static_cast<uint32_t>(m) * S::TROW;
+            const uint32_t total = __reduce_add_sync(0xffffffffu, c.bytes) + tbytes;
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive_expect_tx(full(stage), total);
+            __syncwarp();
+            if (c.bytes)
+                bulk_load(dst + lane * S::ROW + c.off, c.src, c.bytes, full(stage), pol);
+            if (lane == 0)
+                bulk_load(dst + 16 * S::ROW, a.plan.t + static_cast<size_t>(p0 + p) * (S::TROW / 2), tbytes, full(stage), pol_keep);
+            if (++stage == S::STAGES) {
+                stage = 0;
+                phase ^= 1u;
+            }
+            // the factors of the adapters that begin in this tile
+            const int mine = lane < m ? s_ad[p + lane] : a.n;
+            const int before = lane == 0 ? held : lane < m ? s_ad[p + lane - 1] : mine;
+            unsigned starts = __ballot_sync(0xffffffffu, mine < a.n && mine != before);
+            while (starts) {
+                const int i = __ffs(starts) - 1;
+                starts &= starts - 1;
+                held = s_ad[p + i];
+                const int slot = loads & 1;
+                ok = mbar_wait_sleep(fempty(slot), ((loads >> 1) & 1u) ^ 1u, abort_flag, budget);
+                if (!ok)
+                    break;
+                if (lane == 0) {
+                    const uint32_t bytes = static_cast<uint32_t>(c1 - c0) * a.R * 2;
+                    mbar_arrive_expect_tx(ffull(slot), bytes);
+                    bulk_load(factor0 + slot * S::FACTOR, a.B + (static_cast<size_t>(held) * a.V + c0) * a.R, bytes, ffull(slot),
+                              pol_keep);
                 }
+                ++loads;
             }
         }
-    };
-    int ad = s_ad[0];
-    Factor<RP, CB> f;
-    if (ad < a.n)
-        f.load(a.B + static_cast<size_t>(ad) * a.V * a.R, v0, a.V, a.R);
-    Raw8<T> x[2][CB];
-    load(x, 0);
-    for (int p = 0; p < rows; p += 16) {
-        Raw8<T> y[2][CB];
+    } else {
+        // ------------------------------------------------------------ products
+        const int w0 = warp * 32 * CB;   // the warp's columns in the slab
+        T *out = static_cast<T *>(a.out);
+        int stage = 0, held = -1;
+        uint32_t phase = 0, taken = 0;   // factors taken
+        bool ok = true;
+        const uint32_t frow = static_cast<uint32_t>(a.R) * 2;
+        const uint32_t fcol = static_cast<uint32_t>(w0 + 8 * (g >> 1) + (g & 1)) * frow + q * (K::STEP * 2);
+        for (int p = 0; p < rows; p += 16) {
+            ok = mbar_wait_sleep(full(stage), phase, abort_flag, budget);
+            if (!ok)
+                break;
+            const uint32_t st = base + stage * S::STAGE, ts = st + 16 * S::ROW;
+            const int e = min(p + 16, rows);
+            float keep[CB][4][4] = {};
+            for (int s = p; s < e;) {
+                // the positions of this tile under one adapter: s .. m - 1
+                const int ad = s_ad[s];
+                int m = e;
+                if (s_ad[e - 1] != ad)
+                    for (m = s + 1; s_ad[m] == ad;)
+                        ++m;
+                if (ad < a.n) {
+                    if (ad != held) {
+                        __syncwarp();
+                        if (held >= 0 && lane == 0)
+                            mbar_arrive(fempty((taken - 1) & 1));
+                        held = ad;
+                        ok = mbar_wait_sleep(ffull(taken & 1), (taken >> 1) & 1u, abort_flag, budget);
+                        if (!ok)
+                            break;
+                        ++taken;
+                    }
+                    const uint32_t fs = factor0 + ((taken - 1) & 1) * S::FACTOR + fcol;
+                    float acc[CB][4][4] = {};
 #pragma unroll
-        for (int c = 0; c < CB; ++c) {
-            y[0][c] = x[0][c];
-            y[1][c] = x[1][c];
-        }
-        if (p + 16 < rows)
-            load(x, p + 16);
-        const int e = min(p + 16, rows);
-        const bool on0 = p + g < e, on1 = p + g + 8 < e;
-        uint32_t t[PARTS][K::GROUPS][2][K::WORDS];   // rows g and g + 8 of t
-        const uint16_t *t0 = a.plan.t + static_cast<size_t>(p0 + p + g) * (PARTS * RP);
-        const bool has0 = on0 && s_ad[p + g] < a.n, has1 = on1 && s_ad[p + g + 8] < a.n;
+                    for (int k = 0; k < K::GROUPS; ++k) {
+                        uint32_t t[PARTS][2][4];   // rows g and g + 8 of t
 #pragma unroll
-        for (int i = 0; i < PARTS; ++i)
+                        for (int i = 0; i < PARTS; ++i)
 #pragma unroll
-            for (int k = 0; k < K::GROUPS; ++k) {
-                const int r = i * RP + k * 32 + q * K::STEP;
-                load_words<K::WORDS>(t[i][k][0], t0 + r, has0);
-                load_words<K::WORDS>(t[i][k][1], t0 + 8 * (PARTS * RP) + r, has1);
-            }
-        float keep[CB][4][4] = {};
-        for (int s = p; s < e;) {
-            // the positions of this tile under the adapter at hand: s .. m - 1
-            int m = e;
-            if (s_ad[e - 1] != ad)
-                for (m = s + 1; s_ad[m] == ad;)
-                    ++m;
-            if (ad < a.n) {
-                float acc[CB][4][4] = {};
-#pragma unroll
-                for (int i = 0; i < PARTS; ++i)
-#pragma unroll
-                    for (int k = 0; k < K::STEPS; ++k) {
-                        const int grp = RP == 16 ? 0 : k / 2, w = RP == 16 ? 0 : (k % 2) * 2;
+                            for (int half = 0; half < 2; ++half)
+                                lds_words<K::WORDS>(t[i][half], ts + (g + half * 8) * S::TROW + (i * RP + k * 32 + q * K::STEP) * 2);
+                        const bool in = k * 32 + q * K::STEP < a.R;   // ranks past R: zeros
 #pragma unroll
                         for (int c = 0; c < CB; ++c)
 #pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                mma16816(acc[c][j],
-                                         {t[i][grp][0][w], t[i][grp][1][w], t[i][grp][0][w + 1], t[i][grp][1][w + 1]},
-                                         f.w[c][j][grp][w], f.w[c][j][grp][w + 1]);
+                            for (int j = 0; j < 4; ++j) {
+                                uint32_t f[4] = {0u, 0u, 0u, 0u};
+                                if (in)
+                                    lds_words<K::WORDS>(f, fs + static_cast<uint32_t>(c * 32 + 2 * j) * frow + k * 64);
+#pragma unroll
+                                for (int i = 0; i < PARTS; ++i) {
+                                    mma16816(acc[c][j], {t[i][0][0], t[i][1][0], t[i][0][1], t[i][1][1]}, f[0], f[1]);
+                                    if (K::WORDS == 4)
+                                        mma16816(acc[c][j], {t[i][0][2], t[i][1][2], t[i][0][3], t[i][1][3]}, f[2], f[3]);
+                                }
+                            }
                     }
-                const bool in0 = p + g >= s && p + g < m, in1 = p + g + 8 >= s && p + g + 8 < m;
+                    const bool in0 = p + g >= s && p + g < m, in1 = p + g + 8 >= s && p + g + 8 < m;
 #pragma unroll
-                for (int c = 0; c < CB; ++c)
+                    for (int c = 0; c < CB; ++c)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        keep[c][j][0] = in0 ? acc[c][j][0] : keep[c][j][0];
-                        keep[c][j][1] = in0 ? acc[c][j][1] : keep[c][j][1];
-                        keep[c][j][2] = in1 ? acc[c][j][2] : keep[c][j][2];
-                        keep[c][j][3] = in1 ? acc[c][j][3] : keep[c][j][3];
+                        for (int j = 0; j < 4; ++j) {
+                            keep[c][j][0] = in0 ? acc[c][j][0] : keep[c][j][0];
+                            keep[c][j][1] = in0 ? acc[c][j][1] : keep[c][j][1];
+                            keep[c][j][2] = in1 ? acc[c][j][2] : keep[c][j][2];
+                            keep[c][j][3] = in1 ? acc[c][j][3] : keep[c][j][3];
+                        }
+                }
+                s = m;
+            }
+            if (!ok)
+                break;
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const int i = p + g + half * 8;
+                const bool on = i < e, has = on && s_ad[on ? i : p] < a.n;
+                const int n = on ? s_row[i] : 0;
+                T *row = out + static_cast<size_t>(n) * a.ldo;
+                const bool any = !AL && __any_sync(0xffffffffu, row_shift(row) != 0);
+                const uint32_t shift = AL ? 0u : row_shift(z + static_cast<size_t>(n) * a.ld);
+#pragma unroll
+                for (int c = 0; c < CB; ++c) {
+                    const int col = c0 + w0 + c * 32 + q * 8;
+                    const uint8_t *src = smem + stage * S::STAGE + (g + half * 8) * S::ROW + (w0 + c * 32 + q * 8) * sizeof(T);
+                    Raw8<T> y;
+                    uint32_t x[W + 4];
+#pragma unroll
+                    for (int k = 0; k < W / 4 + (AL ? 0 : 1); ++k) {
+                        const uint4 v = reinterpret_cast<const uint4 *>(src)[k];
+                        x[4 * k] = v.x;
+                        x[4 * k + 1] = v.y;
+                        x[4 * k + 2] = v.z;
+                        x[4 * k + 3] = v.w;
                     }
+                    if (AL) {
+#pragma unroll
+                        for (int k = 0; k < W; ++k)
+                            y.w[k] = x[k];
+                    } else {
+                        shift_words<W, sizeof(T) == 2>(y.w, x, shift);
+                    }
+                    float v[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        v[k] = Elem<T>::get(y.w, k) + keep[c][k >> 1][2 * half + (k & 1)];
+                    Raw8<T> w = pack8<T>(v);
+                    if (!has)
+                        w = y;   // a row under no adapter keeps its bits
+                    store_quad<T>(row, col, a.V, w, on && col < a.V, any);
+                }
             }
-            s = m;
-            if (s_ad[m] >= 0 && s_ad[m] != ad) {   // (-1 behind the last position)
-                ad = s_ad[m];
-                if (ad < a.n)
-                    f.load(a.B + static_cast<size_t>(ad) * a.V * a.R, v0, a.V, a.R);
-            }
-        }
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            const bool on = half ? on1 : on0, has = half ? has1 : has0;
-            T *row = out + static_cast<size_t>(on ? s_row[p + g + half * 8] : 0) * a.ldo;
-            const bool any = !AL && __any_sync(0xffffffffu, row_shift(row) != 0);
-#pragma unroll
-            for (int c = 0; c < CB; ++c) {
-                float v[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    v[i] = Elem<T>::get(y[half][c].w, i) + keep[c][i >> 1][2 * half + (i & 1)];
-                Raw8<T> w = pack8<T>(v);
-                if (!has)
-                    w = y[half][c];   // a row under no adapter keeps its bits
-                const int col = v0 + c * 32 + q * 8;
-                store_quad<T>(row, col, a.V, w, on && col < a.V, any);
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(empty(stage));
+            if (++stage == S::STAGES) {
+                stage = 0;
+                phase ^= 1u;
             }
         }
     }
+    __syncthreads();
+    if (tid == 0 && *abort_flag) {
+        // copies may still be on their way: every stage's and buffer's last one lands, or not, within the wait
+        for (int i = 0; i < S::STAGES; ++i)
+            for (uint32_t f = 0; f < 2; ++f)
+                drain_wait(full(i), f, 100000000ull);
+        for (int i = 0; i < 2; ++i)
+            for (uint32_t f = 0; f < 2; ++f)
+                drain_wait(ffull(i), f, 100000000ull);
+        atomicCAS(a.status, 0, static_cast<int>(TIM_ERR_TIMEOUT));
+    }
 }
 
-template <typename F> cudaError_t launch(F kernel, dim3 grid, int threads, const AdapterArgs &a, cudaStream_t s)
+template <typename F>
+cudaError_t launch(F kernel, dim3 grid, int threads, int smem, const AdapterArgs &a, cudaStream_t s)
 {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1] = {pdl_attribute()};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
@@ -418,20 +513,35 @@ template <typename F> cudaError_t launch(F kernel, dim3 grid, int threads, const
 template <int PARTS> cudaError_t shrink(const AdapterArgs &a, dim3 grid, cudaStream_t s)
 {
     switch (ad_rank_pad(a.R)) {
-    case 16: return launch(adapters_shrink_kernel<16, PARTS>, grid, AD_SHRINK_THREADS, a, s);
-    case 32: return launch(adapters_shrink_kernel<32, PARTS>, grid, AD_SHRINK_THREADS, a, s);
-    case 64: return launch(adapters_shrink_kernel<64, PARTS>, grid, AD_SHRINK_THREADS, a, s);
-    default: return launch(adapters_shrink_kernel<128, PARTS>, grid, AD_SHRINK_THREADS, a, s);
+    case 16: return launch(adapters_shrink_kernel<16, PARTS>, grid, AD_SHRINK_THREADS, 0, a, s);
+    case 32: return launch(adapters_shrink_kernel<32, PARTS>, grid, AD_SHRINK_THREADS, 0, a, s);
+    case 64: return launch(adapters_shrink_kernel<64, PARTS>, grid, AD_SHRINK_THREADS, 0, a, s);
+    default: return launch(adapters_shrink_kernel<128, PARTS>, grid, AD_SHRINK_THREADS, 0, a, s);
     }
 }
 
-// Column blocks of a warp: 128 bytes of a row where the factor's registers allow it.
-template <typename T, int RP> constexpr int map_blocks() { return sizeof(T) == 2 && RP <= 32 ? 2 : 1; }
+// Blocks of 32 columns of a warp: 128 bytes of a row where two factors leave room for
+// two CTAs an SM.
+template <typename T, int RP> constexpr int map_blocks() { return sizeof(T) == 2 && RP == 16 ? 2 : 1; }
 
-template <typename T, int PARTS, int RP> cudaError_t map(AdapterArgs a, int num_sms, cudaStream_t s)
+template <typename T, int PARTS, int RP, bool AL> cudaError_t map(const AdapterArgs &a, dim3 grid, cudaStream_t s, bool set)
 {
-    constexpr int CB = map_blocks<T, RP>();
-    const int slabs = (a.V + 256 * CB - 1) / (256 * CB);
+    constexpr int CB = map_blocks<T, RP>(), BYTES = MapShape<T, RP, PARTS, CB>::BYTES;
+    auto kernel = adapters_map_kernel<T, RP, PARTS, CB, AL>;
+    if (set)
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, BYTES);
+    return launch(kernel, grid, AD_MAP_THREADS, BYTES, a, s);
+}
+
+// set: the kernels' shared memory is granted instead.
+template <typename T, int PARTS, int RP> cudaError_t map(AdapterArgs a, int num_sms, cudaStream_t s, bool set)
+{
+    if (set) {
+        const cudaError_t e = map<T, PARTS, RP, true>(a, dim3(1), s, true);
+        return e != cudaSuccess ? e : map<T, PARTS, RP, false>(a, dim3(1), s, true);
+    }
+    constexpr int COLS = 256 * map_blocks<T, RP>();
+    const int slabs = (a.V + COLS - 1) / COLS;
     // few rows: a tile a CTA, so that the adapters' factors come in parallel
     int64_t rows = AD_MAP_ROWS;
     while (rows > 16 && slabs * ((a.N + rows - 1) / rows) < int64_t(8) * num_sms)
@@ -442,21 +552,40 @@ template <typename T, int PARTS, int RP> cudaError_t map(AdapterArgs a, int num_
         return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && (N == 1 || ld * sizeof(T) % 16 == 0);
     };
     if (aligned(a.z, a.ld, a.N) && aligned(a.out, a.ldo, a.N))
-        return launch(adapters_map_kernel<T, RP, PARTS, CB, true>, grid, AD_MAP_THREADS, a, s);
-    return launch(adapters_map_kernel<T, RP, PARTS, CB, false>, grid, AD_MAP_THREADS, a, s);
+        return map<T, PARTS, RP, true>(a, grid, s, false);
+    return map<T, PARTS, RP, false>(a, grid, s, false);
 }
 
 template <typename T, int PARTS> cudaError_t map(const AdapterArgs &a, int num_sms, cudaStream_t s)
 {
     switch (ad_rank_pad(a.R)) {
-    case 16: return map<T, PARTS, 16>(a, num_sms, s);
-    case 32: return map<T, PARTS, 32>(a, num_sms, s);
-    case 64: return map<T, PARTS, 64>(a, num_sms, s);
-    default: return map<T, PARTS, 128>(a, num_sms, s);
+    case 16: return map<T, PARTS, 16>(a, num_sms, s, false);
+    case 32: return map<T, PARTS, 32>(a, num_sms, s, false);
+    case 64: return map<T, PARTS, 64>(a, num_sms, s, false);
+    default: return map<T, PARTS, 128>(a, num_sms, s, false);
     }
 }
 
+template <typename T, int PARTS> cudaError_t prepare()
+{
+    const AdapterArgs a{};
+    cudaError_t e = map<T, PARTS, 16>(a, 1, nullptr, true);
+    if (e == cudaSuccess)
+        e = map<T, PARTS, 32>(a, 1, nullptr, true);
+    if (e == cudaSuccess)
+        e = map<T, PARTS, 64>(a, 1, nullptr, true);
+    return e != cudaSuccess ? e : map<T, PARTS, 128>(a, 1, nullptr, true);
+}
+
 } // namespace
+
+cudaError_t adapters_prepare_device()
+{
+    cudaError_t e = prepare<float, 3>();
+    if (e == cudaSuccess)
+        e = prepare<__nv_bfloat16, 2>();
+    return e != cudaSuccess ? e : prepare<__half, 2>();
+}
 
 cudaError_t adapters_shrink_launch(AdapterArgs a, int parts, int num_sms, cudaStream_t s)
 {

@@ -33,4 +33,34 @@ template <int PARTS> __device__ __forceinline__ void split_bf16(float x, uint16_
     }
 }
 
+// Columns c0 .. c1 - 1 of a row of V on their way to shared memory at st (16-byte
+// aligned), where they keep their address's low bits: the aligned pieces inside the row
+// as one bulk copy, which the caller issues, the elements before and behind them at once
+// (no access leaves the row).  Ends with a fence towards the copies.
+struct RowCopy {
+    const char *src;
+    uint32_t off, bytes;   // into st + off
+};
+
+template <typename T> __device__ __forceinline__ RowCopy stage_row(const T *row, int c0, int c1, int V, uint8_t *st)
+{
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(row + c0), hi = reinterpret_cast<uintptr_t>(row + c1);
+    const uintptr_t from = lo & ~uintptr_t(15), end = reinterpret_cast<uintptr_t>(row + V);
+    uintptr_t x = from, y = (hi + 15) & ~uintptr_t(15);
+    if (x < reinterpret_cast<uintptr_t>(row))
+        x += 16;
+    if (y > end)
+        y = end & ~uintptr_t(15);
+    for (uintptr_t k = lo; k < min(hi, x); k += sizeof(T))
+        *reinterpret_cast<T *>(st + (k - from)) = *reinterpret_cast<const T *>(k);
+    for (uintptr_t k = max(lo, max(x, y)); k < hi; k += sizeof(T))
+        *reinterpret_cast<T *>(st + (k - from)) = *reinterpret_cast<const T *>(k);
+    fence_proxy_async_smem();
+    RowCopy c;
+    c.src = reinterpret_cast<const char *>(x);
+    c.off = static_cast<uint32_t>(x - from);
+    c.bytes = y > x ? static_cast<uint32_t>(y - x) : 0u;
+    return c;
+}
+
 } // namespace tim

@@ -169,39 +169,23 @@ __global__ void __launch_bounds__(THREADS, 1) adapters_grad_kernel(const Adapter
     auto fill = [&](int stage) {
         const int rows = min(STEP, mine.e - mine.p);
         const uint32_t dst = base + stage * S::STAGE;
-        uint32_t bytes = 0, off = 0;
-        const char *src = nullptr;
+        RowCopy c{};
         uint8_t *st = smem + stage * S::STAGE + lane * S::ROW;
         if (lane < rows) {
-            const T *row = dy + static_cast<size_t>(row_of) * a.ld;
-            const uintptr_t lo = reinterpret_cast<uintptr_t>(row + c0), hi = reinterpret_cast<uintptr_t>(row + c1);
-            const uintptr_t from = lo & ~uintptr_t(15);   // a staged row keeps its address's low bits
-            const uintptr_t end = reinterpret_cast<uintptr_t>(row + a.V);
-            uintptr_t x = from, y = (hi + 15) & ~uintptr_t(15);
-            if (x < reinterpret_cast<uintptr_t>(row))
-                x += 16;   // the row's first elements come one by one
-            if (y > end)
-                y = end & ~uintptr_t(15);
-            off = static_cast<uint32_t>(x - from);
-            bytes = y > x ? static_cast<uint32_t>(y - x) : 0u;
-            src = reinterpret_cast<const char *>(x);
-            for (uintptr_t k = lo; k < min(hi, x); k += sizeof(T))
-                *reinterpret_cast<T *>(st + (k - from)) = *reinterpret_cast<const T *>(k);
-            for (uintptr_t k = max(lo, max(x, y)); k < hi; k += sizeof(T))
-                *reinterpret_cast<T *>(st + (k - from)) = *reinterpret_cast<const T *>(k);
+            c = stage_row<T>(dy + static_cast<size_t>(row_of) * a.ld, c0, c1, a.V, st);
         } else if (lane < STEP && !RAW) {
             for (int k = 0; k < S::COLS * 2; k += 16)
                 *reinterpret_cast<uint4 *>(st + k) = make_uint4(0u, 0u, 0u, 0u);
+            fence_proxy_async_smem();
         }
         const uint32_t tbytes = static_cast<uint32_t>(rows) * trow;
-        const uint32_t total = __reduce_add_sync(0xffffffffu, bytes) + tbytes;
-        fence_proxy_async_smem();
+        const uint32_t total = __reduce_add_sync(0xffffffffu, c.bytes) + tbytes;
         __syncwarp();
         if (lane == 0)
             mbar_arrive_expect_tx(full(stage), total);
         __syncwarp();
-        if (bytes)
-            bulk_load(dst + lane * S::ROW + off, src, bytes, full(stage), pol);
+        if (c.bytes)
+            bulk_load(dst + lane * S::ROW + c.off, c.src, c.bytes, full(stage), pol);
         if (lane == 0)
             bulk_load(dst + STEP * S::ROW, a.plan.t + static_cast<size_t>(mine.p) * (trow / 2), tbytes, full(stage), pol_t);
         more = mine.skip(a, WARPS);

@@ -78,8 +78,9 @@ __device__ __forceinline__ int warp_scan(int x)   // inclusive
 __global__ void __launch_bounds__(EM_SORT_THREADS) embedding_sort_kernel(const EmbeddingArgs a)
 {
     constexpr int WARPS = EM_SORT_THREADS / 32;
-    static_assert(EM_RANGE == EM_SORT_THREADS, "a thread scans one id's counts");
-    __shared__ int counts[WARPS][EM_RANGE];   // a warp's tokens of each id, then where its next one goes
+    static_assert(EM_RANGE <= EM_SORT_THREADS, "a thread scans one id's counts");
+    extern __shared__ int counts_of[];
+    int (&counts)[WARPS][EM_RANGE] = *reinterpret_cast<int (*)[WARPS][EM_RANGE]>(counts_of);   // a warp's tokens of each id, then where its next one goes
     __shared__ int sb[WARPS], so[WARPS], sums[WARPS];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int lo = blockIdx.x * EM_RANGE, hi = min(a.V, lo + EM_RANGE);
@@ -113,7 +114,7 @@ __global__ void __launch_bounds__(EM_SORT_THREADS) embedding_sort_kernel(const E
     }
     at += base;
     if (own > 0) {
-#pragma unroll 4
+#pragma unroll 8
         for (int n = n0; n < n1; n += 32) {
             const int id = n + lane < n1 ? a.tokens[n + lane] : -1;
             const bool in = id >= lo && id < hi;
@@ -133,9 +134,11 @@ __global__ void __launch_bounds__(EM_SORT_THREADS) embedding_sort_kernel(const E
     __syncthreads();
     // where each id starts, and where each warp's tokens of it do
     int mine = 0;
+    if (tid < EM_RANGE) {
 #pragma unroll
-    for (int w = 0; w < WARPS; ++w)
-        mine += counts[w][tid];
+        for (int w = 0; w < WARPS; ++w)
+            mine += counts[w][tid];
+    }
     const int scan = warp_scan(mine);
     if (lane == 31)
         sums[warp] = scan;
@@ -146,11 +149,13 @@ __global__ void __launch_bounds__(EM_SORT_THREADS) embedding_sort_kernel(const E
         start += w < warp ? sums[w] : 0;
     if (lo + tid < hi)
         a.offsets[lo + tid] = start;
+    if (tid < EM_RANGE) {
 #pragma unroll
-    for (int w = 0; w < WARPS; ++w) {
-        const int c = counts[w][tid];
-        counts[w][tid] = start;
-        start += c;
+        for (int w = 0; w < WARPS; ++w) {
+            const int c = counts[w][tid];
+            counts[w][tid] = start;
+            start += c;
+        }
     }
     if (hi == a.V && tid == 0)
         a.offsets[a.V] = base + total;
@@ -290,20 +295,44 @@ __device__ __forceinline__ void sum_positions(float (&acc)[EM_PIECES][8], const 
     }
 }
 
-// Tiles of EM_TILE sorted positions: the part of a tile that belongs to an id of more
-// than EM_LONG tokens is summed into partial[tile][0] where the id goes on from the
-// tile before, into partial[tile][1] where it begins in the tile.
-template <typename T, bool VEC> __global__ void __launch_bounds__(256) embedding_tiles_kernel(const EmbeddingArgs a)
+// Two kinds of CTAs.  The first tile_ctas: tiles of EM_TILE sorted positions, a warp EM_COLS
+// columns of one: the part of a tile that belongs to an id of more than EM_LONG tokens is
+// summed into partial[tile][0] where the id goes on from the tile before, into
+// partial[tile][1] where it begins in the tile.  The others: zeros for the rows of dW that
+// no token has, EM_IDS rows a warp (nothing but stores, and a read of the offsets).
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(256, 3) embedding_tiles_kernel(const EmbeddingArgs a, int tile_ctas, int column_blocks)
 {
-    const int tile = blockIdx.x * 8 + (threadIdx.x >> 5);
-    const int col0 = blockIdx.y * EM_COLS;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     pdl_wait();
     pdl_launch_dependents();
-    const int total = a.offsets[a.V];
-    const int p0 = tile * EM_TILE;
-    if (p0 >= total)
+    if (blockIdx.x >= tile_ctas) {
+        const int id0 = (static_cast<int>(blockIdx.x - tile_ctas) * 8 + warp) * EM_IDS;
+        if (id0 >= a.V)
+            return;
+        const int at = lane <= EM_IDS ? a.offsets[min(a.V, id0 + lane)] : 0;
+        for (int i = 0; i < EM_IDS && id0 + i < a.V; ++i) {
+            if (__shfl_sync(0xffffffffu, at, i) != __shfl_sync(0xffffffffu, at, i + 1))
+                continue;
+            float *row = a.dW + static_cast<size_t>(id0 + i) * a.D;
+            if (VEC) {
+#pragma unroll 4
+                for (int c = lane * 4; c < a.D; c += 128)
+                    *reinterpret_cast<float4 *>(row + c) = make_float4(0.f, 0.f, 0.f, 0.f);
+            } else {
+#pragma unroll 4
+                for (int c = lane; c < a.D; c += 32)
+                    row[c] = 0.f;
+            }
+        }
         return;
-    const int p1 = min(total, p0 + EM_TILE);
+    }
+    const int unit = static_cast<int>(blockIdx.x) * 8 + warp;
+    const int tile = unit / column_blocks, col0 = unit % column_blocks * EM_COLS;
+    const int total = a.offsets[a.V];
+    if (tile >= (total + EM_TILE - 1) / EM_TILE)
+        return;
+    const int p0 = tile * EM_TILE, p1 = min(total, p0 + EM_TILE);
 #pragma unroll 1
     for (int k = 0; k < 2; ++k) {   // an id of more than EM_TILE tokens is the tile's first or its last
         const int id = a.ids[k == 0 ? p0 : p1 - 1];
@@ -316,10 +345,20 @@ template <typename T, bool VEC> __global__ void __launch_bounds__(256) embedding
     }
 }
 
-// One row of dW: the sum of the id's tokens (sorted positions b .. e - 1), or of its tiles.
-template <typename T, bool VEC>
-__device__ __forceinline__ void write_row(const EmbeddingArgs &a, int id, int b, int e, int col0)
+// Rows that have tokens, EM_COLS columns a warp: unit (position, columns); the warp takes
+// the id whose first sorted position that is, if there is one.
+template <typename T, bool VEC> __global__ void __launch_bounds__(256, 3) embedding_rows_kernel(const EmbeddingArgs a, int column_blocks)
 {
+    const int64_t unit = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    const int u = static_cast<int>(unit / column_blocks), col0 = static_cast<int>(unit % column_blocks) * EM_COLS;
+    pdl_wait();
+    pdl_launch_dependents();
+    if (u >= a.offsets[a.V])
+        return;
+    const int id = a.ids[u];
+    const int b = a.offsets[id], e = a.offsets[id + 1];
+    if (b != u)
+        return;
     float acc[EM_PIECES][8] = {};
     if (e - b > EM_LONG) {
         // the first tile's partial is in slot 1 (the id begins in it), the others' in slot 0
@@ -341,53 +380,26 @@ __device__ __forceinline__ void write_row(const EmbeddingArgs &a, int id, int b,
     put_row<VEC>(a.dW + static_cast<size_t>(id) * a.D, acc, col0, a.D, a.scale, a.accumulate);
 }
 
-// Every row of dW, EM_IDS a warp: zeros where no token has the id.
-template <typename T, bool VEC> __global__ void __launch_bounds__(256) embedding_all_rows_kernel(const EmbeddingArgs a)
-{
-    const int lane = threadIdx.x & 31;
-    const int id0 = (blockIdx.x * 8 + (threadIdx.x >> 5)) * EM_IDS;
-    const int col0 = blockIdx.y * EM_COLS;
-    pdl_wait();
-    pdl_launch_dependents();
-    if (id0 >= a.V)
-        return;
-    const int at = lane <= EM_IDS ? a.offsets[min(a.V, id0 + lane)] : 0;
-    for (int i = 0; i < EM_IDS && id0 + i < a.V; ++i)
-        write_row<T, VEC>(a, id0 + i, __shfl_sync(0xffffffffu, at, i), __shfl_sync(0xffffffffu, at, i + 1), col0);
-}
-
-// Rows that have tokens: warp u takes the id whose first sorted position is u, if there is one.
-template <typename T, bool VEC> __global__ void __launch_bounds__(256) embedding_used_rows_kernel(const EmbeddingArgs a)
-{
-    const int u = blockIdx.x * 8 + (threadIdx.x >> 5);
-    pdl_wait();
-    pdl_launch_dependents();
-    if (u >= a.offsets[a.V])
-        return;
-    const int id = a.ids[u];
-    const int b = a.offsets[id], e = a.offsets[id + 1];
-    if (b == u)
-        write_row<T, VEC>(a, id, b, e, blockIdx.y * EM_COLS);
-}
-
-template <typename F> cudaError_t launch(F kernel, dim3 grid, int threads, const EmbeddingArgs &a, cudaStream_t s)
+template <typename F, typename... Rest>
+cudaError_t launch(F kernel, int64_t ctas, int threads, int smem, cudaStream_t s, const EmbeddingArgs &a, Rest... rest)
 {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1] = {pdl_attribute()};
-    cfg.gridDim = grid;
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas), 1, 1);
     cfg.blockDim = dim3(threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, a);
+    return cudaLaunchKernelEx(&cfg, kernel, a, rest...);
 }
 
 template <typename TW, typename TO> cudaError_t lookup(const EmbeddingArgs &a, cudaStream_t s)
 {
     const int64_t units = static_cast<int64_t>(a.N) * ((a.D + 255) / 256);
     if (units <= 4096)   // few tokens: one piece a warp
-        return launch(embedding_kernel<TW, TO, 1>, dim3(static_cast<unsigned>((units + 7) / 8)), 256, a, s);
-    return launch(embedding_kernel<TW, TO, 4>, dim3(static_cast<unsigned>((units + 31) / 32)), 256, a, s);
+        return launch(embedding_kernel<TW, TO, 1>, (units + 7) / 8, 256, 0, s, a);
+    return launch(embedding_kernel<TW, TO, 4>, (units + 31) / 32, 256, 0, s, a);
 }
 
 template <typename TW> cudaError_t lookup_to(const EmbeddingArgs &a, int out_dtype, cudaStream_t s)
@@ -401,16 +413,17 @@ template <typename TW> cudaError_t lookup_to(const EmbeddingArgs &a, int out_dty
 
 template <typename T, bool VEC> cudaError_t sum(const EmbeddingArgs &a, cudaStream_t s)
 {
-    const unsigned ys = static_cast<unsigned>((a.D + EM_COLS - 1) / EM_COLS);
-    auto warps = [&](int64_t n) { return dim3(static_cast<unsigned>((n + 7) / 8), ys); };
-    cudaError_t e = cudaSuccess;
-    if (a.N > EM_LONG)
-        e = launch(embedding_tiles_kernel<T, VEC>, warps((a.N + EM_TILE - 1) / EM_TILE), 256, a, s);
-    if (e != cudaSuccess)
-        return e;
-    if (a.accumulate)
-        return launch(embedding_used_rows_kernel<T, VEC>, warps(a.N), 256, a, s);
-    return launch(embedding_all_rows_kernel<T, VEC>, warps((a.V + EM_IDS - 1) / EM_IDS), 256, a, s);
+    const int blocks = (a.D + EM_COLS - 1) / EM_COLS;
+    const int64_t tiles = a.N > EM_LONG ? (a.N + EM_TILE - 1) / EM_TILE : 0;
+    const int64_t tile_ctas = (tiles * blocks + 7) / 8;
+    const int64_t zero_ctas = a.accumulate ? 0 : (a.V + 8 * EM_IDS - 1) / (8 * EM_IDS);
+    if (tile_ctas + zero_ctas > 0) {
+        const cudaError_t e = launch(embedding_tiles_kernel<T, VEC>, tile_ctas + zero_ctas, 256, 0, s, a,
+                                     static_cast<int>(tile_ctas), blocks);
+        if (e != cudaSuccess)
+            return e;
+    }
+    return launch(embedding_rows_kernel<T, VEC>, (static_cast<int64_t>(a.N) * blocks + 7) / 8, 256, 0, s, a, blocks);
 }
 
 template <typename T> cudaError_t sum(const EmbeddingArgs &a, cudaStream_t s)
@@ -430,9 +443,16 @@ cudaError_t embedding_launch(const EmbeddingArgs &a, int dtype, int out_dtype, c
     return lookup_to<__half>(a, out_dtype, s);
 }
 
+constexpr int SORT_SMEM = EM_SORT_THREADS / 32 * EM_RANGE * static_cast<int>(sizeof(int));
+
+cudaError_t embedding_prepare_device()
+{
+    return cudaFuncSetAttribute(embedding_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SORT_SMEM);
+}
+
 cudaError_t embedding_sort_launch(const EmbeddingArgs &a, cudaStream_t s)
 {
-    return launch(embedding_sort_kernel, dim3(static_cast<unsigned>((a.V + EM_RANGE - 1) / EM_RANGE)), EM_SORT_THREADS, a, s);
+    return launch(embedding_sort_kernel, (a.V + EM_RANGE - 1) / EM_RANGE, EM_SORT_THREADS, SORT_SMEM, s, a);
 }
 
 cudaError_t embedding_sum_launch(const EmbeddingArgs &a, int dtype, cudaStream_t s)

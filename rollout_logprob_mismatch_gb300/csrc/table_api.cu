@@ -138,7 +138,9 @@ int tim_adapter_logits(const void *logits, int dtype, int64_t N, int64_t V, int6
     const int parts = dtype == TIM_F32 ? 3 : 2;
     const size_t b_off = tim::ws_round(sizeof(int32_t) * (static_cast<size_t>(a.n) + 2));
     const size_t b_n = tim::ws_round(sizeof(int32_t) * static_cast<size_t>(N));
-    a.plan.t_pitch = parts * tim::ad_rank_pad(a.R);
+    a.plan.t_pitch = parts * tim::ad_rank_pad(a.R) + 8;
+    a.wait_budget_ns = tim::pipeline_wait_budget_ns();
+    a.status = status;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     void *ws = nullptr;
     if ((rc = tim::workspace_alloc(&ws, b_off + 2 * b_n + static_cast<size_t>(N) * a.plan.t_pitch * 2, s)) != TIM_OK)

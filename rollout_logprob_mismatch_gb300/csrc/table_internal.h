@@ -20,8 +20,9 @@ constexpr int AD_MAX_RANK = 128;
 constexpr int AD_MAX_ADAPTERS = 65535;
 constexpr int AD_SHRINK_THREADS = 512;
 constexpr int AD_CHUNK = 64;         // rows of one adapter that a CTA projects at a time, at most
-constexpr int AD_MAP_THREADS = 256;  // eight warps
+constexpr int AD_MAP_THREADS = 288;  // eight warps of products, one of copies
 constexpr int AD_MAP_ROWS = 256;     // positions of a CTA of the map, at most
+constexpr int AD_MAP_SMEM = 224 * 1024;   // beside the lists of its rows
 
 // Ranks are padded to 16, 32, 64 or 128 inside the kernels (zeros).
 inline int ad_rank_pad(int64_t R) { return R <= 16 ? 16 : R <= 32 ? 32 : R <= 64 ? 64 : 128; }
@@ -51,12 +52,15 @@ struct AdapterArgs {
     int32_t in_place;
     int32_t chunk;            // shrink: rows at a time, 16 .. AD_CHUNK
     int32_t row_chunk;        // map: positions of a CTA, a multiple of 16
+    uint64_t wait_budget_ns;
+    int *status;
 };
 
 // Orders the rows and projects them: one launch.  parts: 2 or 3.
 cudaError_t adapters_shrink_launch(AdapterArgs a, int parts, int num_sms, cudaStream_t s);
 // out = z + t B^T
 cudaError_t adapters_expand_launch(AdapterArgs a, int dtype, int num_sms, cudaStream_t s);
+cudaError_t adapters_prepare_device();   // shared-memory sizes
 
 // The gradient: slabs of the vocabulary, steps of 16 rows.
 constexpr int AG_STEP = 16;
@@ -101,10 +105,10 @@ cudaError_t adapters_grad_prepare_device();
 
 // ---------------------------------------------------------------- embedding
 constexpr int EM_RANGE = 512;        // ids that one CTA of the sort orders
-constexpr int EM_SORT_THREADS = 512;
+constexpr int EM_SORT_THREADS = 1024;
 constexpr int EM_TILE = 32;          // sorted positions of a partial sum of a long row
 constexpr int EM_LONG = 64;          // tokens of an id above which its row is summed in tiles
-constexpr int EM_IDS = 8;            // rows of the table that a warp writes
+constexpr int EM_IDS = 4;            // rows of the table that a warp looks at for zeros
 
 struct EmbeddingArgs {
     const int32_t *tokens;    // [N]
@@ -122,6 +126,7 @@ struct EmbeddingArgs {
 };
 
 cudaError_t embedding_launch(const EmbeddingArgs &a, int dtype, int out_dtype, cudaStream_t s);
+cudaError_t embedding_prepare_device();   // shared-memory size of the sort
 cudaError_t embedding_sort_launch(const EmbeddingArgs &a, cudaStream_t s);
 cudaError_t embedding_sum_launch(const EmbeddingArgs &a, int dtype, cudaStream_t s);
 

@@ -111,6 +111,7 @@ int device_state(DeviceState **out)
         (e = tim::monitor_prepare_device()) != cudaSuccess || (e = tim::gemm_prepare_device()) != cudaSuccess ||
         (e = tim::logits_process_prepare_device()) != cudaSuccess ||
         (e = tim::distill_topk_prepare_device()) != cudaSuccess ||
+        (e = tim::embedding_prepare_device()) != cudaSuccess || (e = tim::adapters_prepare_device()) != cudaSuccess ||
         (e = tim::adapters_grad_prepare_device()) != cudaSuccess)
         return cuda_fail(e, "cudaFuncSetAttribute");
     if (!g_encode) {
