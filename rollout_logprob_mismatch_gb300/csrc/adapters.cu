@@ -4,7 +4,7 @@
 // logits, A_a [R, D] and B_a [V, R] the adapter's factors.  Two launches:
 //   shrink  orders the rows by adapter (a CTA counts the ids below its own and takes
 //           its own in order: no counter to clear, no atomics, the same order every
-//           time) and writes t_n = s_a A_a h_n in bf16 parts;
+//           time) and writes t_n = s_a A_a h_n in bf16 parts; two launches for many rows;
 //   map     y = z + t B^T, one pass over the logits.
 // A row's products are formed with its own adapter's factors only: where a tile of 16
 // rows meets several adapters, the tile is multiplied with each and every row keeps its
@@ -36,29 +36,24 @@ __device__ __forceinline__ void own_rows(const AdapterArgs &a, int ad, int r0, i
     }
 }
 
-// CTA (a, c): the rows of adapter a, chunks c, c + gridDim.y, ... of a.chunk of them.
-// a = n: the rows under no adapter (only ordered).  The 16 warps take a chunk's tiles of
-// 16 rows and share k among those of a tile, then add up through shared memory in order.
-template <int RP, int PARTS>
-__global__ void __launch_bounds__(AD_SHRINK_THREADS) adapters_shrink_kernel(const AdapterArgs a)
+// The warp's part [r0, r1) of the list of ids, and what lies before the rows of adapter
+// ad: the rows of lower adapters (base), in all (count), in the warps before (before).
+struct Own {
+    int r0, r1, own, base, count, before;
+};
+
+__device__ __forceinline__ Own count_rows(const AdapterArgs &a, int ad)
 {
     constexpr int WARPS = AD_SHRINK_THREADS / 32;
-    constexpr int NC = RP < 32 ? RP : 32;      // rank columns at a time
-    constexpr int AHEAD = 4;                   // steps of 32 k whose loads are in flight together
-    __shared__ int32_t mine[AD_CHUNK];
-    __shared__ float sums[WARPS][16][NC + 1];
     __shared__ int sb[WARPS], so[WARPS];
-    const int ad = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int g = lane >> 2, q = lane & 3;
-    pdl_wait();
-    pdl_launch_dependents();
-
-    // each warp has a part of the list, in order
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int per = ((a.N + 31) / 32 + WARPS - 1) / WARPS * 32;
-    const int r0 = min(a.N, warp * per), r1 = min(a.N, r0 + per);
+    Own o;
+    o.r0 = min(a.N, warp * per);
+    o.r1 = min(a.N, o.r0 + per);
     int below = 0, own = 0;
 #pragma unroll 8
-    for (int r = r0 + lane; r < r1; r += 32) {
+    for (int r = o.r0 + lane; r < o.r1; r += 32) {
         int id = a.rows[r];
         id = static_cast<unsigned>(id) < static_cast<unsigned>(a.n) ? id : a.n;
         below += id < ad;
@@ -71,97 +66,169 @@ __global__ void __launch_bounds__(AD_SHRINK_THREADS) adapters_shrink_kernel(cons
         so[warp] = own;
     }
     __syncthreads();
-    int base = 0, count = 0, before = 0;
+    o.own = own;
+    o.base = o.count = o.before = 0;
 #pragma unroll
     for (int w = 0; w < WARPS; ++w) {
-        base += sb[w];
-        count += so[w];
-        before += w < warp ? so[w] : 0;
+        o.base += sb[w];
+        o.count += so[w];
+        o.before += w < warp ? so[w] : 0;
     }
-    if (blockIdx.y == 0) {
-        if (tid == 0) {
-            a.plan.offsets[ad] = base;
-            if (ad == a.n)
-                a.plan.offsets[ad + 1] = a.N;
-        }
-        if (own > 0)
-            own_rows(a, ad, r0, r1, base + before, [&](int r, int p) {
-                a.plan.perm[p] = r;
-                a.plan.adapter[p] = ad;
-            });
+    return o;
+}
+
+__device__ __forceinline__ void write_order(const AdapterArgs &a, int ad, const Own &o)
+{
+    if (threadIdx.x == 0) {
+        a.plan.offsets[ad] = o.base;
+        if (ad == a.n)
+            a.plan.offsets[ad + 1] = a.N;
     }
-    if (ad == a.n)
-        return;
+    if (o.own > 0)
+        own_rows(a, ad, o.r0, o.r1, o.base + o.before, [&](int r, int p) {
+            a.plan.perm[p] = r;
+            a.plan.adapter[p] = ad;
+        });
+}
+
+// t of up to 16 MT rows under adapter ad, written for rows lo .. hi - 1 of them at
+// positions pos + lo ..  The eight warps share k (every eighth 32 of it each) and add up
+// through shared memory in their order, so that a row's sum depends on D alone.
+template <int RP, int PARTS, int MT>
+__device__ __forceinline__ void project(const AdapterArgs &a, int ad, const int32_t *rows, int lo, int hi, int pos)
+{
+    constexpr int WARPS = AD_SHRINK_THREADS / 32;
+    constexpr int NC = RP < 32 ? RP : 32;      // rank columns at a time
+    constexpr int AHEAD = MT == 1 ? 4 : 2;     // steps of 32 k whose loads are in flight together
+    __shared__ float sums[WARPS][16 * MT][NC + 1];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
     const float scale = a.scale ? a.scale[ad] : 1.f;
     const uint16_t *A = a.A + static_cast<size_t>(ad) * a.R * a.D;
     const int kchunks = (a.D + 31) / 32;
     const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+    const uint16_t *h[2 * MT];
+    bool on[2 * MT];
+#pragma unroll
+    for (int m = 0; m < 2 * MT; ++m) {
+        const int i = m * 8 + g;
+        on[m] = i >= lo && i < hi;
+        h[m] = a.h + static_cast<size_t>(on[m] ? rows[i] : 0) * a.D;
+    }
+    for (int n0 = 0; n0 < RP; n0 += NC) {
+        float acc[MT][NC / 8][4] = {};
+        if (n0 < a.R) {
+            for (int kc0 = warp; kc0 < kchunks; kc0 += WARPS * AHEAD) {
+                uint4 x[AHEAD][2 * MT], w[AHEAD][NC / 8];
+#pragma unroll
+                for (int i = 0; i < AHEAD; ++i) {
+                    const int k = (kc0 + i * WARPS) * 32 + q * 8;   // D is a multiple of 8: the eight are in or out together
+                    const bool in = k < a.D;
+#pragma unroll
+                    for (int m = 0; m < 2 * MT; ++m)
+                        x[i][m] = in && on[m] ? __ldg(reinterpret_cast<const uint4 *>(h[m] + k)) : zero;
+#pragma unroll
+                    for (int j = 0; j < NC / 8; ++j) {
+                        const int r = n0 + j * 8 + g;
+                        w[i][j] = in && r < a.R ? __ldg(reinterpret_cast<const uint4 *>(A + static_cast<size_t>(r) * a.D + k)) : zero;
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < AHEAD; ++i)
+#pragma unroll
+                    for (int m = 0; m < MT; ++m)
+#pragma unroll
+                        for (int j = 0; j < NC / 8; ++j) {
+                            const uint4 x0 = x[i][2 * m], x1 = x[i][2 * m + 1];
+                            mma16816(acc[m][j], {x0.x, x1.x, x0.y, x1.y}, w[i][j].x, w[i][j].y);
+                            mma16816(acc[m][j], {x0.z, x1.z, x0.w, x1.w}, w[i][j].z, w[i][j].w);
+                        }
+            }
+        }
+        __syncthreads();   // the sums before have been read
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int j = 0; j < NC / 8; ++j) {
+                sums[warp][m * 16 + g][j * 8 + 2 * q] = acc[m][j][0];
+                sums[warp][m * 16 + g][j * 8 + 2 * q + 1] = acc[m][j][1];
+                sums[warp][m * 16 + g + 8][j * 8 + 2 * q] = acc[m][j][2];
+                sums[warp][m * 16 + g + 8][j * 8 + 2 * q + 1] = acc[m][j][3];
+            }
+        __syncthreads();
+        for (int i = tid; i < (hi - lo) * NC; i += AD_SHRINK_THREADS) {
+            const int m = lo + i / NC, r = i % NC;
+            float u = 0.f;
+#pragma unroll
+            for (int w = 0; w < WARPS; ++w)
+                u += sums[w][m][r];
+            uint16_t p[PARTS];
+            split_bf16<PARTS>(u * scale, p);
+            uint16_t *t = a.plan.t + (static_cast<size_t>(pos) + m) * a.plan.t_pitch + n0 + r;
+#pragma unroll
+            for (int k = 0; k < PARTS; ++k)
+                t[k * RP] = p[k];
+        }
+    }
+}
 
-    for (int c = blockIdx.y; c * a.chunk < count; c += gridDim.y) {
-        const int c0 = c * a.chunk, rows = min(a.chunk, count - c0);
-        __syncthreads();   // the chunk before has been read
-        if (own > 0 && before < c0 + rows && before + own > c0)
-            own_rows(a, ad, r0, r1, before, [&](int r, int p) {
+// Few rows, one launch.  CTA (a, y): the rows of adapter a, 16 at a time from the y-th 16
+// on; a = n: the rows under no adapter (only ordered).
+template <int RP, int PARTS>
+__global__ void __launch_bounds__(AD_SHRINK_THREADS, 2) adapters_shrink_kernel(const AdapterArgs a)
+{
+    __shared__ int32_t mine[16];
+    const int ad = blockIdx.x;
+    pdl_wait();
+    pdl_launch_dependents();
+    const Own o = count_rows(a, ad);
+    if (blockIdx.y == 0)
+        write_order(a, ad, o);
+    if (ad == a.n)
+        return;
+    for (int c0 = blockIdx.y * 16; c0 < o.count; c0 += gridDim.y * 16) {
+        const int rows = min(16, o.count - c0);
+        if (o.own > 0 && o.before < c0 + rows && o.before + o.own > c0)
+            own_rows(a, ad, o.r0, o.r1, o.before, [&](int r, int p) {
                 if (p >= c0 && p < c0 + rows)
                     mine[p - c0] = r;
             });
         __syncthreads();
-        const int tiles = a.chunk / 16;             // 1, 2 or 4
-        const int m0 = (warp % tiles) * 16, kw = warp / tiles, ks = WARPS / tiles;
-        const bool on0 = m0 + g < rows, on1 = m0 + g + 8 < rows;
-        const uint16_t *h0 = a.h + static_cast<size_t>(on0 ? mine[m0 + g] : 0) * a.D;
-        const uint16_t *h1 = a.h + static_cast<size_t>(on1 ? mine[m0 + g + 8] : 0) * a.D;
-        for (int n0 = 0; n0 < RP; n0 += NC) {
-            float acc[NC / 8][4] = {};
-            if (m0 < rows && n0 < a.R) {
-                for (int kc0 = kw; kc0 < kchunks; kc0 += ks * AHEAD) {
-                    uint4 x0[AHEAD], x1[AHEAD], w[AHEAD][NC / 8];
-#pragma unroll
-                    for (int i = 0; i < AHEAD; ++i) {
-                        const int k = (kc0 + i * ks) * 32 + q * 8;   // D is a multiple of 8: the eight are in or out together
-                        const bool on = k < a.D;
-                        x0[i] = on && on0 ? __ldg(reinterpret_cast<const uint4 *>(h0 + k)) : zero;
-                        x1[i] = on && on1 ? __ldg(reinterpret_cast<const uint4 *>(h1 + k)) : zero;
-#pragma unroll
-                        for (int j = 0; j < NC / 8; ++j) {
-                            const int r = n0 + j * 8 + g;
-                            w[i][j] = on && r < a.R
-                                          ? __ldg(reinterpret_cast<const uint4 *>(A + static_cast<size_t>(r) * a.D + k))
-                                          : zero;
-                        }
-                    }
-#pragma unroll
-                    for (int i = 0; i < AHEAD; ++i)
-#pragma unroll
-                        for (int j = 0; j < NC / 8; ++j) {
-                            mma16816(acc[j], {x0[i].x, x1[i].x, x0[i].y, x1[i].y}, w[i][j].x, w[i][j].y);
-                            mma16816(acc[j], {x0[i].z, x1[i].z, x0[i].w, x1[i].w}, w[i][j].z, w[i][j].w);
-                        }
-                }
-            }
-            if (n0 > 0)
-                __syncthreads();   // the ranks before have been added up
-#pragma unroll
-            for (int j = 0; j < NC / 8; ++j) {
-                sums[warp][g][j * 8 + 2 * q] = acc[j][0];
-                sums[warp][g][j * 8 + 2 * q + 1] = acc[j][1];
-                sums[warp][g + 8][j * 8 + 2 * q] = acc[j][2];
-                sums[warp][g + 8][j * 8 + 2 * q + 1] = acc[j][3];
-            }
-            __syncthreads();
-            for (int i = tid; i < rows * NC; i += AD_SHRINK_THREADS) {
-                const int m = i / NC, r = i % NC;
-                float u = 0.f;
-                for (int w = m / 16; w < WARPS; w += tiles)
-                    u += sums[w][m % 16][r];
-                uint16_t p[PARTS];
-                split_bf16<PARTS>(u * scale, p);
-                uint16_t *t = a.plan.t + (static_cast<size_t>(base) + c0 + m) * a.plan.t_pitch + n0 + r;
-#pragma unroll
-                for (int k = 0; k < PARTS; ++k)
-                    t[k * RP] = p[k];
-            }
-        }
+        project<RP, PARTS, 1>(a, ad, mine, 0, rows, o.base + c0);
+        __syncthreads();
+    }
+}
+
+// Many rows: the order in a launch of its own, then a CTA for every 32 positions.
+__global__ void __launch_bounds__(AD_SHRINK_THREADS) adapters_order_kernel(const AdapterArgs a)
+{
+    pdl_wait();
+    pdl_launch_dependents();
+    const Own o = count_rows(a, blockIdx.x);
+    write_order(a, blockIdx.x, o);
+}
+
+template <int RP, int PARTS>
+__global__ void __launch_bounds__(AD_SHRINK_THREADS, 2) adapters_project_kernel(const AdapterArgs a)
+{
+    __shared__ int32_t s_row[32], s_ad[33];
+    pdl_wait();
+    pdl_launch_dependents();
+    const int p0 = blockIdx.x * 32, rows = min(32, a.plan.offsets[a.n] - p0);
+    if (rows <= 0)
+        return;
+    if (threadIdx.x < rows) {
+        s_row[threadIdx.x] = a.plan.perm[p0 + threadIdx.x];
+        s_ad[threadIdx.x] = a.plan.adapter[p0 + threadIdx.x];
+    }
+    if (threadIdx.x == 0)
+        s_ad[rows] = -1;
+    __syncthreads();
+    for (int s = 0; s < rows;) {
+        int m = s + 1;
+        while (s_ad[m] == s_ad[s])
+            ++m;
+        project<RP, PARTS, 2>(a, s_ad[s], s_row, s, m, p0);
+        s = m;
     }
 }
 
@@ -293,6 +360,14 @@ __global__ void __launch_bounds__(AD_MAP_THREADS) adapters_map_kernel(const Adap
         }
         *abort_flag = 0;
         fence_mbar_init();
+    }
+    if (warp == WARPS && lane < 16 && a.row_chunk == 16 && p0 + lane < a.N) {
+        // few rows: while they are projected, the factors' slabs (and the logits') of as many
+        // rows come into L2.  What the launches before the projection's wrote is there: it
+        // waited for them before it let this kernel start.
+        const int id = a.rows[p0 + lane];
+        if (static_cast<unsigned>(id) < static_cast<unsigned>(a.n))
+            bulk_prefetch(a.B + (static_cast<size_t>(id) * a.V + c0) * a.R, static_cast<uint32_t>(c1 - c0) * a.R * 2);
     }
     pdl_wait();
     pdl_launch_dependents();
@@ -510,13 +585,27 @@ cudaError_t launch(F kernel, dim3 grid, int threads, int smem, const AdapterArgs
     return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
-template <int PARTS> cudaError_t shrink(const AdapterArgs &a, dim3 grid, cudaStream_t s)
+template <int RP, int PARTS> cudaError_t shrink(const AdapterArgs &a, int num_sms, cudaStream_t s)
+{
+    if (a.N > AD_FEW_ROWS) {
+        const cudaError_t e = launch(adapters_order_kernel, dim3(static_cast<unsigned>(a.n + 1)), AD_SHRINK_THREADS, 0, a, s);
+        if (e != cudaSuccess)
+            return e;
+        return launch(adapters_project_kernel<RP, PARTS>, dim3(static_cast<unsigned>((a.N + 31) / 32)), AD_SHRINK_THREADS, 0,
+                      a, s);
+    }
+    const int ys = std::max(1, std::min((a.N + 15) / 16, (2 * num_sms + a.n) / (a.n + 1)));
+    return launch(adapters_shrink_kernel<RP, PARTS>, dim3(static_cast<unsigned>(a.n + 1), static_cast<unsigned>(ys)),
+                  AD_SHRINK_THREADS, 0, a, s);
+}
+
+template <int PARTS> cudaError_t shrink(const AdapterArgs &a, int num_sms, cudaStream_t s)
 {
     switch (ad_rank_pad(a.R)) {
-    case 16: return launch(adapters_shrink_kernel<16, PARTS>, grid, AD_SHRINK_THREADS, 0, a, s);
-    case 32: return launch(adapters_shrink_kernel<32, PARTS>, grid, AD_SHRINK_THREADS, 0, a, s);
-    case 64: return launch(adapters_shrink_kernel<64, PARTS>, grid, AD_SHRINK_THREADS, 0, a, s);
-    default: return launch(adapters_shrink_kernel<128, PARTS>, grid, AD_SHRINK_THREADS, 0, a, s);
+    case 16: return shrink<16, PARTS>(a, num_sms, s);
+    case 32: return shrink<32, PARTS>(a, num_sms, s);
+    case 64: return shrink<64, PARTS>(a, num_sms, s);
+    default: return shrink<128, PARTS>(a, num_sms, s);
     }
 }
 
@@ -587,17 +676,9 @@ cudaError_t adapters_prepare_device()
     return e != cudaSuccess ? e : prepare<__half, 2>();
 }
 
-cudaError_t adapters_shrink_launch(AdapterArgs a, int parts, int num_sms, cudaStream_t s)
+cudaError_t adapters_shrink_launch(const AdapterArgs &a, int parts, int num_sms, cudaStream_t s)
 {
-    // a CTA of 16 rows at a time while that does not give every SM more than two
-    a.chunk = 16;
-    while (a.chunk < AD_CHUNK && a.N > 2 * num_sms * a.chunk)
-        a.chunk *= 2;
-    // about two CTAs an SM in all: each reads the whole list of ids
-    const int chunks = (a.N + a.chunk - 1) / a.chunk;
-    const int ys = std::max(1, std::min(chunks, (2 * num_sms + a.n) / (a.n + 1)));
-    const dim3 grid(static_cast<unsigned>(a.n + 1), static_cast<unsigned>(ys), 1);
-    return parts == 3 ? shrink<3>(a, grid, s) : shrink<2>(a, grid, s);
+    return parts == 3 ? shrink<3>(a, num_sms, s) : shrink<2>(a, num_sms, s);
 }
 
 cudaError_t adapters_expand_launch(AdapterArgs a, int dtype, int num_sms, cudaStream_t s)

@@ -301,7 +301,7 @@ __device__ __forceinline__ void sum_positions(float (&acc)[EM_PIECES][8], const 
 // partial[tile][1] where it begins in the tile.  The others: zeros for the rows of dW that
 // no token has, EM_IDS rows a warp (nothing but stores, and a read of the offsets).
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(256, 3) embedding_tiles_kernel(const EmbeddingArgs a, int tile_ctas, int column_blocks)
+__global__ void __launch_bounds__(256, 2) embedding_tiles_kernel(const EmbeddingArgs a, int tile_ctas, int column_blocks)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     pdl_wait();
@@ -315,15 +315,16 @@ __global__ void __launch_bounds__(256, 3) embedding_tiles_kernel(const Embedding
             if (__shfl_sync(0xffffffffu, at, i) != __shfl_sync(0xffffffffu, at, i + 1))
                 continue;
             float *row = a.dW + static_cast<size_t>(id0 + i) * a.D;
-            if (VEC) {
+            // up to a 16-byte boundary, whole 16 bytes, the rest
+            const int head = VEC ? 0 : min(a.D, static_cast<int>((16 - (reinterpret_cast<uintptr_t>(row) & 15)) / 4 & 3));
+            const int whole = head + (a.D - head) / 4 * 4;
+            if (lane < head)
+                row[lane] = 0.f;
 #pragma unroll 4
-                for (int c = lane * 4; c < a.D; c += 128)
-                    *reinterpret_cast<float4 *>(row + c) = make_float4(0.f, 0.f, 0.f, 0.f);
-            } else {
-#pragma unroll 4
-                for (int c = lane; c < a.D; c += 32)
-                    row[c] = 0.f;
-            }
+            for (int c = head + lane * 4; c < whole; c += 128)
+                *reinterpret_cast<float4 *>(row + c) = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (whole + lane < a.D)
+                row[whole + lane] = 0.f;
         }
         return;
     }
@@ -345,39 +346,50 @@ __global__ void __launch_bounds__(256, 3) embedding_tiles_kernel(const Embedding
     }
 }
 
-// Rows that have tokens, EM_COLS columns a warp: unit (position, columns); the warp takes
-// the id whose first sorted position that is, if there is one.
-template <typename T, bool VEC> __global__ void __launch_bounds__(256, 3) embedding_rows_kernel(const EmbeddingArgs a, int column_blocks)
+// Rows that have tokens, EM_COLS columns a warp: unit (EM_FIRST positions, columns); the
+// warp takes the ids whose first sorted position is among them.
+constexpr int EM_FIRST = 8;
+
+template <typename T, bool VEC> __global__ void __launch_bounds__(256, 2) embedding_rows_kernel(const EmbeddingArgs a, int column_blocks)
 {
     const int64_t unit = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-    const int u = static_cast<int>(unit / column_blocks), col0 = static_cast<int>(unit % column_blocks) * EM_COLS;
+    const int u0 = static_cast<int>(unit / column_blocks) * EM_FIRST, col0 = static_cast<int>(unit % column_blocks) * EM_COLS;
+    const int lane = threadIdx.x & 31;
     pdl_wait();
     pdl_launch_dependents();
-    if (u >= a.offsets[a.V])
+    const int total = a.offsets[a.V];
+    if (u0 >= total)
         return;
-    const int id = a.ids[u];
-    const int b = a.offsets[id], e = a.offsets[id + 1];
-    if (b != u)
-        return;
-    float acc[EM_PIECES][8] = {};
-    if (e - b > EM_LONG) {
-        // the first tile's partial is in slot 1 (the id begins in it), the others' in slot 0
-        const int t1 = (e + EM_TILE - 1) / EM_TILE;
-        for (int t = b / EM_TILE; t < t1; t += EM_AHEAD) {
-            Pieces<float, VEC> r[EM_AHEAD];
-#pragma unroll
-            for (int i = 0; i < EM_AHEAD; ++i)
-                if (t + i < t1)
-                    r[i].load(a.partial + (static_cast<size_t>(t + i) * 2 + ((t + i) * EM_TILE <= b)) * a.D, col0, a.D);
-#pragma unroll
-            for (int i = 0; i < EM_AHEAD; ++i)
-                if (t + i < t1)
-                    r[i].add_to(acc);
-        }
-    } else {
-        sum_positions<T, VEC>(acc, a, b, e, col0);
+    int my_id = 0, my_b = -1, my_e = 0;
+    if (lane < EM_FIRST && u0 + lane < total) {
+        my_id = a.ids[u0 + lane];
+        my_b = a.offsets[my_id];
+        my_e = a.offsets[my_id + 1];
     }
-    put_row<VEC>(a.dW + static_cast<size_t>(id) * a.D, acc, col0, a.D, a.scale, a.accumulate);
+    for (unsigned first = __ballot_sync(0xffffffffu, my_b == u0 + lane); first; first &= first - 1) {
+        const int from = __ffs(first) - 1;
+        const int id = __shfl_sync(0xffffffffu, my_id, from);
+        const int b = u0 + from, e = __shfl_sync(0xffffffffu, my_e, from);
+        float acc[EM_PIECES][8] = {};
+        if (e - b > EM_LONG) {
+            // the first tile's partial is in slot 1 (the id begins in it), the others' in slot 0
+            const int t1 = (e + EM_TILE - 1) / EM_TILE;
+            for (int t = b / EM_TILE; t < t1; t += EM_AHEAD) {
+                Pieces<float, VEC> r[EM_AHEAD];
+#pragma unroll
+                for (int i = 0; i < EM_AHEAD; ++i)
+                    if (t + i < t1)
+                        r[i].load(a.partial + (static_cast<size_t>(t + i) * 2 + ((t + i) * EM_TILE <= b)) * a.D, col0, a.D);
+#pragma unroll
+                for (int i = 0; i < EM_AHEAD; ++i)
+                    if (t + i < t1)
+                        r[i].add_to(acc);
+            }
+        } else {
+            sum_positions<T, VEC>(acc, a, b, e, col0);
+        }
+        put_row<VEC>(a.dW + static_cast<size_t>(id) * a.D, acc, col0, a.D, a.scale, a.accumulate);
+    }
 }
 
 template <typename F, typename... Rest>
@@ -423,7 +435,8 @@ template <typename T, bool VEC> cudaError_t sum(const EmbeddingArgs &a, cudaStre
         if (e != cudaSuccess)
             return e;
     }
-    return launch(embedding_rows_kernel<T, VEC>, (static_cast<int64_t>(a.N) * blocks + 7) / 8, 256, 0, s, a, blocks);
+    return launch(embedding_rows_kernel<T, VEC>, (static_cast<int64_t>((a.N + EM_FIRST - 1) / EM_FIRST) * blocks + 7) / 8, 256, 0,
+                  s, a, blocks);
 }
 
 template <typename T> cudaError_t sum(const EmbeddingArgs &a, cudaStream_t s)

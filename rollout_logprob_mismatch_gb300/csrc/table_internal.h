@@ -18,8 +18,8 @@ inline size_t ws_round(size_t x) { return (x + 255) / 256 * 256; }
 // ---------------------------------------------------------------- adapters
 constexpr int AD_MAX_RANK = 128;
 constexpr int AD_MAX_ADAPTERS = 65535;
-constexpr int AD_SHRINK_THREADS = 512;
-constexpr int AD_CHUNK = 64;         // rows of one adapter that a CTA projects at a time, at most
+constexpr int AD_SHRINK_THREADS = 256;
+constexpr int AD_FEW_ROWS = 1024;    // rows up to which they are ordered and projected in one launch
 constexpr int AD_MAP_THREADS = 288;  // eight warps of products, one of copies
 constexpr int AD_MAP_ROWS = 256;     // positions of a CTA of the map, at most
 constexpr int AD_MAP_SMEM = 224 * 1024;   // beside the lists of its rows
@@ -50,14 +50,13 @@ struct AdapterArgs {
     void *out;
     int64_t ldo;
     int32_t in_place;
-    int32_t chunk;            // shrink: rows at a time, 16 .. AD_CHUNK
     int32_t row_chunk;        // map: positions of a CTA, a multiple of 16
     uint64_t wait_budget_ns;
     int *status;
 };
 
-// Orders the rows and projects them: one launch.  parts: 2 or 3.
-cudaError_t adapters_shrink_launch(AdapterArgs a, int parts, int num_sms, cudaStream_t s);
+// Orders the rows and projects them.  parts: 2 or 3.
+cudaError_t adapters_shrink_launch(const AdapterArgs &a, int parts, int num_sms, cudaStream_t s);
 // out = z + t B^T
 cudaError_t adapters_expand_launch(AdapterArgs a, int dtype, int num_sms, cudaStream_t s);
 cudaError_t adapters_prepare_device();   // shared-memory sizes
