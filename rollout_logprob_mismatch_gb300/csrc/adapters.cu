@@ -163,12 +163,23 @@ __device__ __forceinline__ void project(const AdapterArgs &a, int ad, const int3
                 u += sums[w][m][r];
             uint16_t p[PARTS];
             split_bf16<PARTS>(u * scale, p);
-            uint16_t *t = a.plan.t + (static_cast<size_t>(pos) + m) * a.plan.t_pitch + n0 + r;
+            uint16_t *t = a.plan.t + (static_cast<size_t>(pos) + static_cast<size_t>(ad) * a.plan.t_pad + m) * a.plan.t_pitch + n0 + r;
 #pragma unroll
             for (int k = 0; k < PARTS; ++k)
                 t[k * RP] = p[k];
         }
     }
+}
+
+// The zeros behind the last of an adapter's `count` rows, whose positions end at `end`.
+__device__ __forceinline__ void pad_rows(const AdapterArgs &a, int ad, int count, int end)
+{
+    if (a.plan.t_pad == 0)
+        return;
+    const int words = (-count & (AG_PAD - 1)) * (a.plan.t_pitch / 2);
+    uint32_t *t = reinterpret_cast<uint32_t *>(a.plan.t + (static_cast<size_t>(end) + static_cast<size_t>(ad) * a.plan.t_pad) * a.plan.t_pitch);
+    for (int i = threadIdx.x; i < words; i += AD_SHRINK_THREADS)
+        t[i] = 0u;
 }
 
 // Few rows, one launch.  CTA (a, y): the rows of adapter a, 16 at a time from the y-th 16
@@ -194,6 +205,8 @@ __global__ void __launch_bounds__(AD_SHRINK_THREADS, 2) adapters_shrink_kernel(c
             });
         __syncthreads();
         project<RP, PARTS, 1>(a, ad, mine, 0, rows, o.base + c0);
+        if (c0 + rows == o.count)
+            pad_rows(a, ad, o.count, o.base + o.count);
         __syncthreads();
     }
 }
@@ -228,6 +241,9 @@ __global__ void __launch_bounds__(AD_SHRINK_THREADS, 2) adapters_project_kernel(
         while (s_ad[m] == s_ad[s])
             ++m;
         project<RP, PARTS, 2>(a, s_ad[s], s_row, s, m, p0);
+        const int ad = s_ad[s], e = a.plan.offsets[ad + 1];
+        if (p0 + m == e)
+            pad_rows(a, ad, e - a.plan.offsets[ad], e);
         s = m;
     }
 }
@@ -392,7 +408,7 @@ __global__ void __launch_bounds__(AD_MAP_THREADS) adapters_map_kernel(const Adap
         uint32_t phase = 0, loads = 0;
         bool ok = true;
         for (int p = 0; ok && p < rows; p += 16) {
-            ok = mbar_wait_sleep(empty(stage), phase ^ 1u, abort_flag, budget);
+            ok = warp_wait(empty(stage), phase ^ 1u, abort_flag, budget);
             if (!ok)
                 break;
             const int m = min(16, rows - p);
@@ -423,7 +439,7 @@ __global__ void __launch_bounds__(AD_MAP_THREADS) adapters_map_kernel(const Adap
                 starts &= starts - 1;
                 held = s_ad[p + i];
                 const int slot = loads & 1;
-                ok = mbar_wait_sleep(fempty(slot), ((loads >> 1) & 1u) ^ 1u, abort_flag, budget);
+                ok = warp_wait(fempty(slot), ((loads >> 1) & 1u) ^ 1u, abort_flag, budget);
                 if (!ok)
                     break;
                 if (lane == 0) {
@@ -445,7 +461,7 @@ __global__ void __launch_bounds__(AD_MAP_THREADS) adapters_map_kernel(const Adap
         const uint32_t frow = static_cast<uint32_t>(a.R) * 2;
         const uint32_t fcol = static_cast<uint32_t>(w0 + 8 * (g >> 1) + (g & 1)) * frow + q * (K::STEP * 2);
         for (int p = 0; p < rows; p += 16) {
-            ok = mbar_wait_sleep(full(stage), phase, abort_flag, budget);
+            ok = warp_wait(full(stage), phase, abort_flag, budget);
             if (!ok)
                 break;
             const uint32_t st = base + stage * S::STAGE, ts = st + 16 * S::ROW;
@@ -464,7 +480,7 @@ __global__ void __launch_bounds__(AD_MAP_THREADS) adapters_map_kernel(const Adap
                         if (held >= 0 && lane == 0)
                             mbar_arrive(fempty((taken - 1) & 1));
                         held = ad;
-                        ok = mbar_wait_sleep(ffull(taken & 1), (taken >> 1) & 1u, abort_flag, budget);
+                        ok = warp_wait(ffull(taken & 1), (taken >> 1) & 1u, abort_flag, budget);
                         if (!ok)
                             break;
                         ++taken;

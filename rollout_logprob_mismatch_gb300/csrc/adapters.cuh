@@ -33,6 +33,13 @@ template <int PARTS> __device__ __forceinline__ void split_bf16(float x, uint16_
     }
 }
 
+// A whole warp waits for a barrier's phase; the same answer in every lane (false: some
+// lane's wait ran out, or another role's did), so that the warp leaves its loops together.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *abort, uint64_t budget_ns)
+{
+    return __all_sync(0xffffffffu, mbar_wait_sleep(bar, parity, abort, budget_ns));
+}
+
 // Columns c0 .. c1 - 1 of a row of V on their way to shared memory at st (16-byte
 // aligned), where they keep their address's low bits: the aligned pieces inside the row
 // as one bulk copy, which the caller issues, the elements before and behind them at once

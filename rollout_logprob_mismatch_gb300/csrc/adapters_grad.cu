@@ -6,16 +6,19 @@
 //   dA_a = sum_i du_i h_i^T        [R, D]
 //   dh_i (+)= A_a^T du_i           [D]
 // dy is by far the largest operand and is read once: a CTA owns a slab of the vocabulary
-// and walks all rows, adapter by adapter in steps of 16, so that dB's part of the slab
-// stays in registers until the adapter's last row, and du of a step (the slab's part of
-// the sum over V) goes to a partial array that a second launch folds in slab order.
-// The eight warps split the slab's columns (mma.sync, bf16 operands, fp32 sums) and take
-// turns to refill the ring of stages, with bulk copies of the rows' slabs and of t, after
-// the one barrier of a step; a ninth warp for the copies would hold every thread to 168
-// registers, too few for dB.  The adapter's factor comes by 16-byte asynchronous copies.
-// Both products take the same tile from shared memory, dB with it transposed.  bf16 rows
-// that start on 16 bytes are used as they land; others (fp16, fp32, odd rows) are first
-// rewritten as one or two planes of bf16 parts: x = hi + lo leaves at most 2^-16 |x|.
+// (up to 1024 columns) and walks all rows, adapter by adapter in steps of 128, so that
+// dB's part of the slab stays in TMEM until the adapter's last row, and du of a step (the
+// slab's part of the sum over V) goes to a partial array that a second launch folds in
+// slab order.  Both products take the same tile [128 rows x 128 columns] from shared
+// memory (tcgen05.mma, bf16 -> fp32): du with the rows as M and the columns as K
+// (K-major), dB with the columns as M and the rows as K (MN-major, the same bytes).
+//   warp 0      copies: dy's rows by TMA gathers (the rows of an adapter lie anywhere),
+//               the adapter's factor and t by TMA tiles
+//   warp 1      one thread issues the products
+//   warps 2-5   du and dB from TMEM to memory
+//   warps 6-13  fp32, fp16 or rows off a 16-byte boundary only (RAW): the tile from plain
+//               loads, as one or two planes of bf16 parts, x = hi + lo leaves at most
+//               2^-16 |x|
 // Every sum has one order, fixed by the rows' order and V: the same call gives the same bits.
 #include <algorithm>
 #include <type_traits>
@@ -26,38 +29,41 @@
 namespace tim {
 namespace {
 
-constexpr int WARPS = 8, STEP = AG_STEP;
-constexpr int THREADS = WARPS * 32;
+constexpr int BC = AG_BLOCK;            // columns of a tile
+constexpr int STEP = AG_STEP;           // rows of a tile
+constexpr int SUB = STEP * 128;         // bytes of 64 columns of a tile
+constexpr int PARTS = 2;                // of t
 
-// Shared-memory layout and sizes of a variant.  RAW: stages hold rows as they are in
-// memory (type T, any alignment) and are rewritten as planes; else they are bf16 rows.
-template <typename T, bool RAW, int RP, int COLUMNS> struct Shape {
-    static constexpr int COLS = COLUMNS;
-    static constexpr int CW = COLS / WARPS;                    // columns of a warp
+template <typename T, bool RAW, int RP> struct Shape {
     static constexpr int PLANES = std::is_same<T, __nv_bfloat16>::value ? 1 : 2;
-    static constexpr int ROW = COLS * static_cast<int>(sizeof(T)) + 16;   // bytes of a staged row
-    static constexpr int PROW = COLS * 2 + 16;                 // bytes of a plane's row
-    static constexpr int TROW = ag_t_pitch(RP == 64 ? 128 : RP) * 2;   // bytes of a row of t at most
-    static constexpr int STAGE = STEP * (ROW + TROW);
-    static constexpr int STAGES = 3;
-    static constexpr int FROW = RP * 2 + 16;                   // bytes of a row of the factor
-    static constexpr int FACTOR = COLS * FROW;
-    static constexpr int RED = WARPS * STEP * (RP + 4) * 4;    // du's parts of the warps
-    static constexpr int PLANE = RAW ? PLANES * STEP * PROW : 0;
-    static constexpr int FIXED = PLANE + 2 * RED + 256;
-    static constexpr int FACTORS = STAGES * STAGE + 2 * FACTOR + FIXED <= AG_SMEM ? 2 : 1;
-    static constexpr int BYTES = STAGES * STAGE + FACTORS * FACTOR + FIXED;
-    static_assert(BYTES <= AG_SMEM, "shared memory of a CTA");
-    static_assert(STAGE % 16 == 0 && FACTOR % 16 == 0 && RED % 16 == 0 && PLANE % 16 == 0, "alignment");
+    static constexpr int SPAN = RP * 2;                        // bytes of a row of the factor, or of a part of t
+    static constexpr int BLOCKS = ag_blocks(RP);               // tiles of a slab at most
+    static constexpr int TILE = 2 * SUB * PLANES;
+    static constexpr int FACTOR = BLOCKS * BC * SPAN;
+    static constexpr int TT = PARTS * STEP * SPAN;
+    static constexpr int FACTORS = RP == 16 ? 2 : 1;
+    static constexpr int TS = RP == 64 && PLANES == 2 ? 1 : 2;
+    static constexpr int ROOM = AG_SMEM - 2048 - FACTORS * FACTOR - TS * TT;
+    static constexpr int STAGES = ROOM / TILE < 4 ? ROOM / TILE : 4;
+    static constexpr int BYTES = AG_SMEM;
+    static constexpr int CONVERT = RAW ? 8 : 0;                // warps that write tiles
+    static constexpr int THREADS = (6 + CONVERT) * 32;
+    static constexpr uint32_t TMEM = (2 + BLOCKS) * RP <= 256 ? 256 : 512;   // du twice, dB's blocks
+    static_assert(STAGES >= 2 && (2 + BLOCKS) * RP <= 512, "shared memory, TMEM");
 };
 
-__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr)
-{
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr)
-                 : "memory");
-}
+// An adapter's positions [begin, end) of a part [p0, p1) of the batch: parts meet at a
+// multiple of 16 rows of the adapter (t has zeros behind its last row only).
+struct Part {
+    int begin, end;
+    __device__ __forceinline__ Part(int first, int last, int p0, int p1)
+        : begin(min(last, cut(first, p0))), end(min(last, cut(first, p1)))
+    {
+    }
+    static __device__ __forceinline__ int cut(int first, int p) { return p <= first ? first : first + (p - first + 15) / 16 * 16; }
+};
+
+// ldmatrix, for the smaller products below
 __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr)
 {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -66,344 +72,394 @@ __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr)
                  : "memory");
 }
 
-// 16 bytes global -> shared (zeros where n = 0), counted by cp_async_arrive.
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, uint32_t n)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src)), "r"(n)
-                 : "memory");
-}
-// One arrival on `bar` when this thread's asynchronous copies so far have landed.
-__device__ __forceinline__ void cp_async_arrive(uint32_t bar)
-{
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
-}
-
-// The steps of a launch in order: STEP positions (fewer at an adapter's end) of one
-// adapter.
-struct Cursor {
-    int ad, p, e;
-    // the first step; false if there is none
-    __device__ __forceinline__ bool start(const AdapterGradArgs &a)
+// A ring's place: its slot, and the parity of the slot's current use.
+template <int SLOTS> struct Ring {
+    int slot = 0;
+    uint32_t parity = 0;
+    __device__ __forceinline__ void next()
     {
-        ad = -1;
-        return seek(a);
-    }
-    __device__ __forceinline__ bool seek(const AdapterGradArgs &a)   // the next adapter with positions
-    {
-        while (++ad < a.n) {
-            p = max(a.plan.offsets[ad], a.p0);
-            e = min(a.plan.offsets[ad + 1], a.p1);
-            if (p < e)
-                return true;
+        if (++slot == SLOTS) {
+            slot = 0;
+            parity ^= 1u;
         }
-        return false;
-    }
-    __device__ __forceinline__ bool skip(const AdapterGradArgs &a, int steps)
-    {
-        while (steps > 0) {
-            const int here = (e - p + STEP - 1) / STEP;   // steps left of this adapter, this one included
-            if (steps < here) {
-                p += steps * STEP;
-                return true;
-            }
-            steps -= here;
-            if (!seek(a))
-                return false;
-        }
-        return true;
     }
 };
 
-template <typename T, bool RAW, int RP, int COLUMNS>
-__global__ void __launch_bounds__(THREADS, 1) adapters_grad_kernel(const AdapterGradArgs a)
+template <int RP> __device__ __forceinline__ void tmem_row(uint32_t taddr, float (&v)[RP])
 {
-    using S = Shape<T, RAW, RP, COLUMNS>;
-    constexpr int CW = S::CW, MB = CW / 16, RB = RP / 8, PARTS = 2;
-    extern __shared__ __align__(16) uint8_t smem[];
-    const uint32_t base = smem_u32(smem);
-    const uint32_t factor0 = base + S::STAGES * S::STAGE, plane0 = factor0 + S::FACTORS * S::FACTOR;
-    uint8_t *red0 = smem + (plane0 - base) + S::PLANE;
-    uint64_t *bars = reinterpret_cast<uint64_t *>(red0 + 2 * S::RED);
-    const uint32_t bar0 = smem_u32(bars);
-    auto full = [&](int i) { return bar0 + 8u * i; };
-    auto ffull = [&](int i) { return bar0 + 8u * (S::STAGES + i); };
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(bars + S::STAGES + 2);
-
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q = lane & 3;
-    const int c0 = blockIdx.x * S::COLS, c1 = min(a.V, c0 + S::COLS);   // the slab's columns
-    if (tid == 0) {
-        for (int i = 0; i < S::STAGES; ++i)
-            mbar_init(full(i), 1);
-        for (int i = 0; i < 2; ++i)
-            mbar_init(ffull(i), THREADS);
-        *abort_flag = 0;
-        fence_mbar_init();
-    }
-    if (!RAW) {
-        // columns past the row's last whole 16 bytes are zeros: nothing below writes there
-        // but a row's last elements
-        const int whole = (c1 - c0) / 8 * 16;
-        for (int i = tid; i < S::STAGES * STEP; i += THREADS)
-            for (int b = whole; b < S::COLS * 2; b += 16)
-                *reinterpret_cast<uint4 *>(smem + (i / STEP) * S::STAGE + (i % STEP) * S::ROW + b) = make_uint4(0u, 0u, 0u, 0u);
-        fence_proxy_async_smem();
-    }
-    __syncthreads();
-    pdl_wait();
-    pdl_launch_dependents();
-    const uint64_t budget = a.wait_budget_ns;
-    const T *dy = static_cast<const T *>(a.dy);
-    const uint32_t trow = static_cast<uint32_t>(ag_t_pitch(a.RT)) * 2;
-    const uint64_t pol = l2_policy_evict_first(), pol_t = l2_policy_evict_last();
-
-    // Each warp fills every eighth step, and has its next one's rows at hand.
-    Cursor mine;
-    bool more = mine.start(a) && mine.skip(a, warp);
-    int row_of = 0;
-    auto look_up = [&] {
-        if (more && lane < min(STEP, mine.e - mine.p))
-            row_of = a.plan.perm[mine.p + lane];
-    };
-    look_up();
-    // One warp: bulk copies of its next step's rows and of their t into a stage.
-    auto fill = [&](int stage) {
-        const int rows = min(STEP, mine.e - mine.p);
-        const uint32_t dst = base + stage * S::STAGE;
-        RowCopy c{};
-        uint8_t *st = smem + stage * S::STAGE + lane * S::ROW;
-        if (lane < rows) {
-            c = stage_row<T>(dy + static_cast<size_t>(row_of) * a.ld, c0, c1, a.V, st);
-        } else if (lane < STEP && !RAW) {
-            for (int k = 0; k < S::COLS * 2; k += 16)
-                *reinterpret_cast<uint4 *>(st + k) = make_uint4(0u, 0u, 0u, 0u);
-            fence_proxy_async_smem();
-        }
-        const uint32_t tbytes = static_cast<uint32_t>(rows) * trow;
-        const uint32_t total = __reduce_add_sync(0xffffffffu, c.bytes) + tbytes;
-        __syncwarp();
-        if (lane == 0)
-            mbar_arrive_expect_tx(full(stage), total);
-        __syncwarp();
-        if (c.bytes)
-            bulk_load(dst + lane * S::ROW + c.off, c.src, c.bytes, full(stage), pol);
-        if (lane == 0)
-            bulk_load(dst + STEP * S::ROW, a.plan.t + static_cast<size_t>(mine.p) * (trow / 2), tbytes, full(stage), pol_t);
-        more = mine.skip(a, WARPS);
-        look_up();
-    };
-    // All threads: the slab of an adapter's factor, ranks r0 .. r0 + RP - 1, into buffer fb.
-    auto load_factor = [&](int ad, int fb) {
-        const uint16_t *B = a.B + static_cast<size_t>(ad) * a.V * a.R;
-        for (int i = tid; i < S::COLS * (RP / 8); i += THREADS) {
-            const int v = c0 + i / (RP / 8), r = a.r0 + i % (RP / 8) * 8;
-            const bool on = v < a.V && r < a.R;
-            cp_async16(factor0 + fb * S::FACTOR + (i / (RP / 8)) * S::FROW + (i % (RP / 8)) * 16,
-                       B + static_cast<size_t>(on ? v : 0) * a.R + (on ? r : 0), on ? 16u : 0u);
-        }
-        cp_async_arrive(ffull(fb));
-    };
-
-    if (warp < S::STAGES && more)
-        fill(warp);
-    Cursor factors;   // the adapter whose factor is loaded next
-    bool more_factors = factors.start(a);
-    if (S::FACTORS == 2 && more_factors) {
-        load_factor(factors.ad, 0);
-        more_factors = factors.seek(a);
-    }
-    int stage = 0, fb = 0, rb = 0, turn = S::STAGES;   // turn: the warp that fills the next step
-    uint32_t phase = 0, fphase = 0;
-    // A wait that runs out sets the abort word and the status; the warps go on through
-    // the same barriers (with what they find) and end.
-    bool ok = true;
-    const int w0 = warp * CW;   // the warp's columns in the slab
-    for (int ad = 0; ad < a.n; ++ad) {
-        const int ob = a.plan.offsets[ad], oe = a.plan.offsets[ad + 1];
-        const int b = max(ob, a.p0), e = min(oe, a.p1);
-        float db[MB][RB][4];
+    if constexpr (RP == 16) {
+        tmem_load16(taddr, v);
+    } else {
 #pragma unroll
-        for (int m = 0; m < MB; ++m)
-#pragma unroll
-            for (int r = 0; r < RB; ++r)
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    db[m][r][k] = 0.f;
-        if (b < e) {
-            // the other buffer's (or the only one's) last use is behind the last step's barrier
-            if (S::FACTORS == 1) {
-                load_factor(ad, 0);
-            } else if (more_factors) {
-                load_factor(factors.ad, fb ^ 1);
-                more_factors = factors.seek(a);
-            }
-            if (ok)
-                ok = mbar_wait_sleep(ffull(fb), fphase, abort_flag, budget);
-        }
-        for (int p = b; p < e; p += STEP) {
-            if (ok)
-                ok = mbar_wait_sleep(full(stage), phase, abort_flag, budget);
-            const int rows = min(STEP, e - p);
-            const uint32_t st = base + stage * S::STAGE, ts = st + STEP * S::ROW;
-            uint32_t tile = st;
-            if (RAW) {
-                // 16 rows as planes of bf16 parts, eight columns at a time (the step before's
-                // planes have been read: every warp has passed its barrier on du)
-                for (int i = tid; i < STEP * (S::COLS / 8); i += THREADS) {
-                    const int m = i / (S::COLS / 8), c = i % (S::COLS / 8) * 8;
-                    uint32_t o[S::PLANES][4] = {};
-                    if (m < rows && c0 + c < a.V) {
-                        const uintptr_t lo = reinterpret_cast<uintptr_t>(dy + static_cast<size_t>(a.plan.perm[p + m]) * a.ld + c0);
-                        const T *x = reinterpret_cast<const T *>(smem + stage * S::STAGE + m * S::ROW + (lo & 15)) + c;
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            uint16_t part[S::PLANES];
-                            split_bf16<S::PLANES>(c0 + c + k < a.V ? Elem<T>::load(x + k) : 0.f, part);
-#pragma unroll
-                            for (int i2 = 0; i2 < S::PLANES; ++i2)
-                                o[i2][k >> 1] |= static_cast<uint32_t>(part[i2]) << ((k & 1) * 16);
-                        }
-                    }
-#pragma unroll
-                    for (int i2 = 0; i2 < S::PLANES; ++i2)
-                        *reinterpret_cast<uint4 *>(smem + (plane0 - base) + (i2 * STEP + m) * S::PROW + c * 2) =
-                            make_uint4(o[i2][0], o[i2][1], o[i2][2], o[i2][3]);
-                }
-                __syncthreads();
-                tile = plane0;
-            }
-            constexpr int TPITCH = RAW ? S::PROW : S::ROW;
-            // t's fragments: k = rows of the step, n = ranks.  Rows past the step's are
-            // not in the stage: zeros
-            uint32_t tf[PARTS][RB][2];
-#pragma unroll
-            for (int i = 0; i < PARTS; ++i)
-#pragma unroll
-                for (int r = 0; r < RB; r += 2) {
-                    uint32_t x[4];
-                    ldsm4t(x, ts + (lane & 15) * trow + (i * a.RT + a.r0 + r * 8 + (lane >> 4) * 8) * 2);
-                    // a lane's two words hold rows 2q, 2q + 1 and 8 + 2q, 9 + 2q
-                    const uint32_t k0 = (2 * q < rows ? 0xffffu : 0u) | (2 * q + 1 < rows ? 0xffff0000u : 0u);
-                    const uint32_t k1 = (8 + 2 * q < rows ? 0xffffu : 0u) | (9 + 2 * q < rows ? 0xffff0000u : 0u);
-                    tf[i][r][0] = x[0] & k0;
-                    tf[i][r][1] = x[1] & k1;
-                    tf[i][r + 1][0] = x[2] & k0;
-                    tf[i][r + 1][1] = x[3] & k1;
-                }
-            float du[RB][4];
-#pragma unroll
-            for (int r = 0; r < RB; ++r)
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    du[r][k] = 0.f;
-            const uint32_t fs = factor0 + fb * S::FACTOR;
-#pragma unroll
-            for (int m = 0; m < MB; ++m) {
-                const int c = w0 + m * 16;
-                uint32_t ff[RB][2];
-#pragma unroll
-                for (int r = 0; r < RB; r += 2) {
-                    uint32_t x[4];
-                    ldsm4t(x, fs + (c + (lane & 15)) * S::FROW + (r * 8 + (lane >> 4) * 8) * 2);
-                    ff[r][0] = x[0];
-                    ff[r][1] = x[1];
-                    ff[r + 1][0] = x[2];
-                    ff[r + 1][1] = x[3];
-                }
-#pragma unroll
-                for (int i = 0; i < S::PLANES; ++i) {
-                    const uint32_t pl = tile + i * (STEP * S::PROW);
-                    uint32_t x[4];
-                    // columns as rows: dB's operand
-                    ldsm4t(x, pl + ((lane & 7) + (lane >> 4) * 8) * TPITCH + (c + ((lane >> 3) & 1) * 8) * 2);
-#pragma unroll
-                    for (int r = 0; r < RB; ++r) {
-                        mma16816(db[m][r], x, tf[0][r][0], tf[0][r][1]);
-                        if (i == 0)   // lo lo is of the size of what the parts leave
-                            mma16816(db[m][r], x, tf[1][r][0], tf[1][r][1]);
-                    }
-                    ldsm4(x, pl + (lane & 15) * TPITCH + (c + (lane >> 4) * 8) * 2);
-#pragma unroll
-                    for (int r = 0; r < RB; ++r)
-                        mma16816(du[r], x, ff[r][0], ff[r][1]);
-                }
-            }
-            float *red = reinterpret_cast<float *>(red0 + rb * S::RED);
-#pragma unroll
-            for (int r = 0; r < RB; ++r) {
-                *reinterpret_cast<float2 *>(red + (warp * STEP + g) * (RP + 4) + r * 8 + 2 * q) = make_float2(du[r][0], du[r][1]);
-                *reinterpret_cast<float2 *>(red + (warp * STEP + g + 8) * (RP + 4) + r * 8 + 2 * q) = make_float2(du[r][2], du[r][3]);
-            }
-            __syncthreads();   // du's parts are there; the stage, and in an adapter's last step the factor, have been read
-            if (warp == turn && more && ok)
-                fill(stage);
-            turn = turn + 1 == WARPS ? 0 : turn + 1;
-            float *part = a.partial + (static_cast<size_t>(blockIdx.x) * (a.p1 - a.p0) + (p - a.p0)) * RP;
-            for (int i = tid; i < rows * (RP / 4); i += THREADS) {
-                const int m = i / (RP / 4), r = i % (RP / 4) * 4;
-                float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                for (int w = 0; w < WARPS; ++w) {
-                    const float4 x = *reinterpret_cast<const float4 *>(red + (w * STEP + m) * (RP + 4) + r);
-                    s.x += x.x;
-                    s.y += x.y;
-                    s.z += x.z;
-                    s.w += x.w;
-                }
-                *reinterpret_cast<float4 *>(part + static_cast<size_t>(m) * RP + r) = s;
-            }
-            rb ^= 1;
-            if (++stage == S::STAGES) {
-                stage = 0;
-                phase ^= 1u;
-            }
-        }
-        if (b < e && ++fb == S::FACTORS) {
-            fb = 0;
-            fphase ^= 1u;
-        }
-        // an adapter whose rows began in an earlier part of the batch is added to; one
-        // without rows is written (zeros) by the first part
-        const bool add = a.accumulate || (ob < oe && ob < a.p0);
-        if (b < e || (ob == oe && a.p0 == 0 && !a.accumulate)) {
-            float *dB = a.dB + static_cast<size_t>(ad) * a.V * a.R;
-#pragma unroll
-            for (int m = 0; m < MB; ++m)
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    const int v = c0 + w0 + m * 16 + half * 8 + g;
-                    if (v >= a.V)
-                        continue;
-#pragma unroll
-                    for (int r = 0; r < RB; ++r) {
-                        const int rr = a.r0 + r * 8 + 2 * q;
-                        if (rr >= a.R)
-                            continue;
-                        float2 *p = reinterpret_cast<float2 *>(dB + static_cast<size_t>(v) * a.R + rr);
-                        float2 x = make_float2(db[m][r][half * 2], db[m][r][half * 2 + 1]);
-                        if (add) {
-                            const float2 y = *p;
-                            x.x += y.x;
-                            x.y += y.y;
-                        }
-                        *p = x;
-                    }
-                }
-        }
-    }
-    __syncthreads();
-    if (*abort_flag) {   // copies may still be on their way
-        asm volatile("cp.async.wait_all;" ::: "memory");
-        if (tid == 0) {
-            for (int i = 0; i < S::STAGES; ++i)
-                drain_wait(full(i), i < stage ? phase : phase ^ 1u);
-            atomicCAS(a.status, 0, static_cast<int>(TIM_ERR_TIMEOUT));
-        }
-        __syncthreads();
+        for (int i = 0; i < RP; i += 32)
+            tmem_load32(taddr + i, *reinterpret_cast<float (*)[32]>(&v[i]));
     }
 }
 
+template <typename T, bool RAW, int RP>
+__global__ void __launch_bounds__(Shape<T, RAW, RP>::THREADS, 1)
+    adapters_grad_kernel(const __grid_constant__ CUtensorMap map_dy, const __grid_constant__ CUtensorMap map_b,
+                         const __grid_constant__ CUtensorMap map_t, const __grid_constant__ AdapterGradArgs a)
+{
+    using S = Shape<T, RAW, RP>;
+    constexpr uint32_t IDESC_DU = idesc_bf16_f32(STEP, RP, false, true), IDESC_DB = idesc_bf16_f32(BC, RP, true, true);
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t tiles = smem_u32(smem), factors = tiles + S::STAGES * S::TILE, ts = factors + S::FACTORS * S::FACTOR;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + S::STAGES * S::TILE + S::FACTORS * S::FACTOR + S::TS * S::TT);
+    const uint32_t bar0 = smem_u32(bars);
+    auto full = [&](int i) { return bar0 + 8u * i; };
+    auto empty = [&](int i) { return bar0 + 8u * (4 + i); };
+    auto tfull = [&](int i) { return bar0 + 8u * (8 + i); };
+    auto tempty = [&](int i) { return bar0 + 8u * (10 + i); };
+    auto ffull = [&](int i) { return bar0 + 8u * (12 + i); };
+    auto fempty = [&](int i) { return bar0 + 8u * (14 + i); };
+    auto dufull = [&](int i) { return bar0 + 8u * (16 + i); };
+    auto duempty = [&](int i) { return bar0 + 8u * (18 + i); };
+    const uint32_t dbfull = bar0 + 8u * 20, dbempty = bar0 + 8u * 21, drain = bar0 + 8u * 22;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 23);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int c0 = blockIdx.x * a.cols;                                   // the slab's columns
+    const int blocks = (min(a.V, c0 + a.cols) - c0 + BC - 1) / BC;
+    if (tid == 0) {
+        for (int i = 0; i < S::STAGES; ++i) {
+            mbar_init(full(i), RAW ? S::CONVERT : 1);
+            mbar_init(empty(i), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(tfull(i), 1);
+            mbar_init(tempty(i), 1);
+            mbar_init(ffull(i), 1);
+            mbar_init(fempty(i), 1);
+            mbar_init(dufull(i), 1);
+            mbar_init(duempty(i), 4);
+        }
+        mbar_init(dbfull, 1);
+        mbar_init(dbempty, 4);
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 0 && lane == 0) {
+        if (!RAW)
+            tma_prefetch_desc(&map_dy);
+        tma_prefetch_desc(&map_b);
+        tma_prefetch_desc(&map_t);
+    }
+    pdl_wait();
+    pdl_launch_dependents();
+    if (warp == 1) {
+        tmem_alloc(smem_u32(tmem_slot), S::TMEM);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;   // du: 2 x RP columns, then dB: RP columns a block
+    const uint64_t budget = a.wait_budget_ns;
+    const T *dy = static_cast<const T *>(a.dy);
+
+    // The adapters with positions in this part, in order: f(adapter, first, end); false ends.
+    auto segments = [&](auto f) {
+        for (int ad = 0; ad < a.n; ++ad) {
+            const Part r(a.plan.offsets[ad], a.plan.offsets[ad + 1], a.p0, a.p1);
+            if (r.begin < r.end && !f(ad, r.begin, r.end))
+                break;
+        }
+    };
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ copies
+        const uint64_t pol = l2_policy_evict_first(), pol_keep = l2_policy_evict_normal();
+        Ring<S::STAGES> st;
+        Ring<S::TS> tr;
+        Ring<S::FACTORS> fr;
+        uint32_t used = 0, used_t = 0, used_f = 0, par = 0, par_t = 0, par_f = 0;   // slots filled, parity of their last fill
+        segments([&](int ad, int b, int e) {
+            if (!warp_wait(fempty(fr.slot), fr.parity ^ 1u, abort_flag, budget))
+                return false;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(ffull(fr.slot), static_cast<uint32_t>(blocks) * BC * S::SPAN);
+                for (int c = 0; c < blocks; ++c)
+                    tma_load_3d(factors + fr.slot * S::FACTOR + c * BC * S::SPAN, &map_b, ffull(fr.slot), a.r0, c0 + c * BC, ad,
+                                pol_keep);
+            }
+            used_f |= 1u << fr.slot;
+            par_f = (par_f & ~(1u << fr.slot)) | (fr.parity << fr.slot);
+            fr.next();
+            for (int p = b; p < e; p += STEP) {
+                if (!warp_wait(tempty(tr.slot), tr.parity ^ 1u, abort_flag, budget))
+                    return false;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(tfull(tr.slot), S::TT);
+                    for (int i = 0; i < PARTS; ++i)
+                        tma_load_2d(ts + tr.slot * S::TT + i * STEP * S::SPAN, &map_t, tfull(tr.slot), i * a.RT + a.r0,
+                                    p + ad * AG_PAD, pol_keep);
+                }
+                used_t |= 1u << tr.slot;
+                par_t = (par_t & ~(1u << tr.slot)) | (tr.parity << tr.slot);
+                tr.next();
+                if (RAW)
+                    continue;
+                // rows in whole sixteens: past the adapter's last its last once more (their t is 0)
+                const int groups = (min(STEP, e - p) + 15) / 16 * 4;
+                int row[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    row[j] = a.plan.perm[min(p + 4 * lane + j, e - 1)];
+                for (int c = 0; c < blocks; ++c) {
+                    if (!warp_wait(empty(st.slot), st.parity ^ 1u, abort_flag, budget))
+                        return false;
+                    if (lane == 0)
+                        mbar_arrive_expect_tx(full(st.slot), static_cast<uint32_t>(groups) * 1024u);
+                    __syncwarp();
+                    if (lane < groups) {
+                        const uint32_t dst = tiles + st.slot * S::TILE + lane * 512;
+                        const int x = c0 + c * BC;
+                        TIM_DCHECK((x & 7) == 0 && row[3] >= 0 && row[3] < a.N, a.status, TIM_CHECK_TMA_COORD, x, row[3]);
+                        tma_gather4(dst, &map_dy, full(st.slot), x, row[0], row[1], row[2], row[3], pol);
+                        tma_gather4(dst + SUB, &map_dy, full(st.slot), x + 64, row[0], row[1], row[2], row[3], pol);
+                    }
+                    used |= 1u << st.slot;
+                    par = (par & ~(1u << st.slot)) | (st.parity << st.slot);
+                    st.next();
+                }
+            }
+            return true;
+        });
+        // no copy is in flight when the CTA leaves
+        if (lane == 0) {
+            for (int i = 0; i < S::STAGES; ++i)
+                if (!RAW && (used >> i & 1u))
+                    drain_wait(full(i), par >> i & 1u);
+            for (int i = 0; i < 2; ++i) {
+                if (used_t >> i & 1u)
+                    drain_wait(tfull(i), par_t >> i & 1u);
+                if (used_f >> i & 1u)
+                    drain_wait(ffull(i), par_f >> i & 1u);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ products
+        if (lane == 0) {
+            Ring<S::STAGES> st;
+            Ring<S::TS> tr;
+            Ring<S::FACTORS> fr;
+            Ring<2> du;
+            Ring<1> db;
+            segments([&](int, int b, int e) {
+                if (!mbar_wait(ffull(fr.slot), fr.parity, abort_flag, budget) ||
+                    !mbar_wait(dbempty, db.parity ^ 1u, abort_flag, budget))
+                    return false;
+                const uint32_t fs = factors + fr.slot * S::FACTOR;
+                for (int p = b; p < e; p += STEP) {
+                    if (!mbar_wait(tfull(tr.slot), tr.parity, abort_flag, budget) ||
+                        !mbar_wait(duempty(du.slot), du.parity ^ 1u, abort_flag, budget))
+                        return false;
+                    tc_fence_after();
+                    const int steps = (min(STEP, e - p) + 15) / 16;   // of 16 rows
+                    const uint32_t td = tmem + du.slot * RP, tt = ts + tr.slot * S::TT;
+                    for (int c = 0; c < blocks; ++c) {
+                        if (!mbar_wait(full(st.slot), st.parity, abort_flag, budget))
+                            return false;
+                        tc_fence_after();
+                        const uint32_t tile = tiles + st.slot * S::TILE, tb = tmem + 2 * RP + c * RP;
+#pragma unroll
+                        for (int i = 0; i < S::PLANES; ++i) {
+                            const uint32_t pl = tile + i * 2 * SUB;
+                            // du += tile x factor, 16 columns at a time
+#pragma unroll
+                            for (int k = 0; k < BC / 16; ++k)
+                                umma_bf16(td, sdesc_kmajor_sw128(pl + (k / 4) * SUB) + 2u * (k % 4),
+                                          sdesc_mnmajor_span<S::SPAN>(fs + (c * BC + k * 16) * S::SPAN), IDESC_DU,
+                                          (c | i | k) != 0);
+                            // dB += tile^T x t, 16 rows at a time; lo lo is of the size of what the parts leave
+                            for (int j = 0; j < (i == 0 ? PARTS : 1); ++j)
+                                for (int k = 0; k < steps; ++k)
+                                    umma_bf16(tb, sdesc_mnmajor_sw128(pl, SUB) + 128u * k,
+                                              sdesc_mnmajor_span<S::SPAN>(tt + (j * STEP + k * 16) * S::SPAN), IDESC_DB,
+                                              p != b || (i | j | k) != 0);
+                        }
+                        umma_commit(empty(st.slot));
+                        st.next();
+                    }
+                    umma_commit(tempty(tr.slot));
+                    umma_commit(dufull(du.slot));
+                    tr.next();
+                    du.next();
+                }
+                umma_commit(fempty(fr.slot));
+                umma_commit(dbfull);
+                fr.next();
+                db.next();
+                return true;
+            });
+            umma_commit(drain);   // every product has finished before TMEM is released
+            drain_wait(drain, 0);
+        }
+        __syncwarp();
+    } else if (warp < 6) {
+        // ------------------------------------------------------------ results
+        const int m = (warp & 3) * 32 + lane;   // row of du, column of dB's block
+        const uint32_t mine = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+        Ring<2> du;
+        Ring<1> db;
+        bool ok = true;
+        for (int ad = 0; ok && ad < a.n; ++ad) {
+            const int ob = a.plan.offsets[ad], oe = a.plan.offsets[ad + 1];
+            const Part r(ob, oe, a.p0, a.p1);
+            const int b = r.begin, e = r.end;
+            const bool some = b < e;
+            // an adapter whose rows began in an earlier part of the batch is added to; one
+            // without rows is written (zeros) by the first part
+            const bool add = a.accumulate || b > ob;
+            if (!some && !(ob == oe && a.p0 == 0 && !a.accumulate))
+                continue;
+            for (int p = b; p < e; p += STEP) {
+                ok = warp_wait(dufull(du.slot), du.parity, abort_flag, budget);
+                if (!ok)
+                    break;
+                tc_fence_after();
+                float v[RP];
+                __syncwarp();
+                tmem_row<RP>(mine + du.slot * RP, v);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(duempty(du.slot));
+                if (p + m < e) {
+                    float4 *o = reinterpret_cast<float4 *>(
+                        a.partial + (static_cast<size_t>(blockIdx.x) * (a.p1 - a.p0 + 16) + (p + m - a.p0)) * RP);
+#pragma unroll
+                    for (int r = 0; r < RP / 4; ++r)
+                        o[r] = make_float4(v[4 * r], v[4 * r + 1], v[4 * r + 2], v[4 * r + 3]);
+                }
+                du.next();
+            }
+            if (!ok)
+                break;
+            if (some) {
+                ok = warp_wait(dbfull, db.parity, abort_flag, budget);
+                if (!ok)
+                    break;
+                tc_fence_after();
+            }
+            for (int c = 0; c < blocks; ++c) {
+                float v[RP];
+                if (some) {
+                    __syncwarp();
+                    tmem_row<RP>(mine + 2 * RP + c * RP, v);
+                } else {
+#pragma unroll
+                    for (int r = 0; r < RP; ++r)
+                        v[r] = 0.f;
+                }
+                const int col = c0 + c * BC + m;
+                if (col >= a.V)
+                    continue;
+                float4 *o = reinterpret_cast<float4 *>(a.dB + (static_cast<size_t>(ad) * a.V + col) * a.R + a.r0);
+#pragma unroll
+                for (int r = 0; r < RP / 4; ++r) {
+                    if (a.r0 + 4 * r >= a.R)
+                        break;
+                    float4 x = make_float4(v[4 * r], v[4 * r + 1], v[4 * r + 2], v[4 * r + 3]);
+                    if (add) {
+                        const float4 y = o[r];
+                        x.x += y.x;
+                        x.y += y.y;
+                        x.z += y.z;
+                        x.w += y.w;
+                    }
+                    o[r] = x;
+                }
+            }
+            if (some) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(dbempty);
+                db.next();
+            }
+        }
+    } else {
+        // ------------------------------------------------------------ tiles from plain loads
+        // thread: columns 8 (t % 16) .. of rows t / 16, t / 16 + 16, ... of a tile
+        constexpr int AHEAD = 4;   // rows in flight together
+        const int t = tid - 6 * 32, chunk = t & 15, r0 = t >> 4;
+        Ring<S::STAGES> st;
+        segments([&](int, int b, int e) {
+            for (int p = b; p < e; p += STEP) {
+                const int rows = min(STEP, e - p), padded = (rows + 15) / 16 * 16;
+                const T *row[STEP / 16];
+#pragma unroll
+                for (int i = 0; i < STEP / 16; ++i) {
+                    const int m = r0 + 16 * i;
+                    row[i] = m < rows ? dy + static_cast<size_t>(a.plan.perm[p + m]) * a.ld : nullptr;
+                }
+                for (int c = 0; c < blocks; ++c) {
+                    const int col = c0 + c * BC + chunk * 8;
+                    bool waited = false;
+#pragma unroll
+                    for (int i0 = 0; i0 < STEP / 16; i0 += AHEAD) {
+                        if (i0 * 16 >= padded)
+                            break;
+                        Raw8<T> x[AHEAD];
+#pragma unroll
+                        for (int i = 0; i < AHEAD; ++i)
+                            if (row[i0 + i] && col < a.V)
+                                load8<T>(x[i], row[i0 + i], col, a.V, row_shift(row[i0 + i]));
+                        if (!waited) {   // the first loads are on their way meanwhile
+                            if (!warp_wait(empty(st.slot), st.parity ^ 1u, abort_flag, budget))
+                                return false;
+                            waited = true;
+                        }
+#pragma unroll
+                        for (int i = 0; i < AHEAD; ++i) {
+                            const int m = r0 + 16 * (i0 + i);
+                            if (m >= padded)
+                                continue;
+                            uint32_t o[S::PLANES][4] = {};
+                            if (row[i0 + i]) {
+#pragma unroll
+                                for (int k = 0; k < 8; ++k) {
+                                    uint16_t part[S::PLANES];
+                                    split_bf16<S::PLANES>(col + k < a.V ? Elem<T>::get(x[i].w, k) : 0.f, part);
+#pragma unroll
+                                    for (int j = 0; j < S::PLANES; ++j)
+                                        o[j][k >> 1] |= static_cast<uint32_t>(part[j]) << ((k & 1) * 16);
+                                }
+                            }
+                            // 128-byte swizzle: the 16-byte pieces of row m are exchanged by m % 8
+                            uint8_t *dst = smem + st.slot * S::TILE + (chunk >> 3) * SUB + m * 128 + (((chunk & 7) ^ (m & 7)) << 4);
+#pragma unroll
+                            for (int j = 0; j < S::PLANES; ++j)
+                                *reinterpret_cast<uint4 *>(dst + j * 2 * SUB) = make_uint4(o[j][0], o[j][1], o[j][2], o[j][3]);
+                        }
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(full(st.slot));
+                    st.next();
+                }
+            }
+            return true;
+        });
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1)
+        tmem_dealloc(tmem, S::TMEM);
+    if (tid == 0 && *abort_flag)
+        atomicCAS(a.status, 0, static_cast<int>(TIM_ERR_TIMEOUT));
+}
+
 // ---------------------------------------------------------------- fold
-// du of positions p0 .. p1 - 1, ranks r0 .. r0 + RP - 1: the slabs' parts added in slab
+// du of a part's positions, ranks r0 .. r0 + RP - 1: the slabs' parts added in slab
 // order by eight threads (slabs k, k + 8, ... each, then joined in order), times scale,
 // in three bf16 parts.
 template <int RP> __global__ void __launch_bounds__(256) adapters_fold_kernel(const AdapterGradArgs a)
@@ -411,11 +467,20 @@ template <int RP> __global__ void __launch_bounds__(256) adapters_fold_kernel(co
     constexpr int SHARE = 8, ITEMS = 256 / SHARE;
     __shared__ float4 sums[SHARE][ITEMS];
     const int item = threadIdx.x % ITEMS, k = threadIdx.x / ITEMS;
-    const int64_t count = a.p1 - a.p0;
+    const int64_t count = a.p1 - a.p0 + 16;   // a part may end up to 15 positions past p1
     const int64_t i = (static_cast<int64_t>(blockIdx.x) * ITEMS + item);   // four ranks of a position
     pdl_wait();
     pdl_launch_dependents();
-    const bool on = i < count * (RP / 4);
+    const int pos = a.p0 + static_cast<int>(i / (RP / 4)), r = static_cast<int>(i % (RP / 4)) * 4;
+    int ad = a.n;
+    if (i < count * (RP / 4) && pos < a.N) {
+        ad = a.plan.adapter[pos];
+        if (ad < a.n) {
+            const Part in(a.plan.offsets[ad], a.plan.offsets[ad + 1], a.p0, a.p1);
+            ad = pos >= in.begin && pos < in.end ? ad : a.n;
+        }
+    }
+    const bool on = ad < a.n;
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
     if (on) {
         const float4 *p = reinterpret_cast<const float4 *>(a.partial) + i;
@@ -440,10 +505,6 @@ template <int RP> __global__ void __launch_bounds__(256) adapters_fold_kernel(co
         s.z += x.z;
         s.w += x.w;
     }
-    const int pos = a.p0 + static_cast<int>(i / (RP / 4)), r = static_cast<int>(i % (RP / 4)) * 4;
-    const int ad = a.plan.adapter[pos];
-    if (ad >= a.n)
-        return;   // no adapter: nothing was summed
     const float scale = a.scale ? a.scale[ad] : 1.f;
     uint16_t x0[3], x1[3], x2[3], x3[3];
     split_bf16<3>(s.x * scale, x0);
@@ -459,11 +520,28 @@ template <int RP> __global__ void __launch_bounds__(256) adapters_fold_kernel(co
 
 // ---------------------------------------------------------------- dA
 // CTA (x, a): dA of adapter a, columns x * 128 .. + 127 of D; a warp has 16 of them for
-// all ranks.  Rows in chunks of 32 through shared memory (gathered in the plan's order).
+// all ranks.  Rows in chunks of 32 (gathered in the plan's order) by asynchronous copies
+// into a ring of three stages.
+template <int RT> struct DaShape {
+    static constexpr int ROWS = 32, COLS = 128, STAGES = 3;
+    static constexpr int HROW = COLS * 2 + 16, UROW = 3 * RT * 2 + 16;   // padded: no bank twice
+    static constexpr int STAGE = ROWS * (HROW + UROW), BYTES = STAGES * STAGE;
+};
+
+// 16 bytes global -> shared, zeros where on is false.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool on)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src)),
+                 "r"(on ? 16u : 0u)
+                 : "memory");
+}
+
 template <int RT> __global__ void __launch_bounds__(256) adapters_dA_kernel(const AdapterGradArgs a)
 {
-    constexpr int ROWS = 32, COLS = 128, HROW = COLS * 2 + 16, UROW = 3 * RT * 2 + 16, RM = RT / 16;
-    __shared__ __align__(16) uint8_t hs[ROWS * HROW], us[ROWS * UROW];
+    using S = DaShape<RT>;
+    constexpr int ROWS = S::ROWS, COLS = S::COLS, HROW = S::HROW, UROW = S::UROW, RM = RT / 16;
+    extern __shared__ __align__(16) uint8_t ring[];
+    const uint32_t ring0 = smem_u32(ring);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q = lane & 3;
     const int ad = blockIdx.y, d0 = blockIdx.x * COLS;
     pdl_wait();
@@ -472,22 +550,41 @@ template <int RT> __global__ void __launch_bounds__(256) adapters_dA_kernel(cons
     if (b == e && a.accumulate)
         return;
     float acc[RM][2][4] = {};
-    const uint32_t h0 = smem_u32(hs), u0 = smem_u32(us);
-    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+    const int hc = tid % 16 * 8;   // this thread's piece of rows tid / 16 and tid / 16 + 16 of a chunk
+    int row[2];
+    auto look_up = [&](int p) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int at = p + tid / 16 + i * 16;
+            row[i] = at < e ? a.plan.perm[at] : -1;
+        }
+    };
+    auto fill = [&](int stage, int p) {
+        const uint32_t h0 = ring0 + stage * S::STAGE, u0 = h0 + ROWS * HROW;
+        if (p < e) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const bool on = row[i] >= 0 && d0 + hc < a.D;
+                cp_async16(h0 + (tid / 16 + i * 16) * HROW + hc * 2, a.h + (on ? static_cast<size_t>(row[i]) * a.D + d0 + hc : 0), on);
+            }
+            for (int i = tid; i < ROWS * (3 * RT / 8); i += 256) {
+                const int m = i / (3 * RT / 8), c = i % (3 * RT / 8) * 8;
+                const bool on = p + m < e;
+                cp_async16(u0 + m * UROW + c * 2, a.du + (on ? static_cast<size_t>(p + m) * (3 * RT) + c : 0), on);
+            }
+            look_up(p + ROWS);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    look_up(b);
+    for (int i = 0; i < S::STAGES - 1; ++i)
+        fill(i, b + i * ROWS);
+    int stage = 0;
     for (int p = b; p < e; p += ROWS) {
-        __syncthreads();
-        for (int i = tid; i < ROWS * (COLS / 8); i += 256) {
-            const int m = i / (COLS / 8), c = i % (COLS / 8) * 8;
-            const bool on = p + m < e && d0 + c < a.D;
-            *reinterpret_cast<uint4 *>(hs + m * HROW + c * 2) =
-                on ? __ldg(reinterpret_cast<const uint4 *>(a.h + static_cast<size_t>(a.plan.perm[p + m]) * a.D + d0 + c)) : zero;
-        }
-        for (int i = tid; i < ROWS * (3 * RT / 8); i += 256) {
-            const int m = i / (3 * RT / 8), c = i % (3 * RT / 8) * 8;
-            *reinterpret_cast<uint4 *>(us + m * UROW + c * 2) =
-                p + m < e ? *reinterpret_cast<const uint4 *>(a.du + static_cast<size_t>(p + m) * (3 * RT) + c) : zero;
-        }
-        __syncthreads();
+        asm volatile("cp.async.wait_group %0;" ::"n"(S::STAGES - 2) : "memory");
+        __syncthreads();   // the chunk is there; the one before has been read
+        fill(stage == 0 ? S::STAGES - 1 : stage - 1, p + (S::STAGES - 1) * ROWS);
+        const uint32_t h0 = ring0 + stage * S::STAGE, u0 = h0 + ROWS * HROW;
 #pragma unroll
         for (int k = 0; k < ROWS; k += 16) {
             uint32_t x[4];   // k = rows, n = the warp's 16 columns
@@ -502,6 +599,7 @@ template <int RT> __global__ void __launch_bounds__(256) adapters_dA_kernel(cons
                     mma16816(acc[m][1], u, x[2], x[3]);
                 }
         }
+        stage = stage + 1 == S::STAGES ? 0 : stage + 1;
     }
 #pragma unroll
     for (int m = 0; m < RM; ++m)
@@ -623,43 +721,40 @@ cudaError_t launch(F kernel, dim3 grid, int threads, int smem, const AdapterGrad
     return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
-template <typename T, bool RAW, int RP, int COLS> cudaError_t grad(const AdapterGradArgs &a, cudaStream_t s, bool set)
+// The gradient's launch; maps = null: the kernel's shared memory is granted instead.
+template <typename T, bool RAW, int RP> cudaError_t grad(const CUtensorMap *maps, const AdapterGradArgs &a, cudaStream_t s)
 {
-    using S = Shape<T, RAW, RP, COLS>;
-    if (set)
-        return cudaFuncSetAttribute(adapters_grad_kernel<T, RAW, RP, COLS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    S::BYTES);
-    return launch(adapters_grad_kernel<T, RAW, RP, COLS>, dim3(static_cast<unsigned>(a.slabs)), THREADS, S::BYTES, a, s);
+    using S = Shape<T, RAW, RP>;
+    auto kernel = adapters_grad_kernel<T, RAW, RP>;
+    if (!maps)
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::BYTES);
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1] = {pdl_attribute()};
+    cfg.gridDim = dim3(static_cast<unsigned>(a.slabs), 1, 1);
+    cfg.blockDim = dim3(S::THREADS, 1, 1);
+    cfg.dynamicSmemBytes = S::BYTES;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, maps[0], maps[1], maps[2], a);
 }
 
-// The variant for the slab's width; set: its shared memory is granted instead.
-template <typename T, bool RAW, int RP> cudaError_t grad(const AdapterGradArgs &a, int cols, cudaStream_t s, bool set)
-{
-    constexpr int WIDE = ag_cols(RP, RAW, true), NARROW = ag_cols(RP, RAW, false);
-    return cols == WIDE ? grad<T, RAW, RP, WIDE>(a, s, set) : grad<T, RAW, RP, NARROW>(a, s, set);
-}
-
-template <int RP>
-cudaError_t grad(const AdapterGradArgs &a, int dtype, bool raw, int cols, cudaStream_t s, bool set = false)
+template <int RP> cudaError_t grad(const CUtensorMap *maps, const AdapterGradArgs &a, int dtype, bool raw, cudaStream_t s)
 {
     if (dtype == TIM_F32)
-        return grad<float, true, RP>(a, cols, s, set);
+        return grad<float, true, RP>(maps, a, s);
     if (dtype == TIM_F16)
-        return grad<__half, true, RP>(a, cols, s, set);
-    return raw ? grad<__nv_bfloat16, true, RP>(a, cols, s, set) : grad<__nv_bfloat16, false, RP>(a, cols, s, set);
+        return grad<__half, true, RP>(maps, a, s);
+    return raw ? grad<__nv_bfloat16, true, RP>(maps, a, s) : grad<__nv_bfloat16, false, RP>(maps, a, s);
 }
 
 template <int RP> cudaError_t prepare()
 {
     const AdapterGradArgs a{};
-    cudaError_t e = cudaSuccess;
-    for (int wide = 0; wide < 2; ++wide) {
-        for (int dtype : {TIM_F32, TIM_F16, TIM_BF16})
-            if (e == cudaSuccess)
-                e = grad<RP>(a, dtype, true, ag_cols(RP, true, wide), nullptr, true);
+    cudaError_t e = grad<RP>(nullptr, a, TIM_BF16, false, nullptr);
+    for (int dtype : {TIM_F32, TIM_F16, TIM_BF16})
         if (e == cudaSuccess)
-            e = grad<RP>(a, TIM_BF16, false, ag_cols(RP, false, wide), nullptr, true);
-    }
+            e = grad<RP>(nullptr, a, dtype, true, nullptr);
     return e;
 }
 
@@ -674,22 +769,26 @@ cudaError_t adapters_grad_prepare_device()
         e = prepare<64>();
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(adapters_dh_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, 128 * 528);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(adapters_dA_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, DaShape<64>::BYTES);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(adapters_dA_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, DaShape<128>::BYTES);
     return e;
 }
 
-cudaError_t adapters_grad_launch(AdapterGradArgs a, int dtype, cudaStream_t s)
+cudaError_t adapters_grad_launch(const CUtensorMap (&maps)[3], AdapterGradArgs a, int dtype, int num_sms, cudaStream_t s)
 {
     const int RP = std::min(a.RT, 64);
     for (int64_t p0 = 0; p0 < a.N; p0 += a.row_part)
         for (a.r0 = 0; a.r0 < a.R; a.r0 += RP) {
             a.p0 = static_cast<int32_t>(p0);
             a.p1 = static_cast<int32_t>(std::min<int64_t>(a.N, p0 + a.row_part));
-            cudaError_t e = RP == 16   ? grad<16>(a, dtype, a.raw, a.cols, s)
-                            : RP == 32 ? grad<32>(a, dtype, a.raw, a.cols, s)
-                                       : grad<64>(a, dtype, a.raw, a.cols, s);
+            cudaError_t e = RP == 16   ? grad<16>(maps, a, dtype, a.raw, s)
+                            : RP == 32 ? grad<32>(maps, a, dtype, a.raw, s)
+                                       : grad<64>(maps, a, dtype, a.raw, s);
             if (e != cudaSuccess)
                 return e;
-            const int64_t items = static_cast<int64_t>(a.p1 - a.p0) * (RP / 4);
+            const int64_t items = static_cast<int64_t>(a.p1 - a.p0 + 16) * (RP / 4);
             const dim3 grid(static_cast<unsigned>((items + 31) / 32));
             e = RP == 16   ? launch(adapters_fold_kernel<16>, grid, 256, 0, a, s)
                 : RP == 32 ? launch(adapters_fold_kernel<32>, grid, 256, 0, a, s)
@@ -698,25 +797,28 @@ cudaError_t adapters_grad_launch(AdapterGradArgs a, int dtype, cudaStream_t s)
                 return e;
         }
     const dim3 grid_a(static_cast<unsigned>((a.D + 127) / 128), static_cast<unsigned>(a.n));
+    const int64_t columns = (a.D + 255) / 256;
     int64_t chunk = 128;
+    while (chunk > 16 && columns * ((a.N + chunk - 1) / chunk) < 4 * num_sms)
+        chunk /= 2;
     while ((a.N + chunk - 1) / chunk > 65535)
         chunk *= 2;
     a.row_chunk = static_cast<int32_t>(chunk);
-    const dim3 grid_h(static_cast<unsigned>((a.D + 255) / 256), static_cast<unsigned>((a.N + chunk - 1) / chunk));
+    const dim3 grid_h(static_cast<unsigned>(columns), static_cast<unsigned>((a.N + chunk - 1) / chunk));
     const int smem = a.RT * 528;
     cudaError_t e;
     switch (a.RT) {
     case 16:
-        e = launch(adapters_dA_kernel<16>, grid_a, 256, 0, a, s);
+        e = launch(adapters_dA_kernel<16>, grid_a, 256, DaShape<16>::BYTES, a, s);
         return e != cudaSuccess ? e : launch(adapters_dh_kernel<16>, grid_h, 256, smem, a, s);
     case 32:
-        e = launch(adapters_dA_kernel<32>, grid_a, 256, 0, a, s);
+        e = launch(adapters_dA_kernel<32>, grid_a, 256, DaShape<32>::BYTES, a, s);
         return e != cudaSuccess ? e : launch(adapters_dh_kernel<32>, grid_h, 256, smem, a, s);
     case 64:
-        e = launch(adapters_dA_kernel<64>, grid_a, 256, 0, a, s);
+        e = launch(adapters_dA_kernel<64>, grid_a, 256, DaShape<64>::BYTES, a, s);
         return e != cudaSuccess ? e : launch(adapters_dh_kernel<64>, grid_h, 256, smem, a, s);
     default:
-        e = launch(adapters_dA_kernel<128>, grid_a, 256, 0, a, s);
+        e = launch(adapters_dA_kernel<128>, grid_a, 256, DaShape<128>::BYTES, a, s);
         return e != cudaSuccess ? e : launch(adapters_dh_kernel<128>, grid_h, 256, smem, a, s);
     }
 }

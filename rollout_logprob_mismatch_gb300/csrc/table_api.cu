@@ -220,15 +220,17 @@ int tim_adapter_logits_backward(const void *dlogits, int dtype, int64_t N, int64
     a.R = f.R;
     a.n = f.n;
     a.RT = tim::ad_rank_pad(R);
-    a.raw = dtype != TIM_BF16 || !aligned(dlogits, 16) || (N > 1 && stride % 8 != 0);
+    a.raw = dtype != TIM_BF16 || !aligned(dlogits, 16) || (N > 1 && (stride % 8 != 0 || stride >= int64_t(1) << 39));
     const int RP = std::min(a.RT, 64);
-    const int wide = tim::ag_cols(RP, a.raw != 0, true), narrow = tim::ag_cols(RP, a.raw != 0, false);
-    a.cols = (V + wide - 1) / wide >= sms - sms / 4 ? wide : narrow;
-    a.slabs = static_cast<int32_t>((V + a.cols - 1) / a.cols);
+    // a slab an SM while TMEM has room for its dB, else as many waves of them as it takes
+    const int64_t blocks = (V + tim::AG_BLOCK - 1) / tim::AG_BLOCK, most = tim::ag_blocks(RP);
+    const int64_t waves = (blocks + most * sms - 1) / (most * sms);
+    const int64_t per_slab = (blocks + waves * sms - 1) / (waves * sms);
+    a.cols = static_cast<int32_t>(per_slab * tim::AG_BLOCK);
+    a.slabs = static_cast<int32_t>((blocks + per_slab - 1) / per_slab);
     const int64_t per_row = int64_t(4) * a.slabs * RP;
     a.row_part = static_cast<int32_t>(std::min<int64_t>(
-        (N + tim::AG_STEP - 1) / tim::AG_STEP * tim::AG_STEP,
-        std::max<int64_t>(tim::AG_PARTIAL_BYTES / per_row / tim::AG_STEP, 1) * tim::AG_STEP));
+        N, std::max<int64_t>(tim::AG_PARTIAL_BYTES / per_row / tim::AG_STEP, 1) * tim::AG_STEP));
     a.dh = dh;
     a.dA = dA;
     a.dB = dB;
@@ -238,9 +240,10 @@ int tim_adapter_logits_backward(const void *dlogits, int dtype, int64_t N, int64
     a.status = status;
     const size_t b_off = tim::ws_round(sizeof(int32_t) * (static_cast<size_t>(n) + 2));
     const size_t b_n = tim::ws_round(sizeof(int32_t) * static_cast<size_t>(N));
-    const size_t b_t = tim::ws_round(static_cast<size_t>(N) * tim::ag_t_pitch(a.RT) * 2);
+    const size_t t_rows = static_cast<size_t>(N) + static_cast<size_t>(n) * tim::AG_PAD;
+    const size_t b_t = tim::ws_round(t_rows * 2 * a.RT * 2);
     const size_t b_du = tim::ws_round(static_cast<size_t>(N) * 3 * a.RT * 2);
-    const size_t b_part = static_cast<size_t>(per_row) * a.row_part;
+    const size_t b_part = static_cast<size_t>(per_row) * (a.row_part + 16);
     void *ws = nullptr;
     if ((rc = tim::workspace_alloc(&ws, b_off + 2 * b_n + b_t + b_du + b_part, s)) != TIM_OK)
         return rc;
@@ -250,13 +253,27 @@ int tim_adapter_logits_backward(const void *dlogits, int dtype, int64_t N, int64
     f.plan.adapter = reinterpret_cast<int32_t *>(w + b_off + b_n);
     w += b_off + 2 * b_n;
     f.plan.t = reinterpret_cast<uint16_t *>(w);
-    f.plan.t_pitch = tim::ag_t_pitch(a.RT);
+    f.plan.t_pitch = 2 * a.RT;
+    f.plan.t_pad = tim::AG_PAD;
     a.plan = f.plan;
     a.du = reinterpret_cast<uint16_t *>(w + b_t);
     a.partial = reinterpret_cast<float *>(w + b_t + b_du);
+    CUtensorMap maps[3] = {};
+    const uint64_t d_dy[2] = {static_cast<uint64_t>(V), static_cast<uint64_t>(N)}, s_dy[1] = {static_cast<uint64_t>(N == 1 ? (V + 7) / 8 * 8 : stride) * 2};
+    const uint64_t d_b[3] = {static_cast<uint64_t>(R), static_cast<uint64_t>(V), static_cast<uint64_t>(n)};
+    const uint64_t s_b[2] = {static_cast<uint64_t>(R) * 2, static_cast<uint64_t>(V * R) * 2};
+    const uint64_t d_t[2] = {static_cast<uint64_t>(2 * a.RT), t_rows}, s_t[1] = {static_cast<uint64_t>(2 * a.RT) * 2};
+    const uint32_t box_dy[2] = {64, 1}, box_b[3] = {static_cast<uint32_t>(RP), tim::AG_BLOCK, 1};
+    const uint32_t box_t[2] = {static_cast<uint32_t>(RP), tim::AG_STEP};
+    if ((!a.raw && (rc = tim::encode_bf16_map(&maps[0], dlogits, 2, d_dy, s_dy, box_dy, 128)) != TIM_OK) ||
+        (rc = tim::encode_bf16_map(&maps[1], a.B, 3, d_b, s_b, box_b, 2 * RP)) != TIM_OK ||
+        (rc = tim::encode_bf16_map(&maps[2], f.plan.t, 2, d_t, s_t, box_t, 2 * RP)) != TIM_OK) {
+        tim::workspace_free(ws, s);
+        return rc;
+    }
     cudaError_t e = tim::adapters_shrink_launch(f, 2, sms, s);
     if (e == cudaSuccess)
-        e = tim::adapters_grad_launch(a, dtype, s);
+        e = tim::adapters_grad_launch(maps, a, dtype, sms, s);
     return finish(e, tim::workspace_free(ws, s), "adapter_logits_backward launch");
 }
 

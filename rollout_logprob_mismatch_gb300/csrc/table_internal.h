@@ -5,6 +5,7 @@
 
 #include <cstdint>
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 namespace tim {
@@ -12,6 +13,11 @@ namespace tim {
 // Device memory from the library's stream-ordered pool; a tim_status code.
 int workspace_alloc(void **p, size_t bytes, cudaStream_t s);
 cudaError_t workspace_free(void *p, cudaStream_t s);
+
+// Tensor map of bf16 elements: dims and box innermost first, strides in bytes of the
+// outer dims, swizzle span in bytes; out-of-range elements read as zero.  A tim_status code.
+int encode_bf16_map(CUtensorMap *m, const void *base, int rank, const uint64_t *dims, const uint64_t *strides,
+                    const uint32_t *box, int span);
 
 inline size_t ws_round(size_t x) { return (x + 255) / 256 * 256; }
 
@@ -33,8 +39,9 @@ struct AdapterPlan {
     int32_t *offsets;   // [n + 2]: positions of adapter a are offsets[a] .. offsets[a + 1]; n = no adapter
     int32_t *perm;      // [N]: row of each position
     int32_t *adapter;   // [N]: adapter of each position, n = none
-    uint16_t *t;        // bf16 [N][t_pitch]: [parts][RP] and padding
+    uint16_t *t;        // bf16 [N + t_pad n][t_pitch]: [parts][RP] and padding; position p of adapter a in row p + t_pad a
     int32_t t_pitch;
+    int32_t t_pad;      // 0, or AG_PAD: the rows behind an adapter's last, up to a multiple of 16 of them in all, are zeros
 };
 
 struct AdapterArgs {
@@ -61,22 +68,14 @@ cudaError_t adapters_shrink_launch(const AdapterArgs &a, int parts, int num_sms,
 cudaError_t adapters_expand_launch(AdapterArgs a, int dtype, int num_sms, cudaStream_t s);
 cudaError_t adapters_prepare_device();   // shared-memory sizes
 
-// The gradient: slabs of the vocabulary, steps of 16 rows.
-constexpr int AG_STEP = 16;
+// The gradient: slabs of the vocabulary, tiles of 128 rows and 128 columns.
+constexpr int AG_STEP = 128, AG_BLOCK = 128;
+constexpr int AG_PAD = 16;           // t has room for so many rows of zeros behind each adapter's
 constexpr int AG_SMEM = 227 * 1024;
 constexpr int64_t AG_PARTIAL_BYTES = int64_t(1) << 30;   // du's partial sums at most, per part of the batch
 
-// Elements of a row of t in the gradient: two parts, and 16 bytes that spread the rows
-// over the banks.
-constexpr int ag_t_pitch(int RT) { return 2 * RT + 8; }
-
-// Columns of a slab: as many as dB's sums have registers for (128 a thread), or fewer
-// where the vocabulary would not give every SM a slab.
-constexpr int ag_cols(int RP, bool raw, bool wide)
-{
-    const int most = (RP <= 32 ? 1024 : 512) / (raw ? 2 : 1);
-    return wide ? most : most / 4 < 128 ? 128 : most / 4;
-}
+// Tiles of a slab: as many as dB's sums have TMEM for, beside two of du (512 columns).
+constexpr int ag_blocks(int RP) { return RP <= 32 ? 8 : 4; }
 
 struct AdapterGradArgs {
     const uint16_t *h, *A, *B;
@@ -99,7 +98,8 @@ struct AdapterGradArgs {
     int *status;
 };
 
-cudaError_t adapters_grad_launch(AdapterGradArgs a, int dtype, cudaStream_t s);
+// maps: dy, B, t
+cudaError_t adapters_grad_launch(const CUtensorMap (&maps)[3], AdapterGradArgs a, int dtype, int num_sms, cudaStream_t s);
 cudaError_t adapters_grad_prepare_device();
 
 // ---------------------------------------------------------------- embedding

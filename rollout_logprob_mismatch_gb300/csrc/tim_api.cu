@@ -240,6 +240,27 @@ int workspace_alloc(void **p, size_t bytes, cudaStream_t s)
     return e == cudaSuccess ? TIM_OK : cuda_fail(e, "cudaMallocFromPoolAsync(workspace)");
 }
 
+int encode_bf16_map(CUtensorMap *m, const void *base, int rank, const uint64_t *dims, const uint64_t *strides,
+                    const uint32_t *box, int span)
+{
+    cuuint64_t d[3], st[2] = {};
+    cuuint32_t b[3], es[3] = {1, 1, 1};
+    for (int i = 0; i < rank; ++i) {
+        d[i] = dims[i];
+        b[i] = box[i];
+        if (i > 0)
+            st[i - 1] = strides[i - 1];
+    }
+    const CUresult r =
+        g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<cuuint32_t>(rank), const_cast<void *>(base), d, st, b, es,
+                 CU_TENSOR_MAP_INTERLEAVE_NONE,
+                 span == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
+                 : span == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                              : CU_TENSOR_MAP_SWIZZLE_32B,
+                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? TIM_OK : fail(TIM_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
+}
+
 cudaError_t workspace_free(void *p, cudaStream_t s) { return cudaFreeAsync(p, s); }
 
 // Records a formatted message for tim_last_error() on the calling thread; returns code.

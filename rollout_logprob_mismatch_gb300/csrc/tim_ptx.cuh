@@ -167,6 +167,29 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map
         : "memory");
 }
 
+// 3-D tiled tensor load (x innermost).
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, uint32_t bar,
+                                            int32_t x, int32_t y, int32_t z, uint64_t policy)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "l"(policy)
+        : "memory");
+}
+
+// Four rows of a 2-D tensor, one box row each, from column x on (the map's box is one
+// row high); they land one after the other.
+__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap *map, uint32_t bar, int32_t x, int32_t y0,
+                                            int32_t y1, int32_t y2, int32_t y3, uint64_t policy)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%3, %4, %5, %6, %7}], [%2], %8;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y0), "r"(y1), "r"(y2), "r"(y3), "l"(policy)
+        : "memory");
+}
+
 // The same load issued by either CTA of a CTA pair (2-SM UMMA): the tile lands
 // in this CTA's shared memory at `dst`, and the transaction bytes complete on
 // the mbarrier at shared::cluster address `bar`, which may be the peer's.
@@ -464,6 +487,21 @@ __device__ __forceinline__ uint64_t sdesc_mnmajor_sw128(uint32_t saddr, uint32_t
     return d;
 }
 
+// The same for an operand whose M (or N) extent is one swizzle span of SPAN = 32, 64 or
+// 128 bytes: each k index is a row of SPAN bytes, 8-row core groups 8 SPAN bytes apart,
+// swizzle mode 6, 4 or 2.
+template <int SPAN> __device__ __forceinline__ uint64_t sdesc_mnmajor_span(uint32_t saddr)
+{
+    static_assert(SPAN == 32 || SPAN == 64 || SPAN == 128, "a swizzle span");
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+    d |= static_cast<uint64_t>(1u) << 16;
+    d |= static_cast<uint64_t>((8u * SPAN) >> 4) << 32;
+    d |= static_cast<uint64_t>(1u) << 46;
+    d |= static_cast<uint64_t>(SPAN == 128 ? 2u : SPAN == 64 ? 4u : 6u) << 61;
+    return d;
+}
+
 // Instruction descriptor for tcgen05.mma kind::f16: D fp32 (bits 4-5 = 1),
 // A and B bf16 (bits 7-9 = 1, 10-12 = 1), A / B K-major (bit 15 / 16 = 0) or
 // MN-major (= 1), N >> 3 in bits 17-22, M >> 4 in bits 24-28.
@@ -492,6 +530,24 @@ __device__ __forceinline__ void tmem_load32(uint32_t taddr, float (&v)[32])
         : "memory");
 #pragma unroll
     for (int j = 0; j < 32; ++j)
+        v[j] = __uint_as_float(r[j]);
+}
+
+// 16 of them.
+__device__ __forceinline__ void tmem_load16(uint32_t taddr, float (&v)[16])
+{
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
         v[j] = __uint_as_float(r[j]);
 }
 
