@@ -33,6 +33,39 @@ template <int PARTS> __device__ __forceinline__ void split_bf16(float x, uint16_
     }
 }
 
+// Eight values as P planes of packed bf16 parts, split_bf16 of each.
+template <int P> __device__ __forceinline__ void split8(const float (&x)[8], uint32_t (&o)[P][4])
+{
+    float most = 0.f;
+    if (P > 1) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            most = fmaxf(most, fabsf(x[k]));
+    }
+    const bool finite = most <= 3.38953139e38f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        float lo = x[2 * k], hi = x[2 * k + 1];
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            o[i][k] = pack2<__nv_bfloat16>(lo, hi);
+            lo -= __uint_as_float(o[i][k] << 16);
+            hi -= __uint_as_float(o[i][k] & 0xffff0000u);
+        }
+    }
+    if (P > 1 && !finite) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            uint16_t a[P], b[P];
+            split_bf16<P>(x[2 * k], a);
+            split_bf16<P>(x[2 * k + 1], b);
+#pragma unroll
+            for (int i = 0; i < P; ++i)
+                o[i][k] = a[i] | static_cast<uint32_t>(b[i]) << 16;
+        }
+    }
+}
+
 // A whole warp waits for a barrier's phase; the same answer in every lane (false: some
 // lane's wait ran out, or another role's did), so that the warp leaves its loops together.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *abort, uint64_t budget_ns)

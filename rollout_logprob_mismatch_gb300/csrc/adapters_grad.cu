@@ -12,13 +12,14 @@
 // slab order.  Both products take the same tile [128 rows x 128 columns] from shared
 // memory (tcgen05.mma, bf16 -> fp32): du with the rows as M and the columns as K
 // (K-major), dB with the columns as M and the rows as K (MN-major, the same bytes).
-//   warp 0      copies: dy's rows by TMA gathers (the rows of an adapter lie anywhere),
-//               the adapter's factor and t by TMA tiles
+//   warp 0      the adapter's factor and t, by TMA
 //   warp 1      one thread issues the products
 //   warps 2-5   du and dB from TMEM to memory
-//   warps 6-13  fp32, fp16 or rows off a 16-byte boundary only (RAW): the tile from plain
-//               loads, as one or two planes of bf16 parts, x = hi + lo leaves at most
-//               2^-16 |x|
+//   warps 6-    the tiles (the rows of an adapter lie anywhere): 16-byte asynchronous
+//               copies to their swizzled places; fp32, fp16 and rows off a 16-byte boundary
+//               (RAW) by plain loads, as one or two planes of bf16 parts, x = hi + lo leaves
+//               at most 2^-16 |x|
+// (TMA gathers of four rows brought the same tiles at 3.0 us a tile of 32 KB and SM.)
 // Every sum has one order, fixed by the rows' order and V: the same call gives the same bits.
 #include <algorithm>
 #include <type_traits>
@@ -34,7 +35,12 @@ constexpr int STEP = AG_STEP;           // rows of a tile
 constexpr int SUB = STEP * 128;         // bytes of 64 columns of a tile
 constexpr int PARTS = 2;                // of t
 
-template <typename T, bool RAW, int RP> struct Shape {
+// How tiles are brought: COPY, bf16 rows from 16-byte boundaries on; LOAD, other types'
+// rows from there; ANY, rows that start anywhere.
+enum { COPY, LOAD, ANY };
+
+template <typename T, int HOW, int RP> struct Shape {
+    static constexpr bool RAW = HOW != COPY;
     static constexpr int PLANES = std::is_same<T, __nv_bfloat16>::value ? 1 : 2;
     static constexpr int SPAN = RP * 2;                        // bytes of a row of the factor, or of a part of t
     static constexpr int BLOCKS = ag_blocks(RP);               // tiles of a slab at most
@@ -46,10 +52,11 @@ template <typename T, bool RAW, int RP> struct Shape {
     static constexpr int ROOM = AG_SMEM - 2048 - FACTORS * FACTOR - TS * TT;
     static constexpr int STAGES = ROOM / TILE < 4 ? ROOM / TILE : 4;
     static constexpr int BYTES = AG_SMEM;
-    static constexpr int CONVERT = RAW ? 8 : 0;                // warps that write tiles
-    static constexpr int THREADS = (6 + CONVERT) * 32;
-    static constexpr uint32_t TMEM = (2 + BLOCKS) * RP <= 256 ? 256 : 512;   // du twice, dB's blocks
-    static_assert(STAGES >= 2 && (2 + BLOCKS) * RP <= 512, "shared memory, TMEM");
+    static constexpr int WRITERS = RAW ? 8 : 4;                // warps that bring tiles
+    static constexpr int THREADS = (6 + WRITERS) * 32;
+    static constexpr int DBS = (2 + 2 * BLOCKS) * RP <= 512 ? 2 : 1;   // dB's sums: while one adapter's are written the next's begin
+    static constexpr uint32_t TMEM = 512;                      // du twice, dB's blocks
+    static_assert(STAGES >= 2 && (2 + DBS * BLOCKS) * RP <= 512, "shared memory, TMEM");
 };
 
 // An adapter's positions [begin, end) of a part [p0, p1) of the batch: parts meet at a
@@ -69,6 +76,13 @@ __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr)
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                  : "r"(addr)
+                 : "memory");
+}
+
+// `bytes` of 16 global -> shared, zeros in the rest.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, uint32_t bytes)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes)
                  : "memory");
 }
 
@@ -96,12 +110,13 @@ template <int RP> __device__ __forceinline__ void tmem_row(uint32_t taddr, float
     }
 }
 
-template <typename T, bool RAW, int RP>
-__global__ void __launch_bounds__(Shape<T, RAW, RP>::THREADS, 1)
-    adapters_grad_kernel(const __grid_constant__ CUtensorMap map_dy, const __grid_constant__ CUtensorMap map_b,
-                         const __grid_constant__ CUtensorMap map_t, const __grid_constant__ AdapterGradArgs a)
+template <typename T, int HOW, int RP>
+__global__ void __launch_bounds__(Shape<T, HOW, RP>::THREADS, 1)
+    adapters_grad_kernel(const __grid_constant__ CUtensorMap map_b, const __grid_constant__ CUtensorMap map_t,
+                         const __grid_constant__ AdapterGradArgs a)
 {
-    using S = Shape<T, RAW, RP>;
+    using S = Shape<T, HOW, RP>;
+    constexpr bool RAW = HOW != COPY;
     constexpr uint32_t IDESC_DU = idesc_bf16_f32(STEP, RP, false, true), IDESC_DB = idesc_bf16_f32(BC, RP, true, true);
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -116,8 +131,10 @@ __global__ void __launch_bounds__(Shape<T, RAW, RP>::THREADS, 1)
     auto fempty = [&](int i) { return bar0 + 8u * (14 + i); };
     auto dufull = [&](int i) { return bar0 + 8u * (16 + i); };
     auto duempty = [&](int i) { return bar0 + 8u * (18 + i); };
-    const uint32_t dbfull = bar0 + 8u * 20, dbempty = bar0 + 8u * 21, drain = bar0 + 8u * 22;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 23);
+    auto dbfull = [&](int i) { return bar0 + 8u * (20 + i); };
+    auto dbempty = [&](int i) { return bar0 + 8u * (22 + i); };
+    const uint32_t drain = bar0 + 8u * 24;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 25);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -125,7 +142,7 @@ __global__ void __launch_bounds__(Shape<T, RAW, RP>::THREADS, 1)
     const int blocks = (min(a.V, c0 + a.cols) - c0 + BC - 1) / BC;
     if (tid == 0) {
         for (int i = 0; i < S::STAGES; ++i) {
-            mbar_init(full(i), RAW ? S::CONVERT : 1);
+            mbar_init(full(i), S::WRITERS);
             mbar_init(empty(i), 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -135,16 +152,14 @@ __global__ void __launch_bounds__(Shape<T, RAW, RP>::THREADS, 1)
             mbar_init(fempty(i), 1);
             mbar_init(dufull(i), 1);
             mbar_init(duempty(i), 4);
+            mbar_init(dbfull(i), 1);
+            mbar_init(dbempty(i), 4);
         }
-        mbar_init(dbfull, 1);
-        mbar_init(dbempty, 4);
         mbar_init(drain, 1);
         *abort_flag = 0;
         fence_mbar_init();
     }
     if (warp == 0 && lane == 0) {
-        if (!RAW)
-            tma_prefetch_desc(&map_dy);
         tma_prefetch_desc(&map_b);
         tma_prefetch_desc(&map_t);
     }
@@ -172,11 +187,10 @@ __global__ void __launch_bounds__(Shape<T, RAW, RP>::THREADS, 1)
 
     if (warp == 0) {
         // ------------------------------------------------------------ copies
-        const uint64_t pol = l2_policy_evict_first(), pol_keep = l2_policy_evict_normal();
-        Ring<S::STAGES> st;
+        const uint64_t pol_keep = l2_policy_evict_normal();
         Ring<S::TS> tr;
         Ring<S::FACTORS> fr;
-        uint32_t used = 0, used_t = 0, used_f = 0, par = 0, par_t = 0, par_f = 0;   // slots filled, parity of their last fill
+        uint32_t used_t = 0, used_f = 0, par_t = 0, par_f = 0;   // slots filled, parity of their last fill
         segments([&](int ad, int b, int e) {
             if (!warp_wait(fempty(fr.slot), fr.parity ^ 1u, abort_flag, budget))
                 return false;
@@ -201,39 +215,11 @@ __global__ void __launch_bounds__(Shape<T, RAW, RP>::THREADS, 1)
                 used_t |= 1u << tr.slot;
                 par_t = (par_t & ~(1u << tr.slot)) | (tr.parity << tr.slot);
                 tr.next();
-                if (RAW)
-                    continue;
-                // rows in whole sixteens: past the adapter's last its last once more (their t is 0)
-                const int groups = (min(STEP, e - p) + 15) / 16 * 4;
-                int row[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    row[j] = a.plan.perm[min(p + 4 * lane + j, e - 1)];
-                for (int c = 0; c < blocks; ++c) {
-                    if (!warp_wait(empty(st.slot), st.parity ^ 1u, abort_flag, budget))
-                        return false;
-                    if (lane == 0)
-                        mbar_arrive_expect_tx(full(st.slot), static_cast<uint32_t>(groups) * 1024u);
-                    __syncwarp();
-                    if (lane < groups) {
-                        const uint32_t dst = tiles + st.slot * S::TILE + lane * 512;
-                        const int x = c0 + c * BC;
-                        TIM_DCHECK((x & 7) == 0 && row[3] >= 0 && row[3] < a.N, a.status, TIM_CHECK_TMA_COORD, x, row[3]);
-                        tma_gather4(dst, &map_dy, full(st.slot), x, row[0], row[1], row[2], row[3], pol);
-                        tma_gather4(dst + SUB, &map_dy, full(st.slot), x + 64, row[0], row[1], row[2], row[3], pol);
-                    }
-                    used |= 1u << st.slot;
-                    par = (par & ~(1u << st.slot)) | (st.parity << st.slot);
-                    st.next();
-                }
             }
             return true;
         });
         // no copy is in flight when the CTA leaves
         if (lane == 0) {
-            for (int i = 0; i < S::STAGES; ++i)
-                if (!RAW && (used >> i & 1u))
-                    drain_wait(full(i), par >> i & 1u);
             for (int i = 0; i < 2; ++i) {
                 if (used_t >> i & 1u)
                     drain_wait(tfull(i), par_t >> i & 1u);
@@ -249,39 +235,46 @@ __global__ void __launch_bounds__(Shape<T, RAW, RP>::THREADS, 1)
             Ring<S::TS> tr;
             Ring<S::FACTORS> fr;
             Ring<2> du;
-            Ring<1> db;
+            Ring<S::DBS> db;
             segments([&](int, int b, int e) {
                 if (!mbar_wait(ffull(fr.slot), fr.parity, abort_flag, budget) ||
-                    !mbar_wait(dbempty, db.parity ^ 1u, abort_flag, budget))
+                    !mbar_wait(dbempty(db.slot), db.parity ^ 1u, abort_flag, budget))
                     return false;
-                const uint32_t fs = factors + fr.slot * S::FACTOR;
+                const uint64_t fdesc = sdesc_mnmajor_span<S::SPAN>(factors + fr.slot * S::FACTOR);
+                const uint32_t tdb = tmem + 2 * RP + db.slot * (S::BLOCKS * RP);
                 for (int p = b; p < e; p += STEP) {
                     if (!mbar_wait(tfull(tr.slot), tr.parity, abort_flag, budget) ||
                         !mbar_wait(duempty(du.slot), du.parity ^ 1u, abort_flag, budget))
                         return false;
                     tc_fence_after();
                     const int steps = (min(STEP, e - p) + 15) / 16;   // of 16 rows
-                    const uint32_t td = tmem + du.slot * RP, tt = ts + tr.slot * S::TT;
+                    const uint32_t td = tmem + du.slot * RP;
+                    const uint64_t tdesc = sdesc_mnmajor_span<S::SPAN>(ts + tr.slot * S::TT);
                     for (int c = 0; c < blocks; ++c) {
                         if (!mbar_wait(full(st.slot), st.parity, abort_flag, budget))
                             return false;
                         tc_fence_after();
-                        const uint32_t tile = tiles + st.slot * S::TILE, tb = tmem + 2 * RP + c * RP;
+                        const uint32_t tile = tiles + st.slot * S::TILE, tb = tdb + c * RP;
+                        const uint64_t fd = fdesc + static_cast<uint32_t>(c * (BC * S::SPAN / 16));
 #pragma unroll
                         for (int i = 0; i < S::PLANES; ++i) {
-                            const uint32_t pl = tile + i * 2 * SUB;
-                            // du += tile x factor, 16 columns at a time
+                            // du += tile x factor, 16 columns at a time, and dB += tile^T x t, 16 rows at
+                            // a time, in turn (neither waits for itself); lo lo is of the size of what
+                            // the parts leave
+                            const uint64_t ud = sdesc_kmajor_sw128(tile + i * 2 * SUB);
+                            const uint64_t bd = sdesc_mnmajor_sw128(tile + i * 2 * SUB, SUB);
+                            const int parts = i == 0 ? PARTS : 1;
 #pragma unroll
-                            for (int k = 0; k < BC / 16; ++k)
-                                umma_bf16(td, sdesc_kmajor_sw128(pl + (k / 4) * SUB) + 2u * (k % 4),
-                                          sdesc_mnmajor_span<S::SPAN>(fs + (c * BC + k * 16) * S::SPAN), IDESC_DU,
-                                          (c | i | k) != 0);
-                            // dB += tile^T x t, 16 rows at a time; lo lo is of the size of what the parts leave
-                            for (int j = 0; j < (i == 0 ? PARTS : 1); ++j)
-                                for (int k = 0; k < steps; ++k)
-                                    umma_bf16(tb, sdesc_mnmajor_sw128(pl, SUB) + 128u * k,
-                                              sdesc_mnmajor_span<S::SPAN>(tt + (j * STEP + k * 16) * S::SPAN), IDESC_DB,
-                                              p != b || (i | j | k) != 0);
+                            for (int k = 0; k < BC / 16; ++k) {
+                                umma_bf16(td, ud + static_cast<uint32_t>((k / 4) * (SUB / 16) + 2 * (k % 4)),
+                                          fd + static_cast<uint32_t>(k * S::SPAN), IDESC_DU, (c | i | k) != 0);
+                                if (k < steps) {
+#pragma unroll
+                                    for (int j = 0; j < parts; ++j)
+                                        umma_bf16(tb, bd + 128u * k, tdesc + static_cast<uint32_t>((j * STEP / 16 + k) * S::SPAN),
+                                                  IDESC_DB, p != b || (i | j | k) != 0);
+                                }
+                            }
                         }
                         umma_commit(empty(st.slot));
                         st.next();
@@ -292,7 +285,7 @@ __global__ void __launch_bounds__(Shape<T, RAW, RP>::THREADS, 1)
                     du.next();
                 }
                 umma_commit(fempty(fr.slot));
-                umma_commit(dbfull);
+                umma_commit(dbfull(db.slot));
                 fr.next();
                 db.next();
                 return true;
@@ -306,7 +299,7 @@ __global__ void __launch_bounds__(Shape<T, RAW, RP>::THREADS, 1)
         const int m = (warp & 3) * 32 + lane;   // row of du, column of dB's block
         const uint32_t mine = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
         Ring<2> du;
-        Ring<1> db;
+        Ring<S::DBS> db;
         bool ok = true;
         for (int ad = 0; ok && ad < a.n; ++ad) {
             const int ob = a.plan.offsets[ad], oe = a.plan.offsets[ad + 1];
@@ -342,7 +335,7 @@ __global__ void __launch_bounds__(Shape<T, RAW, RP>::THREADS, 1)
             if (!ok)
                 break;
             if (some) {
-                ok = warp_wait(dbfull, db.parity, abort_flag, budget);
+                ok = warp_wait(dbfull(db.slot), db.parity, abort_flag, budget);
                 if (!ok)
                     break;
                 tc_fence_after();
@@ -351,7 +344,7 @@ __global__ void __launch_bounds__(Shape<T, RAW, RP>::THREADS, 1)
                 float v[RP];
                 if (some) {
                     __syncwarp();
-                    tmem_row<RP>(mine + 2 * RP + c * RP, v);
+                    tmem_row<RP>(mine + 2 * RP + (db.slot * S::BLOCKS + c) * RP, v);
                 } else {
 #pragma unroll
                     for (int r = 0; r < RP; ++r)
@@ -380,74 +373,146 @@ __global__ void __launch_bounds__(Shape<T, RAW, RP>::THREADS, 1)
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0)
-                    mbar_arrive(dbempty);
+                    mbar_arrive(dbempty(db.slot));
                 db.next();
             }
         }
     } else {
-        // ------------------------------------------------------------ tiles from plain loads
-        // thread: columns 8 (t % 16) .. of rows t / 16, t / 16 + 16, ... of a tile
-        constexpr int AHEAD = 4;   // rows in flight together
+        // ------------------------------------------------------------ tiles
+        // a thread has columns 8 (t % 16) .. of every EACH-th row of a tile; 128-byte swizzle:
+        // the 16-byte pieces of row m are exchanged by m % 8
+        constexpr int EACH = S::WRITERS * 2, ROWS = STEP / EACH;
         const int t = tid - 6 * 32, chunk = t & 15, r0 = t >> 4;
+        auto place = [&](int m) {
+            return static_cast<uint32_t>((chunk >> 3) * SUB + m * 128 + (((chunk & 7) ^ (m & 7)) << 4));
+        };
+        int row[ROWS];   // of the step; negative: past its last
+        auto look_up = [&](int p, int rows) {
+#pragma unroll
+            for (int i = 0; i < ROWS; ++i)
+                row[i] = r0 + EACH * i < rows ? a.plan.perm[p + r0 + EACH * i] : -1;
+        };
+        auto at = [&](int i) { return dy + static_cast<size_t>(row[i]) * a.ld; };
         Ring<S::STAGES> st;
-        segments([&](int, int b, int e) {
-            for (int p = b; p < e; p += STEP) {
-                const int rows = min(STEP, e - p), padded = (rows + 15) / 16 * 16;
-                const T *row[STEP / 16];
+        if constexpr (!RAW) {
+            constexpr int LAG = 2;   // tiles on their way behind the one being asked for
+            Ring<S::STAGES> landed;
+            int asked = 0;
+            auto arrive = [&] {   // the oldest tile on its way has landed
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(full(landed.slot));
+                landed.next();
+            };
+            segments([&](int, int b, int e) {
+                for (int p = b; p < e; p += STEP) {
+                    const int rows = min(STEP, e - p), padded = (rows + 15) / 16 * 16;
+                    look_up(p, rows);
+                    for (int c = 0; c < blocks; ++c) {
+                        const int col = c0 + c * BC + chunk * 8;
+                        const uint32_t bytes = col < a.V ? static_cast<uint32_t>(min(8, a.V - col)) * 2u : 0u;
+                        if (!warp_wait(empty(st.slot), st.parity ^ 1u, abort_flag, budget))
+                            return false;
+                        const uint32_t dst = tiles + st.slot * S::TILE;
 #pragma unroll
-                for (int i = 0; i < STEP / 16; ++i) {
-                    const int m = r0 + 16 * i;
-                    row[i] = m < rows ? dy + static_cast<size_t>(a.plan.perm[p + m]) * a.ld : nullptr;
-                }
-                for (int c = 0; c < blocks; ++c) {
-                    const int col = c0 + c * BC + chunk * 8;
-                    bool waited = false;
-#pragma unroll
-                    for (int i0 = 0; i0 < STEP / 16; i0 += AHEAD) {
-                        if (i0 * 16 >= padded)
-                            break;
-                        Raw8<T> x[AHEAD];
-#pragma unroll
-                        for (int i = 0; i < AHEAD; ++i)
-                            if (row[i0 + i] && col < a.V)
-                                load8<T>(x[i], row[i0 + i], col, a.V, row_shift(row[i0 + i]));
-                        if (!waited) {   // the first loads are on their way meanwhile
-                            if (!warp_wait(empty(st.slot), st.parity ^ 1u, abort_flag, budget))
-                                return false;
-                            waited = true;
-                        }
-#pragma unroll
-                        for (int i = 0; i < AHEAD; ++i) {
-                            const int m = r0 + 16 * (i0 + i);
-                            if (m >= padded)
-                                continue;
-                            uint32_t o[S::PLANES][4] = {};
-                            if (row[i0 + i]) {
-#pragma unroll
-                                for (int k = 0; k < 8; ++k) {
-                                    uint16_t part[S::PLANES];
-                                    split_bf16<S::PLANES>(col + k < a.V ? Elem<T>::get(x[i].w, k) : 0.f, part);
-#pragma unroll
-                                    for (int j = 0; j < S::PLANES; ++j)
-                                        o[j][k >> 1] |= static_cast<uint32_t>(part[j]) << ((k & 1) * 16);
-                                }
-                            }
-                            // 128-byte swizzle: the 16-byte pieces of row m are exchanged by m % 8
-                            uint8_t *dst = smem + st.slot * S::TILE + (chunk >> 3) * SUB + m * 128 + (((chunk & 7) ^ (m & 7)) << 4);
-#pragma unroll
-                            for (int j = 0; j < S::PLANES; ++j)
-                                *reinterpret_cast<uint4 *>(dst + j * 2 * SUB) = make_uint4(o[j][0], o[j][1], o[j][2], o[j][3]);
+                        for (int i = 0; i < ROWS; ++i)   // zeros past the row's end and past the step's last row
+                            if (r0 + EACH * i < padded)
+                                cp_async16(dst + place(r0 + EACH * i), row[i] >= 0 && bytes ? at(i) + col : dy,
+                                           row[i] >= 0 ? bytes : 0u);
+                        asm volatile("cp.async.commit_group;" ::: "memory");
+                        st.next();
+                        if (++asked > LAG) {
+                            asm volatile("cp.async.wait_group %0;" ::"n"(LAG) : "memory");
+                            arrive();
                         }
                     }
+                }
+                return true;
+            });
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            for (int i = min(asked, LAG); i > 0; --i)
+                arrive();
+        } else {
+            constexpr int AHEAD = 4;   // rows that are loaded while the four before are rewritten
+            Raw8<T> x[AHEAD];
+            int x_row = -1, x_slot = 0, x_col = 0, x_padded = 0;   // x_row < 0: nothing is loaded
+            uint32_t x_parity = 0, x_live = 0;
+            bool x_last = false;
+            auto put = [&]() {   // the rows loaded before
+                if (x_row < 0)
+                    return true;
+                if (x_row == 0 && !warp_wait(empty(x_slot), x_parity ^ 1u, abort_flag, budget))
+                    return false;
+#pragma unroll
+                for (int i = 0; i < AHEAD; ++i) {
+                    const int m = r0 + EACH * (x_row + i);
+                    if (m >= x_padded)
+                        continue;
+                    uint32_t o[S::PLANES][4] = {};
+                    if (x_live >> i & 1u) {
+                        float v[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            v[k] = Elem<T>::get(x[i].w, k);
+                        if (x_col + 8 > a.V) {
+#pragma unroll
+                            for (int k = 0; k < 8; ++k)
+                                v[k] = x_col + k < a.V ? v[k] : 0.f;
+                        }
+                        split8<S::PLANES>(v, o);
+                    }
+#pragma unroll
+                    for (int j = 0; j < S::PLANES; ++j)
+                        *reinterpret_cast<uint4 *>(smem + x_slot * S::TILE + j * 2 * SUB + place(m)) =
+                            make_uint4(o[j][0], o[j][1], o[j][2], o[j][3]);
+                }
+                if (x_last) {
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0)
-                        mbar_arrive(full(st.slot));
-                    st.next();
+                        mbar_arrive(full(x_slot));
                 }
-            }
-            return true;
-        });
+                return true;
+            };
+            segments([&](int, int b, int e) {
+                for (int p = b; p < e; p += STEP) {
+                    const int rows = min(STEP, e - p), padded = (rows + 15) / 16 * 16;
+                    look_up(p, rows);
+                    for (int c = 0; c < blocks; ++c) {
+                        const int col = c0 + c * BC + chunk * 8;
+#pragma unroll
+                        for (int i0 = 0; i0 < ROWS; i0 += AHEAD) {
+                            if (i0 * EACH >= padded)
+                                break;
+                            Raw8<T> y[AHEAD];
+                            uint32_t y_live = 0;
+#pragma unroll
+                            for (int i = 0; i < AHEAD; ++i)
+                                if (row[i0 + i] >= 0 && col < a.V) {
+                                    load8<T>(y[i], at(i0 + i), col, a.V, HOW == LOAD ? 0u : row_shift(at(i0 + i)));
+                                    y_live |= 1u << i;
+                                }
+                            if (!put())
+                                return false;
+#pragma unroll
+                            for (int i = 0; i < AHEAD; ++i)
+                                x[i] = y[i];
+                            x_row = i0;
+                            x_slot = st.slot;
+                            x_parity = st.parity;
+                            x_col = col;
+                            x_padded = padded;
+                            x_live = y_live;
+                            x_last = (i0 + AHEAD) * EACH >= padded;
+                        }
+                        st.next();
+                    }
+                }
+                return true;
+            });
+            put();
+        }
     }
     tc_fence_before();
     __syncthreads();
@@ -528,14 +593,6 @@ template <int RT> struct DaShape {
     static constexpr int STAGE = ROWS * (HROW + UROW), BYTES = STAGES * STAGE;
 };
 
-// 16 bytes global -> shared, zeros where on is false.
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool on)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src)),
-                 "r"(on ? 16u : 0u)
-                 : "memory");
-}
-
 template <int RT> __global__ void __launch_bounds__(256) adapters_dA_kernel(const AdapterGradArgs a)
 {
     using S = DaShape<RT>;
@@ -565,12 +622,12 @@ template <int RT> __global__ void __launch_bounds__(256) adapters_dA_kernel(cons
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const bool on = row[i] >= 0 && d0 + hc < a.D;
-                cp_async16(h0 + (tid / 16 + i * 16) * HROW + hc * 2, a.h + (on ? static_cast<size_t>(row[i]) * a.D + d0 + hc : 0), on);
+                cp_async16(h0 + (tid / 16 + i * 16) * HROW + hc * 2, a.h + (on ? static_cast<size_t>(row[i]) * a.D + d0 + hc : 0), on ? 16u : 0u);
             }
             for (int i = tid; i < ROWS * (3 * RT / 8); i += 256) {
                 const int m = i / (3 * RT / 8), c = i % (3 * RT / 8) * 8;
                 const bool on = p + m < e;
-                cp_async16(u0 + m * UROW + c * 2, a.du + (on ? static_cast<size_t>(p + m) * (3 * RT) + c : 0), on);
+                cp_async16(u0 + m * UROW + c * 2, a.du + (on ? static_cast<size_t>(p + m) * (3 * RT) + c : 0), on ? 16u : 0u);
             }
             look_up(p + ROWS);
         }
@@ -722,10 +779,10 @@ cudaError_t launch(F kernel, dim3 grid, int threads, int smem, const AdapterGrad
 }
 
 // The gradient's launch; maps = null: the kernel's shared memory is granted instead.
-template <typename T, bool RAW, int RP> cudaError_t grad(const CUtensorMap *maps, const AdapterGradArgs &a, cudaStream_t s)
+template <typename T, int HOW, int RP> cudaError_t grad(const CUtensorMap *maps, const AdapterGradArgs &a, cudaStream_t s)
 {
-    using S = Shape<T, RAW, RP>;
-    auto kernel = adapters_grad_kernel<T, RAW, RP>;
+    using S = Shape<T, HOW, RP>;
+    auto kernel = adapters_grad_kernel<T, HOW, RP>;
     if (!maps)
         return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::BYTES);
     cudaLaunchConfig_t cfg = {};
@@ -736,25 +793,26 @@ template <typename T, bool RAW, int RP> cudaError_t grad(const CUtensorMap *maps
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, maps[0], maps[1], maps[2], a);
+    return cudaLaunchKernelEx(&cfg, kernel, maps[0], maps[1], a);
 }
 
-template <int RP> cudaError_t grad(const CUtensorMap *maps, const AdapterGradArgs &a, int dtype, bool raw, cudaStream_t s)
+template <int RP> cudaError_t grad(const CUtensorMap *maps, const AdapterGradArgs &a, int dtype, bool aligned, cudaStream_t s)
 {
     if (dtype == TIM_F32)
-        return grad<float, true, RP>(maps, a, s);
+        return aligned ? grad<float, LOAD, RP>(maps, a, s) : grad<float, ANY, RP>(maps, a, s);
     if (dtype == TIM_F16)
-        return grad<__half, true, RP>(maps, a, s);
-    return raw ? grad<__nv_bfloat16, true, RP>(maps, a, s) : grad<__nv_bfloat16, false, RP>(maps, a, s);
+        return aligned ? grad<__half, LOAD, RP>(maps, a, s) : grad<__half, ANY, RP>(maps, a, s);
+    return aligned ? grad<__nv_bfloat16, COPY, RP>(maps, a, s) : grad<__nv_bfloat16, ANY, RP>(maps, a, s);
 }
 
 template <int RP> cudaError_t prepare()
 {
     const AdapterGradArgs a{};
-    cudaError_t e = grad<RP>(nullptr, a, TIM_BF16, false, nullptr);
+    cudaError_t e = cudaSuccess;
     for (int dtype : {TIM_F32, TIM_F16, TIM_BF16})
-        if (e == cudaSuccess)
-            e = grad<RP>(nullptr, a, dtype, true, nullptr);
+        for (bool aligned : {true, false})
+            if (e == cudaSuccess)
+                e = grad<RP>(nullptr, a, dtype, aligned, nullptr);
     return e;
 }
 
@@ -776,16 +834,16 @@ cudaError_t adapters_grad_prepare_device()
     return e;
 }
 
-cudaError_t adapters_grad_launch(const CUtensorMap (&maps)[3], AdapterGradArgs a, int dtype, int num_sms, cudaStream_t s)
+cudaError_t adapters_grad_launch(const CUtensorMap (&maps)[2], AdapterGradArgs a, int dtype, int num_sms, cudaStream_t s)
 {
     const int RP = std::min(a.RT, 64);
     for (int64_t p0 = 0; p0 < a.N; p0 += a.row_part)
         for (a.r0 = 0; a.r0 < a.R; a.r0 += RP) {
             a.p0 = static_cast<int32_t>(p0);
             a.p1 = static_cast<int32_t>(std::min<int64_t>(a.N, p0 + a.row_part));
-            cudaError_t e = RP == 16   ? grad<16>(maps, a, dtype, a.raw, s)
-                            : RP == 32 ? grad<32>(maps, a, dtype, a.raw, s)
-                                       : grad<64>(maps, a, dtype, a.raw, s);
+            cudaError_t e = RP == 16   ? grad<16>(maps, a, dtype, a.aligned, s)
+                            : RP == 32 ? grad<32>(maps, a, dtype, a.aligned, s)
+                                       : grad<64>(maps, a, dtype, a.aligned, s);
             if (e != cudaSuccess)
                 return e;
             const int64_t items = static_cast<int64_t>(a.p1 - a.p0 + 16) * (RP / 4);

@@ -220,7 +220,7 @@ int tim_adapter_logits_backward(const void *dlogits, int dtype, int64_t N, int64
     a.R = f.R;
     a.n = f.n;
     a.RT = tim::ad_rank_pad(R);
-    a.raw = dtype != TIM_BF16 || !aligned(dlogits, 16) || (N > 1 && (stride % 8 != 0 || stride >= int64_t(1) << 39));
+    a.aligned = aligned(dlogits, 16) && (N == 1 || stride * static_cast<int64_t>(elem_bytes(dtype)) % 16 == 0);
     const int RP = std::min(a.RT, 64);
     // a slab an SM while TMEM has room for its dB, else as many waves of them as it takes
     const int64_t blocks = (V + tim::AG_BLOCK - 1) / tim::AG_BLOCK, most = tim::ag_blocks(RP);
@@ -258,16 +258,13 @@ int tim_adapter_logits_backward(const void *dlogits, int dtype, int64_t N, int64
     a.plan = f.plan;
     a.du = reinterpret_cast<uint16_t *>(w + b_t);
     a.partial = reinterpret_cast<float *>(w + b_t + b_du);
-    CUtensorMap maps[3] = {};
-    const uint64_t d_dy[2] = {static_cast<uint64_t>(V), static_cast<uint64_t>(N)}, s_dy[1] = {static_cast<uint64_t>(N == 1 ? (V + 7) / 8 * 8 : stride) * 2};
+    CUtensorMap maps[2];
     const uint64_t d_b[3] = {static_cast<uint64_t>(R), static_cast<uint64_t>(V), static_cast<uint64_t>(n)};
     const uint64_t s_b[2] = {static_cast<uint64_t>(R) * 2, static_cast<uint64_t>(V * R) * 2};
     const uint64_t d_t[2] = {static_cast<uint64_t>(2 * a.RT), t_rows}, s_t[1] = {static_cast<uint64_t>(2 * a.RT) * 2};
-    const uint32_t box_dy[2] = {64, 1}, box_b[3] = {static_cast<uint32_t>(RP), tim::AG_BLOCK, 1};
-    const uint32_t box_t[2] = {static_cast<uint32_t>(RP), tim::AG_STEP};
-    if ((!a.raw && (rc = tim::encode_bf16_map(&maps[0], dlogits, 2, d_dy, s_dy, box_dy, 128)) != TIM_OK) ||
-        (rc = tim::encode_bf16_map(&maps[1], a.B, 3, d_b, s_b, box_b, 2 * RP)) != TIM_OK ||
-        (rc = tim::encode_bf16_map(&maps[2], f.plan.t, 2, d_t, s_t, box_t, 2 * RP)) != TIM_OK) {
+    const uint32_t box_b[3] = {static_cast<uint32_t>(RP), tim::AG_BLOCK, 1}, box_t[2] = {static_cast<uint32_t>(RP), tim::AG_STEP};
+    if ((rc = tim::encode_bf16_map(&maps[0], a.B, 3, d_b, s_b, box_b, 2 * RP)) != TIM_OK ||
+        (rc = tim::encode_bf16_map(&maps[1], f.plan.t, 2, d_t, s_t, box_t, 2 * RP)) != TIM_OK) {
         tim::workspace_free(ws, s);
         return rc;
     }

@@ -85,7 +85,7 @@ struct AdapterGradArgs {
     int64_t ld;
     int32_t N, V, D, R, n;
     int32_t RT;               // the rank padded (16, 32, 64, 128)
-    int32_t raw;              // rows of dy that are not bf16 from a 16-byte boundary on
+    int32_t aligned;          // every row of dy starts on 16 bytes
     int32_t cols, slabs;      // columns of a slab, slabs
     int32_t row_part;         // positions of a launch
     int32_t p0, p1, r0;       // the launch's positions and first rank
@@ -98,8 +98,8 @@ struct AdapterGradArgs {
     int *status;
 };
 
-// maps: dy, B, t
-cudaError_t adapters_grad_launch(const CUtensorMap (&maps)[3], AdapterGradArgs a, int dtype, int num_sms, cudaStream_t s);
+// maps: B, t
+cudaError_t adapters_grad_launch(const CUtensorMap (&maps)[2], AdapterGradArgs a, int dtype, int num_sms, cudaStream_t s);
 cudaError_t adapters_grad_prepare_device();
 
 // ---------------------------------------------------------------- embedding

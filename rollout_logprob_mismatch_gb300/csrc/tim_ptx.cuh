@@ -178,18 +178,6 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map
         : "memory");
 }
 
-// Four rows of a 2-D tensor, one box row each, from column x on (the map's box is one
-// row high); they land one after the other.
-__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap *map, uint32_t bar, int32_t x, int32_t y0,
-                                            int32_t y1, int32_t y2, int32_t y3, uint64_t policy)
-{
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.L2::cache_hint"
-        " [%0], [%1, {%3, %4, %5, %6, %7}], [%2], %8;" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y0), "r"(y1), "r"(y2), "r"(y3), "l"(policy)
-        : "memory");
-}
-
 // The same load issued by either CTA of a CTA pair (2-SM UMMA): the tile lands
 // in this CTA's shared memory at `dst`, and the transaction bytes complete on
 // the mbarrier at shared::cluster address `bar`, which may be the peer's.
