@@ -31,8 +31,6 @@ namespace tim {
 namespace {
 
 constexpr int BC = AG_BLOCK;            // columns of a tile
-constexpr int STEP = AG_STEP;           // rows of a tile
-constexpr int SUB = STEP * 128;         // bytes of 64 columns of a tile
 constexpr int PARTS = 2;                // of t
 
 // How tiles are brought: COPY, bf16 rows from 16-byte boundaries on; LOAD, other types'
@@ -40,23 +38,27 @@ constexpr int PARTS = 2;                // of t
 enum { COPY, LOAD, ANY };
 
 template <typename T, int HOW, int RP> struct Shape {
-    static constexpr bool RAW = HOW != COPY;
     static constexpr int PLANES = std::is_same<T, __nv_bfloat16>::value ? 1 : 2;
+    static constexpr int STEP = ag_step(HOW != COPY);          // rows of a tile
+    static constexpr int SUB = STEP * 128;                     // bytes of 64 columns of it
     static constexpr int SPAN = RP * 2;                        // bytes of a row of the factor, or of a part of t
     static constexpr int BLOCKS = ag_blocks(RP);               // tiles of a slab at most
     static constexpr int TILE = 2 * SUB * PLANES;
-    static constexpr int FACTOR = BLOCKS * BC * SPAN;
+    static constexpr int FACTORS = (RP == 16 && HOW == COPY ? 2 : 1) * BLOCKS * BC * SPAN;   // bytes for factors: two where they fit
     static constexpr int TT = PARTS * STEP * SPAN;
-    static constexpr int FACTORS = RP == 16 ? 2 : 1;
-    static constexpr int TS = RP == 64 && PLANES == 2 ? 1 : 2;
-    static constexpr int ROOM = AG_SMEM - 2048 - FACTORS * FACTOR - TS * TT;
+    static constexpr int TS = 2;
+    // not COPY: bytes on their way to the threads that rewrite them, in batches of two
+    // 16 x 128 pieces; PIECES 16-byte pieces hold a thread's eight columns
+    static constexpr int PIECES = static_cast<int>(sizeof(T)) / 2 + (HOW == ANY ? 1 : 0);
+    static constexpr int BATCH = 2 * 256 * 16 * PIECES, BATCHES = 65536 / BATCH < 4 ? 65536 / BATCH : 4;
+    static constexpr int STAGING = HOW == COPY ? 0 : BATCHES * BATCH;
+    static constexpr int ROOM = AG_SMEM - 2048 - FACTORS - TS * TT - STAGING;
     static constexpr int STAGES = ROOM / TILE < 4 ? ROOM / TILE : 4;
     static constexpr int BYTES = AG_SMEM;
-    static constexpr int WRITERS = RAW ? 8 : 4;                // warps that bring tiles
+    static constexpr int WRITERS = HOW == COPY ? 4 : 8;        // warps that bring tiles
     static constexpr int THREADS = (6 + WRITERS) * 32;
-    static constexpr int DBS = (2 + 2 * BLOCKS) * RP <= 512 ? 2 : 1;   // dB's sums: while one adapter's are written the next's begin
     static constexpr uint32_t TMEM = 512;                      // du twice, dB's blocks
-    static_assert(STAGES >= 2 && (2 + DBS * BLOCKS) * RP <= 512, "shared memory, TMEM");
+    static_assert(STAGES >= 2 && (2 + BLOCKS) * RP <= 512, "shared memory, TMEM");
 };
 
 // An adapter's positions [begin, end) of a part [p0, p1) of the batch: parts meet at a
@@ -87,12 +89,13 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, uint32
 }
 
 // A ring's place: its slot, and the parity of the slot's current use.
-template <int SLOTS> struct Ring {
-    int slot = 0;
+struct Ring {
+    int slots, slot = 0;
     uint32_t parity = 0;
+    __device__ __forceinline__ explicit Ring(int n) : slots(n) {}
     __device__ __forceinline__ void next()
     {
-        if (++slot == SLOTS) {
+        if (++slot == slots) {
             slot = 0;
             parity ^= 1u;
         }
@@ -116,12 +119,14 @@ __global__ void __launch_bounds__(Shape<T, HOW, RP>::THREADS, 1)
                          const __grid_constant__ AdapterGradArgs a)
 {
     using S = Shape<T, HOW, RP>;
-    constexpr bool RAW = HOW != COPY;
-    constexpr uint32_t IDESC_DU = idesc_bf16_f32(STEP, RP, false, true), IDESC_DB = idesc_bf16_f32(BC, RP, true, true);
+    constexpr int STEP = S::STEP, SUB = S::SUB;
+    // M = 128 in both; of du's rows the first STEP are the tile's (what lies behind a smaller tile is not used)
+    constexpr uint32_t IDESC_DU = idesc_bf16_f32(128, RP, false, true), IDESC_DB = idesc_bf16_f32(BC, RP, true, true);
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    const uint32_t tiles = smem_u32(smem), factors = tiles + S::STAGES * S::TILE, ts = factors + S::FACTORS * S::FACTOR;
-    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + S::STAGES * S::TILE + S::FACTORS * S::FACTOR + S::TS * S::TT);
+    const uint32_t tiles = smem_u32(smem), factors = tiles + S::STAGES * S::TILE, ts = factors + S::FACTORS;
+    const uint32_t staging = ts + S::TS * S::TT;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + S::STAGES * S::TILE + S::FACTORS + S::TS * S::TT + S::STAGING);
     const uint32_t bar0 = smem_u32(bars);
     auto full = [&](int i) { return bar0 + 8u * i; };
     auto empty = [&](int i) { return bar0 + 8u * (4 + i); };
@@ -140,6 +145,9 @@ __global__ void __launch_bounds__(Shape<T, HOW, RP>::THREADS, 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int c0 = blockIdx.x * a.cols;                                   // the slab's columns
     const int blocks = (min(a.V, c0 + a.cols) - c0 + BC - 1) / BC;
+    // two factors, and dB's sums of two adapters, where a slab's are small enough
+    const int factor_bytes = a.cols * S::SPAN, num_factors = 2 * factor_bytes <= S::FACTORS ? 2 : 1;
+    const int db_columns = a.cols / BC * RP, num_db = 2 * RP + 2 * db_columns <= 512 ? 2 : 1;
     if (tid == 0) {
         for (int i = 0; i < S::STAGES; ++i) {
             mbar_init(full(i), S::WRITERS);
@@ -188,8 +196,7 @@ __global__ void __launch_bounds__(Shape<T, HOW, RP>::THREADS, 1)
     if (warp == 0) {
         // ------------------------------------------------------------ copies
         const uint64_t pol_keep = l2_policy_evict_normal();
-        Ring<S::TS> tr;
-        Ring<S::FACTORS> fr;
+        Ring tr(S::TS), fr(num_factors);
         uint32_t used_t = 0, used_f = 0, par_t = 0, par_f = 0;   // slots filled, parity of their last fill
         segments([&](int ad, int b, int e) {
             if (!warp_wait(fempty(fr.slot), fr.parity ^ 1u, abort_flag, budget))
@@ -197,7 +204,7 @@ __global__ void __launch_bounds__(Shape<T, HOW, RP>::THREADS, 1)
             if (lane == 0) {
                 mbar_arrive_expect_tx(ffull(fr.slot), static_cast<uint32_t>(blocks) * BC * S::SPAN);
                 for (int c = 0; c < blocks; ++c)
-                    tma_load_3d(factors + fr.slot * S::FACTOR + c * BC * S::SPAN, &map_b, ffull(fr.slot), a.r0, c0 + c * BC, ad,
+                    tma_load_3d(factors + fr.slot * factor_bytes + c * BC * S::SPAN, &map_b, ffull(fr.slot), a.r0, c0 + c * BC, ad,
                                 pol_keep);
             }
             used_f |= 1u << fr.slot;
@@ -231,17 +238,13 @@ __global__ void __launch_bounds__(Shape<T, HOW, RP>::THREADS, 1)
     } else if (warp == 1) {
         // ------------------------------------------------------------ products
         if (lane == 0) {
-            Ring<S::STAGES> st;
-            Ring<S::TS> tr;
-            Ring<S::FACTORS> fr;
-            Ring<2> du;
-            Ring<S::DBS> db;
+            Ring st(S::STAGES), tr(S::TS), fr(num_factors), du(2), db(num_db);
             segments([&](int, int b, int e) {
                 if (!mbar_wait(ffull(fr.slot), fr.parity, abort_flag, budget) ||
                     !mbar_wait(dbempty(db.slot), db.parity ^ 1u, abort_flag, budget))
                     return false;
-                const uint64_t fdesc = sdesc_mnmajor_span<S::SPAN>(factors + fr.slot * S::FACTOR);
-                const uint32_t tdb = tmem + 2 * RP + db.slot * (S::BLOCKS * RP);
+                const uint64_t fdesc = sdesc_mnmajor_span<S::SPAN>(factors + fr.slot * factor_bytes);
+                const uint32_t tdb = tmem + 2 * RP + db.slot * db_columns;
                 for (int p = b; p < e; p += STEP) {
                     if (!mbar_wait(tfull(tr.slot), tr.parity, abort_flag, budget) ||
                         !mbar_wait(duempty(du.slot), du.parity ^ 1u, abort_flag, budget))
@@ -268,7 +271,7 @@ __global__ void __launch_bounds__(Shape<T, HOW, RP>::THREADS, 1)
                             for (int k = 0; k < BC / 16; ++k) {
                                 umma_bf16(td, ud + static_cast<uint32_t>((k / 4) * (SUB / 16) + 2 * (k % 4)),
                                           fd + static_cast<uint32_t>(k * S::SPAN), IDESC_DU, (c | i | k) != 0);
-                                if (k < steps) {
+                                if (k < STEP / 16 && k < steps) {
 #pragma unroll
                                     for (int j = 0; j < parts; ++j)
                                         umma_bf16(tb, bd + 128u * k, tdesc + static_cast<uint32_t>((j * STEP / 16 + k) * S::SPAN),
@@ -298,8 +301,7 @@ __global__ void __launch_bounds__(Shape<T, HOW, RP>::THREADS, 1)
         // ------------------------------------------------------------ results
         const int m = (warp & 3) * 32 + lane;   // row of du, column of dB's block
         const uint32_t mine = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-        Ring<2> du;
-        Ring<S::DBS> db;
+        Ring du(2), db(num_db);
         bool ok = true;
         for (int ad = 0; ok && ad < a.n; ++ad) {
             const int ob = a.plan.offsets[ad], oe = a.plan.offsets[ad + 1];
@@ -323,7 +325,7 @@ __global__ void __launch_bounds__(Shape<T, HOW, RP>::THREADS, 1)
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive(duempty(du.slot));
-                if (p + m < e) {
+                if (m < STEP && p + m < e) {
                     float4 *o = reinterpret_cast<float4 *>(
                         a.partial + (static_cast<size_t>(blockIdx.x) * (a.p1 - a.p0 + 16) + (p + m - a.p0)) * RP);
 #pragma unroll
@@ -344,7 +346,7 @@ __global__ void __launch_bounds__(Shape<T, HOW, RP>::THREADS, 1)
                 float v[RP];
                 if (some) {
                     __syncwarp();
-                    tmem_row<RP>(mine + 2 * RP + (db.slot * S::BLOCKS + c) * RP, v);
+                    tmem_row<RP>(mine + 2 * RP + db.slot * db_columns + c * RP, v);
                 } else {
 #pragma unroll
                     for (int r = 0; r < RP; ++r)
@@ -392,19 +394,16 @@ __global__ void __launch_bounds__(Shape<T, HOW, RP>::THREADS, 1)
             for (int i = 0; i < ROWS; ++i)
                 row[i] = r0 + EACH * i < rows ? a.plan.perm[p + r0 + EACH * i] : -1;
         };
-        auto at = [&](int i) { return dy + static_cast<size_t>(row[i]) * a.ld; };
-        Ring<S::STAGES> st;
-        if constexpr (!RAW) {
+        auto arrive = [&](int slot) {   // the warp's part of a tile is there
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(full(slot));
+        };
+        if constexpr (HOW == COPY) {
             constexpr int LAG = 2;   // tiles on their way behind the one being asked for
-            Ring<S::STAGES> landed;
+            Ring st(S::STAGES), landed(S::STAGES);
             int asked = 0;
-            auto arrive = [&] {   // the oldest tile on its way has landed
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(full(landed.slot));
-                landed.next();
-            };
             segments([&](int, int b, int e) {
                 for (int p = b; p < e; p += STEP) {
                     const int rows = min(STEP, e - p), padded = (rows + 15) / 16 * 16;
@@ -418,100 +417,157 @@ __global__ void __launch_bounds__(Shape<T, HOW, RP>::THREADS, 1)
 #pragma unroll
                         for (int i = 0; i < ROWS; ++i)   // zeros past the row's end and past the step's last row
                             if (r0 + EACH * i < padded)
-                                cp_async16(dst + place(r0 + EACH * i), row[i] >= 0 && bytes ? at(i) + col : dy,
+                                cp_async16(dst + place(r0 + EACH * i),
+                                           row[i] >= 0 && bytes ? dy + static_cast<size_t>(row[i]) * a.ld + col : dy,
                                            row[i] >= 0 ? bytes : 0u);
                         asm volatile("cp.async.commit_group;" ::: "memory");
                         st.next();
                         if (++asked > LAG) {
                             asm volatile("cp.async.wait_group %0;" ::"n"(LAG) : "memory");
-                            arrive();
+                            arrive(landed.slot);
+                            landed.next();
                         }
                     }
                 }
                 return true;
             });
             asm volatile("cp.async.wait_all;" ::: "memory");
-            for (int i = min(asked, LAG); i > 0; --i)
-                arrive();
+            for (int i = min(asked, LAG); i > 0; --i) {
+                arrive(landed.slot);
+                landed.next();
+            }
         } else {
-            constexpr int AHEAD = 4;   // rows that are loaded while the four before are rewritten
-            Raw8<T> x[AHEAD];
-            int x_row = -1, x_slot = 0, x_col = 0, x_padded = 0;   // x_row < 0: nothing is loaded
-            uint32_t x_parity = 0, x_live = 0;
-            bool x_last = false;
-            auto put = [&]() {   // the rows loaded before
-                if (x_row < 0)
-                    return true;
-                if (x_row == 0 && !warp_wait(empty(x_slot), x_parity ^ 1u, abort_flag, budget))
+            // A thread's pieces go to its own places of the staging ring, so that it waits for
+            // nobody to rewrite them; batches of two rows, up to BATCHES of them on their way.
+            struct Cursor {   // batch `half` (rows 32 half ..) of tile (p, c) of an adapter
+                int ad = -1, p = 0, e = 0, c = 0, half = 0;
+                __device__ __forceinline__ bool seek(const AdapterGradArgs &a)
+                {
+                    while (++ad < a.n) {
+                        const Part r(a.plan.offsets[ad], a.plan.offsets[ad + 1], a.p0, a.p1);
+                        p = r.begin;
+                        e = r.end;
+                        if (p < e)
+                            return true;
+                    }
                     return false;
+                }
+                __device__ __forceinline__ int rows() const { return min(STEP, e - p); }
+                __device__ __forceinline__ bool last() const { return half * 32 + 32 >= rows(); }
+                __device__ __forceinline__ bool next(const AdapterGradArgs &a, int blocks)
+                {
+                    if (!last()) {
+                        ++half;
+                        return true;
+                    }
+                    half = 0;
+                    if (++c < blocks)
+                        return true;
+                    c = 0;
+                    p += STEP;
+                    return p < e || seek(a);
+                }
+            };
+            constexpr int ES = static_cast<int>(sizeof(T)), P = S::PIECES;
+            auto piece = [&](int batch, int i, int k) {
+                return staging + static_cast<uint32_t>(((batch * 2 + i) * P + k) * 4096 + t * 16);
+            };
+            Cursor head;
+            bool more = head.seek(a);
+            Cursor tail = head;
+            bool left = more;
+            Ring st(S::STAGES), in(S::BATCHES), out(S::BATCHES);
+            uint32_t shifts = 0;   // a byte a batch, the latest lowest: the two rows' bytes past a 16-byte boundary
+            auto ask = [&] {       // for the pieces of the head's batch
+                uint32_t two = 0;
+                if (more) {
+                    if (head.c == 0 && head.half == 0)
+                        look_up(head.p, head.rows());
+                    const int col = c0 + head.c * BC + chunk * 8;
 #pragma unroll
-                for (int i = 0; i < AHEAD; ++i) {
-                    const int m = r0 + EACH * (x_row + i);
-                    if (m >= x_padded)
+                    for (int i = 0; i < 2; ++i) {
+                        const int n = head.half ? row[2 + i] : row[i];
+                        if (n < 0 || col >= a.V)
+                            continue;
+                        const T *from = dy + static_cast<size_t>(n) * a.ld + col;
+                        const uint32_t shift = HOW == ANY ? row_shift(from) : 0u;
+                        two |= shift << (4 * i);
+                        const char *src = reinterpret_cast<const char *>(from) - shift;
+                        if (shift == 0 ? col + 8 <= a.V : col >= 8 && col + 16 <= a.V) {
+#pragma unroll
+                            for (int k = 0; k < P; ++k)
+                                if (HOW == LOAD || k < P - 1 || shift != 0)
+                                    cp_async16(piece(in.slot, i, k), src + 16 * k, 16u);
+                        } else {   // a row's first or last columns, one by one
+                            for (int k = 0; k < 8 && col + k < a.V; ++k) {
+                                const uint32_t at = shift + k * ES;
+                                *reinterpret_cast<T *>(smem + (piece(in.slot, i, at / 16) - tiles) + at % 16) = from[k];
+                            }
+                        }
+                    }
+                    more = head.next(a, blocks);
+                }
+                asm volatile("cp.async.commit_group;" ::: "memory");
+                shifts = shifts << 8 | two;
+                in.next();
+            };
+            for (int i = 0; i < S::BATCHES - 1; ++i)
+                ask();
+            while (left) {
+                ask();
+                asm volatile("cp.async.wait_group %0;" ::"n"(S::BATCHES - 1) : "memory");
+                const int rows = tail.rows(), padded = (rows + 15) / 16 * 16, col = c0 + tail.c * BC + chunk * 8;
+                if (tail.half == 0 && !warp_wait(empty(st.slot), st.parity ^ 1u, abort_flag, budget))
+                    break;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int m = tail.half * 32 + i * 16 + r0;
+                    if (m >= padded)
                         continue;
                     uint32_t o[S::PLANES][4] = {};
-                    if (x_live >> i & 1u) {
+                    if (m < rows && col < a.V) {
+                        constexpr int W = Elem<T>::WORDS;
+                        uint32_t x[W + 4] = {};
+#pragma unroll
+                        for (int k = 0; k < P; ++k) {
+                            const uint4 v = *reinterpret_cast<const uint4 *>(smem + (piece(out.slot, i, k) - tiles));
+                            x[4 * k] = v.x;
+                            x[4 * k + 1] = v.y;
+                            x[4 * k + 2] = v.z;
+                            x[4 * k + 3] = v.w;
+                        }
+                        Raw8<T> w;
+                        if (HOW == ANY) {
+                            shift_words<W, ES == 2>(w.w, x, shifts >> (8 * (S::BATCHES - 1) + 4 * i) & 15u);
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < W; ++k)
+                                w.w[k] = x[k];
+                        }
                         float v[8];
 #pragma unroll
                         for (int k = 0; k < 8; ++k)
-                            v[k] = Elem<T>::get(x[i].w, k);
-                        if (x_col + 8 > a.V) {
+                            v[k] = Elem<T>::get(w.w, k);
+                        if (col + 8 > a.V) {
 #pragma unroll
                             for (int k = 0; k < 8; ++k)
-                                v[k] = x_col + k < a.V ? v[k] : 0.f;
+                                v[k] = col + k < a.V ? v[k] : 0.f;
                         }
                         split8<S::PLANES>(v, o);
                     }
 #pragma unroll
                     for (int j = 0; j < S::PLANES; ++j)
-                        *reinterpret_cast<uint4 *>(smem + x_slot * S::TILE + j * 2 * SUB + place(m)) =
+                        *reinterpret_cast<uint4 *>(smem + st.slot * S::TILE + j * 2 * SUB + place(m)) =
                             make_uint4(o[j][0], o[j][1], o[j][2], o[j][3]);
                 }
-                if (x_last) {
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0)
-                        mbar_arrive(full(x_slot));
+                if (tail.last()) {
+                    arrive(st.slot);
+                    st.next();
                 }
-                return true;
-            };
-            segments([&](int, int b, int e) {
-                for (int p = b; p < e; p += STEP) {
-                    const int rows = min(STEP, e - p), padded = (rows + 15) / 16 * 16;
-                    look_up(p, rows);
-                    for (int c = 0; c < blocks; ++c) {
-                        const int col = c0 + c * BC + chunk * 8;
-#pragma unroll
-                        for (int i0 = 0; i0 < ROWS; i0 += AHEAD) {
-                            if (i0 * EACH >= padded)
-                                break;
-                            Raw8<T> y[AHEAD];
-                            uint32_t y_live = 0;
-#pragma unroll
-                            for (int i = 0; i < AHEAD; ++i)
-                                if (row[i0 + i] >= 0 && col < a.V) {
-                                    load8<T>(y[i], at(i0 + i), col, a.V, HOW == LOAD ? 0u : row_shift(at(i0 + i)));
-                                    y_live |= 1u << i;
-                                }
-                            if (!put())
-                                return false;
-#pragma unroll
-                            for (int i = 0; i < AHEAD; ++i)
-                                x[i] = y[i];
-                            x_row = i0;
-                            x_slot = st.slot;
-                            x_parity = st.parity;
-                            x_col = col;
-                            x_padded = padded;
-                            x_live = y_live;
-                            x_last = (i0 + AHEAD) * EACH >= padded;
-                        }
-                        st.next();
-                    }
-                }
-                return true;
-            });
-            put();
+                out.next();
+                left = tail.next(a, blocks);
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
         }
     }
     tc_fence_before();

@@ -230,7 +230,7 @@ int tim_adapter_logits_backward(const void *dlogits, int dtype, int64_t N, int64
     a.slabs = static_cast<int32_t>((blocks + per_slab - 1) / per_slab);
     const int64_t per_row = int64_t(4) * a.slabs * RP;
     a.row_part = static_cast<int32_t>(std::min<int64_t>(
-        N, std::max<int64_t>(tim::AG_PARTIAL_BYTES / per_row / tim::AG_STEP, 1) * tim::AG_STEP));
+        N, std::max<int64_t>(tim::AG_PARTIAL_BYTES / per_row / 128, 1) * 128));
     a.dh = dh;
     a.dA = dA;
     a.dB = dB;
@@ -262,7 +262,8 @@ int tim_adapter_logits_backward(const void *dlogits, int dtype, int64_t N, int64
     const uint64_t d_b[3] = {static_cast<uint64_t>(R), static_cast<uint64_t>(V), static_cast<uint64_t>(n)};
     const uint64_t s_b[2] = {static_cast<uint64_t>(R) * 2, static_cast<uint64_t>(V * R) * 2};
     const uint64_t d_t[2] = {static_cast<uint64_t>(2 * a.RT), t_rows}, s_t[1] = {static_cast<uint64_t>(2 * a.RT) * 2};
-    const uint32_t box_b[3] = {static_cast<uint32_t>(RP), tim::AG_BLOCK, 1}, box_t[2] = {static_cast<uint32_t>(RP), tim::AG_STEP};
+    const uint32_t box_b[3] = {static_cast<uint32_t>(RP), tim::AG_BLOCK, 1}, box_t[2] = {
+        static_cast<uint32_t>(RP), static_cast<uint32_t>(tim::ag_step(dtype != TIM_BF16 || !a.aligned))};
     if ((rc = tim::encode_bf16_map(&maps[0], a.B, 3, d_b, s_b, box_b, 2 * RP)) != TIM_OK ||
         (rc = tim::encode_bf16_map(&maps[1], f.plan.t, 2, d_t, s_t, box_t, 2 * RP)) != TIM_OK) {
         tim::workspace_free(ws, s);

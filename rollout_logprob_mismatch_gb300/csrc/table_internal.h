@@ -68,8 +68,10 @@ cudaError_t adapters_shrink_launch(const AdapterArgs &a, int parts, int num_sms,
 cudaError_t adapters_expand_launch(AdapterArgs a, int dtype, int num_sms, cudaStream_t s);
 cudaError_t adapters_prepare_device();   // shared-memory sizes
 
-// The gradient: slabs of the vocabulary, tiles of 128 rows and 128 columns.
-constexpr int AG_STEP = 128, AG_BLOCK = 128;
+// The gradient: slabs of the vocabulary, tiles of 128 columns and 128 rows (64 where the
+// rows are rewritten: half of the shared memory then holds what is on its way).
+constexpr int AG_BLOCK = 128;
+constexpr int ag_step(bool rewritten) { return rewritten ? 64 : 128; }
 constexpr int AG_PAD = 16;           // t has room for so many rows of zeros behind each adapter's
 constexpr int AG_SMEM = 227 * 1024;
 constexpr int64_t AG_PARTIAL_BYTES = int64_t(1) << 30;   // du's partial sums at most, per part of the batch
