@@ -39,23 +39,24 @@ enum { COPY, LOAD, ANY };
 
 template <typename T, int HOW, int RP> struct Shape {
     static constexpr int PLANES = std::is_same<T, __nv_bfloat16>::value ? 1 : 2;
-    static constexpr int STEP = ag_step(HOW != COPY);          // rows of a tile
-    static constexpr int SUB = STEP * 128;                     // bytes of 64 columns of it
+    static constexpr int STEP = 128 / PLANES;                  // rows of a tile; the second plane lies behind the first as rows 64 ..
+    static constexpr int SUB = 128 * 128;                      // bytes of 64 columns of it
     static constexpr int SPAN = RP * 2;                        // bytes of a row of the factor, or of a part of t
+    static constexpr int SPAN2 = SPAN == 128 ? 128 : 2 * SPAN; // of two parts of t side by side (ranks up to 32)
     static constexpr int BLOCKS = ag_blocks(RP);               // tiles of a slab at most
-    static constexpr int TILE = 2 * SUB * PLANES;
+    static constexpr int TILE = 2 * SUB;
     static constexpr int FACTORS = (RP == 16 && HOW == COPY ? 2 : 1) * BLOCKS * BC * SPAN;   // bytes for factors: two where they fit
     static constexpr int TT = PARTS * STEP * SPAN;
-    static constexpr int TS = 2;
-    // not COPY: bytes on their way to the threads that rewrite them, in batches of two
-    // 16 x 128 pieces; PIECES 16-byte pieces hold a thread's eight columns
+    static constexpr int TS = RP == 64 && PLANES == 1 && HOW != COPY ? 1 : 2;
+    // not COPY: bytes on their way to the threads that rewrite them, in batches of 32 x 128;
+    // PIECES 16-byte pieces hold a thread's eight columns
     static constexpr int PIECES = static_cast<int>(sizeof(T)) / 2 + (HOW == ANY ? 1 : 0);
-    static constexpr int BATCH = 2 * 256 * 16 * PIECES, BATCHES = 65536 / BATCH < 4 ? 65536 / BATCH : 4;
+    static constexpr int BATCH = 512 * 16 * PIECES, BATCHES = 65536 / BATCH < 4 ? 65536 / BATCH : 4;
     static constexpr int STAGING = HOW == COPY ? 0 : BATCHES * BATCH;
     static constexpr int ROOM = AG_SMEM - 2048 - FACTORS - TS * TT - STAGING;
     static constexpr int STAGES = ROOM / TILE < 4 ? ROOM / TILE : 4;
     static constexpr int BYTES = AG_SMEM;
-    static constexpr int WRITERS = HOW == COPY ? 4 : 8;        // warps that bring tiles
+    static constexpr int WRITERS = HOW == COPY ? 8 : 16;       // warps that bring tiles
     static constexpr int THREADS = (6 + WRITERS) * 32;
     static constexpr uint32_t TMEM = 512;                      // du twice, dB's blocks
     static_assert(STAGES >= 2 && (2 + BLOCKS) * RP <= 512, "shared memory, TMEM");
@@ -88,6 +89,12 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, uint32
                  : "memory");
 }
 
+// One arrival on `bar` when this thread's asynchronous copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar)
+{
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
 // A ring's place: its slot, and the parity of the slot's current use.
 struct Ring {
     int slots, slot = 0;
@@ -101,6 +108,17 @@ struct Ring {
         }
     }
 };
+
+// High words of the operands' descriptors (their low words: the address / 16, and the
+// leading offset / 16 from bit 16 on) as of sdesc_kmajor_sw128, sdesc_mnmajor_sw128, and of
+// one swizzle span (32, 64 or 128 bytes, modes 6, 4, 2) as the M or N extent: a row of
+// `span` bytes for each k, 8-row groups 8 span bytes apart.
+__host__ __device__ constexpr uint32_t desc_kmajor_hi() { return 1024u / 16 | 1u << 14 | 2u << 29; }
+__host__ __device__ constexpr uint32_t desc_mnmajor_hi() { return desc_kmajor_hi(); }
+__host__ __device__ constexpr uint32_t desc_span_hi(int span)
+{
+    return static_cast<uint32_t>(8 * span) / 16 | 1u << 14 | (span == 128 ? 2u : span == 64 ? 4u : 6u) << 29;
+}
 
 template <int RP> __device__ __forceinline__ void tmem_row(uint32_t taddr, float (&v)[RP])
 {
@@ -120,8 +138,9 @@ __global__ void __launch_bounds__(Shape<T, HOW, RP>::THREADS, 1)
 {
     using S = Shape<T, HOW, RP>;
     constexpr int STEP = S::STEP, SUB = S::SUB;
-    // M = 128 in both; of du's rows the first STEP are the tile's (what lies behind a smaller tile is not used)
-    constexpr uint32_t IDESC_DU = idesc_bf16_f32(128, RP, false, true), IDESC_DB = idesc_bf16_f32(BC, RP, true, true);
+    // M = 128 in both: du's rows are the tile's (the two planes' products are two parts of the sum)
+    constexpr uint32_t IDESC_DU = idesc_bf16_f32(128, RP, false, true), IDESC_DB = idesc_bf16_f32(BC, RP, true, true),
+                       IDESC_DB2 = idesc_bf16_f32(BC, 2 * RP, true, true);
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t tiles = smem_u32(smem), factors = tiles + S::STAGES * S::TILE, ts = factors + S::FACTORS;
@@ -147,10 +166,11 @@ __global__ void __launch_bounds__(Shape<T, HOW, RP>::THREADS, 1)
     const int blocks = (min(a.V, c0 + a.cols) - c0 + BC - 1) / BC;
     // two factors, and dB's sums of two adapters, where a slab's are small enough
     const int factor_bytes = a.cols * S::SPAN, num_factors = 2 * factor_bytes <= S::FACTORS ? 2 : 1;
-    const int db_columns = a.cols / BC * RP, num_db = 2 * RP + 2 * db_columns <= 512 ? 2 : 1;
+    // t's two parts side by side as one operand (N = 2 RP, their products in columns of their own) where TMEM has room
+    const int db_block = a.merged ? 2 * RP : RP, db_columns = a.cols / BC * db_block, num_db = 2 * RP + 2 * db_columns <= 512 ? 2 : 1;
     if (tid == 0) {
         for (int i = 0; i < S::STAGES; ++i) {
-            mbar_init(full(i), S::WRITERS);
+            mbar_init(full(i), HOW == COPY ? S::WRITERS * 32 : S::WRITERS);
             mbar_init(empty(i), 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -215,7 +235,7 @@ __global__ void __launch_bounds__(Shape<T, HOW, RP>::THREADS, 1)
                     return false;
                 if (lane == 0) {
                     mbar_arrive_expect_tx(tfull(tr.slot), S::TT);
-                    for (int i = 0; i < PARTS; ++i)
+                    for (int i = 0; i < (a.merged ? 1 : PARTS); ++i)   // merged: one box of both
                         tma_load_2d(ts + tr.slot * S::TT + i * STEP * S::SPAN, &map_t, tfull(tr.slot), i * a.RT + a.r0,
                                     p + ad * AG_PAD, pol_keep);
                 }
@@ -237,65 +257,83 @@ __global__ void __launch_bounds__(Shape<T, HOW, RP>::THREADS, 1)
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------------------ products
-        if (lane == 0) {
-            Ring st(S::STAGES), tr(S::TS), fr(num_factors), du(2), db(num_db);
-            segments([&](int, int b, int e) {
-                if (!mbar_wait(ffull(fr.slot), fr.parity, abort_flag, budget) ||
-                    !mbar_wait(dbempty(db.slot), db.parity ^ 1u, abort_flag, budget))
-                    return false;
-                const uint64_t fdesc = sdesc_mnmajor_span<S::SPAN>(factors + fr.slot * factor_bytes);
-                const uint32_t tdb = tmem + 2 * RP + db.slot * db_columns;
-                for (int p = b; p < e; p += STEP) {
-                    if (!mbar_wait(tfull(tr.slot), tr.parity, abort_flag, budget) ||
-                        !mbar_wait(duempty(du.slot), du.parity ^ 1u, abort_flag, budget))
-                        return false;
-                    tc_fence_after();
-                    const int steps = (min(STEP, e - p) + 15) / 16;   // of 16 rows
-                    const uint32_t td = tmem + du.slot * RP;
-                    const uint64_t tdesc = sdesc_mnmajor_span<S::SPAN>(ts + tr.slot * S::TT);
-                    for (int c = 0; c < blocks; ++c) {
-                        if (!mbar_wait(full(st.slot), st.parity, abort_flag, budget))
-                            return false;
-                        tc_fence_after();
-                        const uint32_t tile = tiles + st.slot * S::TILE, tb = tdb + c * RP;
-                        const uint64_t fd = fdesc + static_cast<uint32_t>(c * (BC * S::SPAN / 16));
+        // the whole warp, one lane issues
+        const uint32_t lead = elect_one();
+        Ring st(S::STAGES), tr(S::TS), fr(num_factors), du(2), db(num_db);
+        constexpr uint32_t KHI = static_cast<uint32_t>(desc_kmajor_hi()), MHI = static_cast<uint32_t>(desc_mnmajor_hi());
+        // du += tile x factor, 16 columns at a time, and dB += tile^T x t, 16 rows at a time,
+        // in turn (neither waits for itself); lo lo is of the size of what the parts leave
+        auto tile_products = [&](auto merged, auto whole, uint32_t tile, uint32_t td, uint32_t tb, uint32_t fd, uint32_t tt,
+                                 int steps, uint32_t first_du, uint32_t first_db) {
+            constexpr bool MERGED = decltype(merged)::value, WHOLE = decltype(whole)::value;
+            constexpr int TSPAN = MERGED ? S::SPAN2 : S::SPAN;
+            const uint32_t a0 = tile >> 4, am = a0 | (static_cast<uint32_t>(SUB) >> 4) << 16;
 #pragma unroll
-                        for (int i = 0; i < S::PLANES; ++i) {
-                            // du += tile x factor, 16 columns at a time, and dB += tile^T x t, 16 rows at
-                            // a time, in turn (neither waits for itself); lo lo is of the size of what
-                            // the parts leave
-                            const uint64_t ud = sdesc_kmajor_sw128(tile + i * 2 * SUB);
-                            const uint64_t bd = sdesc_mnmajor_sw128(tile + i * 2 * SUB, SUB);
-                            const int parts = i == 0 ? PARTS : 1;
-#pragma unroll
-                            for (int k = 0; k < BC / 16; ++k) {
-                                umma_bf16(td, ud + static_cast<uint32_t>((k / 4) * (SUB / 16) + 2 * (k % 4)),
-                                          fd + static_cast<uint32_t>(k * S::SPAN), IDESC_DU, (c | i | k) != 0);
-                                if (k < STEP / 16 && k < steps) {
-#pragma unroll
-                                    for (int j = 0; j < parts; ++j)
-                                        umma_bf16(tb, bd + 128u * k, tdesc + static_cast<uint32_t>((j * STEP / 16 + k) * S::SPAN),
-                                                  IDESC_DB, p != b || (i | j | k) != 0);
-                                }
-                            }
-                        }
-                        umma_commit(empty(st.slot));
-                        st.next();
-                    }
-                    umma_commit(tempty(tr.slot));
-                    umma_commit(dufull(du.slot));
-                    tr.next();
-                    du.next();
+            for (int k = 0; k < 8; ++k) {
+                umma_bf16_lead(lead, td, (a0 | 1u << 16) + (k / 4) * (SUB / 16) + 2 * (k % 4), KHI,
+                               fd + k * S::SPAN, desc_span_hi(S::SPAN), IDESC_DU, k == 0 ? first_du : 1u);
+                const int kr = k % (STEP / 16), plane = k / (STEP / 16);
+                if (WHOLE || kr < steps) {
+                    const uint32_t more = k == 0 ? first_db : 1u;
+                    umma_bf16_lead(lead, tb, am + 128 * k, MHI, tt + kr * TSPAN, desc_span_hi(TSPAN), MERGED ? IDESC_DB2 : IDESC_DB,
+                                   more);
+                    if (!MERGED && plane == 0)
+                        umma_bf16_lead(lead, tb, am + 128 * k, MHI, tt + (STEP / 16 + kr) * TSPAN, desc_span_hi(TSPAN), IDESC_DB, 1u);
                 }
-                umma_commit(fempty(fr.slot));
-                umma_commit(dbfull(db.slot));
-                fr.next();
-                db.next();
-                return true;
-            });
-            umma_commit(drain);   // every product has finished before TMEM is released
+            }
+        };
+        constexpr std::integral_constant<bool, true> yes{};
+        constexpr std::integral_constant<bool, false> no{};
+        segments([&](int, int b, int e) {
+            if (!warp_wait(ffull(fr.slot), fr.parity, abort_flag, budget) ||
+                !warp_wait(dbempty(db.slot), db.parity ^ 1u, abort_flag, budget))
+                return false;
+            const uint32_t fd = ((factors + fr.slot * factor_bytes) >> 4) | 1u << 16;
+            const uint32_t tdb = tmem + 2 * RP + db.slot * db_columns;
+            for (int p = b; p < e; p += STEP) {
+                if (!warp_wait(tfull(tr.slot), tr.parity, abort_flag, budget) ||
+                    !warp_wait(duempty(du.slot), du.parity ^ 1u, abort_flag, budget))
+                    return false;
+                tc_fence_after();
+                const int steps = (min(STEP, e - p) + 15) / 16;   // of 16 rows
+                const uint32_t td = tmem + du.slot * RP, tt = ((ts + tr.slot * S::TT) >> 4) | 1u << 16;
+                for (int c = 0; c < blocks; ++c) {
+                    if (!warp_wait(full(st.slot), st.parity, abort_flag, budget))
+                        return false;
+                    // the writers' shared memory for the products: the fence stands here, since a
+                    // writer's would wait for its copies of later tiles too
+                    fence_proxy_async_smem();
+                    tc_fence_after();
+                    const uint32_t tile = tiles + st.slot * S::TILE, tb = tdb + c * db_block, f = fd + c * (BC * S::SPAN / 16);
+                    const uint32_t first_du = c != 0, first_db = p != b;
+                    if (a.merged) {
+                        if (steps == STEP / 16)
+                            tile_products(yes, yes, tile, td, tb, f, tt, steps, first_du, first_db);
+                        else
+                            tile_products(yes, no, tile, td, tb, f, tt, steps, first_du, first_db);
+                    } else {
+                        if (steps == STEP / 16)
+                            tile_products(no, yes, tile, td, tb, f, tt, steps, first_du, first_db);
+                        else
+                            tile_products(no, no, tile, td, tb, f, tt, steps, first_du, first_db);
+                    }
+                    umma_commit_lead(lead, empty(st.slot));
+                    st.next();
+                }
+                umma_commit_lead(lead, tempty(tr.slot));
+                umma_commit_lead(lead, dufull(du.slot));
+                tr.next();
+                du.next();
+            }
+            umma_commit_lead(lead, fempty(fr.slot));
+            umma_commit_lead(lead, dbfull(db.slot));
+            fr.next();
+            db.next();
+            return true;
+        });
+        umma_commit_lead(lead, drain);   // every product has finished before TMEM is released
+        if (lead)
             drain_wait(drain, 0);
-        }
         __syncwarp();
     } else if (warp < 6) {
         // ------------------------------------------------------------ results
@@ -325,9 +363,10 @@ __global__ void __launch_bounds__(Shape<T, HOW, RP>::THREADS, 1)
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive(duempty(du.slot));
-                if (m < STEP && p + m < e) {
+                const int at = p + m % STEP;
+                if (at < e) {
                     float4 *o = reinterpret_cast<float4 *>(
-                        a.partial + (static_cast<size_t>(blockIdx.x) * (a.p1 - a.p0 + 16) + (p + m - a.p0)) * RP);
+                        a.partial + (static_cast<size_t>(blockIdx.x * S::PLANES + m / STEP) * (a.p1 - a.p0 + 16) + (at - a.p0)) * RP);
 #pragma unroll
                     for (int r = 0; r < RP / 4; ++r)
                         o[r] = make_float4(v[4 * r], v[4 * r + 1], v[4 * r + 2], v[4 * r + 3]);
@@ -346,7 +385,14 @@ __global__ void __launch_bounds__(Shape<T, HOW, RP>::THREADS, 1)
                 float v[RP];
                 if (some) {
                     __syncwarp();
-                    tmem_row<RP>(mine + 2 * RP + db.slot * db_columns + c * RP, v);
+                    tmem_row<RP>(mine + 2 * RP + db.slot * db_columns + c * db_block, v);
+                    if (a.merged) {
+                        float low[RP];
+                        tmem_row<RP>(mine + 2 * RP + db.slot * db_columns + c * db_block + RP, low);
+#pragma unroll
+                        for (int r = 0; r < RP; ++r)
+                            v[r] += low[r];
+                    }
                 } else {
 #pragma unroll
                     for (int r = 0; r < RP; ++r)
@@ -383,27 +429,19 @@ __global__ void __launch_bounds__(Shape<T, HOW, RP>::THREADS, 1)
         // ------------------------------------------------------------ tiles
         // a thread has columns 8 (t % 16) .. of every EACH-th row of a tile; 128-byte swizzle:
         // the 16-byte pieces of row m are exchanged by m % 8
-        constexpr int EACH = S::WRITERS * 2, ROWS = STEP / EACH;
+        constexpr int EACH = S::WRITERS * 2, ROWS = STEP / EACH;   // 16, or 32 rows apart
         const int t = tid - 6 * 32, chunk = t & 15, r0 = t >> 4;
         auto place = [&](int m) {
             return static_cast<uint32_t>((chunk >> 3) * SUB + m * 128 + (((chunk & 7) ^ (m & 7)) << 4));
         };
-        int row[ROWS];   // of the step; negative: past its last
+        const T *row[ROWS];   // of the step, from the slab on; null: past the step's last
         auto look_up = [&](int p, int rows) {
 #pragma unroll
             for (int i = 0; i < ROWS; ++i)
-                row[i] = r0 + EACH * i < rows ? a.plan.perm[p + r0 + EACH * i] : -1;
-        };
-        auto arrive = [&](int slot) {   // the warp's part of a tile is there
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(full(slot));
+                row[i] = r0 + EACH * i < rows ? dy + static_cast<size_t>(a.plan.perm[p + r0 + EACH * i]) * a.ld + c0 + chunk * 8 : nullptr;
         };
         if constexpr (HOW == COPY) {
-            constexpr int LAG = 2;   // tiles on their way behind the one being asked for
-            Ring st(S::STAGES), landed(S::STAGES);
-            int asked = 0;
+            Ring st(S::STAGES);
             segments([&](int, int b, int e) {
                 for (int p = b; p < e; p += STEP) {
                     const int rows = min(STEP, e - p), padded = (rows + 15) / 16 * 16;
@@ -417,29 +455,20 @@ __global__ void __launch_bounds__(Shape<T, HOW, RP>::THREADS, 1)
 #pragma unroll
                         for (int i = 0; i < ROWS; ++i)   // zeros past the row's end and past the step's last row
                             if (r0 + EACH * i < padded)
-                                cp_async16(dst + place(r0 + EACH * i),
-                                           row[i] >= 0 && bytes ? dy + static_cast<size_t>(row[i]) * a.ld + col : dy,
-                                           row[i] >= 0 ? bytes : 0u);
-                        asm volatile("cp.async.commit_group;" ::: "memory");
+                                cp_async16(dst + place(r0 + EACH * i), row[i] && bytes ? row[i] + c * BC : dy, row[i] ? bytes : 0u);
+                        cp_async_arrive(full(st.slot));
                         st.next();
-                        if (++asked > LAG) {
-                            asm volatile("cp.async.wait_group %0;" ::"n"(LAG) : "memory");
-                            arrive(landed.slot);
-                            landed.next();
-                        }
                     }
                 }
                 return true;
             });
-            asm volatile("cp.async.wait_all;" ::: "memory");
-            for (int i = min(asked, LAG); i > 0; --i) {
-                arrive(landed.slot);
-                landed.next();
-            }
+            asm volatile("cp.async.wait_all;" ::: "memory");   // no copy is in flight when the CTA leaves
         } else {
             // A thread's pieces go to its own places of the staging ring, so that it waits for
-            // nobody to rewrite them; batches of two rows, up to BATCHES of them on their way.
-            struct Cursor {   // batch `half` (rows 32 half ..) of tile (p, c) of an adapter
+            // nobody to rewrite them; a batch is 32 rows, a row a thread, and up to BATCHES of
+            // them are on their way.
+            static_assert(EACH == 32, "a row a thread and batch");
+            struct Cursor {   // batch `half` (rows 32 half ..) of the tile (p, c) of an adapter
                 int ad = -1, p = 0, e = 0, c = 0, half = 0;
                 __device__ __forceinline__ bool seek(const AdapterGradArgs &a)
                 {
@@ -469,46 +498,44 @@ __global__ void __launch_bounds__(Shape<T, HOW, RP>::THREADS, 1)
                 }
             };
             constexpr int ES = static_cast<int>(sizeof(T)), P = S::PIECES;
-            auto piece = [&](int batch, int i, int k) {
-                return staging + static_cast<uint32_t>(((batch * 2 + i) * P + k) * 4096 + t * 16);
-            };
+            auto piece = [&](int batch, int k) { return staging + static_cast<uint32_t>((batch * P + k) * 8192 + t * 16); };
             Cursor head;
             bool more = head.seek(a);
             Cursor tail = head;
             bool left = more;
             Ring st(S::STAGES), in(S::BATCHES), out(S::BATCHES);
-            uint32_t shifts = 0;   // a byte a batch, the latest lowest: the two rows' bytes past a 16-byte boundary
+            uint32_t shifts = 0;   // a nibble a batch, the latest lowest: the row's bytes past a 16-byte boundary
             auto ask = [&] {       // for the pieces of the head's batch
-                uint32_t two = 0;
+                uint32_t shift = 0;
                 if (more) {
                     if (head.c == 0 && head.half == 0)
                         look_up(head.p, head.rows());
                     const int col = c0 + head.c * BC + chunk * 8;
+                    const T *from = row[0];
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int n = head.half ? row[2 + i] : row[i];
-                        if (n < 0 || col >= a.V)
-                            continue;
-                        const T *from = dy + static_cast<size_t>(n) * a.ld + col;
-                        const uint32_t shift = HOW == ANY ? row_shift(from) : 0u;
-                        two |= shift << (4 * i);
+                    for (int k = 1; k < ROWS; ++k)
+                        from = head.half == k ? row[k] : from;
+                    if (from && col < a.V) {
+                        from += head.c * BC;
+                        if (HOW == ANY)
+                            shift = row_shift(from);
                         const char *src = reinterpret_cast<const char *>(from) - shift;
                         if (shift == 0 ? col + 8 <= a.V : col >= 8 && col + 16 <= a.V) {
 #pragma unroll
                             for (int k = 0; k < P; ++k)
                                 if (HOW == LOAD || k < P - 1 || shift != 0)
-                                    cp_async16(piece(in.slot, i, k), src + 16 * k, 16u);
+                                    cp_async16(piece(in.slot, k), src + 16 * k, 16u);
                         } else {   // a row's first or last columns, one by one
                             for (int k = 0; k < 8 && col + k < a.V; ++k) {
                                 const uint32_t at = shift + k * ES;
-                                *reinterpret_cast<T *>(smem + (piece(in.slot, i, at / 16) - tiles) + at % 16) = from[k];
+                                *reinterpret_cast<T *>(smem + (piece(in.slot, at / 16) - tiles) + at % 16) = from[k];
                             }
                         }
                     }
                     more = head.next(a, blocks);
                 }
                 asm volatile("cp.async.commit_group;" ::: "memory");
-                shifts = shifts << 8 | two;
+                shifts = shifts << 4 | shift;
                 in.next();
             };
             for (int i = 0; i < S::BATCHES - 1; ++i)
@@ -519,18 +546,15 @@ __global__ void __launch_bounds__(Shape<T, HOW, RP>::THREADS, 1)
                 const int rows = tail.rows(), padded = (rows + 15) / 16 * 16, col = c0 + tail.c * BC + chunk * 8;
                 if (tail.half == 0 && !warp_wait(empty(st.slot), st.parity ^ 1u, abort_flag, budget))
                     break;
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int m = tail.half * 32 + i * 16 + r0;
-                    if (m >= padded)
-                        continue;
+                const int m = tail.half * 32 + r0;
+                if (m < padded) {
                     uint32_t o[S::PLANES][4] = {};
                     if (m < rows && col < a.V) {
                         constexpr int W = Elem<T>::WORDS;
                         uint32_t x[W + 4] = {};
 #pragma unroll
                         for (int k = 0; k < P; ++k) {
-                            const uint4 v = *reinterpret_cast<const uint4 *>(smem + (piece(out.slot, i, k) - tiles));
+                            const uint4 v = *reinterpret_cast<const uint4 *>(smem + (piece(out.slot, k) - tiles));
                             x[4 * k] = v.x;
                             x[4 * k + 1] = v.y;
                             x[4 * k + 2] = v.z;
@@ -538,7 +562,7 @@ __global__ void __launch_bounds__(Shape<T, HOW, RP>::THREADS, 1)
                         }
                         Raw8<T> w;
                         if (HOW == ANY) {
-                            shift_words<W, ES == 2>(w.w, x, shifts >> (8 * (S::BATCHES - 1) + 4 * i) & 15u);
+                            shift_words<W, ES == 2>(w.w, x, shifts >> (4 * (S::BATCHES - 1)) & 15u);
                         } else {
 #pragma unroll
                             for (int k = 0; k < W; ++k)
@@ -557,11 +581,13 @@ __global__ void __launch_bounds__(Shape<T, HOW, RP>::THREADS, 1)
                     }
 #pragma unroll
                     for (int j = 0; j < S::PLANES; ++j)
-                        *reinterpret_cast<uint4 *>(smem + st.slot * S::TILE + j * 2 * SUB + place(m)) =
+                        *reinterpret_cast<uint4 *>(smem + st.slot * S::TILE + place(j * STEP + m)) =
                             make_uint4(o[j][0], o[j][1], o[j][2], o[j][3]);
                 }
                 if (tail.last()) {
-                    arrive(st.slot);
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(full(st.slot));
                     st.next();
                 }
                 out.next();
@@ -606,7 +632,7 @@ template <int RP> __global__ void __launch_bounds__(256) adapters_fold_kernel(co
     if (on) {
         const float4 *p = reinterpret_cast<const float4 *>(a.partial) + i;
 #pragma unroll 4
-        for (int slab = k; slab < a.slabs; slab += SHARE) {
+        for (int slab = k; slab < a.du_parts; slab += SHARE) {
             const float4 x = p[slab * (count * (RP / 4))];
             s.x += x.x;
             s.y += x.y;

@@ -228,7 +228,9 @@ int tim_adapter_logits_backward(const void *dlogits, int dtype, int64_t N, int64
     const int64_t per_slab = (blocks + waves * sms - 1) / (waves * sms);
     a.cols = static_cast<int32_t>(per_slab * tim::AG_BLOCK);
     a.slabs = static_cast<int32_t>((blocks + per_slab - 1) / per_slab);
-    const int64_t per_row = int64_t(4) * a.slabs * RP;
+    a.merged = RP <= 32 && 2 * RP + per_slab * 2 * RP <= 512;
+    a.du_parts = a.slabs * tim::ag_planes(dtype);
+    const int64_t per_row = int64_t(4) * a.du_parts * RP;
     a.row_part = static_cast<int32_t>(std::min<int64_t>(
         N, std::max<int64_t>(tim::AG_PARTIAL_BYTES / per_row / 128, 1) * 128));
     a.dh = dh;
@@ -263,9 +265,9 @@ int tim_adapter_logits_backward(const void *dlogits, int dtype, int64_t N, int64
     const uint64_t s_b[2] = {static_cast<uint64_t>(R) * 2, static_cast<uint64_t>(V * R) * 2};
     const uint64_t d_t[2] = {static_cast<uint64_t>(2 * a.RT), t_rows}, s_t[1] = {static_cast<uint64_t>(2 * a.RT) * 2};
     const uint32_t box_b[3] = {static_cast<uint32_t>(RP), tim::AG_BLOCK, 1}, box_t[2] = {
-        static_cast<uint32_t>(RP), static_cast<uint32_t>(tim::ag_step(dtype != TIM_BF16 || !a.aligned))};
+        static_cast<uint32_t>(a.merged ? 2 * RP : RP), static_cast<uint32_t>(128 / tim::ag_planes(dtype))};
     if ((rc = tim::encode_bf16_map(&maps[0], a.B, 3, d_b, s_b, box_b, 2 * RP)) != TIM_OK ||
-        (rc = tim::encode_bf16_map(&maps[1], f.plan.t, 2, d_t, s_t, box_t, 2 * RP)) != TIM_OK) {
+        (rc = tim::encode_bf16_map(&maps[1], f.plan.t, 2, d_t, s_t, box_t, a.merged ? 4 * RP : 2 * RP)) != TIM_OK) {
         tim::workspace_free(ws, s);
         return rc;
     }

@@ -8,6 +8,8 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include "../../include/tim.h"
+
 namespace tim {
 
 // Device memory from the library's stream-ordered pool; a tim_status code.
@@ -68,10 +70,10 @@ cudaError_t adapters_shrink_launch(const AdapterArgs &a, int parts, int num_sms,
 cudaError_t adapters_expand_launch(AdapterArgs a, int dtype, int num_sms, cudaStream_t s);
 cudaError_t adapters_prepare_device();   // shared-memory sizes
 
-// The gradient: slabs of the vocabulary, tiles of 128 columns and 128 rows (64 where the
-// rows are rewritten: half of the shared memory then holds what is on its way).
+// The gradient: slabs of the vocabulary, tiles of 128 columns and 128 rows of bf16, or of
+// 64 rows in two planes of bf16 parts.
 constexpr int AG_BLOCK = 128;
-constexpr int ag_step(bool rewritten) { return rewritten ? 64 : 128; }
+constexpr int ag_planes(int dtype) { return dtype == TIM_BF16 ? 1 : 2; }
 constexpr int AG_PAD = 16;           // t has room for so many rows of zeros behind each adapter's
 constexpr int AG_SMEM = 227 * 1024;
 constexpr int64_t AG_PARTIAL_BYTES = int64_t(1) << 30;   // du's partial sums at most, per part of the batch
@@ -89,10 +91,12 @@ struct AdapterGradArgs {
     int32_t RT;               // the rank padded (16, 32, 64, 128)
     int32_t aligned;          // every row of dy starts on 16 bytes
     int32_t cols, slabs;      // columns of a slab, slabs
+    int32_t merged;           // t's two parts are one operand
+    int32_t du_parts;         // parts of a sum of du: slabs times planes
     int32_t row_part;         // positions of a launch
     int32_t p0, p1, r0;       // the launch's positions and first rank
     int32_t row_chunk;        // dh: positions of a CTA
-    float *partial;           // [slabs][p1 - p0][min(RT, 64)]
+    float *partial;           // [du_parts][p1 - p0 + 16][min(RT, 64)]
     uint16_t *du;             // [N][3][RT] bf16 parts of scale B^T dy
     float *dh, *dA, *dB;
     int32_t accumulate, accumulate_dh;

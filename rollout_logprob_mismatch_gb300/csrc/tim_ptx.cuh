@@ -391,6 +391,45 @@ __device__ __forceinline__ void umma_bf16(uint32_t d_tmem, uint64_t a_desc, uint
         : "memory");
 }
 
+// The same for a warp that runs in step, issued by the thread whose `lead` is not 0: with
+// the operands' arithmetic outside any branch on the lane it stays in uniform registers,
+// where the instruction takes its operands from.  Descriptors in two words.
+__device__ __forceinline__ void umma_bf16_lead(uint32_t lead, uint32_t d_tmem, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo,
+                                               uint32_t b_hi, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\t"
+        "setp.ne.b32 q, %0, 0;\n\t"
+        "setp.ne.b32 p, %7, 0;\n\t"
+        "mov.b64 a, {%2, %3};\n\t"
+        "mov.b64 b, {%4, %5};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%1], a, b, %6, p;\n\t}" ::"r"(lead),
+        "r"(d_tmem), "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ void umma_commit_lead(uint32_t lead, uint32_t bar)
+{
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %0, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%1];\n\t}" ::"r"(lead),
+        "r"(bar)
+        : "memory");
+}
+
+// 1 in one lane of the warp, 0 in the others.
+__device__ __forceinline__ uint32_t elect_one()
+{
+    uint32_t x;
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "elect.sync _|q, 0xffffffff;\n\t"
+        "selp.b32 %0, 1, 0, q;\n\t}"
+        : "=r"(x));
+    return x;
+}
+
 // Arrives once on `bar` when every tcgen05.mma issued so far by this thread has completed.
 __device__ __forceinline__ void umma_commit(uint32_t bar)
 {
@@ -472,21 +511,6 @@ __device__ __forceinline__ uint64_t sdesc_mnmajor_sw128(uint32_t saddr, uint32_t
     d |= static_cast<uint64_t>(1024u >> 4) << 32;
     d |= static_cast<uint64_t>(1u) << 46;
     d |= static_cast<uint64_t>(2u) << 61;
-    return d;
-}
-
-// The same for an operand whose M (or N) extent is one swizzle span of SPAN = 32, 64 or
-// 128 bytes: each k index is a row of SPAN bytes, 8-row core groups 8 SPAN bytes apart,
-// swizzle mode 6, 4 or 2.
-template <int SPAN> __device__ __forceinline__ uint64_t sdesc_mnmajor_span(uint32_t saddr)
-{
-    static_assert(SPAN == 32 || SPAN == 64 || SPAN == 128, "a swizzle span");
-    uint64_t d = 0;
-    d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
-    d |= static_cast<uint64_t>(1u) << 16;
-    d |= static_cast<uint64_t>((8u * SPAN) >> 4) << 32;
-    d |= static_cast<uint64_t>(1u) << 46;
-    d |= static_cast<uint64_t>(SPAN == 128 ? 2u : SPAN == 64 ? 4u : 6u) << 61;
     return d;
 }
 
