@@ -91,41 +91,35 @@ __device__ __forceinline__ void write_order(const AdapterArgs &a, int ad, const 
         });
 }
 
-// t of up to 16 MT rows under adapter ad, written for rows lo .. hi - 1 of them at
-// positions pos + lo ..  The eight warps share k (every eighth 32 of it each) and add up
-// through shared memory in their order, so that a row's sum depends on D alone.
-template <int RP, int PARTS, int MT>
+// t of up to 16 rows under adapter ad, written for rows lo .. hi - 1 of them at positions
+// pos + lo ..  The 16 warps share k (every 16th 32 of it each) and add up through shared
+// memory in their order, so that a row's sum depends on D alone.
+template <int RP, int PARTS>
 __device__ __forceinline__ void project(const AdapterArgs &a, int ad, const int32_t *rows, int lo, int hi, int pos)
 {
     constexpr int WARPS = AD_SHRINK_THREADS / 32;
     constexpr int NC = RP < 32 ? RP : 32;      // rank columns at a time
-    constexpr int AHEAD = MT == 1 ? 4 : 2;     // steps of 32 k whose loads are in flight together
-    __shared__ float sums[WARPS][16 * MT][NC + 1];
+    constexpr int AHEAD = 4;                   // steps of 32 k whose loads are in flight together
+    __shared__ float sums[WARPS][16][NC + 1];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
     const float scale = a.scale ? a.scale[ad] : 1.f;
     const uint16_t *A = a.A + static_cast<size_t>(ad) * a.R * a.D;
     const int kchunks = (a.D + 31) / 32;
     const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-    const uint16_t *h[2 * MT];
-    bool on[2 * MT];
-#pragma unroll
-    for (int m = 0; m < 2 * MT; ++m) {
-        const int i = m * 8 + g;
-        on[m] = i >= lo && i < hi;
-        h[m] = a.h + static_cast<size_t>(on[m] ? rows[i] : 0) * a.D;
-    }
+    const bool on0 = g >= lo && g < hi, on1 = g + 8 >= lo && g + 8 < hi;
+    const uint16_t *h0 = a.h + static_cast<size_t>(on0 ? rows[g] : 0) * a.D;
+    const uint16_t *h1 = a.h + static_cast<size_t>(on1 ? rows[g + 8] : 0) * a.D;
     for (int n0 = 0; n0 < RP; n0 += NC) {
-        float acc[MT][NC / 8][4] = {};
+        float acc[NC / 8][4] = {};
         if (n0 < a.R) {
             for (int kc0 = warp; kc0 < kchunks; kc0 += WARPS * AHEAD) {
-                uint4 x[AHEAD][2 * MT], w[AHEAD][NC / 8];
+                uint4 x0[AHEAD], x1[AHEAD], w[AHEAD][NC / 8];
 #pragma unroll
                 for (int i = 0; i < AHEAD; ++i) {
                     const int k = (kc0 + i * WARPS) * 32 + q * 8;   // D is a multiple of 8: the eight are in or out together
                     const bool in = k < a.D;
-#pragma unroll
-                    for (int m = 0; m < 2 * MT; ++m)
-                        x[i][m] = in && on[m] ? __ldg(reinterpret_cast<const uint4 *>(h[m] + k)) : zero;
+                    x0[i] = in && on0 ? __ldg(reinterpret_cast<const uint4 *>(h0 + k)) : zero;
+                    x1[i] = in && on1 ? __ldg(reinterpret_cast<const uint4 *>(h1 + k)) : zero;
 #pragma unroll
                     for (int j = 0; j < NC / 8; ++j) {
                         const int r = n0 + j * 8 + g;
@@ -135,25 +129,20 @@ __device__ __forceinline__ void project(const AdapterArgs &a, int ad, const int3
 #pragma unroll
                 for (int i = 0; i < AHEAD; ++i)
 #pragma unroll
-                    for (int m = 0; m < MT; ++m)
-#pragma unroll
-                        for (int j = 0; j < NC / 8; ++j) {
-                            const uint4 x0 = x[i][2 * m], x1 = x[i][2 * m + 1];
-                            mma16816(acc[m][j], {x0.x, x1.x, x0.y, x1.y}, w[i][j].x, w[i][j].y);
-                            mma16816(acc[m][j], {x0.z, x1.z, x0.w, x1.w}, w[i][j].z, w[i][j].w);
-                        }
+                    for (int j = 0; j < NC / 8; ++j) {
+                        mma16816(acc[j], {x0[i].x, x1[i].x, x0[i].y, x1[i].y}, w[i][j].x, w[i][j].y);
+                        mma16816(acc[j], {x0[i].z, x1[i].z, x0[i].w, x1[i].w}, w[i][j].z, w[i][j].w);
+                    }
             }
         }
         __syncthreads();   // the sums before have been read
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int j = 0; j < NC / 8; ++j) {
-                sums[warp][m * 16 + g][j * 8 + 2 * q] = acc[m][j][0];
-                sums[warp][m * 16 + g][j * 8 + 2 * q + 1] = acc[m][j][1];
-                sums[warp][m * 16 + g + 8][j * 8 + 2 * q] = acc[m][j][2];
-                sums[warp][m * 16 + g + 8][j * 8 + 2 * q + 1] = acc[m][j][3];
-            }
+        for (int j = 0; j < NC / 8; ++j) {
+            sums[warp][g][j * 8 + 2 * q] = acc[j][0];
+            sums[warp][g][j * 8 + 2 * q + 1] = acc[j][1];
+            sums[warp][g + 8][j * 8 + 2 * q] = acc[j][2];
+            sums[warp][g + 8][j * 8 + 2 * q + 1] = acc[j][3];
+        }
         __syncthreads();
         for (int i = tid; i < (hi - lo) * NC; i += AD_SHRINK_THREADS) {
             const int m = lo + i / NC, r = i % NC;
@@ -185,7 +174,7 @@ __device__ __forceinline__ void pad_rows(const AdapterArgs &a, int ad, int count
 // Few rows, one launch.  CTA (a, y): the rows of adapter a, 16 at a time from the y-th 16
 // on; a = n: the rows under no adapter (only ordered).
 template <int RP, int PARTS>
-__global__ void __launch_bounds__(AD_SHRINK_THREADS, 2) adapters_shrink_kernel(const AdapterArgs a)
+__global__ void __launch_bounds__(AD_SHRINK_THREADS) adapters_shrink_kernel(const AdapterArgs a)
 {
     __shared__ int32_t mine[16];
     const int ad = blockIdx.x;
@@ -204,14 +193,14 @@ __global__ void __launch_bounds__(AD_SHRINK_THREADS, 2) adapters_shrink_kernel(c
                     mine[p - c0] = r;
             });
         __syncthreads();
-        project<RP, PARTS, 1>(a, ad, mine, 0, rows, o.base + c0);
+        project<RP, PARTS>(a, ad, mine, 0, rows, o.base + c0);
         if (c0 + rows == o.count)
             pad_rows(a, ad, o.count, o.base + o.count);
         __syncthreads();
     }
 }
 
-// Many rows: the order in a launch of its own, then a CTA for every 32 positions.
+// Many rows: the order in a launch of its own, then a CTA for every 16 positions.
 __global__ void __launch_bounds__(AD_SHRINK_THREADS) adapters_order_kernel(const AdapterArgs a)
 {
     pdl_wait();
@@ -221,12 +210,12 @@ __global__ void __launch_bounds__(AD_SHRINK_THREADS) adapters_order_kernel(const
 }
 
 template <int RP, int PARTS>
-__global__ void __launch_bounds__(AD_SHRINK_THREADS, 2) adapters_project_kernel(const AdapterArgs a)
+__global__ void __launch_bounds__(AD_SHRINK_THREADS) adapters_project_kernel(const AdapterArgs a)
 {
-    __shared__ int32_t s_row[32], s_ad[33];
+    __shared__ int32_t s_row[16], s_ad[17];
     pdl_wait();
     pdl_launch_dependents();
-    const int p0 = blockIdx.x * 32, rows = min(32, a.plan.offsets[a.n] - p0);
+    const int p0 = blockIdx.x * 16, rows = min(16, a.plan.offsets[a.n] - p0);
     if (rows <= 0)
         return;
     if (threadIdx.x < rows) {
@@ -240,7 +229,7 @@ __global__ void __launch_bounds__(AD_SHRINK_THREADS, 2) adapters_project_kernel(
         int m = s + 1;
         while (s_ad[m] == s_ad[s])
             ++m;
-        project<RP, PARTS, 2>(a, s_ad[s], s_row, s, m, p0);
+        project<RP, PARTS>(a, s_ad[s], s_row, s, m, p0);
         const int ad = s_ad[s], e = a.plan.offsets[ad + 1];
         if (p0 + m == e)
             pad_rows(a, ad, e - a.plan.offsets[ad], e);
@@ -607,7 +596,7 @@ template <int RP, int PARTS> cudaError_t shrink(const AdapterArgs &a, int num_sm
         const cudaError_t e = launch(adapters_order_kernel, dim3(static_cast<unsigned>(a.n + 1)), AD_SHRINK_THREADS, 0, a, s);
         if (e != cudaSuccess)
             return e;
-        return launch(adapters_project_kernel<RP, PARTS>, dim3(static_cast<unsigned>((a.N + 31) / 32)), AD_SHRINK_THREADS, 0,
+        return launch(adapters_project_kernel<RP, PARTS>, dim3(static_cast<unsigned>((a.N + 15) / 16)), AD_SHRINK_THREADS, 0,
                       a, s);
     }
     const int ys = std::max(1, std::min((a.N + 15) / 16, (2 * num_sms + a.n) / (a.n + 1)));

@@ -47,19 +47,19 @@ template <typename T, int HOW, int RP> struct Shape {
     static constexpr int TILE = 2 * SUB;
     static constexpr int FACTORS = (RP == 16 && HOW == COPY ? 2 : 1) * BLOCKS * BC * SPAN;   // bytes for factors: two where they fit
     static constexpr int TT = PARTS * STEP * SPAN;
-    static constexpr int TS = RP == 64 && PLANES == 1 && HOW != COPY ? 1 : 2;
-    // not COPY: bytes on their way to the threads that rewrite them, in batches of 32 x 128;
-    // PIECES 16-byte pieces hold a thread's eight columns
-    static constexpr int PIECES = static_cast<int>(sizeof(T)) / 2 + (HOW == ANY ? 1 : 0);
-    static constexpr int BATCH = 512 * 16 * PIECES, BATCHES = 65536 / BATCH < 4 ? 65536 / BATCH : 4;
+    static constexpr int TS = RP == 64 && HOW != COPY ? 1 : 2;
+    static constexpr int REST = AG_SMEM - 2048 - FACTORS - TS * TT;
+    // not COPY: rows on their way to the warps that rewrite them, 32 NR in a batch
+    static constexpr int SROW = BC * static_cast<int>(sizeof(T)) + (HOW == ANY ? 16 : 0);
+    static constexpr int NR = 2, BATCH = NR * 32 * SROW;
+    static constexpr int FIT = (REST - 2 * TILE) / BATCH, BATCHES = FIT < 4 ? FIT : 4;
     static constexpr int STAGING = HOW == COPY ? 0 : BATCHES * BATCH;
-    static constexpr int ROOM = AG_SMEM - 2048 - FACTORS - TS * TT - STAGING;
-    static constexpr int STAGES = ROOM / TILE < 4 ? ROOM / TILE : 4;
+    static constexpr int STAGES = (REST - STAGING) / TILE < 4 ? (REST - STAGING) / TILE : 4;
     static constexpr int BYTES = AG_SMEM;
     static constexpr int WRITERS = HOW == COPY ? 8 : 16;       // warps that bring tiles
     static constexpr int THREADS = (6 + WRITERS) * 32;
     static constexpr uint32_t TMEM = 512;                      // du twice, dB's blocks
-    static_assert(STAGES >= 2 && (2 + BLOCKS) * RP <= 512, "shared memory, TMEM");
+    static_assert(STAGES >= 2 && BATCHES >= 2 && (2 + BLOCKS) * RP <= 512, "shared memory, TMEM");
 };
 
 // An adapter's positions [begin, end) of a part [p0, p1) of the batch: parts meet at a
@@ -120,15 +120,13 @@ __host__ __device__ constexpr uint32_t desc_span_hi(int span)
     return static_cast<uint32_t>(8 * span) / 16 | 1u << 14 | (span == 128 ? 2u : span == 64 ? 4u : 6u) << 29;
 }
 
-template <int RP> __device__ __forceinline__ void tmem_row(uint32_t taddr, float (&v)[RP])
+template <int RC> __device__ __forceinline__ void tmem_row(uint32_t taddr, float (&v)[RC])
 {
-    if constexpr (RP == 16) {
+    static_assert(RC == 16 || RC == 32, "columns of one load");
+    if constexpr (RC == 16)
         tmem_load16(taddr, v);
-    } else {
-#pragma unroll
-        for (int i = 0; i < RP; i += 32)
-            tmem_load32(taddr + i, *reinterpret_cast<float (*)[32]>(&v[i]));
-    }
+    else
+        tmem_load32(taddr, v);
 }
 
 template <typename T, int HOW, int RP>
@@ -337,6 +335,7 @@ __global__ void __launch_bounds__(Shape<T, HOW, RP>::THREADS, 1)
         __syncwarp();
     } else if (warp < 6) {
         // ------------------------------------------------------------ results
+        constexpr int RC = RP < 32 ? RP : 32;   // ranks at a time
         const int m = (warp & 3) * 32 + lane;   // row of du, column of dB's block
         const uint32_t mine = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
         Ring du(2), db(num_db);
@@ -356,21 +355,26 @@ __global__ void __launch_bounds__(Shape<T, HOW, RP>::THREADS, 1)
                 if (!ok)
                     break;
                 tc_fence_after();
-                float v[RP];
-                __syncwarp();
-                tmem_row<RP>(mine + du.slot * RP, v);
+                const int at = p + m % STEP;
+                // [part][four ranks][position]: a warp's rows lie together
+                const size_t count = a.p1 - a.p0 + 16;
+                float4 *o = reinterpret_cast<float4 *>(a.partial) +
+                            static_cast<size_t>(blockIdx.x * S::PLANES + m / STEP) * (RP / 4) * count + (at - a.p0);
+#pragma unroll
+                for (int r0 = 0; r0 < RP; r0 += RC) {
+                    float v[RC];
+                    __syncwarp();
+                    tmem_row<RC>(mine + du.slot * RP + r0, v);
+                    if (at < e) {
+#pragma unroll
+                        for (int r = 0; r < RC / 4; ++r)
+                            o[(r0 / 4 + r) * count] = make_float4(v[4 * r], v[4 * r + 1], v[4 * r + 2], v[4 * r + 3]);
+                    }
+                }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive(duempty(du.slot));
-                const int at = p + m % STEP;
-                if (at < e) {
-                    float4 *o = reinterpret_cast<float4 *>(
-                        a.partial + (static_cast<size_t>(blockIdx.x * S::PLANES + m / STEP) * (a.p1 - a.p0 + 16) + (at - a.p0)) * RP);
-#pragma unroll
-                    for (int r = 0; r < RP / 4; ++r)
-                        o[r] = make_float4(v[4 * r], v[4 * r + 1], v[4 * r + 2], v[4 * r + 3]);
-                }
                 du.next();
             }
             if (!ok)
@@ -382,39 +386,41 @@ __global__ void __launch_bounds__(Shape<T, HOW, RP>::THREADS, 1)
                 tc_fence_after();
             }
             for (int c = 0; c < blocks; ++c) {
-                float v[RP];
-                if (some) {
-                    __syncwarp();
-                    tmem_row<RP>(mine + 2 * RP + db.slot * db_columns + c * db_block, v);
-                    if (a.merged) {
-                        float low[RP];
-                        tmem_row<RP>(mine + 2 * RP + db.slot * db_columns + c * db_block + RP, low);
-#pragma unroll
-                        for (int r = 0; r < RP; ++r)
-                            v[r] += low[r];
-                    }
-                } else {
-#pragma unroll
-                    for (int r = 0; r < RP; ++r)
-                        v[r] = 0.f;
-                }
                 const int col = c0 + c * BC + m;
-                if (col >= a.V)
-                    continue;
+                const uint32_t tb = mine + 2 * RP + db.slot * db_columns + c * db_block;
                 float4 *o = reinterpret_cast<float4 *>(a.dB + (static_cast<size_t>(ad) * a.V + col) * a.R + a.r0);
 #pragma unroll
-                for (int r = 0; r < RP / 4; ++r) {
-                    if (a.r0 + 4 * r >= a.R)
+                for (int r0 = 0; r0 < RP; r0 += RC) {
+                    if (a.r0 + r0 >= a.R)
                         break;
-                    float4 x = make_float4(v[4 * r], v[4 * r + 1], v[4 * r + 2], v[4 * r + 3]);
-                    if (add) {
-                        const float4 y = o[r];
-                        x.x += y.x;
-                        x.y += y.y;
-                        x.z += y.z;
-                        x.w += y.w;
+                    float v[RC] = {};
+                    if (some) {
+                        __syncwarp();
+                        tmem_row<RC>(tb + r0, v);
+                        if (RP <= 32 && a.merged) {
+                            float low[RC];
+                            tmem_row<RC>(tb + RP, low);
+#pragma unroll
+                            for (int r = 0; r < RC; ++r)
+                                v[r] += low[r];
+                        }
                     }
-                    o[r] = x;
+                    if (col >= a.V)
+                        continue;
+#pragma unroll
+                    for (int r = 0; r < RC / 4; ++r) {
+                        if (a.r0 + r0 + 4 * r >= a.R)
+                            break;
+                        float4 x = make_float4(v[4 * r], v[4 * r + 1], v[4 * r + 2], v[4 * r + 3]);
+                        if (add) {
+                            const float4 y = o[r0 / 4 + r];
+                            x.x += y.x;
+                            x.y += y.y;
+                            x.z += y.z;
+                            x.w += y.w;
+                        }
+                        o[r0 / 4 + r] = x;
+                    }
                 }
             }
             if (some) {
@@ -434,11 +440,12 @@ __global__ void __launch_bounds__(Shape<T, HOW, RP>::THREADS, 1)
         auto place = [&](int m) {
             return static_cast<uint32_t>((chunk >> 3) * SUB + m * 128 + (((chunk & 7) ^ (m & 7)) << 4));
         };
-        const T *row[ROWS];   // of the step, from the slab on; null: past the step's last
+        const T *row[ROWS];   // of the step, from the slab's (COPY: the thread's) first column on; null: past its last
+        const int mine = HOW == COPY ? chunk * 8 : 0;
         auto look_up = [&](int p, int rows) {
 #pragma unroll
             for (int i = 0; i < ROWS; ++i)
-                row[i] = r0 + EACH * i < rows ? dy + static_cast<size_t>(a.plan.perm[p + r0 + EACH * i]) * a.ld + c0 + chunk * 8 : nullptr;
+                row[i] = r0 + EACH * i < rows ? dy + static_cast<size_t>(a.plan.perm[p + r0 + EACH * i]) * a.ld + c0 + mine : nullptr;
         };
         if constexpr (HOW == COPY) {
             Ring st(S::STAGES);
@@ -464,12 +471,13 @@ __global__ void __launch_bounds__(Shape<T, HOW, RP>::THREADS, 1)
             });
             asm volatile("cp.async.wait_all;" ::: "memory");   // no copy is in flight when the CTA leaves
         } else {
-            // A thread's pieces go to its own places of the staging ring, so that it waits for
-            // nobody to rewrite them; a batch is 32 rows, a row a thread, and up to BATCHES of
-            // them are on their way.
-            static_assert(EACH == 32, "a row a thread and batch");
-            struct Cursor {   // batch `half` (rows 32 half ..) of the tile (p, c) of an adapter
-                int ad = -1, p = 0, e = 0, c = 0, half = 0;
+            // Half a warp has a row of the staging ring, brings it in whole 16-byte pieces and
+            // rewrites it, so that no warp waits for another; a batch is 32 NR rows, and up to
+            // BATCHES are on their way.
+            constexpr int NR = S::NR;
+            static_assert(EACH == 32, "half a warp a row of 32");
+            struct Cursor {   // batch `part` (rows 32 NR part ..) of the tile (p, c) of an adapter
+                int ad = -1, p = 0, e = 0, c = 0, part = 0;
                 __device__ __forceinline__ bool seek(const AdapterGradArgs &a)
                 {
                     while (++ad < a.n) {
@@ -482,14 +490,14 @@ __global__ void __launch_bounds__(Shape<T, HOW, RP>::THREADS, 1)
                     return false;
                 }
                 __device__ __forceinline__ int rows() const { return min(STEP, e - p); }
-                __device__ __forceinline__ bool last() const { return half * 32 + 32 >= rows(); }
+                __device__ __forceinline__ bool last() const { return (part + 1) * 32 * S::NR >= rows(); }
                 __device__ __forceinline__ bool next(const AdapterGradArgs &a, int blocks)
                 {
                     if (!last()) {
-                        ++half;
+                        ++part;
                         return true;
                     }
-                    half = 0;
+                    part = 0;
                     if (++c < blocks)
                         return true;
                     c = 0;
@@ -497,45 +505,54 @@ __global__ void __launch_bounds__(Shape<T, HOW, RP>::THREADS, 1)
                     return p < e || seek(a);
                 }
             };
-            constexpr int ES = static_cast<int>(sizeof(T)), P = S::PIECES;
-            auto piece = [&](int batch, int k) { return staging + static_cast<uint32_t>((batch * P + k) * 8192 + t * 16); };
+            constexpr int ES = static_cast<int>(sizeof(T)), P = ES / 2;   // 16-byte pieces of a thread's eight columns
+            auto staged = [&](int batch, int i) { return staging + static_cast<uint32_t>(((batch * NR + i) * 32 + r0) * S::SROW); };
             Cursor head;
             bool more = head.seek(a);
             Cursor tail = head;
             bool left = more;
             Ring st(S::STAGES), in(S::BATCHES), out(S::BATCHES);
-            uint32_t shifts = 0;   // a nibble a batch, the latest lowest: the row's bytes past a 16-byte boundary
+            uint32_t shifts = 0;   // a nibble a row, the latest lowest: its bytes past a 16-byte boundary
             auto ask = [&] {       // for the pieces of the head's batch
-                uint32_t shift = 0;
+                uint32_t bits = 0;
                 if (more) {
-                    if (head.c == 0 && head.half == 0)
+                    if (head.c == 0 && head.part == 0)
                         look_up(head.p, head.rows());
-                    const int col = c0 + head.c * BC + chunk * 8;
-                    const T *from = row[0];
+                    const int col = c0 + head.c * BC;
 #pragma unroll
-                    for (int k = 1; k < ROWS; ++k)
-                        from = head.half == k ? row[k] : from;
-                    if (from && col < a.V) {
-                        from += head.c * BC;
-                        if (HOW == ANY)
-                            shift = row_shift(from);
+                    for (int i = 0; i < NR; ++i) {
+                        const T *from = row[i];
+#pragma unroll
+                        for (int k = 1; k < ROWS / NR; ++k)
+                            from = head.part == k ? row[k * NR + i] : from;
+                        if (!from || col >= a.V)
+                            continue;
+                        from += head.c * BC;   // the tile's first column of the row
+                        const uint32_t shift = HOW == ANY ? row_shift(from) : 0u;
+                        bits |= shift << (4 * i);
                         const char *src = reinterpret_cast<const char *>(from) - shift;
-                        if (shift == 0 ? col + 8 <= a.V : col >= 8 && col + 16 <= a.V) {
-#pragma unroll
-                            for (int k = 0; k < P; ++k)
-                                if (HOW == LOAD || k < P - 1 || shift != 0)
-                                    cp_async16(piece(in.slot, k), src + 16 * k, 16u);
-                        } else {   // a row's first or last columns, one by one
-                            for (int k = 0; k < 8 && col + k < a.V; ++k) {
-                                const uint32_t at = shift + k * ES;
-                                *reinterpret_cast<T *>(smem + (piece(in.slot, at / 16) - tiles) + at % 16) = from[k];
+                        const uint32_t dst = staged(in.slot, i);
+                        // columns of piece k of the tile: first .. first + 16 / ES - 1
+                        auto bring = [&](int k) {
+                            const int first = col + (16 * k - static_cast<int>(shift)) / ES;
+                            if (first >= 0 && first + 16 / ES <= a.V) {
+                                cp_async16(dst + 16 * k, src + 16 * k, 16u);
+                            } else {   // a row's ends, one by one
+                                for (int x = 0; x < 16 / ES; ++x)
+                                    if (first + x >= 0 && first + x < a.V)
+                                        reinterpret_cast<T *>(smem + (dst - tiles) + 16 * k)[x] = reinterpret_cast<const T *>(src + 16 * k)[x];
                             }
-                        }
+                        };
+#pragma unroll
+                        for (int k = 0; k < P; ++k)
+                            bring(k * 16 + chunk);
+                        if (HOW == ANY && chunk == 0 && shift != 0)
+                            bring(P * 16);
                     }
                     more = head.next(a, blocks);
                 }
                 asm volatile("cp.async.commit_group;" ::: "memory");
-                shifts = shifts << 4 | shift;
+                shifts = shifts << (4 * NR) | bits;
                 in.next();
             };
             for (int i = 0; i < S::BATCHES - 1; ++i)
@@ -543,18 +560,23 @@ __global__ void __launch_bounds__(Shape<T, HOW, RP>::THREADS, 1)
             while (left) {
                 ask();
                 asm volatile("cp.async.wait_group %0;" ::"n"(S::BATCHES - 1) : "memory");
+                __syncwarp();   // every lane's pieces of the warp's rows
                 const int rows = tail.rows(), padded = (rows + 15) / 16 * 16, col = c0 + tail.c * BC + chunk * 8;
-                if (tail.half == 0 && !warp_wait(empty(st.slot), st.parity ^ 1u, abort_flag, budget))
+                if (tail.part == 0 && !warp_wait(empty(st.slot), st.parity ^ 1u, abort_flag, budget))
                     break;
-                const int m = tail.half * 32 + r0;
-                if (m < padded) {
+#pragma unroll
+                for (int i = 0; i < NR; ++i) {
+                    const int m = (tail.part * NR + i) * 32 + r0;
+                    if (m >= padded)
+                        continue;
                     uint32_t o[S::PLANES][4] = {};
                     if (m < rows && col < a.V) {
                         constexpr int W = Elem<T>::WORDS;
                         uint32_t x[W + 4] = {};
+                        const uint4 *in_row = reinterpret_cast<const uint4 *>(smem + (staged(out.slot, i) - tiles)) + chunk * P;
 #pragma unroll
-                        for (int k = 0; k < P; ++k) {
-                            const uint4 v = *reinterpret_cast<const uint4 *>(smem + (piece(out.slot, k) - tiles));
+                        for (int k = 0; k < P + (HOW == ANY ? 1 : 0); ++k) {
+                            const uint4 v = in_row[k];
                             x[4 * k] = v.x;
                             x[4 * k + 1] = v.y;
                             x[4 * k + 2] = v.z;
@@ -562,7 +584,7 @@ __global__ void __launch_bounds__(Shape<T, HOW, RP>::THREADS, 1)
                         }
                         Raw8<T> w;
                         if (HOW == ANY) {
-                            shift_words<W, ES == 2>(w.w, x, shifts >> (4 * (S::BATCHES - 1)) & 15u);
+                            shift_words<W, ES == 2>(w.w, x, shifts >> (4 * (NR * (S::BATCHES - 1) + i)) & 15u);
                         } else {
 #pragma unroll
                             for (int k = 0; k < W; ++k)
@@ -584,8 +606,8 @@ __global__ void __launch_bounds__(Shape<T, HOW, RP>::THREADS, 1)
                         *reinterpret_cast<uint4 *>(smem + st.slot * S::TILE + place(j * STEP + m)) =
                             make_uint4(o[j][0], o[j][1], o[j][2], o[j][3]);
                 }
+                __syncwarp();   // the rows have been read, the tile's part is written
                 if (tail.last()) {
-                    __syncwarp();
                     if (lane == 0)
                         mbar_arrive(full(st.slot));
                     st.next();
@@ -615,10 +637,10 @@ template <int RP> __global__ void __launch_bounds__(256) adapters_fold_kernel(co
     __shared__ float4 sums[SHARE][ITEMS];
     const int item = threadIdx.x % ITEMS, k = threadIdx.x / ITEMS;
     const int64_t count = a.p1 - a.p0 + 16;   // a part may end up to 15 positions past p1
-    const int64_t i = (static_cast<int64_t>(blockIdx.x) * ITEMS + item);   // four ranks of a position
+    const int64_t i = (static_cast<int64_t>(blockIdx.x) * ITEMS + item);   // four ranks of a position, positions side by side
     pdl_wait();
     pdl_launch_dependents();
-    const int pos = a.p0 + static_cast<int>(i / (RP / 4)), r = static_cast<int>(i % (RP / 4)) * 4;
+    const int pos = a.p0 + static_cast<int>(i % count), r = static_cast<int>(i / count) * 4;
     int ad = a.n;
     if (i < count * (RP / 4) && pos < a.N) {
         ad = a.plan.adapter[pos];
@@ -667,10 +689,10 @@ template <int RP> __global__ void __launch_bounds__(256) adapters_fold_kernel(co
 
 // ---------------------------------------------------------------- dA
 // CTA (x, a): dA of adapter a, columns x * 128 .. + 127 of D; a warp has 16 of them for
-// all ranks.  Rows in chunks of 32 (gathered in the plan's order) by asynchronous copies
+// all ranks.  Rows in chunks of 64 (gathered in the plan's order) by asynchronous copies
 // into a ring of three stages.
 template <int RT> struct DaShape {
-    static constexpr int ROWS = 32, COLS = 128, STAGES = 3;
+    static constexpr int ROWS = 64, COLS = 128, STAGES = 3;
     static constexpr int HROW = COLS * 2 + 16, UROW = 3 * RT * 2 + 16;   // padded: no bank twice
     static constexpr int STAGE = ROWS * (HROW + UROW), BYTES = STAGES * STAGE;
 };
@@ -689,11 +711,11 @@ template <int RT> __global__ void __launch_bounds__(256) adapters_dA_kernel(cons
     if (b == e && a.accumulate)
         return;
     float acc[RM][2][4] = {};
-    const int hc = tid % 16 * 8;   // this thread's piece of rows tid / 16 and tid / 16 + 16 of a chunk
-    int row[2];
+    const int hc = tid % 16 * 8;   // this thread's piece of rows tid / 16, tid / 16 + 16, .. of a chunk
+    int row[ROWS / 16];
     auto look_up = [&](int p) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < ROWS / 16; ++i) {
             const int at = p + tid / 16 + i * 16;
             row[i] = at < e ? a.plan.perm[at] : -1;
         }
@@ -702,7 +724,7 @@ template <int RT> __global__ void __launch_bounds__(256) adapters_dA_kernel(cons
         const uint32_t h0 = ring0 + stage * S::STAGE, u0 = h0 + ROWS * HROW;
         if (p < e) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
+            for (int i = 0; i < ROWS / 16; ++i) {
                 const bool on = row[i] >= 0 && d0 + hc < a.D;
                 cp_async16(h0 + (tid / 16 + i * 16) * HROW + hc * 2, a.h + (on ? static_cast<size_t>(row[i]) * a.D + d0 + hc : 0), on ? 16u : 0u);
             }
@@ -794,7 +816,7 @@ template <int RT> __global__ void __launch_bounds__(256) adapters_dh_kernel(cons
             const bool on0 = p + g < e, on1 = p + g + 8 < e;
             float acc[4][4] = {};
             const uint16_t *u = a.du + static_cast<size_t>(p + g) * (3 * RT);
-#pragma unroll 1
+#pragma unroll(RT <= 32 ? 3 : 1)
             for (int i = 0; i < 3; ++i)
 #pragma unroll
                 for (int k = 0; k < KS; ++k) {
@@ -909,10 +931,14 @@ cudaError_t adapters_grad_prepare_device()
         e = prepare<64>();
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(adapters_dh_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, 128 * 528);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(adapters_dA_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, DaShape<64>::BYTES);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(adapters_dA_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, DaShape<128>::BYTES);
+    auto set = [&](auto kernel, int bytes) {
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    };
+    set(adapters_dA_kernel<16>, DaShape<16>::BYTES);
+    set(adapters_dA_kernel<32>, DaShape<32>::BYTES);
+    set(adapters_dA_kernel<64>, DaShape<64>::BYTES);
+    set(adapters_dA_kernel<128>, DaShape<128>::BYTES);
     return e;
 }
 
@@ -938,7 +964,7 @@ cudaError_t adapters_grad_launch(const CUtensorMap (&maps)[2], AdapterGradArgs a
         }
     const dim3 grid_a(static_cast<unsigned>((a.D + 127) / 128), static_cast<unsigned>(a.n));
     const int64_t columns = (a.D + 255) / 256;
-    int64_t chunk = 128;
+    int64_t chunk = 32;
     while (chunk > 16 && columns * ((a.N + chunk - 1) / chunk) < 4 * num_sms)
         chunk /= 2;
     while ((a.N + chunk - 1) / chunk > 65535)

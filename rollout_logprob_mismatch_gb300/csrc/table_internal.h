@@ -26,7 +26,7 @@ inline size_t ws_round(size_t x) { return (x + 255) / 256 * 256; }
 // ---------------------------------------------------------------- adapters
 constexpr int AD_MAX_RANK = 128;
 constexpr int AD_MAX_ADAPTERS = 65535;
-constexpr int AD_SHRINK_THREADS = 256;
+constexpr int AD_SHRINK_THREADS = 512;
 constexpr int AD_FEW_ROWS = 1024;    // rows up to which they are ordered and projected in one launch
 constexpr int AD_MAP_THREADS = 288;  // eight warps of products, one of copies
 constexpr int AD_MAP_ROWS = 256;     // positions of a CTA of the map, at most
@@ -96,7 +96,7 @@ struct AdapterGradArgs {
     int32_t row_part;         // positions of a launch
     int32_t p0, p1, r0;       // the launch's positions and first rank
     int32_t row_chunk;        // dh: positions of a CTA
-    float *partial;           // [du_parts][p1 - p0 + 16][min(RT, 64)]
+    float *partial;           // [du_parts][min(RT, 64) / 4][p1 - p0 + 16][4]
     uint16_t *du;             // [N][3][RT] bf16 parts of scale B^T dy
     float *dh, *dA, *dB;
     int32_t accumulate, accumulate_dh;
