@@ -314,18 +314,16 @@ template <int WORDS> __device__ __forceinline__ void lds_words(uint32_t (&w)[4],
 }
 
 // Shared memory of a CTA of the map: a ring of tiles (16 rows of the slab and their t),
-// and two buffers for the slab of an adapter's factor.
+// and one of the slabs of adapters' factors.
 template <typename T, int RP, int PARTS, int CB> struct MapShape {
     static constexpr int COLS = 256 * CB;                              // columns of a slab
     static constexpr int ROW = COLS * static_cast<int>(sizeof(T)) + 64;   // bytes of a staged row: a warp's 16-byte reads meet no bank twice
     static constexpr int TROW = (PARTS * RP + 8) * 2;
     static constexpr int STAGE = 16 * (ROW + TROW);
     static constexpr int FACTOR = COLS * RP * 2;
-    static constexpr int MOST = AD_MAP_SMEM - 256 - 2 * FACTOR;
-    static constexpr int STAGES = 4 * STAGE <= MOST ? 4 : 3;
-    static constexpr int BYTES = STAGES * STAGE + 2 * FACTOR + 256;
-    static_assert(BYTES <= AD_MAP_SMEM, "shared memory of a CTA");
-    static_assert(ROW % 16 == 0 && TROW % 16 == 0, "alignment");
+    static constexpr int bytes(int stages, int factors) { return stages * STAGE + factors * FACTOR + 256; }
+    static constexpr int MOST = bytes(4, 2) <= AD_MAP_SMEM ? 4 : 3;    // stages
+    static_assert(bytes(MOST, 2) <= AD_MAP_SMEM, "shared memory of a CTA");
 };
 
 // A CTA: row_chunk positions, 256 CB columns, eight warps of 32 CB columns (the CTAs
@@ -334,7 +332,7 @@ template <typename T, int RP, int PARTS, int CB> struct MapShape {
 // the logits' column 8 (n / 2) + 2 j + n % 2, so that lane q's eight results are eight
 // neighbours.
 template <typename T, int RP, int PARTS, int CB, bool AL>
-__global__ void __launch_bounds__(AD_MAP_THREADS) adapters_map_kernel(const AdapterArgs a)
+__global__ void __launch_bounds__(AD_MAP_THREADS, CB == 1 && RP <= 32 ? 3 : 2) adapters_map_kernel(const AdapterArgs a)
 {
     using K = Ranks<RP>;
     using S = MapShape<T, RP, PARTS, CB>;
@@ -342,24 +340,22 @@ __global__ void __launch_bounds__(AD_MAP_THREADS) adapters_map_kernel(const Adap
     constexpr int W = Elem<T>::WORDS;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int32_t s_row[AD_MAP_ROWS], s_ad[AD_MAP_ROWS + 1];
-    const uint32_t base = smem_u32(smem), factor0 = base + S::STAGES * S::STAGE;
-    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + S::STAGES * S::STAGE + 2 * S::FACTOR);
+    const uint32_t base = smem_u32(smem), factor0 = base + a.stages * S::STAGE;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + a.stages * S::STAGE + a.factors * S::FACTOR);
     const uint32_t bar0 = smem_u32(bars);
     auto full = [&](int i) { return bar0 + 8u * i; };
-    auto empty = [&](int i) { return bar0 + 8u * (S::STAGES + i); };
-    auto ffull = [&](int i) { return bar0 + 8u * (2 * S::STAGES + i); };
-    auto fempty = [&](int i) { return bar0 + 8u * (2 * S::STAGES + 2 + i); };
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(bars + 2 * S::STAGES + 4);
+    auto empty = [&](int i) { return bar0 + 8u * (4 + i); };
+    auto ffull = [&](int i) { return bar0 + 8u * (8 + i); };
+    auto fempty = [&](int i) { return bar0 + 8u * (12 + i); };
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(bars + 16);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q = lane & 3;
     const int slabs = (a.V + S::COLS - 1) / S::COLS;
     const int c0 = static_cast<int>(blockIdx.x % slabs) * S::COLS, c1 = min(a.V, c0 + S::COLS);
     const int p0 = static_cast<int>(blockIdx.x / slabs) * a.row_chunk;
     if (tid == 0) {
-        for (int i = 0; i < S::STAGES; ++i) {
+        for (int i = 0; i < 4; ++i) {
             mbar_init(full(i), 1);
             mbar_init(empty(i), WARPS);
-        }
-        for (int i = 0; i < 2; ++i) {
             mbar_init(ffull(i), 1);
             mbar_init(fempty(i), WARPS);
         }
@@ -393,8 +389,8 @@ __global__ void __launch_bounds__(AD_MAP_THREADS) adapters_map_kernel(const Adap
     if (warp == WARPS) {
         // ------------------------------------------------------------ copies
         const uint64_t pol = l2_policy_evict_first(), pol_keep = l2_policy_evict_normal();
-        int stage = 0, held = -1;   // held: the adapter of the last factor copied
-        uint32_t phase = 0, loads = 0;
+        int stage = 0, slot = 0, held = -1;   // held: the adapter of the last factor copied
+        uint32_t phase = 0, fphase = 0;
         bool ok = true;
         for (int p = 0; ok && p < rows; p += 16) {
             ok = warp_wait(empty(stage), phase ^ 1u, abort_flag, budget);
@@ -415,7 +411,7 @@ __global__ void __launch_bounds__(AD_MAP_THREADS) adapters_map_kernel(const Adap
                 bulk_load(dst + lane * S::ROW + c.off, c.src, c.bytes, full(stage), pol);
             if (lane == 0)
                 bulk_load(dst + 16 * S::ROW, a.plan.t + static_cast<size_t>(p0 + p) * (S::TROW / 2), tbytes, full(stage), pol_keep);
-            if (++stage == S::STAGES) {
+            if (++stage == a.stages) {
                 stage = 0;
                 phase ^= 1u;
             }
@@ -427,8 +423,7 @@ __global__ void __launch_bounds__(AD_MAP_THREADS) adapters_map_kernel(const Adap
                 const int i = __ffs(starts) - 1;
                 starts &= starts - 1;
                 held = s_ad[p + i];
-                const int slot = loads & 1;
-                ok = warp_wait(fempty(slot), ((loads >> 1) & 1u) ^ 1u, abort_flag, budget);
+                ok = warp_wait(fempty(slot), fphase ^ 1u, abort_flag, budget);
                 if (!ok)
                     break;
                 if (lane == 0) {
@@ -437,15 +432,18 @@ __global__ void __launch_bounds__(AD_MAP_THREADS) adapters_map_kernel(const Adap
                     bulk_load(factor0 + slot * S::FACTOR, a.B + (static_cast<size_t>(held) * a.V + c0) * a.R, bytes, ffull(slot),
                               pol_keep);
                 }
-                ++loads;
+                if (++slot == a.factors) {
+                    slot = 0;
+                    fphase ^= 1u;
+                }
             }
         }
     } else {
         // ------------------------------------------------------------ products
         const int w0 = warp * 32 * CB;   // the warp's columns in the slab
         T *out = static_cast<T *>(a.out);
-        int stage = 0, held = -1;
-        uint32_t phase = 0, taken = 0;   // factors taken
+        int stage = 0, held = -1, slot = a.factors - 1;   // slot: of the factor held
+        uint32_t phase = 0, fphase = 1;
         bool ok = true;
         const uint32_t frow = static_cast<uint32_t>(a.R) * 2;
         const uint32_t fcol = static_cast<uint32_t>(w0 + 8 * (g >> 1) + (g & 1)) * frow + q * (K::STEP * 2);
@@ -467,14 +465,17 @@ __global__ void __launch_bounds__(AD_MAP_THREADS) adapters_map_kernel(const Adap
                     if (ad != held) {
                         __syncwarp();
                         if (held >= 0 && lane == 0)
-                            mbar_arrive(fempty((taken - 1) & 1));
+                            mbar_arrive(fempty(slot));
                         held = ad;
-                        ok = warp_wait(ffull(taken & 1), (taken >> 1) & 1u, abort_flag, budget);
+                        if (++slot == a.factors) {
+                            slot = 0;
+                            fphase ^= 1u;
+                        }
+                        ok = warp_wait(ffull(slot), fphase, abort_flag, budget);
                         if (!ok)
                             break;
-                        ++taken;
                     }
-                    const uint32_t fs = factor0 + ((taken - 1) & 1) * S::FACTOR + fcol;
+                    const uint32_t fs = factor0 + slot * S::FACTOR + fcol;
                     float acc[CB][4][4] = {};
 #pragma unroll
                     for (int k = 0; k < K::GROUPS; ++k) {
@@ -557,7 +558,7 @@ __global__ void __launch_bounds__(AD_MAP_THREADS) adapters_map_kernel(const Adap
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(empty(stage));
-            if (++stage == S::STAGES) {
+            if (++stage == a.stages) {
                 stage = 0;
                 phase ^= 1u;
             }
@@ -566,12 +567,11 @@ __global__ void __launch_bounds__(AD_MAP_THREADS) adapters_map_kernel(const Adap
     __syncthreads();
     if (tid == 0 && *abort_flag) {
         // copies may still be on their way: every stage's and buffer's last one lands, or not, within the wait
-        for (int i = 0; i < S::STAGES; ++i)
-            for (uint32_t f = 0; f < 2; ++f)
+        for (int i = 0; i < 4; ++i)
+            for (uint32_t f = 0; f < 2; ++f) {
                 drain_wait(full(i), f, 100000000ull);
-        for (int i = 0; i < 2; ++i)
-            for (uint32_t f = 0; f < 2; ++f)
                 drain_wait(ffull(i), f, 100000000ull);
+            }
         atomicCAS(a.status, 0, static_cast<int>(TIM_ERR_TIMEOUT));
     }
 }
@@ -614,40 +614,43 @@ template <int PARTS> cudaError_t shrink(const AdapterArgs &a, int num_sms, cudaS
     }
 }
 
-// Blocks of 32 columns of a warp: 128 bytes of a row where two factors leave room for
-// two CTAs an SM.
-template <typename T, int RP> constexpr int map_blocks() { return sizeof(T) == 2 && RP == 16 ? 2 : 1; }
-
-template <typename T, int PARTS, int RP, bool AL> cudaError_t map(const AdapterArgs &a, dim3 grid, cudaStream_t s, bool set)
+template <typename T, int PARTS, int RP, int CB> cudaError_t map(AdapterArgs a, int num_sms, cudaStream_t s, bool set)
 {
-    constexpr int CB = map_blocks<T, RP>(), BYTES = MapShape<T, RP, PARTS, CB>::BYTES;
-    auto kernel = adapters_map_kernel<T, RP, PARTS, CB, AL>;
-    if (set)
-        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, BYTES);
-    return launch(kernel, grid, AD_MAP_THREADS, BYTES, a, s);
-}
-
-// set: the kernels' shared memory is granted instead.
-template <typename T, int PARTS, int RP> cudaError_t map(AdapterArgs a, int num_sms, cudaStream_t s, bool set)
-{
+    using S = MapShape<T, RP, PARTS, CB>;
+    auto aligned = adapters_map_kernel<T, RP, PARTS, CB, true>, any = adapters_map_kernel<T, RP, PARTS, CB, false>;
     if (set) {
-        const cudaError_t e = map<T, PARTS, RP, true>(a, dim3(1), s, true);
-        return e != cudaSuccess ? e : map<T, PARTS, RP, false>(a, dim3(1), s, true);
+        const cudaError_t e = cudaFuncSetAttribute(aligned, cudaFuncAttributeMaxDynamicSharedMemorySize, AD_MAP_SMEM);
+        return e != cudaSuccess ? e : cudaFuncSetAttribute(any, cudaFuncAttributeMaxDynamicSharedMemorySize, AD_MAP_SMEM);
     }
-    constexpr int COLS = 256 * map_blocks<T, RP>();
-    const int slabs = (a.V + COLS - 1) / COLS;
-    // few rows: a tile a CTA, so that the adapters' factors come in parallel
+    const int slabs = (a.V + S::COLS - 1) / S::COLS;
+    // few rows: a tile a CTA, so that the adapters' factors come in parallel, and more of them at a time
     int64_t rows = AD_MAP_ROWS;
     while (rows > 16 && slabs * ((a.N + rows - 1) / rows) < int64_t(8) * num_sms)
         rows /= 2;
     a.row_chunk = static_cast<int32_t>(rows);
+    a.stages = std::min<int>(S::MOST, static_cast<int>(rows / 16));
+    a.factors = a.stages == 1 && S::bytes(1, 4) <= AD_MAP_SMEM / 3 ? 4 : 2;
     const dim3 grid(static_cast<unsigned>(slabs * ((a.N + rows - 1) / rows)));
-    auto aligned = [](const void *p, int64_t ld, int64_t N) {
+    auto starts16 = [](const void *p, int64_t ld, int64_t N) {
         return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && (N == 1 || ld * sizeof(T) % 16 == 0);
     };
-    if (aligned(a.z, a.ld, a.N) && aligned(a.out, a.ldo, a.N))
-        return map<T, PARTS, RP, true>(a, grid, s, false);
-    return map<T, PARTS, RP, false>(a, grid, s, false);
+    return launch(starts16(a.z, a.ld, a.N) && starts16(a.out, a.ldo, a.N) ? aligned : any, grid, AD_MAP_THREADS,
+                  S::bytes(a.stages, a.factors), a, s);
+}
+
+// A warp has 32 columns, or 64 (128 bytes of a row) of 16-bit logits at the smallest
+// ranks, where a batch is large enough to be bound by them.
+template <typename T, int PARTS, int RP> cudaError_t map(const AdapterArgs &a, int num_sms, cudaStream_t s, bool set)
+{
+    if constexpr (sizeof(T) == 2 && RP == 16) {
+        if (set) {
+            const cudaError_t e = map<T, PARTS, RP, 1>(a, num_sms, s, true);
+            return e != cudaSuccess ? e : map<T, PARTS, RP, 2>(a, num_sms, s, true);
+        }
+        if (static_cast<int64_t>(a.N) * a.V >= int64_t(num_sms) * 512 * AD_MAP_ROWS)
+            return map<T, PARTS, RP, 2>(a, num_sms, s, false);
+    }
+    return map<T, PARTS, RP, 1>(a, num_sms, s, set);
 }
 
 template <typename T, int PARTS> cudaError_t map(const AdapterArgs &a, int num_sms, cudaStream_t s)

@@ -788,7 +788,10 @@ template <int RT> __global__ void __launch_bounds__(256) adapters_dA_kernel(cons
 
 // ---------------------------------------------------------------- dh
 // CTA (x, y): columns x * 256 .. + 255 of D (a warp 32) of positions y * chunk ...; the
-// adapter's A slab is in shared memory while the rows' adapter is the same.
+// adapter's A slab is in registers while the rows' adapter is the same, and the next 16
+// rows' du is on its way while the products of the 16 before are written.  A lane has
+// four neighbouring ranks (8 bytes) of du where the product's order of k is two pairs; A's
+// rows are taken in the same order.
 template <int RT> __global__ void __launch_bounds__(256) adapters_dh_kernel(const AdapterGradArgs a)
 {
     constexpr int COLS = 256, AROW = COLS * 2 + 16, KS = RT / 16;
@@ -800,9 +803,29 @@ template <int RT> __global__ void __launch_bounds__(256) adapters_dh_kernel(cons
     const int live = a.plan.offsets[a.n];
     const int p0 = blockIdx.y * a.row_chunk, p1 = min(a.N, p0 + a.row_chunk);
     const uint32_t a0 = smem_u32(as);
+    const int kr = lane & 15;   // k of the lane's row address: 2 q + i is rank 4 q + i, 2 q + 8 + i is 4 q + 2 + i
+    const int rank = (kr & 7) / 2 * 4 + (kr & 1) + (kr >= 8 ? 2 : 0);
     for (int p = p0; p < min(p1, live);) {   // adapter by adapter
         const int ad = a.plan.adapter[p];
         const int e = min(p1, a.plan.offsets[ad + 1]);
+        uint2 u[3][KS][2];   // rows g and g + 8
+        int row[2];
+        auto fetch = [&](int at) {
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const int i = at + g + half * 8;
+                row[half] = i < e ? a.plan.perm[i] : -1;
+#pragma unroll
+                for (int part = 0; part < 3; ++part)
+#pragma unroll
+                    for (int k = 0; k < KS; ++k)
+                        u[part][k][half] = i < e ? *reinterpret_cast<const uint2 *>(a.du + static_cast<size_t>(i) * (3 * RT) +
+                                                                                     part * RT + k * 16 + 4 * q)
+                                                 : make_uint2(0u, 0u);
+            }
+        };
+        if (KS <= 4)
+            fetch(p);
         __syncthreads();
         for (int i = tid; i < RT * (COLS / 8); i += 256) {
             const int r = i / (COLS / 8), c = i % (COLS / 8) * 8;
@@ -812,39 +835,43 @@ template <int RT> __global__ void __launch_bounds__(256) adapters_dh_kernel(cons
                    : make_uint4(0u, 0u, 0u, 0u);
         }
         __syncthreads();
+        uint32_t w[KS][4][2];
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+#pragma unroll
+            for (int j = 0; j < 4; j += 2) {
+                uint32_t x[4];
+                ldsm4t(x, a0 + (k * 16 + rank) * AROW + (warp * 32 + j * 8 + (lane >> 4) * 8) * 2);
+                w[k][j][0] = x[0];
+                w[k][j][1] = x[1];
+                w[k][j + 1][0] = x[2];
+                w[k][j + 1][1] = x[3];
+            }
         for (; p < e; p += 16) {
-            const bool on0 = p + g < e, on1 = p + g + 8 < e;
+            if (KS > 4)   // no room for the next ones
+                fetch(p);
             float acc[4][4] = {};
-            const uint16_t *u = a.du + static_cast<size_t>(p + g) * (3 * RT);
-#pragma unroll(RT <= 32 ? 3 : 1)
-            for (int i = 0; i < 3; ++i)
 #pragma unroll
-                for (int k = 0; k < KS; ++k) {
-                    const int r = i * RT + k * 16 + 2 * q;
-                    uint32_t x[4];
-                    x[0] = on0 ? *reinterpret_cast<const uint32_t *>(u + r) : 0u;
-                    x[1] = on1 ? *reinterpret_cast<const uint32_t *>(u + 8 * (3 * RT) + r) : 0u;
-                    x[2] = on0 ? *reinterpret_cast<const uint32_t *>(u + r + 8) : 0u;
-                    x[3] = on1 ? *reinterpret_cast<const uint32_t *>(u + 8 * (3 * RT) + r + 8) : 0u;
+            for (int part = 0; part < 3; ++part)
 #pragma unroll
-                    for (int j = 0; j < 4; j += 2) {
-                        uint32_t w[4];
-                        ldsm4t(w, a0 + (k * 16 + (lane & 15)) * AROW + (warp * 32 + j * 8 + (lane >> 4) * 8) * 2);
-                        mma16816(acc[j], x, w[0], w[1]);
-                        mma16816(acc[j + 1], x, w[2], w[3]);
-                    }
-                }
+                for (int k = 0; k < KS; ++k)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        mma16816(acc[j], {u[part][k][0].x, u[part][k][1].x, u[part][k][0].y, u[part][k][1].y}, w[k][j][0], w[k][j][1]);
+            const int to[2] = {row[0], row[1]};
+            if (KS <= 4 && p + 16 < e)
+                fetch(p + 16);
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-                if (!(half ? on1 : on0))
+                if (to[half] < 0)
                     continue;
-                float *row = a.dh + static_cast<size_t>(a.plan.perm[p + g + half * 8]) * a.D;
+                float *out = a.dh + static_cast<size_t>(to[half]) * a.D;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const int d = dw + j * 8 + 2 * q;
                     if (d >= a.D)
                         continue;
-                    float2 *o = reinterpret_cast<float2 *>(row + d);
+                    float2 *o = reinterpret_cast<float2 *>(out + d);
                     float2 x = make_float2(acc[j][half * 2], acc[j][half * 2 + 1]);
                     if (a.accumulate_dh) {
                         const float2 y = *o;
@@ -964,7 +991,7 @@ cudaError_t adapters_grad_launch(const CUtensorMap (&maps)[2], AdapterGradArgs a
         }
     const dim3 grid_a(static_cast<unsigned>((a.D + 127) / 128), static_cast<unsigned>(a.n));
     const int64_t columns = (a.D + 255) / 256;
-    int64_t chunk = 32;
+    int64_t chunk = 128;
     while (chunk > 16 && columns * ((a.N + chunk - 1) / chunk) < 4 * num_sms)
         chunk /= 2;
     while ((a.N + chunk - 1) / chunk > 65535)

@@ -60,6 +60,7 @@ struct AdapterArgs {
     int64_t ldo;
     int32_t in_place;
     int32_t row_chunk;        // map: positions of a CTA, a multiple of 16
+    int32_t stages, factors;  // map: tiles and factors that a CTA has room for
     uint64_t wait_budget_ns;
     int *status;
 };
