@@ -93,13 +93,13 @@ __device__ __forceinline__ void write_order(const AdapterArgs &a, int ad, const 
 
 // t of up to 16 rows under adapter ad, written for rows lo .. hi - 1 of them at positions
 // pos + lo ..  The 16 warps share k (every 16th 32 of it each) and add up through shared
-// memory in their order, so that a row's sum depends on D alone.
-template <int RP, int PARTS>
+// memory in their order, so that a row's sum depends on D alone.  AHEAD: steps of 32 k
+// whose loads are in flight together.
+template <int RP, int PARTS, int AHEAD>
 __device__ __forceinline__ void project(const AdapterArgs &a, int ad, const int32_t *rows, int lo, int hi, int pos)
 {
     constexpr int WARPS = AD_SHRINK_THREADS / 32;
     constexpr int NC = RP < 32 ? RP : 32;      // rank columns at a time
-    constexpr int AHEAD = 4;                   // steps of 32 k whose loads are in flight together
     __shared__ float sums[WARPS][16][NC + 1];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
     const float scale = a.scale ? a.scale[ad] : 1.f;
@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(AD_SHRINK_THREADS) adapters_shrink_kernel(cons
                     mine[p - c0] = r;
             });
         __syncthreads();
-        project<RP, PARTS>(a, ad, mine, 0, rows, o.base + c0);
+        project<RP, PARTS, 4>(a, ad, mine, 0, rows, o.base + c0);
         if (c0 + rows == o.count)
             pad_rows(a, ad, o.count, o.base + o.count);
         __syncthreads();
@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(AD_SHRINK_THREADS) adapters_order_kernel(const
 }
 
 template <int RP, int PARTS>
-__global__ void __launch_bounds__(AD_SHRINK_THREADS) adapters_project_kernel(const AdapterArgs a)
+__global__ void __launch_bounds__(AD_SHRINK_THREADS, 2) adapters_project_kernel(const AdapterArgs a)
 {
     __shared__ int32_t s_row[16], s_ad[17];
     pdl_wait();
@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(AD_SHRINK_THREADS) adapters_project_kernel(con
         int m = s + 1;
         while (s_ad[m] == s_ad[s])
             ++m;
-        project<RP, PARTS>(a, s_ad[s], s_row, s, m, p0);
+        project<RP, PARTS, RP == 16 ? 2 : 1>(a, s_ad[s], s_row, s, m, p0);
         const int ad = s_ad[s], e = a.plan.offsets[ad + 1];
         if (p0 + m == e)
             pad_rows(a, ad, e - a.plan.offsets[ad], e);
@@ -361,14 +361,6 @@ __global__ void __launch_bounds__(AD_MAP_THREADS, CB == 1 && RP <= 32 ? 3 : 2) a
         }
         *abort_flag = 0;
         fence_mbar_init();
-    }
-    if (warp == WARPS && lane < 16 && a.row_chunk == 16 && p0 + lane < a.N) {
-        // few rows: while they are projected, the factors' slabs (and the logits') of as many
-        // rows come into L2.  What the launches before the projection's wrote is there: it
-        // waited for them before it let this kernel start.
-        const int id = a.rows[p0 + lane];
-        if (static_cast<unsigned>(id) < static_cast<unsigned>(a.n))
-            bulk_prefetch(a.B + (static_cast<size_t>(id) * a.V + c0) * a.R, static_cast<uint32_t>(c1 - c0) * a.R * 2);
     }
     pdl_wait();
     pdl_launch_dependents();

@@ -688,25 +688,23 @@ template <int RP> __global__ void __launch_bounds__(256) adapters_fold_kernel(co
 }
 
 // ---------------------------------------------------------------- dA
-// CTA (x, a): dA of adapter a, columns x * 128 .. + 127 of D; a warp has 16 of them for
+// dA of an adapter, 128 columns of D from 128 x on, by a CTA; a warp has 16 of them for
 // all ranks.  Rows in chunks of 64 (gathered in the plan's order) by asynchronous copies
 // into a ring of three stages.
 template <int RT> struct DaShape {
     static constexpr int ROWS = 64, COLS = 128, STAGES = 3;
     static constexpr int HROW = COLS * 2 + 16, UROW = 3 * RT * 2 + 16;   // padded: no bank twice
     static constexpr int STAGE = ROWS * (HROW + UROW), BYTES = STAGES * STAGE;
+    static_assert(BYTES >= RT * 528, "dh's slab of A lies there too");
 };
 
-template <int RT> __global__ void __launch_bounds__(256) adapters_dA_kernel(const AdapterGradArgs a)
+template <int RT> __device__ __forceinline__ void dA_part(const AdapterGradArgs &a, int column_block, int ad, uint8_t *ring)
 {
     using S = DaShape<RT>;
     constexpr int ROWS = S::ROWS, COLS = S::COLS, HROW = S::HROW, UROW = S::UROW, RM = RT / 16;
-    extern __shared__ __align__(16) uint8_t ring[];
     const uint32_t ring0 = smem_u32(ring);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q = lane & 3;
-    const int ad = blockIdx.y, d0 = blockIdx.x * COLS;
-    pdl_wait();
-    pdl_launch_dependents();
+    const int d0 = column_block * COLS;
     const int b = a.plan.offsets[ad], e = a.plan.offsets[ad + 1];
     if (b == e && a.accumulate)
         return;
@@ -787,21 +785,18 @@ template <int RT> __global__ void __launch_bounds__(256) adapters_dA_kernel(cons
 }
 
 // ---------------------------------------------------------------- dh
-// CTA (x, y): columns x * 256 .. + 255 of D (a warp 32) of positions y * chunk ...; the
+// dh in 256 columns (a warp 32) of row_chunk positions, by a CTA; the
 // adapter's A slab is in registers while the rows' adapter is the same, and the next 16
 // rows' du is on its way while the products of the 16 before are written.  A lane has
 // four neighbouring ranks (8 bytes) of du where the product's order of k is two pairs; A's
 // rows are taken in the same order.
-template <int RT> __global__ void __launch_bounds__(256) adapters_dh_kernel(const AdapterGradArgs a)
+template <int RT> __device__ __forceinline__ void dh_part(const AdapterGradArgs &a, int column_block, int64_t chunk, uint8_t *as)
 {
     constexpr int COLS = 256, AROW = COLS * 2 + 16, KS = RT / 16;
-    extern __shared__ __align__(16) uint8_t as[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q = lane & 3;
-    const int d0 = blockIdx.x * COLS, dw = d0 + warp * 32;
-    pdl_wait();
-    pdl_launch_dependents();
+    const int d0 = column_block * COLS, dw = d0 + warp * 32;
     const int live = a.plan.offsets[a.n];
-    const int p0 = blockIdx.y * a.row_chunk, p1 = min(a.N, p0 + a.row_chunk);
+    const int p0 = static_cast<int>(chunk * a.row_chunk), p1 = min(a.N, p0 + a.row_chunk);
     const uint32_t a0 = smem_u32(as);
     const int kr = lane & 15;   // k of the lane's row address: 2 q + i is rank 4 q + i, 2 q + 8 + i is 4 q + 2 + i
     const int rank = (kr & 7) / 2 * 4 + (kr & 1) + (kr >= 8 ? 2 : 0);
@@ -895,6 +890,20 @@ template <int RT> __global__ void __launch_bounds__(256) adapters_dh_kernel(cons
     }
 }
 
+// Both, which wait for du alone: the first CTAs dA (fewer, and longer), the others dh.
+template <int RT> __global__ void __launch_bounds__(256) adapters_outer_kernel(const AdapterGradArgs a)
+{
+    extern __shared__ __align__(16) uint8_t shared[];
+    const int blocks_a = (a.D + 127) / 128, blocks_h = (a.D + 255) / 256;
+    const int64_t first_h = static_cast<int64_t>(blocks_a) * a.n;
+    pdl_wait();
+    pdl_launch_dependents();
+    if (blockIdx.x < first_h)
+        dA_part<RT>(a, static_cast<int>(blockIdx.x % blocks_a), static_cast<int>(blockIdx.x / blocks_a), shared);
+    else
+        dh_part<RT>(a, static_cast<int>((blockIdx.x - first_h) % blocks_h), (blockIdx.x - first_h) / blocks_h, shared);
+}
+
 template <typename F>
 cudaError_t launch(F kernel, dim3 grid, int threads, int smem, const AdapterGradArgs &a, cudaStream_t s)
 {
@@ -956,16 +965,14 @@ cudaError_t adapters_grad_prepare_device()
         e = prepare<32>();
     if (e == cudaSuccess)
         e = prepare<64>();
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(adapters_dh_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, 128 * 528);
     auto set = [&](auto kernel, int bytes) {
         if (e == cudaSuccess)
             e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     };
-    set(adapters_dA_kernel<16>, DaShape<16>::BYTES);
-    set(adapters_dA_kernel<32>, DaShape<32>::BYTES);
-    set(adapters_dA_kernel<64>, DaShape<64>::BYTES);
-    set(adapters_dA_kernel<128>, DaShape<128>::BYTES);
+    set(adapters_outer_kernel<16>, DaShape<16>::BYTES);
+    set(adapters_outer_kernel<32>, DaShape<32>::BYTES);
+    set(adapters_outer_kernel<64>, DaShape<64>::BYTES);
+    set(adapters_outer_kernel<128>, DaShape<128>::BYTES);
     return e;
 }
 
@@ -989,30 +996,17 @@ cudaError_t adapters_grad_launch(const CUtensorMap (&maps)[2], AdapterGradArgs a
             if (e != cudaSuccess)
                 return e;
         }
-    const dim3 grid_a(static_cast<unsigned>((a.D + 127) / 128), static_cast<unsigned>(a.n));
     const int64_t columns = (a.D + 255) / 256;
     int64_t chunk = 128;
     while (chunk > 16 && columns * ((a.N + chunk - 1) / chunk) < 4 * num_sms)
         chunk /= 2;
-    while ((a.N + chunk - 1) / chunk > 65535)
-        chunk *= 2;
     a.row_chunk = static_cast<int32_t>(chunk);
-    const dim3 grid_h(static_cast<unsigned>(columns), static_cast<unsigned>((a.N + chunk - 1) / chunk));
-    const int smem = a.RT * 528;
-    cudaError_t e;
+    const dim3 grid(static_cast<unsigned>((a.D + 127) / 128 * static_cast<int64_t>(a.n) + columns * ((a.N + chunk - 1) / chunk)));
     switch (a.RT) {
-    case 16:
-        e = launch(adapters_dA_kernel<16>, grid_a, 256, DaShape<16>::BYTES, a, s);
-        return e != cudaSuccess ? e : launch(adapters_dh_kernel<16>, grid_h, 256, smem, a, s);
-    case 32:
-        e = launch(adapters_dA_kernel<32>, grid_a, 256, DaShape<32>::BYTES, a, s);
-        return e != cudaSuccess ? e : launch(adapters_dh_kernel<32>, grid_h, 256, smem, a, s);
-    case 64:
-        e = launch(adapters_dA_kernel<64>, grid_a, 256, DaShape<64>::BYTES, a, s);
-        return e != cudaSuccess ? e : launch(adapters_dh_kernel<64>, grid_h, 256, smem, a, s);
-    default:
-        e = launch(adapters_dA_kernel<128>, grid_a, 256, DaShape<128>::BYTES, a, s);
-        return e != cudaSuccess ? e : launch(adapters_dh_kernel<128>, grid_h, 256, smem, a, s);
+    case 16: return launch(adapters_outer_kernel<16>, grid, 256, DaShape<16>::BYTES, a, s);
+    case 32: return launch(adapters_outer_kernel<32>, grid, 256, DaShape<32>::BYTES, a, s);
+    case 64: return launch(adapters_outer_kernel<64>, grid, 256, DaShape<64>::BYTES, a, s);
+    default: return launch(adapters_outer_kernel<128>, grid, 256, DaShape<128>::BYTES, a, s);
     }
 }
 
