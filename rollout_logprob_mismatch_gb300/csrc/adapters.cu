@@ -92,7 +92,7 @@ __device__ __forceinline__ void write_order(const AdapterArgs &a, int ad, const 
 }
 
 // t of up to 16 rows under adapter ad, written for rows lo .. hi - 1 of them at positions
-// pos + lo ..  The 16 warps share k (every 16th 32 of it each) and add up through shared
+// pos + lo ..  The eight warps share k (every eighth 32 of it each) and add up through shared
 // memory in their order, so that a row's sum depends on D alone.  AHEAD: steps of 32 k
 // whose loads are in flight together.
 template <int RP, int PARTS, int AHEAD>
@@ -174,7 +174,7 @@ __device__ __forceinline__ void pad_rows(const AdapterArgs &a, int ad, int count
 // Few rows, one launch.  CTA (a, y): the rows of adapter a, 16 at a time from the y-th 16
 // on; a = n: the rows under no adapter (only ordered).
 template <int RP, int PARTS>
-__global__ void __launch_bounds__(AD_SHRINK_THREADS) adapters_shrink_kernel(const AdapterArgs a)
+__global__ void __launch_bounds__(AD_SHRINK_THREADS, 2) adapters_shrink_kernel(const AdapterArgs a)
 {
     __shared__ int32_t mine[16];
     const int ad = blockIdx.x;
@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(AD_SHRINK_THREADS) adapters_order_kernel(const
 }
 
 template <int RP, int PARTS>
-__global__ void __launch_bounds__(AD_SHRINK_THREADS, 2) adapters_project_kernel(const AdapterArgs a)
+__global__ void __launch_bounds__(AD_SHRINK_THREADS, 4) adapters_project_kernel(const AdapterArgs a)
 {
     __shared__ int32_t s_row[16], s_ad[17];
     pdl_wait();

@@ -17,8 +17,8 @@
 //   warps 2-5   du and dB from TMEM to memory
 //   warps 6-    the tiles (the rows of an adapter lie anywhere): 16-byte asynchronous
 //               copies to their swizzled places; fp32, fp16 and rows off a 16-byte boundary
-//               (RAW) by plain loads, as one or two planes of bf16 parts, x = hi + lo leaves
-//               at most 2^-16 |x|
+//               (RAW) by plain loads, as planes of bf16 parts: one, two (fp16, exactly), or
+//               three (fp32: 2^-24 of it is left at most)
 // (TMA gathers of four rows brought the same tiles at 3.0 us a tile of 32 KB and SM.)
 // Every sum has one order, fixed by the rows' order and V: the same call gives the same bits.
 #include <algorithm>
@@ -31,27 +31,27 @@ namespace tim {
 namespace {
 
 constexpr int BC = AG_BLOCK;            // columns of a tile
-constexpr int PARTS = 2;                // of t
+constexpr int PARTS = 3;                // of t
 
 // How tiles are brought: COPY, bf16 rows from 16-byte boundaries on; LOAD, other types'
 // rows from there; ANY, rows that start anywhere.
 enum { COPY, LOAD, ANY };
 
 template <typename T, int HOW, int RP> struct Shape {
-    static constexpr int PLANES = std::is_same<T, __nv_bfloat16>::value ? 1 : 2;
-    static constexpr int STEP = 128 / PLANES;                  // rows of a tile; the second plane lies behind the first as rows 64 ..
+    static constexpr int PLANES = sizeof(T) == 4 ? 3 : std::is_same<T, __nv_bfloat16>::value ? 1 : 2;
+    static constexpr int STEP = PLANES == 1 ? 128 : PLANES == 2 ? 64 : 32;   // rows of a tile; the planes lie behind each other as its rows
     static constexpr int SUB = 128 * 128;                      // bytes of 64 columns of it
     static constexpr int SPAN = RP * 2;                        // bytes of a row of the factor, or of a part of t
     static constexpr int SPAN2 = SPAN == 128 ? 128 : 2 * SPAN; // of two parts of t side by side (ranks up to 32)
     static constexpr int BLOCKS = ag_blocks(RP);               // tiles of a slab at most
     static constexpr int TILE = 2 * SUB;
     static constexpr int FACTORS = (RP == 16 && HOW == COPY ? 2 : 1) * BLOCKS * BC * SPAN;   // bytes for factors: two where they fit
-    static constexpr int TT = PARTS * STEP * SPAN;
-    static constexpr int TS = RP == 64 && HOW != COPY ? 1 : 2;
+    static constexpr int TT = (RP <= 32 ? 4 : PARTS) * STEP * SPAN;
+    static constexpr int TS = RP == 64 && PLANES == 1 ? 1 : 2;
     static constexpr int REST = AG_SMEM - 2048 - FACTORS - TS * TT;
     // not COPY: rows on their way to the warps that rewrite them, 32 NR in a batch
     static constexpr int SROW = BC * static_cast<int>(sizeof(T)) + (HOW == ANY ? 16 : 0);
-    static constexpr int NR = 2, BATCH = NR * 32 * SROW;
+    static constexpr int NR = PLANES == 2 ? 2 : 1, BATCH = NR * 32 * SROW;
     static constexpr int FIT = (REST - 2 * TILE) / BATCH, BATCHES = FIT < 4 ? FIT : 4;
     static constexpr int STAGING = HOW == COPY ? 0 : BATCHES * BATCH;
     static constexpr int STAGES = (REST - STAGING) / TILE < 4 ? (REST - STAGING) / TILE : 4;
@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(Shape<T, HOW, RP>::THREADS, 1)
     const int blocks = (min(a.V, c0 + a.cols) - c0 + BC - 1) / BC;
     // two factors, and dB's sums of two adapters, where a slab's are small enough
     const int factor_bytes = a.cols * S::SPAN, num_factors = 2 * factor_bytes <= S::FACTORS ? 2 : 1;
-    // t's two parts side by side as one operand (N = 2 RP, their products in columns of their own) where TMEM has room
+    // t's first two parts side by side as one operand (N = 2 RP, the second's products in columns of their own) where TMEM has room
     const int db_block = a.merged ? 2 * RP : RP, db_columns = a.cols / BC * db_block, num_db = 2 * RP + 2 * db_columns <= 512 ? 2 : 1;
     if (tid == 0) {
         for (int i = 0; i < S::STAGES; ++i) {
@@ -232,10 +232,12 @@ __global__ void __launch_bounds__(Shape<T, HOW, RP>::THREADS, 1)
                 if (!warp_wait(tempty(tr.slot), tr.parity ^ 1u, abort_flag, budget))
                     return false;
                 if (lane == 0) {
-                    mbar_arrive_expect_tx(tfull(tr.slot), S::TT);
-                    for (int i = 0; i < (a.merged ? 1 : PARTS); ++i)   // merged: one box of both
-                        tma_load_2d(ts + tr.slot * S::TT + i * STEP * S::SPAN, &map_t, tfull(tr.slot), i * a.RT + a.r0,
-                                    p + ad * AG_PAD, pol_keep);
+                    mbar_arrive_expect_tx(tfull(tr.slot), (a.merged ? 4 : PARTS) * STEP * S::SPAN);
+                    // part by part; or the first two side by side, then the third beside zeros (past t's last column)
+                    const int boxes = a.merged ? 2 : PARTS, width = a.merged ? 2 * RP : RP;
+                    for (int i = 0; i < boxes; ++i)
+                        tma_load_2d(ts + tr.slot * S::TT + i * STEP * width * 2, &map_t, tfull(tr.slot),
+                                    a.merged ? i * width : i * a.RT + a.r0, p + ad * AG_PAD, pol_keep);
                 }
                 used_t |= 1u << tr.slot;
                 par_t = (par_t & ~(1u << tr.slot)) | (tr.parity << tr.slot);
@@ -260,7 +262,7 @@ __global__ void __launch_bounds__(Shape<T, HOW, RP>::THREADS, 1)
         Ring st(S::STAGES), tr(S::TS), fr(num_factors), du(2), db(num_db);
         constexpr uint32_t KHI = static_cast<uint32_t>(desc_kmajor_hi()), MHI = static_cast<uint32_t>(desc_mnmajor_hi());
         // du += tile x factor, 16 columns at a time, and dB += tile^T x t, 16 rows at a time,
-        // in turn (neither waits for itself); lo lo is of the size of what the parts leave
+        // in turn (neither waits for itself); products of parts below 2^-16 of the first's are left out
         auto tile_products = [&](auto merged, auto whole, uint32_t tile, uint32_t td, uint32_t tb, uint32_t fd, uint32_t tt,
                                  int steps, uint32_t first_du, uint32_t first_db) {
             constexpr bool MERGED = decltype(merged)::value, WHOLE = decltype(whole)::value;
@@ -271,12 +273,20 @@ __global__ void __launch_bounds__(Shape<T, HOW, RP>::THREADS, 1)
                 umma_bf16_lead(lead, td, (a0 | 1u << 16) + (k / 4) * (SUB / 16) + 2 * (k % 4), KHI,
                                fd + k * S::SPAN, desc_span_hi(S::SPAN), IDESC_DU, k == 0 ? first_du : 1u);
                 const int kr = k % (STEP / 16), plane = k / (STEP / 16);
-                if (WHOLE || kr < steps) {
+                if (plane < S::PLANES && (WHOLE || kr < steps)) {
                     const uint32_t more = k == 0 ? first_db : 1u;
                     umma_bf16_lead(lead, tb, am + 128 * k, MHI, tt + kr * TSPAN, desc_span_hi(TSPAN), MERGED ? IDESC_DB2 : IDESC_DB,
                                    more);
-                    if (!MERGED && plane == 0)
-                        umma_bf16_lead(lead, tb, am + 128 * k, MHI, tt + (STEP / 16 + kr) * TSPAN, desc_span_hi(TSPAN), IDESC_DB, 1u);
+                    if (MERGED) {
+                        if (plane == 0)
+                            umma_bf16_lead(lead, tb, am + 128 * k, MHI, tt + (STEP / 16 + kr) * TSPAN, desc_span_hi(TSPAN), IDESC_DB,
+                                           1u);
+                    } else {
+#pragma unroll
+                        for (int j = 1; j < PARTS - plane; ++j)
+                            umma_bf16_lead(lead, tb, am + 128 * k, MHI, tt + (j * STEP / 16 + kr) * TSPAN, desc_span_hi(TSPAN),
+                                           IDESC_DB, 1u);
+                    }
                 }
             }
         };
@@ -365,7 +375,7 @@ __global__ void __launch_bounds__(Shape<T, HOW, RP>::THREADS, 1)
                     float v[RC];
                     __syncwarp();
                     tmem_row<RC>(mine + du.slot * RP + r0, v);
-                    if (at < e) {
+                    if (at < e && m / STEP < S::PLANES) {
 #pragma unroll
                         for (int r = 0; r < RC / 4; ++r)
                             o[(r0 / 4 + r) * count] = make_float4(v[4 * r], v[4 * r + 1], v[4 * r + 2], v[4 * r + 3]);
@@ -744,19 +754,29 @@ template <int RT> __device__ __forceinline__ void dA_part(const AdapterGradArgs 
         __syncthreads();   // the chunk is there; the one before has been read
         fill(stage == 0 ? S::STAGES - 1 : stage - 1, p + (S::STAGES - 1) * ROWS);
         const uint32_t h0 = ring0 + stage * S::STAGE, u0 = h0 + ROWS * HROW;
+        // a chunk's sums by themselves, then added: the tensor cores cut, rather than round,
+        // what they add up, and a long chain of that leans to one side
+        uint32_t x[ROWS / 16][4];   // k = rows, n = the warp's 16 columns
 #pragma unroll
-        for (int k = 0; k < ROWS; k += 16) {
-            uint32_t x[4];   // k = rows, n = the warp's 16 columns
-            ldsm4t(x, h0 + (k + (lane & 15)) * HROW + (warp * 16 + (lane >> 4) * 8) * 2);
+        for (int k = 0; k < ROWS / 16; ++k)
+            ldsm4t(x[k], h0 + (k * 16 + (lane & 15)) * HROW + (warp * 16 + (lane >> 4) * 8) * 2);
 #pragma unroll
-            for (int i = 0; i < 3; ++i)
+        for (int m = 0; m < RM; ++m) {
+            float part[2][4] = {};
 #pragma unroll
-                for (int m = 0; m < RM; ++m) {
+            for (int k = 0; k < ROWS / 16; ++k)
+#pragma unroll
+                for (int i = 0; i < 3; ++i) {
                     uint32_t u[4];   // ranks as rows
-                    ldsm4t(u, u0 + (k + (lane & 7) + (lane >> 4) * 8) * UROW + (i * RT + m * 16 + ((lane >> 3) & 1) * 8) * 2);
-                    mma16816(acc[m][0], u, x[0], x[1]);
-                    mma16816(acc[m][1], u, x[2], x[3]);
+                    ldsm4t(u, u0 + (k * 16 + (lane & 7) + (lane >> 4) * 8) * UROW + (i * RT + m * 16 + ((lane >> 3) & 1) * 8) * 2);
+                    mma16816(part[0], u, x[k][0], x[k][1]);
+                    mma16816(part[1], u, x[k][2], x[k][3]);
                 }
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    acc[m][j][k] += part[j][k];
         }
         stage = stage + 1 == S::STAGES ? 0 : stage + 1;
     }

@@ -243,7 +243,7 @@ int tim_adapter_logits_backward(const void *dlogits, int dtype, int64_t N, int64
     const size_t b_off = tim::ws_round(sizeof(int32_t) * (static_cast<size_t>(n) + 2));
     const size_t b_n = tim::ws_round(sizeof(int32_t) * static_cast<size_t>(N));
     const size_t t_rows = static_cast<size_t>(N) + static_cast<size_t>(n) * tim::AG_PAD;
-    const size_t b_t = tim::ws_round(t_rows * 2 * a.RT * 2);
+    const size_t b_t = tim::ws_round(t_rows * 3 * a.RT * 2);
     const size_t b_du = tim::ws_round(static_cast<size_t>(N) * 3 * a.RT * 2);
     const size_t b_part = static_cast<size_t>(per_row) * (a.row_part + 16);
     void *ws = nullptr;
@@ -255,7 +255,7 @@ int tim_adapter_logits_backward(const void *dlogits, int dtype, int64_t N, int64
     f.plan.adapter = reinterpret_cast<int32_t *>(w + b_off + b_n);
     w += b_off + 2 * b_n;
     f.plan.t = reinterpret_cast<uint16_t *>(w);
-    f.plan.t_pitch = 2 * a.RT;
+    f.plan.t_pitch = 3 * a.RT;
     f.plan.t_pad = tim::AG_PAD;
     a.plan = f.plan;
     a.du = reinterpret_cast<uint16_t *>(w + b_t);
@@ -263,15 +263,15 @@ int tim_adapter_logits_backward(const void *dlogits, int dtype, int64_t N, int64
     CUtensorMap maps[2];
     const uint64_t d_b[3] = {static_cast<uint64_t>(R), static_cast<uint64_t>(V), static_cast<uint64_t>(n)};
     const uint64_t s_b[2] = {static_cast<uint64_t>(R) * 2, static_cast<uint64_t>(V * R) * 2};
-    const uint64_t d_t[2] = {static_cast<uint64_t>(2 * a.RT), t_rows}, s_t[1] = {static_cast<uint64_t>(2 * a.RT) * 2};
+    const uint64_t d_t[2] = {static_cast<uint64_t>(3 * a.RT), t_rows}, s_t[1] = {static_cast<uint64_t>(3 * a.RT) * 2};
     const uint32_t box_b[3] = {static_cast<uint32_t>(RP), tim::AG_BLOCK, 1}, box_t[2] = {
-        static_cast<uint32_t>(a.merged ? 2 * RP : RP), static_cast<uint32_t>(128 / tim::ag_planes(dtype))};
+        static_cast<uint32_t>(a.merged ? 2 * RP : RP), static_cast<uint32_t>(tim::ag_step(dtype))};
     if ((rc = tim::encode_bf16_map(&maps[0], a.B, 3, d_b, s_b, box_b, 2 * RP)) != TIM_OK ||
         (rc = tim::encode_bf16_map(&maps[1], f.plan.t, 2, d_t, s_t, box_t, a.merged ? 4 * RP : 2 * RP)) != TIM_OK) {
         tim::workspace_free(ws, s);
         return rc;
     }
-    cudaError_t e = tim::adapters_shrink_launch(f, 2, sms, s);
+    cudaError_t e = tim::adapters_shrink_launch(f, 3, sms, s);
     if (e == cudaSuccess)
         e = tim::adapters_grad_launch(maps, a, dtype, sms, s);
     return finish(e, tim::workspace_free(ws, s), "adapter_logits_backward launch");

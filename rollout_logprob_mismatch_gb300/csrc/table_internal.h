@@ -26,7 +26,7 @@ inline size_t ws_round(size_t x) { return (x + 255) / 256 * 256; }
 // ---------------------------------------------------------------- adapters
 constexpr int AD_MAX_RANK = 128;
 constexpr int AD_MAX_ADAPTERS = 65535;
-constexpr int AD_SHRINK_THREADS = 512;
+constexpr int AD_SHRINK_THREADS = 256;
 constexpr int AD_FEW_ROWS = 1024;    // rows up to which they are ordered and projected in one launch
 constexpr int AD_MAP_THREADS = 288;  // eight warps of products, one of copies
 constexpr int AD_MAP_ROWS = 256;     // positions of a CTA of the map, at most
@@ -72,9 +72,10 @@ cudaError_t adapters_expand_launch(AdapterArgs a, int dtype, int num_sms, cudaSt
 cudaError_t adapters_prepare_device();   // shared-memory sizes
 
 // The gradient: slabs of the vocabulary, tiles of 128 columns and 128 rows of bf16, or of
-// 64 rows in two planes of bf16 parts.
+// 64 rows in two planes of bf16 parts (fp16), 32 rows in three (fp32).
 constexpr int AG_BLOCK = 128;
-constexpr int ag_planes(int dtype) { return dtype == TIM_BF16 ? 1 : 2; }
+constexpr int ag_planes(int dtype) { return dtype == TIM_BF16 ? 1 : dtype == TIM_F16 ? 2 : 3; }
+constexpr int ag_step(int dtype) { return 128 >> (ag_planes(dtype) - 1); }   // rows of a tile
 constexpr int AG_PAD = 16;           // t has room for so many rows of zeros behind each adapter's
 constexpr int AG_SMEM = 227 * 1024;
 constexpr int64_t AG_PARTIAL_BYTES = int64_t(1) << 30;   // du's partial sums at most, per part of the batch
@@ -92,7 +93,7 @@ struct AdapterGradArgs {
     int32_t RT;               // the rank padded (16, 32, 64, 128)
     int32_t aligned;          // every row of dy starts on 16 bytes
     int32_t cols, slabs;      // columns of a slab, slabs
-    int32_t merged;           // t's two parts are one operand
+    int32_t merged;           // t's first two parts are one operand
     int32_t du_parts;         // parts of a sum of du: slabs times planes
     int32_t row_part;         // positions of a launch
     int32_t p0, p1, r0;       // the launch's positions and first rank
