@@ -42,9 +42,8 @@ struct Own {
     int r0, r1, own, base, count, before;
 };
 
-__device__ __forceinline__ Own count_rows(const AdapterArgs &a, int ad)
+template <int WARPS> __device__ __forceinline__ Own count_rows(const AdapterArgs &a, int ad)
 {
-    constexpr int WARPS = AD_SHRINK_THREADS / 32;
     __shared__ int sb[WARPS], so[WARPS];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int per = ((a.N + 31) / 32 + WARPS - 1) / WARPS * 32;
@@ -92,15 +91,15 @@ __device__ __forceinline__ void write_order(const AdapterArgs &a, int ad, const 
 }
 
 // t of up to 16 rows under adapter ad, written for rows lo .. hi - 1 of them at positions
-// pos + lo ..  The eight warps share k (every eighth 32 of it each) and add up through shared
-// memory in their order, so that a row's sum depends on D alone.  AHEAD: steps of 32 k
-// whose loads are in flight together.
-template <int RP, int PARTS, int AHEAD>
+// pos + lo ..  k is shared among 16 (every 16th 32 of it each: a warp is one of them, or
+// two), whose sums are added up through shared memory in their order, so that a row's sum
+// depends on D alone.  AHEAD: steps of 32 k whose loads are in flight together.
+template <int RP, int PARTS, int WARPS, int AHEAD>
 __device__ __forceinline__ void project(const AdapterArgs &a, int ad, const int32_t *rows, int lo, int hi, int pos)
 {
-    constexpr int WARPS = AD_SHRINK_THREADS / 32;
     constexpr int NC = RP < 32 ? RP : 32;      // rank columns at a time
-    __shared__ float sums[WARPS][16][NC + 1];
+    constexpr int EACH = 16 / WARPS;
+    __shared__ float sums[16][16][NC + 1];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
     const float scale = a.scale ? a.scale[ad] : 1.f;
     const uint16_t *A = a.A + static_cast<size_t>(ad) * a.R * a.D;
@@ -110,12 +109,12 @@ __device__ __forceinline__ void project(const AdapterArgs &a, int ad, const int3
     const uint16_t *h0 = a.h + static_cast<size_t>(on0 ? rows[g] : 0) * a.D;
     const uint16_t *h1 = a.h + static_cast<size_t>(on1 ? rows[g + 8] : 0) * a.D;
     for (int n0 = 0; n0 < RP; n0 += NC) {
-        float acc[NC / 8][4] = {};
+        float acc[EACH][NC / 8][4] = {};
         if (n0 < a.R) {
-            for (int kc0 = warp; kc0 < kchunks; kc0 += WARPS * AHEAD) {
-                uint4 x0[AHEAD], x1[AHEAD], w[AHEAD][NC / 8];
+            for (int kc0 = warp; kc0 < kchunks; kc0 += 16 * AHEAD) {
+                uint4 x0[AHEAD * EACH], x1[AHEAD * EACH], w[AHEAD * EACH][NC / 8];
 #pragma unroll
-                for (int i = 0; i < AHEAD; ++i) {
+                for (int i = 0; i < AHEAD * EACH; ++i) {
                     const int k = (kc0 + i * WARPS) * 32 + q * 8;   // D is a multiple of 8: the eight are in or out together
                     const bool in = k < a.D;
                     x0[i] = in && on0 ? __ldg(reinterpret_cast<const uint4 *>(h0 + k)) : zero;
@@ -127,28 +126,31 @@ __device__ __forceinline__ void project(const AdapterArgs &a, int ad, const int3
                     }
                 }
 #pragma unroll
-                for (int i = 0; i < AHEAD; ++i)
+                for (int i = 0; i < AHEAD * EACH; ++i)
 #pragma unroll
                     for (int j = 0; j < NC / 8; ++j) {
-                        mma16816(acc[j], {x0[i].x, x1[i].x, x0[i].y, x1[i].y}, w[i][j].x, w[i][j].y);
-                        mma16816(acc[j], {x0[i].z, x1[i].z, x0[i].w, x1[i].w}, w[i][j].z, w[i][j].w);
+                        mma16816(acc[i % EACH][j], {x0[i].x, x1[i].x, x0[i].y, x1[i].y}, w[i][j].x, w[i][j].y);
+                        mma16816(acc[i % EACH][j], {x0[i].z, x1[i].z, x0[i].w, x1[i].w}, w[i][j].z, w[i][j].w);
                     }
             }
         }
         __syncthreads();   // the sums before have been read
 #pragma unroll
-        for (int j = 0; j < NC / 8; ++j) {
-            sums[warp][g][j * 8 + 2 * q] = acc[j][0];
-            sums[warp][g][j * 8 + 2 * q + 1] = acc[j][1];
-            sums[warp][g + 8][j * 8 + 2 * q] = acc[j][2];
-            sums[warp][g + 8][j * 8 + 2 * q + 1] = acc[j][3];
-        }
+        for (int v = 0; v < EACH; ++v)
+#pragma unroll
+            for (int j = 0; j < NC / 8; ++j) {
+                float (&to)[16][NC + 1] = sums[warp + v * WARPS];
+                to[g][j * 8 + 2 * q] = acc[v][j][0];
+                to[g][j * 8 + 2 * q + 1] = acc[v][j][1];
+                to[g + 8][j * 8 + 2 * q] = acc[v][j][2];
+                to[g + 8][j * 8 + 2 * q + 1] = acc[v][j][3];
+            }
         __syncthreads();
-        for (int i = tid; i < (hi - lo) * NC; i += AD_SHRINK_THREADS) {
+        for (int i = tid; i < (hi - lo) * NC; i += WARPS * 32) {
             const int m = lo + i / NC, r = i % NC;
             float u = 0.f;
 #pragma unroll
-            for (int w = 0; w < WARPS; ++w)
+            for (int w = 0; w < 16; ++w)
                 u += sums[w][m][r];
             uint16_t p[PARTS];
             split_bf16<PARTS>(u * scale, p);
@@ -167,20 +169,20 @@ __device__ __forceinline__ void pad_rows(const AdapterArgs &a, int ad, int count
         return;
     const int words = (-count & (AG_PAD - 1)) * (a.plan.t_pitch / 2);
     uint32_t *t = reinterpret_cast<uint32_t *>(a.plan.t + (static_cast<size_t>(end) + static_cast<size_t>(ad) * a.plan.t_pad) * a.plan.t_pitch);
-    for (int i = threadIdx.x; i < words; i += AD_SHRINK_THREADS)
+    for (int i = threadIdx.x; i < words; i += blockDim.x)
         t[i] = 0u;
 }
 
 // Few rows, one launch.  CTA (a, y): the rows of adapter a, 16 at a time from the y-th 16
 // on; a = n: the rows under no adapter (only ordered).
 template <int RP, int PARTS>
-__global__ void __launch_bounds__(AD_SHRINK_THREADS, 2) adapters_shrink_kernel(const AdapterArgs a)
+__global__ void __launch_bounds__(256, 2) adapters_shrink_kernel(const AdapterArgs a)
 {
     __shared__ int32_t mine[16];
     const int ad = blockIdx.x;
     pdl_wait();
     pdl_launch_dependents();
-    const Own o = count_rows(a, ad);
+    const Own o = count_rows<8>(a, ad);
     if (blockIdx.y == 0)
         write_order(a, ad, o);
     if (ad == a.n)
@@ -193,7 +195,7 @@ __global__ void __launch_bounds__(AD_SHRINK_THREADS, 2) adapters_shrink_kernel(c
                     mine[p - c0] = r;
             });
         __syncthreads();
-        project<RP, PARTS, 4>(a, ad, mine, 0, rows, o.base + c0);
+        project<RP, PARTS, 8, 2>(a, ad, mine, 0, rows, o.base + c0);
         if (c0 + rows == o.count)
             pad_rows(a, ad, o.count, o.base + o.count);
         __syncthreads();
@@ -201,16 +203,16 @@ __global__ void __launch_bounds__(AD_SHRINK_THREADS, 2) adapters_shrink_kernel(c
 }
 
 // Many rows: the order in a launch of its own, then a CTA for every 16 positions.
-__global__ void __launch_bounds__(AD_SHRINK_THREADS) adapters_order_kernel(const AdapterArgs a)
+__global__ void __launch_bounds__(512) adapters_order_kernel(const AdapterArgs a)
 {
     pdl_wait();
     pdl_launch_dependents();
-    const Own o = count_rows(a, blockIdx.x);
+    const Own o = count_rows<16>(a, blockIdx.x);
     write_order(a, blockIdx.x, o);
 }
 
 template <int RP, int PARTS>
-__global__ void __launch_bounds__(AD_SHRINK_THREADS, 4) adapters_project_kernel(const AdapterArgs a)
+__global__ void __launch_bounds__(512, 2) adapters_project_kernel(const AdapterArgs a)
 {
     __shared__ int32_t s_row[16], s_ad[17];
     pdl_wait();
@@ -229,7 +231,7 @@ __global__ void __launch_bounds__(AD_SHRINK_THREADS, 4) adapters_project_kernel(
         int m = s + 1;
         while (s_ad[m] == s_ad[s])
             ++m;
-        project<RP, PARTS, RP == 16 ? 2 : 1>(a, s_ad[s], s_row, s, m, p0);
+        project<RP, PARTS, 16, RP == 16 ? 2 : 1>(a, s_ad[s], s_row, s, m, p0);
         const int ad = s_ad[s], e = a.plan.offsets[ad + 1];
         if (p0 + m == e)
             pad_rows(a, ad, e - a.plan.offsets[ad], e);
@@ -585,15 +587,14 @@ cudaError_t launch(F kernel, dim3 grid, int threads, int smem, const AdapterArgs
 template <int RP, int PARTS> cudaError_t shrink(const AdapterArgs &a, int num_sms, cudaStream_t s)
 {
     if (a.N > AD_FEW_ROWS) {
-        const cudaError_t e = launch(adapters_order_kernel, dim3(static_cast<unsigned>(a.n + 1)), AD_SHRINK_THREADS, 0, a, s);
+        const cudaError_t e = launch(adapters_order_kernel, dim3(static_cast<unsigned>(a.n + 1)), 512, 0, a, s);
         if (e != cudaSuccess)
             return e;
-        return launch(adapters_project_kernel<RP, PARTS>, dim3(static_cast<unsigned>((a.N + 15) / 16)), AD_SHRINK_THREADS, 0,
-                      a, s);
+        return launch(adapters_project_kernel<RP, PARTS>, dim3(static_cast<unsigned>((a.N + 15) / 16)), 512, 0, a, s);
     }
     const int ys = std::max(1, std::min((a.N + 15) / 16, (2 * num_sms + a.n) / (a.n + 1)));
     return launch(adapters_shrink_kernel<RP, PARTS>, dim3(static_cast<unsigned>(a.n + 1), static_cast<unsigned>(ys)),
-                  AD_SHRINK_THREADS, 0, a, s);
+                  256, 0, a, s);
 }
 
 template <int PARTS> cudaError_t shrink(const AdapterArgs &a, int num_sms, cudaStream_t s)

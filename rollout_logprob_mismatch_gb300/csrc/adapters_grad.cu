@@ -278,9 +278,9 @@ __global__ void __launch_bounds__(Shape<T, HOW, RP>::THREADS, 1)
                     umma_bf16_lead(lead, tb, am + 128 * k, MHI, tt + kr * TSPAN, desc_span_hi(TSPAN), MERGED ? IDESC_DB2 : IDESC_DB,
                                    more);
                     if (MERGED) {
-                        if (plane == 0)
-                            umma_bf16_lead(lead, tb, am + 128 * k, MHI, tt + (STEP / 16 + kr) * TSPAN, desc_span_hi(TSPAN), IDESC_DB,
-                                           1u);
+                        if (plane == 0)   // the third part's beside the second's: the chain of the first is shorter
+                            umma_bf16_lead(lead, tb + RP, am + 128 * k, MHI, tt + (STEP / 16 + kr) * TSPAN, desc_span_hi(TSPAN),
+                                           IDESC_DB, 1u);
                     } else {
 #pragma unroll
                         for (int j = 1; j < PARTS - plane; ++j)
@@ -639,11 +639,11 @@ __global__ void __launch_bounds__(Shape<T, HOW, RP>::THREADS, 1)
 
 // ---------------------------------------------------------------- fold
 // du of a part's positions, ranks r0 .. r0 + RP - 1: the slabs' parts added in slab
-// order by eight threads (slabs k, k + 8, ... each, then joined in order), times scale,
+// order by 16 threads (slabs k, k + 16, ... each, then joined in order), times scale,
 // in three bf16 parts.
 template <int RP> __global__ void __launch_bounds__(256) adapters_fold_kernel(const AdapterGradArgs a)
 {
-    constexpr int SHARE = 8, ITEMS = 256 / SHARE;
+    constexpr int SHARE = 16, ITEMS = 256 / SHARE;
     __shared__ float4 sums[SHARE][ITEMS];
     const int item = threadIdx.x % ITEMS, k = threadIdx.x / ITEMS;
     const int64_t count = a.p1 - a.p0 + 16;   // a part may end up to 15 positions past p1
@@ -1009,7 +1009,7 @@ cudaError_t adapters_grad_launch(const CUtensorMap (&maps)[2], AdapterGradArgs a
             if (e != cudaSuccess)
                 return e;
             const int64_t items = static_cast<int64_t>(a.p1 - a.p0 + 16) * (RP / 4);
-            const dim3 grid(static_cast<unsigned>((items + 31) / 32));
+            const dim3 grid(static_cast<unsigned>((items + 15) / 16));
             e = RP == 16   ? launch(adapters_fold_kernel<16>, grid, 256, 0, a, s)
                 : RP == 32 ? launch(adapters_fold_kernel<32>, grid, 256, 0, a, s)
                            : launch(adapters_fold_kernel<64>, grid, 256, 0, a, s);

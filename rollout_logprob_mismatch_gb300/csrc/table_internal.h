@@ -26,8 +26,7 @@ inline size_t ws_round(size_t x) { return (x + 255) / 256 * 256; }
 // ---------------------------------------------------------------- adapters
 constexpr int AD_MAX_RANK = 128;
 constexpr int AD_MAX_ADAPTERS = 65535;
-constexpr int AD_SHRINK_THREADS = 256;
-constexpr int AD_FEW_ROWS = 1024;    // rows up to which they are ordered and projected in one launch
+constexpr int AD_FEW_ROWS = 256;     // rows up to which they are ordered and projected in one launch
 constexpr int AD_MAP_THREADS = 288;  // eight warps of products, one of copies
 constexpr int AD_MAP_ROWS = 256;     // positions of a CTA of the map, at most
 constexpr int AD_MAP_SMEM = 224 * 1024;   // beside the lists of its rows
