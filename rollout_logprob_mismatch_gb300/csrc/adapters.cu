@@ -202,7 +202,8 @@ __global__ void __launch_bounds__(256, 2) adapters_shrink_kernel(const AdapterAr
     }
 }
 
-// Many rows: the order in a launch of its own, then a CTA for every 16 positions.
+// Many rows: the order in a launch of its own, then a CTA for every 16 positions (two an SM
+// where there are that many, else one with more loads in flight).
 __global__ void __launch_bounds__(512) adapters_order_kernel(const AdapterArgs a)
 {
     pdl_wait();
@@ -211,8 +212,8 @@ __global__ void __launch_bounds__(512) adapters_order_kernel(const AdapterArgs a
     write_order(a, blockIdx.x, o);
 }
 
-template <int RP, int PARTS>
-__global__ void __launch_bounds__(512, 2) adapters_project_kernel(const AdapterArgs a)
+template <int RP, int PARTS, bool MANY>
+__global__ void __launch_bounds__(512, MANY ? 2 : 1) adapters_project_kernel(const AdapterArgs a)
 {
     __shared__ int32_t s_row[16], s_ad[17];
     pdl_wait();
@@ -231,7 +232,7 @@ __global__ void __launch_bounds__(512, 2) adapters_project_kernel(const AdapterA
         int m = s + 1;
         while (s_ad[m] == s_ad[s])
             ++m;
-        project<RP, PARTS, 16, RP == 16 ? 2 : 1>(a, s_ad[s], s_row, s, m, p0);
+        project<RP, PARTS, 16, MANY ? (RP == 16 ? 2 : 1) : 4>(a, s_ad[s], s_row, s, m, p0);
         const int ad = s_ad[s], e = a.plan.offsets[ad + 1];
         if (p0 + m == e)
             pad_rows(a, ad, e - a.plan.offsets[ad], e);
@@ -590,7 +591,9 @@ template <int RP, int PARTS> cudaError_t shrink(const AdapterArgs &a, int num_sm
         const cudaError_t e = launch(adapters_order_kernel, dim3(static_cast<unsigned>(a.n + 1)), 512, 0, a, s);
         if (e != cudaSuccess)
             return e;
-        return launch(adapters_project_kernel<RP, PARTS>, dim3(static_cast<unsigned>((a.N + 15) / 16)), 512, 0, a, s);
+        const int ctas = (a.N + 15) / 16;
+        return launch(ctas > num_sms ? adapters_project_kernel<RP, PARTS, true> : adapters_project_kernel<RP, PARTS, false>,
+                      dim3(static_cast<unsigned>(ctas)), 512, 0, a, s);
     }
     const int ys = std::max(1, std::min((a.N + 15) / 16, (2 * num_sms + a.n) / (a.n + 1)));
     return launch(adapters_shrink_kernel<RP, PARTS>, dim3(static_cast<unsigned>(a.n + 1), static_cast<unsigned>(ys)),

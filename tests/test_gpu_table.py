@@ -5,10 +5,9 @@ Tolerances, element by element, from the arithmetic (half = half a unit of the l
 place of a type, relative: 2^-24, 2^-8, 2^-11 for fp32, bf16, fp16):
   * a product of k steps of 16 on the tensor cores adds at most (k + 8) 2^-23 of the
     sum of its terms' magnitudes (each step rounds, or cuts, the running sum);
-  * t is held in two bf16 parts for 16-bit logits and in the gradient (2^-16 of it is
-    left at most: each part leaves half a unit, 2^-8), in three for fp32 logits and du (2^-24);
-  * fp32 logits' gradients are held in two parts, and the product of the two rests is
-    left out (2^-16 each).
+  * t is held in two bf16 parts for 16-bit logits (2^-16 of it is left at most: each
+    part leaves half a unit, 2^-8), in three for fp32 logits and in the gradient, and so
+    are fp32 dlogits and du (2^-24; products of parts of that size are left out).
 """
 import math
 
@@ -56,7 +55,7 @@ def parts64(h, ad, rows):
         i = torch.nonzero(rows == k).view(-1)
         t[i] = s[i] * (h[i].to(F64) @ ad.A[k].to(F64).t())
         m[i] = s[i] * (h[i].to(F64).abs() @ ad.A[k].to(F64).abs().t())
-    # a warp's chain: two steps for every fourth 32 columns at least, then up to 16 warps' parts
+    # a chain: two steps for every 16th 32 columns, then 16 shares
     return t, m * ((D + 31) // 32 / 2 + 24) * U
 
 
@@ -140,6 +139,19 @@ def test_a_row_has_the_same_bits_whatever_rows_are_beside_it():
     assert torch.equal(bits(again), bits(out[perm]))
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_a_rows_bits_are_those_of_larger_batches(dtype):
+    """Batches that are ordered and projected in one launch, in two, and in two with
+    more CTAs than SMs."""
+    z, h, ad, rows = draw(6000, 700, 520, 40, 5, dtype, 15)
+    out = tim.adapter_logits(z, h, ad, rows)
+    for n in (1, 40, 256, 257, 2000):
+        part = tim.adapter_logits(z[:n], h[:n], ad, rows[:n])
+        assert torch.equal(bits(part), bits(out[:n])), n
+    y, tol = logits64(z, h, ad, rows, dtype)
+    check(out, y, tol)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_one_tenants_infinities_reach_no_other(dtype):
     z, h, ad, rows = draw(64, 900, 64, 16, 6, dtype, 4)
@@ -204,7 +216,7 @@ def grads64(dy, h, ad, rows, dtype):
     N, V = dy.shape
     d, x = dy.to(F64), h.to(F64)
     t, dt = parts64(h, ad, rows)
-    left = 2.0 ** -16 + (2.0 ** -15 if dtype == "f32" else 2.0 ** -16 if dtype == "f16" else 0)
+    left = 5 * 2.0 ** -24   # t's and dlogits' third parts, three products of parts
     z = lambda *s: torch.zeros(s, dtype=F64, device=dy.device)   # noqa: E731
     dh, th, dA, tA, dB, tB = z(N, D), z(N, D), z(n, R, D), z(n, R, D), z(n, V, R), z(n, V, R)
     s = torch.ones(n, dtype=F64, device=dy.device) if ad.scale is None else ad.scale.to(F64)
@@ -216,7 +228,7 @@ def grads64(dy, h, ad, rows, dtype):
         tB[k] = d[i].abs().t() @ (t[i].abs() * (left + (m / 4 + 16) * U) + dt[i])
         du = s[k] * (d[i] @ B)
         # steps of a slab, slabs by eight, eight parts: far fewer than V / 16
-        tu = s[k] * (d[i].abs() @ B.abs()) * ((2.0 ** -16 if dtype == "f32" else 0) + (96 + V / 1024) * U)
+        tu = s[k] * (d[i].abs() @ B.abs()) * (96 + V / 1024) * U
         dA[k] = du.t() @ x[i]
         tA[k] = (tu + du.abs() * (m / 4 + 16) * U).t() @ x[i].abs()
         dh[i] = du @ A
@@ -273,7 +285,7 @@ def test_gradient_of_a_batch_in_parts():
         i = torch.nonzero(rows == k).view(-1)
         t, dt = parts64(h[i], tim.Adapters(A[k:k + 1], B[k:k + 1]), torch.zeros_like(rows[i]))
         steps = i.numel() / 8 + 16
-        tt = t.abs() * (2.0 ** -16 + 2 * steps * U) + dt
+        tt = t.abs() * 2 * steps * U + dt
         wB, mB = torch.zeros((V, R), dtype=F64, device="cuda"), torch.zeros((V, R), dtype=F64, device="cuda")
         du = torch.empty((i.numel(), R), dtype=F64, device="cuda")
         mu = torch.empty_like(du)
@@ -447,7 +459,7 @@ def test_a_tied_head_with_adapters_as_it_is_trained():
     wW = W1.grad.index_add(0, tokens.long().clamp(min=0), torch.where(live_t, h64.grad * s, 0.0))
     rel = lambda x, y: float((x.to(F64) - y).norm() / y.norm())   # noqa: E731
     # fp32 logits of size up to some 30 hold 2^-24 of it, and so do lse and the
-    # probabilities' exponents: 1e-5 of a probability; dz goes on in two parts (2^-16)
+    # probabilities' exponents: 1e-5 of a probability
     assert float((logp.to(F64) - want.detach()).abs().max()) <= 2e-5
     for got, ref in ((dh, h64.grad), (dA, A1.grad), (dB, B1.grad), (dW, wW)):
         assert rel(got, ref) <= 6e-5
