@@ -129,8 +129,13 @@ __device__ __forceinline__ void project(const AdapterArgs &a, int ad, const int3
                 for (int i = 0; i < AHEAD * EACH; ++i)
 #pragma unroll
                     for (int j = 0; j < NC / 8; ++j) {
-                        mma16816(acc[i % EACH][j], {x0[i].x, x1[i].x, x0[i].y, x1[i].y}, w[i][j].x, w[i][j].y);
-                        mma16816(acc[i % EACH][j], {x0[i].z, x1[i].z, x0[i].w, x1[i].w}, w[i][j].z, w[i][j].w);
+                        // 32 k by themselves, then added: the tensor cores cut, rather than round, what they add up
+                        float part[4] = {};
+                        mma16816(part, {x0[i].x, x1[i].x, x0[i].y, x1[i].y}, w[i][j].x, w[i][j].y);
+                        mma16816(part, {x0[i].z, x1[i].z, x0[i].w, x1[i].w}, w[i][j].z, w[i][j].w);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            acc[i % EACH][j][k] += part[k];
                     }
             }
         }

@@ -59,6 +59,8 @@ template <typename T, int HOW, int RP> struct Shape {
     static constexpr int WRITERS = HOW == COPY ? 8 : 16;       // warps that bring tiles
     static constexpr int THREADS = (6 + WRITERS) * 32;
     static constexpr uint32_t TMEM = 512;                      // du twice, dB's blocks
+    static constexpr int CHAIN = 4;                            // tiles of a sum of du in TMEM
+    static_assert(RP <= 32 || CHAIN >= BLOCKS, "ranks beyond 32 are not added up in registers");
     static_assert(STAGES >= 2 && BATCHES >= 2 && (2 + BLOCKS) * RP <= 512, "shared memory, TMEM");
 };
 
@@ -165,7 +167,8 @@ __global__ void __launch_bounds__(Shape<T, HOW, RP>::THREADS, 1)
     // two factors, and dB's sums of two adapters, where a slab's are small enough
     const int factor_bytes = a.cols * S::SPAN, num_factors = 2 * factor_bytes <= S::FACTORS ? 2 : 1;
     // t's first two parts side by side as one operand (N = 2 RP, the second's products in columns of their own) where TMEM has room
-    const int db_block = a.merged ? 2 * RP : RP, db_columns = a.cols / BC * db_block, num_db = 2 * RP + 2 * db_columns <= 512 ? 2 : 1;
+    const int db_block = a.merged ? 2 * RP : RP, db_chain = a.cols / BC * db_block;
+    const int db_columns = (a.chains + a.low) * db_chain, num_db = 2 * RP + 2 * db_columns <= 512 ? 2 : 1;
     if (tid == 0) {
         for (int i = 0; i < S::STAGES; ++i) {
             mbar_init(full(i), HOW == COPY ? S::WRITERS * 32 : S::WRITERS);
@@ -262,9 +265,11 @@ __global__ void __launch_bounds__(Shape<T, HOW, RP>::THREADS, 1)
         Ring st(S::STAGES), tr(S::TS), fr(num_factors), du(2), db(num_db);
         constexpr uint32_t KHI = static_cast<uint32_t>(desc_kmajor_hi()), MHI = static_cast<uint32_t>(desc_mnmajor_hi());
         // du += tile x factor, 16 columns at a time, and dB += tile^T x t, 16 rows at a time,
-        // in turn (neither waits for itself); products of parts below 2^-16 of the first's are left out
-        auto tile_products = [&](auto merged, auto whole, uint32_t tile, uint32_t td, uint32_t tb, uint32_t fd, uint32_t tt,
-                                 int steps, uint32_t first_du, uint32_t first_db) {
+        // in turn (neither waits for itself); products of parts below 2^-16 of the first's are left out.
+        // The first parts' products go to tb, all others to low: the tensor cores cut, rather
+        // than round, what they add up, and the chain of the first is as short as can be.
+        auto tile_products = [&](auto merged, auto whole, uint32_t tile, uint32_t td, uint32_t tb, uint32_t low, uint32_t fd,
+                                 uint32_t tt, int steps, uint32_t first_du, uint32_t first_db, uint32_t first_low) {
             constexpr bool MERGED = decltype(merged)::value, WHOLE = decltype(whole)::value;
             constexpr int TSPAN = MERGED ? S::SPAN2 : S::SPAN;
             const uint32_t a0 = tile >> 4, am = a0 | (static_cast<uint32_t>(SUB) >> 4) << 16;
@@ -275,17 +280,16 @@ __global__ void __launch_bounds__(Shape<T, HOW, RP>::THREADS, 1)
                 const int kr = k % (STEP / 16), plane = k / (STEP / 16);
                 if (plane < S::PLANES && (WHOLE || kr < steps)) {
                     const uint32_t more = k == 0 ? first_db : 1u;
-                    umma_bf16_lead(lead, tb, am + 128 * k, MHI, tt + kr * TSPAN, desc_span_hi(TSPAN), MERGED ? IDESC_DB2 : IDESC_DB,
-                                   more);
-                    if (MERGED) {
-                        if (plane == 0)   // the third part's beside the second's: the chain of the first is shorter
-                            umma_bf16_lead(lead, tb + RP, am + 128 * k, MHI, tt + (STEP / 16 + kr) * TSPAN, desc_span_hi(TSPAN),
-                                           IDESC_DB, 1u);
-                    } else {
+                    if (plane == 0)   // merged: part 1 of t beside it, whose columns are `low`
+                        umma_bf16_lead(lead, tb, am + 128 * k, MHI, tt + kr * TSPAN, desc_span_hi(TSPAN), MERGED ? IDESC_DB2 : IDESC_DB,
+                                       more);
 #pragma unroll
-                        for (int j = 1; j < PARTS - plane; ++j)
-                            umma_bf16_lead(lead, tb, am + 128 * k, MHI, tt + (j * STEP / 16 + kr) * TSPAN, desc_span_hi(TSPAN),
-                                           IDESC_DB, 1u);
+                    for (int j = plane > 0 ? 0 : MERGED ? 2 : 1; j < PARTS - plane; ++j) {
+                        // merged: parts 0 and 1 share rows of 2 RP, part 2 lies behind them
+                        const uint32_t at = MERGED ? (j == 2 ? (STEP / 16 + kr) * TSPAN : kr * TSPAN + j * (S::SPAN / 16))
+                                                   : (j * STEP / 16 + kr) * TSPAN;
+                        umma_bf16_lead(lead, low, am + 128 * k, MHI, tt + at, desc_span_hi(TSPAN), IDESC_DB,
+                                       !MERGED && k == 0 && j == 1 && low != tb ? first_low : 1u);
                     }
                 }
             }
@@ -298,40 +302,49 @@ __global__ void __launch_bounds__(Shape<T, HOW, RP>::THREADS, 1)
                 return false;
             const uint32_t fd = ((factors + fr.slot * factor_bytes) >> 4) | 1u << 16;
             const uint32_t tdb = tmem + 2 * RP + db.slot * db_columns;
+            int chain = 0;   // the steps' products go to dB's sums in turn
             for (int p = b; p < e; p += STEP) {
-                if (!warp_wait(tfull(tr.slot), tr.parity, abort_flag, budget) ||
-                    !warp_wait(duempty(du.slot), du.parity ^ 1u, abort_flag, budget))
+                if (!warp_wait(tfull(tr.slot), tr.parity, abort_flag, budget))
                     return false;
-                tc_fence_after();
                 const int steps = (min(STEP, e - p) + 15) / 16;   // of 16 rows
-                const uint32_t td = tmem + du.slot * RP, tt = ((ts + tr.slot * S::TT) >> 4) | 1u << 16;
+                const uint32_t tt = ((ts + tr.slot * S::TT) >> 4) | 1u << 16;
+                const uint32_t tdb0 = tdb + chain * db_chain, first_db = p >= b + a.chains * STEP, first_low = a.merged ? first_db : p != b;
+                const uint32_t low = a.merged ? RP : a.low ? (a.chains - chain) * db_chain : 0;
+                chain = chain + 1 == a.chains ? 0 : chain + 1;
                 for (int c = 0; c < blocks; ++c) {
+                    if (c % S::CHAIN == 0) {
+                        if (!warp_wait(duempty(du.slot), du.parity ^ 1u, abort_flag, budget))
+                            return false;
+                    }
+                    const uint32_t td = tmem + du.slot * RP;
                     if (!warp_wait(full(st.slot), st.parity, abort_flag, budget))
                         return false;
                     // the writers' shared memory for the products: the fence stands here, since a
                     // writer's would wait for its copies of later tiles too
                     fence_proxy_async_smem();
                     tc_fence_after();
-                    const uint32_t tile = tiles + st.slot * S::TILE, tb = tdb + c * db_block, f = fd + c * (BC * S::SPAN / 16);
-                    const uint32_t first_du = c != 0, first_db = p != b;
+                    const uint32_t tile = tiles + st.slot * S::TILE, f = fd + c * (BC * S::SPAN / 16);
+                    const uint32_t tb = tdb0 + c * db_block, first_du = c % S::CHAIN != 0;
                     if (a.merged) {
                         if (steps == STEP / 16)
-                            tile_products(yes, yes, tile, td, tb, f, tt, steps, first_du, first_db);
+                            tile_products(yes, yes, tile, td, tb, tb + low, f, tt, steps, first_du, first_db, first_low);
                         else
-                            tile_products(yes, no, tile, td, tb, f, tt, steps, first_du, first_db);
+                            tile_products(yes, no, tile, td, tb, tb + low, f, tt, steps, first_du, first_db, first_low);
                     } else {
                         if (steps == STEP / 16)
-                            tile_products(no, yes, tile, td, tb, f, tt, steps, first_du, first_db);
+                            tile_products(no, yes, tile, td, tb, tb + low, f, tt, steps, first_du, first_db, first_low);
                         else
-                            tile_products(no, no, tile, td, tb, f, tt, steps, first_du, first_db);
+                            tile_products(no, no, tile, td, tb, tb + low, f, tt, steps, first_du, first_db, first_low);
                     }
                     umma_commit_lead(lead, empty(st.slot));
                     st.next();
+                    if ((c + 1) % S::CHAIN == 0 || c + 1 == blocks) {
+                        umma_commit_lead(lead, dufull(du.slot));
+                        du.next();
+                    }
                 }
                 umma_commit_lead(lead, tempty(tr.slot));
-                umma_commit_lead(lead, dufull(du.slot));
                 tr.next();
-                du.next();
             }
             umma_commit_lead(lead, fempty(fr.slot));
             umma_commit_lead(lead, dbfull(db.slot));
@@ -355,37 +368,54 @@ __global__ void __launch_bounds__(Shape<T, HOW, RP>::THREADS, 1)
             const Part r(ob, oe, a.p0, a.p1);
             const int b = r.begin, e = r.end;
             const bool some = b < e;
+            const int chains = min(a.chains, (e - b + STEP - 1) / STEP);   // dB's sums that have something
             // an adapter whose rows began in an earlier part of the batch is added to; one
             // without rows is written (zeros) by the first part
             const bool add = a.accumulate || b > ob;
             if (!some && !(ob == oe && a.p0 == 0 && !a.accumulate))
                 continue;
             for (int p = b; p < e; p += STEP) {
-                ok = warp_wait(dufull(du.slot), du.parity, abort_flag, budget);
-                if (!ok)
-                    break;
-                tc_fence_after();
                 const int at = p + m % STEP;
                 // [part][four ranks][position]: a warp's rows lie together
                 const size_t count = a.p1 - a.p0 + 16;
                 float4 *o = reinterpret_cast<float4 *>(a.partial) +
                             static_cast<size_t>(blockIdx.x * S::PLANES + m / STEP) * (RP / 4) * count + (at - a.p0);
-#pragma unroll
-                for (int r0 = 0; r0 < RP; r0 += RC) {
-                    float v[RC];
-                    __syncwarp();
-                    tmem_row<RC>(mine + du.slot * RP + r0, v);
+                auto put = [&](int r0, const float (&v)[RC]) {
                     if (at < e && m / STEP < S::PLANES) {
 #pragma unroll
                         for (int r = 0; r < RC / 4; ++r)
                             o[(r0 / 4 + r) * count] = make_float4(v[4 * r], v[4 * r + 1], v[4 * r + 2], v[4 * r + 3]);
                     }
+                };
+                float sum[RC] = {};   // of the chains of a slab (more than one where RP = RC)
+                for (int c = 0; c < blocks; c += S::CHAIN) {
+                    ok = warp_wait(dufull(du.slot), du.parity, abort_flag, budget);
+                    if (!ok)
+                        break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int r0 = 0; r0 < RP; r0 += RC) {
+                        float v[RC];
+                        __syncwarp();
+                        tmem_row<RC>(mine + du.slot * RP + r0, v);
+                        if constexpr (RP == RC) {
+#pragma unroll
+                            for (int r = 0; r < RC; ++r)
+                                sum[r] += v[r];
+                        } else {
+                            put(r0, v);
+                        }
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(duempty(du.slot));
+                    du.next();
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(duempty(du.slot));
-                du.next();
+                if (!ok)
+                    break;
+                if (RP == RC)
+                    put(0, sum);
             }
             if (!ok)
                 break;
@@ -407,12 +437,20 @@ __global__ void __launch_bounds__(Shape<T, HOW, RP>::THREADS, 1)
                     if (some) {
                         __syncwarp();
                         tmem_row<RC>(tb + r0, v);
-                        if (RP <= 32 && a.merged) {
-                            float low[RC];
-                            tmem_row<RC>(tb + RP, low);
+                        auto add_up = [&](uint32_t from) {
+                            float x[RC];
+                            tmem_row<RC>(from, x);
 #pragma unroll
                             for (int r = 0; r < RC; ++r)
-                                v[r] += low[r];
+                                v[r] += x[r];
+                        };
+                        for (int i = 1; i < chains; ++i)
+                            add_up(tb + i * db_chain + r0);
+                        if (RP <= 32 && a.merged) {
+                            for (int i = 0; i < chains; ++i)
+                                add_up(tb + i * db_chain + RP);
+                        } else if (a.low) {
+                            add_up(tb + a.chains * db_chain + r0);
                         }
                     }
                     if (col >= a.V)
@@ -764,9 +802,9 @@ template <int RT> __device__ __forceinline__ void dA_part(const AdapterGradArgs 
         for (int m = 0; m < RM; ++m) {
             float part[2][4] = {};
 #pragma unroll
-            for (int k = 0; k < ROWS / 16; ++k)
+            for (int i = 2; i >= 0; --i)   // the smallest first, so that they are not cut off the large sum
 #pragma unroll
-                for (int i = 0; i < 3; ++i) {
+                for (int k = 0; k < ROWS / 16; ++k) {
                     uint32_t u[4];   // ranks as rows
                     ldsm4t(u, u0 + (k * 16 + (lane & 7) + (lane >> 4) * 8) * UROW + (i * RT + m * 16 + ((lane >> 3) & 1) * 8) * 2);
                     mma16816(part[0], u, x[k][0], x[k][1]);
@@ -867,7 +905,7 @@ template <int RT> __device__ __forceinline__ void dh_part(const AdapterGradArgs 
                 fetch(p);
             float acc[4][4] = {};
 #pragma unroll
-            for (int part = 0; part < 3; ++part)
+            for (int part = 2; part >= 0; --part)   // the smallest first
 #pragma unroll
                 for (int k = 0; k < KS; ++k)
 #pragma unroll

@@ -229,6 +229,10 @@ int tim_adapter_logits_backward(const void *dlogits, int dtype, int64_t N, int64
     a.cols = static_cast<int32_t>(per_slab * tim::AG_BLOCK);
     a.slabs = static_cast<int32_t>((blocks + per_slab - 1) / per_slab);
     a.merged = RP <= 32 && 2 * RP + per_slab * 2 * RP <= 512;
+    // dB's sums: as many (up to four) as TMEM has room for beside du, for two adapters where that leaves two
+    const int64_t columns = per_slab * (a.merged ? 2 : 1) * RP, fit = (512 - 2 * RP) / columns, sums = fit >= 4 ? fit / 2 : fit;
+    a.low = !a.merged && sums >= 2;   // merged: the low products have columns of their own already
+    a.chains = static_cast<int32_t>(std::min<int64_t>(sums - a.low, 4));
     a.du_parts = a.slabs * tim::ag_planes(dtype);
     const int64_t per_row = int64_t(4) * a.du_parts * RP;
     a.row_part = static_cast<int32_t>(std::min<int64_t>(

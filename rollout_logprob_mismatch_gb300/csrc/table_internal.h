@@ -93,6 +93,7 @@ struct AdapterGradArgs {
     int32_t aligned;          // every row of dy starts on 16 bytes
     int32_t cols, slabs;      // columns of a slab, slabs
     int32_t merged;           // t's first two parts are one operand
+    int32_t chains, low;      // sums of dB in TMEM that take steps of rows in turn; one more for the low products, or 0
     int32_t du_parts;         // parts of a sum of du: slabs times planes
     int32_t row_part;         // positions of a launch
     int32_t p0, p1, r0;       // the launch's positions and first rank
