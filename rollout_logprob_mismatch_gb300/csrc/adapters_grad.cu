@@ -288,7 +288,7 @@ __global__ void __launch_bounds__(Shape<T, HOW, RP>::THREADS, 1)
                         // merged: parts 0 and 1 share rows of 2 RP, part 2 lies behind them
                         const uint32_t at = MERGED ? (j == 2 ? (STEP / 16 + kr) * TSPAN : kr * TSPAN + j * (S::SPAN / 16))
                                                    : (j * STEP / 16 + kr) * TSPAN;
-                        umma_bf16_lead(lead, low, am + 128 * k, MHI, tt + at, desc_span_hi(TSPAN), IDESC_DB,
+                        umma_bf16_lead(lead, MERGED ? tb + RP : low, am + 128 * k, MHI, tt + at, desc_span_hi(TSPAN), IDESC_DB,
                                        !MERGED && k == 0 && j == 1 && low != tb ? first_low : 1u);
                     }
                 }
@@ -309,7 +309,7 @@ __global__ void __launch_bounds__(Shape<T, HOW, RP>::THREADS, 1)
                 const int steps = (min(STEP, e - p) + 15) / 16;   // of 16 rows
                 const uint32_t tt = ((ts + tr.slot * S::TT) >> 4) | 1u << 16;
                 const uint32_t tdb0 = tdb + chain * db_chain, first_db = p >= b + a.chains * STEP, first_low = a.merged ? first_db : p != b;
-                const uint32_t low = a.merged ? RP : a.low ? (a.chains - chain) * db_chain : 0;
+                const uint32_t low = a.low ? (a.chains - chain) * db_chain : 0;   // merged: beside the first part's columns
                 chain = chain + 1 == a.chains ? 0 : chain + 1;
                 for (int c = 0; c < blocks; ++c) {
                     if (c % S::CHAIN == 0) {
