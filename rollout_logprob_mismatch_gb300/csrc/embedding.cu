@@ -8,9 +8,9 @@
 // them, takes its own in order and orders those by counting, so that nothing has to be
 // cleared and no atomic decides an order.  Then every row of dW is written once, with
 // the sum of its tokens' gradients taken in the tokens' order; rows of many tokens are
-// summed in tiles of EM_TILE sorted positions first, so that one frequent id does not
-// hold one warp for the whole call.  The order of a row's sum depends on its tokens'
-// sorted positions alone: the same call gives the same bits.
+// summed in tiles of sorted positions first, so that one frequent id does not hold one
+// warp for the whole call.  The order of a row's sum depends on N and its tokens' sorted
+// positions alone: the same call gives the same bits.
 #include <algorithm>
 
 #include "logits_rows.cuh"
@@ -295,8 +295,8 @@ __device__ __forceinline__ void sum_positions(float (&acc)[EM_PIECES][8], const 
     }
 }
 
-// Two kinds of CTAs.  The first tile_ctas: tiles of EM_TILE sorted positions, a warp EM_COLS
-// columns of one: the part of a tile that belongs to an id of more than EM_LONG tokens is
+// Two kinds of CTAs.  The first tile_ctas: tiles of a.tile sorted positions, a warp EM_COLS
+// columns of one: the part of a tile that belongs to an id of more than a.many tokens is
 // summed into partial[tile][0] where the id goes on from the tile before, into
 // partial[tile][1] where it begins in the tile.  The others: zeros for the rows of dW that
 // no token has, EM_IDS rows a warp (nothing but stores, and a read of the offsets).
@@ -331,14 +331,14 @@ __global__ void __launch_bounds__(256, 2) embedding_tiles_kernel(const Embedding
     const int unit = static_cast<int>(blockIdx.x) * 8 + warp;
     const int tile = unit / column_blocks, col0 = unit % column_blocks * EM_COLS;
     const int total = a.offsets[a.V];
-    if (tile >= (total + EM_TILE - 1) / EM_TILE)
+    if (tile >= (total + a.tile - 1) / a.tile)
         return;
-    const int p0 = tile * EM_TILE, p1 = min(total, p0 + EM_TILE);
+    const int p0 = tile * a.tile, p1 = min(total, p0 + a.tile);
 #pragma unroll 1
-    for (int k = 0; k < 2; ++k) {   // an id of more than EM_TILE tokens is the tile's first or its last
+    for (int k = 0; k < 2; ++k) {   // an id of more than a tile's tokens is the tile's first or its last
         const int id = a.ids[k == 0 ? p0 : p1 - 1];
         const int b = a.offsets[id], e = a.offsets[id + 1];
-        if (e - b <= EM_LONG || (b >= p0) != (k == 1))
+        if (e - b <= a.many || (b >= p0) != (k == 1))
             continue;
         float acc[EM_PIECES][8] = {};
         sum_positions<T, VEC>(acc, a, max(p0, b), min(p1, e), col0);
@@ -371,15 +371,15 @@ template <typename T, bool VEC> __global__ void __launch_bounds__(256, 2) embedd
         const int id = __shfl_sync(0xffffffffu, my_id, from);
         const int b = u0 + from, e = __shfl_sync(0xffffffffu, my_e, from);
         float acc[EM_PIECES][8] = {};
-        if (e - b > EM_LONG) {
+        if (e - b > a.many) {
             // the first tile's partial is in slot 1 (the id begins in it), the others' in slot 0
-            const int t1 = (e + EM_TILE - 1) / EM_TILE;
-            for (int t = b / EM_TILE; t < t1; t += EM_AHEAD) {
+            const int t1 = (e + a.tile - 1) / a.tile;
+            for (int t = b / a.tile; t < t1; t += EM_AHEAD) {
                 Pieces<float, VEC> r[EM_AHEAD];
 #pragma unroll
                 for (int i = 0; i < EM_AHEAD; ++i)
                     if (t + i < t1)
-                        r[i].load(a.partial + (static_cast<size_t>(t + i) * 2 + ((t + i) * EM_TILE <= b)) * a.D, col0, a.D);
+                        r[i].load(a.partial + (static_cast<size_t>(t + i) * 2 + ((t + i) * a.tile <= b)) * a.D, col0, a.D);
 #pragma unroll
                 for (int i = 0; i < EM_AHEAD; ++i)
                     if (t + i < t1)
@@ -426,7 +426,7 @@ template <typename TW> cudaError_t lookup_to(const EmbeddingArgs &a, int out_dty
 template <typename T, bool VEC> cudaError_t sum(const EmbeddingArgs &a, cudaStream_t s)
 {
     const int blocks = (a.D + EM_COLS - 1) / EM_COLS;
-    const int64_t tiles = a.N > EM_LONG ? (a.N + EM_TILE - 1) / EM_TILE : 0;
+    const int64_t tiles = a.N > a.many ? (a.N + a.tile - 1) / a.tile : 0;
     const int64_t tile_ctas = (tiles * blocks + 7) / 8;
     const int64_t zero_ctas = a.accumulate ? 0 : (a.V + 8 * EM_IDS - 1) / (8 * EM_IDS);
     if (tile_ctas + zero_ctas > 0) {

@@ -113,8 +113,8 @@ cudaError_t adapters_grad_prepare_device();
 // ---------------------------------------------------------------- embedding
 constexpr int EM_RANGE = 512;        // ids that one CTA of the sort orders
 constexpr int EM_SORT_THREADS = 1024;
-constexpr int EM_TILE = 32;          // sorted positions of a partial sum of a long row
-constexpr int EM_LONG = 64;          // tokens of an id above which its row is summed in tiles
+constexpr int EM_TILE = 32;          // sorted positions of a partial sum of a long row, at least
+constexpr int EM_LONG = 64;          // tokens of an id above which its row is summed in tiles, at least
 constexpr int EM_IDS = 4;            // rows of the table that a warp looks at for zeros
 
 struct EmbeddingArgs {
@@ -129,7 +129,8 @@ struct EmbeddingArgs {
     int32_t *order;           // [N] tokens ordered by id (stable)
     int32_t *ids;             // [N] id of each sorted position
     int2 *staged;             // [N] scratch of the sort
-    float *partial;           // [ceil(N / EM_TILE)][2][D]
+    int32_t tile, many;       // positions of a tile; tokens of an id above which it is summed in tiles (>= tile)
+    float *partial;           // [ceil(N / tile)][2][D]
 };
 
 cudaError_t embedding_launch(const EmbeddingArgs &a, int dtype, int out_dtype, cudaStream_t s);

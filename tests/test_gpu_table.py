@@ -374,7 +374,8 @@ def tokens_like(kind, N, V, gen):
 
 @pytest.mark.parametrize("kind", ["uniform", "one", "few", "out", "text"])
 @pytest.mark.parametrize("N,V,D,dtype", [(1, 7, 8, "bf16"), (33, 1025, 40, "f32"), (65, 50, 257, "f16"),
-                                          (1000, 5000, 1032, "bf16"), (5000, 3000, 64, "bf16"), (2048, 512, 100, "f32")])
+                                          (1000, 5000, 1032, "bf16"), (5000, 3000, 64, "bf16"), (2048, 512, 100, "f32"),
+                                          (20001, 2000, 72, "bf16"), (70000, 700, 33, "f16")])
 def test_embedding_backward(kind, N, V, D, dtype):
     gen = torch.Generator(device="cuda").manual_seed(N)
     t = tokens_like(kind, N, V, gen)
@@ -385,8 +386,11 @@ def test_embedding_backward(kind, N, V, D, dtype):
     want = torch.zeros((V, D), dtype=F64, device="cuda").index_add_(0, t[on].long(), x)
     size = torch.zeros((V, D), dtype=F64, device="cuda").index_add_(0, t[on].long(), x.abs())
     count = torch.zeros(V, dtype=F64, device="cuda").index_add_(0, t[on].long(), torch.ones_like(on, dtype=F64))
-    # a chain of at most 64 tokens, or 32 and then the tiles; and the product with the scale
-    chain = torch.where(count <= 64, count, 32 + count / 32 + 2).view(-1, 1)
+    # a chain of at most max(64, tile) tokens, or a tile's and then the tiles; and the product with the scale
+    tile = 32
+    while 16 * tile * tile < N:
+        tile *= 2
+    chain = torch.where(count <= max(64, tile), count, tile + count / tile + 2).view(-1, 1)
     tol = size * (chain + 1) * 2.0 ** -24
     dW = tim.embedding_backward(t, g, V, scale)
     tim.check()
