@@ -592,16 +592,16 @@ TIM_API int tim_adapter_logits(const void *logits, int dtype, int64_t N, int64_t
  * tim_processed_logprob_backward gives it), with t as above and du_i = scale_a B_a^T dy_i:
  *   dB_a = sum_i dy_i t_i^T,  dA_a = sum_i du_i h_i^T,  dh_i = A_a^T du_i,
  * over the rows i of adapter a.  The shared head's part, dh += dlogits W, is the
- * caller's (accumulate_dh adds to it); dL / dz is dlogits itself.  fp32 sums; t is held
- * to 2^-16 of its value, fp32 dlogits to 2^-16, du to 2^-24.
+ * caller's (accumulate_dh adds to it); dL / dz is dlogits itself.  fp32 sums; t, du and
+ * fp32 dlogits are held to 2^-24 of their values, 16-bit dlogits exactly.
  *   dlogits, dtype, N, V, stride, h, D, adapters, rows   as above
  *   dh   fp32 [N, D], 16-byte aligned; rows under no adapter: zeros (with accumulate_dh
  *        not touched)
  *   dA   fp32 [num_adapters, rank, D];  dB  fp32 [num_adapters, V, rank]; 16-byte
  *        aligned; an adapter without rows: zeros (with accumulate_adapters not touched)
  * No output shares a byte with an input or another.  The same call gives the same bits.
- * Scratch (stream-ordered pool): up to about 2 KB a row, and partial sums of du of at
- * most 1 GB (larger batches go in parts). */
+ * Scratch (stream-ordered pool): up to 1.6 KB a row and 12 KB an adapter, and partial
+ * sums of du of at most 1 GB and a little (larger batches go in parts). */
 TIM_API int tim_adapter_logits_backward(const void *dlogits, int dtype, int64_t N, int64_t V, int64_t stride,
                                         const void *h, int64_t D, const tim_adapters *adapters, const int32_t *rows,
                                         float *dh, float *dA, float *dB, int accumulate_dh, int accumulate_adapters,
@@ -617,8 +617,8 @@ TIM_API int tim_embedding(const int32_t *tokens, int64_t N, const void *W, int d
                           float scale, void *out, int out_dtype, tim_stream_t stream);
 
 /* Its gradient: dW[v] (+)= scale sum over n with tokens_n = v of grad_n, in fp32, the
- * tokens of an id added in their order (ids with more than 64 tokens in partial sums
- * over tiles of 32): the same call gives the same bits.
+ * tokens of an id added in their order (ids with many tokens, more than 64 at least, in
+ * partial sums over tiles whose length N decides): the same call gives the same bits.
  *   grad           [N, D] of type dtype, contiguous, aligned to its elements
  *   dW             fp32 [V, D], contiguous; written whole, or with accumulate_dW added to
  *                  (rows without a token are not touched: the gradient of a tied head,

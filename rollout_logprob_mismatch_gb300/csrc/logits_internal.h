@@ -25,7 +25,7 @@ constexpr int LP_MAP_THREADS = 256, LP_MAP_CTAS = 6;     // WRITE, GRAD; CTAs of
 constexpr int LP_SHORT = 12, LP_LONG = 4096;       // slices up to which, a row's tokens above which all of them build the table
 constexpr int LP_WARPS = 8;                        // warps of a CTA at most
 constexpr int LP_MAP_SLICES = 64;                  // slices of a segment at most
-constexpr int LP_MAP_CAP = 3008, LP_LOGP_CAP = 1536;     // touched columns a table holds (at least LG_SLICE; 3072 measures as 3008)
+constexpr int LP_MAP_CAP = 3008, LP_LOGP_CAP = 1536;     // touched columns a table holds (at least LG_SLICE)
 constexpr int LP_HEAVY = 1536, LP_HEAVY_CAP = 5120;      // tokens of history a row, on average; the table then
 constexpr int LP_TABLE = 1 << 18;                  // columns a table covers
 static_assert(LP_MAP_SLICES * LG_SLICE <= 65536, "a segment's columns are counted in 16 bits");
