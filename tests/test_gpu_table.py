@@ -539,3 +539,104 @@ def test_wrappers_refuse():
               lambda: tim.embedding_backward(t, z, 9, dW=torch.empty((8, 100), device="cuda"))):
         with pytest.raises((TypeError, ValueError)):
             f()
+
+
+# ----------------------------------------------------------------------------- the far ends
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("V,R", [(130, 16), (130, 32), (300, 64), (2050, 8), (2050, 128)])
+def test_gradient_of_adapters_of_many_steps(V, R, dtype):
+    """Adapters of none to 21 steps of rows: dB's sums, taken in turn, that have something or not."""
+    counts = [1, 0, 32, 129, 300, 0, 500, 1300, 17]
+    gen = torch.Generator(device="cuda").manual_seed(V + R)
+    N, n = sum(counts) + 11, len(counts)
+    dy, h, ad, rows = draw(N, V, 72, R, n, dtype, 21)
+    ids = torch.cat([torch.full((c,), k, dtype=torch.int32) for k, c in enumerate(counts)] + [torch.full((11,), -7, dtype=torch.int32)])
+    rows = ids.cuda()[torch.randperm(N, generator=gen, device="cuda")].contiguous()
+    want = grads64(dy, h, ad, rows, dtype)
+    for name, got in zip(("dh", "dA", "dB"), tim.adapter_logits_backward(dy, h, ad, rows)):
+        check(got, *want[name], name)
+    tim.check()
+
+
+def test_as_many_adapters_as_there_can_be():
+    n, N, V, D, R = 65535, 300, 24, 16, 8
+    z, h, ad, rows = draw(N, V, D, R, n, "bf16", 22)
+    rows[:4] = torch.tensor([65534, 0, 65535, 65534], dtype=torch.int32, device="cuda")
+    on = live(rows, n)
+    some = rows[on].long().unique()
+    slot = torch.full((n + 2,), -1, dtype=torch.int32, device="cuda")
+    slot[some] = torch.arange(some.numel(), dtype=torch.int32, device="cuda")
+    few = tim.Adapters(ad.A[some].contiguous(), ad.B[some].contiguous(), ad.scale[some].contiguous())
+    short = torch.where(on, slot[rows.long().clamp(0, n + 1)], -1).to(torch.int32)
+    assert torch.equal(bits(tim.adapter_logits(z, h, ad, rows)), bits(tim.adapter_logits(z, h, few, short)))
+    dh, dA, dB = tim.adapter_logits_backward(z, h, ad, rows)
+    fh, fA, fB = tim.adapter_logits_backward(z, h, few, short)
+    tim.check()
+    assert torch.equal(dh, fh) and torch.equal(dA[some], fA) and torch.equal(dB[some], fB)
+    assert int((dA != 0).any(2).any(1).sum()) <= some.numel() and int((dB != 0).any(2).any(1).sum()) <= some.numel()
+    check(tim.adapter_logits(z, h, few, short), *logits64(z, h, few, short, "bf16"))
+
+
+def test_offsets_past_32_bits():
+    """Logits, factors, a table and gradients of more than 2^32 bytes, and 2^31 elements."""
+    N, V, D, R, n = 16500, 131072, 64, 64, 270
+    gen = torch.Generator(device="cuda").manual_seed(23)
+    last = torch.arange(N - 70, N, device="cuda")
+    z = torch.zeros((N, V), dtype=torch.bfloat16, device="cuda")
+    z[last] = torch.randn((70, V), generator=gen, device="cuda").to(torch.bfloat16)
+    h = torch.randn((N, D), generator=gen, device="cuda").to(torch.bfloat16)
+    A = torch.zeros((n, R, D), dtype=torch.bfloat16, device="cuda")
+    B = torch.zeros((n, V, R), dtype=torch.bfloat16, device="cuda")
+    A[-1] = (torch.rand((R, D), generator=gen, device="cuda") * 0.2 - 0.1).to(torch.bfloat16)
+    B[-1] = torch.randn((V, R), generator=gen, device="cuda").to(torch.bfloat16)
+    rows = torch.full((N,), -1, dtype=torch.int32, device="cuda")
+    rows[last] = n - 1
+    ad, one = tim.Adapters(A, B), tim.Adapters(A[-1:].contiguous(), B[-1:].contiguous())
+    under = torch.zeros(70, dtype=torch.int32, device="cuda")
+    dh, dA, dB = tim.adapter_logits_backward(z, h, ad, rows)
+    tim.check()
+    want = grads64(z[last], h[last], one, under, "bf16")
+    check(dh[last], *want["dh"], "dh")
+    check(dA[-1:], *want["dA"], "dA")
+    check(dB[-1:], *want["dB"], "dB")
+    assert not bool(dh[:N - 70].any()) and not bool(dA[:-1].any()) and float(dB[:-1].abs().amax()) == 0
+    del dh, dA, dB
+    y, tol = logits64(z[last], h[last], one, under, "bf16")
+    tim.adapter_logits(z, h, ad, rows, out=z)
+    tim.check()
+    check(z[last], y, tol)
+    assert float(z[:N - 70].abs().amax()) == 0
+    del z, A, B, ad, y, tol
+    V, D = 1 << 20, 2056
+    W = torch.zeros((V, D), dtype=torch.bfloat16, device="cuda")
+    W[-3:] = torch.randn((3, D), generator=gen, device="cuda").to(torch.bfloat16)
+    t = torch.tensor([V - 1, 0, V - 3, V, V - 2, V - 1], dtype=torch.int32, device="cuda")
+    out = tim.embedding(t, W)
+    zero = torch.zeros(D, dtype=W.dtype, device="cuda")
+    assert torch.equal(out, torch.stack([W[-1], zero, W[-3], zero, W[-2], W[-1]]))
+    del W
+    dW = tim.embedding_backward(t, out, V)
+    tim.check()
+    assert torch.equal(dW[-1], 2 * out[0].float()) and torch.equal(dW[-3], out[2].float()) and torch.equal(dW[-2], out[4].float())
+    assert float(dW[:-3].abs().amax()) == 0
+
+
+def test_calls_side_by_side_on_two_streams():
+    cases = [draw(700, 3001, 256, 32, 5, "f16", 24), draw(300, 5000, 512, 16, 9, "bf16", 25)]
+    tokens = torch.randint(-1, 900, (3000,), device="cuda", dtype=torch.int32)
+    g = torch.randn((3000, 257), device="cuda")
+
+    def calls(c):
+        return (tim.adapter_logits(*c), *tim.adapter_logits_backward(*c), tim.embedding_backward(tokens, g, 900))
+
+    want = [calls(c) for c in cases]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream(), torch.cuda.Stream()], [[], []]
+    for _ in range(5):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(calls(cases[i]))
+    torch.cuda.synchronize()
+    tim.check()
+    for w, g_ in zip(want, got):
+        assert all(torch.equal(bits(x), bits(y)) for one in g_ for x, y in zip(w, one))
