@@ -19,6 +19,8 @@ namespace tim {
 namespace {
 
 // ---------------------------------------------------------------- shrink
+constexpr int WARPS = 16;   // of a CTA that orders or projects
+
 // Calls f(row, position among the adapter's rows) for those of the warp's rows
 // [r0, r1) that are under adapter `ad`, in order, `before` of them already counted.
 template <typename F>
@@ -42,7 +44,7 @@ struct Own {
     int r0, r1, own, base, count, before;
 };
 
-template <int WARPS> __device__ __forceinline__ Own count_rows(const AdapterArgs &a, int ad)
+__device__ __forceinline__ Own count_rows(const AdapterArgs &a, int ad)
 {
     __shared__ int sb[WARPS], so[WARPS];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -91,15 +93,13 @@ __device__ __forceinline__ void write_order(const AdapterArgs &a, int ad, const 
 }
 
 // t of up to 16 rows under adapter ad, written for rows lo .. hi - 1 of them at positions
-// pos + lo ..  k is shared among 16 (every 16th 32 of it each: a warp is one of them, or
-// two), whose sums are added up through shared memory in their order, so that a row's sum
+// pos + lo ..  k is shared among the 16 warps (every 16th 32 of it each), whose sums are added up through shared memory in their order, so that a row's sum
 // depends on D alone.  AHEAD: steps of 32 k whose loads are in flight together.
-template <int RP, int PARTS, int WARPS, int AHEAD>
+template <int RP, int PARTS, int AHEAD>
 __device__ __forceinline__ void project(const AdapterArgs &a, int ad, const int32_t *rows, int lo, int hi, int pos)
 {
     constexpr int NC = RP < 32 ? RP : 32;      // rank columns at a time
-    constexpr int EACH = 16 / WARPS;
-    __shared__ float sums[16][16][NC + 1];
+    __shared__ float sums[WARPS][16][NC + 1];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
     const float scale = a.scale ? a.scale[ad] : 1.f;
     const uint16_t *A = a.A + static_cast<size_t>(ad) * a.R * a.D;
@@ -109,12 +109,12 @@ __device__ __forceinline__ void project(const AdapterArgs &a, int ad, const int3
     const uint16_t *h0 = a.h + static_cast<size_t>(on0 ? rows[g] : 0) * a.D;
     const uint16_t *h1 = a.h + static_cast<size_t>(on1 ? rows[g + 8] : 0) * a.D;
     for (int n0 = 0; n0 < RP; n0 += NC) {
-        float acc[EACH][NC / 8][4] = {};
+        float acc[NC / 8][4] = {};
         if (n0 < a.R) {
-            for (int kc0 = warp; kc0 < kchunks; kc0 += 16 * AHEAD) {
-                uint4 x0[AHEAD * EACH], x1[AHEAD * EACH], w[AHEAD * EACH][NC / 8];
+            for (int kc0 = warp; kc0 < kchunks; kc0 += WARPS * AHEAD) {
+                uint4 x0[AHEAD], x1[AHEAD], w[AHEAD][NC / 8];
 #pragma unroll
-                for (int i = 0; i < AHEAD * EACH; ++i) {
+                for (int i = 0; i < AHEAD; ++i) {
                     const int k = (kc0 + i * WARPS) * 32 + q * 8;   // D is a multiple of 8: the eight are in or out together
                     const bool in = k < a.D;
                     x0[i] = in && on0 ? __ldg(reinterpret_cast<const uint4 *>(h0 + k)) : zero;
@@ -126,7 +126,7 @@ __device__ __forceinline__ void project(const AdapterArgs &a, int ad, const int3
                     }
                 }
 #pragma unroll
-                for (int i = 0; i < AHEAD * EACH; ++i)
+                for (int i = 0; i < AHEAD; ++i)
 #pragma unroll
                     for (int j = 0; j < NC / 8; ++j) {
                         // 32 k by themselves, then added: the tensor cores cut, rather than round, what they add up
@@ -135,27 +135,25 @@ __device__ __forceinline__ void project(const AdapterArgs &a, int ad, const int3
                         mma16816(part, {x0[i].z, x1[i].z, x0[i].w, x1[i].w}, w[i][j].z, w[i][j].w);
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            acc[i % EACH][j][k] += part[k];
+                            acc[j][k] += part[k];
                     }
             }
         }
         __syncthreads();   // the sums before have been read
 #pragma unroll
-        for (int v = 0; v < EACH; ++v)
-#pragma unroll
-            for (int j = 0; j < NC / 8; ++j) {
-                float (&to)[16][NC + 1] = sums[warp + v * WARPS];
-                to[g][j * 8 + 2 * q] = acc[v][j][0];
-                to[g][j * 8 + 2 * q + 1] = acc[v][j][1];
-                to[g + 8][j * 8 + 2 * q] = acc[v][j][2];
-                to[g + 8][j * 8 + 2 * q + 1] = acc[v][j][3];
-            }
+        for (int j = 0; j < NC / 8; ++j) {
+            float (&to)[16][NC + 1] = sums[warp];
+            to[g][j * 8 + 2 * q] = acc[j][0];
+            to[g][j * 8 + 2 * q + 1] = acc[j][1];
+            to[g + 8][j * 8 + 2 * q] = acc[j][2];
+            to[g + 8][j * 8 + 2 * q + 1] = acc[j][3];
+        }
         __syncthreads();
         for (int i = tid; i < (hi - lo) * NC; i += WARPS * 32) {
             const int m = lo + i / NC, r = i % NC;
             float u = 0.f;
 #pragma unroll
-            for (int w = 0; w < 16; ++w)
+            for (int w = 0; w < WARPS; ++w)
                 u += sums[w][m][r];
             uint16_t p[PARTS];
             split_bf16<PARTS>(u * scale, p);
@@ -178,16 +176,17 @@ __device__ __forceinline__ void pad_rows(const AdapterArgs &a, int ad, int count
         t[i] = 0u;
 }
 
-// Few rows, one launch.  CTA (a, y): the rows of adapter a, 16 at a time from the y-th 16
+// Few rows, one launch: a chain of loads (ids, rows, their products), 11 us for 64 rows of 4096 under
+// 32 adapters of rank 16, 4.0 MB.  CTA (a, y): the rows of adapter a, 16 at a time from the y-th 16
 // on; a = n: the rows under no adapter (only ordered).
 template <int RP, int PARTS>
-__global__ void __launch_bounds__(256, 2) adapters_shrink_kernel(const AdapterArgs a)
+__global__ void __launch_bounds__(512, 1) adapters_shrink_kernel(const AdapterArgs a)
 {
     __shared__ int32_t mine[16];
     const int ad = blockIdx.x;
     pdl_wait();
     pdl_launch_dependents();
-    const Own o = count_rows<8>(a, ad);
+    const Own o = count_rows(a, ad);
     if (blockIdx.y == 0)
         write_order(a, ad, o);
     if (ad == a.n)
@@ -200,20 +199,21 @@ __global__ void __launch_bounds__(256, 2) adapters_shrink_kernel(const AdapterAr
                     mine[p - c0] = r;
             });
         __syncthreads();
-        project<RP, PARTS, 8, 2>(a, ad, mine, 0, rows, o.base + c0);
+        project<RP, PARTS, RP == 16 ? 4 : 3>(a, ad, mine, 0, rows, o.base + c0);
         if (c0 + rows == o.count)
             pad_rows(a, ad, o.count, o.base + o.count);
         __syncthreads();
     }
 }
 
-// Many rows: the order in a launch of its own, then a CTA for every 16 positions (two an SM
-// where there are that many, else one with more loads in flight).
+// Many rows: the order in a launch of its own (8192 rows 6 us), then a CTA for every 16 positions
+// (two an SM where there are that many, else one with more loads in flight): 8192 x 4096, rank 16,
+// 24 us (h read at 2.9 TB/s; the factors come from L2 for every 16 rows).
 __global__ void __launch_bounds__(512) adapters_order_kernel(const AdapterArgs a)
 {
     pdl_wait();
     pdl_launch_dependents();
-    const Own o = count_rows<16>(a, blockIdx.x);
+    const Own o = count_rows(a, blockIdx.x);
     write_order(a, blockIdx.x, o);
 }
 
@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(512, MANY ? 2 : 1) adapters_project_kernel(con
         int m = s + 1;
         while (s_ad[m] == s_ad[s])
             ++m;
-        project<RP, PARTS, 16, MANY ? (RP == 16 ? 2 : 1) : 4>(a, s_ad[s], s_row, s, m, p0);
+        project<RP, PARTS, MANY ? (RP == 16 ? 2 : 1) : 4>(a, s_ad[s], s_row, s, m, p0);
         const int ad = s_ad[s], e = a.plan.offsets[ad + 1];
         if (p0 + m == e)
             pad_rows(a, ad, e - a.plan.offsets[ad], e);
@@ -338,13 +338,16 @@ template <typename T, int RP, int PARTS, int CB> struct MapShape {
 // side by side in the grid share their rows), and a ninth that keeps the copies of the
 // next tiles and factors in flight.  Product j (of four) of 32 columns has as its column n
 // the logits' column 8 (n / 2) + 2 j + n % 2, so that lane q's eight results are eight
-// neighbours.
+// neighbours.  Measured, inputs out of L2: 8192 x 151936 bf16, rank 16 of 4 adapters, 845 us
+// (5.0 GB, 88 % of the copy rate); 64 x 128256 bf16 under 32 adapters 39 us (133 MB, a CTA's only
+// tile waits for its factors); rank 64, 16384 x 32000 bf16, 1118 us against a floor of 311: the
+// factor is read from shared memory for every 16 rows.
 template <typename T, int RP, int PARTS, int CB, bool AL>
 __global__ void __launch_bounds__(AD_MAP_THREADS, CB == 1 && RP <= 32 ? 3 : 2) adapters_map_kernel(const AdapterArgs a)
 {
     using K = Ranks<RP>;
     using S = MapShape<T, RP, PARTS, CB>;
-    constexpr int WARPS = AD_MAP_THREADS / 32 - 1;
+    constexpr int MAP_WARPS = AD_MAP_THREADS / 32 - 1;
     constexpr int W = Elem<T>::WORDS;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int32_t s_row[AD_MAP_ROWS], s_ad[AD_MAP_ROWS + 1];
@@ -363,9 +366,9 @@ __global__ void __launch_bounds__(AD_MAP_THREADS, CB == 1 && RP <= 32 ? 3 : 2) a
     if (tid == 0) {
         for (int i = 0; i < 4; ++i) {
             mbar_init(full(i), 1);
-            mbar_init(empty(i), WARPS);
+            mbar_init(empty(i), MAP_WARPS);
             mbar_init(ffull(i), 1);
-            mbar_init(fempty(i), WARPS);
+            mbar_init(fempty(i), MAP_WARPS);
         }
         *abort_flag = 0;
         fence_mbar_init();
@@ -386,7 +389,7 @@ __global__ void __launch_bounds__(AD_MAP_THREADS, CB == 1 && RP <= 32 ? 3 : 2) a
     const T *z = static_cast<const T *>(a.z);
     const uint64_t budget = a.wait_budget_ns;
 
-    if (warp == WARPS) {
+    if (warp == MAP_WARPS) {
         // ------------------------------------------------------------ copies
         const uint64_t pol = l2_policy_evict_first(), pol_keep = l2_policy_evict_normal();
         int stage = 0, slot = 0, held = -1;   // held: the adapter of the last factor copied
@@ -602,7 +605,7 @@ template <int RP, int PARTS> cudaError_t shrink(const AdapterArgs &a, int num_sm
     }
     const int ys = std::max(1, std::min((a.N + 15) / 16, (2 * num_sms + a.n) / (a.n + 1)));
     return launch(adapters_shrink_kernel<RP, PARTS>, dim3(static_cast<unsigned>(a.n + 1), static_cast<unsigned>(ys)),
-                  256, 0, a, s);
+                  512, 0, a, s);
 }
 
 template <int PARTS> cudaError_t shrink(const AdapterArgs &a, int num_sms, cudaStream_t s)
@@ -629,8 +632,12 @@ template <typename T, int PARTS, int RP, int CB> cudaError_t map(AdapterArgs a, 
     while (rows > 16 && slabs * ((a.N + rows - 1) / rows) < int64_t(8) * num_sms)
         rows /= 2;
     a.row_chunk = static_cast<int32_t>(rows);
-    a.stages = std::min<int>(S::MOST, static_cast<int>(rows / 16));
-    a.factors = a.stages == 1 && S::bytes(1, 4) <= AD_MAP_SMEM / 3 ? 4 : 2;
+    a.stages = std::min<int>(a.N > AD_FEW_ROWS ? S::MOST : 2, static_cast<int>(rows / 16));
+    // and then most of what is read are factors: as many as leave room for three CTAs an SM
+    // (256 x 151936 bf16, rank 32 of 64: 167 us with three factors and two tiles, 198 with two and four)
+    a.factors = 2;
+    while (a.N <= AD_FEW_ROWS && a.factors < 4 && S::bytes(a.stages, a.factors + 1) <= AD_MAP_SMEM / 3)
+        ++a.factors;
     const dim3 grid(static_cast<unsigned>(slabs * ((a.N + rows - 1) / rows)));
     auto starts16 = [](const void *p, int64_t ld, int64_t N) {
         return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && (N == 1 || ld * sizeof(T) % 16 == 0);
