@@ -581,8 +581,9 @@ typedef struct {
  *   out    [N, V] of type dtype, rows out_stride apart; may be the logits themselves
  *          (rows under no adapter are then not touched), else no shared element; its
  *          extent, from the first row to the last, shares no byte with the other inputs
- * An infinite or NaN factor of an adapter reaches no row of another.  A row's bits do
- * not depend on the rows beside it.  Scratch (stream-ordered pool): 8 N + 4 num_adapters
+ * An infinite or NaN factor of an adapter reaches no row of another (its own rows may get
+ * a NaN where the formula has an infinity: t comes in parts, of either sign).  A row's
+ * bits do not depend on the rows beside it.  Scratch (stream-ordered pool): 8 N + 4 num_adapters
  * bytes and at most 784 N bytes. */
 TIM_API int tim_adapter_logits(const void *logits, int dtype, int64_t N, int64_t V, int64_t stride, const void *h,
                                int64_t D, const tim_adapters *adapters, const int32_t *rows, void *out,
@@ -593,7 +594,8 @@ TIM_API int tim_adapter_logits(const void *logits, int dtype, int64_t N, int64_t
  *   dB_a = sum_i dy_i t_i^T,  dA_a = sum_i du_i h_i^T,  dh_i = A_a^T du_i,
  * over the rows i of adapter a.  The shared head's part, dh += dlogits W, is the
  * caller's (accumulate_dh adds to it); dL / dz is dlogits itself.  fp32 sums; t, du and
- * fp32 dlogits are held to 2^-24 of their values, 16-bit dlogits exactly.
+ * fp32 dlogits are held to 2^-24 of their values, 16-bit dlogits exactly; an infinity
+ * in dlogits or B may come out as a NaN, and reaches its own adapter and rows only.
  *   dlogits, dtype, N, V, stride, h, D, adapters, rows   as above
  *   dh   fp32 [N, D], 16-byte aligned; rows under no adapter: zeros (with accumulate_dh
  *        not touched)
