@@ -307,6 +307,10 @@ template <int RP> struct Ranks {
     static constexpr int STEP = RP == 16 ? 4 : 8;        // neighbouring ranks of a lane
     static constexpr int GROUPS = RP == 16 ? 1 : RP / 32;
     static constexpr int WORDS = STEP / 2;
+    // A warp keeps its part of a factor in registers, so that the buffer is free at once (256 x 151936
+    // bf16, rank 32 of 64: 154 us, 167 without).  At rank 16 it takes the room of the wide form
+    // (8192 x 151936: 1129 us, 878 without); at 64 it gains 1 %; at 128 there is no room.
+    static constexpr bool HELD = RP == 32;
 };
 
 template <int WORDS> __device__ __forceinline__ void lds_words(uint32_t (&w)[4], uint32_t addr)
@@ -449,7 +453,13 @@ __global__ void __launch_bounds__(AD_MAP_THREADS, CB == 1 && RP <= 32 ? 3 : 2) a
         uint32_t phase = 0, fphase = 1;
         bool ok = true;
         const uint32_t frow = static_cast<uint32_t>(a.R) * 2;
+        uint32_t f[K::HELD ? K::GROUPS : 1][CB][4][4];   // the factor's columns and ranks of this lane
         const uint32_t fcol = static_cast<uint32_t>(w0 + 8 * (g >> 1) + (g & 1)) * frow + q * (K::STEP * 2);
+        auto load_factor = [&](uint32_t (&w)[4], int from, int k, int c, int j) {
+            w[0] = w[1] = w[2] = w[3] = 0u;
+            if (k * 32 + q * K::STEP < a.R)   // ranks past R: zeros
+                lds_words<K::WORDS>(w, factor0 + from * S::FACTOR + fcol + static_cast<uint32_t>(c * 32 + 2 * j) * frow + k * 64);
+        };
         for (int p = 0; p < rows; p += 16) {
             ok = warp_wait(full(stage), phase, abort_flag, budget);
             if (!ok)
@@ -466,9 +476,11 @@ __global__ void __launch_bounds__(AD_MAP_THREADS, CB == 1 && RP <= 32 ? 3 : 2) a
                         ++m;
                 if (ad < a.n) {
                     if (ad != held) {
-                        __syncwarp();
-                        if (held >= 0 && lane == 0)
-                            mbar_arrive(fempty(slot));
+                        if (!K::HELD) {
+                            __syncwarp();
+                            if (held >= 0 && lane == 0)
+                                mbar_arrive(fempty(slot));
+                        }
                         held = ad;
                         if (++slot == a.factors) {
                             slot = 0;
@@ -477,8 +489,19 @@ __global__ void __launch_bounds__(AD_MAP_THREADS, CB == 1 && RP <= 32 ? 3 : 2) a
                         ok = warp_wait(ffull(slot), fphase, abort_flag, budget);
                         if (!ok)
                             break;
+                        if constexpr (K::HELD) {   // the buffer is free again as soon as every warp has its part
+#pragma unroll
+                            for (int k = 0; k < K::GROUPS; ++k)
+#pragma unroll
+                                for (int c = 0; c < CB; ++c)
+#pragma unroll
+                                    for (int j = 0; j < 4; ++j)
+                                        load_factor(f[k][c][j], slot, k, c, j);
+                            __syncwarp();
+                            if (lane == 0)
+                                mbar_arrive(fempty(slot));
+                        }
                     }
-                    const uint32_t fs = factor0 + slot * S::FACTOR + fcol;
                     float acc[CB][4][4] = {};
 #pragma unroll
                     for (int k = 0; k < K::GROUPS; ++k) {
@@ -488,19 +511,18 @@ __global__ void __launch_bounds__(AD_MAP_THREADS, CB == 1 && RP <= 32 ? 3 : 2) a
 #pragma unroll
                             for (int half = 0; half < 2; ++half)
                                 lds_words<K::WORDS>(t[i][half], ts + (g + half * 8) * S::TROW + (i * RP + k * 32 + q * K::STEP) * 2);
-                        const bool in = k * 32 + q * K::STEP < a.R;   // ranks past R: zeros
 #pragma unroll
                         for (int c = 0; c < CB; ++c)
 #pragma unroll
                             for (int j = 0; j < 4; ++j) {
-                                uint32_t f[4] = {0u, 0u, 0u, 0u};
-                                if (in)
-                                    lds_words<K::WORDS>(f, fs + static_cast<uint32_t>(c * 32 + 2 * j) * frow + k * 64);
+                                uint32_t (&w)[4] = f[K::HELD ? k : 0][c][j];
+                                if (!K::HELD)
+                                    load_factor(w, slot, k, c, j);
 #pragma unroll
                                 for (int i = 0; i < PARTS; ++i) {
-                                    mma16816(acc[c][j], {t[i][0][0], t[i][1][0], t[i][0][1], t[i][1][1]}, f[0], f[1]);
+                                    mma16816(acc[c][j], {t[i][0][0], t[i][1][0], t[i][0][1], t[i][1][1]}, w[0], w[1]);
                                     if (K::WORDS == 4)
-                                        mma16816(acc[c][j], {t[i][0][2], t[i][1][2], t[i][0][3], t[i][1][3]}, f[2], f[3]);
+                                        mma16816(acc[c][j], {t[i][0][2], t[i][1][2], t[i][0][3], t[i][1][3]}, w[2], w[3]);
                                 }
                             }
                     }
