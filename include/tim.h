@@ -596,6 +596,9 @@ TIM_API int tim_adapter_logits(const void *logits, int dtype, int64_t N, int64_t
  * caller's (accumulate_dh adds to it); dL / dz is dlogits itself.  fp32 sums; t, du and
  * fp32 dlogits are held to 2^-24 of their values, 16-bit dlogits exactly; an infinity
  * in dlogits or B may come out as a NaN, and reaches its own adapter and rows only.
+ * The tensor cores cut what they add up: dB is added in fp32 from sums of at most 48 products of
+ * 16 rows, so that its error does not grow with the adapter's rows (1e-6 of its norm; sums
+ * below 2^-126 of an adapter of more rows than one sum takes may count as zero).
  *   dlogits, dtype, N, V, stride, h, D, adapters, rows   as above
  *   dh   fp32 [N, D], 16-byte aligned; rows under no adapter: zeros (with accumulate_dh
  *        not touched)

@@ -7,9 +7,10 @@
 //   dh_i (+)= A_a^T du_i           [D]
 // dy is by far the largest operand and is read once: a CTA owns a slab of the vocabulary
 // (up to 1024 columns) and walks all rows, adapter by adapter in steps of 128, so that
-// dB's part of the slab stays in TMEM until the adapter's last row, and du of a step (the
-// slab's part of the sum over V) goes to a partial array that a second launch folds in
-// slab order.  Both products take the same tile [128 rows x 128 columns] from shared
+// dB's part of the slab stays in TMEM for up to a.link rows of the adapter (the tensor cores
+// cut what they add up: a chain over all of 8200 rows lost 1e-5 to 5e-5 of dB) and then
+// goes to memory, further links' added to it, and du of a step (the slab's part of the sum
+// over V) goes to a partial array that a second launch folds in slab order.  Both products take the same tile [128 rows x 128 columns] from shared
 // memory (tcgen05.mma, bf16 -> fp32): du with the rows as M and the columns as K
 // (K-major), dB with the columns as M and the rows as K (MN-major, the same bytes).
 //   warp 0      the adapter's factor and t, by TMA
@@ -51,7 +52,7 @@ template <typename T, int HOW, int RP> struct Shape {
     static constexpr int TILE = 2 * SUB;
     static constexpr int FACTORS = (RP == 16 && HOW == COPY ? 2 : 1) * BLOCKS * BC * SPAN;   // bytes for factors: two where they fit
     static constexpr int TT = (RP <= 32 ? 4 : PARTS) * STEP * SPAN;
-    static constexpr int TS = RP == 64 && PLANES == 1 ? 1 : 2;
+    static constexpr int TS = RP == 64 && PLANES == 1 && HOW != COPY ? 1 : 2;
     static constexpr int REST = AG_SMEM - 2048 - FACTORS - TS * TT;
     // not COPY: rows on their way to the warps that rewrite them, 32 NR in a batch
     static constexpr int SROW = BC * static_cast<int>(sizeof(T)) + (HOW == ANY ? 16 : 0);
@@ -65,7 +66,7 @@ template <typename T, int HOW, int RP> struct Shape {
     static constexpr uint32_t TMEM = 512;                      // du twice, dB's blocks
     static constexpr int CHAIN = 4;                            // tiles of a sum of du in TMEM
     static_assert(RP <= 32 || CHAIN >= BLOCKS, "ranks beyond 32 are not added up in registers");
-    static_assert(STAGES >= 2 && BATCHES >= 2 && (2 + BLOCKS) * RP <= 512, "shared memory, TMEM");
+    static_assert(STAGES >= 2 && (HOW == COPY || BATCHES >= 2) && (2 + BLOCKS) * RP <= 512, "shared memory, TMEM");
 };
 
 // An adapter's positions [begin, end) of a part [p0, p1) of the batch: parts meet at a
@@ -126,6 +127,17 @@ __host__ __device__ constexpr uint32_t desc_span_hi(int span)
     return static_cast<uint32_t>(8 * span) / 16 | 1u << 14 | (span == 128 ? 2u : span == 64 ? 4u : 6u) << 29;
 }
 
+__device__ __forceinline__ float4 plus(float4 x, float4 y) { return make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w); }
+
+// *p += x without waiting for *p (loads of it held the products up: 8192 x 151936 under one
+// adapter of rank 32 936 us, 863 so).  One thread alone adds to p, so the order is its own.
+// Sums below 2^-126 may count as zero.
+__device__ __forceinline__ void red_add4(float4 *p, float4 x)
+{
+    asm volatile("red.relaxed.gpu.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p), "f"(x.x), "f"(x.y), "f"(x.z), "f"(x.w)
+                 : "memory");
+}
+
 template <int RC> __device__ __forceinline__ void tmem_row(uint32_t taddr, float (&v)[RC])
 {
     static_assert(RC == 16 || RC == 32, "columns of one load");
@@ -160,9 +172,9 @@ __global__ void __launch_bounds__(Shape<T, HOW, RP>::THREADS, 1)
     auto dufull = [&](int i) { return bar0 + 8u * (16 + i); };
     auto duempty = [&](int i) { return bar0 + 8u * (18 + i); };
     auto dbfull = [&](int i) { return bar0 + 8u * (20 + i); };
-    auto dbempty = [&](int i) { return bar0 + 8u * (22 + i); };
-    const uint32_t drain = bar0 + 8u * 24;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 25);
+    const uint32_t drain = bar0 + 8u * 22;
+    auto dbempty = [&](int i, int block) { return bar0 + 8u * (23 + i * S::BLOCKS + block); };
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 23 + 2 * S::BLOCKS);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -186,7 +198,8 @@ __global__ void __launch_bounds__(Shape<T, HOW, RP>::THREADS, 1)
             mbar_init(dufull(i), 1);
             mbar_init(duempty(i), 4);
             mbar_init(dbfull(i), 1);
-            mbar_init(dbempty(i), 4);
+            for (int c = 0; c < S::BLOCKS; ++c)
+                mbar_init(dbempty(i, c), 4);
         }
         mbar_init(drain, 1);
         *abort_flag = 0;
@@ -301,18 +314,23 @@ __global__ void __launch_bounds__(Shape<T, HOW, RP>::THREADS, 1)
         constexpr std::integral_constant<bool, true> yes{};
         constexpr std::integral_constant<bool, false> no{};
         segments([&](int, int b, int e) {
-            if (!warp_wait(ffull(fr.slot), fr.parity, abort_flag, budget) ||
-                !warp_wait(dbempty(db.slot), db.parity ^ 1u, abort_flag, budget))
+            if (!warp_wait(ffull(fr.slot), fr.parity, abort_flag, budget))
                 return false;
             const uint32_t fd = ((factors + fr.slot * factor_bytes) >> 4) | 1u << 16;
-            const uint32_t tdb = tmem + 2 * RP + db.slot * db_columns;
-            int chain = 0;   // the steps' products go to dB's sums in turn
+            int link = b, chain = 0;   // where dB's sums began; the steps' products go to them in turn
             for (int p = b; p < e; p += STEP) {
+                if (p == link + a.link) {   // long enough: what they have goes to memory
+                    umma_commit_lead(lead, dbfull(db.slot));
+                    db.next();
+                    link = p;
+                    chain = 0;
+                }
                 if (!warp_wait(tfull(tr.slot), tr.parity, abort_flag, budget))
                     return false;
                 const int steps = (min(STEP, e - p) + 15) / 16;   // of 16 rows
                 const uint32_t tt = ((ts + tr.slot * S::TT) >> 4) | 1u << 16;
-                const uint32_t tdb0 = tdb + chain * db_chain, first_db = p >= b + a.chains * STEP, first_low = a.merged ? first_db : p != b;
+                const uint32_t tdb0 = tmem + 2 * RP + db.slot * db_columns + chain * db_chain;
+                const uint32_t first_db = p >= link + a.chains * STEP, first_low = a.merged ? first_db : p != link;
                 const uint32_t low = a.low ? (a.chains - chain) * db_chain : 0;   // merged: beside the first part's columns
                 chain = chain + 1 == a.chains ? 0 : chain + 1;
                 for (int c = 0; c < blocks; ++c) {
@@ -322,6 +340,9 @@ __global__ void __launch_bounds__(Shape<T, HOW, RP>::THREADS, 1)
                     }
                     const uint32_t td = tmem + du.slot * RP;
                     if (!warp_wait(full(st.slot), st.parity, abort_flag, budget))
+                        return false;
+                    // tile by tile, so that the first ones go on while the last ones' sums are written
+                    if (p == link && !warp_wait(dbempty(db.slot, c), db.parity ^ 1u, abort_flag, budget))
                         return false;
                     // the writers' shared memory for the products: the fence stands here, since a
                     // writer's would wait for its copies of later tiles too
@@ -362,7 +383,7 @@ __global__ void __launch_bounds__(Shape<T, HOW, RP>::THREADS, 1)
         __syncwarp();
     } else if (warp < 6) {
         // ------------------------------------------------------------ results
-        constexpr int RC = RP < 32 ? RP : 32;   // ranks at a time
+        constexpr int RC = RP < 32 ? RP : 32, DC = 16;   // ranks of du, of dB at a time
         const int m = (warp & 3) * 32 + lane;   // row of du, column of dB's block
         const uint32_t mine = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
         Ring du(2), db(num_db);
@@ -372,115 +393,118 @@ __global__ void __launch_bounds__(Shape<T, HOW, RP>::THREADS, 1)
             const Part r(ob, oe, a.p0, a.p1);
             const int b = r.begin, e = r.end;
             const bool some = b < e;
-            const int chains = min(a.chains, (e - b + STEP - 1) / STEP);   // dB's sums that have something
             // an adapter whose rows began in an earlier part of the batch is added to; one
             // without rows is written (zeros) by the first part
             const bool add = a.accumulate || b > ob;
             if (!some && !(ob == oe && a.p0 == 0 && !a.accumulate))
                 continue;
-            for (int p = b; p < e; p += STEP) {
-                const int at = p + m % STEP;
-                // [part][four ranks][position]: a warp's rows lie together
-                const size_t count = a.p1 - a.p0 + 16;
-                float4 *o = reinterpret_cast<float4 *>(a.partial) +
-                            static_cast<size_t>(blockIdx.x * S::PLANES + m / STEP) * (RP / 4) * count + (at - a.p0);
-                auto put = [&](int r0, const float (&v)[RC]) {
-                    if (at < e && m / STEP < S::PLANES) {
+            for (int link = b; ok && link < max(e, b + 1); link += a.link) {   // dB's sums, from begun to written
+                const int link_end = min(e, link + a.link);
+                const int chains = min(a.chains, (link_end - link + STEP - 1) / STEP);   // dB's sums that have something
+                for (int p = link; p < link_end; p += STEP) {
+                    const int at = p + m % STEP;
+                    // [part][four ranks][position]: a warp's rows lie together
+                    const size_t count = a.p1 - a.p0 + 16;
+                    float4 *o = reinterpret_cast<float4 *>(a.partial) +
+                                static_cast<size_t>(blockIdx.x * S::PLANES + m / STEP) * (RP / 4) * count + (at - a.p0);
+                    auto put = [&](int r0, const float (&v)[RC]) {
+                        if (at < e && m / STEP < S::PLANES) {
 #pragma unroll
-                        for (int r = 0; r < RC / 4; ++r)
-                            o[(r0 / 4 + r) * count] = make_float4(v[4 * r], v[4 * r + 1], v[4 * r + 2], v[4 * r + 3]);
+                            for (int r = 0; r < RC / 4; ++r)
+                                o[(r0 / 4 + r) * count] = make_float4(v[4 * r], v[4 * r + 1], v[4 * r + 2], v[4 * r + 3]);
+                        }
+                    };
+                    float sum[RC] = {};   // of the chains of a slab (more than one where RP = RC)
+                    for (int c = 0; c < blocks; c += S::CHAIN) {
+                        ok = warp_wait(dufull(du.slot), du.parity, abort_flag, budget);
+                        if (!ok)
+                            break;
+                        tc_fence_after();
+#pragma unroll
+                        for (int r0 = 0; r0 < RP; r0 += RC) {
+                            float v[RC];
+                            __syncwarp();
+                            tmem_row<RC>(mine + du.slot * RP + r0, v);
+                            if constexpr (RP == RC) {
+#pragma unroll
+                                for (int r = 0; r < RC; ++r)
+                                    sum[r] += v[r];
+                            } else {
+                                put(r0, v);
+                            }
+                        }
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0)
+                            mbar_arrive(duempty(du.slot));
+                        du.next();
                     }
-                };
-                float sum[RC] = {};   // of the chains of a slab (more than one where RP = RC)
-                for (int c = 0; c < blocks; c += S::CHAIN) {
-                    ok = warp_wait(dufull(du.slot), du.parity, abort_flag, budget);
+                    if (!ok)
+                        break;
+                    if (RP == RC)
+                        put(0, sum);
+                }
+                if (!ok)
+                    break;
+                if (some) {
+                    ok = warp_wait(dbfull(db.slot), db.parity, abort_flag, budget);
                     if (!ok)
                         break;
                     tc_fence_after();
-#pragma unroll
-                    for (int r0 = 0; r0 < RP; r0 += RC) {
-                        float v[RC];
-                        __syncwarp();
-                        tmem_row<RC>(mine + du.slot * RP + r0, v);
-                        if constexpr (RP == RC) {
-#pragma unroll
-                            for (int r = 0; r < RC; ++r)
-                                sum[r] += v[r];
-                        } else {
-                            put(r0, v);
-                        }
-                    }
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0)
-                        mbar_arrive(duempty(du.slot));
-                    du.next();
                 }
-                if (!ok)
-                    break;
-                if (RP == RC)
-                    put(0, sum);
-            }
-            if (!ok)
-                break;
-            if (some) {
-                ok = warp_wait(dbfull(db.slot), db.parity, abort_flag, budget);
-                if (!ok)
-                    break;
-                tc_fence_after();
-            }
-            for (int c = 0; c < blocks; ++c) {
-                const int col = c0 + c * BC + m;
-                const uint32_t tb = mine + 2 * RP + db.slot * db_columns + c * db_block;
-                float4 *o = reinterpret_cast<float4 *>(a.dB + (static_cast<size_t>(ad) * a.V + col) * a.R + a.r0);
+                for (int c = 0; c < blocks; ++c) {
+                    const int col = c0 + c * BC + m;
+                    const uint32_t tb = mine + 2 * RP + db.slot * db_columns + c * db_block;
+                    float4 *o = reinterpret_cast<float4 *>(a.dB + (static_cast<size_t>(ad) * a.V + col) * a.R + a.r0);
 #pragma unroll
-                for (int r0 = 0; r0 < RP; r0 += RC) {
-                    if (a.r0 + r0 >= a.R)
-                        break;
-                    float v[RC] = {};
-                    if (some) {
-                        __syncwarp();
-                        tmem_row<RC>(tb + r0, v);
-                        auto add_up = [&](uint32_t from) {
-                            float x[RC];
-                            tmem_row<RC>(from, x);
-#pragma unroll
-                            for (int r = 0; r < RC; ++r)
-                                v[r] += x[r];
-                        };
-                        for (int i = 1; i < chains; ++i)
-                            add_up(tb + i * db_chain + r0);
-                        if (RP <= 32 && a.merged) {
-                            for (int i = 0; i < chains; ++i)
-                                add_up(tb + i * db_chain + RP);
-                        } else if (a.low) {
-                            add_up(tb + a.chains * db_chain + r0);
-                        }
-                    }
-                    if (col >= a.V)
-                        continue;
-#pragma unroll
-                    for (int r = 0; r < RC / 4; ++r) {
-                        if (a.r0 + r0 + 4 * r >= a.R)
+                    for (int r0 = 0; r0 < RP; r0 += DC) {
+                        if (a.r0 + r0 >= a.R)
                             break;
-                        float4 x = make_float4(v[4 * r], v[4 * r + 1], v[4 * r + 2], v[4 * r + 3]);
-                        if (add) {
-                            const float4 y = o[r0 / 4 + r];
-                            x.x += y.x;
-                            x.y += y.y;
-                            x.z += y.z;
-                            x.w += y.w;
+                        float v[DC] = {};
+                        if (some) {
+                            __syncwarp();
+                            tmem_row<DC>(tb + r0, v);
+                            auto add_up = [&](uint32_t from) {
+                                float x[DC];
+                                tmem_row<DC>(from, x);
+#pragma unroll
+                                for (int r = 0; r < DC; ++r)
+                                    v[r] += x[r];
+                            };
+                            for (int i = 1; i < chains; ++i)
+                                add_up(tb + i * db_chain + r0);
+                            if (RP <= 32 && a.merged) {
+                                for (int i = 0; i < chains; ++i)
+                                    add_up(tb + i * db_chain + RP + r0);
+                            } else if (a.low) {
+                                add_up(tb + a.chains * db_chain + r0);
+                            }
                         }
-                        o[r0 / 4 + r] = x;
+                        if (r0 + DC >= min(RP, a.R - a.r0) && some) {   // the tile's last ranks are read
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0)
+                                mbar_arrive(dbempty(db.slot, c));
+                        }
+                        if (col >= a.V)
+                            continue;
+#pragma unroll
+                        for (int r = 0; r < DC / 4; ++r) {
+                            if (a.r0 + r0 + 4 * r >= a.R)
+                                break;
+                            float4 x = make_float4(v[4 * r], v[4 * r + 1], v[4 * r + 2], v[4 * r + 3]);
+                            if (link > b) {
+                                red_add4(o + r0 / 4 + r, x);
+                                continue;
+                            }
+                            if (add)
+                                x = plus(x, o[r0 / 4 + r]);
+                            o[r0 / 4 + r] = x;
+                        }
                     }
                 }
-            }
-            if (some) {
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(dbempty(db.slot));
-                db.next();
+                if (some)
+                    db.next();
             }
         }
     } else {

@@ -233,6 +233,8 @@ int tim_adapter_logits_backward(const void *dlogits, int dtype, int64_t N, int64
     const int64_t columns = per_slab * (a.merged ? 2 : 1) * RP, fit = (512 - 2 * RP) / columns, sums = fit >= 4 ? fit / 2 : fit;
     a.low = !a.merged && sums >= 2;   // merged: the low products have columns of their own already
     a.chains = static_cast<int32_t>(std::min<int64_t>(sums - a.low, 4));
+    const int products = tim::ag_step(dtype) / 16 * (a.merged || a.low ? 1 : tim::ag_products(tim::ag_planes(dtype)));
+    a.link = a.chains * tim::ag_step(dtype) * (tim::AG_CHAIN / products);
     a.du_parts = a.slabs * tim::ag_planes(dtype);
     const int64_t per_row = int64_t(4) * a.du_parts * RP;
     a.row_part = static_cast<int32_t>(std::min<int64_t>(

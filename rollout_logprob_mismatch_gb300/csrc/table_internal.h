@@ -80,7 +80,17 @@ constexpr int AG_SMEM = 227 * 1024;
 constexpr int64_t AG_PARTIAL_BYTES = int64_t(1) << 30;   // du's partial sums at most, per part of the batch
 
 // Tiles of a slab: as many as dB's sums have TMEM for, beside two of du (512 columns).
-constexpr int ag_blocks(int RP) { return RP <= 32 ? 8 : 4; }
+constexpr int ag_blocks(int RP) { return RP == 16 ? 8 : RP == 32 ? 7 : 4; }
+
+// Products that go to one sum of dB in TMEM at most.  The tensor cores cut, rather than
+// round, what they add up, so a sum loses in proportion to its length (1.8e-8 of dB's norm a
+// product); after these many it is added in fp32 to what is in memory.  Errors of dB at 8200
+// rows an adapter and more: 5.0e-7 with 32, 7.5e-7 to 1.0e-6 with 48
+// (rank 64 of 4096 x 128256 bf16 618 us, 688 with 32), 1.0e-6 with 64.
+constexpr int AG_CHAIN = 48;
+
+// Products of 16 rows of dy with all parts of t (part p of one with part j of the other where p + j < 3).
+constexpr int ag_products(int planes) { return planes == 1 ? 3 : planes == 2 ? 5 : 6; }
 
 struct AdapterGradArgs {
     const uint16_t *h, *A, *B;
@@ -94,6 +104,7 @@ struct AdapterGradArgs {
     int32_t cols, slabs;      // columns of a slab, slabs
     int32_t merged;           // t's first two parts are one operand
     int32_t chains, low;      // sums of dB in TMEM that take steps of rows in turn; one more for the low products, or 0
+    int32_t link;             // rows of an adapter that go to them before they are written
     int32_t du_parts;         // parts of a sum of du: slabs times planes
     int32_t row_part;         // positions of a launch
     int32_t p0, p1, r0;       // the launch's positions and first rank
