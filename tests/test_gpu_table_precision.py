@@ -63,3 +63,96 @@ def test_dB_of_a_long_adapter(N, V, R, dtype):
     error = float((got - want).norm() / want.norm())
     print("dB of %d x %d %s, rank %d: %.2e of %.2e" % (N, V, dtype, R, error, bound))
     assert error <= bound
+
+
+# ----------------------------------------------------------------------------- parts
+def parts(x, k):
+    """What k bf16 parts hold of fp32 x, each the rest rounded to nearest."""
+    got, left = torch.zeros_like(x, dtype=F64), x.to(F64)
+    for _ in range(k):
+        p = left.float().to(torch.bfloat16).to(F64)
+        got, left = got + p, left - p
+    return got
+
+
+def mantissas(count, bits, gen):
+    """fp32 values in [1, 2) of `bits` bits; of 24: values of which two parts leave 2^-18 at least."""
+    x = 1 + torch.randint(0, 1 << (bits - 1), (64 * count,), generator=gen).to(F64) * 2.0 ** (1 - bits)
+    if bits == 24:
+        x = x[(parts(x.float(), 2) - x).abs() >= 2.0 ** -18]
+    return x[:count].float()
+
+
+def powers(shape, gen):
+    return (torch.randint(0, 2, shape, generator=gen) * 2 - 1) * 2.0 ** torch.randint(-3, 4, shape, generator=gen)
+
+
+def singles(M, V, R, dtype, seed):
+    """Two adapters of M rows each, R of which (in any order) have one logit, one element of h and
+    one rank of their own: every t, du and element of dh, dA, dB is one product, or zero."""
+    gen = torch.Generator().manual_seed(seed)
+    n, D, N = 2, R + 8, 2 * M + 3
+    order = torch.randperm(N, generator=gen)
+    rows, h, dy = torch.full((N,), -1, dtype=torch.int32), torch.zeros((N, D)), torch.zeros((N, V))
+    A, B, scale = torch.zeros((n, R, D)), torch.zeros((n, V, R)), mantissas(n, 24, gen)
+    bits = {"f32": 24, "bf16": 8, "f16": 11}[dtype]
+    at = []
+    for a in range(n):
+        mine = order[a * M:(a + 1) * M]
+        rows[mine] = a
+        i, r = mine[torch.randperm(M, generator=gen)[:R]], torch.arange(R)
+        v = torch.randperm(V, generator=gen)[:R]
+        v[0] = V - 1 if not bool((v[1:] == V - 1).any()) else v[0]
+        h[i, r], A[a, r, r], B[a, v, r] = powers((R,), gen), powers((R,), gen), powers((R,), gen)
+        dy[i, v] = (mantissas(R, bits, gen) * powers((R,), gen)).float()
+        at.append((i, v, r))
+    ad = tim.Adapters(A.to(torch.bfloat16).cuda(), B.to(torch.bfloat16).cuda(), scale.cuda())
+    return dy.to(TYPES[dtype]).cuda(), h.to(torch.bfloat16).cuda(), ad, rows.cuda(), at
+
+
+def off(got, want):
+    return float(((got.to(F64) - want) / want).abs().max())
+
+
+SINGLES = [(300, 130, 16), (150, 1000, 32), (200, 700, 64), (140, 300, 128), (60, 400, 24), (300, 33000, 16), (70, 33000, 40),
+           (100, 70000, 32), (100, 70000, 64), (150, 70000, 128), (40, 140000, 8), (50, 140000, 32), (80, 140000, 64)]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("M,V,R", SINGLES)
+def test_gradient_of_single_products(M, V, R, dtype):
+    """t, du and fp32 dlogits are held to 2^-24.  dB: what their three parts leave, the products
+    of parts that are left out, six cuts and the sums' joins: below 2^-19.  dA, dh: three cuts or
+    roundings of du's planes, one with the scale, what du's parts leave and three cuts: below 2^-20.
+    Two parts of any of them leave 2^-18 and more."""
+    dy, h, ad, rows, at = singles(M, V, R, dtype, M + V + R)
+    dh, dA, dB = tim.adapter_logits_backward(dy, h, ad, rows)
+    tim.check()
+    zero_h, zero_A, zero_B = dh.clone(), dA.clone(), dB.clone()
+    for a, (i, v, r) in enumerate(at):
+        d, s = dy[i, v].to(F64), ad.scale[a].to(F64)
+        x, w, b = h[i, r].to(F64), ad.A[a, r, r].to(F64), ad.B[a, v, r].to(F64)
+        t, du = s * x * w, s * b * d
+        assert off(dB[a, v, r], d * t) <= 2.0 ** -19
+        assert off(dA[a, r, r], du * x) <= 2.0 ** -20 and off(dh[i, r], du * w) <= 2.0 ** -20
+        short = parts((s * x * w).float().cpu(), 2).cuda()   # the bounds tell: t, then dlogits and du, in two parts
+        assert off(d * short, d * t) > 2.0 ** -19
+        assert off(parts(du.float().cpu(), 2).cuda() * x, du * x) > 2.0 ** -20
+        if dtype == "f32":
+            assert off(parts(dy[i, v].cpu(), 2).cuda() * t, d * t) > 2.0 ** -19
+        zero_h[i, r], zero_A[a, r, r], zero_B[a, v, r] = 0, 0, 0
+    assert not bool(zero_h.any()) and not bool(zero_A.any()) and not bool(zero_B.any())
+
+
+@pytest.mark.parametrize("M,V,R", SINGLES)
+def test_fp32_logits_of_single_products(M, V, R):
+    """t of fp32 logits is held to 2^-24; three cuts, one rounding: below 2^-21."""
+    dy, h, ad, rows, at = singles(M, V, R, "f32", M + V + R)
+    out = tim.adapter_logits(torch.zeros_like(dy), h, ad, rows)
+    tim.check()
+    for a, (i, v, r) in enumerate(at):
+        t, b = ad.scale[a].to(F64) * h[i, r].to(F64) * ad.A[a, r, r].to(F64), ad.B[a, v, r].to(F64)
+        assert off(out[i, v], t * b) <= 2.0 ** -21
+        assert off(parts(t.float().cpu(), 2).cuda() * b, t * b) > 2.0 ** -21
+        out[i, v] = 0
+    assert not bool(out.any())
