@@ -2,6 +2,8 @@
 // values and the warp's 16 x 8 x 16 product.
 #pragma once
 
+#include <cfloat>
+
 #include "logits_rows.cuh"
 
 namespace tim {
@@ -21,15 +23,18 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
 
 // x = p[0] + p[1] + ... up to half a unit of the last part: each part is what the ones
 // before leave, rounded to bf16 (2^-8 of it at most, so two parts leave 2^-16 |x| and
-// three 2^-24).  An infinite or NaN x is all in part 0.
+// three 2^-24).  A finite x above bf16's largest value has that as its part 0; an infinite
+// or NaN x is all in part 0.
 template <int PARTS> __device__ __forceinline__ void split_bf16(float x, uint16_t (&p)[PARTS])
 {
-    const bool finite = fabsf(x) <= 3.38953139e38f;   // bf16's largest
+    const bool finite = fabsf(x) <= FLT_MAX;
 #pragma unroll
     for (int i = 0; i < PARTS; ++i) {
-        const __nv_bfloat16 b = __float2bfloat16_rn(x);
-        p[i] = i == 0 || finite ? __bfloat16_as_ushort(b) : uint16_t(0);
-        x -= __bfloat162float(b);
+        uint16_t b = __bfloat16_as_ushort(__float2bfloat16_rn(x));
+        if (i == 0 && finite && (b & 0x7fffu) == 0x7f80u)
+            b -= 1;   // rounded to infinity: the largest of its sign
+        p[i] = i == 0 || finite ? b : uint16_t(0);
+        x -= __uint_as_float(static_cast<uint32_t>(b) << 16);
     }
 }
 

@@ -156,3 +156,34 @@ def test_fp32_logits_of_single_products(M, V, R):
         assert off(parts(t.float().cpu(), 2).cuda() * b, t * b) > 2.0 ** -21
         out[i, v] = 0
     assert not bool(out.any())
+
+
+@pytest.mark.parametrize("R", [16, 32, 64, 128])
+@pytest.mark.parametrize("x", [3.4e38, -3.3961e38, 3.392e38])
+def test_values_between_bf16s_largest_and_fp32s(x, R):
+    """Finite fp32 values that a bf16 part rounds to infinity, or whose rest it loses."""
+    N, V, D = 3, 200, 64
+    rows = torch.tensor([0, -1, 0], dtype=torch.int32, device="cuda")
+    z = torch.zeros((N, V), device="cuda")
+    h, A, B = torch.zeros((N, D), device="cuda"), torch.zeros((1, R, D), device="cuda"), torch.zeros((1, V, R), device="cuda")
+    h[2, 5], A[0, 3, 5], B[0, 150, 3] = 1.0, 1.0, 2.0 ** -20
+    h, A, B = (y.to(torch.bfloat16) for y in (h, A, B))
+    big = torch.full((1,), x, device="cuda")
+    value = float(big.to(F64))
+    out = tim.adapter_logits(z, h, tim.Adapters(A, B, big), rows)
+    assert abs(float(out[2, 150].to(F64)) / (value * 2.0 ** -20) - 1) <= 2.0 ** -21 and int((out != 0).sum()) == 1
+    # t, then du, of that size; then dlogits
+    dy = z.clone()
+    dy[2, 150] = 2.0 ** -4
+    dh, dA, dB = tim.adapter_logits_backward(dy, h, tim.Adapters(A, B * 16, big), rows)
+    assert abs(float(dB[0, 150, 3].to(F64)) / (value * 2.0 ** -4) - 1) <= 2.0 ** -19
+    dh, dA, dB = tim.adapter_logits_backward(dy, h * 2.0 ** -6, tim.Adapters(A * 2.0 ** -6, B * 2.0 ** 24, big), rows)
+    assert abs(float(dA[0, 3, 5].to(F64)) / (value * 2.0 ** -6) - 1) <= 2.0 ** -20
+    assert abs(float(dh[2, 5].to(F64)) / (value * 2.0 ** -6) - 1) <= 2.0 ** -20
+    dy[2, 150] = big[0]
+    dh, dA, dB = tim.adapter_logits_backward(dy, h, tim.Adapters(A * 2.0 ** -20, B), rows)
+    tim.check()
+    assert abs(float(dB[0, 150, 3].to(F64)) / (value * 2.0 ** -20) - 1) <= 2.0 ** -19
+    assert abs(float(dA[0, 3, 5].to(F64)) / (value * 2.0 ** -20) - 1) <= 2.0 ** -20
+    for got in (dh, dA, dB):
+        assert int((got != 0).sum()) == 1
