@@ -398,6 +398,11 @@ __global__ void __launch_bounds__(AD_MAP_THREADS, CB == 1 && RP <= 32 ? 3 : 2) a
         const uint64_t pol = l2_policy_evict_first(), pol_keep = l2_policy_evict_normal();
         int stage = 0, slot = 0, held = -1;   // held: the adapter of the last factor copied
         uint32_t phase = 0, fphase = 0;
+        uint32_t used = 0, parity = 0;   // barriers filled (stages from bit 0, factors from bit 8 on), parity of their last fill
+        auto filled = [&](int bit, uint32_t p) {
+            used |= 1u << bit;
+            parity = (parity & ~(1u << bit)) | p << bit;
+        };
         bool ok = true;
         for (int p = 0; ok && p < rows; p += 16) {
             ok = warp_wait(empty(stage), phase ^ 1u, abort_flag, budget);
@@ -418,6 +423,7 @@ __global__ void __launch_bounds__(AD_MAP_THREADS, CB == 1 && RP <= 32 ? 3 : 2) a
                 bulk_load(dst + lane * S::ROW + c.off, c.src, c.bytes, full(stage), pol);
             if (lane == 0)
                 bulk_load(dst + 16 * S::ROW, a.plan.t + static_cast<size_t>(p0 + p) * (S::TROW / 2), tbytes, full(stage), pol_keep);
+            filled(stage, phase);
             if (++stage == a.stages) {
                 stage = 0;
                 phase ^= 1u;
@@ -439,12 +445,20 @@ __global__ void __launch_bounds__(AD_MAP_THREADS, CB == 1 && RP <= 32 ? 3 : 2) a
                     bulk_load(factor0 + slot * S::FACTOR, a.B + (static_cast<size_t>(held) * a.V + c0) * a.R, bytes, ffull(slot),
                               pol_keep);
                 }
+                filled(8 + slot, fphase);
                 if (++slot == a.factors) {
                     slot = 0;
                     fphase ^= 1u;
                 }
             }
         }
+        // no copy is in flight when the CTA leaves
+        if (lane == 0) {
+            for (int i = 0; i < 16; ++i)
+                if (used >> i & 1u)
+                    drain_wait(bar0 + 8u * i, parity >> i & 1u);
+        }
+        __syncwarp();
     } else {
         // ------------------------------------------------------------ products
         const int w0 = warp * 32 * CB;   // the warp's columns in the slab
@@ -590,15 +604,8 @@ __global__ void __launch_bounds__(AD_MAP_THREADS, CB == 1 && RP <= 32 ? 3 : 2) a
         }
     }
     __syncthreads();
-    if (tid == 0 && *abort_flag) {
-        // copies may still be on their way: every stage's and buffer's last one lands, or not, within the wait
-        for (int i = 0; i < 4; ++i)
-            for (uint32_t f = 0; f < 2; ++f) {
-                drain_wait(full(i), f, 100000000ull);
-                drain_wait(ffull(i), f, 100000000ull);
-            }
+    if (tid == 0 && *abort_flag)
         atomicCAS(a.status, 0, static_cast<int>(TIM_ERR_TIMEOUT));
-    }
 }
 
 template <typename F>
