@@ -14,6 +14,7 @@
 
 #include "adapters.cuh"
 #include "table_internal.h"
+#include "tim_internal.h"
 
 namespace tim {
 namespace {
@@ -80,6 +81,7 @@ __device__ __forceinline__ Own count_rows(const AdapterArgs &a, int ad)
 
 __device__ __forceinline__ void write_order(const AdapterArgs &a, int ad, const Own &o)
 {
+    TIM_DCHECK(o.base + o.count <= a.N && (ad < a.n || o.base + o.count == a.N), a.status, TIM_CHECK_UNIT, ad, o.base);
     if (threadIdx.x == 0) {
         a.plan.offsets[ad] = o.base;
         if (ad == a.n)
@@ -87,6 +89,7 @@ __device__ __forceinline__ void write_order(const AdapterArgs &a, int ad, const 
     }
     if (o.own > 0)
         own_rows(a, ad, o.r0, o.r1, o.base + o.before, [&](int r, int p) {
+            TIM_DCHECK(p < o.base + o.count, a.status, TIM_CHECK_STORE, p, r);
             a.plan.perm[p] = r;
             a.plan.adapter[p] = ad;
         });
@@ -106,6 +109,10 @@ __device__ __forceinline__ void project(const AdapterArgs &a, int ad, const int3
     const int kchunks = (a.D + 31) / 32;
     const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
     const bool on0 = g >= lo && g < hi, on1 = g + 8 >= lo && g + 8 < hi;
+    TIM_DCHECK((!on0 || static_cast<unsigned>(rows[g]) < static_cast<unsigned>(a.N)) &&
+                   (!on1 || static_cast<unsigned>(rows[g + 8]) < static_cast<unsigned>(a.N)),
+               a.status, TIM_CHECK_UNIT, pos + g, ad);
+    TIM_DCHECK(static_cast<unsigned>(ad) < static_cast<unsigned>(a.n) && pos + hi <= a.N, a.status, TIM_CHECK_STORE, pos, ad);
     const uint16_t *h0 = a.h + static_cast<size_t>(on0 ? rows[g] : 0) * a.D;
     const uint16_t *h1 = a.h + static_cast<size_t>(on1 ? rows[g + 8] : 0) * a.D;
     for (int n0 = 0; n0 < RP; n0 += NC) {
@@ -171,6 +178,7 @@ __device__ __forceinline__ void pad_rows(const AdapterArgs &a, int ad, int count
     if (a.plan.t_pad == 0)
         return;
     const int words = (-count & (AG_PAD - 1)) * (a.plan.t_pitch / 2);
+    TIM_DCHECK(end <= a.N, a.status, TIM_CHECK_STORE, end, ad);
     uint32_t *t = reinterpret_cast<uint32_t *>(a.plan.t + (static_cast<size_t>(end) + static_cast<size_t>(ad) * a.plan.t_pad) * a.plan.t_pitch);
     for (int i = threadIdx.x; i < words; i += blockDim.x)
         t[i] = 0u;
@@ -386,6 +394,8 @@ __global__ void __launch_bounds__(AD_MAP_THREADS, CB == 1 && RP <= 32 ? 3 : 2) a
     for (int i = tid; i < rows; i += AD_MAP_THREADS) {
         s_row[i] = a.plan.perm[p0 + i];
         s_ad[i] = a.plan.adapter[p0 + i];
+        TIM_DCHECK(static_cast<unsigned>(s_row[i]) < static_cast<unsigned>(a.N) && s_ad[i] >= 0 && s_ad[i] <= a.n, a.status,
+                   TIM_CHECK_UNIT, p0 + i, s_ad[i]);
     }
     if (tid == 0)
         s_ad[rows] = -1;
@@ -419,6 +429,12 @@ __global__ void __launch_bounds__(AD_MAP_THREADS, CB == 1 && RP <= 32 ? 3 : 2) a
             if (lane == 0)
                 mbar_arrive_expect_tx(full(stage), total);
             __syncwarp();
+            TIM_DCHECK(((reinterpret_cast<uintptr_t>(c.src) | c.off | c.bytes | tbytes |
+                         reinterpret_cast<uintptr_t>(a.plan.t + static_cast<size_t>(p0 + p) * (S::TROW / 2))) & 15) == 0 &&
+                           c.off + c.bytes <= S::ROW && (lane >= m || c.bytes == 0 ||
+                           (c.src >= reinterpret_cast<const char *>(z + static_cast<size_t>(s_row[p + lane]) * a.ld) &&
+                            c.src + c.bytes <= reinterpret_cast<const char *>(z + static_cast<size_t>(s_row[p + lane]) * a.ld + a.V))),
+                       a.status, TIM_CHECK_BULK, p0 + p + lane, c.bytes);
             if (c.bytes)
                 bulk_load(dst + lane * S::ROW + c.off, c.src, c.bytes, full(stage), pol);
             if (lane == 0)
@@ -441,6 +457,7 @@ __global__ void __launch_bounds__(AD_MAP_THREADS, CB == 1 && RP <= 32 ? 3 : 2) a
                     break;
                 if (lane == 0) {
                     const uint32_t bytes = static_cast<uint32_t>(c1 - c0) * a.R * 2;
+                    TIM_DCHECK((bytes & 15) == 0 && bytes <= S::FACTOR, a.status, TIM_CHECK_BULK, held, bytes);
                     mbar_arrive_expect_tx(ffull(slot), bytes);
                     bulk_load(factor0 + slot * S::FACTOR, a.B + (static_cast<size_t>(held) * a.V + c0) * a.R, bytes, ffull(slot),
                               pol_keep);

@@ -31,6 +31,7 @@
 
 #include "adapters.cuh"
 #include "table_internal.h"
+#include "tim_internal.h"
 
 namespace tim {
 namespace {
@@ -251,6 +252,9 @@ __global__ void __launch_bounds__(Shape<T, HOW, RP>::THREADS, 1)
             for (int p = b; p < e; p += STEP) {
                 if (!warp_wait(tempty(tr.slot), tr.parity ^ 1u, abort_flag, budget))
                     return false;
+                // t has its zeros up to a multiple of 16 of the adapter's rows
+                TIM_DCHECK(p + ad * AG_PAD + (min(STEP, e - p) + 15) / 16 * 16 <= a.N + a.n * AG_PAD && a.r0 % 8 == 0, a.status,
+                           TIM_CHECK_TMA_COORD, p, ad);
                 if (lane == 0) {
                     mbar_arrive_expect_tx(tfull(tr.slot), (a.merged ? 4 : PARTS) * STEP * S::SPAN);
                     // part by part; or the first two side by side, then the third beside zeros (past t's last column)
@@ -409,6 +413,7 @@ __global__ void __launch_bounds__(Shape<T, HOW, RP>::THREADS, 1)
                                 static_cast<size_t>(blockIdx.x * S::PLANES + m / STEP) * (RP / 4) * count + (at - a.p0);
                     auto put = [&](int r0, const float (&v)[RC]) {
                         if (at < e && m / STEP < S::PLANES) {
+                            TIM_DCHECK(at >= a.p0 && at - a.p0 < static_cast<int>(count) && r0 + RC <= RP, a.status, TIM_CHECK_STORE, at, ad);
 #pragma unroll
                             for (int r = 0; r < RC / 4; ++r)
                                 o[(r0 / 4 + r) * count] = make_float4(v[4 * r], v[4 * r + 1], v[4 * r + 2], v[4 * r + 3]);
@@ -516,12 +521,16 @@ __global__ void __launch_bounds__(Shape<T, HOW, RP>::THREADS, 1)
         auto place = [&](int m) {
             return static_cast<uint32_t>((chunk >> 3) * SUB + m * 128 + (((chunk & 7) ^ (m & 7)) << 4));
         };
+        auto in_batch = [&](int r) {
+            TIM_DCHECK(static_cast<unsigned>(r) < static_cast<unsigned>(a.N), a.status, TIM_CHECK_UNIT, r, blockIdx.x);
+            return static_cast<size_t>(r);
+        };
         const T *row[ROWS];   // of the step, from the slab's (COPY: the thread's) first column on; null: past its last
         const int mine = HOW == COPY ? chunk * 8 : 0;
         auto look_up = [&](int p, int rows) {
 #pragma unroll
             for (int i = 0; i < ROWS; ++i)
-                row[i] = r0 + EACH * i < rows ? dy + static_cast<size_t>(a.plan.perm[p + r0 + EACH * i]) * a.ld + c0 + mine : nullptr;
+                row[i] = r0 + EACH * i < rows ? dy + in_batch(a.plan.perm[p + r0 + EACH * i]) * a.ld + c0 + mine : nullptr;
         };
         if constexpr (HOW == COPY) {
             Ring st(S::STAGES);
@@ -757,6 +766,7 @@ template <int RP> __global__ void __launch_bounds__(256) adapters_fold_kernel(co
     split_bf16<3>(s.y * scale, x1);
     split_bf16<3>(s.z * scale, x2);
     split_bf16<3>(s.w * scale, x3);
+    TIM_DCHECK(a.r0 + r + 4 <= a.RT, a.status, TIM_CHECK_STORE, pos, a.r0 + r);
     uint16_t *du = a.du + static_cast<size_t>(pos) * (3 * a.RT) + a.r0 + r;
 #pragma unroll
     for (int j = 0; j < 3; ++j)
@@ -794,6 +804,7 @@ template <int RT> __device__ __forceinline__ void dA_part(const AdapterGradArgs 
         for (int i = 0; i < ROWS / 16; ++i) {
             const int at = p + tid / 16 + i * 16;
             row[i] = at < e ? a.plan.perm[at] : -1;
+            TIM_DCHECK(row[i] < a.N && (at >= e || row[i] >= 0), a.status, TIM_CHECK_UNIT, at, row[i]);
         }
     };
     auto fill = [&](int stage, int p) {
@@ -898,6 +909,7 @@ template <int RT> __device__ __forceinline__ void dh_part(const AdapterGradArgs 
             for (int half = 0; half < 2; ++half) {
                 const int i = at + g + half * 8;
                 row[half] = i < e ? a.plan.perm[i] : -1;
+                TIM_DCHECK(row[half] < a.N && (i >= e || row[half] >= 0), a.status, TIM_CHECK_STORE, i, row[half]);
 #pragma unroll
                 for (int part = 0; part < 3; ++part)
 #pragma unroll

@@ -15,6 +15,7 @@
 
 #include "logits_rows.cuh"
 #include "table_internal.h"
+#include "tim_internal.h"
 
 namespace tim {
 namespace {
@@ -121,6 +122,7 @@ __global__ void __launch_bounds__(EM_SORT_THREADS) embedding_sort_kernel(const E
             const int id = n + lane < n1 ? a.tokens[n + lane] : -1;
             const bool in = id >= lo && id < hi;
             const unsigned all = __ballot_sync(0xffffffffu, in);
+            TIM_DCHECK(!in || at + __popc(all) <= base + total, a.status, TIM_CHECK_STORE, n + lane, id);
             if (in)
                 a.staged[at + __popc(all & ((1u << lane) - 1u))] = make_int2(id, n + lane);
             at += __popc(all);
@@ -179,6 +181,7 @@ __global__ void __launch_bounds__(EM_SORT_THREADS) embedding_sort_kernel(const E
             if (x[i].x >= 0 && rank == 0)
                 counts[warp][x[i].x - lo] += __popc(same);
             __syncwarp();
+            TIM_DCHECK(x[i].x < 0 || (to >= base && to < base + total), a.status, TIM_CHECK_STORE, to, x[i].x);
             if (x[i].x >= 0) {
                 a.order[to] = x[i].y;
                 a.ids[to] = x[i].x;
@@ -282,6 +285,7 @@ __device__ __forceinline__ void sum_positions(float (&acc)[EM_PIECES][8], const 
     const int lane = threadIdx.x & 31;
     for (int p0 = b; p0 < e; p0 += 32) {
         const int mine = p0 + lane < e ? a.order[p0 + lane] : 0;
+        TIM_DCHECK(static_cast<unsigned>(mine) < static_cast<unsigned>(a.N), a.status, TIM_CHECK_UNIT, p0 + lane, mine);
         const int count = min(32, e - p0);
         for (int j = 0; j < count; j += EM_AHEAD) {
             Pieces<T, VEC> r[EM_AHEAD];
@@ -341,6 +345,8 @@ __global__ void __launch_bounds__(256, 2) embedding_tiles_kernel(const Embedding
     for (int k = 0; k < 2; ++k) {   // an id of more than a tile's tokens is the tile's first or its last
         const int id = a.ids[k == 0 ? p0 : p1 - 1];
         const int b = a.offsets[id], e = a.offsets[id + 1];
+        TIM_DCHECK(static_cast<unsigned>(id) < static_cast<unsigned>(a.V) && b >= 0 && b < e && e <= total, a.status, TIM_CHECK_UNIT,
+                   tile, id);
         if (e - b <= a.many || (b >= p0) != (k == 1))
             continue;
         float acc[EM_PIECES][8] = {};
@@ -369,6 +375,8 @@ template <typename T, bool VEC> __global__ void __launch_bounds__(256, 2) embedd
         my_id = a.ids[u0 + lane];
         my_b = a.offsets[my_id];
         my_e = a.offsets[my_id + 1];
+        TIM_DCHECK(static_cast<unsigned>(my_id) < static_cast<unsigned>(a.V) && my_b <= u0 + lane && u0 + lane < my_e && my_e <= total,
+                   a.status, TIM_CHECK_STORE, u0 + lane, my_id);
     }
     for (unsigned first = __ballot_sync(0xffffffffu, my_b == u0 + lane); first; first &= first - 1) {
         const int from = __ffs(first) - 1;

@@ -207,6 +207,7 @@ int tim_adapter_logits_backward(const void *dlogits, int dtype, int64_t N, int64
     f.D = static_cast<int32_t>(D);
     f.R = adapters->rank;
     f.n = adapters->num_adapters;
+    f.status = status;
     tim::AdapterGradArgs a{};
     a.h = f.h;
     a.A = f.A;
@@ -311,6 +312,7 @@ int tim_embedding(const int32_t *tokens, int64_t N, const void *W, int dtype, in
     a.V = static_cast<int32_t>(V);
     a.D = static_cast<int32_t>(D);
     a.scale = scale;
+    a.status = status;
     a.x = W;
     a.out = out;
     return finish(tim::embedding_launch(a, dtype, out_dtype, reinterpret_cast<cudaStream_t>(stream)), cudaSuccess,
@@ -346,6 +348,7 @@ int tim_embedding_backward(const int32_t *tokens, int64_t N, const void *grad, i
     a.V = static_cast<int32_t>(V);
     a.D = static_cast<int32_t>(D);
     a.scale = scale;
+    a.status = status;
     a.x = grad;
     a.dW = dW;
     a.accumulate = accumulate_dW != 0;

@@ -142,6 +142,7 @@ struct EmbeddingArgs {
     int2 *staged;             // [N] scratch of the sort
     int32_t tile, many;       // positions of a tile; tokens of an id above which it is summed in tiles (>= tile)
     float *partial;           // [ceil(N / tile)][2][D]
+    int *status;
 };
 
 cudaError_t embedding_launch(const EmbeddingArgs &a, int dtype, int out_dtype, cudaStream_t s);
