@@ -66,6 +66,10 @@ template <typename T, int HOW, int RP> struct Shape {
     static constexpr int THREADS = (6 + WRITERS) * 32;
     static constexpr uint32_t TMEM = 512;                      // du twice, dB's blocks
     static constexpr int CHAIN = 4;                            // tiles of a sum of du in TMEM
+    // tiles whose sums of dB are free again together: one (4096 x 128256, rank 64 of 2: bf16 612 us, 681 with
+    // four; fp16 1035, 1139), or four where the issue of the products is the narrow part (fp32, rank 32:
+    // 1024 x 129280 302 us, 308 with one)
+    static constexpr int FREED = PLANES == 3 && RP <= 32 ? CHAIN : 1;
     static_assert(RP <= 32 || CHAIN >= BLOCKS, "ranks beyond 32 are not added up in registers");
     static_assert(STAGES >= 2 && (HOW == COPY || BATCHES >= 2) && (2 + BLOCKS) * RP <= 512, "shared memory, TMEM");
 };
@@ -341,12 +345,14 @@ __global__ void __launch_bounds__(Shape<T, HOW, RP>::THREADS, 1)
                     if (c % S::CHAIN == 0) {
                         if (!warp_wait(duempty(du.slot), du.parity ^ 1u, abort_flag, budget))
                             return false;
+                        // the first tiles go on while the last ones' sums are written
+                        if (S::FREED == S::CHAIN && p == link && !warp_wait(dbempty(db.slot, c / S::CHAIN), db.parity ^ 1u, abort_flag, budget))
+                            return false;
                     }
+                    if (S::FREED == 1 && p == link && !warp_wait(dbempty(db.slot, c), db.parity ^ 1u, abort_flag, budget))
+                        return false;
                     const uint32_t td = tmem + du.slot * RP;
                     if (!warp_wait(full(st.slot), st.parity, abort_flag, budget))
-                        return false;
-                    // tile by tile, so that the first ones go on while the last ones' sums are written
-                    if (p == link && !warp_wait(dbempty(db.slot, c), db.parity ^ 1u, abort_flag, budget))
                         return false;
                     // the writers' shared memory for the products: the fence stands here, since a
                     // writer's would wait for its copies of later tiles too
@@ -485,11 +491,11 @@ __global__ void __launch_bounds__(Shape<T, HOW, RP>::THREADS, 1)
                                 add_up(tb + a.chains * db_chain + r0);
                             }
                         }
-                        if (r0 + DC >= min(RP, a.R - a.r0) && some) {   // the tile's last ranks are read
+                        if (some && r0 + DC >= min(RP, a.R - a.r0) && ((c + 1) % S::FREED == 0 || c + 1 == blocks)) {   // the last ranks are read
                             tc_fence_before();
                             __syncwarp();
                             if (lane == 0)
-                                mbar_arrive(dbempty(db.slot, c));
+                                mbar_arrive(dbempty(db.slot, c / S::FREED));
                         }
                         if (col >= a.V)
                             continue;
