@@ -571,9 +571,10 @@ typedef struct {
 
 /* The adapters' part of a head's logits, for rows that belong to different requests:
  *   y_iv = z_iv + sum_r t_ir B_a[v, r],  t_i = scale_a A_a h_i,  a = rows[i],
- * with fp32 sums (t is held to 2^-16 of its value for 16-bit logits, 2^-24 for fp32
- * ones) and one rounding to the logits' type.  Before tim_process_logits in an engine,
- * before tim_processed_logprob in a trainer.
+ * with fp32 sums (t is held to 2^-24 of its value for fp32 logits, 2^-16 for 16-bit
+ * ones: an fp16 logit that its adapter's part nearly cancels has few bits left) and one
+ * rounding to the logits' type.  Before tim_process_logits in an engine, before
+ * tim_processed_logprob in a trainer.
  *   logits, dtype, N, V, stride   as above, N < 2^30
  *   h      bf16 [N, D], 16-byte aligned, D a multiple of 8 up to 65536
  *   rows   int32 [N]: the row's adapter; outside [0, num_adapters): none, the row's
@@ -594,11 +595,11 @@ TIM_API int tim_adapter_logits(const void *logits, int dtype, int64_t N, int64_t
  *   dB_a = sum_i dy_i t_i^T,  dA_a = sum_i du_i h_i^T,  dh_i = A_a^T du_i,
  * over the rows i of adapter a.  The shared head's part, dh += dlogits W, is the
  * caller's (accumulate_dh adds to it); dL / dz is dlogits itself.  fp32 sums; t, du and
- * fp32 dlogits are held to 2^-24 of their values, 16-bit dlogits exactly; an infinity
- * in dlogits or B may come out as a NaN, and reaches its own adapter and rows only.
- * The tensor cores cut what they add up: dB is added in fp32 from sums of at most 48 products of
- * 16 rows, so that its error does not grow with the adapter's rows (1e-6 of its norm; sums
- * below 2^-126 of an adapter of more rows than one sum takes may count as zero).
+ * fp32 dlogits are held to 2^-24 of their values (those below 2^-110 to 2^-134), 16-bit
+ * dlogits exactly; an infinity in dlogits or B may come out as a NaN, and reaches its own
+ * adapter and rows only.  The tensor cores cut what they add up, so dB is added up in fp32
+ * from sums of at most 48 products of 16 rows each: its error, some 1e-6 of its norm, does
+ * not grow with the adapter's rows (sums below 2^-126 may count as zero there).
  *   dlogits, dtype, N, V, stride, h, D, adapters, rows   as above
  *   dh   fp32 [N, D], 16-byte aligned; rows under no adapter: zeros (with accumulate_dh
  *        not touched)

@@ -214,9 +214,11 @@ __global__ void __launch_bounds__(512, 1) adapters_shrink_kernel(const AdapterAr
     }
 }
 
-// Many rows: the order in a launch of its own (8192 rows 6 us), then a CTA for every 16 positions
-// (two an SM where there are that many, else one with more loads in flight): 8192 x 4096, rank 16,
-// 24 us (h read at 2.9 TB/s; the factors come from L2 for every 16 rows).
+// Many rows: the order in a launch of its own (8192 rows 6 us), then a CTA for every 16 positions:
+// two an SM where there are that many (8192 rows of rank 16: whole call on 8192 columns 99 us, 104 with one
+// an SM; at rank 64 one would win, 246 for 283), else one with more loads in flight (1000 rows of
+// rank 64: 68 us, 104 with two).  8192 x 4096, rank 16, 25 us (h read at 2.7 TB/s; the factors come from
+// L2 for every 16 rows).
 __global__ void __launch_bounds__(512) adapters_order_kernel(const AdapterArgs a)
 {
     pdl_wait();
@@ -317,7 +319,8 @@ template <int RP> struct Ranks {
     static constexpr int WORDS = STEP / 2;
     // A warp keeps its part of a factor in registers, so that the buffer is free at once (256 x 151936
     // bf16, rank 32 of 64: 154 us, 167 without).  At rank 16 it takes the room of the wide form
-    // (8192 x 151936: 1129 us, 878 without); at 64 it gains 1 %; at 128 there is no room.
+    // (8192 x 151936: 1190 us, 906 without) and gains nothing in the narrow one for bf16 (64 x 128256 of
+    // 32: 54 us either way; 2048 x 151936 fp32 420 for 430); at 64 it gains 1 %; at 128 there is no room.
     static constexpr bool HELD = RP == 32;
 };
 
@@ -692,8 +695,9 @@ template <typename T, int PARTS, int RP, int CB> cudaError_t map(AdapterArgs a, 
                   S::bytes(a.stages, a.factors), a, s);
 }
 
-// A warp has 32 columns, or 64 (128 bytes of a row) of 16-bit logits at the smallest
-// ranks, where a batch is large enough to be bound by them.
+// A warp has 32 columns, or 64 (128 bytes of a row) of 16-bit logits at the smallest ranks, where a
+// batch is large enough to be bound by them (8192 x 151936 bf16: 910 us, 1150 with 32; 2400 x 8192, below
+// the rule, 48 us with 32 columns, 56 with 64).
 template <typename T, int PARTS, int RP> cudaError_t map(const AdapterArgs &a, int num_sms, cudaStream_t s, bool set)
 {
     if constexpr (sizeof(T) == 2 && RP == 16) {

@@ -5,26 +5,29 @@
 //   du_i = s_a B_a^T dy_i          [R]
 //   dA_a = sum_i du_i h_i^T        [R, D]
 //   dh_i (+)= A_a^T du_i           [D]
-// dy is by far the largest operand and is read once: a CTA owns a slab of the vocabulary
-// (up to 1024 columns) and walks all rows, adapter by adapter in steps of 128, so that
-// dB's part of the slab stays in TMEM for up to a.link rows of the adapter (the tensor cores
-// cut what they add up: a chain over all of 8200 rows lost 1e-5 to 5e-5 of dB) and then
-// goes to memory, further links' added to it, and du of a step (the slab's part of the sum
-// over V) goes to a partial array that a second launch folds in slab order.  Both products take the same tile [128 rows x 128 columns] from shared
-// memory (tcgen05.mma, bf16 -> fp32): du with the rows as M and the columns as K
-// (K-major), dB with the columns as M and the rows as K (MN-major, the same bytes).
+// dy is by far the largest operand and is read once for every 64 ranks: a CTA owns a slab of the
+// vocabulary (up to 1024 columns) and walks all rows, adapter by adapter in steps of 128 rows
+// (bf16), 64 (fp16) or 32 (fp32).  du of a step (the slab's part of the sum over V) goes to a
+// partial array that a second launch folds in slab order.  dB's part of the slab stays in
+// TMEM for up to a.link rows of the adapter and then goes to memory, where the next link's is
+// added: the tensor cores cut what they add up, and one sum over all of 8200 rows lost 4e-6 to
+// 5e-5 of dB.  Both products take the same tile, 128 columns of a step, from shared memory
+// (tcgen05.mma, bf16 -> fp32; a step's planes of bf16 parts lie behind each other as its 128
+// rows): du with the rows as M and the columns as K (K-major), dB with the columns as M and
+// the rows as K (MN-major, the same bytes).
 //   warp 0      the adapter's factor and t, by TMA
-//   warp 1      one thread issues the products
+//   warp 1      issues the products, one lane of the converged warp
 //   warps 2-5   du and dB from TMEM to memory
-//   warps 6-    the tiles (the rows of an adapter lie anywhere): 16-byte asynchronous
-//               copies to their swizzled places; fp32, fp16 and rows off a 16-byte boundary
-//               (RAW) by plain loads, as planes of bf16 parts: one, two (fp16, exactly), or
-//               three (fp32: 2^-24 of it is left at most)
+//   warps 6-    the tiles (the rows of an adapter lie anywhere).  COPY, bf16 rows that start on
+//               16 bytes: 16-byte asynchronous copies to their swizzled places.  LOAD (fp32 and
+//               fp16 rows that start there) and ANY: such copies into a ring of whole rows, a
+//               row's ends by plain loads, and from there as planes of bf16 parts: one, two
+//               (fp16, exactly), or three (fp32: 2^-24 of it is left at most)
 // (TMA gathers of four rows brought the same tiles at 2 us a tile of 32 KB and SM.)
 // Measured, dy's pass alone, inputs out of L2: 4096 x 128256 bf16, rank 16 of 8 adapters, 207 us
-// (1.02 GB, 62 % of DRAM's nominal peak; what is left are the drains of dB between adapters
-// and slabs that fill 143 of 152 SMs); 1024 x 129280 fp32, rank 32 of 3, 218 us (issue slots 52 %:
-// the rewriting, and nine products of parts a tile); 500 x 50261 fp16 off 16 bytes 65 us.
+// (1.02 GB, 62 % of DRAM's nominal peak; what is left are the drains of dB and slabs that fill
+// 143 of 152 SMs); 1024 x 129280 fp32, rank 32 of 3, 223 us (issue slots 51 %: the rewriting, and
+// nine products of parts a tile); 500 x 50261 fp16 off 16 bytes 64 us.
 // Every sum has one order, fixed by the rows' order and V: the same call gives the same bits.
 #include <algorithm>
 #include <type_traits>
@@ -159,7 +162,7 @@ __global__ void __launch_bounds__(Shape<T, HOW, RP>::THREADS, 1)
 {
     using S = Shape<T, HOW, RP>;
     constexpr int STEP = S::STEP, SUB = S::SUB;
-    // M = 128 in both: du's rows are the tile's (the two planes' products are two parts of the sum)
+    // M = 128 in both: du's rows are the tile's (each plane's product is a part of the sum)
     constexpr uint32_t IDESC_DU = idesc_bf16_f32(128, RP, false, true), IDESC_DB = idesc_bf16_f32(BC, RP, true, true),
                        IDESC_DB2 = idesc_bf16_f32(BC, 2 * RP, true, true);
     extern __shared__ uint8_t smem_raw[];
@@ -290,7 +293,7 @@ __global__ void __launch_bounds__(Shape<T, HOW, RP>::THREADS, 1)
         Ring st(S::STAGES), tr(S::TS), fr(num_factors), du(2), db(num_db);
         constexpr uint32_t KHI = static_cast<uint32_t>(desc_kmajor_hi()), MHI = static_cast<uint32_t>(desc_mnmajor_hi());
         // du += tile x factor, 16 columns at a time, and dB += tile^T x t, 16 rows at a time,
-        // in turn (neither waits for itself); products of parts below 2^-16 of the first's are left out.
+        // in turn (neither waits for itself); products of parts of 2^-24 of the first's are left out.
         // The first parts' products go to tb, all others to low: the tensor cores cut, rather
         // than round, what they add up, and the chain of the first is as short as can be.
         auto tile_products = [&](auto merged, auto whole, uint32_t tile, uint32_t td, uint32_t tb, uint32_t low, uint32_t fd,

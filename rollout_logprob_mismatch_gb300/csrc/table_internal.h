@@ -26,7 +26,12 @@ inline size_t ws_round(size_t x) { return (x + 255) / 256 * 256; }
 // ---------------------------------------------------------------- adapters
 constexpr int AD_MAX_RANK = 128;
 constexpr int AD_MAX_ADAPTERS = 65535;
-constexpr int AD_FEW_ROWS = 256;     // rows up to which they are ordered and projected in one launch
+// Rows up to which they are ordered and projected in one launch, and the map's CTAs have few
+// tiles and more factors.  128256 x 4096 bf16 of rank 16: 64 rows of 32 adapters 54 us, 89 with the
+// other form of both, 256 rows of 128 145 (181).  Above it the one launch would still win at 512
+// and 1000 rows (of 128 adapters 180 us for 201, 233 for 248), and the map's form for few rows wins or
+// loses with the adapters a tile meets (1000 rows, rank 32 of 64: 281 for 312; rank 16 of 4: 136 for 128).
+constexpr int AD_FEW_ROWS = 256;
 constexpr int AD_MAP_THREADS = 288;  // eight warps of products, one of copies
 constexpr int AD_MAP_ROWS = 256;     // positions of a CTA of the map, at most
 constexpr int AD_MAP_SMEM = 224 * 1024;   // beside the lists of its rows
