@@ -187,3 +187,32 @@ def test_values_between_bf16s_largest_and_fp32s(x, R):
     assert abs(float(dA[0, 3, 5].to(F64)) / (value * 2.0 ** -20) - 1) <= 2.0 ** -20
     for got in (dh, dA, dB):
         assert int((got != 0).sum()) == 1
+
+
+@pytest.mark.parametrize("N,V,R,dtype", [(6000, 1500, 16, "bf16"), (3000, 70000, 64, "f16"), (5000, 300, 24, "f32")])
+def test_long_adapters_in_graphs_and_on_two_streams(N, V, R, dtype):
+    """dB's later chains add to what the first one wrote: replayed, and beside another call's."""
+    gen = torch.Generator(device="cuda").manual_seed(N)
+    dy, h = _normal((N, V), gen, TYPES[dtype]), torch.randn((N, 128), generator=gen, device="cuda").to(torch.bfloat16)
+    A, B = (torch.randn(s, generator=gen, device="cuda").to(torch.bfloat16) for s in ((2, R, 128), (2, V, R)))
+    ad, rows = tim.Adapters(A, B), torch.randint(-1, 2, (N,), generator=gen, device="cuda", dtype=torch.int32)
+    other = rows.flip(0).contiguous()
+    want = [tim.adapter_logits_backward(dy, h, ad, r) for r in (rows, other)]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = tim.adapter_logits_backward(dy, h, ad, rows)
+    for _ in range(3):
+        for x in out:
+            x.fill_(7)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(out, want[0]))
+    streams, got = [torch.cuda.Stream(), torch.cuda.Stream()], [[], []]
+    for _ in range(4):
+        for k, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[k].append(tim.adapter_logits_backward(dy, h, ad, (rows, other)[k]))
+    torch.cuda.synchronize()
+    tim.check()
+    for k in range(2):
+        assert all(torch.equal(x, y) for one in got[k] for x, y in zip(one, want[k]))
